@@ -425,7 +425,7 @@ def _run_pages(s, c):
         elif what == "fork":
             out["got"] = s3d8.fork_pages(s["pool"], table, lens, refs, s["parents"], s["children"], workspace=s["space"])
         elif what == "free":
-            s3d8.free_pages(table, lens, refs, s["seqs"], c["page"])
+            s3d8.free_pages(table, lens, refs, s["seqs"])
         else:
             out["live"] = s3d8.compact_pages(s["pool"], table, refs, workspace=s["space"])
         return out
