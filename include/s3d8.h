@@ -61,7 +61,8 @@ typedef enum {
     S3D8_ERR_CUDA = -4,        /* a CUDA call or kernel launch failed             */
     S3D8_ERR_TIMEOUT = -5,     /* a bounded device-side wait ran out (sticky)     */
     S3D8_ERR_WORKSPACE = -6,   /* workspace missing or smaller than required      */
-    S3D8_ERR_BOUNDS = -7       /* debug build only: an in-kernel bounds check failed (sticky) */
+    S3D8_ERR_BOUNDS = -7       /* an index read from device memory (a page id, a row, a position) was out of
+                                  range and its access skipped, or a debug-build bounds check failed (sticky) */
 } s3d8_status;
 
 /* Algorithm choice for s3d8_linear_ex.  AUTO picks by shape: GEMV up to 4
@@ -266,8 +267,183 @@ typedef struct {
  */
 int s3d8_linear_batch(const s3d8_linear_job *jobs, int count, int64_t M, void *stream);
 
+/* ---------------------------------------------------------------------------
+ * Between two linears of a decoder layer: the residual update and its norms,
+ * rotary embedding and the append to a paged key/value cache, attention of one
+ * new token over that cache, and the cache's pages.
+ * ------------------------------------------------------------------------- */
+
+/*
+ * The residual update behind a block with the norm in front of the next one:
+ *   u  = w_post ? y * rsqrt(mean(y^2) + eps) * w_post : y
+ *   h' = bf16_rn(h + alpha * g * u),  g = 1 (no gate), gate, or tanh(gate)
+ *   x  = h' * rsqrt(mean(h'^2) + eps) * w_pre
+ * per row of D columns, in fp32 from bf16 inputs; x is normalised from h' as it
+ * is stored, so that it equals the norm of the stream that later layers read.
+ *   h       : [M, D] bfloat16, the residual stream
+ *   y       : [M, D] bfloat16, the block's output, or NULL (then h' = h, and
+ *             h_out must be NULL: a norm alone)
+ *   w_post  : [D] bfloat16 or NULL (no post-norm; NULL when y is NULL)
+ *   gate    : [1] or [D] bfloat16 (gate_n = 1 or D), or NULL (gate_n = 0)
+ *   w_pre   : [D] bfloat16 or NULL (then x, xq and xscale are NULL: no pre-norm)
+ *   h_out   : [M, D] bfloat16 output h' (may be h itself); required with y
+ *   x       : [M, D] bfloat16 output (bf16_rn), or NULL
+ *   xq, xscale : [M, D] int8 and [M] fp32 outputs, or both NULL: bf16_rn(x) by
+ *             the s3d8_quantize_act rule, ready for s3d8_linear
+ * Exactly one of x and xq is given with w_pre.  D is a multiple of 8 (of 16 with
+ * xq) and at most S3D8_MAX_NORM_D; every matrix is contiguous, 16-byte aligned
+ * (weights and a [D] gate too).
+ */
+#define S3D8_MAX_NORM_D 16384
+int s3d8_residual_norm(const void *h_bf16, const void *y_bf16, const void *w_post_bf16,
+                       const void *gate_bf16, int64_t gate_n, int tanh_gate, const void *w_pre_bf16,
+                       float alpha, float eps, int64_t M, int64_t D, void *h_out_bf16, void *x_bf16,
+                       int8_t *xq, float *xscale, void *stream);
+
+/*
+ * Its gradients.  With G the gradient of h' from both uses (the rounding of h'
+ * taken as the identity), r, r' the two reciprocal roots, a = dx * w_pre,
+ * s = alpha g and b = G * s * w_post:
+ *   G  = dh + r a - h' r^3 mean(a h'),      dh_in = bf16_rn(G)
+ *   dy = r' b - y r'^3 mean(b y)            (G * s without a post-norm)
+ *   dw_pre = sum_m dx h' r,  dw_post = sum_m G s y r',  dgate = alpha g'(gate) sum_m G u
+ *   dh      : [M, D] bfloat16, gradient of h_out, or NULL (zero)
+ *   dx      : [M, D] bfloat16, gradient of x, or NULL (zero; NULL without w_pre)
+ *   h       : [M, D] bfloat16, h' as the forward call wrote it (h itself without y)
+ *   y, w_post, gate, gate_n, tanh_gate, w_pre, alpha, eps : as in the forward call
+ *   dh_in   : [M, D] bfloat16 output, gradient of the forward call's h (may be dh)
+ *   dy      : [M, D] bfloat16 output (with y; NULL without)
+ *   dw_pre, dw_post : [D] fp32 outputs, required with their weight, 16-byte aligned
+ *   dgate   : [gate_n] fp32 output, required with the gate
+ *   workspace : s3d8_residual_norm_backward_workspace_size(M, D) bytes, 16-byte
+ *             aligned, not shared by calls that overlap on the GPU
+ * The sums over rows run in a fixed order: equal inputs give equal bits.
+ */
+size_t s3d8_residual_norm_backward_workspace_size(int64_t M, int64_t D);
+int s3d8_residual_norm_backward(const void *dh_bf16, const void *dx_bf16, const void *h_bf16,
+                                const void *y_bf16, const void *w_post_bf16, const void *gate_bf16,
+                                int64_t gate_n, int tanh_gate, const void *w_pre_bf16, float alpha,
+                                float eps, int64_t M, int64_t D, void *dh_in_bf16, void *dy_bf16,
+                                float *dw_pre, float *dw_post, float *dgate, void *workspace,
+                                size_t workspace_bytes, void *stream);
+
+/*
+ * One layer's paged key/value cache.  Element (page p, token t, head h, column d)
+ * of the keys is k[p * k_stride[0] + t * k_stride[1] + h * k_stride[2] + d]; the
+ * values likewise.  Any order of pages, tokens and heads may be chosen by the
+ * strides (in elements), with contiguous columns and rows that start on 16 bytes.
+ * dtype S3D8_KV_BF16: bfloat16 elements, no scales.  S3D8_KV_INT8: int8 codes
+ * and one fp32 scale per token and head (value = code * scale), at
+ * k_scale[p * scale_stride[0] + t * scale_stride[1] + h * scale_stride[2]]
+ * (v_scale with the same strides).
+ * dim: a multiple of 16, 16..256.  pages * page_size < 2^31.  Sequences address
+ * the cache through a block table, int32 [rows, width] with contiguous columns:
+ * token j of a row is token j % page_size of page table[row][j / page_size].
+ */
+#define S3D8_KV_BF16 0
+#define S3D8_KV_INT8 1
+typedef struct {
+    void *k, *v;
+    float *k_scale, *v_scale;
+    int64_t k_stride[3], v_stride[3], scale_stride[3];
+    int64_t pages;
+    int32_t page_size, heads, dim, dtype;
+} s3d8_kv_cache;
+
+/*
+ * Rotary embedding of T new tokens' queries and keys, and the keys and values
+ * into the cache, in one launch.  Columns 0..rotary-1 of each head turn in
+ * pairs: (i, i + rotary/2), or (2i, 2i + 1) when `interleaved`; with c, s =
+ * cos[pos][i], sin[pos][i]: (a, b) -> (a c - b s, b c + a s).
+ *   q       : [T, Hq, dim] bfloat16, strides q_stride[2] (token, head) in elements
+ *   k, v    : [T, heads, dim] bfloat16, strides likewise
+ *   cos, sin: [max_pos, rotary / 2] fp32 contiguous; rotary even, 0..dim
+ *   positions : [T] int32; a negative one marks a padding token: nothing is
+ *             stored for it and its q_out row is zero
+ *   table, rows : block table [table_rows, width] and [T] int32 (row of each
+ *             token), or rows NULL (token t belongs to row t)
+ *   q_out   : [T, Hq, dim] bfloat16 contiguous output, not overlapping q
+ * Keys and values round once: to bf16, or to codes by the s3d8_quantize_act rule
+ * applied to each (token, head) row.  Tokens of one call have distinct places.
+ * A position, row or page out of range skips that token (q_out zero for a
+ * position >= max_pos) and records S3D8_ERR_BOUNDS.  All pointers and strides
+ * keep 16-byte rows.
+ */
+int s3d8_rope_append(const void *q_bf16, const int64_t q_stride[2], const void *k_bf16,
+                     const int64_t k_stride[2], const void *v_bf16, const int64_t v_stride[2],
+                     const float *cos, const float *sin, int64_t max_pos, int64_t rotary,
+                     int interleaved, const int32_t *positions, const int32_t *rows, int64_t T,
+                     int64_t Hq, const int32_t *table, int64_t table_rows, int64_t width,
+                     const s3d8_kv_cache *cache, void *q_out_bf16, void *stream);
+
+/*
+ * Attention of one new token per sequence over the paged cache:
+ *   out[b, h] = sum_j softmax_j(scale * q[b, h] . k[j]) v[j]
+ * over the last `window` (0: all) of the first lens[b] tokens of row b, query
+ * head h reading key/value head h / (Hq / heads).
+ *   q       : [B, Hq, dim] bfloat16 contiguous, 16-byte aligned; Hq a multiple of heads
+ *   table   : int32 [B, width]; lens : int32 [B], at most width * page_size
+ *   out     : [B, Hq, dim] bfloat16 output, 16-byte aligned
+ *   lse     : [B, Hq] fp32 output log(sum_j exp(scale * q . k[j])), or NULL
+ *   workspace : s3d8_paged_attention_workspace_size(cache, B, Hq) bytes, 16-byte
+ *             aligned, caller-owned, not shared by calls that overlap on the GPU
+ * A sequence of no tokens gives zeros and lse = -inf.  What a page holds behind
+ * a sequence's last token, or in front of its window, is never used, whatever it
+ * is.  A page id out of range counts as masked tokens and records
+ * S3D8_ERR_BOUNDS; so does a length beyond the table (cut to it).  Scores, the softmax's maximum and sum
+ * and the output sums are fp32.
+ */
+size_t s3d8_paged_attention_workspace_size(const s3d8_kv_cache *cache, int64_t B, int64_t Hq);
+int s3d8_paged_attention(const void *q_bf16, const s3d8_kv_cache *cache, const int32_t *table,
+                         int64_t width, const int32_t *lens, int64_t B, int64_t Hq, float scale,
+                         int64_t window, void *out_bf16, float *lse, void *workspace,
+                         size_t workspace_bytes, void *stream);
+
+/*
+ * Pages of a cache of several layers that share one block table.  `layers`: a
+ * host array of `count` caches of equal geometry and strides.  State on the
+ * device: table [rows, width] (-1: no page), lens [rows], refs [pages] int32 (how
+ * many table entries hold the page; 0: free).  Free pages are taken lowest id
+ * first, in the order of the call's list, so that the result is determined; from
+ * the first entry that finds too few, every later one that needs a page is
+ * refused as well (got 0, nothing changed for it).  An index out of range
+ * refuses its entry and records S3D8_ERR_BOUNDS.  Lists hold distinct rows.
+ *   workspace : s3d8_pages_workspace_size(pages, rows) bytes, 16-byte aligned,
+ *               not shared by calls that overlap on the GPU
+ *
+ * s3d8_copy_pages    page src[i] -> dst[i] in every layer, i < n (a negative src
+ *                    or dst skips the pair); no dst is another pair's src or dst
+ * s3d8_extend_pages  sequences seqs[i] grow by add[i] >= 0 tokens: pages for them,
+ *                    lens; refused when width is too small.  got [n] int32 output
+ * s3d8_fork_pages    rows children[i] become copies of rows parents[i]: full pages
+ *                    are shared (refs + 1), the tokens of a last, partial page are
+ *                    copied to a new one in every layer.  What a child's row held
+ *                    is overwritten, not freed; no child is a parent of the call.
+ *                    A refused child gets an empty row (-1, lens 0).  got [n]
+ * s3d8_free_pages    rows seqs[i]: refs - 1 for each page held, row -1, lens 0
+ * s3d8_compact_pages live pages move to the ids 0 .. live-1: those at or above
+ *                    live go, in ascending order, to the free ids below it; their
+ *                    content in every layer, refs and all table entries follow.
+ *                    live [1] int32 output
+ */
+size_t s3d8_pages_workspace_size(int64_t pages, int64_t rows);
+int s3d8_copy_pages(const s3d8_kv_cache *layers, int64_t count, const int32_t *src,
+                    const int32_t *dst, int64_t n, void *stream);
+int s3d8_extend_pages(int32_t *table, int64_t rows, int64_t width, int32_t *lens, int32_t *refs,
+                      int64_t pages, int64_t page_size, const int32_t *seqs, const int32_t *add,
+                      int64_t n, int32_t *got, void *workspace, size_t workspace_bytes, void *stream);
+int s3d8_fork_pages(const s3d8_kv_cache *layers, int64_t count, int32_t *table, int64_t rows,
+                    int64_t width, int32_t *lens, int32_t *refs, const int32_t *parents,
+                    const int32_t *children, int64_t n, int32_t *got, void *workspace,
+                    size_t workspace_bytes, void *stream);
+int s3d8_free_pages(int32_t *table, int64_t rows, int64_t width, int32_t *lens, int32_t *refs,
+                    int64_t pages, const int32_t *seqs, int64_t n, void *stream);
+int s3d8_compact_pages(const s3d8_kv_cache *layers, int64_t count, int32_t *table, int64_t rows,
+                       int64_t width, int32_t *refs, int32_t *live, void *workspace,
+                       size_t workspace_bytes, void *stream);
+
 /* Synchronises `stream`, then returns and clears the sticky device status word
- * (S3D8_OK or S3D8_ERR_TIMEOUT), or S3D8_ERR_CUDA if the synchronisation fails. */
+ * (S3D8_OK, S3D8_ERR_TIMEOUT or S3D8_ERR_BOUNDS), or S3D8_ERR_CUDA if the synchronisation fails. */
 int s3d8_device_status(void *stream);
 
 /*

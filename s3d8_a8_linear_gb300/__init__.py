@@ -101,6 +101,7 @@ def load(build_if_missing: bool = False):
                "s3d8_linear_acc_i32", "s3d8_linear_batch", "s3d8_selftest_wait_timeout",
                "s3d8_device_status", "s3d8_version"):
         getattr(L, fn).restype = I
+    decoder.declare(L)
     _lib = L
     return L
 
@@ -391,6 +392,14 @@ def linear_batch(jobs, M: int):
     st = load().s3d8_linear_batch(arr, len(jobs), M, _stream(device))
     _check("s3d8_linear_batch", st)
     return results
+
+
+from . import decoder  # noqa: E402  (uses the helpers above)
+from .decoder import (KVCache, KVPool, ResidualNorm, compact_pages, copy_pages,  # noqa: E402,F401
+                      extend_pages, fork_pages, free_pages, paged_attention,
+                      paged_attention_workspace, pages_workspace, residual_norm,
+                      residual_norm_backward, residual_norm_backward_workspace,
+                      residual_norm_quant, rope_append)
 
 
 def selftest_wait_timeout(polls: int = 1000) -> None:

@@ -95,4 +95,97 @@ bool tmem_preferred(int M, int N, int K);
 size_t tmem_workspace_bytes(int M, int N, int K);
 cudaError_t launch_tmem(const LinearArgs &a, cudaStream_t stream);
 
+// ---- between two linears (residual_norm.cu, rope_append.cu, paged_attention.cu, pages.cu)
+struct NormArgs {
+    const __nv_bfloat16 *h, *y, *w_post, *gate, *w_pre;   // all but h may be null
+    int gate_n, tanh_gate;
+    float alpha, eps;
+    int M, D;
+    __nv_bfloat16 *h_out, *x;
+    int8_t *xq;
+    float *xscale;
+};
+struct NormGradArgs {
+    NormArgs f;                         // h = h', and the forward call's parameters
+    const __nv_bfloat16 *dh, *dx;       // either may be null
+    __nv_bfloat16 *dh_in, *dy;
+    float *dw_pre, *dw_post, *dgate;
+    float *part;                        // [CTAs][2 D + 4]
+};
+cudaError_t launch_residual_norm(const NormArgs &a, cudaStream_t stream);
+size_t residual_norm_backward_workspace(int64_t M, int64_t D);
+cudaError_t launch_residual_norm_backward(const NormGradArgs &g, cudaStream_t stream);
+
+// One layer's paged cache as the kernels see it (strides in elements).
+struct KvCache {
+    void *k, *v;
+    float *k_scale, *v_scale;           // int8 only
+    int64_t ks[3], vs[3], ss[3];        // page, token, head
+    int pages, page_size, heads, dim;
+    int int8;
+};
+struct RopeArgs {
+    const __nv_bfloat16 *q, *k, *v;
+    int64_t qs[2], ks[2], vs[2];        // token, head
+    const float *cos, *sin;
+    int64_t max_pos;
+    int rotary, interleaved;
+    const int32_t *positions, *rows;
+    int64_t T;
+    int Hq;
+    const int32_t *table;
+    int64_t table_rows, width;
+    KvCache kv;
+    __nv_bfloat16 *q_out;
+    int *status;
+};
+cudaError_t launch_rope_append(const RopeArgs &a, cudaStream_t stream);
+
+struct AttnArgs {
+    const __nv_bfloat16 *q;
+    KvCache kv;
+    const int32_t *table, *lens;
+    int64_t width;
+    int B, Hq;
+    float scale;
+    int64_t window;
+    __nv_bfloat16 *out;
+    float *lse;
+    void *ws;
+    int *status;
+};
+size_t paged_attention_workspace(const KvCache &kv, int64_t B, int64_t Hq);
+cudaError_t launch_paged_attention(const AttnArgs &a, cudaStream_t stream);
+
+constexpr int kPoolLayers = 64;         // layers of one copy launch
+struct PoolArgs {
+    KvCache geo;                        // geometry and strides (its pointers are unused)
+    void *k[kPoolLayers], *v[kPoolLayers];
+    float *k_scale[kPoolLayers], *v_scale[kPoolLayers];
+    int layers;
+};
+struct PagesArgs {
+    int32_t *table, *lens, *refs;
+    int64_t rows, width;
+    int pages, page_size;
+    const int32_t *who, *other;         // seqs and add, or parents and children
+    int n;
+    int32_t *got;                       // got [n], or live [1]
+    int32_t *ws;
+    int *status;
+};
+size_t pages_workspace(int64_t pages, int64_t rows);
+// Copies page src[i] to dst[i]: whole pages, or the first tokens[i] tokens of each
+// (tokens != nullptr); the pair count is n, or *count on the device when given.
+cudaError_t launch_copy_pages(const PoolArgs &p, const int32_t *src, const int32_t *dst, const int32_t *tokens,
+                              int n, const int32_t *count, int *status, cudaStream_t stream);
+cudaError_t launch_extend_pages(const PagesArgs &a, cudaStream_t stream);
+// On return `pairs` holds the workspace's lists of copies to make: src, dst, tokens.
+struct PagePairs {
+    const int32_t *src, *dst, *tokens, *count;
+};
+cudaError_t launch_fork_pages(const PagesArgs &a, PagePairs *pairs, cudaStream_t stream);
+cudaError_t launch_free_pages(const PagesArgs &a, cudaStream_t stream);
+cudaError_t launch_compact_pages(const PagesArgs &a, PagePairs *pairs, cudaStream_t stream);
+
 }  // namespace s3d8

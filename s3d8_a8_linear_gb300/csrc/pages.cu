@@ -1,0 +1,379 @@
+// Pages of a cache of several layers: copies, growth, forks, release and
+// compaction (s3d8_copy_pages and the calls below it in the header).
+//
+// The bookkeeping (block table, lengths, reference counts) is a few hundred KB
+// at most and runs in one CTA, which needs no ordering between CTAs; the page
+// copies that follow read their list from the workspace and use the whole GPU.
+#include "common.cuh"
+#include "launch.h"
+#include "tcgen05.cuh"
+
+namespace s3d8 {
+
+namespace {
+
+constexpr int kMetaThreads = 1024, kMetaWarps = kMetaThreads / 32;
+
+// Exclusive prefix sum of one value per thread; `total` receives the sum.
+__device__ int block_scan(int v, int *warp_sums, int &total)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int inc = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o)
+            inc += u;
+    }
+    __syncthreads();   // the previous call's sums have been read
+    if (lane == 31)
+        warp_sums[warp] = inc;
+    __syncthreads();
+    int w = warp_sums[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, w, o);
+        if (lane >= o)
+            w += u;
+    }
+    total = __shfl_sync(0xffffffffu, w, 31);
+    return inc - v + (warp ? __shfl_sync(0xffffffffu, w, warp - 1) : 0);
+}
+
+// Walks ids begin..end-1 in order over the whole CTA and calls f(id, rank) with
+// the rank of each id for which pick(id) holds; returns how many there are.  f is
+// called for the ranks below `most` only.
+template <class Pick, class F>
+__device__ int enumerate(int begin, int end, int most, int *warp_sums, Pick pick, F f)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // warp w takes a run of whole 32-id groups
+    const int groups = (end - begin + 31) / 32, per = (groups + kMetaWarps - 1) / kMetaWarps;
+    const int g0 = min(groups, warp * per), g1 = min(groups, g0 + per);
+    int mine = 0;
+#pragma unroll 4
+    for (int g = g0; g < g1; ++g) {
+        const int id = begin + g * 32 + lane;
+        mine += __popc(__ballot_sync(0xffffffffu, id < end && pick(id)));
+    }
+    int total;
+    int rank = block_scan(lane == 31 ? mine : 0, warp_sums, total);
+    rank = __shfl_sync(0xffffffffu, rank, 0);
+#pragma unroll 4
+    for (int g = g0; g < g1; ++g) {
+        if (rank >= most)
+            break;
+        const int id = begin + g * 32 + lane;
+        const bool yes = id < end && pick(id);
+        const uint32_t mask = __ballot_sync(0xffffffffu, yes);
+        const int at = rank + __popc(mask & ((1u << lane) - 1u));
+        if (yes && at < most)
+            f(id, at);
+        rank += __popc(mask);
+    }
+    return total;
+}
+
+// Workspace: ids [pages], more [pages], map [pages], then three lists of `rows`.
+__device__ __forceinline__ int32_t *ws_list(const PagesArgs &a, int k)
+{
+    return a.ws + (k < 3 ? (size_t)k * a.pages : (size_t)3 * a.pages + (size_t)(k - 3) * a.rows);
+}
+
+__global__ __launch_bounds__(kMetaThreads) void extend_pages_kernel(PagesArgs a)
+{
+    __shared__ int sums[32];
+    tc::pdl_launch_dependents();
+    tc::pdl_wait();
+    int32_t *ids = ws_list(a, 0), *begins = ws_list(a, 3), *needs = ws_list(a, 4);
+    int asked = 0;
+    for (int i0 = 0; i0 < a.n; i0 += kMetaThreads) {
+        const int i = i0 + threadIdx.x;
+        int need = -1;   // refused
+        if (i < a.n) {
+            const int s = a.who[i];
+            const int64_t add = a.other[i];
+            if (s < 0 || s >= a.rows) {
+                atomicExch(a.status, kStatusBounds);
+            } else {
+                const int64_t len = max(a.lens[s], 0), S = a.page_size;
+                const int64_t have = (len + S - 1) / S, want = (len + add + S - 1) / S;
+                if (add >= 0 && want <= a.width && len + add <= 0x7FFFFFFF)
+                    need = (int)(want - have);
+            }
+        }
+        int total;
+        const int begin = asked + block_scan(max(need, 0), sums, total);
+        asked += total;
+        if (i < a.n) {
+            begins[i] = begin;
+            needs[i] = need;
+        }
+    }
+    __syncthreads();
+    const int32_t *refs = a.refs;
+    const int free = enumerate(0, a.pages, min(asked, a.pages), sums, [&](int id) { return refs[id] == 0; },
+                               [&](int id, int at) { ids[at] = id; });
+    __syncthreads();
+    for (int i = threadIdx.x >> 5; i < a.n; i += kMetaWarps) {
+        const int lane = threadIdx.x & 31, need = needs[i], begin = begins[i];
+        const bool ok = need == 0 || (need > 0 && begin + need <= free);
+        if (ok) {
+            const int s = a.who[i];
+            const int len = max(a.lens[s], 0);
+            const int have = (int)(((int64_t)len + a.page_size - 1) / a.page_size);
+            for (int k = lane; k < need; k += 32) {
+                const int id = ids[begin + k];
+                a.table[s * a.width + have + k] = id;
+                a.refs[id] = 1;
+            }
+            __syncwarp();
+            if (lane == 0)
+                a.lens[s] = len + a.other[i];
+        }
+        if (lane == 0)
+            a.got[i] = ok;
+    }
+}
+
+__global__ __launch_bounds__(kMetaThreads) void fork_pages_kernel(PagesArgs a)
+{
+    __shared__ int sums[32];
+    tc::pdl_launch_dependents();
+    tc::pdl_wait();
+    int32_t *ids = ws_list(a, 0), *src = ws_list(a, 3), *dst = ws_list(a, 4), *tokens = ws_list(a, 5);
+    int asked = 0;
+    for (int i0 = 0; i0 < a.n; i0 += kMetaThreads) {
+        const int i = i0 + threadIdx.x;
+        int part = 0, at = -1;   // tokens of the last page, its column; at -2: refused
+        if (i < a.n) {
+            const int64_t p = a.who[i], c = a.other[i];
+            if (p < 0 || p >= a.rows || c < 0 || c >= a.rows || a.lens[p] < 0 ||
+                a.lens[p] > a.width * a.page_size) {
+                at = -2;
+                atomicExch(a.status, kStatusBounds);
+            } else {
+                part = a.lens[p] % a.page_size;
+                at = part ? a.lens[p] / a.page_size : -1;
+            }
+        }
+        int total;
+        const int begin = asked + block_scan(part > 0, sums, total);
+        asked += total;
+        if (i < a.n) {
+            src[i] = at;
+            dst[i] = begin;
+            tokens[i] = part;
+        }
+    }
+    __syncthreads();
+    const int32_t *refs = a.refs;
+    const int free = enumerate(0, a.pages, min(asked, a.pages), sums, [&](int id) { return refs[id] == 0; },
+                               [&](int id, int at) { ids[at] = id; });
+    __syncthreads();
+    for (int i = threadIdx.x >> 5; i < a.n; i += kMetaWarps) {
+        const int lane = threadIdx.x & 31, part = tokens[i], at = src[i], begin = dst[i];
+        const int64_t p = a.who[i], c = a.other[i];
+        const bool ok = at != -2 && (!part || begin < free);
+        const int fresh = ok && part ? ids[begin] : -1;
+        int from = -1;
+        if (c >= 0 && c < a.rows) {
+            const int full = ok ? a.lens[p] / a.page_size : 0;
+            for (int64_t k = lane; k < a.width; k += 32) {
+                int id = -1;
+                if (k < full) {
+                    id = a.table[p * a.width + k];
+                    if (id >= 0 && id < a.pages)
+                        atomicAdd(a.refs + id, 1);
+                    else
+                        id = -1;
+                } else if (k == full) {
+                    id = fresh;
+                }
+                a.table[c * a.width + k] = id;
+            }
+            if (lane == 0) {
+                a.lens[c] = ok ? a.lens[p] : 0;
+                if (fresh >= 0) {
+                    a.refs[fresh] = 1;
+                    from = a.table[p * a.width + full];
+                    if (from < 0 || from >= a.pages) {
+                        from = -1;
+                        atomicExch(a.status, kStatusBounds);
+                    }
+                }
+            }
+        }
+        if (lane == 0) {
+            src[i] = from;
+            dst[i] = fresh;
+            a.got[i] = ok;
+        }
+    }
+}
+
+__global__ __launch_bounds__(kMetaThreads) void free_pages_kernel(PagesArgs a)
+{
+    tc::pdl_launch_dependents();
+    tc::pdl_wait();
+    for (int i = threadIdx.x >> 5; i < a.n; i += kMetaWarps) {
+        const int lane = threadIdx.x & 31;
+        const int64_t s = a.who[i];
+        if (s < 0 || s >= a.rows) {
+            atomicExch(a.status, kStatusBounds);
+            continue;
+        }
+        for (int64_t k = lane; k < a.width; k += 32) {
+            const int id = a.table[s * a.width + k];
+            const bool page = id >= 0 && id < a.pages;
+            const bool counted = page && atomicSub(a.refs + id, 1) > 0;
+            if (page && !counted)
+                atomicAdd(a.refs + id, 1);   // held by more entries than counted: it stays free
+            if (id >= 0 && !counted)
+                atomicExch(a.status, kStatusBounds);
+            a.table[s * a.width + k] = -1;
+        }
+        if (lane == 0)
+            a.lens[s] = 0;
+    }
+}
+
+// holes -> ids, movers -> more, map[mover] = its new id; refs and live follow.
+__global__ __launch_bounds__(kMetaThreads) void compact_plan_kernel(PagesArgs a)
+{
+    __shared__ int sums[32];
+    tc::pdl_launch_dependents();
+    tc::pdl_wait();
+    int32_t *holes = ws_list(a, 0), *movers = ws_list(a, 1), *map = ws_list(a, 2), *count = ws_list(a, 3);
+    int32_t *refs = a.refs;
+    const int live = enumerate(0, a.pages, 0, sums, [&](int id) { return refs[id] != 0; }, [](int, int) {});
+    const int moves = enumerate(0, live, a.pages, sums, [&](int id) { return refs[id] == 0; },
+                                [&](int id, int at) { holes[at] = id; });
+    enumerate(live, a.pages, a.pages, sums, [&](int id) { return refs[id] != 0; },
+              [&](int id, int at) { movers[at] = id; });
+    for (int id = live + threadIdx.x; id < a.pages; id += kMetaThreads)
+        map[id] = id;   // a dangling entry (of a page that nobody counts) stays
+    __syncthreads();
+    for (int i = threadIdx.x; i < moves; i += kMetaThreads) {
+        const int from = movers[i], to = holes[i];
+        map[from] = to;
+        refs[to] = refs[from];
+        refs[from] = 0;
+    }
+    if (threadIdx.x == 0) {
+        *count = moves;
+        a.got[0] = live;
+    }
+}
+
+__global__ void compact_table_kernel(PagesArgs a)
+{
+    tc::pdl_launch_dependents();
+    tc::pdl_wait();
+    const int32_t *map = ws_list(a, 2);
+    const int live = a.got[0];
+    const int64_t n = a.rows * a.width;
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
+        const int id = a.table[i];
+        if (id >= a.pages)
+            atomicExch(a.status, kStatusBounds);
+        else if (id >= live)
+            a.table[i] = map[id];
+    }
+}
+
+constexpr int kCopyThreads = 256;
+
+// One job = one page pair in one layer, keys or values: rows of dim columns, then
+// (int8) the page's scales.
+template <class T>
+__device__ __forceinline__ void copy_rows(const T *from, T *to, int tokens, int heads, int per_row, const int64_t (&st)[3],
+                                          int elem_per_chunk, bool token_major)
+{
+    const int total = tokens * heads * per_row;
+    for (int u = threadIdx.x; u < total; u += kCopyThreads) {
+        const int c = u % per_row, r = u / per_row;
+        const int t = token_major ? r / heads : r % tokens, h = token_major ? r % heads : r / tokens;
+        const int64_t at = (t * st[1] + h * st[2]) / elem_per_chunk + c;
+        to[at] = from[at];
+    }
+}
+
+__global__ __launch_bounds__(kCopyThreads) void copy_pages_kernel(const __grid_constant__ PoolArgs p, const int32_t *src,
+                                                                  const int32_t *dst, const int32_t *tokens, int n,
+                                                                  const int32_t *count, int *status)
+{
+    tc::pdl_launch_dependents();
+    tc::pdl_wait();
+    if (count)
+        n = *count;
+    const int64_t jobs = (int64_t)n * p.layers * 2;
+    const KvCache &g = p.geo;
+    for (int64_t j = blockIdx.x; j < jobs; j += gridDim.x) {
+        const int pair = (int)(j / (p.layers * 2)), rest = (int)(j % (p.layers * 2)), layer = rest >> 1;
+        const int from = src[pair], to = dst[pair];
+        if (from < 0 || to < 0)
+            continue;
+        if (from >= g.pages || to >= g.pages) {
+            if (threadIdx.x == 0)
+                atomicExch(status, kStatusBounds);
+            continue;
+        }
+        const int nt = tokens ? tokens[pair] : g.page_size;
+        const bool value = rest & 1;
+        const int64_t (&st)[3] = value ? g.vs : g.ks;
+        const int es = g.int8 ? 1 : 2, epc = 16 / es;
+        char *base = static_cast<char *>(value ? p.v[layer] : p.k[layer]);
+        copy_rows(reinterpret_cast<const uint4 *>(base + from * st[0] * es), reinterpret_cast<uint4 *>(base + to * st[0] * es), nt,
+                  g.heads, g.dim / epc, st, epc, st[1] >= st[2]);
+        if (g.int8) {
+            float *sc = value ? p.v_scale[layer] : p.k_scale[layer];
+            copy_rows(sc + from * g.ss[0], sc + to * g.ss[0], nt, g.heads, 1, g.ss, 1, g.ss[1] >= g.ss[2]);
+        }
+    }
+}
+
+}  // namespace
+
+size_t pages_workspace(int64_t pages, int64_t rows)
+{
+    return ((size_t)3 * pages + (size_t)3 * rows + 4) * sizeof(int32_t);
+}
+
+cudaError_t launch_copy_pages(const PoolArgs &p, const int32_t *src, const int32_t *dst, const int32_t *tokens, int n,
+                              const int32_t *count, int *status, cudaStream_t stream)
+{
+    if (n == 0)
+        return cudaSuccess;
+    const int64_t jobs = (int64_t)n * p.layers * 2, most = 16 * (int64_t)device_sm_count();
+    return tc::launch_pdl(copy_pages_kernel, dim3((unsigned)(jobs < most ? jobs : most)), dim3(kCopyThreads), 0, stream, p,
+                          src, dst, tokens, n, count, status);
+}
+
+cudaError_t launch_extend_pages(const PagesArgs &a, cudaStream_t stream)
+{
+    return tc::launch_pdl(extend_pages_kernel, dim3(1), dim3(kMetaThreads), 0, stream, a);
+}
+
+cudaError_t launch_fork_pages(const PagesArgs &a, PagePairs *pairs, cudaStream_t stream)
+{
+    const int32_t *lists = a.ws + (size_t)3 * a.pages;
+    *pairs = PagePairs{lists, lists + a.rows, lists + 2 * a.rows, nullptr};
+    return tc::launch_pdl(fork_pages_kernel, dim3(1), dim3(kMetaThreads), 0, stream, a);
+}
+
+cudaError_t launch_free_pages(const PagesArgs &a, cudaStream_t stream)
+{
+    return tc::launch_pdl(free_pages_kernel, dim3(1), dim3(kMetaThreads), 0, stream, a);
+}
+
+cudaError_t launch_compact_pages(const PagesArgs &a, PagePairs *pairs, cudaStream_t stream)
+{
+    *pairs = PagePairs{a.ws + a.pages, a.ws, nullptr, a.ws + (size_t)3 * a.pages};
+    cudaError_t e = tc::launch_pdl(compact_plan_kernel, dim3(1), dim3(kMetaThreads), 0, stream, a);
+    if (e != cudaSuccess)
+        return e;
+    return tc::launch_pdl(compact_table_kernel, dim3(64), dim3(256), 0, stream, a);
+}
+
+}  // namespace s3d8
