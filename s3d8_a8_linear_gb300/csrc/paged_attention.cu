@@ -1,101 +1,920 @@
 // Attention of one new token per sequence over the paged cache
 // (s3d8_paged_attention).
 //
-// One CTA per (sequence, query head); its warps walk the tokens with a running
-// maximum and sum (lane l holds columns l, l + 32, ...) and join at the end.
+// Bound by HBM: every visible key and value is read once, for 2 to 16 query rows
+// at a time.  The unit of work is a tile of 16 tokens of one (sequence, key/value
+// head); all tiles of a call, in that order, are dealt out in equal contiguous runs
+// to the warps of one CTA per SM, whatever the lengths are.  A warp streams its
+// tiles through a ring of its own in shared memory (cp.async, no barrier with
+// other warps) and carries the softmax's running maximum m, sum l and the output
+// sums O in fp32:
+//   S = Q K^T (tensor cores, rows = the query heads of the key/value head),
+//   m' = max(m, S), O = 2^(m - m') O + 2^(S - m') V, l likewise.
+// The matrix products are mma.sync: 16 rows (tcgen05's smallest M is 64) at a rate
+// far below the tensor cores' limit.  The weights 2^(S - m') enter the second
+// product as a 16-bit value and its 16-bit remainder: with up to 8 query rows the
+// remainder takes the upper 8 rows of the same instruction.
+//
+// A run that ends inside a sequence leaves (m, l, O) in the workspace; the warps of
+// a CTA join theirs, and where a sequence crosses CTAs the last of them to arrive
+// joins all of its parts, in order of position.
 #include "common.cuh"
 #include "launch.h"
 #include "tcgen05.cuh"
+
+#include <atomic>
 
 namespace s3d8 {
 
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kCols = 8;   // 256 columns / 32 lanes
+constexpr int kTile = 16;          // tokens
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
 
-__device__ __forceinline__ float element(const void *base, int64_t at, int int8)
+template <int DP, bool INT8>
+struct Shape {
+    static constexpr int kRow = INT8 ? DP : 2 * DP;       // bytes of a key or value row in shared memory
+    static constexpr int kChunks = kRow / 16;
+    static constexpr int kKv = kTile * kRow;              // bytes of a tile's keys (and of its values)
+    static constexpr int kScales = INT8 ? 2 * kTile * 4 : 0;
+    static constexpr int kStage = 2 * kKv + kScales + 16; // + the tile's mask
+};
+
+// ---- the plan: which tiles, and whose -----------------------------------------
+
+struct Seq {
+    int len, first, tiles;   // visible tokens first..len-1; tiles of 16 from the one that holds `first`
+};
+
+__device__ __forceinline__ Seq sequence(const AttnArgs &a, int b)
 {
-    return int8 ? (float)static_cast<const int8_t *>(base)[at]
-                : __bfloat162float(static_cast<const __nv_bfloat16 *>(base)[at]);
+    const int64_t room = a.width * a.kv.page_size;
+    Seq s;
+    s.len = (int)min((int64_t)max(a.lens[b], 0), room);
+    s.first = a.window > 0 && s.len > a.window ? (int)(s.len - a.window) : 0;
+    s.tiles = s.len > 0 ? (s.len + kTile - 1) / kTile - s.first / kTile : 0;
+    return s;
 }
 
-__global__ __launch_bounds__(kWarps * 32) void paged_attention_kernel(AttnArgs a)
+// A position in the list of tiles: tile k of unit u (key/value head, block of
+// query rows) of sequence b.
+struct Cursor {
+    int b, u, k;
+    Seq s;
+
+    __device__ __forceinline__ void next(const AttnArgs &a, int units)
+    {
+        if (++k < s.tiles)
+            return;
+        k = 0;
+        if (++u < units)
+            return;
+        u = 0;
+        for (++b; b < a.B; ++b) {
+            s = sequence(a, b);
+            if (s.tiles > 0)
+                return;
+        }
+    }
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int bytes)
 {
-    __shared__ float om[kWarps], ol[kWarps], oo[kWarps][256];
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, int bytes)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+}
+__device__ __forceinline__ void ldsm_x4_trans(uint32_t addr, uint32_t (&r)[4])
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+}
+
+template <bool F16>
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    if (F16)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// {lo, hi} as two 16-bit values in one register, and what their rounding left.
+template <bool F16>
+__device__ __forceinline__ void split2(float x, float y, uint32_t &top, uint32_t &rest)
+{
+    if (F16) {
+        const __half2 h = __floats2half2_rn(x, y);
+        const float2 f = __half22float2(h);
+        const __half2 r = __floats2half2_rn(x - f.x, y - f.y);
+        top = *reinterpret_cast<const uint32_t *>(&h);
+        rest = *reinterpret_cast<const uint32_t *>(&r);
+    } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+        const float2 f = __bfloat1622float2(h);
+        const __nv_bfloat162 r = __floats2bfloat162_rn(x - f.x, y - f.y);
+        top = *reinterpret_cast<const uint32_t *>(&h);
+        rest = *reinterpret_cast<const uint32_t *>(&r);
+    }
+}
+
+// 16-byte chunk c of row r of an int8 tile lies at chunk c ^ swz8(r): the reads
+// below then meet no bank twice.
+template <int CHUNKS>
+__device__ __forceinline__ int swz8(int r)
+{
+    return CHUNKS >= 8 ? (r & 6) ^ ((r & 1) << 2) : (r >> 1) & (CHUNKS - 1);
+}
+
+// Four int8 codes (bytes of w) as two pairs of fp16, exactly: byte + 128 in the
+// low bits of 1024 (0x6400), less 1152.
+__device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t &p01, uint32_t &p23)
+{
+    const uint32_t u = w ^ 0x80808080u, magic = 0x64646464u;
+    p01 = tc::f16x2_sub(prmt(u, magic, 0x4140), 0x64806480u);
+    p23 = tc::f16x2_sub(prmt(u, magic, 0x4342), 0x64806480u);
+}
+
+// Bytes i of two words as a pair of fp16.
+template <int I>
+__device__ __forceinline__ uint32_t pair_to_f16(uint32_t w0, uint32_t w1)
+{
+    const uint32_t both = prmt(w0, w1, I | ((4 + I) << 8));    // low half: {w0[I], -, w1[I], -}
+    return tc::f16x2_sub(prmt(both ^ 0x80808080u, 0x64646464u, 0x4240), 0x64806480u);
+}
+
+struct AttnPlan {
+    int units, blocks, rows;     // per sequence: key/value heads x blocks of query rows; rows per block at most
+    int group;                   // query heads per key/value head
+    float *warp_part, *cta_part; // partial states
+    unsigned long long *arrived; // per CTA
+    unsigned long long tag;
+};
+
+// One partial state in the workspace: rows x (m, l), then rows x D output sums.
+__device__ __forceinline__ size_t part_floats(int rows, int D) { return (size_t)rows * (D + 2); }
+
+template <int DP, bool INT8, bool R8, int WARPS, int STAGES>
+__global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __grid_constant__ AttnArgs a,
+                                                                     const __grid_constant__ AttnPlan p)
+{
+    using Sh = Shape<DP, INT8>;
+    constexpr int NT = DP / 8;                    // 8-column tiles of the output
+    constexpr int kScanThreads = WARPS * 32;
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    __shared__ long long scan[kScanThreads + 1];
+    __shared__ long long warp_tot[WARPS];
+    // what each warp left: its first run's sequence (begun before the warp), and the last one's (continued behind it)
+    __shared__ int part_b[2 * WARPS], part_u[2 * WARPS];   // part_b < 0: nothing
+    __shared__ unsigned char part_ends[2 * WARPS], part_begins[2 * WARPS];
+    __shared__ int last_flag[2];
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int D = a.kv.dim, S = a.kv.page_size;
     tc::pdl_launch_dependents();
     tc::pdl_wait();
-    const int b = blockIdx.x / a.Hq, hq = blockIdx.x % a.Hq, h = hq / (a.Hq / a.kv.heads);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, D = a.kv.dim;
-    int64_t len = a.lens[b];
-    if (len > a.width * a.kv.page_size) {
-        len = a.width * a.kv.page_size;
+
+    // ---- tiles in front of each sequence ------------------------------------------
+    const int per = (a.B + kScanThreads - 1) / kScanThreads;   // sequences per scanning thread
+    {
+        long long mine = 0;
+        for (int i = 0; i < per; ++i) {
+            const int b = threadIdx.x * per + i;
+            if (b < a.B) {
+                mine += (long long)sequence(a, b).tiles * p.units;
+                if (blockIdx.x == 0 && a.lens[b] > a.width * S)
+                    atomicExch(a.status, kStatusBounds);
+            }
+        }
+        long long inc = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long v = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o)
+                inc += v;
+        }
+        if (lane == 31)
+            warp_tot[warp] = inc;
+        scan[threadIdx.x + 1] = inc;
+    }
+    if (threadIdx.x < 2 * WARPS)
+        part_b[threadIdx.x] = -1;
+    __syncthreads();
+    {
+        long long before = 0;
+        for (int w = 0; w < warp; ++w)
+            before += warp_tot[w];
+        scan[threadIdx.x + 1] += before;
         if (threadIdx.x == 0)
-            atomicExch(a.status, kStatusBounds);
+            scan[0] = 0;
     }
-    const int64_t first = a.window > 0 && len > a.window ? len - a.window : 0;
-    float q[kCols], o[kCols];
-    for (int i = 0; i < kCols; ++i) {
-        const int d = lane + 32 * i;
-        q[i] = d < D ? __bfloat162float(a.q[((int64_t)b * a.Hq + hq) * D + d]) : 0.0f;
-        o[i] = 0.0f;
+    __syncthreads();
+    const long long total = scan[kScanThreads];
+
+    // ---- sequences of no tokens: zeros ------------------------------------------------
+    for (int b = blockIdx.x * WARPS + warp; b < a.B; b += gridDim.x * WARPS) {
+        if (a.lens[b] > 0 && a.width > 0)
+            continue;
+        for (int64_t i = lane; i < (int64_t)a.Hq * D; i += 32)
+            a.out[(int64_t)b * a.Hq * D + i] = __float2bfloat16_rn(0.0f);
+        if (a.lse)
+            for (int i = lane; i < a.Hq; i += 32)
+                a.lse[(int64_t)b * a.Hq + i] = -INFINITY;
     }
-    float m = -INFINITY, l = 0.0f;
-    for (int64_t j = first + warp; j < len; j += kWarps) {
-        const int page = a.table[b * a.width + j / a.kv.page_size], t = (int)(j % a.kv.page_size);
-        if (page < 0 || page >= a.kv.pages) {
-            atomicExch(a.status, kStatusBounds);
+
+    // ---- this CTA's run of tiles, and this warp's part of it -----------------------------
+    long long span = (total + gridDim.x - 1) / gridDim.x;
+    if (span < WARPS)
+        span = WARPS;      // a CTA takes a tile per warp before another one joins in
+    const long long c0 = (long long)blockIdx.x * span;
+    if (c0 >= total)
+        return;
+    const long long c1 = min(total, c0 + span);
+    const long long w0 = c0 + (c1 - c0) * warp / WARPS, w1 = c0 + (c1 - c0) * (warp + 1) / WARPS;
+    const int n = (int)(w1 - w0);
+    const size_t part_size = part_floats(p.rows, D);
+
+    if (n > 0) {
+        // first tile: the scanning thread that holds it, then its sequences
+        Cursor in;
+        {
+            int lo = 0, hi = kScanThreads;
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) / 2;
+                if (scan[mid] <= w0)
+                    lo = mid;
+                else
+                    hi = mid;
+            }
+            long long left = w0 - scan[lo];
+            in.b = lo * per;
+            in.s = sequence(a, in.b);
+            while (left >= (long long)in.s.tiles * p.units) {
+                left -= (long long)in.s.tiles * p.units;
+                in.s = sequence(a, ++in.b);
+            }
+            in.u = (int)(left / in.s.tiles);
+            in.k = (int)(left % in.s.tiles);
+        }
+        Cursor at = in;                       // the tile being computed; `in`: the tile being fetched
+        const uint32_t ring = smem_addr(smem_raw) + warp * (STAGES * Sh::kStage);
+
+        // ---- fetching: lanes 0-15 hold the tile's key rows, lanes 16-31 its value rows ------
+        const int side = lane >> 4;
+        int64_t row_off = 0;                  // of the next tile to fetch: offset inside its page,
+        int64_t scale_off = 0;
+        int row_page = -1;                    // its page,
+        bool row_seen = false;                // and whether it holds a visible token
+        auto look_up = [&](bool live) {
+            row_seen = false;
+            if (!live)
+                return;
+            const int tok = (in.s.first / kTile + in.k) * kTile + (lane & 15);
+            if (tok < in.s.first || tok >= in.s.len)
+                return;
+            row_seen = true;
+            const int col = tok / S, slot = tok - col * S, h = in.u / p.blocks;
+            row_page = a.table[in.b * a.width + col];
+            const int64_t *st = side ? a.kv.vs : a.kv.ks;
+            row_off = slot * st[1] + h * st[2];
+            if (INT8)
+                scale_off = slot * a.kv.ss[1] + h * a.kv.ss[2];
+        };
+        auto fetch = [&](int stage) {
+            const uint32_t base = ring + stage * Sh::kStage;
+            const bool ok = row_seen && row_page >= 0 && row_page < a.kv.pages;
+            if (row_seen && !ok)
+                atomicExch(a.status, kStatusBounds);   // its token stays masked
+            const char *src = static_cast<const char *>(side ? a.kv.v : a.kv.k);
+            if (ok)
+                src += (row_page * (side ? a.kv.vs[0] : a.kv.ks[0]) + row_off) * (INT8 ? 1 : 2);
+            const uint32_t mask = __ballot_sync(0xffffffffu, ok);
+            if (INT8) {
+                const float *sc = side ? a.kv.v_scale : a.kv.k_scale;
+                if (ok)
+                    sc += row_page * a.kv.ss[0] + scale_off;
+                cp_async4(base + 2 * Sh::kKv + side * (kTile * 4) + (lane & 15) * 4, sc, ok ? 4 : 0);
+            }
+            if (lane == 0)
+                asm volatile("st.shared.u32 [%0], %1;" ::"r"(base + 2 * Sh::kKv + Sh::kScales), "r"(mask & 0xFFFFu) : "memory");
+            const int row_bytes = INT8 ? D : 2 * D;
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+#pragma unroll
+                for (int i = 0; i < kTile * Sh::kChunks / 32; ++i) {
+                    const int idx = i * 32 + lane, r = idx / Sh::kChunks, c = idx % Sh::kChunks;
+                    const char *from = reinterpret_cast<const char *>(
+                        __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), kv * 16 + r));
+                    const bool live = ((mask >> r) & 1) && c * 16 < row_bytes;
+                    const int phys = INT8 ? c ^ swz8<Sh::kChunks>(r) : c ^ (r & 7);
+                    cp_async16(base + kv * Sh::kKv + r * Sh::kRow + phys * 16, live ? from + c * 16 : from, live ? 16 : 0);
+                }
+            }
+        };
+
+        look_up(true);
+        int fetched = 0;
+#pragma unroll
+        for (int s = 0; s < STAGES - 1; ++s) {
+            if (fetched < n) {
+                fetch(s);
+                ++fetched;
+                in.next(a, p.units);
+                look_up(fetched < n);
+            }
+            cp_commit();
+        }
+
+        // ---- state of the current sequence -----------------------------------------------------
+        float o[NT][4], m[2], l[2];
+        uint32_t q[DP / 16][R8 ? 2 : 4];
+        float qs[2] = {0.0f, 0.0f};           // factor of a score's row, log2(e) in it
+        float vf = 0.0f, vinv = 0.0f;         // int8: the power of two that carries the value scales
+        bool whole = at.k == 0;               // this warp has the sequence from its first tile on
+        bool fresh = true;
+
+        for (int i = 0; i < n; ++i) {
+            cp_wait<STAGES - 2>();
+            __syncwarp();
+            if (fetched < n) {
+                fetch((i + STAGES - 1) % STAGES);
+                ++fetched;
+                in.next(a, p.units);
+                look_up(fetched < n);
+            }
+            cp_commit();
+
+            const int h = at.u / p.blocks, r0 = (at.u % p.blocks) * 16;
+            const int rows = min(p.group - r0, p.rows);
+            const int64_t head0 = (int64_t)at.b * a.Hq + h * p.group + r0;   // query row of the state's row 0
+            if (fresh) {
+                fresh = false;
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+                    o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
+                m[0] = m[1] = -INFINITY;
+                l[0] = l[1] = 0.0f;
+                vf = vinv = 0.0f;
+#pragma unroll
+                for (int x = 0; x < (R8 ? 1 : 2); ++x) {
+                    const __nv_bfloat16 *src = a.q + (head0 + g + 8 * x) * D;
+                    const bool in_row = g + 8 * x < rows;
+                    qs[x] = a.scale * kLog2e;
+                    if (!INT8) {
+#pragma unroll
+                        for (int ks = 0; ks < DP / 16; ++ks)
+#pragma unroll
+                            for (int y = 0; y < 2; ++y) {
+                                const int d = ks * 16 + y * 8 + 2 * t;
+                                q[ks][(R8 ? 1 : 2) * y + x] = in_row && d < D ? __ldg(reinterpret_cast<const uint32_t *>(src + d)) : 0u;
+                            }
+                    } else {
+                        // 16-bit chunk order of the int8 keys: step 4 i + w, lane t <-> columns 16 (4 i + t) + 4 w ..+3.
+                        // fp16 operands: the row times a power of two that puts its largest value near 2^14, exactly.
+                        uint32_t raw[DP / 16][2];
+                        uint32_t top = 0u;
+#pragma unroll
+                        for (int ks = 0; ks < DP / 16; ++ks) {
+                            const int d = 16 * (4 * (ks / 4) + t) + 4 * (ks % 4);
+                            const uint2 v = in_row && d < D ? __ldg(reinterpret_cast<const uint2 *>(src + d)) : make_uint2(0u, 0u);
+                            raw[ks][0] = v.x;
+                            raw[ks][1] = v.y;
+                            top = max_u16x2(top, v.x & 0x7FFF7FFFu);
+                            top = max_u16x2(top, v.y & 0x7FFF7FFFu);
+                        }
+                        int e = (int)(max(top >> 16, top & 0xFFFFu) >> 7);        // largest biased exponent
+                        e = max(e, __shfl_xor_sync(0xffffffffu, e, 1));
+                        e = max(e, __shfl_xor_sync(0xffffffffu, e, 2));
+                        e = min(max(e, 24), 254);
+                        const float up = __uint_as_float((uint32_t)(127 + 13 + 127 - e) << 23);   // 2^(13 - (e - 127))
+                        qs[x] *= __uint_as_float((uint32_t)(e - 13) << 23);                       // 2^((e - 127) - 13)
+#pragma unroll
+                        for (int ks = 0; ks < DP / 16; ++ks)
+#pragma unroll
+                            for (int y = 0; y < 2; ++y) {
+                                const __half2 f = __floats2half2_rn(__uint_as_float(raw[ks][y] << 16) * up,
+                                                                    __uint_as_float(raw[ks][y] & 0xFFFF0000u) * up);
+                                q[ks][(R8 ? 1 : 2) * y + x] = *reinterpret_cast<const uint32_t *>(&f);
+                            }
+                    }
+                }
+            }
+
+            // ---- scores ---------------------------------------------------------------------------
+            const uint32_t base = ring + (i % STAGES) * Sh::kStage;
+            const uint32_t mask = lds_u32(base + 2 * Sh::kKv + Sh::kScales);
+            float sc[2][4] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+            auto q_frag = [&](int ks, uint32_t (&f)[4]) {
+                f[0] = q[ks][0];
+                f[1] = R8 ? 0u : q[ks][1];
+                f[2] = q[ks][R8 ? 1 : 2];
+                f[3] = R8 ? 0u : q[ks][R8 ? 0 : 3];
+            };
+            if (!INT8) {
+#pragma unroll
+                for (int x = 0; x < DP / 32; ++x) {
+                    uint32_t f0[4], f1[4];
+                    q_frag(2 * x, f0);
+                    q_frag(2 * x + 1, f1);
+#pragma unroll
+                    for (int nt = 0; nt < 2; ++nt) {
+                        const int r = nt * 8 + (lane & 7), c = 4 * x + (lane >> 3);
+                        uint32_t kf[4];
+                        ldsm_x4(base + r * Sh::kRow + ((c ^ (r & 7)) << 4), kf);
+                        mma<false>(sc[nt], f0, kf[0], kf[1]);
+                        mma<false>(sc[nt], f1, kf[2], kf[3]);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int x = 0; x < DP / 64; ++x) {
+#pragma unroll
+                    for (int nt = 0; nt < 2; ++nt) {
+                        const int r = nt * 8 + g, c = 4 * x + t;
+                        const uint4 w = lds_v4(base + r * Sh::kRow + ((c ^ swz8<Sh::kChunks>(r)) << 4));
+                        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            uint32_t f[4], b0, b1;
+                            q_frag(4 * x + y, f);
+                            codes_to_f16(ws[y], b0, b1);
+                            mma<true>(sc[nt], f, b0, b1);
+                        }
+                    }
+                }
+            }
+            float vsc[2][2];
+            float tops[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt) {
+                float ks0 = 1.0f, ks1 = 1.0f;
+                if (INT8) {
+                    const uint32_t at0 = base + 2 * Sh::kKv + (nt * 8 + 2 * t) * 4;
+                    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(ks0), "=f"(ks1) : "r"(at0));
+                    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(vsc[nt][0]), "=f"(vsc[nt][1]) : "r"(at0 + kTile * 4));
+                }
+                const uint32_t bits = mask >> (nt * 8 + 2 * t);
+#pragma unroll
+                for (int x = 0; x < (R8 ? 1 : 2); ++x) {
+                    sc[nt][2 * x] = bits & 1u ? sc[nt][2 * x] * (INT8 ? qs[x] * ks0 : qs[x]) : -INFINITY;
+                    sc[nt][2 * x + 1] = bits & 2u ? sc[nt][2 * x + 1] * (INT8 ? qs[x] * ks1 : qs[x]) : -INFINITY;
+                    tops[x] = fmaxf(tops[x], fmaxf(sc[nt][2 * x], sc[nt][2 * x + 1]));
+                }
+            }
+            // ---- running maximum, weights ---------------------------------------------------------------
+            float keep[2] = {1.0f, 1.0f};
+#pragma unroll
+            for (int x = 0; x < (R8 ? 1 : 2); ++x) {
+                tops[x] = fmaxf(tops[x], __shfl_xor_sync(0xffffffffu, tops[x], 1));
+                tops[x] = fmaxf(tops[x], __shfl_xor_sync(0xffffffffu, tops[x], 2));
+                const float now = fmaxf(m[x], tops[x]);
+                const float zero = now == -INFINITY ? 0.0f : now;   // nothing seen so far: every weight is 0
+                keep[x] = ex2(m[x] - zero);
+                m[x] = now;
+                l[x] *= keep[x];
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const float w = ex2(sc[nt][2 * x + y] - zero);
+                        l[x] += w;
+                        sc[nt][2 * x + y] = w;
+                    }
+            }
+            if (INT8) {
+                // the weights take the values' scales, over a power of two that only grows
+                float top = fmaxf(fmaxf(fabsf(vsc[0][0]), fabsf(vsc[0][1])), fmaxf(fabsf(vsc[1][0]), fabsf(vsc[1][1])));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                if (top > vf) {
+                    const uint32_t e = min(max((__float_as_uint(top) >> 23) + 1u, 16u), 253u);   // 2^(e - 127) > top
+                    const float old = vf;
+                    vf = __uint_as_float(e << 23);
+                    vinv = __uint_as_float((254u + 14u - e) << 23);   // 2^14 / vf
+                    keep[0] *= old / vf;
+                    keep[1] *= old / vf;
+                }
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const float f = vsc[nt][y] * vinv;
+                        sc[nt][y] *= f;
+                        if (!R8)
+                            sc[nt][2 + y] *= f;
+                    }
+            }
+            if (__any_sync(0xffffffffu, keep[0] != 1.0f || (!R8 && keep[1] != 1.0f))) {
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    o[j][0] *= keep[0];
+                    o[j][1] *= keep[0];
+                    o[j][2] *= keep[R8 ? 0 : 1];
+                    o[j][3] *= keep[R8 ? 0 : 1];
+                }
+            }
+            uint32_t hi[4], lo[4];
+            split2<INT8>(sc[0][0], sc[0][1], hi[0], lo[0]);
+            split2<INT8>(sc[1][0], sc[1][1], hi[2], lo[2]);
+            if (R8) {
+                hi[1] = lo[0];
+                hi[3] = lo[2];
+            } else {
+                split2<INT8>(sc[0][2], sc[0][3], hi[1], lo[1]);
+                split2<INT8>(sc[1][2], sc[1][3], hi[3], lo[3]);
+            }
+            // ---- values ---------------------------------------------------------------------------------
+            const uint32_t vb = base + Sh::kKv;
+            if (!INT8) {
+#pragma unroll
+                for (int j = 0; j < NT; j += 2) {
+                    const int r = (lane & 7) + ((lane >> 3) & 1) * 8, c = j + (lane >> 4);
+                    uint32_t vfr[4];
+                    ldsm_x4_trans(vb + r * Sh::kRow + ((c ^ (r & 7)) << 4), vfr);
+                    mma<false>(o[j], hi, vfr[0], vfr[1]);
+                    mma<false>(o[j + 1], hi, vfr[2], vfr[3]);
+                    if (!R8) {
+                        mma<false>(o[j], lo, vfr[0], vfr[1]);
+                        mma<false>(o[j + 1], lo, vfr[2], vfr[3]);
+                    }
+                }
+            } else {
+                // lane (g, t) reads tokens 2t, 2t+1, 2t+8, 2t+9 at the columns of its g: with 16-byte chunks, output tile
+                // 16 x + y, column n <-> column 16 (8 x + n) + y; with 64 columns, tile y <-> column 8 n + y
+                constexpr int X = DP >= 128 ? DP / 128 : 1, W = DP >= 128 ? 4 : 2;
+#pragma unroll
+                for (int x = 0; x < X; ++x) {
+                    uint32_t w[4][W];
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        const int r = 2 * t + (y & 1) + (y >> 1) * 8;
+                        if (DP >= 128) {
+                            const uint4 v = lds_v4(vb + r * Sh::kRow + (((8 * x + g) ^ swz8<Sh::kChunks>(r)) << 4));
+                            w[y][0] = v.x;
+                            w[y][1] = v.y;
+                            w[y][W - 2] = v.z;
+                            w[y][W - 1] = v.w;
+                        } else {
+                            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];"
+                                         : "=r"(w[y][0]), "=r"(w[y][1])
+                                         : "r"(vb + r * Sh::kRow + (((g >> 1) ^ swz8<Sh::kChunks>(r)) << 4) + (g & 1) * 8));
+                        }
+                    }
+#pragma unroll
+                    for (int z = 0; z < W; ++z) {
+                        const uint32_t b0[4] = {pair_to_f16<0>(w[0][z], w[1][z]), pair_to_f16<1>(w[0][z], w[1][z]),
+                                                pair_to_f16<2>(w[0][z], w[1][z]), pair_to_f16<3>(w[0][z], w[1][z])};
+                        const uint32_t b1[4] = {pair_to_f16<0>(w[2][z], w[3][z]), pair_to_f16<1>(w[2][z], w[3][z]),
+                                                pair_to_f16<2>(w[2][z], w[3][z]), pair_to_f16<3>(w[2][z], w[3][z])};
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            mma<true>(o[(x * W + z) * 4 + y], hi, b0[y], b1[y]);
+                            if (!R8)
+                                mma<true>(o[(x * W + z) * 4 + y], lo, b0[y], b1[y]);
+                        }
+                    }
+                }
+            }
+
+            // ---- the end of the sequence, or of the run ----------------------------------------------------
+            const bool ends = at.k == at.s.tiles - 1, stop = i == n - 1;
+            if (ends || stop) {
+#pragma unroll
+                for (int x = 0; x < (R8 ? 1 : 2); ++x) {
+                    l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
+                    l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
+                }
+                const bool final = ends && whole;
+                const int slot = 2 * warp + (whole ? 1 : 0);
+                float *part = p.warp_part + ((size_t)blockIdx.x * 2 * WARPS + slot) * part_size;
+                const float f = INT8 ? vf * 6.103515625e-05f : 1.0f;   // 2^-14
+#pragma unroll
+                for (int x = 0; x < (R8 ? 1 : 2); ++x) {
+                    const int r = g + 8 * x;
+                    if (r >= rows)
+                        continue;
+                    const float inv = final ? (l[x] == 0.0f ? 0.0f : f / l[x]) : f;
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) {
+                        float v0 = o[j][2 * x], v1 = o[j][2 * x + 1];
+                        if (R8) {
+                            v0 += o[j][2];
+                            v1 += o[j][3];
+                        }
+                        v0 *= inv;
+                        v1 *= inv;
+                        int d0 = 8 * j + 2 * t, d1 = d0 + 1;
+                        if (INT8) {
+                            d0 = DP >= 128 ? 16 * (8 * (j / 16) + 2 * t) + j % 16 : 16 * t + j;
+                            d1 = d0 + (DP >= 128 ? 16 : 8);
+                        }
+                        if (final) {
+                            if (d0 < D)
+                                a.out[(head0 + r) * D + d0] = __float2bfloat16_rn(v0);
+                            if (d1 < D)
+                                a.out[(head0 + r) * D + d1] = __float2bfloat16_rn(v1);
+                        } else {
+                            float *row = part + 2 * p.rows + (size_t)r * D;
+                            if (d0 < D)
+                                row[d0] = v0;
+                            if (d1 < D)
+                                row[d1] = v1;
+                        }
+                    }
+                    if (t == 0) {
+                        if (!final) {
+                            part[2 * r] = m[x];
+                            part[2 * r + 1] = l[x];
+                        } else if (a.lse) {
+                            a.lse[head0 + r] = (m[x] + log2f(l[x])) * kLn2;
+                        }
+                    }
+                }
+                if (!final && lane == 0) {
+                    part_b[slot] = at.b;
+                    part_u[slot] = at.u;
+                    part_begins[slot] = whole;
+                    part_ends[slot] = ends;
+                }
+                whole = fresh = true;
+            }
+            at.next(a, p.units);
+        }
+        cp_wait<0>();
+    }
+    __syncthreads();
+
+    // ---- join the warps' parts: runs of slots of the same sequence; a (run, row) per warp ------------
+    // A run that holds its sequence's first and last tile is an output; the others are this CTA's parts: slot 0 for
+    // a sequence begun before it, slot 1 for one that goes on behind it.
+    int first_of[2] = {-1, -1}, task = 0;
+    auto join_row = [&](const float *parts, size_t step, const int *pick, int begin, int count, int r, float &top, float &sum,
+                        float (&acc)[DP / 32]) {
+        top = -INFINITY;
+        sum = 0.0f;
+#pragma unroll
+        for (int y = 0; y < DP / 32; ++y)
+            acc[y] = 0.0f;
+        for (int e = begin; e < begin + count; ++e)
+            if (!pick || pick[e] >= 0)
+                top = fmaxf(top, __ldcg(parts + e * step + 2 * r));
+        const float zero = top == -INFINITY ? 0.0f : top;
+        for (int e = begin; e < begin + count; ++e) {
+            if (pick && pick[e] < 0)
+                continue;
+            const float *part = parts + e * step;
+            const float w = ex2(__ldcg(part + 2 * r) - zero);
+            sum = fmaf(w, __ldcg(part + 2 * r + 1), sum);
+#pragma unroll
+            for (int y = 0; y < DP / 32; ++y)
+                if (32 * y + lane < D)
+                    acc[y] = fmaf(w, __ldcg(part + 2 * p.rows + (size_t)r * D + 32 * y + lane), acc[y]);
+        }
+    };
+    auto write_row = [&](int b, int u, int r, float top, float sum, const float (&acc)[DP / 32]) {
+        const int64_t row = (int64_t)b * a.Hq + (u / p.blocks) * p.group + (u % p.blocks) * 16 + r;
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+        for (int y = 0; y < DP / 32; ++y)
+            if (32 * y + lane < D)
+                a.out[row * D + 32 * y + lane] = __float2bfloat16_rn(acc[y] * inv);
+        if (lane == 0 && a.lse)
+            a.lse[row] = (top + log2f(sum)) * kLn2;
+    };
+    const float *mine = p.warp_part + (size_t)blockIdx.x * 2 * WARPS * part_size;
+    for (int e = 0; e < 2 * WARPS;) {
+        if (part_b[e] < 0) {
+            ++e;
             continue;
         }
-        const int64_t ka = page * a.kv.ks[0] + t * a.kv.ks[1] + h * a.kv.ks[2];
-        const int64_t va = page * a.kv.vs[0] + t * a.kv.vs[1] + h * a.kv.vs[2];
-        const int64_t sa = page * a.kv.ss[0] + t * a.kv.ss[1] + h * a.kv.ss[2];
-        float s = 0.0f;
-        for (int i = 0; i < kCols; ++i)
-            if (lane + 32 * i < D)
-                s = fmaf(q[i], element(a.kv.k, ka + lane + 32 * i, a.kv.int8), s);
-        for (int x = 16; x > 0; x >>= 1)
-            s += __shfl_xor_sync(0xffffffffu, s, x);
-        s *= a.scale * (a.kv.int8 ? a.kv.k_scale[sa] : 1.0f);
-        const float top = fmaxf(m, s), base = top == -INFINITY ? 0.0f : top;
-        const float old = expf(m - base), p = expf(s - base);
-        m = top;
-        l = l * old + p;
-        const float pv = p * (a.kv.int8 ? a.kv.v_scale[sa] : 1.0f);
-        for (int i = 0; i < kCols; ++i)
-            if (lane + 32 * i < D)
-                o[i] = fmaf(pv, element(a.kv.v, va + lane + 32 * i, a.kv.int8), o[i] * old);
+        int end = e + 1, last = e;
+        while (end < 2 * WARPS && (part_b[end] < 0 || (part_b[end] == part_b[e] && part_u[end] == part_u[e]))) {
+            if (part_b[end] >= 0)
+                last = end;
+            ++end;
+        }
+        const bool begins = part_begins[e], ends = part_ends[last];
+        const int b = part_b[e], u = part_u[e], rows = min(p.group - (u % p.blocks) * 16, p.rows);
+        const int slot = begins ? 1 : 0;
+        if (!(begins && ends))
+            first_of[slot] = e;
+        for (int r = 0; r < rows; ++r, ++task) {
+            if (task % WARPS != warp)
+                continue;
+            float top, sum, acc[DP / 32];
+            join_row(mine, part_size, part_b, e, last - e + 1, r, top, sum, acc);
+            if (begins && ends) {
+                write_row(b, u, r, top, sum, acc);
+            } else {
+                float *part = p.cta_part + ((size_t)blockIdx.x * 2 + slot) * part_size;
+#pragma unroll
+                for (int y = 0; y < DP / 32; ++y)
+                    if (32 * y + lane < D)
+                        part[2 * p.rows + (size_t)r * D + 32 * y + lane] = acc[y];
+                if (lane == 0) {
+                    part[2 * r] = top;
+                    part[2 * r + 1] = sum;
+                }
+            }
+        }
+        e = end;
     }
-    if (lane == 0) {
-        om[warp] = m;
-        ol[warp] = l;
-    }
-    for (int i = 0; i < kCols; ++i)
-        oo[warp][lane + 32 * i] = o[i];
+    if (first_of[0] < 0 && first_of[1] < 0)
+        return;
+
+    // ---- join the CTAs' parts: the last one to arrive at a sequence's counter -------------------------
+    __threadfence();
     __syncthreads();
-    float top = -INFINITY, sum = 0.0f;
-    for (int w = 0; w < kWarps; ++w)
-        top = fmaxf(top, om[w]);
-    const float base = top == -INFINITY ? 0.0f : top;
-    for (int w = 0; w < kWarps; ++w)
-        sum += ol[w] * expf(om[w] - base);
-    for (int d = threadIdx.x; d < D; d += kWarps * 32) {
-        float v = 0.0f;
-        for (int w = 0; w < kWarps; ++w)
-            v += oo[w][d] * expf(om[w] - base);
-        a.out[((int64_t)b * a.Hq + hq) * D + d] = __float2bfloat16_rn(sum == 0.0f ? 0.0f : v / sum);
+    for (int slot = 0; slot < 2; ++slot) {
+        const int e = first_of[slot];
+        if (e < 0)
+            continue;
+        const int b = part_b[e], u = part_u[e], rows = min(p.group - (u % p.blocks) * 16, p.rows);
+        const int bucket = b / per;
+        long long s0 = scan[bucket];
+        for (int x = bucket * per; x < b; ++x)
+            s0 += (long long)sequence(a, x).tiles * p.units;
+        const int tiles = sequence(a, b).tiles;
+        s0 += (long long)u * tiles;
+        const int from = (int)(s0 / span), to = (int)((s0 + tiles - 1) / span), count = to - from + 1;
+        if (threadIdx.x == 0) {
+            // (tag, arrivals) in one word: whatever the workspace held before this call counts as none
+            unsigned long long *word = p.arrived + from, seen = *reinterpret_cast<volatile unsigned long long *>(word), next;
+            int arrived;
+            do {
+                const unsigned long long old = seen;
+                arrived = (old >> 16) == p.tag ? (int)(old & 0xFFFFu) + 1 : 1;
+                next = arrived == count ? 0ull : (p.tag << 16) | (unsigned long long)arrived;
+                seen = atomicCAS(word, old, next);
+                if (seen == old)
+                    break;
+            } while (true);
+            last_flag[slot] = arrived == count;
+        }
+        __syncthreads();
+        if (!last_flag[slot])
+            continue;
+        __threadfence();
+        // CTA `from` left its part in slot 1, the others in slot 0
+        const float *parts = p.cta_part + (size_t)from * 2 * part_size;
+        float *stage = reinterpret_cast<float *>(smem_raw);   // [WARPS][rows][D + 2]
+        const int share = (count + WARPS - 1) / WARPS;
+        for (int r = 0; r < rows; ++r) {
+            float top = -INFINITY, sum = 0.0f, acc[DP / 32];
+#pragma unroll
+            for (int y = 0; y < DP / 32; ++y)
+                acc[y] = 0.0f;
+            const int x0 = min(count, warp * share), x1 = min(count, x0 + share);
+            for (int x = x0; x < x1; ++x)
+                top = fmaxf(top, __ldcg(parts + (2 * x + (x == 0)) * part_size + 2 * r));
+            const float zero = top == -INFINITY ? 0.0f : top;
+#pragma unroll 4
+            for (int x = x0; x < x1; ++x) {
+                const float *part = parts + (2 * x + (x == 0)) * part_size;
+                const float w = ex2(__ldcg(part + 2 * r) - zero);
+                sum = fmaf(w, __ldcg(part + 2 * r + 1), sum);
+#pragma unroll
+                for (int y = 0; y < DP / 32; ++y)
+                    if (32 * y + lane < D)
+                        acc[y] = fmaf(w, __ldcg(part + 2 * p.rows + (size_t)r * D + 32 * y + lane), acc[y]);
+            }
+            float *row = stage + ((size_t)warp * p.rows + r) * (D + 2);
+            if (lane == 0) {
+                row[0] = top;
+                row[1] = sum;
+            }
+#pragma unroll
+            for (int y = 0; y < DP / 32; ++y)
+                if (32 * y + lane < D)
+                    row[2 + 32 * y + lane] = acc[y];
+        }
+        __syncthreads();
+        for (int r = warp; r < rows; r += WARPS) {
+            float top = -INFINITY, sum = 0.0f, acc[DP / 32];
+#pragma unroll
+            for (int y = 0; y < DP / 32; ++y)
+                acc[y] = 0.0f;
+            for (int x = 0; x < WARPS; ++x)
+                top = fmaxf(top, stage[((size_t)x * p.rows + r) * (D + 2)]);
+            const float zero = top == -INFINITY ? 0.0f : top;
+            for (int x = 0; x < WARPS; ++x) {
+                const float *row = stage + ((size_t)x * p.rows + r) * (D + 2);
+                const float w = ex2(row[0] - zero);
+                sum = fmaf(w, row[1], sum);
+#pragma unroll
+                for (int y = 0; y < DP / 32; ++y)
+                    if (32 * y + lane < D)
+                        acc[y] = fmaf(w, row[2 + 32 * y + lane], acc[y]);
+            }
+            write_row(b, u, r, top, sum, acc);
+        }
+        __syncthreads();
     }
-    if (threadIdx.x == 0 && a.lse)
-        a.lse[(int64_t)b * a.Hq + hq] = top + logf(sum);
+}
+
+// The workspace's layout: counters, then the warps' and the CTAs' partial states.
+struct Layout {
+    int ctas, warps, rows;
+    size_t arrived, warp_part, cta_part, bytes;
+};
+
+constexpr int kMaxWarps = 8;
+
+Layout layout(const KvCache &kv, int64_t Hq)
+{
+    Layout w;
+    const int group = (int)(Hq / kv.heads);
+    w.ctas = device_sm_count();
+    w.warps = kMaxWarps;
+    w.rows = group < 16 ? group : 16;
+    const size_t part = (size_t)w.rows * (kv.dim + 2) * sizeof(float);
+    w.arrived = 0;
+    w.warp_part = ((size_t)w.ctas * 8 + 255) / 256 * 256;
+    w.cta_part = w.warp_part + (size_t)w.ctas * w.warps * 2 * part;
+    w.bytes = w.cta_part + (size_t)w.ctas * 2 * part;
+    return w;
+}
+
+template <int DP, bool INT8, bool R8, int WARPS, int STAGES>
+cudaError_t launch(const AttnArgs &a, const AttnPlan &p, int ctas, cudaStream_t stream)
+{
+    constexpr int smem = WARPS * STAGES * Shape<DP, INT8>::kStage;
+    static_assert(WARPS <= kMaxWarps && smem >= WARPS * 16 * (DP + 2) * 4 && smem <= 226 * 1024,
+                  "the ring, and room for the last join");
+    auto kernel = paged_attention_kernel<DP, INT8, R8, WARPS, STAGES>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess)
+        return e;
+    return tc::launch_pdl(kernel, dim3(ctas), dim3(WARPS * 32), (size_t)smem, stream, a, p);
+}
+
+template <bool INT8, bool R8>
+cudaError_t launch_dim(const AttnArgs &a, const AttnPlan &p, int ctas, cudaStream_t stream)
+{
+    if (a.kv.dim <= 64)
+        return launch<64, INT8, R8, 8, INT8 ? 11 : 6>(a, p, ctas, stream);
+    if (a.kv.dim <= 128)
+        return launch<128, INT8, R8, 8, INT8 ? 6 : 3>(a, p, ctas, stream);
+    return launch<256, INT8, R8, INT8 ? 8 : 4, 3>(a, p, ctas, stream);
+}
+
+// A number for each call that no earlier content of a workspace's counters holds
+// (48 bits, counted up from where the process began).
+unsigned long long next_tag()
+{
+    static std::atomic<unsigned long long> tag{0x5A3D8000001ull};
+    return tag.fetch_add(1, std::memory_order_relaxed) & 0xFFFFFFFFFFFFull;
 }
 
 }  // namespace
 
-size_t paged_attention_workspace(const KvCache &, int64_t, int64_t) { return 16; }
+size_t paged_attention_workspace(const KvCache &kv, int64_t, int64_t Hq) { return layout(kv, Hq).bytes; }
 
 cudaError_t launch_paged_attention(const AttnArgs &a, cudaStream_t stream)
 {
-    return tc::launch_pdl(paged_attention_kernel, dim3((unsigned)(a.B * a.Hq)), dim3(kWarps * 32), 0, stream, a);
+    const Layout w = layout(a.kv, a.Hq);
+    char *ws = static_cast<char *>(a.ws);
+    AttnPlan p;
+    p.group = a.Hq / a.kv.heads;
+    p.rows = w.rows;
+    p.blocks = (p.group + 15) / 16;
+    p.units = a.kv.heads * p.blocks;
+    p.arrived = reinterpret_cast<unsigned long long *>(ws + w.arrived);
+    p.warp_part = reinterpret_cast<float *>(ws + w.warp_part);
+    p.cta_part = reinterpret_cast<float *>(ws + w.cta_part);
+    p.tag = next_tag();
+    const bool r8 = p.group <= 8;
+    if (a.kv.int8)
+        return r8 ? launch_dim<true, true>(a, p, w.ctas, stream) : launch_dim<true, false>(a, p, w.ctas, stream);
+    return r8 ? launch_dim<false, true>(a, p, w.ctas, stream) : launch_dim<false, false>(a, p, w.ctas, stream);
 }
 
 }  // namespace s3d8
