@@ -57,20 +57,23 @@ __device__ __forceinline__ Seq sequence(const AttnArgs &a, int b)
     return s;
 }
 
-// A position in the list of tiles: tile k of unit u (key/value head, block of
-// query rows) of sequence b.
+// A position in the list of tiles: tile k of key/value head h, block of query
+// rows blk, of sequence b.
 struct Cursor {
-    int b, u, k;
+    int b, h, blk, k;
     Seq s;
 
-    __device__ __forceinline__ void next(const AttnArgs &a, int units)
+    __device__ __forceinline__ void next(const AttnArgs &a, int blocks)
     {
         if (++k < s.tiles)
             return;
         k = 0;
-        if (++u < units)
+        if (++blk < blocks)
             return;
-        u = 0;
+        blk = 0;
+        if (++h < a.kv.heads)
+            return;
+        h = 0;
         for (++b; b < a.B; ++b) {
             s = sequence(a, b);
             if (s.tiles > 0)
@@ -82,6 +85,10 @@ struct Cursor {
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int bytes)
 {
     asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, int bytes)
 {
@@ -163,17 +170,20 @@ __device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t &p01, uint32_t
     p23 = tc::f16x2_sub(prmt(u, magic, 0x4342), 0x64806480u);
 }
 
-// Bytes i of two words as a pair of fp16.
-template <int I>
-__device__ __forceinline__ uint32_t pair_to_f16(uint32_t w0, uint32_t w1)
+// Byte i of either word as pair i of fp16, exactly.
+__device__ __forceinline__ void pairs_to_f16(uint32_t w0, uint32_t w1, uint32_t (&f)[4])
 {
-    const uint32_t both = prmt(w0, w1, I | ((4 + I) << 8));    // low half: {w0[I], -, w1[I], -}
-    return tc::f16x2_sub(prmt(both ^ 0x80808080u, 0x64646464u, 0x4240), 0x64806480u);
+    const uint32_t lo = prmt(w0, w1, 0x5140) ^ 0x80808080u, hi = prmt(w0, w1, 0x7362) ^ 0x80808080u, magic = 0x64646464u;
+    f[0] = tc::f16x2_sub(prmt(lo, magic, 0x4140), 0x64806480u);
+    f[1] = tc::f16x2_sub(prmt(lo, magic, 0x4342), 0x64806480u);
+    f[2] = tc::f16x2_sub(prmt(hi, magic, 0x4140), 0x64806480u);
+    f[3] = tc::f16x2_sub(prmt(hi, magic, 0x4342), 0x64806480u);
 }
 
 struct AttnPlan {
     int units, blocks, rows;     // per sequence: key/value heads x blocks of query rows; rows per block at most
     int group;                   // query heads per key/value head
+    int log_page;                // of a page size that is a power of two, else -1
     float *warp_part, *cta_part; // partial states
     unsigned long long *arrived; // per CTA
     unsigned long long tag;
@@ -182,7 +192,9 @@ struct AttnPlan {
 // One partial state in the workspace: rows x (m, l), then rows x D output sums.
 __device__ __forceinline__ size_t part_floats(int rows, int D) { return (size_t)rows * (D + 2); }
 
-template <int DP, bool INT8, bool R8, int WARPS, int STAGES>
+// ALIGNED: pages of a multiple of 16 tokens, so that a tile lies in one page and
+// its rows follow one another at one stride.
+template <int DP, bool INT8, bool R8, bool ALIGNED, int WARPS, int STAGES>
 __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __grid_constant__ AttnArgs a,
                                                                      const __grid_constant__ AttnPlan p)
 {
@@ -281,63 +293,108 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
                 left -= (long long)in.s.tiles * p.units;
                 in.s = sequence(a, ++in.b);
             }
-            in.u = (int)(left / in.s.tiles);
-            in.k = (int)(left % in.s.tiles);
+            const int u = (int)(left / in.s.tiles);
+            in.k = (int)(left - (long long)u * in.s.tiles);
+            in.h = u / p.blocks;
+            in.blk = u - in.h * p.blocks;
         }
         Cursor at = in;                       // the tile being computed; `in`: the tile being fetched
         const uint32_t ring = smem_addr(smem_raw) + warp * (STAGES * Sh::kStage);
 
-        // ---- fetching: lanes 0-15 hold the tile's key rows, lanes 16-31 its value rows ------
-        const int side = lane >> 4;
-        int64_t row_off = 0;                  // of the next tile to fetch: offset inside its page,
-        int64_t scale_off = 0;
-        int row_page = -1;                    // its page,
-        bool row_seen = false;                // and whether it holds a visible token
+        // ---- fetching: pages are looked up one tile ahead of the copies -----------------------
+        const int side = lane >> 4;           // lanes 0-15 stand for the tile's keys, lanes 16-31 for its values
+        constexpr int ES = INT8 ? 1 : 2, RPI = 32 / Sh::kChunks;   // element bytes; rows per round of 32 chunks
+        const int fr = lane / Sh::kChunks, fc = lane % Sh::kChunks;
+        const uint32_t lane_dst = fr * Sh::kRow + ((fc ^ (INT8 ? swz8<Sh::kChunks>(fr) : fr)) << 4);
+        // round i of the copies: rows i RPI + fr; their swizzle differs from lane_dst's by a constant
+        auto round_dst = [&](int i) {
+            const uint32_t flip = (INT8 ? swz8<Sh::kChunks>((i * RPI) & 7) : (i * RPI) & 7) << 4;
+            return i * RPI * Sh::kRow + (lane_dst ^ flip);
+        };
+        int64_t row_off = 0, scale_off = 0;   // of the next tile to fetch, inside its page
+        int row_page = -1, row_slot = 0;      // its page; ALIGNED: the tile's first slot
+        bool row_seen = false;                // whether there is a visible token
         auto look_up = [&](bool live) {
             row_seen = false;
             if (!live)
                 return;
-            const int tok = (in.s.first / kTile + in.k) * kTile + (lane & 15);
-            if (tok < in.s.first || tok >= in.s.len)
+            const int tok = (in.s.first / kTile + in.k) * kTile + (ALIGNED ? 0 : lane & 15);
+            if (!ALIGNED && (tok < in.s.first || tok >= in.s.len))
                 return;
             row_seen = true;
-            const int col = tok / S, slot = tok - col * S, h = in.u / p.blocks;
+            const int col = p.log_page >= 0 ? tok >> p.log_page : tok / S;
+            row_slot = tok - col * S;
             row_page = a.table[in.b * a.width + col];
-            const int64_t *st = side ? a.kv.vs : a.kv.ks;
-            row_off = slot * st[1] + h * st[2];
-            if (INT8)
-                scale_off = slot * a.kv.ss[1] + h * a.kv.ss[2];
+            if (!ALIGNED) {
+                const int64_t *st = side ? a.kv.vs : a.kv.ks;
+                row_off = row_slot * st[1] + in.h * st[2];
+                if (INT8)
+                    scale_off = row_slot * a.kv.ss[1] + in.h * a.kv.ss[2];
+            }
         };
+        // Copies the tile that `in` stands at, looked up before.
         auto fetch = [&](int stage) {
             const uint32_t base = ring + stage * Sh::kStage;
             const bool ok = row_seen && row_page >= 0 && row_page < a.kv.pages;
             if (row_seen && !ok)
-                atomicExch(a.status, kStatusBounds);   // its token stays masked
-            const char *src = static_cast<const char *>(side ? a.kv.v : a.kv.k);
-            if (ok)
-                src += (row_page * (side ? a.kv.vs[0] : a.kv.ks[0]) + row_off) * (INT8 ? 1 : 2);
-            const uint32_t mask = __ballot_sync(0xffffffffu, ok);
-            if (INT8) {
-                const float *sc = side ? a.kv.v_scale : a.kv.k_scale;
+                atomicExch(a.status, kStatusBounds);   // its tokens stay masked
+            const int row_bytes = D * ES;
+            uint32_t mask;
+            if (ALIGNED) {
+                const int tok = (in.s.first / kTile + in.k) * kTile;
+                const int lo = max(in.s.first - tok, 0), hi = min(in.s.len - tok, kTile);
+                mask = ok ? ((1u << hi) - 1u) & ~((1u << lo) - 1u) : 0u;
+                const int64_t page = ok ? row_page : 0;
+                if (INT8) {
+                    const int r = lane & 15;
+                    const float *sc = (side ? a.kv.v_scale : a.kv.k_scale) + page * a.kv.ss[0] +
+                                      (int64_t)(row_slot + r) * a.kv.ss[1] + in.h * a.kv.ss[2];
+                    cp_async4(base + 2 * Sh::kKv + side * (kTile * 4) + r * 4, sc, (mask >> r) & 1 ? 4 : 0);
+                }
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv) {
+                    const int64_t *st = kv ? a.kv.vs : a.kv.ks;
+                    const char *src = static_cast<const char *>(kv ? a.kv.v : a.kv.k) +
+                                      (page * st[0] + (int64_t)(row_slot + fr) * st[1] + in.h * st[2]) * ES + fc * 16;
+                    const int64_t step = st[1] * (ES * RPI);
+                    const uint32_t dst = base + kv * Sh::kKv;
+                    if (mask == 0xFFFFu && D == DP) {
+#pragma unroll
+                        for (int i = 0; i < kTile / RPI; ++i, src += step)
+                            cp_async16(dst + round_dst(i), src);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < kTile / RPI; ++i, src += step) {
+                            const bool live = ((mask >> (i * RPI + fr)) & 1) && fc * 16 < row_bytes;
+                            cp_async16(dst + round_dst(i), live ? src : static_cast<const char *>(a.kv.k), live ? 16 : 0);
+                        }
+                    }
+                }
+            } else {
+                const char *src = static_cast<const char *>(side ? a.kv.v : a.kv.k);
                 if (ok)
-                    sc += row_page * a.kv.ss[0] + scale_off;
-                cp_async4(base + 2 * Sh::kKv + side * (kTile * 4) + (lane & 15) * 4, sc, ok ? 4 : 0);
+                    src += (row_page * (side ? a.kv.vs[0] : a.kv.ks[0]) + row_off) * ES;
+                mask = __ballot_sync(0xffffffffu, ok);
+                if (INT8) {
+                    const float *sc = side ? a.kv.v_scale : a.kv.k_scale;
+                    if (ok)
+                        sc += row_page * a.kv.ss[0] + scale_off;
+                    cp_async4(base + 2 * Sh::kKv + side * (kTile * 4) + (lane & 15) * 4, sc, ok ? 4 : 0);
+                }
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv) {
+#pragma unroll
+                    for (int i = 0; i < kTile / RPI; ++i) {
+                        const int r = i * RPI + fr;
+                        const char *from = reinterpret_cast<const char *>(
+                            __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), kv * 16 + r));
+                        const bool live = ((mask >> r) & 1) && fc * 16 < row_bytes;
+                        cp_async16(base + kv * Sh::kKv + round_dst(i), live ? from + fc * 16 : from, live ? 16 : 0);
+                    }
+                }
             }
             if (lane == 0)
                 asm volatile("st.shared.u32 [%0], %1;" ::"r"(base + 2 * Sh::kKv + Sh::kScales), "r"(mask & 0xFFFFu) : "memory");
-            const int row_bytes = INT8 ? D : 2 * D;
-#pragma unroll
-            for (int kv = 0; kv < 2; ++kv) {
-#pragma unroll
-                for (int i = 0; i < kTile * Sh::kChunks / 32; ++i) {
-                    const int idx = i * 32 + lane, r = idx / Sh::kChunks, c = idx % Sh::kChunks;
-                    const char *from = reinterpret_cast<const char *>(
-                        __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(src), kv * 16 + r));
-                    const bool live = ((mask >> r) & 1) && c * 16 < row_bytes;
-                    const int phys = INT8 ? c ^ swz8<Sh::kChunks>(r) : c ^ (r & 7);
-                    cp_async16(base + kv * Sh::kKv + r * Sh::kRow + phys * 16, live ? from + c * 16 : from, live ? 16 : 0);
-                }
-            }
         };
 
         look_up(true);
@@ -347,7 +404,7 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
             if (fetched < n) {
                 fetch(s);
                 ++fetched;
-                in.next(a, p.units);
+                in.next(a, p.blocks);
                 look_up(fetched < n);
             }
             cp_commit();
@@ -367,14 +424,13 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
             if (fetched < n) {
                 fetch((i + STAGES - 1) % STAGES);
                 ++fetched;
-                in.next(a, p.units);
+                in.next(a, p.blocks);
                 look_up(fetched < n);
             }
             cp_commit();
 
-            const int h = at.u / p.blocks, r0 = (at.u % p.blocks) * 16;
-            const int rows = min(p.group - r0, p.rows);
-            const int64_t head0 = (int64_t)at.b * a.Hq + h * p.group + r0;   // query row of the state's row 0
+            const int rows = min(p.group - at.blk * 16, p.rows);
+            const int64_t head0 = (int64_t)at.b * a.Hq + at.h * p.group + at.blk * 16;   // query row of the state's row 0
             if (fresh) {
                 fresh = false;
 #pragma unroll
@@ -590,10 +646,9 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
                     }
 #pragma unroll
                     for (int z = 0; z < W; ++z) {
-                        const uint32_t b0[4] = {pair_to_f16<0>(w[0][z], w[1][z]), pair_to_f16<1>(w[0][z], w[1][z]),
-                                                pair_to_f16<2>(w[0][z], w[1][z]), pair_to_f16<3>(w[0][z], w[1][z])};
-                        const uint32_t b1[4] = {pair_to_f16<0>(w[2][z], w[3][z]), pair_to_f16<1>(w[2][z], w[3][z]),
-                                                pair_to_f16<2>(w[2][z], w[3][z]), pair_to_f16<3>(w[2][z], w[3][z])};
+                        uint32_t b0[4], b1[4];
+                        pairs_to_f16(w[0][z], w[1][z], b0);
+                        pairs_to_f16(w[2][z], w[3][z], b1);
 #pragma unroll
                         for (int y = 0; y < 4; ++y) {
                             mma<true>(o[(x * W + z) * 4 + y], hi, b0[y], b1[y]);
@@ -660,13 +715,13 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
                 }
                 if (!final && lane == 0) {
                     part_b[slot] = at.b;
-                    part_u[slot] = at.u;
+                    part_u[slot] = at.h * p.blocks + at.blk;
                     part_begins[slot] = whole;
                     part_ends[slot] = ends;
                 }
                 whole = fresh = true;
             }
-            at.next(a, p.units);
+            at.next(a, p.blocks);
         }
         cp_wait<0>();
     }
@@ -846,7 +901,7 @@ struct Layout {
     size_t arrived, warp_part, cta_part, bytes;
 };
 
-constexpr int kMaxWarps = 8;
+constexpr int kMaxWarps = 16;
 
 Layout layout(const KvCache &kv, int64_t Hq)
 {
@@ -863,27 +918,34 @@ Layout layout(const KvCache &kv, int64_t Hq)
     return w;
 }
 
-template <int DP, bool INT8, bool R8, int WARPS, int STAGES>
+template <int DP, bool INT8, bool R8, bool ALIGNED, int WARPS, int STAGES>
 cudaError_t launch(const AttnArgs &a, const AttnPlan &p, int ctas, cudaStream_t stream)
 {
     constexpr int smem = WARPS * STAGES * Shape<DP, INT8>::kStage;
     static_assert(WARPS <= kMaxWarps && smem >= WARPS * 16 * (DP + 2) * 4 && smem <= 226 * 1024,
                   "the ring, and room for the last join");
-    auto kernel = paged_attention_kernel<DP, INT8, R8, WARPS, STAGES>;
+    auto kernel = paged_attention_kernel<DP, INT8, R8, ALIGNED, WARPS, STAGES>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess)
         return e;
     return tc::launch_pdl(kernel, dim3(ctas), dim3(WARPS * 32), (size_t)smem, stream, a, p);
 }
 
-template <bool INT8, bool R8>
+template <bool INT8, bool R8, bool ALIGNED>
 cudaError_t launch_dim(const AttnArgs &a, const AttnPlan &p, int ctas, cudaStream_t stream)
 {
     if (a.kv.dim <= 64)
-        return launch<64, INT8, R8, 8, INT8 ? 11 : 6>(a, p, ctas, stream);
+        return launch<64, INT8, R8, ALIGNED, 8, INT8 ? 11 : 6>(a, p, ctas, stream);
     if (a.kv.dim <= 128)
-        return launch<128, INT8, R8, 8, INT8 ? 6 : 3>(a, p, ctas, stream);
-    return launch<256, INT8, R8, INT8 ? 8 : 4, 3>(a, p, ctas, stream);
+        return launch<128, INT8, R8, ALIGNED, INT8 ? 16 : 8, 3>(a, p, ctas, stream);
+    return launch<256, INT8, R8, ALIGNED, INT8 ? 8 : 4, 3>(a, p, ctas, stream);
+}
+
+template <bool INT8, bool R8>
+cudaError_t launch_pages(const AttnArgs &a, const AttnPlan &p, int ctas, cudaStream_t stream)
+{
+    return a.kv.page_size % kTile == 0 ? launch_dim<INT8, R8, true>(a, p, ctas, stream)
+                                       : launch_dim<INT8, R8, false>(a, p, ctas, stream);
 }
 
 // A number for each call that no earlier content of a workspace's counters holds
@@ -911,10 +973,14 @@ cudaError_t launch_paged_attention(const AttnArgs &a, cudaStream_t stream)
     p.warp_part = reinterpret_cast<float *>(ws + w.warp_part);
     p.cta_part = reinterpret_cast<float *>(ws + w.cta_part);
     p.tag = next_tag();
+    p.log_page = -1;
+    for (int i = 0; i < 31; ++i)
+        if (a.kv.page_size == 1 << i)
+            p.log_page = i;
     const bool r8 = p.group <= 8;
     if (a.kv.int8)
-        return r8 ? launch_dim<true, true>(a, p, w.ctas, stream) : launch_dim<true, false>(a, p, w.ctas, stream);
-    return r8 ? launch_dim<false, true>(a, p, w.ctas, stream) : launch_dim<false, false>(a, p, w.ctas, stream);
+        return r8 ? launch_pages<true, true>(a, p, w.ctas, stream) : launch_pages<true, false>(a, p, w.ctas, stream);
+    return r8 ? launch_pages<false, true>(a, p, w.ctas, stream) : launch_pages<false, false>(a, p, w.ctas, stream);
 }
 
 }  // namespace s3d8
