@@ -8,12 +8,12 @@
 // tiles through a ring of its own in shared memory (cp.async, no barrier with
 // other warps) and carries the softmax's running maximum m, sum l and the output
 // sums O in fp32:
-//   S = Q K^T (tensor cores, rows = the query heads of the key/value head),
-//   m' = max(m, S), O = 2^(m - m') O + 2^(S - m') V, l likewise.
-// The matrix products are mma.sync: 16 rows (tcgen05's smallest M is 64) at a rate
-// far below the tensor cores' limit.  The weights 2^(S - m') enter the second
-// product as a 16-bit value and its 16-bit remainder: with up to 8 query rows the
-// remainder takes the upper 8 rows of the same instruction.
+//   S = K Q^T (tensor cores, rows = tokens, columns = 8 or 16 query rows),
+//   m' = max(m, S), O = 2^(m - m') O + V^T 2^(S - m'), l likewise.
+// The matrix products are mma.sync (tcgen05's smallest tile is 64 rows, and the
+// rate needed here is far below the tensor cores' limit).  The weights 2^(S - m')
+// enter the second product as a 16-bit value and its 16-bit remainder, so that
+// they keep 16 bits or more.
 //
 // A run that ends inside a sequence leaves (m, l, O) in the workspace; the warps of
 // a CTA join theirs, and where a sequence crosses CTAs the last of them to arrive
@@ -127,6 +127,14 @@ __device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint3
                      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// Transposes an 8 x 8 matrix of 16-bit values held two a lane.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v)
+{
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
 __device__ __forceinline__ float ex2(float x)
 {
     float y;
@@ -194,12 +202,13 @@ __device__ __forceinline__ size_t part_floats(int rows, int D) { return (size_t)
 
 // ALIGNED: pages of a multiple of 16 tokens, so that a tile lies in one page and
 // its rows follow one another at one stride.
-template <int DP, bool INT8, bool R8, bool ALIGNED, int WARPS, int STAGES>
+// NB: blocks of 8 query rows.
+template <int DP, bool INT8, int NB, bool ALIGNED, int WARPS, int STAGES>
 __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __grid_constant__ AttnArgs a,
                                                                      const __grid_constant__ AttnPlan p)
 {
     using Sh = Shape<DP, INT8>;
-    constexpr int NT = DP / 8;                    // 8-column tiles of the output
+    constexpr int MT = DP / 16;                   // 16-column tiles of the output
     constexpr int kScanThreads = WARPS * 32;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     __shared__ long long scan[kScanThreads + 1];
@@ -410,10 +419,11 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
             cp_commit();
         }
 
-        // ---- state of the current sequence -----------------------------------------------------
-        float o[NT][4], m[2], l[2];
-        uint32_t q[DP / 16][R8 ? 2 : 4];
-        float qs[2] = {0.0f, 0.0f};           // factor of a score's row, log2(e) in it
+        // ---- state of the current sequence: O^T, 16 columns x 8 query rows a tensor-core tile ----
+        // lane (g, t) holds columns g and g + 8 of a tile for query rows 2t and 2t + 1
+        float o[MT][NB][4], m[NB][2], l[NB][2];
+        uint32_t q[DP / 16][NB][2];
+        float qs[NB][2];                      // factor of a query row's scores, log2(e) in it
         float vf = 0.0f, vinv = 0.0f;         // int8: the power of two that carries the value scales
         bool whole = at.k == 0;               // this warp has the sequence from its first tile on
         bool fresh = true;
@@ -433,36 +443,35 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
             const int64_t head0 = (int64_t)at.b * a.Hq + at.h * p.group + at.blk * 16;   // query row of the state's row 0
             if (fresh) {
                 fresh = false;
-#pragma unroll
-                for (int j = 0; j < NT; ++j)
-                    o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
-                m[0] = m[1] = -INFINITY;
-                l[0] = l[1] = 0.0f;
                 vf = vinv = 0.0f;
 #pragma unroll
-                for (int x = 0; x < (R8 ? 1 : 2); ++x) {
+                for (int x = 0; x < NB; ++x) {
+#pragma unroll
+                    for (int j = 0; j < MT; ++j)
+                        o[j][x][0] = o[j][x][1] = o[j][x][2] = o[j][x][3] = 0.0f;
+                    m[x][0] = m[x][1] = -INFINITY;
+                    l[x][0] = l[x][1] = 0.0f;
+                    qs[x][0] = qs[x][1] = a.scale * kLog2e;
                     const __nv_bfloat16 *src = a.q + (head0 + g + 8 * x) * D;
                     const bool in_row = g + 8 * x < rows;
-                    qs[x] = a.scale * kLog2e;
                     if (!INT8) {
 #pragma unroll
                         for (int ks = 0; ks < DP / 16; ++ks)
 #pragma unroll
                             for (int y = 0; y < 2; ++y) {
                                 const int d = ks * 16 + y * 8 + 2 * t;
-                                q[ks][(R8 ? 1 : 2) * y + x] = in_row && d < D ? __ldg(reinterpret_cast<const uint32_t *>(src + d)) : 0u;
+                                q[ks][x][y] = in_row && d < D ? __ldg(reinterpret_cast<const uint32_t *>(src + d)) : 0u;
                             }
                     } else {
-                        // 16-bit chunk order of the int8 keys: step 4 i + w, lane t <-> columns 16 (4 i + t) + 4 w ..+3.
+                        // chunk order of the int8 keys: step 4 i + w, lane t <-> columns 16 (4 i + t) + 4 w ..+3.
                         // fp16 operands: the row times a power of two that puts its largest value near 2^14, exactly.
-                        uint32_t raw[DP / 16][2];
                         uint32_t top = 0u;
 #pragma unroll
                         for (int ks = 0; ks < DP / 16; ++ks) {
                             const int d = 16 * (4 * (ks / 4) + t) + 4 * (ks % 4);
                             const uint2 v = in_row && d < D ? __ldg(reinterpret_cast<const uint2 *>(src + d)) : make_uint2(0u, 0u);
-                            raw[ks][0] = v.x;
-                            raw[ks][1] = v.y;
+                            q[ks][x][0] = v.x;
+                            q[ks][x][1] = v.y;
                             top = max_u16x2(top, v.x & 0x7FFF7FFFu);
                             top = max_u16x2(top, v.y & 0x7FFF7FFFu);
                         }
@@ -470,161 +479,156 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
                         e = max(e, __shfl_xor_sync(0xffffffffu, e, 1));
                         e = max(e, __shfl_xor_sync(0xffffffffu, e, 2));
                         e = min(max(e, 24), 254);
-                        const float up = __uint_as_float((uint32_t)(127 + 13 + 127 - e) << 23);   // 2^(13 - (e - 127))
-                        qs[x] *= __uint_as_float((uint32_t)(e - 13) << 23);                       // 2^((e - 127) - 13)
+                        const float up = __uint_as_float((uint32_t)(127 + 13 + 127 - e) << 23);    // 2^(13 - (e - 127))
+                        const float down = __uint_as_float((uint32_t)(e - 13) << 23);              // 2^((e - 127) - 13)
+                        qs[x][0] *= __shfl_sync(0xffffffffu, down, 8 * t);       // rows 2t and 2t + 1
+                        qs[x][1] *= __shfl_sync(0xffffffffu, down, 8 * t + 4);
 #pragma unroll
                         for (int ks = 0; ks < DP / 16; ++ks)
 #pragma unroll
                             for (int y = 0; y < 2; ++y) {
-                                const __half2 f = __floats2half2_rn(__uint_as_float(raw[ks][y] << 16) * up,
-                                                                    __uint_as_float(raw[ks][y] & 0xFFFF0000u) * up);
-                                q[ks][(R8 ? 1 : 2) * y + x] = *reinterpret_cast<const uint32_t *>(&f);
+                                const __half2 f = __floats2half2_rn(__uint_as_float(q[ks][x][y] << 16) * up,
+                                                                    __uint_as_float(q[ks][x][y] & 0xFFFF0000u) * up);
+                                q[ks][x][y] = *reinterpret_cast<const uint32_t *>(&f);
                             }
                     }
                 }
             }
 
-            // ---- scores ---------------------------------------------------------------------------
+            // ---- scores S^T = K Q^T: lane (g, t) holds tokens g and g + 8 of query rows 2t and 2t + 1 ----
             const uint32_t base = ring + (i % STAGES) * Sh::kStage;
             const uint32_t mask = lds_u32(base + 2 * Sh::kKv + Sh::kScales);
-            float sc[2][4] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
-            auto q_frag = [&](int ks, uint32_t (&f)[4]) {
-                f[0] = q[ks][0];
-                f[1] = R8 ? 0u : q[ks][1];
-                f[2] = q[ks][R8 ? 1 : 2];
-                f[3] = R8 ? 0u : q[ks][R8 ? 0 : 3];
-            };
+            float sc[NB][4];
+#pragma unroll
+            for (int x = 0; x < NB; ++x)
+                sc[x][0] = sc[x][1] = sc[x][2] = sc[x][3] = 0.0f;
             if (!INT8) {
+                const int r = lane & 15;
+                const uint32_t row = base + r * Sh::kRow;
 #pragma unroll
-                for (int x = 0; x < DP / 32; ++x) {
-                    uint32_t f0[4], f1[4];
-                    q_frag(2 * x, f0);
-                    q_frag(2 * x + 1, f1);
+                for (int ks = 0; ks < DP / 16; ++ks) {
+                    uint32_t kf[4];
+                    ldsm_x4(row + (((2 * ks + (lane >> 4)) ^ (r & 7)) << 4), kf);
 #pragma unroll
-                    for (int nt = 0; nt < 2; ++nt) {
-                        const int r = nt * 8 + (lane & 7), c = 4 * x + (lane >> 3);
-                        uint32_t kf[4];
-                        ldsm_x4(base + r * Sh::kRow + ((c ^ (r & 7)) << 4), kf);
-                        mma<false>(sc[nt], f0, kf[0], kf[1]);
-                        mma<false>(sc[nt], f1, kf[2], kf[3]);
-                    }
+                    for (int x = 0; x < NB; ++x)
+                        mma<false>(sc[x], kf, q[ks][x][0], q[ks][x][1]);
                 }
             } else {
 #pragma unroll
-                for (int x = 0; x < DP / 64; ++x) {
+                for (int y = 0; y < DP / 64; ++y) {
+                    const int c = 4 * y + t;
+                    const uint4 w0 = lds_v4(base + g * Sh::kRow + ((c ^ swz8<Sh::kChunks>(g)) << 4));
+                    const uint4 w1 = lds_v4(base + (g + 8) * Sh::kRow + ((c ^ swz8<Sh::kChunks>(g + 8)) << 4));
+                    const uint32_t u0[4] = {w0.x, w0.y, w0.z, w0.w}, u1[4] = {w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
-                    for (int nt = 0; nt < 2; ++nt) {
-                        const int r = nt * 8 + g, c = 4 * x + t;
-                        const uint4 w = lds_v4(base + r * Sh::kRow + ((c ^ swz8<Sh::kChunks>(r)) << 4));
-                        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
+                    for (int z = 0; z < 4; ++z) {
+                        uint32_t kf[4];
+                        codes_to_f16(u0[z], kf[0], kf[2]);
+                        codes_to_f16(u1[z], kf[1], kf[3]);
 #pragma unroll
-                        for (int y = 0; y < 4; ++y) {
-                            uint32_t f[4], b0, b1;
-                            q_frag(4 * x + y, f);
-                            codes_to_f16(ws[y], b0, b1);
-                            mma<true>(sc[nt], f, b0, b1);
-                        }
+                        for (int x = 0; x < NB; ++x)
+                            mma<true>(sc[x], kf, q[4 * y + z][x][0], q[4 * y + z][x][1]);
                     }
                 }
             }
-            float vsc[2][2];
-            float tops[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-            for (int nt = 0; nt < 2; ++nt) {
-                float ks0 = 1.0f, ks1 = 1.0f;
-                if (INT8) {
-                    const uint32_t at0 = base + 2 * Sh::kKv + (nt * 8 + 2 * t) * 4;
-                    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(ks0), "=f"(ks1) : "r"(at0));
-                    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(vsc[nt][0]), "=f"(vsc[nt][1]) : "r"(at0 + kTile * 4));
-                }
-                const uint32_t bits = mask >> (nt * 8 + 2 * t);
-#pragma unroll
-                for (int x = 0; x < (R8 ? 1 : 2); ++x) {
-                    sc[nt][2 * x] = bits & 1u ? sc[nt][2 * x] * (INT8 ? qs[x] * ks0 : qs[x]) : -INFINITY;
-                    sc[nt][2 * x + 1] = bits & 2u ? sc[nt][2 * x + 1] * (INT8 ? qs[x] * ks1 : qs[x]) : -INFINITY;
-                    tops[x] = fmaxf(tops[x], fmaxf(sc[nt][2 * x], sc[nt][2 * x + 1]));
-                }
+            float ks0 = 1.0f, ks1 = 1.0f, vs0 = 0.0f, vs1 = 0.0f;
+            if (INT8) {
+                const uint32_t at0 = base + 2 * Sh::kKv + g * 4;
+                ks0 = __uint_as_float(lds_u32(at0));
+                ks1 = __uint_as_float(lds_u32(at0 + 32));
+                vs0 = __uint_as_float(lds_u32(at0 + kTile * 4));
+                vs1 = __uint_as_float(lds_u32(at0 + kTile * 4 + 32));
             }
+            const bool see0 = (mask >> g) & 1, see1 = (mask >> (g + 8)) & 1;
+            float tops[NB][2];
+#pragma unroll
+            for (int x = 0; x < NB; ++x)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    sc[x][y] = see0 ? sc[x][y] * (INT8 ? qs[x][y] * ks0 : qs[x][y]) : -INFINITY;
+                    sc[x][2 + y] = see1 ? sc[x][2 + y] * (INT8 ? qs[x][y] * ks1 : qs[x][y]) : -INFINITY;
+                    tops[x][y] = fmaxf(sc[x][y], sc[x][2 + y]);
+                }
             // ---- running maximum, weights ---------------------------------------------------------------
-            float keep[2] = {1.0f, 1.0f};
+            float vtop = fmaxf(fabsf(vs0), fabsf(vs1));
 #pragma unroll
-            for (int x = 0; x < (R8 ? 1 : 2); ++x) {
-                tops[x] = fmaxf(tops[x], __shfl_xor_sync(0xffffffffu, tops[x], 1));
-                tops[x] = fmaxf(tops[x], __shfl_xor_sync(0xffffffffu, tops[x], 2));
-                const float now = fmaxf(m[x], tops[x]);
-                const float zero = now == -INFINITY ? 0.0f : now;   // nothing seen so far: every weight is 0
-                keep[x] = ex2(m[x] - zero);
-                m[x] = now;
-                l[x] *= keep[x];
+            for (int off = 4; off <= 16; off <<= 1) {
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt)
+                for (int x = 0; x < NB; ++x)
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        const float w = ex2(sc[nt][2 * x + y] - zero);
-                        l[x] += w;
-                        sc[nt][2 * x + y] = w;
-                    }
+                    for (int y = 0; y < 2; ++y)
+                        tops[x][y] = fmaxf(tops[x][y], __shfl_xor_sync(0xffffffffu, tops[x][y], off));
+                if (INT8)
+                    vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, off));
             }
+            float vkeep = 1.0f;
             if (INT8) {
                 // the weights take the values' scales, over a power of two that only grows
-                float top = fmaxf(fmaxf(fabsf(vsc[0][0]), fabsf(vsc[0][1])), fmaxf(fabsf(vsc[1][0]), fabsf(vsc[1][1])));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                if (top > vf) {
-                    const uint32_t e = min(max((__float_as_uint(top) >> 23) + 1u, 16u), 253u);   // 2^(e - 127) > top
+                if (vtop > vf) {
+                    const uint32_t e = min(max((__float_as_uint(vtop) >> 23) + 1u, 16u), 253u);   // 2^(e - 127) > vtop
                     const float old = vf;
                     vf = __uint_as_float(e << 23);
                     vinv = __uint_as_float((254u + 14u - e) << 23);   // 2^14 / vf
-                    keep[0] *= old / vf;
-                    keep[1] *= old / vf;
+                    vkeep = old / vf;
                 }
+                vs0 *= vinv;
+                vs1 *= vinv;
+            }
+            bool moved = vkeep != 1.0f;
+            float keep[NB][2];
+            uint32_t hi[NB][2], lo[NB][2];     // P^T as the second operand: tokens 2t, 2t + 1 (+ 8) of query row g
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt)
+            for (int x = 0; x < NB; ++x) {
 #pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        const float f = vsc[nt][y] * vinv;
-                        sc[nt][y] *= f;
-                        if (!R8)
-                            sc[nt][2 + y] *= f;
+                for (int y = 0; y < 2; ++y) {
+                    const float now = fmaxf(m[x][y], tops[x][y]);
+                    const float zero = now == -INFINITY ? 0.0f : now;   // nothing seen so far: every weight is 0
+                    keep[x][y] = ex2(m[x][y] - zero);
+                    m[x][y] = now;
+                    const float w0 = ex2(sc[x][y] - zero), w1 = ex2(sc[x][2 + y] - zero);
+                    l[x][y] = fmaf(l[x][y], keep[x][y], w0 + w1);
+                    keep[x][y] *= vkeep;
+                    moved |= keep[x][y] != 1.0f;
+                    sc[x][y] = INT8 ? w0 * vs0 : w0;
+                    sc[x][2 + y] = INT8 ? w1 * vs1 : w1;
+                }
+                uint32_t top, rest;
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    split2<INT8>(sc[x][2 * y], sc[x][2 * y + 1], top, rest);
+                    hi[x][y] = transpose8(top);
+                    lo[x][y] = transpose8(rest);
+                }
+            }
+            if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+                for (int j = 0; j < MT; ++j)
+#pragma unroll
+                    for (int x = 0; x < NB; ++x) {
+                        o[j][x][0] *= keep[x][0];
+                        o[j][x][1] *= keep[x][1];
+                        o[j][x][2] *= keep[x][0];
+                        o[j][x][3] *= keep[x][1];
                     }
             }
-            if (__any_sync(0xffffffffu, keep[0] != 1.0f || (!R8 && keep[1] != 1.0f))) {
-#pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    o[j][0] *= keep[0];
-                    o[j][1] *= keep[0];
-                    o[j][2] *= keep[R8 ? 0 : 1];
-                    o[j][3] *= keep[R8 ? 0 : 1];
-                }
-            }
-            uint32_t hi[4], lo[4];
-            split2<INT8>(sc[0][0], sc[0][1], hi[0], lo[0]);
-            split2<INT8>(sc[1][0], sc[1][1], hi[2], lo[2]);
-            if (R8) {
-                hi[1] = lo[0];
-                hi[3] = lo[2];
-            } else {
-                split2<INT8>(sc[0][2], sc[0][3], hi[1], lo[1]);
-                split2<INT8>(sc[1][2], sc[1][3], hi[3], lo[3]);
-            }
-            // ---- values ---------------------------------------------------------------------------------
+            // ---- O^T += V^T P^T --------------------------------------------------------------------------
             const uint32_t vb = base + Sh::kKv;
             if (!INT8) {
+                const int r = (lane & 7) + (lane >> 4) * 8;
+                const uint32_t row = vb + r * Sh::kRow;
 #pragma unroll
-                for (int j = 0; j < NT; j += 2) {
-                    const int r = (lane & 7) + ((lane >> 3) & 1) * 8, c = j + (lane >> 4);
+                for (int j = 0; j < MT; ++j) {
                     uint32_t vfr[4];
-                    ldsm_x4_trans(vb + r * Sh::kRow + ((c ^ (r & 7)) << 4), vfr);
-                    mma<false>(o[j], hi, vfr[0], vfr[1]);
-                    mma<false>(o[j + 1], hi, vfr[2], vfr[3]);
-                    if (!R8) {
-                        mma<false>(o[j], lo, vfr[0], vfr[1]);
-                        mma<false>(o[j + 1], lo, vfr[2], vfr[3]);
+                    ldsm_x4_trans(row + (((2 * j + ((lane >> 3) & 1)) ^ (r & 7)) << 4), vfr);
+#pragma unroll
+                    for (int x = 0; x < NB; ++x) {
+                        mma<false>(o[j][x], vfr, hi[x][0], hi[x][1]);
+                        mma<false>(o[j][x], vfr, lo[x][0], lo[x][1]);
                     }
                 }
             } else {
-                // lane (g, t) reads tokens 2t, 2t+1, 2t+8, 2t+9 at the columns of its g: with 16-byte chunks, output tile
-                // 16 x + y, column n <-> column 16 (8 x + n) + y; with 64 columns, tile y <-> column 8 n + y
+                // Lane (g, t) reads tokens 2t, 2t+1, 2t+8, 2t+9 at the columns of its g: columns 16 (8 x + g) ..+15 in 16-byte
+                // chunks, two a tile (rows g and g + 8 of it); with 64 columns, 8 g ..+7.
                 constexpr int X = DP >= 128 ? DP / 128 : 1, W = DP >= 128 ? 4 : 2;
 #pragma unroll
                 for (int x = 0; x < X; ++x) {
@@ -646,14 +650,18 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
                     }
 #pragma unroll
                     for (int z = 0; z < W; ++z) {
-                        uint32_t b0[4], b1[4];
-                        pairs_to_f16(w[0][z], w[1][z], b0);
-                        pairs_to_f16(w[2][z], w[3][z], b1);
+                        uint32_t f01[4], f89[4];
+                        pairs_to_f16(w[0][z], w[1][z], f01);
+                        pairs_to_f16(w[2][z], w[3][z], f89);
 #pragma unroll
-                        for (int y = 0; y < 4; ++y) {
-                            mma<true>(o[(x * W + z) * 4 + y], hi, b0[y], b1[y]);
-                            if (!R8)
-                                mma<true>(o[(x * W + z) * 4 + y], lo, b0[y], b1[y]);
+                        for (int y = 0; y < 2; ++y) {
+                            const uint32_t vfr[4] = {f01[2 * y], f01[2 * y + 1], f89[2 * y], f89[2 * y + 1]};
+                            const int j = x * 8 + 2 * z + y;
+#pragma unroll
+                            for (int b = 0; b < NB; ++b) {
+                                mma<true>(o[j][b], vfr, hi[b][0], hi[b][1]);
+                                mma<true>(o[j][b], vfr, lo[b][0], lo[b][1]);
+                            }
                         }
                     }
                 }
@@ -663,53 +671,60 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
             const bool ends = at.k == at.s.tiles - 1, stop = i == n - 1;
             if (ends || stop) {
 #pragma unroll
-                for (int x = 0; x < (R8 ? 1 : 2); ++x) {
-                    l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
-                    l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
-                }
+                for (int off = 4; off <= 16; off <<= 1)
+#pragma unroll
+                    for (int x = 0; x < NB; ++x)
+#pragma unroll
+                        for (int y = 0; y < 2; ++y)
+                            l[x][y] += __shfl_xor_sync(0xffffffffu, l[x][y], off);
                 const bool final = ends && whole;
                 const int slot = 2 * warp + (whole ? 1 : 0);
                 float *part = p.warp_part + ((size_t)blockIdx.x * 2 * WARPS + slot) * part_size;
                 const float f = INT8 ? vf * 6.103515625e-05f : 1.0f;   // 2^-14
 #pragma unroll
-                for (int x = 0; x < (R8 ? 1 : 2); ++x) {
-                    const int r = g + 8 * x;
-                    if (r >= rows)
-                        continue;
-                    const float inv = final ? (l[x] == 0.0f ? 0.0f : f / l[x]) : f;
+                for (int x = 0; x < NB; ++x) {
+                    float inv[2];
 #pragma unroll
-                    for (int j = 0; j < NT; ++j) {
-                        float v0 = o[j][2 * x], v1 = o[j][2 * x + 1];
-                        if (R8) {
-                            v0 += o[j][2];
-                            v1 += o[j][3];
-                        }
-                        v0 *= inv;
-                        v1 *= inv;
-                        int d0 = 8 * j + 2 * t, d1 = d0 + 1;
-                        if (INT8) {
-                            d0 = DP >= 128 ? 16 * (8 * (j / 16) + 2 * t) + j % 16 : 16 * t + j;
-                            d1 = d0 + (DP >= 128 ? 16 : 8);
-                        }
-                        if (final) {
-                            if (d0 < D)
-                                a.out[(head0 + r) * D + d0] = __float2bfloat16_rn(v0);
-                            if (d1 < D)
-                                a.out[(head0 + r) * D + d1] = __float2bfloat16_rn(v1);
-                        } else {
-                            float *row = part + 2 * p.rows + (size_t)r * D;
-                            if (d0 < D)
-                                row[d0] = v0;
-                            if (d1 < D)
-                                row[d1] = v1;
+                    for (int y = 0; y < 2; ++y)
+                        inv[y] = final ? (l[x][y] == 0.0f ? 0.0f : f / l[x][y]) : f;
+#pragma unroll
+                    for (int j = 0; j < MT; ++j) {
+                        // columns of the tile's rows g and g + 8
+                        const int d0 = INT8 ? (DP >= 128 ? 16 * (8 * (j / 8) + g) + 2 * (j % 8) : 8 * g + 2 * j) : 16 * j + g;
+                        const int d1 = INT8 ? d0 + 1 : d0 + 8;
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const int r = 8 * x + 2 * t + y;
+                            if (r < rows) {
+                                const float v0 = o[j][x][y] * inv[y], v1 = o[j][x][2 + y] * inv[y];
+                                if (final) {
+                                    __nv_bfloat16 *row = a.out + (head0 + r) * D;
+                                    if (d0 < D)
+                                        row[d0] = __float2bfloat16_rn(v0);
+                                    if (d1 < D)
+                                        row[d1] = __float2bfloat16_rn(v1);
+                                } else {
+                                    float *row = part + 2 * p.rows + (size_t)r * D;
+                                    if (d0 < D)
+                                        row[d0] = v0;
+                                    if (d1 < D)
+                                        row[d1] = v1;
+                                }
+                            }
                         }
                     }
-                    if (t == 0) {
-                        if (!final) {
-                            part[2 * r] = m[x];
-                            part[2 * r + 1] = l[x];
-                        } else if (a.lse) {
-                            a.lse[head0 + r] = (m[x] + log2f(l[x])) * kLn2;
+                    if (g == 0) {
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const int r = 8 * x + 2 * t + y;
+                            if (r < rows) {
+                                if (!final) {
+                                    part[2 * r] = m[x][y];
+                                    part[2 * r + 1] = l[x][y];
+                                } else if (a.lse) {
+                                    a.lse[head0 + r] = (m[x][y] + log2f(l[x][y])) * kLn2;
+                                }
+                            }
                         }
                     }
                 }
@@ -918,34 +933,34 @@ Layout layout(const KvCache &kv, int64_t Hq)
     return w;
 }
 
-template <int DP, bool INT8, bool R8, bool ALIGNED, int WARPS, int STAGES>
+template <int DP, bool INT8, int NB, bool ALIGNED, int WARPS, int STAGES>
 cudaError_t launch(const AttnArgs &a, const AttnPlan &p, int ctas, cudaStream_t stream)
 {
     constexpr int smem = WARPS * STAGES * Shape<DP, INT8>::kStage;
     static_assert(WARPS <= kMaxWarps && smem >= WARPS * 16 * (DP + 2) * 4 && smem <= 226 * 1024,
                   "the ring, and room for the last join");
-    auto kernel = paged_attention_kernel<DP, INT8, R8, ALIGNED, WARPS, STAGES>;
+    auto kernel = paged_attention_kernel<DP, INT8, NB, ALIGNED, WARPS, STAGES>;
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess)
         return e;
     return tc::launch_pdl(kernel, dim3(ctas), dim3(WARPS * 32), (size_t)smem, stream, a, p);
 }
 
-template <bool INT8, bool R8, bool ALIGNED>
+template <bool INT8, int NB, bool ALIGNED>
 cudaError_t launch_dim(const AttnArgs &a, const AttnPlan &p, int ctas, cudaStream_t stream)
 {
     if (a.kv.dim <= 64)
-        return launch<64, INT8, R8, ALIGNED, 8, INT8 ? 11 : 6>(a, p, ctas, stream);
+        return launch<64, INT8, NB, ALIGNED, 8, INT8 ? 11 : 6>(a, p, ctas, stream);
     if (a.kv.dim <= 128)
-        return launch<128, INT8, R8, ALIGNED, INT8 ? 16 : 8, 3>(a, p, ctas, stream);
-    return launch<256, INT8, R8, ALIGNED, INT8 ? 8 : 4, 3>(a, p, ctas, stream);
+        return launch<128, INT8, NB, ALIGNED, INT8 ? (NB == 1 ? 16 : 12) : 8, INT8 && NB == 2 ? 4 : 3>(a, p, ctas, stream);
+    return launch<256, INT8, NB, ALIGNED, INT8 ? 8 : 4, 3>(a, p, ctas, stream);
 }
 
-template <bool INT8, bool R8>
+template <bool INT8, int NB>
 cudaError_t launch_pages(const AttnArgs &a, const AttnPlan &p, int ctas, cudaStream_t stream)
 {
-    return a.kv.page_size % kTile == 0 ? launch_dim<INT8, R8, true>(a, p, ctas, stream)
-                                       : launch_dim<INT8, R8, false>(a, p, ctas, stream);
+    return a.kv.page_size % kTile == 0 ? launch_dim<INT8, NB, true>(a, p, ctas, stream)
+                                       : launch_dim<INT8, NB, false>(a, p, ctas, stream);
 }
 
 // A number for each call that no earlier content of a workspace's counters holds
@@ -977,10 +992,9 @@ cudaError_t launch_paged_attention(const AttnArgs &a, cudaStream_t stream)
     for (int i = 0; i < 31; ++i)
         if (a.kv.page_size == 1 << i)
             p.log_page = i;
-    const bool r8 = p.group <= 8;
-    if (a.kv.int8)
-        return r8 ? launch_pages<true, true>(a, p, w.ctas, stream) : launch_pages<true, false>(a, p, w.ctas, stream);
-    return r8 ? launch_pages<false, true>(a, p, w.ctas, stream) : launch_pages<false, false>(a, p, w.ctas, stream);
+    if (p.group <= 8)
+        return a.kv.int8 ? launch_pages<true, 1>(a, p, w.ctas, stream) : launch_pages<false, 1>(a, p, w.ctas, stream);
+    return a.kv.int8 ? launch_pages<true, 2>(a, p, w.ctas, stream) : launch_pages<false, 2>(a, p, w.ctas, stream);
 }
 
 }  // namespace s3d8
