@@ -331,7 +331,8 @@ int s3d8_residual_norm_backward(const void *dh_bf16, const void *dx_bf16, const 
  * One layer's paged key/value cache.  Element (page p, token t, head h, column d)
  * of the keys is k[p * k_stride[0] + t * k_stride[1] + h * k_stride[2] + d]; the
  * values likewise.  Any order of pages, tokens and heads may be chosen by the
- * strides (in elements), with contiguous columns and rows that start on 16 bytes.
+ * strides (in elements), with contiguous columns and rows that start on 16 bytes
+ * (S3D8_ERR_UNSUPPORTED for a stride of 2^32 times 16 bytes, or 2^32 scales, and more).
  * dtype S3D8_KV_BF16: bfloat16 elements, no scales.  S3D8_KV_INT8: int8 codes
  * and one fp32 scale per token and head (value = code * scale), at
  * k_scale[p * scale_stride[0] + t * scale_stride[1] + h * scale_stride[2]]

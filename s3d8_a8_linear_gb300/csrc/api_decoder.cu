@@ -47,6 +47,9 @@ int check_cache(const s3d8_kv_cache *c, KvCache *out)
     for (int i = 0; i < 3; ++i) {
         if (c->k_stride[i] < 0 || c->v_stride[i] < 0 || (int8 && c->scale_stride[i] < 0))
             return S3D8_ERR_INVALID_ARG;
+        if (c->k_stride[i] / unit > 0xFFFFFFFFLL || c->v_stride[i] / unit > 0xFFFFFFFFLL ||
+            (int8 && c->scale_stride[i] > 0xFFFFFFFFLL))
+            return S3D8_ERR_UNSUPPORTED;   // 64 GB from one page to the next
         if (c->k_stride[i] % unit != 0 || c->v_stride[i] % unit != 0)
             return S3D8_ERR_ALIGNMENT;
     }

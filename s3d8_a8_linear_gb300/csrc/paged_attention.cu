@@ -31,6 +31,8 @@ namespace {
 constexpr int kTile = 16;          // tokens
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kSlack = 8.0f;     // weights reach 2^8,
+constexpr int kUp = 6;             // and with their value scales, below 2^6, stay inside fp16 (int8 caches)
 
 template <int DP, bool INT8>
 struct Shape {
@@ -135,6 +137,12 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t v)
     return r;
 }
 
+// a b + c, 32 x 32 -> 64 bits.
+__device__ __forceinline__ uint64_t wide(uint32_t a, uint32_t b, uint64_t c)
+{
+    return (uint64_t)a * b + c;
+}
+
 __device__ __forceinline__ float ex2(float x)
 {
     float y;
@@ -192,6 +200,7 @@ struct AttnPlan {
     int units, blocks, rows;     // per sequence: key/value heads x blocks of query rows; rows per block at most
     int group;                   // query heads per key/value head
     int log_page;                // of a page size that is a power of two, else -1
+    uint32_t k16[3], v16[3], sc[3];   // strides of pages, tokens, heads: 16 bytes of keys and values, scales
     float *warp_part, *cta_part; // partial states
     unsigned long long *arrived; // per CTA
     unsigned long long tag;
@@ -216,6 +225,7 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
     // what each warp left: its first run's sequence (begun before the warp), and the last one's (continued behind it)
     __shared__ int part_b[2 * WARPS], part_u[2 * WARPS];   // part_b < 0: nothing
     __shared__ unsigned char part_ends[2 * WARPS], part_begins[2 * WARPS];
+    __shared__ const float *part_at[2 * WARPS];
     __shared__ int last_flag[2];
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -320,8 +330,11 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
             const uint32_t flip = (INT8 ? swz8<Sh::kChunks>((i * RPI) & 7) : (i * RPI) & 7) << 4;
             return i * RPI * Sh::kRow + (lane_dst ^ flip);
         };
-        int64_t row_off = 0, scale_off = 0;   // of the next tile to fetch, inside its page
-        int row_page = -1, row_slot = 0;      // its page; ALIGNED: the tile's first slot
+        // this lane's chunk of the first rows of page 0, slot 0, head 0; its token's scale there
+        const char *k_lane = static_cast<const char *>(a.kv.k) + (wide(fr, p.k16[1], fc) << 4);
+        const char *v_lane = static_cast<const char *>(a.kv.v) + (wide(fr, p.v16[1], fc) << 4);
+        const float *sc_lane = (side ? a.kv.v_scale : a.kv.k_scale) + (INT8 ? wide(lane & 15, p.sc[1], 0) : 0);
+        int row_page = -1, row_slot = 0;      // of the next tile to fetch: its page and slot (ALIGNED: of its first token)
         bool row_seen = false;                // whether there is a visible token
         auto look_up = [&](bool live) {
             row_seen = false;
@@ -334,12 +347,6 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
             const int col = p.log_page >= 0 ? tok >> p.log_page : tok / S;
             row_slot = tok - col * S;
             row_page = a.table[in.b * a.width + col];
-            if (!ALIGNED) {
-                const int64_t *st = side ? a.kv.vs : a.kv.ks;
-                row_off = row_slot * st[1] + in.h * st[2];
-                if (INT8)
-                    scale_off = row_slot * a.kv.ss[1] + in.h * a.kv.ss[2];
-            }
         };
         // Copies the tile that `in` stands at, looked up before.
         auto fetch = [&](int stage) {
@@ -353,19 +360,16 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
                 const int tok = (in.s.first / kTile + in.k) * kTile;
                 const int lo = max(in.s.first - tok, 0), hi = min(in.s.len - tok, kTile);
                 mask = ok ? ((1u << hi) - 1u) & ~((1u << lo) - 1u) : 0u;
-                const int64_t page = ok ? row_page : 0;
+                const uint32_t page = ok ? row_page : 0;
                 if (INT8) {
-                    const int r = lane & 15;
-                    const float *sc = (side ? a.kv.v_scale : a.kv.k_scale) + page * a.kv.ss[0] +
-                                      (int64_t)(row_slot + r) * a.kv.ss[1] + in.h * a.kv.ss[2];
-                    cp_async4(base + 2 * Sh::kKv + side * (kTile * 4) + r * 4, sc, (mask >> r) & 1 ? 4 : 0);
+                    const float *sc = sc_lane + wide(page, p.sc[0], wide(row_slot, p.sc[1], wide(in.h, p.sc[2], 0)));
+                    cp_async4(base + 2 * Sh::kKv + lane * 4, sc, (mask >> (lane & 15)) & 1 ? 4 : 0);
                 }
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv) {
-                    const int64_t *st = kv ? a.kv.vs : a.kv.ks;
-                    const char *src = static_cast<const char *>(kv ? a.kv.v : a.kv.k) +
-                                      (page * st[0] + (int64_t)(row_slot + fr) * st[1] + in.h * st[2]) * ES + fc * 16;
-                    const int64_t step = st[1] * (ES * RPI);
+                    const uint32_t(&st)[3] = kv ? p.v16 : p.k16;
+                    const char *src = (kv ? v_lane : k_lane) + (wide(page, st[0], wide(row_slot, st[1], wide(in.h, st[2], 0))) << 4);
+                    const uint64_t step = wide(st[1], 16 * RPI, 0);
                     const uint32_t dst = base + kv * Sh::kKv;
                     if (mask == 0xFFFFu && D == DP) {
 #pragma unroll
@@ -381,14 +385,16 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
                 }
             } else {
                 const char *src = static_cast<const char *>(side ? a.kv.v : a.kv.k);
-                if (ok)
-                    src += (row_page * (side ? a.kv.vs[0] : a.kv.ks[0]) + row_off) * ES;
+                if (ok) {
+                    const uint32_t(&st)[3] = side ? p.v16 : p.k16;
+                    src += wide(row_page, st[0], wide(row_slot, st[1], wide(in.h, st[2], 0))) << 4;
+                }
                 mask = __ballot_sync(0xffffffffu, ok);
                 if (INT8) {
                     const float *sc = side ? a.kv.v_scale : a.kv.k_scale;
                     if (ok)
-                        sc += row_page * a.kv.ss[0] + scale_off;
-                    cp_async4(base + 2 * Sh::kKv + side * (kTile * 4) + (lane & 15) * 4, sc, ok ? 4 : 0);
+                        sc += wide(row_page, p.sc[0], wide(row_slot, p.sc[1], wide(in.h, p.sc[2], 0)));
+                    cp_async4(base + 2 * Sh::kKv + lane * 4, sc, ok ? 4 : 0);
                 }
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv) {
@@ -429,8 +435,7 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
         bool fresh = true;
 
         for (int i = 0; i < n; ++i) {
-            cp_wait<STAGES - 2>();
-            __syncwarp();
+            __syncwarp();                     // every lane is done with tile i - 1, whose stage is filled again
             if (fetched < n) {
                 fetch((i + STAGES - 1) % STAGES);
                 ++fetched;
@@ -495,6 +500,9 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
                 }
             }
 
+            cp_wait<STAGES - 1>();
+            __syncwarp();
+
             // ---- scores S^T = K Q^T: lane (g, t) holds tokens g and g + 8 of query rows 2t and 2t + 1 ----
             const uint32_t base = ring + (i % STAGES) * Sh::kStage;
             const uint32_t mask = lds_u32(base + 2 * Sh::kKv + Sh::kScales);
@@ -540,67 +548,48 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
                 vs1 = __uint_as_float(lds_u32(at0 + kTile * 4 + 32));
             }
             const bool see0 = (mask >> g) & 1, see1 = (mask >> (g + 8)) & 1;
-            float tops[NB][2];
+            // ---- running maximum, weights ---------------------------------------------------------------
+            // The maximum (and, in int8, the power of two over the value scales) moves only when a tile exceeds it by more
+            // than 2^kSlack: until then no lane has to hear of the others' scores, and the weights stay below 2^kSlack.
+            bool above = INT8 && fmaxf(fabsf(vs0), fabsf(vs1)) > vf;
 #pragma unroll
             for (int x = 0; x < NB; ++x)
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
                     sc[x][y] = see0 ? sc[x][y] * (INT8 ? qs[x][y] * ks0 : qs[x][y]) : -INFINITY;
                     sc[x][2 + y] = see1 ? sc[x][2 + y] * (INT8 ? qs[x][y] * ks1 : qs[x][y]) : -INFINITY;
-                    tops[x][y] = fmaxf(sc[x][y], sc[x][2 + y]);
+                    above |= fmaxf(sc[x][y], sc[x][2 + y]) > m[x][y] + kSlack;
                 }
-            // ---- running maximum, weights ---------------------------------------------------------------
-            float vtop = fmaxf(fabsf(vs0), fabsf(vs1));
+            if (__any_sync(0xffffffffu, above)) {
+                float vkeep = 1.0f;
+                if (INT8) {
+                    float vtop = fmaxf(fabsf(vs0), fabsf(vs1));
 #pragma unroll
-            for (int off = 4; off <= 16; off <<= 1) {
+                    for (int off = 4; off <= 16; off <<= 1)
+                        vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, off));
+                    if (vtop > vf) {
+                        const uint32_t e = min(max((__float_as_uint(vtop) >> 23) + 1u, 16u), 253u);   // 2^(e - 127) > vtop
+                        const float old = vf;
+                        vf = __uint_as_float(e << 23);
+                        vinv = __uint_as_float((254u + (uint32_t)kUp - e) << 23);   // 2^kUp / vf
+                        vkeep = old / vf;
+                    }
+                }
+                float keep[NB][2];
 #pragma unroll
                 for (int x = 0; x < NB; ++x)
 #pragma unroll
-                    for (int y = 0; y < 2; ++y)
-                        tops[x][y] = fmaxf(tops[x][y], __shfl_xor_sync(0xffffffffu, tops[x][y], off));
-                if (INT8)
-                    vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, off));
-            }
-            float vkeep = 1.0f;
-            if (INT8) {
-                // the weights take the values' scales, over a power of two that only grows
-                if (vtop > vf) {
-                    const uint32_t e = min(max((__float_as_uint(vtop) >> 23) + 1u, 16u), 253u);   // 2^(e - 127) > vtop
-                    const float old = vf;
-                    vf = __uint_as_float(e << 23);
-                    vinv = __uint_as_float((254u + 14u - e) << 23);   // 2^14 / vf
-                    vkeep = old / vf;
-                }
-                vs0 *= vinv;
-                vs1 *= vinv;
-            }
-            bool moved = vkeep != 1.0f;
-            float keep[NB][2];
-            uint32_t hi[NB][2], lo[NB][2];     // P^T as the second operand: tokens 2t, 2t + 1 (+ 8) of query row g
+                    for (int y = 0; y < 2; ++y) {
+                        float top = fmaxf(sc[x][y], sc[x][2 + y]);
 #pragma unroll
-            for (int x = 0; x < NB; ++x) {
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    const float now = fmaxf(m[x][y], tops[x][y]);
-                    const float zero = now == -INFINITY ? 0.0f : now;   // nothing seen so far: every weight is 0
-                    keep[x][y] = ex2(m[x][y] - zero);
-                    m[x][y] = now;
-                    const float w0 = ex2(sc[x][y] - zero), w1 = ex2(sc[x][2 + y] - zero);
-                    l[x][y] = fmaf(l[x][y], keep[x][y], w0 + w1);
-                    keep[x][y] *= vkeep;
-                    moved |= keep[x][y] != 1.0f;
-                    sc[x][y] = INT8 ? w0 * vs0 : w0;
-                    sc[x][2 + y] = INT8 ? w1 * vs1 : w1;
-                }
-                uint32_t top, rest;
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    split2<INT8>(sc[x][2 * y], sc[x][2 * y + 1], top, rest);
-                    hi[x][y] = transpose8(top);
-                    lo[x][y] = transpose8(rest);
-                }
-            }
-            if (__any_sync(0xffffffffu, moved)) {
+                        for (int off = 4; off <= 16; off <<= 1)
+                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+                        top = fmaxf(m[x][y], top);
+                        keep[x][y] = top == m[x][y] ? 1.0f : ex2(m[x][y] - top);
+                        m[x][y] = top;
+                        l[x][y] *= keep[x][y];
+                        keep[x][y] *= vkeep;
+                    }
 #pragma unroll
                 for (int j = 0; j < MT; ++j)
 #pragma unroll
@@ -610,6 +599,27 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
                         o[j][x][2] *= keep[x][0];
                         o[j][x][3] *= keep[x][1];
                     }
+            }
+            vs0 *= vinv;
+            vs1 *= vinv;
+            uint32_t hi[NB][2], lo[NB][2];     // P^T as the second operand: tokens 2t, 2t + 1 (+ 8) of query row g
+#pragma unroll
+            for (int x = 0; x < NB; ++x) {
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const float zero = m[x][y] == -INFINITY ? 0.0f : m[x][y];   // nothing seen so far: every weight is 0
+                    const float w0 = ex2(sc[x][y] - zero), w1 = ex2(sc[x][2 + y] - zero);
+                    l[x][y] += w0 + w1;
+                    sc[x][y] = INT8 ? w0 * vs0 : w0;
+                    sc[x][2 + y] = INT8 ? w1 * vs1 : w1;
+                }
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    uint32_t top, rest;
+                    split2<INT8>(sc[x][2 * y], sc[x][2 * y + 1], top, rest);
+                    hi[x][y] = transpose8(top);
+                    lo[x][y] = transpose8(rest);
+                }
             }
             // ---- O^T += V^T P^T --------------------------------------------------------------------------
             const uint32_t vb = base + Sh::kKv;
@@ -679,8 +689,14 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
                             l[x][y] += __shfl_xor_sync(0xffffffffu, l[x][y], off);
                 const bool final = ends && whole;
                 const int slot = 2 * warp + (whole ? 1 : 0);
-                float *part = p.warp_part + ((size_t)blockIdx.x * 2 * WARPS + slot) * part_size;
-                const float f = INT8 ? vf * 6.103515625e-05f : 1.0f;   // 2^-14
+                // the last part stays in the ring, which has been read; one that ends before waits in the workspace
+                if (stop) {
+                    cp_wait<0>();
+                    __syncwarp();
+                }
+                float *part = stop ? reinterpret_cast<float *>(smem_raw + warp * (STAGES * Sh::kStage))
+                                   : p.warp_part + ((size_t)blockIdx.x * WARPS + warp) * part_size;
+                const float f = INT8 ? vf * (1.0f / (1 << kUp)) : 1.0f;
 #pragma unroll
                 for (int x = 0; x < NB; ++x) {
                     float inv[2];
@@ -733,12 +749,12 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
                     part_u[slot] = at.h * p.blocks + at.blk;
                     part_begins[slot] = whole;
                     part_ends[slot] = ends;
+                    part_at[slot] = part;
                 }
                 whole = fresh = true;
             }
             at.next(a, p.blocks);
         }
-        cp_wait<0>();
     }
     __syncthreads();
 
@@ -746,27 +762,26 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
     // A run that holds its sequence's first and last tile is an output; the others are this CTA's parts: slot 0 for
     // a sequence begun before it, slot 1 for one that goes on behind it.
     int first_of[2] = {-1, -1}, task = 0;
-    auto join_row = [&](const float *parts, size_t step, const int *pick, int begin, int count, int r, float &top, float &sum,
-                        float (&acc)[DP / 32]) {
+    auto join_row = [&](int begin, int end, int r, float &top, float &sum, float (&acc)[DP / 32]) {
         top = -INFINITY;
         sum = 0.0f;
 #pragma unroll
         for (int y = 0; y < DP / 32; ++y)
             acc[y] = 0.0f;
-        for (int e = begin; e < begin + count; ++e)
-            if (!pick || pick[e] >= 0)
-                top = fmaxf(top, __ldcg(parts + e * step + 2 * r));
+        for (int e = begin; e < end; ++e)
+            if (part_b[e] >= 0)
+                top = fmaxf(top, part_at[e][2 * r]);
         const float zero = top == -INFINITY ? 0.0f : top;
-        for (int e = begin; e < begin + count; ++e) {
-            if (pick && pick[e] < 0)
+        for (int e = begin; e < end; ++e) {
+            if (part_b[e] < 0)
                 continue;
-            const float *part = parts + e * step;
-            const float w = ex2(__ldcg(part + 2 * r) - zero);
-            sum = fmaf(w, __ldcg(part + 2 * r + 1), sum);
+            const float *part = part_at[e];
+            const float w = ex2(part[2 * r] - zero);
+            sum = fmaf(w, part[2 * r + 1], sum);
 #pragma unroll
             for (int y = 0; y < DP / 32; ++y)
                 if (32 * y + lane < D)
-                    acc[y] = fmaf(w, __ldcg(part + 2 * p.rows + (size_t)r * D + 32 * y + lane), acc[y]);
+                    acc[y] = fmaf(w, part[2 * p.rows + r * D + 32 * y + lane], acc[y]);
         }
     };
     auto write_row = [&](int b, int u, int r, float top, float sum, const float (&acc)[DP / 32]) {
@@ -779,7 +794,6 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
         if (lane == 0 && a.lse)
             a.lse[row] = (top + log2f(sum)) * kLn2;
     };
-    const float *mine = p.warp_part + (size_t)blockIdx.x * 2 * WARPS * part_size;
     for (int e = 0; e < 2 * WARPS;) {
         if (part_b[e] < 0) {
             ++e;
@@ -800,7 +814,7 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
             if (task % WARPS != warp)
                 continue;
             float top, sum, acc[DP / 32];
-            join_row(mine, part_size, part_b, e, last - e + 1, r, top, sum, acc);
+            join_row(e, last + 1, r, top, sum, acc);
             if (begins && ends) {
                 write_row(b, u, r, top, sum, acc);
             } else {
@@ -928,7 +942,7 @@ Layout layout(const KvCache &kv, int64_t Hq)
     const size_t part = (size_t)w.rows * (kv.dim + 2) * sizeof(float);
     w.arrived = 0;
     w.warp_part = ((size_t)w.ctas * 8 + 255) / 256 * 256;
-    w.cta_part = w.warp_part + (size_t)w.ctas * w.warps * 2 * part;
+    w.cta_part = w.warp_part + (size_t)w.ctas * w.warps * part;
     w.bytes = w.cta_part + (size_t)w.ctas * 2 * part;
     return w;
 }
@@ -937,6 +951,7 @@ template <int DP, bool INT8, int NB, bool ALIGNED, int WARPS, int STAGES>
 cudaError_t launch(const AttnArgs &a, const AttnPlan &p, int ctas, cudaStream_t stream)
 {
     constexpr int smem = WARPS * STAGES * Shape<DP, INT8>::kStage;
+    static_assert(STAGES * Shape<DP, INT8>::kStage >= 8 * NB * (DP + 2) * 4, "a warp's ring holds its last part");
     static_assert(WARPS <= kMaxWarps && smem >= WARPS * 16 * (DP + 2) * 4 && smem <= 226 * 1024,
                   "the ring, and room for the last join");
     auto kernel = paged_attention_kernel<DP, INT8, NB, ALIGNED, WARPS, STAGES>;
@@ -988,6 +1003,11 @@ cudaError_t launch_paged_attention(const AttnArgs &a, cudaStream_t stream)
     p.warp_part = reinterpret_cast<float *>(ws + w.warp_part);
     p.cta_part = reinterpret_cast<float *>(ws + w.cta_part);
     p.tag = next_tag();
+    for (int i = 0; i < 3; ++i) {
+        p.k16[i] = (uint32_t)(a.kv.ks[i] / (a.kv.int8 ? 16 : 8));
+        p.v16[i] = (uint32_t)(a.kv.vs[i] / (a.kv.int8 ? 16 : 8));
+        p.sc[i] = (uint32_t)a.kv.ss[i];
+    }
     p.log_page = -1;
     for (int i = 0; i < 31; ++i)
         if (a.kv.page_size == 1 << i)
