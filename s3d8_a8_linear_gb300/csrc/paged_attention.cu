@@ -967,7 +967,7 @@ cudaError_t launch_dim(const AttnArgs &a, const AttnPlan &p, int ctas, cudaStrea
     if (a.kv.dim <= 64)
         return launch<64, INT8, NB, ALIGNED, 8, INT8 ? 11 : 6>(a, p, ctas, stream);
     if (a.kv.dim <= 128)
-        return launch<128, INT8, NB, ALIGNED, INT8 ? (NB == 1 ? 16 : 12) : 8, INT8 && NB == 2 ? 4 : 3>(a, p, ctas, stream);
+        return launch<128, INT8, NB, ALIGNED, INT8 && NB == 1 ? 16 : 12, !INT8 ? 2 : NB == 1 ? 3 : 4>(a, p, ctas, stream);
     return launch<256, INT8, NB, ALIGNED, INT8 ? 8 : 4, 3>(a, p, ctas, stream);
 }
 
