@@ -1,13 +1,12 @@
 // Attention of one new token per sequence over the paged cache
 // (s3d8_paged_attention).
 //
-// Bound by HBM: every visible key and value is read once, for 2 to 16 query rows
+// Bound by HBM: every visible key and value is read once, for up to 16 query rows
 // at a time.  The unit of work is a tile of 16 tokens of one (sequence, key/value
-// head); all tiles of a call, in that order, are dealt out in equal contiguous runs
-// to the warps of one CTA per SM, whatever the lengths are.  A warp streams its
-// tiles through a ring of its own in shared memory (cp.async, no barrier with
-// other warps) and carries the softmax's running maximum m, sum l and the output
-// sums O in fp32:
+// head); the list of all tiles is cut into contiguous runs, whatever the lengths
+// are.  A warp streams its runs through a ring of its own in shared memory
+// (cp.async, no barrier with other warps) and carries the softmax's running maximum
+// m, sum l and the output sums O in fp32:
 //   S = K Q^T (tensor cores, rows = tokens, columns = 8 or 16 query rows),
 //   m' = max(m, S), O = 2^(m - m') O + V^T 2^(S - m'), l likewise.
 // The matrix products are mma.sync (tcgen05's smallest tile is 64 rows, and the
@@ -15,14 +14,15 @@
 // enter the second product as a 16-bit value and its 16-bit remainder, so that
 // they keep 16 bits or more.
 //
-// A run that ends inside a sequence leaves (m, l, O) in the workspace; the warps of
-// a CTA join theirs, and where a sequence crosses CTAs the last of them to arrive
-// joins all of its parts, in order of position.
+// Every warp has one run of three quarters of its even share; the last quarter of
+// the tiles is in short runs that go to whichever warp is free (SMs differ by a
+// quarter in the bandwidth they get: with even shares alone the slowest CTA of 64
+// sequences of up to 8191 tokens ended at 174 us, the middle one at 146).  A run that
+// ends inside a sequence leaves (m, l, O) in the workspace, and a second kernel joins
+// the parts of each such sequence, in order of position.
 #include "common.cuh"
 #include "launch.h"
 #include "tcgen05.cuh"
-
-#include <atomic>
 
 namespace s3d8 {
 
@@ -40,7 +40,7 @@ struct Shape {
     static constexpr int kChunks = kRow / 16;
     static constexpr int kKv = kTile * kRow;              // bytes of a tile's keys (and of its values)
     static constexpr int kScales = INT8 ? 2 * kTile * 4 : 0;
-    static constexpr int kStage = 2 * kKv + kScales + 16; // + the tile's mask
+    static constexpr int kStage = 2 * kKv + kScales + 16; // + what the tile is (TileInfo)
 };
 
 // ---- the plan: which tiles, and whose -----------------------------------------
@@ -201,13 +201,73 @@ struct AttnPlan {
     int group;                   // query heads per key/value head
     int log_page;                // of a page size that is a power of two, else -1
     uint32_t k16[3], v16[3], sc[3];   // strides of pages, tokens, heads: 16 bytes of keys and values, scales
-    float *warp_part, *cta_part; // partial states
-    unsigned long long *arrived; // per CTA
-    unsigned long long tag;
+    unsigned long long *queue;   // (kQueueTag, next short run): see grab
+    int2 *joins;                 // [B units] first and last run of each sequence's parts, first < 0: nothing to join
+    float *parts;                // [runs][2] partial states: of the sequence begun before the run, and of one that goes on behind it
 };
 
-// One partial state in the workspace: rows x (m, l), then rows x D output sums.
-__device__ __forceinline__ size_t part_floats(int rows, int D) { return (size_t)rows * (D + 2); }
+// One partial state: rows x D output sums, then rows x (m, l); 16-byte aligned.
+__host__ __device__ __forceinline__ size_t part_floats(int rows, int D)
+{
+    return (size_t)rows * D + ((2 * rows + 3) & ~3);
+}
+
+// ---- runs: `warps` long ones, then short ones that are handed out ---------------------------
+struct Runs {
+    long long head, rest, total;   // tiles of a long run, of a short one, of the call
+    int warps, count;
+
+    __device__ __forceinline__ Runs(long long tiles, int w) : total(tiles), warps(w)
+    {
+        const long long share = tiles / w;
+        if (share < 8) {           // too few for short runs: even shares
+            head = (tiles + w - 1) / w;
+            rest = 1;
+            count = head ? (int)((tiles + head - 1) / head) : 0;
+        } else {
+            head = share * 3 / 4;
+            rest = share / 8 > 8 ? share / 8 : 8;
+            count = w + (int)((tiles - head * w + rest - 1) / rest);
+        }
+    }
+    __device__ __forceinline__ long long begin(int r) const
+    {
+        return r < warps ? r * head : warps * head + (r - warps) * rest;
+    }
+    __device__ __forceinline__ int length(int r) const { return (int)(min(total, begin(r + 1)) - begin(r)); }
+    __device__ __forceinline__ int of(long long tile) const
+    {
+        return tile < warps * head ? (int)(tile / head) : warps + (int)((tile - warps * head) / rest);
+    }
+};
+constexpr int kRunsPerWarp = 4;    // count <= 4 warps: 1/4 of a share and a tile, over an eighth of it or 8
+
+// The number of the next short run.  The join kernel leaves the counter at 0 under a
+// tag; a workspace that holds anything else is set up by the first warp to ask.
+constexpr unsigned long long kQueueTag = 0x53334438ull;
+__device__ int grab(unsigned long long *queue)
+{
+    for (;;) {
+        unsigned long long old = atomicAdd(queue, 1ull);
+        if (old >> 32 == kQueueTag)
+            return (int)(uint32_t)old;
+        ++old;
+        for (;;) {
+            const unsigned long long seen = atomicCAS(queue, old, kQueueTag << 32 | 1ull);
+            if (seen == old)
+                return 0;
+            if (seen >> 32 == kQueueTag)
+                break;
+            old = seen;
+        }
+    }
+}
+
+// What a stage's tile is: visible tokens (16 bits) and flags, sequence, unit, run.
+constexpr uint32_t kNew = 1u << 16;       // first tile of a state: of its run, or of its sequence
+constexpr uint32_t kFirst = 1u << 17;     // first tile of its sequence
+constexpr uint32_t kLast = 1u << 18;      // last tile of its sequence
+constexpr uint32_t kStop = 1u << 19;      // last tile of its run
 
 // ALIGNED: pages of a multiple of 16 tokens, so that a tile lies in one page and
 // its rows follow one another at one stride.
@@ -222,12 +282,6 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     __shared__ long long scan[kScanThreads + 1];
     __shared__ long long warp_tot[WARPS];
-    // what each warp left: its first run's sequence (begun before the warp), and the last one's (continued behind it)
-    __shared__ int part_b[2 * WARPS], part_u[2 * WARPS];   // part_b < 0: nothing
-    __shared__ unsigned char part_ends[2 * WARPS], part_begins[2 * WARPS];
-    __shared__ const float *part_at[2 * WARPS];
-    __shared__ int last_flag[2];
-
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int D = a.kv.dim, S = a.kv.page_size;
     tc::pdl_launch_dependents();
@@ -256,8 +310,6 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
             warp_tot[warp] = inc;
         scan[threadIdx.x + 1] = inc;
     }
-    if (threadIdx.x < 2 * WARPS)
-        part_b[threadIdx.x] = -1;
     __syncthreads();
     {
         long long before = 0;
@@ -274,6 +326,8 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
     for (int b = blockIdx.x * WARPS + warp; b < a.B; b += gridDim.x * WARPS) {
         if (a.lens[b] > 0 && a.width > 0)
             continue;
+        for (int i = lane; i < p.units; i += 32)
+            p.joins[(int64_t)b * p.units + i] = make_int2(-1, -1);
         for (int64_t i = lane; i < (int64_t)a.Hq * D; i += 32)
             a.out[(int64_t)b * a.Hq * D + i] = __float2bfloat16_rn(0.0f);
         if (a.lse)
@@ -281,44 +335,70 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
                 a.lse[(int64_t)b * a.Hq + i] = -INFINITY;
     }
 
-    // ---- this CTA's run of tiles, and this warp's part of it -----------------------------
-    long long span = (total + gridDim.x - 1) / gridDim.x;
-    if (span < WARPS)
-        span = WARPS;      // a CTA takes a tile per warp before another one joins in
-    const long long c0 = (long long)blockIdx.x * span;
-    if (c0 >= total)
+    const Runs runs(total, gridDim.x * WARPS);
+    const int own = warp * gridDim.x + blockIdx.x;    // neighbouring runs on different SMs
+    if (own >= runs.count)
         return;
-    const long long c1 = min(total, c0 + span);
-    const long long w0 = c0 + (c1 - c0) * warp / WARPS, w1 = c0 + (c1 - c0) * (warp + 1) / WARPS;
-    const int n = (int)(w1 - w0);
     const size_t part_size = part_floats(p.rows, D);
-
-    if (n > 0) {
-        // first tile: the scanning thread that holds it, then its sequences
-        Cursor in;
-        {
+    {
+        const uint32_t ring = smem_addr(smem_raw) + warp * (STAGES * Sh::kStage);
+        Cursor in;                            // the tile to fetch next,
+        int run = own, left = 0;              // its run, and the tiles left of that, with it
+        bool new_run = true, done = false;
+        int asked = -1;                       // lane 0: the short run that comes next
+        auto ask = [&]() {
+            if (lane == 0 && runs.count > runs.warps)
+                asked = runs.warps + grab(p.queue);
+        };
+        auto enter = [&]() {                  // to the first tile of `run`
+            const long long tile = runs.begin(run);
+            left = runs.length(run);
+            new_run = true;
+            // the scanning thread that holds it, then that one's sequences
             int lo = 0, hi = kScanThreads;
             while (hi - lo > 1) {
                 const int mid = (lo + hi) / 2;
-                if (scan[mid] <= w0)
+                if (scan[mid] <= tile)
                     lo = mid;
                 else
                     hi = mid;
             }
-            long long left = w0 - scan[lo];
+            long long ahead = tile - scan[lo];
             in.b = lo * per;
             in.s = sequence(a, in.b);
-            while (left >= (long long)in.s.tiles * p.units) {
-                left -= (long long)in.s.tiles * p.units;
+            while (ahead >= (long long)in.s.tiles * p.units) {
+                ahead -= (long long)in.s.tiles * p.units;
                 in.s = sequence(a, ++in.b);
             }
-            const int u = (int)(left / in.s.tiles);
-            in.k = (int)(left - (long long)u * in.s.tiles);
-            in.h = u / p.blocks;
-            in.blk = u - in.h * p.blocks;
-        }
-        Cursor at = in;                       // the tile being computed; `in`: the tile being fetched
-        const uint32_t ring = smem_addr(smem_raw) + warp * (STAGES * Sh::kStage);
+            uint32_t u, k;
+            if (ahead >> 32) {
+                u = (uint32_t)(ahead / in.s.tiles);
+                k = (uint32_t)(ahead - (long long)u * in.s.tiles);
+            } else {
+                u = (uint32_t)ahead / (uint32_t)in.s.tiles;
+                k = (uint32_t)ahead - u * (uint32_t)in.s.tiles;
+            }
+            in.k = (int)k;
+            in.h = p.blocks == 1 ? (int)u : (int)u / p.blocks;
+            in.blk = (int)u - in.h * p.blocks;
+            if (left <= 2)
+                ask();
+        };
+        auto advance = [&]() {
+            new_run = false;
+            if (--left > 0) {
+                in.next(a, p.blocks);
+                if (left == 2)
+                    ask();                    // the answer is there when this run ends
+                return;
+            }
+            run = runs.count > runs.warps ? __shfl_sync(0xffffffffu, asked, 0) : runs.count;
+            if (run < runs.count)
+                enter();
+            else
+                done = true;
+        };
+        enter();
 
         // ---- fetching: pages are looked up one tile ahead of the copies -----------------------
         const int side = lane >> 4;           // lanes 0-15 stand for the tile's keys, lanes 16-31 for its values
@@ -408,19 +488,31 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
                     }
                 }
             }
-            if (lane == 0)
-                asm volatile("st.shared.u32 [%0], %1;" ::"r"(base + 2 * Sh::kKv + Sh::kScales), "r"(mask & 0xFFFFu) : "memory");
+            if (lane == 0) {
+                const int u = in.h * p.blocks + in.blk;
+                const uint32_t what = (mask & 0xFFFFu) | (new_run || in.k == 0 ? kNew : 0u) | (in.k == 0 ? kFirst : 0u) |
+                                      (in.k == in.s.tiles - 1 ? kLast : 0u) | (left == 1 ? kStop : 0u);
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(base + 2 * Sh::kKv + Sh::kScales), "r"(what),
+                             "r"(in.b), "r"(u), "r"(run)
+                             : "memory");
+                if (in.k == 0) {
+                    int2 join = make_int2(-1, -1);
+                    if (in.s.tiles > left)    // goes on behind this run
+                        join = make_int2(run, runs.of(runs.begin(run) + runs.length(run) - left + in.s.tiles - 1));
+                    p.joins[(int64_t)in.b * p.units + u] = join;
+                }
+            }
         };
 
         look_up(true);
         int fetched = 0;
 #pragma unroll
         for (int s = 0; s < STAGES - 1; ++s) {
-            if (fetched < n) {
+            if (!done) {
                 fetch(s);
                 ++fetched;
-                in.next(a, p.blocks);
-                look_up(fetched < n);
+                advance();
+                look_up(!done);
             }
             cp_commit();
         }
@@ -431,23 +523,27 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
         uint32_t q[DP / 16][NB][2];
         float qs[NB][2];                      // factor of a query row's scores, log2(e) in it
         float vf = 0.0f, vinv = 0.0f;         // int8: the power of two that carries the value scales
-        bool whole = at.k == 0;               // this warp has the sequence from its first tile on
-        bool fresh = true;
+        bool whole = false;                   // this run has the sequence from its first tile on
 
-        for (int i = 0; i < n; ++i) {
+        for (int i = 0; i < fetched; ++i) {
             __syncwarp();                     // every lane is done with tile i - 1, whose stage is filled again
-            if (fetched < n) {
+            if (!done) {
                 fetch((i + STAGES - 1) % STAGES);
                 ++fetched;
-                in.next(a, p.blocks);
-                look_up(fetched < n);
+                advance();
+                look_up(!done);
             }
             cp_commit();
+            __syncwarp();
+            const uint32_t base = ring + (i % STAGES) * Sh::kStage;
+            const uint4 info = lds_v4(base + 2 * Sh::kKv + Sh::kScales);
+            const uint32_t mask = info.x;
+            const int b = (int)info.y, blk = p.blocks == 1 ? 0 : (int)info.z % p.blocks, h = p.blocks == 1 ? (int)info.z : (int)info.z / p.blocks;
 
-            const int rows = min(p.group - at.blk * 16, p.rows);
-            const int64_t head0 = (int64_t)at.b * a.Hq + at.h * p.group + at.blk * 16;   // query row of the state's row 0
-            if (fresh) {
-                fresh = false;
+            const int rows = min(p.group - blk * 16, p.rows);
+            const int64_t head0 = (int64_t)b * a.Hq + h * p.group + blk * 16;   // query row of the state's row 0
+            if (mask & kNew) {
+                whole = mask & kFirst;
                 vf = vinv = 0.0f;
 #pragma unroll
                 for (int x = 0; x < NB; ++x) {
@@ -504,8 +600,6 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
             __syncwarp();
 
             // ---- scores S^T = K Q^T: lane (g, t) holds tokens g and g + 8 of query rows 2t and 2t + 1 ----
-            const uint32_t base = ring + (i % STAGES) * Sh::kStage;
-            const uint32_t mask = lds_u32(base + 2 * Sh::kKv + Sh::kScales);
             float sc[NB][4];
 #pragma unroll
             for (int x = 0; x < NB; ++x)
@@ -678,8 +772,7 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
             }
 
             // ---- the end of the sequence, or of the run ----------------------------------------------------
-            const bool ends = at.k == at.s.tiles - 1, stop = i == n - 1;
-            if (ends || stop) {
+            if (mask & (kLast | kStop)) {
 #pragma unroll
                 for (int off = 4; off <= 16; off <<= 1)
 #pragma unroll
@@ -687,15 +780,8 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
 #pragma unroll
                         for (int y = 0; y < 2; ++y)
                             l[x][y] += __shfl_xor_sync(0xffffffffu, l[x][y], off);
-                const bool final = ends && whole;
-                const int slot = 2 * warp + (whole ? 1 : 0);
-                // the last part stays in the ring, which has been read; one that ends before waits in the workspace
-                if (stop) {
-                    cp_wait<0>();
-                    __syncwarp();
-                }
-                float *part = stop ? reinterpret_cast<float *>(smem_raw + warp * (STAGES * Sh::kStage))
-                                   : p.warp_part + ((size_t)blockIdx.x * WARPS + warp) * part_size;
+                const bool final = (mask & kLast) && whole;
+                float *part = p.parts + ((size_t)info.w * 2 + (whole ? 1 : 0)) * part_size;
                 const float f = INT8 ? vf * (1.0f / (1 << kUp)) : 1.0f;
 #pragma unroll
                 for (int x = 0; x < NB; ++x) {
@@ -720,7 +806,7 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
                                     if (d1 < D)
                                         row[d1] = __float2bfloat16_rn(v1);
                                 } else {
-                                    float *row = part + 2 * p.rows + (size_t)r * D;
+                                    float *row = part + r * D;
                                     if (d0 < D)
                                         row[d0] = v0;
                                     if (d1 < D)
@@ -735,8 +821,7 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
                             const int r = 8 * x + 2 * t + y;
                             if (r < rows) {
                                 if (!final) {
-                                    part[2 * r] = m[x][y];
-                                    part[2 * r + 1] = l[x][y];
+                                    *reinterpret_cast<float2 *>(part + p.rows * D + 2 * r) = make_float2(m[x][y], l[x][y]);
                                 } else if (a.lse) {
                                     a.lse[head0 + r] = (m[x][y] + log2f(l[x][y])) * kLn2;
                                 }
@@ -744,206 +829,141 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
                         }
                     }
                 }
-                if (!final && lane == 0) {
-                    part_b[slot] = at.b;
-                    part_u[slot] = at.h * p.blocks + at.blk;
-                    part_begins[slot] = whole;
-                    part_ends[slot] = ends;
-                    part_at[slot] = part;
-                }
-                whole = fresh = true;
-            }
-            at.next(a, p.blocks);
-        }
-    }
-    __syncthreads();
-
-    // ---- join the warps' parts: runs of slots of the same sequence; a (run, row) per warp ------------
-    // A run that holds its sequence's first and last tile is an output; the others are this CTA's parts: slot 0 for
-    // a sequence begun before it, slot 1 for one that goes on behind it.
-    int first_of[2] = {-1, -1}, task = 0;
-    auto join_row = [&](int begin, int end, int r, float &top, float &sum, float (&acc)[DP / 32]) {
-        top = -INFINITY;
-        sum = 0.0f;
-#pragma unroll
-        for (int y = 0; y < DP / 32; ++y)
-            acc[y] = 0.0f;
-        for (int e = begin; e < end; ++e)
-            if (part_b[e] >= 0)
-                top = fmaxf(top, part_at[e][2 * r]);
-        const float zero = top == -INFINITY ? 0.0f : top;
-        for (int e = begin; e < end; ++e) {
-            if (part_b[e] < 0)
-                continue;
-            const float *part = part_at[e];
-            const float w = ex2(part[2 * r] - zero);
-            sum = fmaf(w, part[2 * r + 1], sum);
-#pragma unroll
-            for (int y = 0; y < DP / 32; ++y)
-                if (32 * y + lane < D)
-                    acc[y] = fmaf(w, part[2 * p.rows + r * D + 32 * y + lane], acc[y]);
-        }
-    };
-    auto write_row = [&](int b, int u, int r, float top, float sum, const float (&acc)[DP / 32]) {
-        const int64_t row = (int64_t)b * a.Hq + (u / p.blocks) * p.group + (u % p.blocks) * 16 + r;
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-#pragma unroll
-        for (int y = 0; y < DP / 32; ++y)
-            if (32 * y + lane < D)
-                a.out[row * D + 32 * y + lane] = __float2bfloat16_rn(acc[y] * inv);
-        if (lane == 0 && a.lse)
-            a.lse[row] = (top + log2f(sum)) * kLn2;
-    };
-    for (int e = 0; e < 2 * WARPS;) {
-        if (part_b[e] < 0) {
-            ++e;
-            continue;
-        }
-        int end = e + 1, last = e;
-        while (end < 2 * WARPS && (part_b[end] < 0 || (part_b[end] == part_b[e] && part_u[end] == part_u[e]))) {
-            if (part_b[end] >= 0)
-                last = end;
-            ++end;
-        }
-        const bool begins = part_begins[e], ends = part_ends[last];
-        const int b = part_b[e], u = part_u[e], rows = min(p.group - (u % p.blocks) * 16, p.rows);
-        const int slot = begins ? 1 : 0;
-        if (!(begins && ends))
-            first_of[slot] = e;
-        for (int r = 0; r < rows; ++r, ++task) {
-            if (task % WARPS != warp)
-                continue;
-            float top, sum, acc[DP / 32];
-            join_row(e, last + 1, r, top, sum, acc);
-            if (begins && ends) {
-                write_row(b, u, r, top, sum, acc);
-            } else {
-                float *part = p.cta_part + ((size_t)blockIdx.x * 2 + slot) * part_size;
-#pragma unroll
-                for (int y = 0; y < DP / 32; ++y)
-                    if (32 * y + lane < D)
-                        part[2 * p.rows + (size_t)r * D + 32 * y + lane] = acc[y];
-                if (lane == 0) {
-                    part[2 * r] = top;
-                    part[2 * r + 1] = sum;
-                }
             }
         }
-        e = end;
-    }
-    if (first_of[0] < 0 && first_of[1] < 0)
-        return;
-
-    // ---- join the CTAs' parts: the last one to arrive at a sequence's counter -------------------------
-    __threadfence();
-    __syncthreads();
-    for (int slot = 0; slot < 2; ++slot) {
-        const int e = first_of[slot];
-        if (e < 0)
-            continue;
-        const int b = part_b[e], u = part_u[e], rows = min(p.group - (u % p.blocks) * 16, p.rows);
-        const int bucket = b / per;
-        long long s0 = scan[bucket];
-        for (int x = bucket * per; x < b; ++x)
-            s0 += (long long)sequence(a, x).tiles * p.units;
-        const int tiles = sequence(a, b).tiles;
-        s0 += (long long)u * tiles;
-        const int from = (int)(s0 / span), to = (int)((s0 + tiles - 1) / span), count = to - from + 1;
-        if (threadIdx.x == 0) {
-            // (tag, arrivals) in one word: whatever the workspace held before this call counts as none
-            unsigned long long *word = p.arrived + from, seen = *reinterpret_cast<volatile unsigned long long *>(word), next;
-            int arrived;
-            do {
-                const unsigned long long old = seen;
-                arrived = (old >> 16) == p.tag ? (int)(old & 0xFFFFu) + 1 : 1;
-                next = arrived == count ? 0ull : (p.tag << 16) | (unsigned long long)arrived;
-                seen = atomicCAS(word, old, next);
-                if (seen == old)
-                    break;
-            } while (true);
-            last_flag[slot] = arrived == count;
-        }
-        __syncthreads();
-        if (!last_flag[slot])
-            continue;
-        __threadfence();
-        // CTA `from` left its part in slot 1, the others in slot 0
-        const float *parts = p.cta_part + (size_t)from * 2 * part_size;
-        float *stage = reinterpret_cast<float *>(smem_raw);   // [WARPS][rows][D + 2]
-        const int share = (count + WARPS - 1) / WARPS;
-        for (int r = 0; r < rows; ++r) {
-            float top = -INFINITY, sum = 0.0f, acc[DP / 32];
-#pragma unroll
-            for (int y = 0; y < DP / 32; ++y)
-                acc[y] = 0.0f;
-            const int x0 = min(count, warp * share), x1 = min(count, x0 + share);
-            for (int x = x0; x < x1; ++x)
-                top = fmaxf(top, __ldcg(parts + (2 * x + (x == 0)) * part_size + 2 * r));
-            const float zero = top == -INFINITY ? 0.0f : top;
-#pragma unroll 4
-            for (int x = x0; x < x1; ++x) {
-                const float *part = parts + (2 * x + (x == 0)) * part_size;
-                const float w = ex2(__ldcg(part + 2 * r) - zero);
-                sum = fmaf(w, __ldcg(part + 2 * r + 1), sum);
-#pragma unroll
-                for (int y = 0; y < DP / 32; ++y)
-                    if (32 * y + lane < D)
-                        acc[y] = fmaf(w, __ldcg(part + 2 * p.rows + (size_t)r * D + 32 * y + lane), acc[y]);
-            }
-            float *row = stage + ((size_t)warp * p.rows + r) * (D + 2);
-            if (lane == 0) {
-                row[0] = top;
-                row[1] = sum;
-            }
-#pragma unroll
-            for (int y = 0; y < DP / 32; ++y)
-                if (32 * y + lane < D)
-                    row[2 + 32 * y + lane] = acc[y];
-        }
-        __syncthreads();
-        for (int r = warp; r < rows; r += WARPS) {
-            float top = -INFINITY, sum = 0.0f, acc[DP / 32];
-#pragma unroll
-            for (int y = 0; y < DP / 32; ++y)
-                acc[y] = 0.0f;
-            for (int x = 0; x < WARPS; ++x)
-                top = fmaxf(top, stage[((size_t)x * p.rows + r) * (D + 2)]);
-            const float zero = top == -INFINITY ? 0.0f : top;
-            for (int x = 0; x < WARPS; ++x) {
-                const float *row = stage + ((size_t)x * p.rows + r) * (D + 2);
-                const float w = ex2(row[0] - zero);
-                sum = fmaf(w, row[1], sum);
-#pragma unroll
-                for (int y = 0; y < DP / 32; ++y)
-                    if (32 * y + lane < D)
-                        acc[y] = fmaf(w, row[2 + 32 * y + lane], acc[y]);
-            }
-            write_row(b, u, r, top, sum, acc);
-        }
-        __syncthreads();
+        cp_wait<0>();
     }
 }
 
-// The workspace's layout: counters, then the warps' and the CTAs' partial states.
+// Joins the parts of every sequence that was cut: block (unit of a sequence, query
+// row or all of them), its warps over the parts.  Run `first` left its part in its
+// second slot, the runs behind it in their first.
+constexpr int kJoinWarps = 8, kJoinBatch = 8;   // parts whose loads leave together
+
+template <int DP>
+__global__ __launch_bounds__(kJoinWarps * 32) void paged_attention_join_kernel(const __grid_constant__ AttnArgs a,
+                                                                             const __grid_constant__ AttnPlan p)
+{
+    constexpr int V = DP > 128 ? DP / 128 : 1;    // 16-byte pieces of a row in a lane
+    __shared__ __align__(16) float sums[kJoinWarps][DP];
+    __shared__ float tops[kJoinWarps], totals[kJoinWarps];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, D = a.kv.dim;
+    tc::pdl_launch_dependents();
+    tc::pdl_wait();
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0)
+        *p.queue = kQueueTag << 32;
+    const int2 join = p.joins[blockIdx.x];
+    if (join.x < 0)
+        return;
+    const int b = blockIdx.x / p.units, u = blockIdx.x % p.units, h = u / p.blocks, blk = u % p.blocks;
+    const int rows = min(p.group - blk * 16, p.rows), count = join.y - join.x + 1;
+    const size_t size = part_floats(p.rows, D);
+    const float *parts = p.parts + (size_t)join.x * 2 * size;
+    auto part = [&](int x) { return parts + (size_t)(2 * x + (x == 0)) * size; };
+    for (int r = blockIdx.y; r < rows; r += gridDim.y) {
+        // this warp's parts, 32 at a time: lane i has the weight of part x0 + i kJoinWarps
+        float top = -INFINITY, sum = 0.0f;
+        float4 acc[V];
+#pragma unroll
+        for (int y = 0; y < V; ++y)
+            acc[y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int x0 = warp; x0 < count; x0 += 32 * kJoinWarps) {
+            const int x = x0 + lane * kJoinWarps, some = min(32, (count - x0 + kJoinWarps - 1) / kJoinWarps);
+            float mx = -INFINITY, lx = 0.0f;
+            if (x < count) {
+                const float2 ml = *reinterpret_cast<const float2 *>(part(x) + p.rows * D + 2 * r);
+                mx = ml.x;
+                lx = ml.y;
+            }
+            float4 o[kJoinBatch][V];
+            auto load = [&](int i0) {
+#pragma unroll
+                for (int i = 0; i < kJoinBatch; ++i)
+#pragma unroll
+                    for (int y = 0; y < V; ++y) {
+                        o[i][y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        if (i0 + i < some && 128 * y + 4 * lane < D)
+                            o[i][y] = *reinterpret_cast<const float4 *>(part(x0 + (i0 + i) * kJoinWarps) + r * D + 128 * y + 4 * lane);
+                    }
+            };
+            load(0);
+            float now = mx;
+#pragma unroll
+            for (int s = 16; s > 0; s >>= 1)
+                now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, s));
+            now = fmaxf(top, now);
+            const float zero = now == -INFINITY ? 0.0f : now;
+            const float keep = ex2(top - zero), w = ex2(mx - zero);
+            lx *= w;
+#pragma unroll
+            for (int s = 16; s > 0; s >>= 1)
+                lx += __shfl_xor_sync(0xffffffffu, lx, s);
+            sum = sum * keep + lx;
+            top = now;
+#pragma unroll
+            for (int y = 0; y < V; ++y)
+                acc[y] = make_float4(acc[y].x * keep, acc[y].y * keep, acc[y].z * keep, acc[y].w * keep);
+            for (int i0 = 0; i0 < some; i0 += kJoinBatch) {
+                if (i0)
+                    load(i0);
+#pragma unroll
+                for (int i = 0; i < kJoinBatch; ++i) {
+                    // a part beyond the last has a weight of 2^-inf, and zeros
+                    const float wi = __shfl_sync(0xffffffffu, w, i0 + i);
+#pragma unroll
+                    for (int y = 0; y < V; ++y)
+                        acc[y] = make_float4(fmaf(wi, o[i][y].x, acc[y].x), fmaf(wi, o[i][y].y, acc[y].y),
+                                             fmaf(wi, o[i][y].z, acc[y].z), fmaf(wi, o[i][y].w, acc[y].w));
+                }
+            }
+        }
+        __syncthreads();                          // the row before has been read
+        if (lane == 0) {
+            tops[warp] = top;
+            totals[warp] = sum;
+        }
+#pragma unroll
+        for (int y = 0; y < V; ++y)
+            if (128 * y + 4 * lane < DP)
+                *reinterpret_cast<float4 *>(&sums[warp][128 * y + 4 * lane]) = acc[y];
+        __syncthreads();
+        float all = -INFINITY, total = 0.0f, v = 0.0f;
+#pragma unroll
+        for (int x = 0; x < kJoinWarps; ++x)
+            all = fmaxf(all, tops[x]);
+        const float zero = all == -INFINITY ? 0.0f : all;
+#pragma unroll
+        for (int x = 0; x < kJoinWarps; ++x) {
+            const float w = ex2(tops[x] - zero);
+            total = fmaf(w, totals[x], total);
+            if (threadIdx.x < D)
+                v = fmaf(w, sums[x][threadIdx.x], v);
+        }
+        const int64_t row = (int64_t)b * a.Hq + h * p.group + blk * 16 + r;
+        if (threadIdx.x < D)
+            a.out[row * D + threadIdx.x] = __float2bfloat16_rn(total == 0.0f ? 0.0f : v / total);
+        if (threadIdx.x == 0 && a.lse)
+            a.lse[row] = (all + log2f(total)) * kLn2;
+    }
+}
+
+// The workspace's layout: the queue, what to join, partial states.
 struct Layout {
-    int ctas, warps, rows;
-    size_t arrived, warp_part, cta_part, bytes;
+    int ctas, rows;
+    size_t joins, parts, bytes;
 };
 
 constexpr int kMaxWarps = 16;
 
-Layout layout(const KvCache &kv, int64_t Hq)
+Layout layout(const KvCache &kv, int64_t B, int64_t Hq)
 {
     Layout w;
     const int group = (int)(Hq / kv.heads);
     w.ctas = device_sm_count();
-    w.warps = kMaxWarps;
     w.rows = group < 16 ? group : 16;
-    const size_t part = (size_t)w.rows * (kv.dim + 2) * sizeof(float);
-    w.arrived = 0;
-    w.warp_part = ((size_t)w.ctas * 8 + 255) / 256 * 256;
-    w.cta_part = w.warp_part + (size_t)w.ctas * w.warps * part;
-    w.bytes = w.cta_part + (size_t)w.ctas * 2 * part;
+    w.joins = 256;
+    w.parts = w.joins + ((size_t)B * kv.heads * ((group + 15) / 16) * sizeof(int2) + 255) / 256 * 256;
+    w.bytes = w.parts + (size_t)w.ctas * kMaxWarps * kRunsPerWarp * 2 * part_floats(w.rows, kv.dim) * sizeof(float);
     return w;
 }
 
@@ -951,14 +971,16 @@ template <int DP, bool INT8, int NB, bool ALIGNED, int WARPS, int STAGES>
 cudaError_t launch(const AttnArgs &a, const AttnPlan &p, int ctas, cudaStream_t stream)
 {
     constexpr int smem = WARPS * STAGES * Shape<DP, INT8>::kStage;
-    static_assert(STAGES * Shape<DP, INT8>::kStage >= 8 * NB * (DP + 2) * 4, "a warp's ring holds its last part");
-    static_assert(WARPS <= kMaxWarps && smem >= WARPS * 16 * (DP + 2) * 4 && smem <= 226 * 1024,
-                  "the ring, and room for the last join");
+    static_assert(WARPS <= kMaxWarps && smem <= 226 * 1024, "the rings");
     auto kernel = paged_attention_kernel<DP, INT8, NB, ALIGNED, WARPS, STAGES>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess)
+        e = tc::launch_pdl(kernel, dim3(ctas), dim3(WARPS * 32), (size_t)smem, stream, a, p);
     if (e != cudaSuccess)
         return e;
-    return tc::launch_pdl(kernel, dim3(ctas), dim3(WARPS * 32), (size_t)smem, stream, a, p);
+    // few sequences: a block a query row, since each may have many parts
+    const unsigned units = (unsigned)a.B * p.units, rows = units <= 1024 ? p.rows : 1;
+    return tc::launch_pdl(paged_attention_join_kernel<DP>, dim3(units, rows), dim3(kJoinWarps * 32), 0, stream, a, p);
 }
 
 template <bool INT8, int NB, bool ALIGNED>
@@ -978,31 +1000,22 @@ cudaError_t launch_pages(const AttnArgs &a, const AttnPlan &p, int ctas, cudaStr
                                        : launch_dim<INT8, NB, false>(a, p, ctas, stream);
 }
 
-// A number for each call that no earlier content of a workspace's counters holds
-// (48 bits, counted up from where the process began).
-unsigned long long next_tag()
-{
-    static std::atomic<unsigned long long> tag{0x5A3D8000001ull};
-    return tag.fetch_add(1, std::memory_order_relaxed) & 0xFFFFFFFFFFFFull;
-}
-
 }  // namespace
 
-size_t paged_attention_workspace(const KvCache &kv, int64_t, int64_t Hq) { return layout(kv, Hq).bytes; }
+size_t paged_attention_workspace(const KvCache &kv, int64_t B, int64_t Hq) { return layout(kv, B, Hq).bytes; }
 
 cudaError_t launch_paged_attention(const AttnArgs &a, cudaStream_t stream)
 {
-    const Layout w = layout(a.kv, a.Hq);
+    const Layout w = layout(a.kv, a.B, a.Hq);
     char *ws = static_cast<char *>(a.ws);
     AttnPlan p;
     p.group = a.Hq / a.kv.heads;
     p.rows = w.rows;
     p.blocks = (p.group + 15) / 16;
     p.units = a.kv.heads * p.blocks;
-    p.arrived = reinterpret_cast<unsigned long long *>(ws + w.arrived);
-    p.warp_part = reinterpret_cast<float *>(ws + w.warp_part);
-    p.cta_part = reinterpret_cast<float *>(ws + w.cta_part);
-    p.tag = next_tag();
+    p.queue = reinterpret_cast<unsigned long long *>(ws);
+    p.joins = reinterpret_cast<int2 *>(ws + w.joins);
+    p.parts = reinterpret_cast<float *>(ws + w.parts);
     for (int i = 0; i < 3; ++i) {
         p.k16[i] = (uint32_t)(a.kv.ks[i] / (a.kv.int8 ? 16 : 8));
         p.v16[i] = (uint32_t)(a.kv.vs[i] / (a.kv.int8 ? 16 : 8));
