@@ -217,16 +217,18 @@ struct Runs {
     long long head, rest, total;   // tiles of a long run, of a short one, of the call
     int warps, count;
 
-    __device__ __forceinline__ Runs(long long tiles, int w) : total(tiles), warps(w)
+    __device__ __forceinline__ Runs(long long tiles, int w, bool short_runs) : total(tiles), warps(w)
     {
         const long long share = tiles / w;
-        if (share < 8) {           // too few for short runs: even shares
+        // Even shares where a short run's own cost (its query rows, a part to write and to join) passes what it evens out
+        // (one sequence of 65536 tokens, 18 tiles a warp: 64 us, against 73 with short runs; 8 of up to 131072: 564 and 550).
+        if (share < 32 || !short_runs) {
             head = (tiles + w - 1) / w;
             rest = 1;
             count = head ? (int)((tiles + head - 1) / head) : 0;
         } else {
             head = share * 3 / 4;
-            rest = share / 8 > 8 ? share / 8 : 8;
+            rest = share / 8;
             count = w + (int)((tiles - head * w + rest - 1) / rest);
         }
     }
@@ -240,7 +242,7 @@ struct Runs {
         return tile < warps * head ? (int)(tile / head) : warps + (int)((tile - warps * head) / rest);
     }
 };
-constexpr int kRunsPerWarp = 4;    // count <= 4 warps: 1/4 of a share and a tile, over an eighth of it or 8
+constexpr int kRunsPerWarp = 4;    // count <= 4 warps: a quarter of a share and two tiles, over an eighth of it
 
 // The number of the next short run.  The join kernel leaves the counter at 0 under a
 // tag; a workspace that holds anything else is set up by the first warp to ask.
@@ -335,7 +337,7 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
                 a.lse[(int64_t)b * a.Hq + i] = -INFINITY;
     }
 
-    const Runs runs(total, gridDim.x * WARPS);
+    const Runs runs(total, gridDim.x * WARPS, !INT8);   // int8: bound by instructions, which every SM issues alike
     const int own = warp * gridDim.x + blockIdx.x;    // neighbouring runs on different SMs
     if (own >= runs.count)
         return;
@@ -430,6 +432,12 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
         };
         // Copies the tile that `in` stands at, looked up before.
         auto fetch = [&](int stage) {
+            if (new_run || in.k == 0) {       // the query rows of a new state: into L1 by the time its first tile is there
+                const int rows = min(p.group - in.blk * 16, p.rows);
+                const char *src = reinterpret_cast<const char *>(a.q + ((int64_t)in.b * a.Hq + in.h * p.group + in.blk * 16) * D);
+                for (int x = lane * 128; x < rows * D * 2; x += 32 * 128)
+                    asm volatile("prefetch.global.L1 [%0];" ::"l"(src + x));
+            }
             const uint32_t base = ring + stage * Sh::kStage;
             const bool ok = row_seen && row_page >= 0 && row_page < a.kv.pages;
             if (row_seen && !ok)
@@ -860,6 +868,54 @@ __global__ __launch_bounds__(kJoinWarps * 32) void paged_attention_join_kernel(c
     const size_t size = part_floats(p.rows, D);
     const float *parts = p.parts + (size_t)join.x * 2 * size;
     auto part = [&](int x) { return parts + (size_t)(2 * x + (x == 0)) * size; };
+    if (count <= kJoinBatch) {                    // few parts: a query row a warp, all parts in it
+        for (int r = blockIdx.y * kJoinWarps + warp; r < rows; r += gridDim.y * kJoinWarps) {
+            float2 ml = make_float2(-INFINITY, 0.0f);
+            if (lane < count)
+                ml = *reinterpret_cast<const float2 *>(part(lane) + p.rows * D + 2 * r);
+            float4 o[kJoinBatch][V];
+#pragma unroll
+            for (int i = 0; i < kJoinBatch; ++i)
+#pragma unroll
+                for (int y = 0; y < V; ++y) {
+                    o[i][y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    if (i < count && 128 * y + 4 * lane < D)
+                        o[i][y] = *reinterpret_cast<const float4 *>(part(i) + r * D + 128 * y + 4 * lane);
+                }
+            float top = ml.x, sum = 0.0f;
+#pragma unroll
+            for (int s = kJoinBatch / 2; s > 0; s >>= 1)
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+            top = __shfl_sync(0xffffffffu, top, 0);
+            const float zero = top == -INFINITY ? 0.0f : top, w = ex2(ml.x - zero), lw = ml.y * w;
+            float4 acc[V];
+#pragma unroll
+            for (int y = 0; y < V; ++y)
+                acc[y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int i = 0; i < kJoinBatch; ++i) {
+                sum += __shfl_sync(0xffffffffu, lw, i);
+                const float wi = __shfl_sync(0xffffffffu, w, i);
+#pragma unroll
+                for (int y = 0; y < V; ++y)
+                    acc[y] = make_float4(fmaf(wi, o[i][y].x, acc[y].x), fmaf(wi, o[i][y].y, acc[y].y),
+                                         fmaf(wi, o[i][y].z, acc[y].z), fmaf(wi, o[i][y].w, acc[y].w));
+            }
+            const int64_t row = (int64_t)b * a.Hq + h * p.group + blk * 16 + r;
+            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+            for (int y = 0; y < V; ++y)
+                if (128 * y + 4 * lane < D) {
+                    const __nv_bfloat162 lo = __floats2bfloat162_rn(acc[y].x * inv, acc[y].y * inv);
+                    const __nv_bfloat162 hi = __floats2bfloat162_rn(acc[y].z * inv, acc[y].w * inv);
+                    *reinterpret_cast<uint2 *>(a.out + row * D + 128 * y + 4 * lane) =
+                        make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+                }
+            if (lane == 0 && a.lse)
+                a.lse[row] = (top + log2f(sum)) * kLn2;
+        }
+        return;
+    }
     for (int r = blockIdx.y; r < rows; r += gridDim.y) {
         // this warp's parts, 32 at a time: lane i has the weight of part x0 + i kJoinWarps
         float top = -INFINITY, sum = 0.0f;
@@ -987,7 +1043,7 @@ template <bool INT8, int NB, bool ALIGNED>
 cudaError_t launch_dim(const AttnArgs &a, const AttnPlan &p, int ctas, cudaStream_t stream)
 {
     if (a.kv.dim <= 64)
-        return launch<64, INT8, NB, ALIGNED, 8, INT8 ? 11 : 6>(a, p, ctas, stream);
+        return launch<64, INT8, NB, ALIGNED, NB == 1 ? 12 : 8, INT8 ? (NB == 1 ? 8 : 11) : (NB == 1 ? 4 : 6)>(a, p, ctas, stream);
     if (a.kv.dim <= 128)
         return launch<128, INT8, NB, ALIGNED, INT8 && NB == 1 ? 16 : 12, !INT8 ? 2 : NB == 1 ? 3 : 4>(a, p, ctas, stream);
     return launch<256, INT8, NB, ALIGNED, INT8 ? 8 : 4, 3>(a, p, ctas, stream);
