@@ -172,6 +172,8 @@ int s3d8_residual_norm(const void *h_bf16, const void *y_bf16, const void *w_pos
     a.x = static_cast<__nv_bfloat16 *>(x_bf16);
     a.xq = xq;
     a.xscale = xscale;
+    if (!(a.status = device_status_ptr()))
+        return S3D8_ERR_CUDA;
     return cuda_status(launch_residual_norm(a, static_cast<cudaStream_t>(stream)));
 }
 
@@ -235,6 +237,8 @@ int s3d8_residual_norm_backward(const void *dh_bf16, const void *dx_bf16, const 
     g.dw_post = dw_post;
     g.dgate = dgate;
     g.part = static_cast<float *>(workspace);
+    if (!(g.f.status = device_status_ptr()))
+        return S3D8_ERR_CUDA;
     return cuda_status(launch_residual_norm_backward(g, s));
 }
 

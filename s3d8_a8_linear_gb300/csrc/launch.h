@@ -104,6 +104,7 @@ struct NormArgs {
     __nv_bfloat16 *h_out, *x;
     int8_t *xq;
     float *xscale;
+    int *status;
 };
 struct NormGradArgs {
     NormArgs f;                         // h = h', and the forward call's parameters

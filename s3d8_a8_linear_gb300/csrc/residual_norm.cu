@@ -4,8 +4,15 @@
 // Row by row, D columns, in fp32 from bf16:
 //   h' = bf16(h + s * y * r' * w_post),  r' = rsqrt(mean(y^2) + eps), s = alpha g
 //   x  = bf16(h' * r * w_pre),           r  = rsqrt(mean(h'^2) + eps)
-// Both directions are bound by HBM: each row is read once into registers, its
-// sums go through the CTA, and the outputs leave from the same registers.
+// Both directions are bound by HBM: each row is read once, its sums go through the
+// CTA (or a group of lanes), and the outputs leave from the same registers.  Four
+// forms, by the shape:
+//   rows of up to 1024 columns: a group of 8 to 32 lanes a row;
+//   up to 8192 columns, more rows than the GPU takes at once (and every backward
+//     call): persistent CTAs, rows by bulk copy through a ring in shared memory, the
+//     columns' factors in registers;
+//   few rows, or longer ones: a CTA a row, straight from global memory (a single
+//     token of 4096 columns is all latency: the ring's set-up would only add to it).
 #include "common.cuh"
 #include "launch.h"
 #include "tcgen05.cuh"
@@ -65,6 +72,64 @@ __device__ __forceinline__ void block_sum(float (&v)[N], float *red)
 #pragma unroll
     for (int i = 0; i < N; ++i)
         v[i] = warp_sum_f(lane < nw ? red[i * 32 + lane] : 0.0f);
+}
+
+// Sums of eight values per thread over the CTA: total j is left in the lanes of
+// every warp whose number is j modulo 8.  9 + 2 shuffles; `red`: 8 floats a warp,
+// with the same rule for two calls in a row.
+__device__ __forceinline__ float block_sum8(float (&v)[8], float *red)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+#pragma unroll
+    for (int n = 8, o = 16; n > 1; n >>= 1, o >>= 1) {
+        const bool upper = (lane & o) != 0;
+#pragma unroll
+        for (int i = 0; i < n / 2; ++i) {
+            const float keep = upper ? v[i + n / 2] : v[i], send = upper ? v[i] : v[i + n / 2];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+        }
+    }
+    float r = v[0];                       // value lane / 4, of this lane's share
+    r += __shfl_xor_sync(0xffffffffu, r, 2);
+    r += __shfl_xor_sync(0xffffffffu, r, 1);
+    if ((lane & 3) == 0)
+        red[warp * 8 + (lane >> 2)] = r;
+    __syncthreads();
+    r = 0.0f;
+    for (int w = lane >> 3; w < nw; w += 4)
+        r += red[w * 8 + (lane & 7)];
+    r += __shfl_xor_sync(0xffffffffu, r, 8);
+    return r + __shfl_xor_sync(0xffffffffu, r, 16);
+}
+
+// Sum, and maximum, over groups of GS neighbouring lanes.
+template <int GS>
+__device__ __forceinline__ float group_sum(float v)
+{
+#pragma unroll
+    for (int o = GS / 2; o > 0; o >>= 1)
+        v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+template <int GS>
+__device__ __forceinline__ float group_max(float v)
+{
+#pragma unroll
+    for (int o = GS / 2; o > 0; o >>= 1)
+        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+
+__device__ __forceinline__ float block_max(float v, float *red)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = blockDim.x >> 5;
+    v = group_max<32>(v);
+    if (nw == 1)
+        return v;
+    if (lane == 0)
+        red[warp] = v;
+    __syncthreads();
+    return group_max<32>(lane < nw ? red[lane] : 0.0f);
 }
 
 __device__ __forceinline__ float gate_value(const NormArgs &a, int col)
@@ -174,21 +239,8 @@ __global__ __launch_bounds__(MAX_T) void residual_norm_kernel(NormArgs a)
             }
         }
         if (a.xq) {
-            float top = absmax_bf16x2_value(m2);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1)
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            const int nw = T >> 5, lane = threadIdx.x & 31;
-            if (nw > 1) {
-                if (lane == 0)
-                    red[flip][threadIdx.x >> 5] = top;
-                __syncthreads();
-                top = lane < nw ? red[flip][lane] : 0.0f;
-                flip ^= 1;
-#pragma unroll
-                for (int o = 16; o > 0; o >>= 1)
-                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            }
+            const float top = block_max(absmax_bf16x2_value(m2), red[flip]);
+            flip ^= 1;
             const float sc = __fdiv_rn(top, 127.0f);
             const float rs = sc > 0.0f ? __frcp_rn(sc) : 0.0f;
             if (threadIdx.x == 0)
@@ -203,170 +255,699 @@ __global__ __launch_bounds__(MAX_T) void residual_norm_kernel(NormArgs a)
     }
 }
 
-// One CTA walks rows blockIdx.x, + gridDim.x, ...; the column sums
-//   P[d] = sum_m dx h' r   and   S[d] = sum_m G y r'
-// stay in its threads' registers (in shared memory for rows over 8192 columns)
-// and leave as one fp32 row of partials per CTA: dw_pre = P, dw_post = s S,
-// dgate = alpha g' w_post S.
-template <int NS, int MAX_T, bool WIDE>
-__global__ __launch_bounds__(MAX_T) void residual_norm_backward_kernel(NormGradArgs g)
+// What the three steps of a row do with one chunk of eight columns.
+__device__ __forceinline__ float square_sum(uint4 v)
 {
-    extern __shared__ float wide_acc[];   // WIDE: [P, S][8][NS * T]
-    __shared__ float red[2][3 * 32];
+    float f[8], s = 0.0f;
+    unpack8(v, f);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        s = fmaf(f[e], f[e], s);
+    return s;
+}
+__device__ __forceinline__ uint4 updated(uint4 hv, uint4 yv, float r, const float (&f)[8])
+{
+    float h[8], y[8];
+    unpack8(hv, h);
+    unpack8(yv, y);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        h[e] = fmaf(y[e] * r, f[e], h[e]);
+    return pack8(h);
+}
+__device__ __forceinline__ uint4 normed(uint4 hv, float r, uint4 wv)
+{
+    float h[8], w[8];
+    unpack8(hv, h);
+    unpack8(wv, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        h[e] = h[e] * r * w[e];
+    return pack8(h);
+}
+
+// Rows of up to GS * NS * 8 columns, one per group of GS lanes; the next row's
+// loads leave before this one's work.
+constexpr int kRowsThreads = 256;
+
+template <int GS, int NS>
+__global__ __launch_bounds__(kRowsThreads) void residual_norm_rows_kernel(NormArgs a)
+{
+    tc::pdl_launch_dependents();
+    tc::pdl_wait();
+    const int lane = threadIdx.x % GS, chunks = a.D / 8;
+    const float inv_d = 1.0f / (float)a.D;
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    float f[NS][8];
+    uint4 w[NS];
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+        const int c = lane + i * GS;
+        w[i] = a.w_pre && c < chunks ? __ldg(reinterpret_cast<const uint4 *>(a.w_pre) + c) : zero;
+        if (a.y && c < chunks)
+            update_factor(a, c, f[i]);
+    }
+    const int step = gridDim.x * (kRowsThreads / GS);
+    int m = blockIdx.x * (kRowsThreads / GS) + threadIdx.x / GS;
+    uint4 hn[NS], yn[NS];
+    auto load = [&](int row) {
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+            const int c = lane + i * GS;
+            hn[i] = yn[i] = zero;
+            if (row < a.M && c < chunks) {
+                hn[i] = reinterpret_cast<const uint4 *>(a.h)[(size_t)row * chunks + c];   // h_out may be h: an ordinary load
+                if (a.y)
+                    yn[i] = ldg_stream_v4(reinterpret_cast<const uint4 *>(a.y) + (size_t)row * chunks + c);
+            }
+        }
+    };
+    load(m);
+    for (int m0 = blockIdx.x * (kRowsThreads / GS); m0 < a.M; m0 += step, m += step) {   // all groups of a CTA together
+        uint4 hv[NS], yv[NS];
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+            hv[i] = hn[i];
+            yv[i] = yn[i];
+        }
+        load(m + step);
+        const bool live = m < a.M;
+        if (a.y) {
+            float r = 1.0f;
+            if (a.w_post) {
+                float s = 0.0f;
+#pragma unroll
+                for (int i = 0; i < NS; ++i)
+                    s += square_sum(yv[i]);
+                r = rsqrtf(group_sum<GS>(s) * inv_d + a.eps);
+            }
+#pragma unroll
+            for (int i = 0; i < NS; ++i) {
+                const int c = lane + i * GS;
+                if (c < chunks) {
+                    hv[i] = updated(hv[i], yv[i], r, f[i]);
+                    if (live)
+                        reinterpret_cast<uint4 *>(a.h_out)[(size_t)m * chunks + c] = hv[i];
+                }
+            }
+        }
+        if (!a.w_pre)
+            continue;
+        float s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NS; ++i)
+            s += square_sum(hv[i]);
+        const float r = rsqrtf(group_sum<GS>(s) * inv_d + a.eps);
+        uint32_t m2 = 0u;
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+            const int c = lane + i * GS;
+            hv[i] = normed(hv[i], r, w[i]);
+            if (c < chunks) {
+                if (a.x && live)
+                    reinterpret_cast<uint4 *>(a.x)[(size_t)m * chunks + c] = hv[i];
+                m2 = absmax_bf16x8(hv[i], m2);
+            }
+        }
+        if (a.xq) {
+            const float sc = __fdiv_rn(group_max<GS>(absmax_bf16x2_value(m2)), 127.0f);
+            const float rs = sc > 0.0f ? __frcp_rn(sc) : 0.0f;
+            if (!live)
+                continue;
+            if (lane == 0)
+                a.xscale[m] = sc;
+#pragma unroll
+            for (int i = 0; i < NS; ++i)
+                if (lane + i * GS < chunks)
+                    reinterpret_cast<uint2 *>(a.xq)[(size_t)m * chunks + lane + i * GS] = quant_chunk8(hv[i], sc, rs);
+        }
+    }
+}
+
+// ---- rows through a ring of bulk copies ---------------------------------------------------
+// N tensors of the same shape, row m of each copied to one stage; rows blockIdx.x,
+// + gridDim.x, ....  Thread 0 issues; a stage is filled again once every thread has
+// passed a barrier behind its reads of it (release).
+constexpr int kRingStages = 8;   // at most
+
+struct RowRing {
+    uint32_t data, bars;
+    int stages, row_bytes, n;
+    const char *src[4];
+    int M, ahead;                 // rows issued so far, in steps of the grid
+
+    __device__ __forceinline__ void issue()
+    {
+        const int64_t m = blockIdx.x + (int64_t)ahead * gridDim.x;
+        if (m >= M)
+            return;
+        const int s = ahead % stages;
+        mbar_arrive_expect_tx(bars + 8 * s, (uint32_t)(n * row_bytes));
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < n)
+                bulk_load(data + (s * n + i) * row_bytes, src[i] + m * row_bytes, (uint32_t)row_bytes, bars + 8 * s);
+        ++ahead;
+    }
+    __device__ __forceinline__ void start(unsigned char *smem, unsigned long long *bar_mem)
+    {
+        data = smem_addr(smem);
+        bars = smem_addr(bar_mem);
+        ahead = 0;
+        if (threadIdx.x == 0) {
+            for (int s = 0; s < stages; ++s)
+                mbar_init(bars + 8 * s, 1);
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+            fence_proxy_async_smem();
+        }
+        __syncthreads();
+    }
+    __device__ __forceinline__ void fill()
+    {
+        if (threadIdx.x == 0)
+            for (int s = 0; s < stages; ++s)
+                issue();
+    }
+    __device__ __forceinline__ bool wait(int k) const { return mbar_wait_bounded(bars + 8 * (k % stages), (k / stages) & 1); }
+    __device__ __forceinline__ uint4 chunk(int k, int tensor, int c) const
+    {
+        return lds_v4(data + ((k % stages) * n + tensor) * row_bytes + c * 16);
+    }
+    // After a wait that ran out: not before the copies in flight have landed, or as many waits have run out again.
+    __device__ __forceinline__ void abandon(int k, int *status) const
+    {
+        if (threadIdx.x == 0) {
+            record_timeout(status);
+            for (int i = k; i < ahead; ++i)
+                (void)wait(i);
+        }
+        __syncthreads();
+    }
+};
+
+template <int NS, int T>
+__global__ __launch_bounds__(T, T <= 256 ? 512 / T : 1) void residual_norm_ring_kernel(NormArgs a, int stages)
+{
+    extern __shared__ __align__(128) unsigned char ring_mem[];
+    __shared__ float red[2][32];
+    __shared__ unsigned long long bars[kRingStages];
+    const int chunks = a.D / 8;
+    const float inv_d = 1.0f / (float)a.D;
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    RowRing ring;
+    ring.stages = stages;
+    ring.row_bytes = a.D * 2;
+    ring.n = a.y ? 2 : 1;
+    ring.M = a.M;
+    ring.src[0] = reinterpret_cast<const char *>(a.h);
+    ring.src[1] = reinterpret_cast<const char *>(a.y);
+    ring.start(ring_mem, bars);
+    tc::pdl_launch_dependents();
+    tc::pdl_wait();
+    ring.fill();
+    float f[NS][8];
+    uint4 w[NS];
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+        const int c = threadIdx.x + i * T;
+        w[i] = a.w_pre && c < chunks ? __ldg(reinterpret_cast<const uint4 *>(a.w_pre) + c) : zero;
+        if (a.y && c < chunks)
+            update_factor(a, c, f[i]);
+    }
+    int flip = 0, k = 0;
+    for (int m = blockIdx.x; m < a.M; m += gridDim.x, ++k) {
+        const size_t base = (size_t)m * chunks;
+        if (!ring.wait(k)) {
+            ring.abandon(k, a.status);
+            return;
+        }
+        uint4 hv[NS], yv[NS];
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+            const int c = threadIdx.x + i * T;
+            hv[i] = c < chunks ? ring.chunk(k, 0, c) : zero;
+            yv[i] = a.y && c < chunks ? ring.chunk(k, 1, c) : zero;
+        }
+        bool held = true;                 // until a barrier shows that every thread has read the stage
+        if (a.y) {
+            float r = 1.0f;
+            if (a.w_post) {
+                float s[1] = {0.0f};
+#pragma unroll
+                for (int i = 0; i < NS; ++i)
+                    s[0] += square_sum(yv[i]);
+                block_sum(s, red[flip]);
+                flip ^= 1;
+                r = rsqrtf(s[0] * inv_d + a.eps);
+                held = false;
+                if (threadIdx.x == 0)
+                    ring.issue();
+            }
+#pragma unroll
+            for (int i = 0; i < NS; ++i) {
+                const int c = threadIdx.x + i * T;
+                if (c < chunks) {
+                    hv[i] = updated(hv[i], yv[i], r, f[i]);
+                    reinterpret_cast<uint4 *>(a.h_out)[base + c] = hv[i];
+                }
+            }
+        }
+        if (!a.w_pre) {
+            if (held) {
+                __syncthreads();
+                if (threadIdx.x == 0)
+                    ring.issue();
+            }
+            continue;
+        }
+        float s[1] = {0.0f};
+#pragma unroll
+        for (int i = 0; i < NS; ++i)
+            s[0] += square_sum(hv[i]);
+        block_sum(s, red[flip]);
+        flip ^= 1;
+        if (held && threadIdx.x == 0)
+            ring.issue();
+        const float r = rsqrtf(s[0] * inv_d + a.eps);
+        uint32_t m2 = 0u;
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+            const int c = threadIdx.x + i * T;
+            hv[i] = normed(hv[i], r, w[i]);
+            if (c < chunks) {
+                if (a.x)
+                    reinterpret_cast<uint4 *>(a.x)[base + c] = hv[i];
+                m2 = absmax_bf16x8(hv[i], m2);
+            }
+        }
+        if (a.xq) {
+            const float sc = __fdiv_rn(block_max(absmax_bf16x2_value(m2), red[flip]), 127.0f);
+            flip ^= 1;
+            const float rs = sc > 0.0f ? __frcp_rn(sc) : 0.0f;
+            if (threadIdx.x == 0)
+                a.xscale[m] = sc;
+#pragma unroll
+            for (int i = 0; i < NS; ++i)
+                if (threadIdx.x + i * T < chunks)
+                    reinterpret_cast<uint2 *>(a.xq)[base + threadIdx.x + i * T] = quant_chunk8(hv[i], sc, rs);
+        }
+    }
+}
+
+// ---- gradients ------------------------------------------------------------------------------
+// Of a row, with a = dx w_pre and f = s w_post, the sums over columns of
+//   h'^2, a h', y^2, f y dh, f y a, f y h'
+// give everything: G = dh + r a - h' ch, ch = r^3 mean(a h'), and
+//   sum(b y) = sum(f y G) = sum(f y dh) + r sum(f y a) - ch sum(f y h').
+struct RowGrad {
+    float r, ch, rp, cy;
+};
+
+__device__ __forceinline__ void grad_sums(uint4 hv, uint4 yv, uint4 xv, uint4 gv, uint4 wv, const float (&f)[8], float (&s)[8])
+{
+    float h[8], y[8], x[8], g[8], w[8];
+    unpack8(hv, h);
+    unpack8(yv, y);
+    unpack8(xv, x);
+    unpack8(gv, g);
+    unpack8(wv, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        const float ae = x[e] * w[e], fy = f[e] * y[e];
+        s[0] = fmaf(h[e], h[e], s[0]);
+        s[1] = fmaf(ae, h[e], s[1]);
+        s[2] = fmaf(y[e], y[e], s[2]);
+        s[3] = fmaf(fy, g[e], s[3]);
+        s[4] = fmaf(fy, ae, s[4]);
+        s[5] = fmaf(fy, h[e], s[5]);
+    }
+}
+
+__device__ __forceinline__ RowGrad grad_factors(const NormArgs &a, float inv_d, float hh, float ah, float yy, float yg, float ya,
+                                                float yh)
+{
+    RowGrad q;
+    q.r = rsqrtf(hh * inv_d + a.eps);
+    q.ch = q.r * q.r * q.r * (ah * inv_d);
+    q.rp = a.w_post ? rsqrtf(yy * inv_d + a.eps) : 1.0f;
+    q.cy = a.w_post ? q.rp * q.rp * q.rp * ((yg + q.r * ya - q.ch * yh) * inv_d) : 0.0f;
+    return q;
+}
+
+// One chunk's gradients, and its columns' sums P += dx h' r, S += G y r'.
+__device__ __forceinline__ void grad_chunk(uint4 hv, uint4 yv, uint4 xv, uint4 gv, uint4 wv, const float (&f)[8], const RowGrad &q,
+                                           float (&P)[8], float (&S)[8], uint4 &dh, uint4 &dy)
+{
+    float h[8], y[8], x[8], g[8], w[8], d[8];
+    unpack8(hv, h);
+    unpack8(yv, y);
+    unpack8(xv, x);
+    unpack8(gv, g);
+    unpack8(wv, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        g[e] = fmaf(-h[e], q.ch, fmaf(q.r, x[e] * w[e], g[e]));
+        P[e] = fmaf(x[e] * h[e], q.r, P[e]);
+        S[e] = fmaf(g[e] * y[e], q.rp, S[e]);
+        d[e] = fmaf(q.rp * g[e], f[e], -y[e] * q.cy);
+    }
+    dh = pack8(g);
+    dy = pack8(d);
+}
+
+// A CTA's row of partials: P, S, and sum_d w_post S for a single gate.
+__device__ __forceinline__ float put_partials(const NormArgs &a, float *row, int c, const float (&P)[8], const float (&S)[8])
+{
+    float w[8] = {1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f}, dot = 0.0f;
+    if (a.w_post)
+        unpack8(__ldg(reinterpret_cast<const uint4 *>(a.w_post) + c), w);
+#pragma unroll
+    for (int e = 0; e < 8; e += 4) {
+        *reinterpret_cast<float4 *>(row + 8 * c + e) = make_float4(P[e], P[e + 1], P[e + 2], P[e + 3]);
+        *reinterpret_cast<float4 *>(row + a.D + 8 * c + e) = make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        dot = fmaf(w[e], S[e], dot);
+    return dot;
+}
+
+template <int GS, int NS>
+__global__ __launch_bounds__(kRowsThreads) void residual_norm_backward_rows_kernel(NormGradArgs g)
+{
+    extern __shared__ __align__(16) float column_sums[];   // [2][D]
+    __shared__ float red[32];
+    const NormArgs &a = g.f;
+    tc::pdl_launch_dependents();
+    tc::pdl_wait();
+    const int lane = threadIdx.x % GS, chunks = a.D / 8;
+    const float inv_d = 1.0f / (float)a.D;
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    float f[NS][8], P[NS][8], S[NS][8];
+    uint4 w[NS];
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+        const int c = lane + i * GS;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            P[i][e] = S[i][e] = f[i][e] = 0.0f;
+        w[i] = a.w_pre && c < chunks ? __ldg(reinterpret_cast<const uint4 *>(a.w_pre) + c) : zero;
+        if (a.y && c < chunks)
+            update_factor(a, c, f[i]);
+    }
+    const int groups = kRowsThreads / GS, group = threadIdx.x / GS;
+    for (int m0 = blockIdx.x * groups; m0 < a.M; m0 += gridDim.x * groups) {
+        const int m = m0 + group;
+        const size_t base = (size_t)m * chunks;
+        uint4 hv[NS], yv[NS], xv[NS], gv[NS];
+        float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+            const int c = lane + i * GS;
+            const bool in = m < a.M && c < chunks;
+            hv[i] = in ? ldg_stream_v4(reinterpret_cast<const uint4 *>(a.h) + base + c) : zero;
+            yv[i] = in && a.y ? ldg_stream_v4(reinterpret_cast<const uint4 *>(a.y) + base + c) : zero;
+            xv[i] = in && g.dx ? ldg_stream_v4(reinterpret_cast<const uint4 *>(g.dx) + base + c) : zero;
+            gv[i] = in && g.dh ? reinterpret_cast<const uint4 *>(g.dh)[base + c] : zero;   // dh_in may be dh
+        }
+#pragma unroll
+        for (int i = 0; i < NS; ++i)
+            grad_sums(hv[i], yv[i], xv[i], gv[i], w[i], f[i], s);
+#pragma unroll
+        for (int i = 0; i < 6; ++i)
+            s[i] = group_sum<GS>(s[i]);
+        const RowGrad q = grad_factors(a, inv_d, s[0], s[1], s[2], s[3], s[4], s[5]);
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+            const int c = lane + i * GS;
+            uint4 dh, dy;
+            grad_chunk(hv[i], yv[i], xv[i], gv[i], w[i], f[i], q, P[i], S[i], dh, dy);   // zeros where there is no row
+            if (m < a.M && c < chunks) {
+                reinterpret_cast<uint4 *>(g.dh_in)[base + c] = dh;
+                if (a.y)
+                    reinterpret_cast<uint4 *>(g.dy)[base + c] = dy;
+            }
+        }
+    }
+    // the sums of a warp's groups, then one warp after another
+#pragma unroll
+    for (int o = GS; o < 32; o <<= 1)
+#pragma unroll
+        for (int i = 0; i < NS; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                P[i][e] += __shfl_xor_sync(0xffffffffu, P[i][e], o);
+                S[i][e] += __shfl_xor_sync(0xffffffffu, S[i][e], o);
+            }
+    const int warp = threadIdx.x >> 5;
+    for (int x = 0; x < kRowsThreads / 32; ++x) {
+        if (warp == x && (threadIdx.x & 31) < GS) {
+#pragma unroll
+            for (int i = 0; i < NS; ++i) {
+                const int c = lane + i * GS;
+                if (c < chunks) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        float *to = column_sums + 8 * c + e;
+                        P[i][e] += x ? to[0] : 0.0f;
+                        S[i][e] += x ? to[a.D] : 0.0f;
+                        to[0] = P[i][e];
+                        to[a.D] = S[i][e];
+                    }
+                }
+            }
+        }
+        __syncthreads();
+    }
+    float *row = g.part + (size_t)blockIdx.x * (2 * a.D + 4);
+    float dot[1] = {0.0f};
+    if (warp == kRowsThreads / 32 - 1 && (threadIdx.x & 31) < GS) {
+#pragma unroll
+        for (int i = 0; i < NS; ++i)
+            if (lane + i * GS < chunks)
+                dot[0] += put_partials(a, row, lane + i * GS, P[i], S[i]);
+    }
+    block_sum(dot, red);
+    if (threadIdx.x == 0)
+        row[2 * a.D] = dot[0];
+}
+
+// One CTA walks rows blockIdx.x, + gridDim.x, ...; the columns' sums P and S stay in
+// its threads' registers.
+// RELOAD: a row's chunks are read from the ring a second time instead of waiting in
+// registers, and the stage is held until then.
+template <int NS, int T, bool RELOAD>
+__global__ __launch_bounds__(T, T <= 256 ? 512 / T : 1) void residual_norm_backward_ring_kernel(NormGradArgs g, int stages)
+{
+    extern __shared__ __align__(128) unsigned char ring_mem[];
+    __shared__ float red[2][8 * 32];
+    __shared__ unsigned long long bars[kRingStages];
+    const NormArgs &a = g.f;
+    const int chunks = a.D / 8;
+    const float inv_d = 1.0f / (float)a.D;
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    RowRing ring;
+    ring.stages = stages;
+    ring.row_bytes = a.D * 2;
+    ring.M = a.M;
+    // h', then those of dh, dx and y that there are
+    const char *dh = reinterpret_cast<const char *>(g.dh), *dx = reinterpret_cast<const char *>(g.dx);
+    const char *y = reinterpret_cast<const char *>(a.y);
+    const int at_g = dh ? 1 : -1, at_x = dx ? 1 + (dh != nullptr) : -1, at_y = y ? 1 + (dh != nullptr) + (dx != nullptr) : -1;
+    ring.n = 1 + (dh != nullptr) + (dx != nullptr) + (y != nullptr);
+    ring.src[0] = reinterpret_cast<const char *>(a.h);
+    ring.src[1] = dh ? dh : dx ? dx : y;
+    ring.src[2] = dh && dx ? dx : y;
+    ring.src[3] = y;
+    ring.start(ring_mem, bars);
+    tc::pdl_launch_dependents();
+    tc::pdl_wait();
+    ring.fill();
+    float f[NS][8], P[NS][8], S[NS][8];
+    uint4 w[NS];
+#pragma unroll
+    for (int i = 0; i < NS; ++i) {
+        const int c = threadIdx.x + i * T;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            P[i][e] = S[i][e] = f[i][e] = 0.0f;
+        w[i] = a.w_pre && c < chunks ? __ldg(reinterpret_cast<const uint4 *>(a.w_pre) + c) : zero;
+        if (a.y && c < chunks)
+            update_factor(a, c, f[i]);
+    }
+    int flip = 0, k = 0;
+    for (int m = blockIdx.x; m < a.M; m += gridDim.x, ++k) {
+        const size_t base = (size_t)m * chunks;
+        if (!ring.wait(k)) {
+            ring.abandon(k, a.status);
+            return;
+        }
+        uint4 hv[NS], yv[NS], xv[NS], gv[NS];
+        auto read = [&](int i) {
+            const int c = threadIdx.x + i * T;
+            const bool in = c < chunks;
+            hv[i] = in ? ring.chunk(k, 0, c) : zero;
+            yv[i] = in && at_y > 0 ? ring.chunk(k, at_y, c) : zero;
+            xv[i] = in && at_x > 0 ? ring.chunk(k, at_x, c) : zero;
+            gv[i] = in && at_g > 0 ? ring.chunk(k, at_g, c) : zero;
+        };
+        float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+            read(i);
+            grad_sums(hv[i], yv[i], xv[i], gv[i], w[i], f[i], s);
+        }
+        const float total = block_sum8(s, red[flip]);
+        flip ^= 1;
+        if (!RELOAD && threadIdx.x == 0)
+            ring.issue();
+        float t[6];
+#pragma unroll
+        for (int i = 0; i < 6; ++i)
+            t[i] = __shfl_sync(0xffffffffu, total, i);
+        const RowGrad q = grad_factors(a, inv_d, t[0], t[1], t[2], t[3], t[4], t[5]);
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+            const int c = threadIdx.x + i * T;
+            uint4 dh, dy;
+            if (RELOAD)
+                read(i);
+            grad_chunk(hv[i], yv[i], xv[i], gv[i], w[i], f[i], q, P[i], S[i], dh, dy);
+            if (c < chunks) {
+                reinterpret_cast<uint4 *>(g.dh_in)[base + c] = dh;
+                if (a.y)
+                    reinterpret_cast<uint4 *>(g.dy)[base + c] = dy;
+            }
+        }
+        if (RELOAD) {
+            __syncthreads();
+            if (threadIdx.x == 0)
+                ring.issue();
+        }
+    }
+    float *row = g.part + (size_t)blockIdx.x * (2 * a.D + 4);
+    float dot[1] = {0.0f};
+#pragma unroll
+    for (int i = 0; i < NS; ++i)
+        if (threadIdx.x + i * T < chunks)
+            dot[0] += put_partials(a, row, threadIdx.x + i * T, P[i], S[i]);
+    block_sum(dot, red[flip]);
+    if (threadIdx.x == 0)
+        row[2 * a.D] = dot[0];
+}
+
+// Rows of more than 8192 columns: straight from global memory, the columns' sums in
+// shared memory.
+constexpr int kWideThreads = 1024, kWideChunks = 2;   // a thread's chunks of 8 columns
+
+__global__ __launch_bounds__(kWideThreads) void residual_norm_backward_wide_kernel(NormGradArgs g)
+{
+    extern __shared__ __align__(16) float column_sums[];   // [P, S][8][chunks]
+    __shared__ float red[2][8 * 32];
     const NormArgs &a = g.f;
     tc::pdl_launch_dependents();
     tc::pdl_wait();
     const int T = blockDim.x, chunks = a.D / 8;
     const float inv_d = 1.0f / (float)a.D;
-    constexpr int NR = WIDE ? 1 : NS;
-    float P[NR][8], S[NR][8];
-#pragma unroll
-    for (int i = 0; i < NR; ++i)
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            P[i][e] = S[i][e] = 0.0f;
-    if (WIDE)
-        for (int i = threadIdx.x; i < 2 * NS * T * 8; i += T)
-            wide_acc[i] = 0.0f;
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    for (int i = threadIdx.x; i < 16 * chunks; i += T)
+        column_sums[i] = 0.0f;
     __syncthreads();
     int flip = 0;
     for (int m = blockIdx.x; m < a.M; m += gridDim.x) {
         const size_t base = (size_t)m * chunks;
-        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-        uint4 hv[NS], yv[NS], xv[NS], gv[NS];
+        uint4 hv[kWideChunks], yv[kWideChunks], xv[kWideChunks], gv[kWideChunks];
+        float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int i = 0; i < NS; ++i) {
+        for (int i = 0; i < kWideChunks; ++i) {
             const int c = threadIdx.x + i * T;
             const bool in = c < chunks;
-            hv[i] = in ? __ldg(reinterpret_cast<const uint4 *>(a.h) + base + c) : zero;
-            yv[i] = in && a.y ? __ldg(reinterpret_cast<const uint4 *>(a.y) + base + c) : zero;
-            xv[i] = in && g.dx ? __ldg(reinterpret_cast<const uint4 *>(g.dx) + base + c) : zero;
-            gv[i] = in && g.dh ? reinterpret_cast<const uint4 *>(g.dh)[base + c] : zero;
+            hv[i] = in ? ldg_stream_v4(reinterpret_cast<const uint4 *>(a.h) + base + c) : zero;
+            yv[i] = in && a.y ? ldg_stream_v4(reinterpret_cast<const uint4 *>(a.y) + base + c) : zero;
+            xv[i] = in && g.dx ? ldg_stream_v4(reinterpret_cast<const uint4 *>(g.dx) + base + c) : zero;
+            gv[i] = in && g.dh ? reinterpret_cast<const uint4 *>(g.dh)[base + c] : zero;   // dh_in may be dh
         }
-        float s[3] = {0.0f, 0.0f, 0.0f};   // h'^2, a h', y^2
+        float f[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int i = 0; i < NS; ++i) {
+        for (int i = 0; i < kWideChunks; ++i) {
             const int c = threadIdx.x + i * T;
-            float h[8], x[8], y[8], w[8];
-            unpack8(hv[i], h);
-            unpack8(xv[i], x);
-            unpack8(yv[i], y);
-            unpack8(a.w_pre && c < chunks ? __ldg(reinterpret_cast<const uint4 *>(a.w_pre) + c) : zero, w);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                s[0] = fmaf(h[e], h[e], s[0]);
-                s[1] = fmaf(x[e] * w[e], h[e], s[1]);
-                s[2] = fmaf(y[e], y[e], s[2]);
-            }
-        }
-        block_sum(s, red[flip]);
-        flip ^= 1;
-        const float r = rsqrtf(s[0] * inv_d + a.eps);
-        const float ch = r * r * r * (s[1] * inv_d);
-        const float rp = a.w_post ? rsqrtf(s[2] * inv_d + a.eps) : 1.0f;
-        float t[1] = {0.0f};   // b y
-        float G[NS][8];
-#pragma unroll
-        for (int i = 0; i < NS; ++i) {
-            const int c = threadIdx.x + i * T;
-            float h[8], x[8], y[8], w[8], f[8];
-            unpack8(hv[i], h);
-            unpack8(xv[i], x);
-            unpack8(yv[i], y);
-            unpack8(gv[i], G[i]);
             if (c < chunks) {
-                unpack8(a.w_pre ? __ldg(reinterpret_cast<const uint4 *>(a.w_pre) + c) : zero, w);
                 if (a.y)
                     update_factor(a, c, f);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    G[i][e] = fmaf(r, x[e] * w[e], G[i][e]) - h[e] * ch;
-                    const float dp = x[e] * h[e] * r, ds = G[i][e] * y[e] * rp;
-                    if (WIDE) {
-                        wide_acc[e * NS * T + c] += dp;
-                        wide_acc[(8 + e) * NS * T + c] += ds;
-                    } else {
-                        P[i][e] += dp;
-                        S[i][e] += ds;
-                    }
-                    if (a.y)
-                        t[0] = fmaf(G[i][e] * f[e], y[e], t[0]);
-                }
-                reinterpret_cast<uint4 *>(g.dh_in)[base + c] = pack8(G[i]);
+                grad_sums(hv[i], yv[i], xv[i], gv[i], a.w_pre ? __ldg(reinterpret_cast<const uint4 *>(a.w_pre) + c) : zero, f, s);
             }
         }
-        float cy = 0.0f;
-        if (a.w_post) {
-            block_sum(t, red[flip]);
-            flip ^= 1;
-            cy = rp * rp * rp * (t[0] * inv_d);
-        }
-        if (a.y) {
+        const float total = block_sum8(s, red[flip]);
+        flip ^= 1;
+        float t[6];
 #pragma unroll
-            for (int i = 0; i < NS; ++i) {
-                const int c = threadIdx.x + i * T;
-                if (c < chunks) {
-                    float y[8], f[8];
-                    unpack8(yv[i], y);
+        for (int i = 0; i < 6; ++i)
+            t[i] = __shfl_sync(0xffffffffu, total, i);
+        const RowGrad q = grad_factors(a, inv_d, t[0], t[1], t[2], t[3], t[4], t[5]);
+#pragma unroll
+        for (int i = 0; i < kWideChunks; ++i) {
+            const int c = threadIdx.x + i * T;
+            if (c < chunks) {
+                if (a.y)
                     update_factor(a, c, f);
+                float P[8], S[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        f[e] = fmaf(rp * G[i][e], f[e], -y[e] * cy);
-                    reinterpret_cast<uint4 *>(g.dy)[base + c] = pack8(f);
+                for (int e = 0; e < 8; ++e) {
+                    P[e] = column_sums[e * chunks + c];
+                    S[e] = column_sums[(8 + e) * chunks + c];
                 }
+                uint4 dh, dy;
+                grad_chunk(hv[i], yv[i], xv[i], gv[i], a.w_pre ? __ldg(reinterpret_cast<const uint4 *>(a.w_pre) + c) : zero, f, q, P,
+                           S, dh, dy);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    column_sums[e * chunks + c] = P[e];
+                    column_sums[(8 + e) * chunks + c] = S[e];
+                }
+                reinterpret_cast<uint4 *>(g.dh_in)[base + c] = dh;
+                if (a.y)
+                    reinterpret_cast<uint4 *>(g.dy)[base + c] = dy;
             }
         }
     }
-    // this CTA's row of partials: P, S, and sum_d w_post S for a single gate
     float *row = g.part + (size_t)blockIdx.x * (2 * a.D + 4);
     float dot[1] = {0.0f};
+    for (int c = threadIdx.x; c < chunks; c += T) {
+        float P[8], S[8];
 #pragma unroll
-    for (int i = 0; i < NS; ++i) {
-        const int c = threadIdx.x + i * T;
-        if (c < chunks) {
-            float p[8], q[8], w[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                p[e] = WIDE ? wide_acc[e * NS * T + c] : P[WIDE ? 0 : i][e];
-                q[e] = WIDE ? wide_acc[(8 + e) * NS * T + c] : S[WIDE ? 0 : i][e];
-                w[e] = 1.0f;
-            }
-            if (a.w_post)
-                unpack8(__ldg(reinterpret_cast<const uint4 *>(a.w_post) + c), w);
-#pragma unroll
-            for (int e = 0; e < 8; e += 4) {
-                *reinterpret_cast<float4 *>(row + 8 * c + e) = make_float4(p[e], p[e + 1], p[e + 2], p[e + 3]);
-                *reinterpret_cast<float4 *>(row + a.D + 8 * c + e) = make_float4(q[e], q[e + 1], q[e + 2], q[e + 3]);
-            }
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                dot[0] = fmaf(w[e], q[e], dot[0]);
+        for (int e = 0; e < 8; ++e) {
+            P[e] = column_sums[e * chunks + c];
+            S[e] = column_sums[(8 + e) * chunks + c];
         }
+        dot[0] += put_partials(a, row, c, P, S);
     }
     block_sum(dot, red[flip]);
     if (threadIdx.x == 0)
         row[2 * a.D] = dot[0];
 }
 
-// Sums the CTAs' partial rows column by column, in the order of the CTAs.
+// Sums the CTAs' partial rows column by column, in a fixed order.
+constexpr int kColumnGroups = 16;
+
 __global__ void residual_norm_columns_kernel(NormGradArgs g, int ctas)
 {
     const NormArgs &a = g.f;
     tc::pdl_wait();
     const int stride = 2 * a.D + 4;
-    __shared__ float part[8][33];
+    __shared__ float part[kColumnGroups][33];
     const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
     const int col = blockIdx.x * 32 + lane;   // 0 .. 2 D: P, S, then the single gate's sum
     float s = 0.0f;
     if (col <= 2 * a.D)
-        for (int i = grp; i < ctas; i += 8)
+#pragma unroll 8
+        for (int i = grp; i < ctas; i += kColumnGroups)
             s += g.part[(size_t)i * stride + col];
     part[grp][lane] = s;
     __syncthreads();
     if (grp != 0 || col > 2 * a.D)
         return;
 #pragma unroll
-    for (int i = 1; i < 8; ++i)
+    for (int i = 1; i < kColumnGroups; ++i)
         s += part[i][lane];
     if (col < a.D) {
         if (g.dw_pre)
@@ -399,20 +980,63 @@ int norm_threads(int D, int ns)
     return (need + 31) / 32 * 32;
 }
 
-// CTAs of the backward kernel: two per SM, each with one row of partials.
-int backward_ctas(int M)
+// CTAs of the backward kernels that an SM holds, and how many have a row of partials.
+int backward_ctas_per_sm(int D) { return D <= 512 ? 2 : D <= 1024 ? 4 : D <= 2048 ? 2 : 1; }
+int backward_ctas(int M, int D)
 {
-    const int most = 2 * device_sm_count();
+    const int most = backward_ctas_per_sm(D) * device_sm_count();
     return M < most ? M : most;
+}
+
+// Stages of a ring of n rows each, for `ctas` CTAs an SM.
+int ring_stages(int D, int n, int ctas)
+{
+    const int fit = (220 * 1024 / ctas - 4096) / (n * D * 2);
+    return fit < kRingStages ? fit : kRingStages;
+}
+
+template <class Kernel, class... Args>
+cudaError_t launch_big(Kernel kernel, int grid, int threads, size_t smem, cudaStream_t stream, Args... args)
+{
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    return e != cudaSuccess ? e : tc::launch_pdl(kernel, dim3(grid), dim3(threads), smem, stream, args...);
+}
+
+template <int GS, int NS>
+cudaError_t launch_rows(const NormArgs &a, cudaStream_t stream)
+{
+    const int need = (a.M + kRowsThreads / GS - 1) / (kRowsThreads / GS), most = 4 * device_sm_count();
+    return tc::launch_pdl(residual_norm_rows_kernel<GS, NS>, dim3(need < most ? need : most), dim3(kRowsThreads), 0, stream, a);
+}
+
+template <int GS, int NS>
+cudaError_t launch_backward_rows(const NormGradArgs &g, int ctas, cudaStream_t stream)
+{
+    return tc::launch_pdl(residual_norm_backward_rows_kernel<GS, NS>, dim3(ctas), dim3(kRowsThreads), 2 * g.f.D * sizeof(float),
+                          stream, g);
 }
 
 }  // namespace
 
 cudaError_t launch_residual_norm(const NormArgs &a, cudaStream_t stream)
 {
+    const int sms = device_sm_count();
+    if (a.D <= 1024) {
+        return a.D <= 64    ? launch_rows<8, 1>(a, stream)
+               : a.D <= 128 ? launch_rows<16, 1>(a, stream)
+               : a.D <= 256 ? launch_rows<32, 1>(a, stream)
+               : a.D <= 512 ? launch_rows<32, 2>(a, stream)
+                            : launch_rows<32, 4>(a, stream);
+    }
+    if (a.M > 2 * sms) {
+        const int n = a.y ? 2 : 1, per_sm = a.D <= 2048 ? 4 : a.D <= 4096 ? 2 : 1, stages = ring_stages(a.D, n, per_sm);
+        const size_t smem = (size_t)stages * n * a.D * 2;
+        return a.D <= 2048   ? launch_big(residual_norm_ring_kernel<2, 128>, per_sm * sms, 128, smem, stream, a, stages)
+               : a.D <= 4096 ? launch_big(residual_norm_ring_kernel<2, 256>, per_sm * sms, 256, smem, stream, a, stages)
+               : a.D <= 8192 ? launch_big(residual_norm_ring_kernel<2, 512>, per_sm * sms, 512, smem, stream, a, stages)
+                             : launch_big(residual_norm_ring_kernel<2, 1024>, per_sm * sms, 1024, smem, stream, a, stages);
+    }
     const int grid = a.M < 65536 ? a.M : 65536;
-    if (a.D <= 256)
-        return tc::launch_pdl(residual_norm_kernel<1, 32>, dim3(grid), dim3(norm_threads(a.D, 1)), 0, stream, a);
     if (a.D <= 8192)
         return tc::launch_pdl(residual_norm_kernel<2, 512>, dim3(grid), dim3(norm_threads(a.D, 2)), 0, stream, a);
     return tc::launch_pdl(residual_norm_kernel<2, 1024>, dim3(grid), dim3(norm_threads(a.D, 2)), 0, stream, a);
@@ -420,30 +1044,38 @@ cudaError_t launch_residual_norm(const NormArgs &a, cudaStream_t stream)
 
 size_t residual_norm_backward_workspace(int64_t M, int64_t D)
 {
-    return (size_t)backward_ctas((int)M) * (2 * (size_t)D + 4) * sizeof(float);
+    return (size_t)backward_ctas((int)M, (int)D) * (2 * (size_t)D + 4) * sizeof(float);
 }
 
 cudaError_t launch_residual_norm_backward(const NormGradArgs &g, cudaStream_t stream)
 {
-    const int ctas = backward_ctas(g.f.M);
+    const int D = g.f.D;
+    int ctas = backward_ctas(g.f.M, D);
     cudaError_t e;
-    if (g.f.D <= 256) {
-        e = tc::launch_pdl(residual_norm_backward_kernel<1, 32, false>, dim3(ctas), dim3(norm_threads(g.f.D, 1)), 0, stream, g);
-    } else if (g.f.D <= 8192) {
-        e = tc::launch_pdl(residual_norm_backward_kernel<2, 512, false>, dim3(ctas), dim3(norm_threads(g.f.D, 2)), 0, stream, g);
+    if (D <= 512) {
+        const int per = D <= 64 ? 32 : D <= 128 ? 16 : 8, need = (g.f.M + per - 1) / per;   // rows of a CTA at a time
+        ctas = need < ctas ? need : ctas;
+        e = D <= 64    ? launch_backward_rows<8, 1>(g, ctas, stream)
+            : D <= 128 ? launch_backward_rows<16, 1>(g, ctas, stream)
+            : D <= 256 ? launch_backward_rows<32, 1>(g, ctas, stream)
+                       : launch_backward_rows<32, 2>(g, ctas, stream);
+    } else if (D <= 8192) {
+        const int n = 1 + (g.f.y != nullptr) + (g.dx != nullptr) + (g.dh != nullptr);
+        const int stages = ring_stages(D, n, backward_ctas_per_sm(D));
+        const size_t smem = (size_t)stages * n * D * 2;
+        e = D <= 1024   ? launch_big(residual_norm_backward_ring_kernel<1, 128, false>, ctas, 128, smem, stream, g, stages)
+            : D <= 2048 ? launch_big(residual_norm_backward_ring_kernel<1, 256, false>, ctas, 256, smem, stream, g, stages)
+            : D <= 4096 ? launch_big(residual_norm_backward_ring_kernel<1, 512, false>, ctas, 512, smem, stream, g, stages)
+                        : launch_big(residual_norm_backward_ring_kernel<2, 512, true>, ctas, 512, smem, stream, g, stages);
     } else {
-        const int T = norm_threads(g.f.D, 2);
-        const size_t smem = (size_t)2 * 2 * T * 8 * sizeof(float);
-        e = cudaFuncSetAttribute(residual_norm_backward_kernel<2, 1024, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)smem);
-        if (e == cudaSuccess)
-            e = tc::launch_pdl(residual_norm_backward_kernel<2, 1024, true>, dim3(ctas), dim3(T), smem, stream, g);
+        e = launch_big(residual_norm_backward_wide_kernel, ctas, norm_threads(D, kWideChunks), (size_t)2 * D * sizeof(float),
+                       stream, g);
     }
     if (e != cudaSuccess)
         return e;
     if (!g.dw_pre && !g.dw_post && !g.dgate)
         return cudaSuccess;
-    return tc::launch_pdl(residual_norm_columns_kernel, dim3((2 * g.f.D + 1 + 31) / 32), dim3(256), 0, stream, g, ctas);
+    return tc::launch_pdl(residual_norm_columns_kernel, dim3((2 * D + 1 + 31) / 32), dim3(32 * kColumnGroups), 0, stream, g, ctas);
 }
 
 }  // namespace s3d8
