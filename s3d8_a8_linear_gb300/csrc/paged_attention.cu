@@ -1029,7 +1029,8 @@ cudaError_t launch(const AttnArgs &a, const AttnPlan &p, int ctas, cudaStream_t 
     constexpr int smem = WARPS * STAGES * Shape<DP, INT8>::kStage;
     static_assert(WARPS <= kMaxWarps && smem <= 226 * 1024, "the rings");
     auto kernel = paged_attention_kernel<DP, INT8, NB, ALIGNED, WARPS, STAGES>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    static std::atomic<unsigned long long> allowed;
+    cudaError_t e = tc::allow_smem(kernel, smem, allowed);
     if (e == cudaSuccess)
         e = tc::launch_pdl(kernel, dim3(ctas), dim3(WARPS * 32), (size_t)smem, stream, a, p);
     if (e != cudaSuccess)

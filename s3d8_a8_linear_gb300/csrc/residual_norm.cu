@@ -990,10 +990,12 @@ int ring_stages(int D, int n, int ctas)
     return fit < kRingStages ? fit : kRingStages;
 }
 
-template <class Kernel, class... Args>
-cudaError_t launch_big(Kernel kernel, int grid, int threads, size_t smem, cudaStream_t stream, Args... args)
+// A kernel whose shared memory follows from the call's width: it is allowed all there is.
+template <auto kernel, class... Args>
+cudaError_t launch_big(int grid, int threads, size_t smem, cudaStream_t stream, Args... args)
 {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static std::atomic<unsigned long long> allowed;
+    const cudaError_t e = tc::allow_smem(kernel, 224 * 1024, allowed);
     return e != cudaSuccess ? e : tc::launch_pdl(kernel, dim3(grid), dim3(threads), smem, stream, args...);
 }
 
@@ -1026,10 +1028,10 @@ cudaError_t launch_residual_norm(const NormArgs &a, cudaStream_t stream)
     if (a.M > 2 * sms) {
         const int n = a.y ? 2 : 1, per_sm = a.D <= 2048 ? 4 : a.D <= 4096 ? 2 : 1, stages = ring_stages(a.D, n, per_sm);
         const size_t smem = (size_t)stages * n * a.D * 2;
-        return a.D <= 2048   ? launch_big(residual_norm_ring_kernel<2, 128>, per_sm * sms, 128, smem, stream, a, stages)
-               : a.D <= 4096 ? launch_big(residual_norm_ring_kernel<2, 256>, per_sm * sms, 256, smem, stream, a, stages)
-               : a.D <= 8192 ? launch_big(residual_norm_ring_kernel<2, 512>, per_sm * sms, 512, smem, stream, a, stages)
-                             : launch_big(residual_norm_ring_kernel<2, 1024>, per_sm * sms, 1024, smem, stream, a, stages);
+        return a.D <= 2048   ? launch_big<residual_norm_ring_kernel<2, 128>>(per_sm * sms, 128, smem, stream, a, stages)
+               : a.D <= 4096 ? launch_big<residual_norm_ring_kernel<2, 256>>(per_sm * sms, 256, smem, stream, a, stages)
+               : a.D <= 8192 ? launch_big<residual_norm_ring_kernel<2, 512>>(per_sm * sms, 512, smem, stream, a, stages)
+                             : launch_big<residual_norm_ring_kernel<2, 1024>>(per_sm * sms, 1024, smem, stream, a, stages);
     }
     const int grid = a.M < 65536 ? a.M : 65536;
     if (a.D <= 8192)
@@ -1058,12 +1060,12 @@ cudaError_t launch_residual_norm_backward(const NormGradArgs &g, cudaStream_t st
         const int n = 1 + (g.f.y != nullptr) + (g.dx != nullptr) + (g.dh != nullptr);
         const int stages = ring_stages(D, n, backward_ctas_per_sm(D));
         const size_t smem = (size_t)stages * n * D * 2;
-        e = D <= 1024   ? launch_big(residual_norm_backward_ring_kernel<2, 64>, ctas, 64, smem, stream, g, stages)
-            : D <= 2048 ? launch_big(residual_norm_backward_ring_kernel<2, 128>, ctas, 128, smem, stream, g, stages)
-            : D <= 4096 ? launch_big(residual_norm_backward_ring_kernel<2, 256>, ctas, 256, smem, stream, g, stages)
-                        : launch_big(residual_norm_backward_ring_kernel<2, 512>, ctas, 512, smem, stream, g, stages);
+        e = D <= 1024   ? launch_big<residual_norm_backward_ring_kernel<2, 64>>(ctas, 64, smem, stream, g, stages)
+            : D <= 2048 ? launch_big<residual_norm_backward_ring_kernel<2, 128>>(ctas, 128, smem, stream, g, stages)
+            : D <= 4096 ? launch_big<residual_norm_backward_ring_kernel<2, 256>>(ctas, 256, smem, stream, g, stages)
+                        : launch_big<residual_norm_backward_ring_kernel<2, 512>>(ctas, 512, smem, stream, g, stages);
     } else {
-        e = launch_big(residual_norm_backward_wide_kernel, ctas, norm_threads(D, kWideChunks), (size_t)2 * D * sizeof(float),
+        e = launch_big<residual_norm_backward_wide_kernel>(ctas, norm_threads(D, kWideChunks), (size_t)2 * D * sizeof(float),
                        stream, g);
     }
     if (e != cudaSuccess)

@@ -6,6 +6,8 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <atomic>
+
 #include "common.cuh"
 #include "launch.h"
 #include "tma.cuh"
@@ -282,6 +284,25 @@ inline cudaError_t launch_pdl(Kernel kernel, dim3 grid, dim3 block, size_t smem,
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Lets `kernel` take `smem` bytes of dynamic shared memory on the current device;
+// asked of the runtime once per device (`done`: a bit for each, one variable per
+// kernel), since the call costs as much as a fifth of a launch.
+template <typename Kernel>
+inline cudaError_t allow_smem(Kernel kernel, size_t smem, std::atomic<unsigned long long> &done)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+    if (done.load(std::memory_order_relaxed) & bit)
+        return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e == cudaSuccess)
+        done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
 }
 
 // ---- SM-pair (cluster of two CTAs) building blocks, shared by the two pair

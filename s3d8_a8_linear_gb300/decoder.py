@@ -8,7 +8,6 @@ formulas, layouts and errors).
 from __future__ import annotations
 
 import ctypes
-import math
 
 import torch
 
@@ -67,46 +66,41 @@ def _rows(t, name, dtype):
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.stride(-1) != 1 and t.shape[-1] != 1:
+    *lead, last = t.stride()
+    if last != 1 and t.shape[-1] != 1:
         raise ValueError(f"{name} must have contiguous columns")
-    return t.data_ptr(), [st if n > 1 else 0 for n, st in zip(t.shape[:-1], t.stride())]
+    if 1 in t.shape:        # an axis of one element may have any stride
+        lead = [st if n > 1 else 0 for n, st in zip(t.shape, lead)]
+    return t.data_ptr(), lead
 
 
 def _space(workspace, need, device):
-    """The caller's workspace, or a new one; its pointer and size."""
+    """The caller's workspace, or a new one of need() bytes; its pointer and size."""
     if workspace is None:
-        workspace = torch.empty((max(need, 1),), dtype=torch.uint8, device=device)
+        workspace = torch.empty((max(need(), 1),), dtype=torch.uint8, device=device)
     return _dev(workspace, "workspace", torch.uint8), workspace.numel()
 
 
 # ---- residual norms ---------------------------------------------------------
 
 
-def _norm_args(h, y, w_post, gate, w_pre, tanh_gate):
-    if h.dim() != 2:
+_BF, _I8, _I32T, _F32 = torch.bfloat16, torch.int8, torch.int32, torch.float32
+
+
+def _norm_args(h, y, w_post, gate, w_pre, tanh_gate, shape):
+    """The arguments that both directions begin with (behind the pointer of h)."""
+    if len(shape) != 2:
         raise ValueError("h must be 2-D [M, D]")
-    M, D = h.shape
-    n = 0 if gate is None else gate.numel()
-    if gate is not None and gate.shape != (n,):
-        raise ValueError(f"gate must be 1-D, got {tuple(gate.shape)}")
-    bf = torch.bfloat16
-    return M, D, (_dev(h, "h", bf), _opt(y, "y", bf, (M, D)), _opt(w_post, "w_post", bf, (D,)),
-                  _opt(gate, "gate", bf), n, int(tanh_gate), _opt(w_pre, "w_pre", bf, (D,)))
-
-
-def _norm(h, y, w_post, gate, w_pre, alpha, eps, tanh_gate, h_out, x, xq, xscale):
-    M, D, args = _norm_args(h, y, w_post, gate, w_pre, tanh_gate)
-    if y is None:
-        if h_out is not None:
-            raise ValueError("h_out needs y: without a block's output the stream does not change")
-    elif h_out is None:
-        h_out = torch.empty_like(h)
-    bf = torch.bfloat16
-    st = _load().s3d8_residual_norm(*args, alpha, eps, M, D, _opt(h_out, "h_out", bf, (M, D)),
-                                    _opt(x, "x", bf, (M, D)), _opt(xq, "xq", torch.int8, (M, D)),
-                                    _opt(xscale, "xscale", torch.float32, (M,)), _stream(h.device))
-    _check("s3d8_residual_norm", st)
-    return h if y is None else h_out
+    cols = shape[1:]
+    n = 0
+    if gate is not None:
+        n = gate.numel()
+        if gate.dim() != 1:
+            raise ValueError(f"gate must be 1-D, got {tuple(gate.shape)}")
+    return (None if y is None else _dev(y, "y", _BF, shape),
+            None if w_post is None else _dev(w_post, "w_post", _BF, cols),
+            None if gate is None else _dev(gate, "gate", _BF), n, tanh_gate,
+            None if w_pre is None else _dev(w_pre, "w_pre", _BF, cols))
 
 
 def residual_norm(h: torch.Tensor, y: torch.Tensor | None = None, w_post: torch.Tensor | None = None,
@@ -117,9 +111,26 @@ def residual_norm(h: torch.Tensor, y: torch.Tensor | None = None, w_post: torch.
     (h', x).  Without w_post y enters as it is; without y the stream stays (h' is
     h); without w_pre there is no x (None).  gate: bf16 [1] or [D], through tanh
     with tanh_gate.  h_out may be h."""
+    shape = h.shape
+    args = _norm_args(h, y, w_post, gate, w_pre, tanh_gate, shape)
     if w_pre is not None and x is None:
         x = torch.empty_like(h)
-    return _norm(h, y, w_post, gate, w_pre, alpha, eps, tanh_gate, h_out, x, None, None), x
+    h_out = _stream_out(h, y, h_out)
+    st = _load().s3d8_residual_norm(_dev(h, "h", _BF), *args, alpha, eps, shape[0], shape[1],
+                                    None if y is None else _dev(h_out, "h_out", _BF, shape),
+                                    None if x is None else _dev(x, "x", _BF, shape), None, None,
+                                    _stream(h.device))
+    if st:
+        _check("s3d8_residual_norm", st)
+    return h_out, x
+
+
+def _stream_out(h, y, h_out):
+    if y is None:
+        if h_out is not None:
+            raise ValueError("h_out needs y: without a block's output the stream does not change")
+        return h
+    return torch.empty_like(h) if h_out is None else h_out
 
 
 def residual_norm_quant(h: torch.Tensor, y: torch.Tensor | None = None,
@@ -131,11 +142,20 @@ def residual_norm_quant(h: torch.Tensor, y: torch.Tensor | None = None,
     it -> (h', xq int8 [M, D], xscale fp32 [M]), ready for linear()."""
     if w_pre is None:
         raise ValueError("residual_norm_quant needs w_pre")
+    shape, dev = h.shape, h.device
+    args = _norm_args(h, y, w_post, gate, w_pre, tanh_gate, shape)
     if xq is None:
-        xq = torch.empty(h.shape, dtype=torch.int8, device=h.device)
+        xq = torch.empty(shape, dtype=_I8, device=dev)
     if xscale is None:
-        xscale = torch.empty(h.shape[:1], dtype=torch.float32, device=h.device)
-    return _norm(h, y, w_post, gate, w_pre, alpha, eps, tanh_gate, h_out, None, xq, xscale), xq, xscale
+        xscale = torch.empty(shape[:1], dtype=_F32, device=dev)
+    h_out = _stream_out(h, y, h_out)
+    st = _load().s3d8_residual_norm(_dev(h, "h", _BF), *args, alpha, eps, shape[0], shape[1],
+                                    None if y is None else _dev(h_out, "h_out", _BF, shape), None,
+                                    _dev(xq, "xq", _I8, shape), _dev(xscale, "xscale", _F32, shape[:1]),
+                                    _stream(dev))
+    if st:
+        _check("s3d8_residual_norm", st)
+    return h_out, xq, xscale
 
 
 def residual_norm_backward_workspace(M: int, D: int, device="cuda") -> torch.Tensor:
@@ -153,8 +173,9 @@ def residual_norm_backward(dh: torch.Tensor | None, dx: torch.Tensor | None, h: 
     as the forward call returned it.  Returns a dict with "dh" (of the forward
     call's h) and, where their argument is given, "dy" (bf16), "dw_post", "dw_pre"
     and "dgate" (fp32)."""
-    M, D, args = _norm_args(h, y, w_post, gate, w_pre, tanh_gate)
-    bf, dev = torch.bfloat16, h.device
+    shape, bf, dev = h.shape, torch.bfloat16, h.device
+    args = _norm_args(h, y, w_post, gate, w_pre, tanh_gate, shape)
+    M, D = shape
     got = {"dh": torch.empty_like(h)}
     if y is not None:
         got["dy"] = torch.empty_like(h)
@@ -165,10 +186,9 @@ def residual_norm_backward(dh: torch.Tensor | None, dx: torch.Tensor | None, h: 
     ptr = {k: t.data_ptr() for k, t in got.items()}
     ws = (None, 0)
     if M > 0:
-        ws = _space(workspace, 0 if workspace is not None else
-                    L.s3d8_residual_norm_backward_workspace_size(M, D), dev)
-    st = L.s3d8_residual_norm_backward(_opt(dh, "dh", bf, (M, D)), _opt(dx, "dx", bf, (M, D)), *args,
-                                       alpha, eps, M, D, ptr["dh"], ptr.get("dy"), ptr.get("dw_pre"),
+        ws = _space(workspace, lambda: L.s3d8_residual_norm_backward_workspace_size(M, D), dev)
+    st = L.s3d8_residual_norm_backward(_opt(dh, "dh", bf, shape), _opt(dx, "dx", bf, shape),
+                                       _dev(h, "h", bf), *args, alpha, eps, M, D, ptr["dh"], ptr.get("dy"), ptr.get("dw_pre"),
                                        ptr.get("dw_post"), ptr.get("dgate"), *ws, _stream(dev))
     _check("s3d8_residual_norm_backward", st)
     return got
@@ -272,25 +292,25 @@ def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cos: torch.Te
     (fp32) at positions [T], and store k, v as tokens `positions` of the block
     table's rows (rows None: token t of row t).  Returns the rotated q; a negative
     position marks a padding token."""
-    bf = torch.bfloat16
-    (qp, qs), (kp, ks), (vp, vs) = _rows(q, "q", bf), _rows(k, "k", bf), _rows(v, "v", bf)
-    T, Hq, D = q.shape
+    (qp, qs), (kp, ks), (vp, vs) = _rows(q, "q", _BF), _rows(k, "k", _BF), _rows(v, "v", _BF)
+    shape = q.shape
+    T, Hq, D = shape
     want = (T, cache.heads, cache.dim)
     if k.shape != want or v.shape != want or D != cache.dim:
         raise ValueError(f"k and v must be {want} and q [{T}, Hq, {cache.dim}], got {tuple(k.shape)}, "
-                         f"{tuple(v.shape)} and {tuple(q.shape)}")
+                         f"{tuple(v.shape)} and {tuple(shape)}")
     if q_out is None:
-        q_out = torch.empty((T, Hq, D), dtype=bf, device=q.device)
-    max_pos, half = cos.shape
+        q_out = torch.empty(shape, dtype=_BF, device=q.device)
+    turns = cos.shape
+    max_pos, half = turns
     n, width = table.shape
-    i32, f32 = torch.int32, torch.float32
     st = _load().s3d8_rope_append(
-        qp, _Two(*qs), kp, _Two(*ks), vp, _Two(*vs), _dev(cos, "cos", f32),
-        _dev(sin, "sin", f32, (max_pos, half)), max_pos, 2 * half, int(interleaved),
-        _dev(positions, "positions", i32, (T,)), _opt(rows, "rows", i32, (T,)), T, Hq,
-        _dev(table, "table", i32), n, width, cache.ref, _dev(q_out, "q_out", bf, (T, Hq, D)),
-        _stream(q.device))
-    _check("s3d8_rope_append", st)
+        qp, _Two(*qs), kp, _Two(*ks), vp, _Two(*vs), _dev(cos, "cos", _F32), _dev(sin, "sin", _F32, turns),
+        max_pos, 2 * half, interleaved, _dev(positions, "positions", _I32T, shape[:1]),
+        None if rows is None else _dev(rows, "rows", _I32T, shape[:1]), T, Hq, _dev(table, "table", _I32T),
+        n, width, cache.ref, _dev(q_out, "q_out", _BF, shape), _stream(q.device))
+    if st:
+        _check("s3d8_rope_append", st)
     return q_out
 
 
@@ -307,22 +327,23 @@ def paged_attention(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: 
     tokens (the last `window` of them, if set) of row b of the block table.  scale
     defaults to dim ** -0.5.  Returns bf16 [B, Hq, dim]; lse [B, Hq] fp32, if
     given, receives the log-sum-exp of the scaled scores."""
-    if q.dim() != 3 or q.shape[2] != cache.dim:
-        raise ValueError(f"q must be [B, Hq, {cache.dim}], got {tuple(q.shape)}")
-    B, Hq, D = q.shape
-    bf, L = torch.bfloat16, _load()
+    shape, dev = q.shape, q.device
+    if len(shape) != 3 or shape[2] != cache.dim:
+        raise ValueError(f"q must be [B, Hq, {cache.dim}], got {tuple(shape)}")
+    B, Hq, D = shape
     if out is None:
-        out = torch.empty((B, Hq, D), dtype=bf, device=q.device)
-    if table.dim() != 2 or table.shape[0] != B:
+        out = torch.empty_like(q)
+    rows, width = table.shape
+    if rows != B:
         raise ValueError(f"table must be [{B}, width], got {tuple(table.shape)}")
-    ws = _space(workspace, 0 if workspace is not None else
-                L.s3d8_paged_attention_workspace_size(cache.ref, B, Hq), q.device)
-    st = L.s3d8_paged_attention(_dev(q, "q", bf), cache.ref, _dev(table, "table", torch.int32),
-                                table.shape[1], _dev(lens, "lens", torch.int32, (B,)), B, Hq,
-                                1.0 / math.sqrt(D) if scale is None else scale, window,
-                                _dev(out, "out", bf, (B, Hq, D)), _opt(lse, "lse", torch.float32, (B, Hq)),
-                                *ws, _stream(q.device))
-    _check("s3d8_paged_attention", st)
+    L = _load()
+    ws = _space(workspace, lambda: L.s3d8_paged_attention_workspace_size(cache.ref, B, Hq), dev)
+    st = L.s3d8_paged_attention(_dev(q, "q", _BF), cache.ref, _dev(table, "table", _I32T), width,
+                                _dev(lens, "lens", _I32T, shape[:1]), B, Hq,
+                                D ** -0.5 if scale is None else scale, window, _dev(out, "out", _BF, shape),
+                                None if lse is None else _dev(lse, "lse", _F32, shape[:2]), *ws, _stream(dev))
+    if st:
+        _check("s3d8_paged_attention", st)
     return out
 
 
@@ -342,8 +363,7 @@ def _table(table, lens, refs):
 
 
 def _meta_space(workspace, pages, rows, device):
-    return _space(workspace, 0 if workspace is not None else
-                  _load().s3d8_pages_workspace_size(pages, rows), device)
+    return _space(workspace, lambda: _load().s3d8_pages_workspace_size(pages, rows), device)
 
 
 def copy_pages(pool: KVPool, src: torch.Tensor, dst: torch.Tensor) -> None:
