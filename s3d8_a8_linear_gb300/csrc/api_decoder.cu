@@ -316,7 +316,7 @@ int s3d8_paged_attention(const void *q_bf16, const s3d8_kv_cache *cache, const i
     if (st != S3D8_OK)
         return st;
     if (B < 0 || B > S3D8_MAX_M || Hq < 1 || Hq > 65535 || Hq % a.kv.heads != 0 || B * Hq > kMaxInt || width < 0 ||
-        width > kMaxInt / a.kv.page_size || window < 0)
+        width > (kMaxInt - 64) / a.kv.page_size || window < 0)
         return S3D8_ERR_INVALID_ARG;
     if (B == 0)
         return S3D8_OK;
