@@ -11,9 +11,9 @@ using namespace attn;
 // Joins the parts of every sequence that was cut: block (unit of a sequence, query
 // row or all of them), its warps over the parts.  Run `first` left its part in its
 // second slot, the runs behind it in their first.
-constexpr int kJoinWarps = 8, kJoinBatch = 8;   // parts whose loads leave together
+constexpr int kJoinBatch = 8;   // parts whose loads leave together
 
-template <int DP>
+template <int DP, int kJoinWarps>
 __global__ __launch_bounds__(kJoinWarps * 32) void paged_attention_join_kernel(const __grid_constant__ AttnArgs a,
                                                                              const __grid_constant__ AttnPlan p)
 {
@@ -34,7 +34,7 @@ __global__ __launch_bounds__(kJoinWarps * 32) void paged_attention_join_kernel(c
     const float *parts = p.parts + (size_t)join.x * 2 * size;
     auto part = [&](int x) { return parts + (size_t)(2 * x + (x == 0)) * size; };
     if (count <= kJoinBatch) {                    // few parts: a query row a warp, all parts in it
-        for (int r = blockIdx.y * kJoinWarps + warp; r < rows; r += gridDim.y * kJoinWarps) {
+        for (int r = blockIdx.y + warp * gridDim.y; r < rows; r += gridDim.y * kJoinWarps) {
             float2 ml = make_float2(-INFINITY, 0.0f);
             if (lane < count)
                 ml = *reinterpret_cast<const float2 *>(part(lane) + p.rows * D + 2 * r);
@@ -148,24 +148,34 @@ __global__ __launch_bounds__(kJoinWarps * 32) void paged_attention_join_kernel(c
             if (128 * y + 4 * lane < DP)
                 *reinterpret_cast<float4 *>(&sums[warp][128 * y + 4 * lane]) = acc[y];
         __syncthreads();
-        float all = -INFINITY, total = 0.0f, v = 0.0f;
+        float all = -INFINITY, total = 0.0f;
 #pragma unroll
         for (int x = 0; x < kJoinWarps; ++x)
             all = fmaxf(all, tops[x]);
         const float zero = all == -INFINITY ? 0.0f : all;
 #pragma unroll
-        for (int x = 0; x < kJoinWarps; ++x) {
-            const float w = ex2(tops[x] - zero);
-            total = fmaf(w, totals[x], total);
-            if (threadIdx.x < D)
-                v = fmaf(w, sums[x][threadIdx.x], v);
-        }
+        for (int x = 0; x < kJoinWarps; ++x)
+            total = fmaf(ex2(tops[x] - zero), totals[x], total);
         const int64_t row = (int64_t)b * a.Hq + h * p.group + blk * 16 + r;
-        if (threadIdx.x < D)
-            a.out[row * D + threadIdx.x] = __float2bfloat16_rn(total == 0.0f ? 0.0f : v / total);
+        for (int d = threadIdx.x; d < D; d += kJoinWarps * 32) {
+            float v = 0.0f;
+#pragma unroll
+            for (int x = 0; x < kJoinWarps; ++x)
+                v = fmaf(ex2(tops[x] - zero), sums[x][d], v);
+            a.out[row * D + d] = __float2bfloat16_rn(total == 0.0f ? 0.0f : v / total);
+        }
         if (threadIdx.x == 0 && a.lse)
             a.lse[row] = (all + log2f(total)) * kLn2;
     }
+}
+
+template <int DP>
+cudaError_t launch_join(const AttnArgs &a, const AttnPlan &p, cudaStream_t stream)
+{
+    const unsigned units = (unsigned)a.B * p.units;
+    if ((int64_t)units * p.rows <= 4 * device_sm_count())
+        return tc::launch_pdl(paged_attention_join_kernel<DP, 16>, dim3(units, p.rows), dim3(16 * 32), 0, stream, a, p);
+    return tc::launch_pdl(paged_attention_join_kernel<DP, 4>, dim3(units), dim3(4 * 32), 0, stream, a, p);
 }
 
 // The workspace's layout: the queue, what to join, partial states.
@@ -216,12 +226,10 @@ cudaError_t launch_paged_attention(const AttnArgs &a, cudaStream_t stream)
     const cudaError_t e = launch(a, p, w.ctas, stream);
     if (e != cudaSuccess)
         return e;
-    // few sequences: a block a query row, since each may have many parts
-    const unsigned units = (unsigned)a.B * p.units, rows = units <= 1024 ? p.rows : 1;
-    const auto join = a.kv.dim <= 64    ? paged_attention_join_kernel<64>
-                      : a.kv.dim <= 128 ? paged_attention_join_kernel<128>
-                                        : paged_attention_join_kernel<256>;
-    return tc::launch_pdl(join, dim3(units, rows), dim3(kJoinWarps * 32), 0, stream, a, p);
+    // few sequences, of many parts perhaps: 16 warps a query row; many: a block of four warps each
+    return a.kv.dim <= 64    ? launch_join<64>(a, p, stream)
+           : a.kv.dim <= 128 ? launch_join<128>(a, p, stream)
+                             : launch_join<256>(a, p, stream);
 }
 
 }  // namespace s3d8

@@ -16,8 +16,8 @@
 // enter the second product as a 16-bit value and its 16-bit remainder, so that
 // they keep 16 bits or more.
 //
-// Every warp has one run of three quarters of its even share; the last quarter of
-// the tiles is in short runs that go to whichever warp is free (SMs differ by a
+// Every warp begins with a run of three quarters of its even share; the last quarter
+// of each share is in short runs that go to whichever warp is free (SMs differ by a
 // quarter in the bandwidth they get: with even shares alone the slowest CTA of 64
 // sequences of up to 8191 tokens ended at 174 us, the middle one at 146).  A run that
 // ends inside a sequence leaves (m, l, O) in the workspace, and a second kernel joins
@@ -216,37 +216,46 @@ __host__ __device__ __forceinline__ size_t part_floats(int rows, int D)
     return (size_t)rows * D + ((2 * rows + 3) & ~3);
 }
 
-// ---- runs: `warps` long ones, then short ones that are handed out ---------------------------
+// ---- runs ------------------------------------------------------------------------------------
+// The list of tiles in even shares, one a warp; of each share a long run, that its
+// warp begins with, and short ones behind it, that are handed out.  Runs are numbered
+// in the order of their tiles.
 struct Runs {
-    long long head, rest, total;   // tiles of a long run, of a short one, of the call
-    int warps, count;
+    long long total;               // tiles of the call
+    int share, head, rest, each;   // tiles of a share, of its long run, of a short one; runs of a share
+    int count;                     // shares
 
-    __device__ __forceinline__ Runs(long long tiles, int w, bool short_runs) : total(tiles), warps(w)
+    __device__ __forceinline__ Runs(long long tiles, int warps, bool short_runs) : total(tiles)
     {
-        const long long share = tiles / w;
-        // Even shares where a short run's own cost (its query rows, a part to write and to join) passes what it evens out
-        // (one sequence of 65536 tokens, 18 tiles a warp: 64 us, against 73 with short runs; 8 of up to 131072: 564 and 550).
-        if (share < 32 || !short_runs) {
-            head = (tiles + w - 1) / w;
-            rest = 1;
-            count = head ? (int)((tiles + head - 1) / head) : 0;
-        } else {
-            head = share * 3 / 4;
-            rest = share / 8;
-            count = w + (int)((tiles - head * w + rest - 1) / rest);
-        }
+        share = (int)((tiles + warps - 1) / warps);
+        // Even shares alone where a short run's own cost (its query rows, a part to write and to join) passes what it evens
+        // out (one sequence of 65536 tokens, 18 tiles a warp: 64 us, against 73 with short runs; 8 of up to 131072: 564 and
+        // 550).
+        const bool cut = share >= 32 && short_runs;
+        head = cut ? share * 3 / 4 : share;
+        rest = cut ? share / 8 : 1;
+        each = 1 + (share - head + rest - 1) / rest;
+        count = share ? (int)((tiles + share - 1) / share) : 0;
     }
     __device__ __forceinline__ long long begin(int r) const
     {
-        return r < warps ? r * head : warps * head + (r - warps) * rest;
+        const int s = r / each, j = r - s * each;
+        return (long long)s * share + (j ? min(share, head + (j - 1) * rest) : 0);
     }
-    __device__ __forceinline__ int length(int r) const { return (int)(min(total, begin(r + 1)) - begin(r)); }
+    // 0 or less where the list ends before it.
+    __device__ __forceinline__ int length(int r) const
+    {
+        const int s = r / each, j = r - s * each;
+        const int from = j ? min(share, head + (j - 1) * rest) : 0, to = min(share, head + j * rest);
+        return (int)min((long long)(to - from), total - (long long)s * share - from);
+    }
     __device__ __forceinline__ int of(long long tile) const
     {
-        return tile < warps * head ? (int)(tile / head) : warps + (int)((tile - warps * head) / rest);
+        const int s = (int)(tile / share), at = (int)(tile - (long long)s * share);
+        return s * each + (at < head ? 0 : 1 + (at - head) / rest);
     }
 };
-constexpr int kRunsPerWarp = 4;    // count <= 4 warps: a quarter of a share and two tiles, over an eighth of it
+constexpr int kRunsPerWarp = 4;    // a long one, and a quarter of a share and a tile in eighths of it
 
 // The number of the next short run.  The join kernel leaves the counter at 0 under a
 // tag; a workspace that holds anything else is set up by the first warp to ask.
@@ -328,33 +337,20 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
     __syncthreads();
     const long long total = scan[kScanThreads];
 
-    // ---- sequences of no tokens: zeros ------------------------------------------------
-    for (int b = blockIdx.x * WARPS + warp; b < a.B; b += gridDim.x * WARPS) {
-        if (a.lens[b] > 0 && a.width > 0)
-            continue;
-        for (int i = lane; i < p.units; i += 32)
-            p.joins[(int64_t)b * p.units + i] = make_int2(-1, -1);
-        for (int64_t i = lane; i < (int64_t)a.Hq * D; i += 32)
-            a.out[(int64_t)b * a.Hq * D + i] = __float2bfloat16_rn(0.0f);
-        if (a.lse)
-            for (int i = lane; i < a.Hq; i += 32)
-                a.lse[(int64_t)b * a.Hq + i] = -INFINITY;
-    }
-
     const Runs runs(total, gridDim.x * WARPS, !INT8);   // int8: bound by instructions, which every SM issues alike
     const int own = warp * gridDim.x + blockIdx.x;    // neighbouring runs on different SMs
-    if (own >= runs.count)
-        return;
     const size_t part_size = part_floats(p.rows, D);
-    {
+    if (own < runs.count) {
         const uint32_t ring = smem_addr(smem_raw) + warp * (STAGES * Sh::kStage);
         Cursor in;                            // the tile to fetch next,
-        int run = own, left = 0;              // its run, and the tiles left of that, with it
+        int run = own * runs.each, left = 0;  // its run, and the tiles left of that, with it
         bool new_run = true, done = false;
         int asked = -1;                       // lane 0: the short run that comes next
         auto ask = [&]() {
-            if (lane == 0 && runs.count > runs.warps)
-                asked = runs.warps + grab(p.queue);
+            if (lane == 0 && runs.each > 1) {
+                const int i = grab(p.queue), s = i / (runs.each - 1);
+                asked = s < runs.count ? s * runs.each + 1 + i - s * (runs.each - 1) : -1;
+            }
         };
         auto enter = [&]() {                  // to the first tile of `run`
             const long long tile = runs.begin(run);
@@ -398,11 +394,17 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
                     ask();                    // the answer is there when this run ends
                 return;
             }
-            run = runs.count > runs.warps ? __shfl_sync(0xffffffffu, asked, 0) : runs.count;
-            if (run < runs.count)
-                enter();
-            else
-                done = true;
+            for (;;) {
+                run = runs.each > 1 ? __shfl_sync(0xffffffffu, asked, 0) : -1;
+                if (run < 0) {
+                    done = true;
+                    return;
+                }
+                if (runs.length(run) > 0)
+                    break;
+                ask();                        // behind the end of the list
+            }
+            enter();
         };
         enter();
 
@@ -844,6 +846,19 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
             }
         }
         cp_wait<0>();
+    }
+
+    // ---- sequences of no tokens: zeros ------------------------------------------------
+    for (int b = blockIdx.x * WARPS + warp; b < a.B; b += gridDim.x * WARPS) {
+        if (a.lens[b] > 0 && a.width > 0)
+            continue;
+        for (int i = lane; i < p.units; i += 32)
+            p.joins[(int64_t)b * p.units + i] = make_int2(-1, -1);
+        for (int64_t i = lane; i < (int64_t)a.Hq * D; i += 32)
+            a.out[(int64_t)b * a.Hq * D + i] = __float2bfloat16_rn(0.0f);
+        if (a.lse)
+            for (int i = lane; i < a.Hq; i += 32)
+                a.lse[(int64_t)b * a.Hq + i] = -INFINITY;
     }
 }
 
