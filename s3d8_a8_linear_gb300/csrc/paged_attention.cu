@@ -217,6 +217,7 @@ cudaError_t launch_paged_attention(const AttnArgs &a, cudaStream_t stream)
         p.v16[i] = (uint32_t)(a.kv.vs[i] / (a.kv.int8 ? 16 : 8));
         p.sc[i] = (uint32_t)a.kv.ss[i];
     }
+    p.alike = p.k16[0] == p.v16[0] && p.k16[1] == p.v16[1] && p.k16[2] == p.v16[2];
     p.log_page = -1;
     for (int i = 0; i < 31; ++i)
         if (a.kv.page_size == 1 << i)

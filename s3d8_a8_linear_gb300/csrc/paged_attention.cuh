@@ -44,7 +44,7 @@ struct Shape {
     static constexpr int kChunks = kRow / 16;
     static constexpr int kKv = kTile * kRow;              // bytes of a tile's keys (and of its values)
     static constexpr int kScales = INT8 ? 2 * kTile * 4 : 0;
-    static constexpr int kStage = 2 * kKv + kScales + 16; // + what the tile is (TileInfo)
+    static constexpr int kStage = 2 * kKv + kScales + 16; // + what the tile is
 };
 
 // ---- the plan: which tiles, and whose -----------------------------------------
@@ -205,6 +205,7 @@ struct AttnPlan {
     int group;                   // query heads per key/value head
     int log_page;                // of a page size that is a power of two, else -1
     uint32_t k16[3], v16[3], sc[3];   // strides of pages, tokens, heads: 16 bytes of keys and values, scales
+    int alike;                   // keys and values have the same strides
     unsigned long long *queue;   // (kQueueTag, next short run): see grab
     int2 *joins;                 // [B units] first and last run of each sequence's parts, first < 0: nothing to join
     float *parts;                // [runs][2] partial states: of the sequence begun before the run, and of one that goes on behind it
@@ -278,7 +279,8 @@ static __device__ int grab(unsigned long long *queue)
     }
 }
 
-// What a stage's tile is: visible tokens (16 bits) and flags, sequence, unit, run.
+// What a stage's tile is: visible tokens (16 bits) and flags; of a new state also its
+// sequence, unit and run.
 constexpr uint32_t kNew = 1u << 16;       // first tile of a state: of its run, or of its sequence
 constexpr uint32_t kFirst = 1u << 17;     // first tile of its sequence
 constexpr uint32_t kLast = 1u << 18;      // last tile of its sequence
@@ -297,6 +299,7 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     __shared__ long long scan[kScanThreads + 1];
     __shared__ long long warp_tot[WARPS];
+    __shared__ uint4 state[WARPS];                // what each warp's running state is of (as its first tile says)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int D = a.kv.dim, S = a.kv.page_size;
     tc::pdl_launch_dependents();
@@ -437,14 +440,14 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
             row_page = a.table[in.b * a.width + col];
         };
         // Copies the tile that `in` stands at, looked up before.
-        auto fetch = [&](int stage) {
-            if (new_run || in.k == 0) {       // the query rows of a new state: into L1 by the time its first tile is there
+        auto fetch = [&](uint32_t base) {
+            const bool fresh = new_run || in.k == 0;
+            if (fresh) {       // the query rows of a new state: into L1 by the time its first tile is there
                 const int rows = min(p.group - in.blk * 16, p.rows);
                 const char *src = reinterpret_cast<const char *>(a.q + ((int64_t)in.b * a.Hq + in.h * p.group + in.blk * 16) * D);
                 for (int x = lane * 128; x < rows * D * 2; x += 32 * 128)
                     asm volatile("prefetch.global.L1 [%0];" ::"l"(src + x));
             }
-            const uint32_t base = ring + stage * Sh::kStage;
             const bool ok = row_seen && row_page >= 0 && row_page < a.kv.pages;
             if (row_seen && !ok)
                 atomicExch(a.status, kStatusBounds);   // its tokens stay masked
@@ -452,18 +455,23 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
             uint32_t mask;
             if (ALIGNED) {
                 const int tok = (in.s.first / kTile + in.k) * kTile;
-                const int lo = max(in.s.first - tok, 0), hi = min(in.s.len - tok, kTile);
-                mask = ok ? ((1u << hi) - 1u) & ~((1u << lo) - 1u) : 0u;
+                mask = 0xFFFFu;
+                if (!ok || tok < in.s.first || tok + kTile > in.s.len) {
+                    const int lo = max(in.s.first - tok, 0), hi = min(in.s.len - tok, kTile);
+                    mask = ok ? ((1u << hi) - 1u) & ~((1u << lo) - 1u) : 0u;
+                }
                 const uint32_t page = ok ? row_page : 0;
+                const uint64_t at_k = wide(page, p.k16[0], wide(row_slot, p.k16[1], wide(in.h, p.k16[2], 0))) << 4;
+                const uint64_t at_v =
+                    p.alike ? at_k : wide(page, p.v16[0], wide(row_slot, p.v16[1], wide(in.h, p.v16[2], 0))) << 4;
                 if (INT8) {
                     const float *sc = sc_lane + wide(page, p.sc[0], wide(row_slot, p.sc[1], wide(in.h, p.sc[2], 0)));
                     cp_async4(base + 2 * Sh::kKv + lane * 4, sc, (mask >> (lane & 15)) & 1 ? 4 : 0);
                 }
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv) {
-                    const uint32_t(&st)[3] = kv ? p.v16 : p.k16;
-                    const char *src = (kv ? v_lane : k_lane) + (wide(page, st[0], wide(row_slot, st[1], wide(in.h, st[2], 0))) << 4);
-                    const uint64_t step = wide(st[1], 16 * RPI, 0);
+                    const char *src = kv ? v_lane + at_v : k_lane + at_k;
+                    const uint64_t step = wide(kv ? p.v16[1] : p.k16[1], 16 * RPI, 0);
                     const uint32_t dst = base + kv * Sh::kKv;
                     if (mask == 0xFFFFu && D == DP) {
 #pragma unroll
@@ -503,12 +511,16 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
                 }
             }
             if (lane == 0) {
+                const uint32_t info = base + 2 * Sh::kKv + Sh::kScales;
                 const int u = in.h * p.blocks + in.blk;
-                const uint32_t what = (mask & 0xFFFFu) | (new_run || in.k == 0 ? kNew : 0u) | (in.k == 0 ? kFirst : 0u) |
+                const uint32_t what = (mask & 0xFFFFu) | (fresh ? kNew : 0u) | (in.k == 0 ? kFirst : 0u) |
                                       (in.k == in.s.tiles - 1 ? kLast : 0u) | (left == 1 ? kStop : 0u);
-                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(base + 2 * Sh::kKv + Sh::kScales), "r"(what),
-                             "r"(in.b), "r"(u), "r"(run)
-                             : "memory");
+                asm volatile("st.shared.u32 [%0], %1;" ::"r"(info), "r"(what) : "memory");
+                if (fresh) {
+                    asm volatile("st.shared.u32 [%0], %1;" ::"r"(info + 4), "r"(in.b) : "memory");
+                    asm volatile("st.shared.u32 [%0], %1;" ::"r"(info + 8), "r"(u) : "memory");
+                    asm volatile("st.shared.u32 [%0], %1;" ::"r"(info + 12), "r"(run) : "memory");
+                }
                 if (in.k == 0) {
                     int2 join = make_int2(-1, -1);
                     if (in.s.tiles > left)    // goes on behind this run
@@ -523,7 +535,7 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
 #pragma unroll
         for (int s = 0; s < STAGES - 1; ++s) {
             if (!done) {
-                fetch(s);
+                fetch(ring + s * Sh::kStage);
                 ++fetched;
                 advance();
                 look_up(!done);
@@ -539,24 +551,31 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
         float vf = 0.0f, vinv = 0.0f;         // int8: the power of two that carries the value scales
         bool whole = false;                   // this run has the sequence from its first tile on
 
-        for (int i = 0; i < fetched; ++i) {
+        uint32_t base = ring, filled = ring + (STAGES - 1) * Sh::kStage;   // stages of the tile, and of the next one to fetch
+        auto turn = [&](uint32_t &stage) {
+            stage += Sh::kStage;
+            if (stage == ring + STAGES * Sh::kStage)
+                stage = ring;
+        };
+        for (int i = 0; i < fetched; ++i, turn(base), turn(filled)) {
             __syncwarp();                     // every lane is done with tile i - 1, whose stage is filled again
             if (!done) {
-                fetch((i + STAGES - 1) % STAGES);
+                fetch(filled);
                 ++fetched;
                 advance();
                 look_up(!done);
             }
             cp_commit();
             __syncwarp();
-            const uint32_t base = ring + (i % STAGES) * Sh::kStage;
-            const uint4 info = lds_v4(base + 2 * Sh::kKv + Sh::kScales);
-            const uint32_t mask = info.x;
-            const int b = (int)info.y, blk = p.blocks == 1 ? 0 : (int)info.z % p.blocks, h = p.blocks == 1 ? (int)info.z : (int)info.z / p.blocks;
+            const uint32_t mask = lds_u32(base + 2 * Sh::kKv + Sh::kScales);
 
-            const int rows = min(p.group - blk * 16, p.rows);
-            const int64_t head0 = (int64_t)b * a.Hq + h * p.group + blk * 16;   // query row of the state's row 0
             if (mask & kNew) {
+                const uint4 info = lds_v4(base + 2 * Sh::kKv + Sh::kScales);
+                if (lane == 0)
+                    state[warp] = info;           // for the state's end
+                const int u = (int)info.z, h = p.blocks == 1 ? u : u / p.blocks, blk = u - h * p.blocks;
+                const int rows = min(p.group - blk * 16, p.rows);
+                const int64_t head0 = (int64_t)info.y * a.Hq + h * p.group + blk * 16;   // query row of the state's row 0
                 whole = mask & kFirst;
                 vf = vinv = 0.0f;
 #pragma unroll
@@ -787,6 +806,11 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
 
             // ---- the end of the sequence, or of the run ----------------------------------------------------
             if (mask & (kLast | kStop)) {
+                __syncwarp();
+                const uint4 info = state[warp];
+                const int u = (int)info.z, h = p.blocks == 1 ? u : u / p.blocks, blk = u - h * p.blocks;
+                const int rows = min(p.group - blk * 16, p.rows);
+                const int64_t head0 = (int64_t)info.y * a.Hq + h * p.group + blk * 16;
 #pragma unroll
                 for (int off = 4; off <= 16; off <<= 1)
 #pragma unroll
