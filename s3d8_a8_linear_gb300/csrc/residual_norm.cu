@@ -42,6 +42,53 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8])
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// Two fp32 lanes in a 64-bit register: one instruction for both, each rounded as the
+// scalar one would.
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 pair2(float lo, float hi)
+{
+    f2 d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+    return d;
+}
+__device__ __forceinline__ float2 split2(f2 v)
+{
+    float2 d;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(v));
+    return d;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c)
+{
+    f2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b)
+{
+    f2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+// Eight bf16 values as four pairs, and back.
+__device__ __forceinline__ void unpack4(uint4 v, f2 (&f)[4])
+{
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        f[j] = pair2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u));
+}
+__device__ __forceinline__ uint4 pack4(const f2 (&f)[4])
+{
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float2 v = split2(f[j]);
+        const __nv_bfloat162 p = __floats2bfloat162_rn(v.x, v.y);
+        w[j] = *reinterpret_cast<const uint32_t *>(&p);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 __device__ __forceinline__ float warp_sum_f(float v)
 {
 #pragma unroll
@@ -151,6 +198,15 @@ __device__ __forceinline__ void update_factor(const NormArgs &a, int chunk, floa
         const float s = a.gate && a.gate_n != 1 ? a.alpha * gate_value(a, 8 * chunk + e) : one;
         f[e] = a.w_post ? s * f[e] : s;
     }
+}
+
+__device__ __forceinline__ void update_factor(const NormArgs &a, int chunk, f2 (&f)[4])
+{
+    float v[8];
+    update_factor(a, chunk, v);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        f[e] = pair2(v[2 * e], v[2 * e + 1]);
 }
 
 template <int NS, int MAX_T>
@@ -563,24 +619,33 @@ struct RowGrad {
     float r, ch, rp, cy;
 };
 
-__device__ __forceinline__ void grad_sums(uint4 hv, uint4 yv, uint4 xv, uint4 gv, uint4 wv, const float (&f)[8], float (&s)[8])
+__device__ __forceinline__ void grad_sums(uint4 hv, uint4 yv, uint4 xv, uint4 gv, uint4 wv, const f2 (&f)[4], f2 (&s)[6])
 {
-    float h[8], y[8], x[8], g[8], w[8];
-    unpack8(hv, h);
-    unpack8(yv, y);
-    unpack8(xv, x);
-    unpack8(gv, g);
-    unpack8(wv, w);
+    f2 h[4], y[4], x[4], g[4], w[4];
+    unpack4(hv, h);
+    unpack4(yv, y);
+    unpack4(xv, x);
+    unpack4(gv, g);
+    unpack4(wv, w);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const float ae = x[e] * w[e], fy = f[e] * y[e];
-        s[0] = fmaf(h[e], h[e], s[0]);
-        s[1] = fmaf(ae, h[e], s[1]);
-        s[2] = fmaf(y[e], y[e], s[2]);
-        s[3] = fmaf(fy, g[e], s[3]);
-        s[4] = fmaf(fy, ae, s[4]);
-        s[5] = fmaf(fy, h[e], s[5]);
+    for (int e = 0; e < 4; ++e) {
+        const f2 ae = mul2(x[e], w[e]), fy = mul2(f[e], y[e]);
+        s[0] = fma2(h[e], h[e], s[0]);
+        s[1] = fma2(ae, h[e], s[1]);
+        s[2] = fma2(y[e], y[e], s[2]);
+        s[3] = fma2(fy, g[e], s[3]);
+        s[4] = fma2(fy, ae, s[4]);
+        s[5] = fma2(fy, h[e], s[5]);
     }
+}
+__device__ __forceinline__ void fold_sums(const f2 (&s)[6], float (&v)[8])
+{
+#pragma unroll
+    for (int i = 0; i < 6; ++i) {
+        const float2 t = split2(s[i]);
+        v[i] = t.x + t.y;
+    }
+    v[6] = v[7] = 0.0f;
 }
 
 __device__ __forceinline__ RowGrad grad_factors(const NormArgs &a, float inv_d, float hh, float ah, float yy, float yg, float ya,
@@ -595,29 +660,38 @@ __device__ __forceinline__ RowGrad grad_factors(const NormArgs &a, float inv_d, 
 }
 
 // One chunk's gradients, and its columns' sums P += dx h' r, S += G y r'.
-__device__ __forceinline__ void grad_chunk(uint4 hv, uint4 yv, uint4 xv, uint4 gv, uint4 wv, const float (&f)[8], const RowGrad &q,
-                                           float (&P)[8], float (&S)[8], uint4 &dh, uint4 &dy)
+__device__ __forceinline__ void grad_chunk(uint4 hv, uint4 yv, uint4 xv, uint4 gv, uint4 wv, const f2 (&f)[4], const RowGrad &q,
+                                           f2 (&P)[4], f2 (&S)[4], uint4 &dh, uint4 &dy)
 {
-    float h[8], y[8], x[8], g[8], w[8], d[8];
-    unpack8(hv, h);
-    unpack8(yv, y);
-    unpack8(xv, x);
-    unpack8(gv, g);
-    unpack8(wv, w);
+    f2 h[4], y[4], x[4], g[4], w[4];
+    unpack4(hv, h);
+    unpack4(yv, y);
+    unpack4(xv, x);
+    unpack4(gv, g);
+    unpack4(wv, w);
+    const f2 r = pair2(q.r, q.r), ch = pair2(-q.ch, -q.ch), rp = pair2(q.rp, q.rp), cy = pair2(-q.cy, -q.cy);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        g[e] = fmaf(-h[e], q.ch, fmaf(q.r, x[e] * w[e], g[e]));
-        P[e] = fmaf(x[e] * h[e], q.r, P[e]);
-        S[e] = fmaf(g[e] * y[e], q.rp, S[e]);
-        d[e] = fmaf(q.rp * g[e], f[e], -y[e] * q.cy);
+    for (int e = 0; e < 4; ++e) {
+        g[e] = fma2(h[e], ch, fma2(r, mul2(x[e], w[e]), g[e]));
+        P[e] = fma2(mul2(x[e], h[e]), r, P[e]);
+        const f2 gr = mul2(rp, g[e]);
+        S[e] = fma2(gr, y[e], S[e]);
+        x[e] = fma2(gr, f[e], mul2(y[e], cy));
     }
-    dh = pack8(g);
-    dy = pack8(d);
+    dh = pack4(g);
+    dy = pack4(x);
 }
 
 // A CTA's row of partials: P, S, and sum_d w_post S for a single gate.
-__device__ __forceinline__ float put_partials(const NormArgs &a, float *row, int c, const float (&P)[8], const float (&S)[8])
+__device__ __forceinline__ float put_partials(const NormArgs &a, float *row, int c, const f2 (&P2)[4], const f2 (&S2)[4])
 {
+    float P[8], S[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float2 u = split2(P2[e]), v = split2(S2[e]);
+        P[2 * e] = u.x, P[2 * e + 1] = u.y;
+        S[2 * e] = v.x, S[2 * e + 1] = v.y;
+    }
     float w[8] = {1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f}, dot = 0.0f;
     if (a.w_post)
         unpack8(__ldg(reinterpret_cast<const uint4 *>(a.w_post) + c), w);
@@ -643,14 +717,14 @@ __global__ __launch_bounds__(kRowsThreads) void residual_norm_backward_rows_kern
     const int lane = threadIdx.x % GS, chunks = a.D / 8;
     const float inv_d = 1.0f / (float)a.D;
     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-    float f[NS][8], P[NS][8], S[NS][8];
+    f2 f[NS][4], P[NS][4], S[NS][4];
     uint4 w[NS];
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
         const int c = lane + i * GS;
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            P[i][e] = S[i][e] = f[i][e] = 0.0f;
+        for (int e = 0; e < 4; ++e)
+            P[i][e] = S[i][e] = f[i][e] = 0ull;
         w[i] = a.w_pre && c < chunks ? __ldg(reinterpret_cast<const uint4 *>(a.w_pre) + c) : zero;
         if (a.y && c < chunks)
             update_factor(a, c, f[i]);
@@ -660,7 +734,7 @@ __global__ __launch_bounds__(kRowsThreads) void residual_norm_backward_rows_kern
         const int m = m0 + group;
         const size_t base = (size_t)m * chunks;
         uint4 hv[NS], yv[NS], xv[NS], gv[NS];
-        float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+        f2 s2[6] = {0ull, 0ull, 0ull, 0ull, 0ull, 0ull};
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
             const int c = lane + i * GS;
@@ -672,7 +746,9 @@ __global__ __launch_bounds__(kRowsThreads) void residual_norm_backward_rows_kern
         }
 #pragma unroll
         for (int i = 0; i < NS; ++i)
-            grad_sums(hv[i], yv[i], xv[i], gv[i], w[i], f[i], s);
+            grad_sums(hv[i], yv[i], xv[i], gv[i], w[i], f[i], s2);
+        float s[8];
+        fold_sums(s2, s);
 #pragma unroll
         for (int i = 0; i < 6; ++i)
             s[i] = group_sum<GS>(s[i]);
@@ -695,9 +771,10 @@ __global__ __launch_bounds__(kRowsThreads) void residual_norm_backward_rows_kern
 #pragma unroll
         for (int i = 0; i < NS; ++i)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                P[i][e] += __shfl_xor_sync(0xffffffffu, P[i][e], o);
-                S[i][e] += __shfl_xor_sync(0xffffffffu, S[i][e], o);
+            for (int e = 0; e < 4; ++e) {
+                const f2 one = pair2(1.0f, 1.0f);
+                P[i][e] = fma2(__shfl_xor_sync(0xffffffffu, P[i][e], o), one, P[i][e]);
+                S[i][e] = fma2(__shfl_xor_sync(0xffffffffu, S[i][e], o), one, S[i][e]);
             }
     const int warp = threadIdx.x >> 5;
     for (int x = 0; x < kRowsThreads / 32; ++x) {
@@ -707,12 +784,15 @@ __global__ __launch_bounds__(kRowsThreads) void residual_norm_backward_rows_kern
                 const int c = lane + i * GS;
                 if (c < chunks) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        float *to = column_sums + 8 * c + e;
-                        P[i][e] += x ? to[0] : 0.0f;
-                        S[i][e] += x ? to[a.D] : 0.0f;
-                        to[0] = P[i][e];
-                        to[a.D] = S[i][e];
+                    for (int e = 0; e < 4; ++e) {
+                        f2 *to = reinterpret_cast<f2 *>(column_sums + 8 * c) + e, *to_s = to + a.D / 2;
+                        if (x) {
+                            const f2 one = pair2(1.0f, 1.0f);
+                            P[i][e] = fma2(*to, one, P[i][e]);
+                            S[i][e] = fma2(*to_s, one, S[i][e]);
+                        }
+                        *to = P[i][e];
+                        *to_s = S[i][e];
                     }
                 }
             }
@@ -763,14 +843,14 @@ __global__ __launch_bounds__(T, T <= 256 ? 512 / T : 1) void residual_norm_backw
     tc::pdl_launch_dependents();
     tc::pdl_wait();
     ring.fill();
-    float f[NS][8], P[NS][8], S[NS][8];
+    f2 f[NS][4], P[NS][4], S[NS][4];
     uint4 w[NS];
 #pragma unroll
     for (int i = 0; i < NS; ++i) {
         const int c = threadIdx.x + i * T;
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            P[i][e] = S[i][e] = f[i][e] = 0.0f;
+        for (int e = 0; e < 4; ++e)
+            P[i][e] = S[i][e] = f[i][e] = 0ull;
         w[i] = a.w_pre && c < chunks ? __ldg(reinterpret_cast<const uint4 *>(a.w_pre) + c) : zero;
         if (a.y && c < chunks)
             update_factor(a, c, f[i]);
@@ -791,12 +871,14 @@ __global__ __launch_bounds__(T, T <= 256 ? 512 / T : 1) void residual_norm_backw
             xv[i] = in && at_x > 0 ? ring.chunk(k, at_x, c) : zero;
             gv[i] = in && at_g > 0 ? ring.chunk(k, at_g, c) : zero;
         };
-        float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+        f2 s2[6] = {0ull, 0ull, 0ull, 0ull, 0ull, 0ull};
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
             read(i);
-            grad_sums(hv[i], yv[i], xv[i], gv[i], w[i], f[i], s);
+            grad_sums(hv[i], yv[i], xv[i], gv[i], w[i], f[i], s2);
         }
+        float s[8];
+        fold_sums(s2, s);
         const float total = block_sum8(s, red[flip]);
         flip ^= 1;
         float t[6];
@@ -833,11 +915,11 @@ __global__ __launch_bounds__(T, T <= 256 ? 512 / T : 1) void residual_norm_backw
 
 // Rows of more than 8192 columns: straight from global memory, the columns' sums in
 // shared memory.
-constexpr int kWideThreads = 1024, kWideChunks = 2;   // a thread's chunks of 8 columns
+constexpr int kWideThreads = 512, kWideChunks = 4;   // a thread's chunks of 8 columns
 
 __global__ __launch_bounds__(kWideThreads) void residual_norm_backward_wide_kernel(NormGradArgs g)
 {
-    extern __shared__ __align__(16) float column_sums[];   // [P, S][8][chunks]
+    extern __shared__ __align__(16) f2 column_pairs[];   // [P, S][4][chunks] pairs
     __shared__ float red[2][8 * 32];
     const NormArgs &a = g.f;
     tc::pdl_launch_dependents();
@@ -845,14 +927,15 @@ __global__ __launch_bounds__(kWideThreads) void residual_norm_backward_wide_kern
     const int T = blockDim.x, chunks = a.D / 8;
     const float inv_d = 1.0f / (float)a.D;
     const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-    for (int i = threadIdx.x; i < 16 * chunks; i += T)
-        column_sums[i] = 0.0f;
+    for (int i = threadIdx.x; i < 8 * chunks; i += T)
+        column_pairs[i] = 0ull;
     __syncthreads();
     int flip = 0;
     for (int m = blockIdx.x; m < a.M; m += gridDim.x) {
         const size_t base = (size_t)m * chunks;
+        f2 s2[6] = {0ull, 0ull, 0ull, 0ull, 0ull, 0ull}, f[4] = {0ull, 0ull, 0ull, 0ull};
         uint4 hv[kWideChunks], yv[kWideChunks], xv[kWideChunks], gv[kWideChunks];
-        float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+        auto weight = [&](int c) { return a.w_pre ? __ldg(reinterpret_cast<const uint4 *>(a.w_pre) + c) : zero; };
 #pragma unroll
         for (int i = 0; i < kWideChunks; ++i) {
             const int c = threadIdx.x + i * T;
@@ -862,16 +945,29 @@ __global__ __launch_bounds__(kWideThreads) void residual_norm_backward_wide_kern
             xv[i] = in && g.dx ? ldg_stream_v4(reinterpret_cast<const uint4 *>(g.dx) + base + c) : zero;
             gv[i] = in && g.dh ? reinterpret_cast<const uint4 *>(g.dh)[base + c] : zero;   // dh_in may be dh
         }
-        float f[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+        // the next row comes as far as L2 meanwhile, a line for every eighth thread
+        if ((threadIdx.x & 7) == 0 && m + (int)gridDim.x < a.M) {
+            const __nv_bfloat16 *rows[4] = {a.h, a.y, g.dx, g.dh};
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+                if (rows[y])
+#pragma unroll
+                    for (int i = 0; i < kWideChunks; ++i)
+                        if (threadIdx.x + i * T < chunks)
+                            asm volatile("prefetch.global.L2 [%0];" ::"l"(reinterpret_cast<const uint4 *>(rows[y]) + base +
+                                                                          (size_t)gridDim.x * chunks + threadIdx.x + i * T));
+        }
 #pragma unroll
         for (int i = 0; i < kWideChunks; ++i) {
             const int c = threadIdx.x + i * T;
             if (c < chunks) {
                 if (a.y)
                     update_factor(a, c, f);
-                grad_sums(hv[i], yv[i], xv[i], gv[i], a.w_pre ? __ldg(reinterpret_cast<const uint4 *>(a.w_pre) + c) : zero, f, s);
+                grad_sums(hv[i], yv[i], xv[i], gv[i], weight(c), f, s2);
             }
         }
+        float s[8];
+        fold_sums(s2, s);
         const float total = block_sum8(s, red[flip]);
         flip ^= 1;
         float t[6];
@@ -885,19 +981,18 @@ __global__ __launch_bounds__(kWideThreads) void residual_norm_backward_wide_kern
             if (c < chunks) {
                 if (a.y)
                     update_factor(a, c, f);
-                float P[8], S[8];
+                f2 P[4], S[4];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    P[e] = column_sums[e * chunks + c];
-                    S[e] = column_sums[(8 + e) * chunks + c];
+                for (int e = 0; e < 4; ++e) {
+                    P[e] = column_pairs[e * chunks + c];
+                    S[e] = column_pairs[(4 + e) * chunks + c];
                 }
                 uint4 dh, dy;
-                grad_chunk(hv[i], yv[i], xv[i], gv[i], a.w_pre ? __ldg(reinterpret_cast<const uint4 *>(a.w_pre) + c) : zero, f, q, P,
-                           S, dh, dy);
+                grad_chunk(hv[i], yv[i], xv[i], gv[i], weight(c), f, q, P, S, dh, dy);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    column_sums[e * chunks + c] = P[e];
-                    column_sums[(8 + e) * chunks + c] = S[e];
+                for (int e = 0; e < 4; ++e) {
+                    column_pairs[e * chunks + c] = P[e];
+                    column_pairs[(4 + e) * chunks + c] = S[e];
                 }
                 reinterpret_cast<uint4 *>(g.dh_in)[base + c] = dh;
                 if (a.y)
@@ -908,11 +1003,11 @@ __global__ __launch_bounds__(kWideThreads) void residual_norm_backward_wide_kern
     float *row = g.part + (size_t)blockIdx.x * (2 * a.D + 4);
     float dot[1] = {0.0f};
     for (int c = threadIdx.x; c < chunks; c += T) {
-        float P[8], S[8];
+        f2 P[4], S[4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            P[e] = column_sums[e * chunks + c];
-            S[e] = column_sums[(8 + e) * chunks + c];
+        for (int e = 0; e < 4; ++e) {
+            P[e] = column_pairs[e * chunks + c];
+            S[e] = column_pairs[(4 + e) * chunks + c];
         }
         dot[0] += put_partials(a, row, c, P, S);
     }
