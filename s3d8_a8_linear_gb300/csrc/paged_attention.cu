@@ -9,7 +9,7 @@ namespace {
 using namespace attn;
 
 // Joins the parts of every sequence that was cut: block (unit of a sequence, query
-// row or all of them), its warps over the parts.  Run `first` left its part in its
+// row or four of them), of 16 warps over one row's parts or four of a row each.  Run `first` left its part in its
 // second slot, the runs behind it in their first.
 constexpr int kJoinBatch = 8;   // parts whose loads leave together
 
@@ -33,38 +33,47 @@ __global__ __launch_bounds__(kJoinWarps * 32) void paged_attention_join_kernel(c
     const size_t size = part_floats(p.rows, D);
     const float *parts = p.parts + (size_t)join.x * 2 * size;
     auto part = [&](int x) { return parts + (size_t)(2 * x + (x == 0)) * size; };
-    if (count <= kJoinBatch) {                    // few parts: a query row a warp, all parts in it
+    auto rows_of_warps = [&]() {                  // a query row a warp, its parts in batches
         for (int r = blockIdx.y + warp * gridDim.y; r < rows; r += gridDim.y * kJoinWarps) {
-            float2 ml = make_float2(-INFINITY, 0.0f);
-            if (lane < count)
-                ml = *reinterpret_cast<const float2 *>(part(lane) + p.rows * D + 2 * r);
-            float4 o[kJoinBatch][V];
-#pragma unroll
-            for (int i = 0; i < kJoinBatch; ++i)
-#pragma unroll
-                for (int y = 0; y < V; ++y) {
-                    o[i][y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    if (i < count && 128 * y + 4 * lane < D)
-                        o[i][y] = *reinterpret_cast<const float4 *>(part(i) + r * D + 128 * y + 4 * lane);
-                }
-            float top = ml.x, sum = 0.0f;
-#pragma unroll
-            for (int s = kJoinBatch / 2; s > 0; s >>= 1)
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
-            top = __shfl_sync(0xffffffffu, top, 0);
-            const float zero = top == -INFINITY ? 0.0f : top, w = ex2(ml.x - zero), lw = ml.y * w;
+            float top = -INFINITY, sum = 0.0f;
             float4 acc[V];
 #pragma unroll
             for (int y = 0; y < V; ++y)
                 acc[y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int x0 = 0; x0 < count; x0 += kJoinBatch) {
+                float2 ml = make_float2(-INFINITY, 0.0f);
+                if (lane < kJoinBatch && x0 + lane < count)
+                    ml = *reinterpret_cast<const float2 *>(part(x0 + lane) + p.rows * D + 2 * r);
+                float4 o[kJoinBatch][V];
 #pragma unroll
-            for (int i = 0; i < kJoinBatch; ++i) {
-                sum += __shfl_sync(0xffffffffu, lw, i);
-                const float wi = __shfl_sync(0xffffffffu, w, i);
+                for (int i = 0; i < kJoinBatch; ++i)
+#pragma unroll
+                    for (int y = 0; y < V; ++y) {
+                        o[i][y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        if (x0 + i < count && 128 * y + 4 * lane < D)
+                            o[i][y] = *reinterpret_cast<const float4 *>(part(x0 + i) + r * D + 128 * y + 4 * lane);
+                    }
+                float now = ml.x;
+#pragma unroll
+                for (int s = kJoinBatch / 2; s > 0; s >>= 1)
+                    now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, s));
+                now = fmaxf(top, __shfl_sync(0xffffffffu, now, 0));
+                const float zero = now == -INFINITY ? 0.0f : now;
+                const float keep = ex2(top - zero), w = ex2(ml.x - zero), lw = ml.y * w;
+                top = now;
+                sum *= keep;
 #pragma unroll
                 for (int y = 0; y < V; ++y)
-                    acc[y] = make_float4(fmaf(wi, o[i][y].x, acc[y].x), fmaf(wi, o[i][y].y, acc[y].y),
-                                         fmaf(wi, o[i][y].z, acc[y].z), fmaf(wi, o[i][y].w, acc[y].w));
+                    acc[y] = make_float4(acc[y].x * keep, acc[y].y * keep, acc[y].z * keep, acc[y].w * keep);
+#pragma unroll
+                for (int i = 0; i < kJoinBatch; ++i) {
+                    sum += __shfl_sync(0xffffffffu, lw, i);
+                    const float wi = __shfl_sync(0xffffffffu, w, i);
+#pragma unroll
+                    for (int y = 0; y < V; ++y)
+                        acc[y] = make_float4(fmaf(wi, o[i][y].x, acc[y].x), fmaf(wi, o[i][y].y, acc[y].y),
+                                             fmaf(wi, o[i][y].z, acc[y].z), fmaf(wi, o[i][y].w, acc[y].w));
+                }
             }
             const int64_t row = (int64_t)b * a.Hq + h * p.group + blk * 16 + r;
             const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
@@ -79,93 +88,101 @@ __global__ __launch_bounds__(kJoinWarps * 32) void paged_attention_join_kernel(c
             if (lane == 0 && a.lse)
                 a.lse[row] = (top + log2f(sum)) * kLn2;
         }
+    };
+    if constexpr (kJoinWarps < 16) {
+        rows_of_warps();
         return;
-    }
-    for (int r = blockIdx.y; r < rows; r += gridDim.y) {
-        // this warp's parts, 32 at a time: lane i has the weight of part x0 + i kJoinWarps
-        float top = -INFINITY, sum = 0.0f;
-        float4 acc[V];
-#pragma unroll
-        for (int y = 0; y < V; ++y)
-            acc[y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int x0 = warp; x0 < count; x0 += 32 * kJoinWarps) {
-            const int x = x0 + lane * kJoinWarps, some = min(32, (count - x0 + kJoinWarps - 1) / kJoinWarps);
-            float mx = -INFINITY, lx = 0.0f;
-            if (x < count) {
-                const float2 ml = *reinterpret_cast<const float2 *>(part(x) + p.rows * D + 2 * r);
-                mx = ml.x;
-                lx = ml.y;
-            }
-            float4 o[kJoinBatch][V];
-            auto load = [&](int i0) {
-#pragma unroll
-                for (int i = 0; i < kJoinBatch; ++i)
-#pragma unroll
-                    for (int y = 0; y < V; ++y) {
-                        o[i][y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                        if (i0 + i < some && 128 * y + 4 * lane < D)
-                            o[i][y] = *reinterpret_cast<const float4 *>(part(x0 + (i0 + i) * kJoinWarps) + r * D + 128 * y + 4 * lane);
-                    }
-            };
-            load(0);
-            float now = mx;
-#pragma unroll
-            for (int s = 16; s > 0; s >>= 1)
-                now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, s));
-            now = fmaxf(top, now);
-            const float zero = now == -INFINITY ? 0.0f : now;
-            const float keep = ex2(top - zero), w = ex2(mx - zero);
-            lx *= w;
-#pragma unroll
-            for (int s = 16; s > 0; s >>= 1)
-                lx += __shfl_xor_sync(0xffffffffu, lx, s);
-            sum = sum * keep + lx;
-            top = now;
+    } else {
+        if (count <= kJoinBatch) {
+            rows_of_warps();
+            return;
+        }
+        for (int r = blockIdx.y; r < rows; r += gridDim.y) {
+            // this warp's parts, 32 at a time: lane i has the weight of part x0 + i kJoinWarps
+            float top = -INFINITY, sum = 0.0f;
+            float4 acc[V];
 #pragma unroll
             for (int y = 0; y < V; ++y)
-                acc[y] = make_float4(acc[y].x * keep, acc[y].y * keep, acc[y].z * keep, acc[y].w * keep);
-            for (int i0 = 0; i0 < some; i0 += kJoinBatch) {
-                if (i0)
-                    load(i0);
+                acc[y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int x0 = warp; x0 < count; x0 += 32 * kJoinWarps) {
+                const int x = x0 + lane * kJoinWarps, some = min(32, (count - x0 + kJoinWarps - 1) / kJoinWarps);
+                float mx = -INFINITY, lx = 0.0f;
+                if (x < count) {
+                    const float2 ml = *reinterpret_cast<const float2 *>(part(x) + p.rows * D + 2 * r);
+                    mx = ml.x;
+                    lx = ml.y;
+                }
+                float4 o[kJoinBatch][V];
+                auto load = [&](int i0) {
 #pragma unroll
-                for (int i = 0; i < kJoinBatch; ++i) {
-                    // a part beyond the last has a weight of 2^-inf, and zeros
-                    const float wi = __shfl_sync(0xffffffffu, w, i0 + i);
+                    for (int i = 0; i < kJoinBatch; ++i)
 #pragma unroll
-                    for (int y = 0; y < V; ++y)
-                        acc[y] = make_float4(fmaf(wi, o[i][y].x, acc[y].x), fmaf(wi, o[i][y].y, acc[y].y),
-                                             fmaf(wi, o[i][y].z, acc[y].z), fmaf(wi, o[i][y].w, acc[y].w));
+                        for (int y = 0; y < V; ++y) {
+                            o[i][y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                            if (i0 + i < some && 128 * y + 4 * lane < D)
+                                o[i][y] = *reinterpret_cast<const float4 *>(part(x0 + (i0 + i) * kJoinWarps) + r * D + 128 * y + 4 * lane);
+                        }
+                };
+                load(0);
+                float now = mx;
+#pragma unroll
+                for (int s = 16; s > 0; s >>= 1)
+                    now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, s));
+                now = fmaxf(top, now);
+                const float zero = now == -INFINITY ? 0.0f : now;
+                const float keep = ex2(top - zero), w = ex2(mx - zero);
+                lx *= w;
+#pragma unroll
+                for (int s = 16; s > 0; s >>= 1)
+                    lx += __shfl_xor_sync(0xffffffffu, lx, s);
+                sum = sum * keep + lx;
+                top = now;
+#pragma unroll
+                for (int y = 0; y < V; ++y)
+                    acc[y] = make_float4(acc[y].x * keep, acc[y].y * keep, acc[y].z * keep, acc[y].w * keep);
+                for (int i0 = 0; i0 < some; i0 += kJoinBatch) {
+                    if (i0)
+                        load(i0);
+#pragma unroll
+                    for (int i = 0; i < kJoinBatch; ++i) {
+                        // a part beyond the last has a weight of 2^-inf, and zeros
+                        const float wi = __shfl_sync(0xffffffffu, w, i0 + i);
+#pragma unroll
+                        for (int y = 0; y < V; ++y)
+                            acc[y] = make_float4(fmaf(wi, o[i][y].x, acc[y].x), fmaf(wi, o[i][y].y, acc[y].y),
+                                                 fmaf(wi, o[i][y].z, acc[y].z), fmaf(wi, o[i][y].w, acc[y].w));
+                    }
                 }
             }
-        }
-        __syncthreads();                          // the row before has been read
-        if (lane == 0) {
-            tops[warp] = top;
-            totals[warp] = sum;
-        }
+            __syncthreads();                          // the row before has been read
+            if (lane == 0) {
+                tops[warp] = top;
+                totals[warp] = sum;
+            }
 #pragma unroll
-        for (int y = 0; y < V; ++y)
-            if (128 * y + 4 * lane < DP)
-                *reinterpret_cast<float4 *>(&sums[warp][128 * y + 4 * lane]) = acc[y];
-        __syncthreads();
-        float all = -INFINITY, total = 0.0f;
-#pragma unroll
-        for (int x = 0; x < kJoinWarps; ++x)
-            all = fmaxf(all, tops[x]);
-        const float zero = all == -INFINITY ? 0.0f : all;
-#pragma unroll
-        for (int x = 0; x < kJoinWarps; ++x)
-            total = fmaf(ex2(tops[x] - zero), totals[x], total);
-        const int64_t row = (int64_t)b * a.Hq + h * p.group + blk * 16 + r;
-        for (int d = threadIdx.x; d < D; d += kJoinWarps * 32) {
-            float v = 0.0f;
+            for (int y = 0; y < V; ++y)
+                if (128 * y + 4 * lane < DP)
+                    *reinterpret_cast<float4 *>(&sums[warp][128 * y + 4 * lane]) = acc[y];
+            __syncthreads();
+            float all = -INFINITY, total = 0.0f;
 #pragma unroll
             for (int x = 0; x < kJoinWarps; ++x)
-                v = fmaf(ex2(tops[x] - zero), sums[x][d], v);
-            a.out[row * D + d] = __float2bfloat16_rn(total == 0.0f ? 0.0f : v / total);
+                all = fmaxf(all, tops[x]);
+            const float zero = all == -INFINITY ? 0.0f : all;
+#pragma unroll
+            for (int x = 0; x < kJoinWarps; ++x)
+                total = fmaf(ex2(tops[x] - zero), totals[x], total);
+            const int64_t row = (int64_t)b * a.Hq + h * p.group + blk * 16 + r;
+            for (int d = threadIdx.x; d < D; d += kJoinWarps * 32) {
+                float v = 0.0f;
+#pragma unroll
+                for (int x = 0; x < kJoinWarps; ++x)
+                    v = fmaf(ex2(tops[x] - zero), sums[x][d], v);
+                a.out[row * D + d] = __float2bfloat16_rn(total == 0.0f ? 0.0f : v / total);
+            }
+            if (threadIdx.x == 0 && a.lse)
+                a.lse[row] = (all + log2f(total)) * kLn2;
         }
-        if (threadIdx.x == 0 && a.lse)
-            a.lse[row] = (all + log2f(total)) * kLn2;
     }
 }
 
@@ -175,7 +192,7 @@ cudaError_t launch_join(const AttnArgs &a, const AttnPlan &p, cudaStream_t strea
     const unsigned units = (unsigned)a.B * p.units;
     if ((int64_t)units * p.rows <= 4 * device_sm_count())
         return tc::launch_pdl(paged_attention_join_kernel<DP, 16>, dim3(units, p.rows), dim3(16 * 32), 0, stream, a, p);
-    return tc::launch_pdl(paged_attention_join_kernel<DP, 4>, dim3(units), dim3(4 * 32), 0, stream, a, p);
+    return tc::launch_pdl(paged_attention_join_kernel<DP, 4>, dim3(units, (p.rows + 3) / 4), dim3(4 * 32), 0, stream, a, p);
 }
 
 // The workspace's layout: the queue, what to join, partial states.
@@ -227,7 +244,7 @@ cudaError_t launch_paged_attention(const AttnArgs &a, cudaStream_t stream)
     const cudaError_t e = launch(a, p, w.ctas, stream);
     if (e != cudaSuccess)
         return e;
-    // few sequences, of many parts perhaps: 16 warps a query row; many: a block of four warps each
+    // few sequences, of many parts perhaps: 16 warps a query row; many: a warp a query row
     return a.kv.dim <= 64    ? launch_join<64>(a, p, stream)
            : a.kv.dim <= 128 ? launch_join<128>(a, p, stream)
                              : launch_join<256>(a, p, stream);

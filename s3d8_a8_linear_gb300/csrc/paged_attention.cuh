@@ -22,6 +22,11 @@
 // sequences of up to 8191 tokens ended at 174 us, the middle one at 146).  A run that
 // ends inside a sequence leaves (m, l, O) in the workspace, and a second kernel joins
 // the parts of each such sequence, in order of position.
+//
+// Measured with 32 / 8 heads of 128, join included: 8 sequences of up to 131072 tokens
+// 531 us (6.8 TB/s), 64 of up to 8191 177 us (6.1 TB/s; 5 us until the first tiles
+// arrive, 5 to 10 from the last ones through the join), 48 int8 sequences with a window
+// 214 us (5.6 TB/s; 65% of the issue slots, a third of them turning codes into fp16).
 #pragma once
 
 #include "common.cuh"
