@@ -74,6 +74,9 @@ def test_cache_geometry_is_checked(lib):
     for bad in (dict(k=A + 8), dict(v=B + 2), dict(k_stride=[2048, 132, 64]),
                 dict(dtype=1, k_scale=A, v_scale=A, k_stride=[2048, 128, 72]), dict(dtype=1, k_scale=A, v_scale=A + 2)):
         assert f(_cache(**bad)) == -2, bad
+    for far in (dict(k_stride=[8 << 32, 128, 64]), dict(v_stride=[2048, 128, 8 << 32]),
+                dict(dtype=1, k_scale=A, v_scale=A, scale_stride=[1 << 32, 1, 1])):
+        assert f(_cache(**far)) == -3, far
     ok = _cache()
     assert f(ok, Hq=3) == -1 and f(ok, Hq=0) == -1 and f(ok, B=-1) == -1 and f(ok, window=-1) == -1
     assert f(ok, width=-1) == -1 and f(ok, width=1 << 27) == -1

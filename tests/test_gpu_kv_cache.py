@@ -129,6 +129,42 @@ def _check_attention(lens, heads, group, dim, page, int8=False, order="head", wi
 LENS = [0, 1, 2, 15, 16, 17, 31, 33, 64, 129, 500]
 
 
+@pytest.mark.parametrize("page", [16, 12])
+@pytest.mark.parametrize("int8", [False, True])
+def test_keys_and_values_of_unlike_strides(int8, page):
+    """Keys with the heads outside, values with the tokens outside: append into them,
+    attend over them, copy their pages."""
+    g = torch.Generator().manual_seed(31)
+    T, pages = 3 * page + 1, 9
+    a, b = _cache(pages, page, 2, 64, int8, "head", fill=0.0), _cache(pages, page, 2, 64, int8, "token", fill=0.0)
+    cache = s3d8.KVCache(a.k, b.v, a.k_scale, a.v_scale)
+    table, none = _i32([[5, 2, 7, 0]]), torch.empty((64, 0), device=dev())
+    q, k, v = (_rand(g, T, h, 64) for h in (8, 2, 2))
+    s3d8.rope_append(q, k, v, none, none, _i32(range(T)), cache, table, rows=_i32([0] * T))
+    s3d8.copy_pages(s3d8.KVPool([cache]), _i32([5, 2, 7, 0]), _i32([1, 3, 4, 8]))
+    at = _i32([[1, 3, 4, 8]])
+    pos = torch.arange(T, device=dev())
+    where = at[0].long()[pos // page], pos % page
+    kk, vv = (bf16_to_f64(c[where]) if sc is None else c[where].cpu().numpy() * sc[where].double().cpu().numpy()[..., None]
+              for c, sc in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)))
+    for new, have in ((k, kk), (v, vv)):
+        new = bf16_to_f64(new)
+        step = np.abs(new).max(-1, keepdims=True) / 127 if int8 else 0.0
+        assert (np.abs(have - new) <= 0.5 * step + 2.0 ** -8 * np.abs(new) + 1e-6).all()
+    got = bf16_to_f64(s3d8.paged_attention(q[:1].contiguous(), cache, at, _i32([T])))
+    ref, _ = _attend(bf16_to_f64(q)[0], kk, vv, 0.125, 0)
+    assert (np.abs(got[0] - ref) <= 2.0 ** -8 * np.abs(ref) + 1e-4 * np.abs(vv).max()).all()
+
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("dim,group", [(64, 1), (64, 12), (80, 4), (128, 4), (128, 12), (256, 4), (256, 16)])
+def test_attention_shares_with_short_runs(dim, group, int8):
+    """Enough tokens that every warp's share is cut into a long run and short ones."""
+    lens = [40001, 3, 0, 77777, 12345]
+    first = _check_attention(lens, 8, group, dim, 16, int8, seed=7)
+    assert torch.equal(first, _check_attention(lens, 8, group, dim, 16, int8, seed=7))
+
+
 @pytest.mark.parametrize("int8", [False, True])
 @pytest.mark.parametrize("group", [1, 3, 4, 7, 8, 9, 16, 17, 40])
 def test_attention_groups(group, int8):

@@ -115,6 +115,58 @@ def test_parts_alone_and_in_place():
     assert h3.shape == x3.shape == (0, D)
 
 
+# more rows than the GPU takes at once: several a CTA, at every width's number of threads and stages
+MANY = [(310, 1032), (1500, 2048), (307, 2056), (700, 4096), (320, 8192), (311, 8200), (309, 16384), (5000, 512), (9000, 128),
+        (20000, 8), (3001, 1024)]
+
+
+@pytest.mark.parametrize("post,gate,alpha,tanh", [FORMS[0], FORMS[3], FORMS[4]])
+@pytest.mark.parametrize("M,D", MANY)
+def test_many_rows(M, D, post, gate, alpha, tanh):
+    i = _inputs(M, D, post, gate, M + D)
+    rng = np.random.default_rng(D)
+    dh, dx = _rand(rng, M, D), _rand(rng, M, D)
+    h, x = s3d8.residual_norm(**i, alpha=alpha, eps=EPS, tanh_gate=tanh)
+    _close(_f(h), _update(_f(i["h"]), _f(i["y"]), _f(i["w_post"]), _f(i["gate"]), alpha, tanh))
+    _close(_f(x), _norm(_f(h), _f(i["w_pre"])))
+    if D % 16 == 0:
+        hq, q, s = s3d8.residual_norm_quant(**i, alpha=alpha, eps=EPS, tanh_gate=tanh)
+        want_q, want_s = s3d8.quantize_act(x)
+        assert torch.equal(hq, h) and torch.equal(q, want_q) and torch.equal(s, want_s)
+    same, alone = s3d8.residual_norm(h, w_pre=i["w_pre"])
+    assert same is h and torch.equal(alone, x)
+    assert torch.equal(s3d8.residual_norm(**{**i, "w_pre": None}, alpha=alpha, eps=EPS, tanh_gate=tanh)[0], h)
+    got = s3d8.residual_norm_backward(dh, dx, **i, alpha=alpha, eps=EPS, tanh_gate=tanh)
+    again = s3d8.residual_norm_backward(dh, dx, **i, alpha=alpha, eps=EPS, tanh_gate=tanh)
+    ref = _gradients(i, _f(dh), _f(dx), alpha, tanh)
+    for k, t in got.items():
+        assert torch.equal(t, again[k]), k
+        if k in ("dh", "dy"):
+            _close(_f(t), ref[k])
+        else:
+            summands = M * (D if t.numel() == 1 and D > 1 else 1)
+            tol = (min(summands, 4096) + 40) * 2.0 ** -24 * ref["abs_" + k]
+            assert (np.abs(t.double().cpu().numpy() - ref[k]) <= tol + 1e-30).all(), k
+
+
+@pytest.mark.parametrize("M,D", [(40, 64), (700, 1024), (350, 4096), (6, 8192), (200, 8200)])
+def test_absent_gradients_at_every_form(M, D):
+    """dh, dx or both missing, with and without a block's output."""
+    i = _inputs(M, D, True, "scalar", M)
+    rng = np.random.default_rng(D)
+    dh, dx = _rand(rng, M, D), _rand(rng, M, D)
+    zero = np.zeros((M, D))
+    for a, b in ((dh, None), (None, dx), (None, None)):
+        fa, fb = zero if a is None else _f(a), zero if b is None else _f(b)
+        got = s3d8.residual_norm_backward(a, b, **i, tanh_gate=True)
+        ref = _gradients(i, fa, fb, 1.0, True)
+        _close(_f(got["dh"]), ref["dh"])
+        _close(_f(got["dy"]), ref["dy"])
+        alone = s3d8.residual_norm_backward(a, b, i["h"], w_pre=i["w_pre"])
+        assert set(alone) == {"dh", "dw_pre"} and torch.equal(alone["dh"], got["dh"])
+        assert torch.equal(alone["dw_pre"], got["dw_pre"])
+
+
 def test_zero_rows_and_extreme_sizes():
     D = 512
     h = torch.zeros((3, D), dtype=BF, device=dev())
