@@ -11,9 +11,8 @@ using namespace attn;
 // Joins the parts of every sequence that was cut: block (unit of a sequence, query
 // row or four of them), of 16 warps over one row's parts or four of a row each.  Run `first` left its part in its
 // second slot, the runs behind it in their first.
-constexpr int kJoinBatch = 8;   // parts whose loads leave together
-
-template <int DP, int kJoinWarps>
+// BATCH: parts whose loads leave together.
+template <int DP, int kJoinWarps, int BATCH>
 __global__ __launch_bounds__(kJoinWarps * 32) void paged_attention_join_kernel(const __grid_constant__ AttnArgs a,
                                                                              const __grid_constant__ AttnPlan p)
 {
@@ -40,13 +39,13 @@ __global__ __launch_bounds__(kJoinWarps * 32) void paged_attention_join_kernel(c
 #pragma unroll
             for (int y = 0; y < V; ++y)
                 acc[y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            for (int x0 = 0; x0 < count; x0 += kJoinBatch) {
+            for (int x0 = 0; x0 < count; x0 += BATCH) {
                 float2 ml = make_float2(-INFINITY, 0.0f);
-                if (lane < kJoinBatch && x0 + lane < count)
+                if (lane < BATCH && x0 + lane < count)
                     ml = *reinterpret_cast<const float2 *>(part(x0 + lane) + p.rows * D + 2 * r);
-                float4 o[kJoinBatch][V];
+                float4 o[BATCH][V];
 #pragma unroll
-                for (int i = 0; i < kJoinBatch; ++i)
+                for (int i = 0; i < BATCH; ++i)
 #pragma unroll
                     for (int y = 0; y < V; ++y) {
                         o[i][y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -55,7 +54,7 @@ __global__ __launch_bounds__(kJoinWarps * 32) void paged_attention_join_kernel(c
                     }
                 float now = ml.x;
 #pragma unroll
-                for (int s = kJoinBatch / 2; s > 0; s >>= 1)
+                for (int s = BATCH / 2; s > 0; s >>= 1)
                     now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, s));
                 now = fmaxf(top, __shfl_sync(0xffffffffu, now, 0));
                 const float zero = now == -INFINITY ? 0.0f : now;
@@ -66,7 +65,7 @@ __global__ __launch_bounds__(kJoinWarps * 32) void paged_attention_join_kernel(c
                 for (int y = 0; y < V; ++y)
                     acc[y] = make_float4(acc[y].x * keep, acc[y].y * keep, acc[y].z * keep, acc[y].w * keep);
 #pragma unroll
-                for (int i = 0; i < kJoinBatch; ++i) {
+                for (int i = 0; i < BATCH; ++i) {
                     sum += __shfl_sync(0xffffffffu, lw, i);
                     const float wi = __shfl_sync(0xffffffffu, w, i);
 #pragma unroll
@@ -93,7 +92,7 @@ __global__ __launch_bounds__(kJoinWarps * 32) void paged_attention_join_kernel(c
         rows_of_warps();
         return;
     } else {
-        if (count <= kJoinBatch) {
+        if (count <= BATCH) {
             rows_of_warps();
             return;
         }
@@ -112,10 +111,10 @@ __global__ __launch_bounds__(kJoinWarps * 32) void paged_attention_join_kernel(c
                     mx = ml.x;
                     lx = ml.y;
                 }
-                float4 o[kJoinBatch][V];
+                float4 o[BATCH][V];
                 auto load = [&](int i0) {
 #pragma unroll
-                    for (int i = 0; i < kJoinBatch; ++i)
+                    for (int i = 0; i < BATCH; ++i)
 #pragma unroll
                         for (int y = 0; y < V; ++y) {
                             o[i][y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -140,11 +139,11 @@ __global__ __launch_bounds__(kJoinWarps * 32) void paged_attention_join_kernel(c
 #pragma unroll
                 for (int y = 0; y < V; ++y)
                     acc[y] = make_float4(acc[y].x * keep, acc[y].y * keep, acc[y].z * keep, acc[y].w * keep);
-                for (int i0 = 0; i0 < some; i0 += kJoinBatch) {
+                for (int i0 = 0; i0 < some; i0 += BATCH) {
                     if (i0)
                         load(i0);
 #pragma unroll
-                    for (int i = 0; i < kJoinBatch; ++i) {
+                    for (int i = 0; i < BATCH; ++i) {
                         // a part beyond the last has a weight of 2^-inf, and zeros
                         const float wi = __shfl_sync(0xffffffffu, w, i0 + i);
 #pragma unroll
@@ -189,10 +188,16 @@ __global__ __launch_bounds__(kJoinWarps * 32) void paged_attention_join_kernel(c
 template <int DP>
 cudaError_t launch_join(const AttnArgs &a, const AttnPlan &p, cudaStream_t stream)
 {
-    const unsigned units = (unsigned)a.B * p.units;
-    if ((int64_t)units * p.rows <= 4 * device_sm_count())
-        return tc::launch_pdl(paged_attention_join_kernel<DP, 16>, dim3(units, p.rows), dim3(16 * 32), 0, stream, a, p);
-    return tc::launch_pdl(paged_attention_join_kernel<DP, 4>, dim3(units, (p.rows + 3) / 4), dim3(4 * 32), 0, stream, a, p);
+    // Up to two SMs a unit: a dozen parts or many more each, so 16 warps a query row, and all of their loads at once where
+    // there is an SM for every row (one sequence of 60000 tokens 56 -> 53 us).  Many units: few parts, a warp a query row.
+    const unsigned units = (unsigned)a.B * p.units, sms = device_sm_count();
+    if (units > 2 * sms)
+        return tc::launch_pdl(paged_attention_join_kernel<DP, 4, 8>, dim3(units, (p.rows + 3) / 4), dim3(4 * 32), 0, stream, a,
+                              p);
+    if (DP <= 128 && units * p.rows <= sms)
+        return tc::launch_pdl(paged_attention_join_kernel<DP, 16, DP <= 128 ? 16 : 8>, dim3(units, p.rows), dim3(16 * 32), 0,
+                              stream, a, p);
+    return tc::launch_pdl(paged_attention_join_kernel<DP, 16, 8>, dim3(units, p.rows), dim3(16 * 32), 0, stream, a, p);
 }
 
 // The workspace's layout: the queue, what to join, partial states.
@@ -244,7 +249,6 @@ cudaError_t launch_paged_attention(const AttnArgs &a, cudaStream_t stream)
     const cudaError_t e = launch(a, p, w.ctas, stream);
     if (e != cudaSuccess)
         return e;
-    // few sequences, of many parts perhaps: 16 warps a query row; many: a warp a query row
     return a.kv.dim <= 64    ? launch_join<64>(a, p, stream)
            : a.kv.dim <= 128 ? launch_join<128>(a, p, stream)
                              : launch_join<256>(a, p, stream);
