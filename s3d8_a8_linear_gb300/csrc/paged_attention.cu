@@ -188,10 +188,13 @@ __global__ __launch_bounds__(kJoinWarps * 32) void paged_attention_join_kernel(c
 template <int DP>
 cudaError_t launch_join(const AttnArgs &a, const AttnPlan &p, cudaStream_t stream)
 {
-    // Up to two SMs a unit: a dozen parts or many more each, so 16 warps a query row, and all of their loads at once where
-    // there is an SM for every row (one sequence of 60000 tokens 56 -> 53 us).  Many units: few parts, a warp a query row.
+    // Few units of sequences that can be long: dozens of parts each, so 16 warps a query row, and all of their loads at once
+    // where there is an SM for every row (one sequence of 60000 tokens 56 -> 53 us; 32 of up to 16000 186 -> 180).  Many
+    // units, or short sequences: few parts, a warp a query row (32 of up to 100 tokens 12.6 -> 10.4 us).
     const unsigned units = (unsigned)a.B * p.units, sms = device_sm_count();
-    if (units > 2 * sms)
+    int64_t longest = a.width * a.kv.page_size;
+    longest = a.window > 0 && a.window < longest ? a.window : longest;
+    if ((int64_t)units * p.rows > 4 * sms && (units > 2 * sms || longest <= 32 * kTile))
         return tc::launch_pdl(paged_attention_join_kernel<DP, 4, 8>, dim3(units, (p.rows + 3) / 4), dim3(4 * 32), 0, stream, a,
                               p);
     if (DP <= 128 && units * p.rows <= sms)

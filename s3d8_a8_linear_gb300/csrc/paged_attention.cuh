@@ -5,8 +5,8 @@
 //
 // Bound by HBM: every visible key and value is read once, for up to 16 query rows
 // at a time.  The unit of work is a tile of 16 tokens of one (sequence, key/value
-// head); the list of all tiles is cut into contiguous runs, whatever the lengths
-// are.  A warp streams its runs through a ring of its own in shared memory
+// head); the list of all tiles (a sequence's beginning counting as one more) is cut
+// into contiguous runs, whatever the lengths are.  A warp streams its runs through a ring of its own in shared memory
 // (cp.async, no barrier with other warps) and carries the softmax's running maximum
 // m, sum l and the output sums O in fp32:
 //   S = K Q^T (tensor cores, rows = tokens, columns = 8 or 16 query rows),
@@ -56,6 +56,10 @@ struct Shape {
 
 struct Seq {
     int len, first, tiles;   // visible tokens first..len-1; tiles of 16 from the one that holds `first`
+
+    // Places in the list: with a weight of 1 a sequence's beginning counts as one more (its query rows, its output), so that a
+    // warp of many short sequences gets fewer tiles (64 of up to 1000 tokens 39 -> 35 us).
+    __device__ __forceinline__ int places(int weight) const { return tiles ? tiles + weight : 0; }
 };
 
 __device__ __forceinline__ Seq sequence(const AttnArgs &a, int b)
@@ -68,15 +72,15 @@ __device__ __forceinline__ Seq sequence(const AttnArgs &a, int b)
     return s;
 }
 
-// A position in the list of tiles: tile k of key/value head h, block of query
-// rows blk, of sequence b.
+// A place in the list: the beginning (k = 0) or tile k (from 1) of key/value head h,
+// block of query rows blk, of sequence b.
 struct Cursor {
     int b, h, blk, k;
     Seq s;
 
     __device__ __forceinline__ void next(const AttnArgs &a, int blocks)
     {
-        if (++k < s.tiles)
+        if (++k <= s.tiles)
             return;
         k = 0;
         if (++blk < blocks)
@@ -223,17 +227,17 @@ __host__ __device__ __forceinline__ size_t part_floats(int rows, int D)
 }
 
 // ---- runs ------------------------------------------------------------------------------------
-// The list of tiles in even shares, one a warp; of each share a long run, that its
-// warp begins with, and short ones behind it, that are handed out.  Runs are numbered
-// in the order of their tiles.
+// The list in even shares, one a warp; of each share a long run, that its warp begins
+// with, and short ones behind it, that are handed out.  Runs are numbered in the
+// order of their places.
 struct Runs {
-    long long total;               // tiles of the call
-    int share, head, rest, each;   // tiles of a share, of its long run, of a short one; runs of a share
+    long long total;               // places of the call
+    int share, head, rest, each;   // places of a share, of its long run, of a short one; runs of a share
     int count;                     // shares
 
-    __device__ __forceinline__ Runs(long long tiles, int warps, bool short_runs) : total(tiles)
+    __device__ __forceinline__ Runs(long long places, int warps, bool short_runs) : total(places)
     {
-        share = (int)((tiles + warps - 1) / warps);
+        share = (int)((places + warps - 1) / warps);
         // Even shares alone where a short run's own cost (its query rows, a part to write and to join) passes what it evens
         // out (one sequence of 65536 tokens, 18 tiles a warp: 64 us, against 73 with short runs; 8 of up to 131072: 564 and
         // 550).
@@ -241,7 +245,7 @@ struct Runs {
         head = cut ? share * 3 / 4 : share;
         rest = cut ? share / 8 : 1;
         each = 1 + (share - head + rest - 1) / rest;
-        count = share ? (int)((tiles + share - 1) / share) : 0;
+        count = share ? (int)((places + share - 1) / share) : 0;
     }
     __device__ __forceinline__ long long begin(int r) const
     {
@@ -255,9 +259,9 @@ struct Runs {
         const int from = j ? min(share, head + (j - 1) * rest) : 0, to = min(share, head + j * rest);
         return (int)min((long long)(to - from), total - (long long)s * share - from);
     }
-    __device__ __forceinline__ int of(long long tile) const
+    __device__ __forceinline__ int of(long long place) const
     {
-        const int s = (int)(tile / share), at = (int)(tile - (long long)s * share);
+        const int s = (int)(place / share), at = (int)(place - (long long)s * share);
         return s * each + (at < head ? 0 : 1 + (at - head) / rest);
     }
 };
@@ -303,42 +307,55 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
     constexpr int kScanThreads = WARPS * 32;
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     __shared__ long long scan[kScanThreads + 1];
-    __shared__ long long warp_tot[WARPS];
+    __shared__ long long warp_tiles[WARPS];
+    __shared__ int warp_some[WARPS];
     __shared__ uint4 state[WARPS];                // what each warp's running state is of (as its first tile says)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int D = a.kv.dim, S = a.kv.page_size;
     tc::pdl_launch_dependents();
     tc::pdl_wait();
 
-    // ---- tiles in front of each sequence ------------------------------------------
+    // ---- places in front of each sequence ------------------------------------------
+    // A beginning counts as a place where a warp gets several; with a tile a warp at most there is nothing to weigh.
     const int per = (a.B + kScanThreads - 1) / kScanThreads;   // sequences per scanning thread
+    int weight;
     {
-        long long mine = 0;
+        long long tiles = 0;
+        int some = 0;                             // sequences with tiles
         for (int i = 0; i < per; ++i) {
             const int b = threadIdx.x * per + i;
             if (b < a.B) {
-                mine += (long long)sequence(a, b).tiles * p.units;
+                const int n = sequence(a, b).tiles;
+                tiles += n;
+                some += n > 0;
                 if (blockIdx.x == 0 && a.lens[b] > a.width * S)
                     atomicExch(a.status, kStatusBounds);
             }
         }
-        long long inc = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const long long v = __shfl_up_sync(0xffffffffu, inc, o);
-            if (lane >= o)
-                inc += v;
+            const long long t = __shfl_up_sync(0xffffffffu, tiles, o);
+            const int n = __shfl_up_sync(0xffffffffu, some, o);
+            if (lane >= o) {
+                tiles += t;
+                some += n;
+            }
         }
-        if (lane == 31)
-            warp_tot[warp] = inc;
-        scan[threadIdx.x + 1] = inc;
-    }
-    __syncthreads();
-    {
-        long long before = 0;
-        for (int w = 0; w < warp; ++w)
-            before += warp_tot[w];
-        scan[threadIdx.x + 1] += before;
+        if (lane == 31) {
+            warp_tiles[warp] = tiles;
+            warp_some[warp] = some;
+        }
+        __syncthreads();
+        long long all = 0;
+        for (int w = 0; w < WARPS; ++w) {
+            all += warp_tiles[w];
+            if (w < warp) {
+                tiles += warp_tiles[w];
+                some += warp_some[w];
+            }
+        }
+        weight = all * p.units > (long long)gridDim.x * WARPS;
+        scan[threadIdx.x + 1] = (tiles + (weight ? some : 0)) * p.units;
         if (threadIdx.x == 0)
             scan[0] = 0;
     }
@@ -351,70 +368,81 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
     if (own < runs.count) {
         const uint32_t ring = smem_addr(smem_raw) + warp * (STAGES * Sh::kStage);
         Cursor in;                            // the tile to fetch next,
-        int run = own * runs.each, left = 0;  // its run, and the tiles left of that, with it
+        int run = own * runs.each, left = 0;  // its run, and the places left of that, with it
         bool new_run = true, done = false;
-        int asked = -1;                       // lane 0: the short run that comes next
+        int asked = -1;                       // lane 0: the short run that comes next,
+        bool pending = false;                 // once it has been asked for
         auto ask = [&]() {
-            if (lane == 0 && runs.each > 1) {
+            if (lane == 0 && runs.each > 1 && !pending) {
                 const int i = grab(p.queue), s = i / (runs.each - 1);
                 asked = s < runs.count ? s * runs.each + 1 + i - s * (runs.each - 1) : -1;
             }
+            pending = true;
         };
-        auto enter = [&]() {                  // to the first tile of `run`
-            const long long tile = runs.begin(run);
+        auto enter = [&]() {                  // to the first place of `run`
+            const long long place = runs.begin(run);
             left = runs.length(run);
             new_run = true;
             // the scanning thread that holds it, then that one's sequences
             int lo = 0, hi = kScanThreads;
             while (hi - lo > 1) {
                 const int mid = (lo + hi) / 2;
-                if (scan[mid] <= tile)
+                if (scan[mid] <= place)
                     lo = mid;
                 else
                     hi = mid;
             }
-            long long ahead = tile - scan[lo];
+            long long ahead = place - scan[lo];
             in.b = lo * per;
             in.s = sequence(a, in.b);
-            while (ahead >= (long long)in.s.tiles * p.units) {
-                ahead -= (long long)in.s.tiles * p.units;
+            while (ahead >= (long long)in.s.places(weight) * p.units) {
+                ahead -= (long long)in.s.places(weight) * p.units;
                 in.s = sequence(a, ++in.b);
             }
+            const uint32_t size = in.s.places(weight);
             uint32_t u, k;
             if (ahead >> 32) {
-                u = (uint32_t)(ahead / in.s.tiles);
-                k = (uint32_t)(ahead - (long long)u * in.s.tiles);
+                u = (uint32_t)(ahead / size);
+                k = (uint32_t)(ahead - (long long)u * size);
             } else {
-                u = (uint32_t)ahead / (uint32_t)in.s.tiles;
-                k = (uint32_t)ahead - u * (uint32_t)in.s.tiles;
+                u = (uint32_t)ahead / size;
+                k = (uint32_t)ahead - u * size;
             }
-            in.k = (int)k;
+            in.k = (int)k + 1 - weight;
             in.h = p.blocks == 1 ? (int)u : (int)u / p.blocks;
             in.blk = (int)u - in.h * p.blocks;
-            if (left <= 2)
-                ask();
         };
-        auto advance = [&]() {
-            new_run = false;
-            if (--left > 0) {
-                in.next(a, p.blocks);
-                if (left == 2)
-                    ask();                    // the answer is there when this run ends
-                return;
-            }
+        auto settle = [&]() {                 // on to a tile: past a beginning, into the next run
             for (;;) {
-                run = runs.each > 1 ? __shfl_sync(0xffffffffu, asked, 0) : -1;
+                if (left > 0 && in.k == 0) {
+                    left -= weight;
+                    in.k = 1;
+                }
+                if (left > 0) {
+                    if (left <= 2)
+                        ask();                // the answer is there when this run ends
+                    return;
+                }
+                ask();
+                pending = false;
+                run = __shfl_sync(0xffffffffu, asked, 0);
                 if (run < 0) {
                     done = true;
                     return;
                 }
-                if (runs.length(run) > 0)
-                    break;
-                ask();                        // behind the end of the list
+                left = 0;
+                if (runs.length(run) > 0)     // else behind the end of the list
+                    enter();
             }
-            enter();
+        };
+        auto advance = [&]() {
+            new_run = false;
+            if (--left > 0)
+                in.next(a, p.blocks);
+            settle();
         };
         enter();
+        settle();
 
         // ---- fetching: pages are looked up one tile ahead of the copies -----------------------
         const int side = lane >> 4;           // lanes 0-15 stand for the tile's keys, lanes 16-31 for its values
@@ -436,7 +464,7 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
             row_seen = false;
             if (!live)
                 return;
-            const int tok = (in.s.first / kTile + in.k) * kTile + (ALIGNED ? 0 : lane & 15);
+            const int tok = (in.s.first / kTile + in.k - 1) * kTile + (ALIGNED ? 0 : lane & 15);
             if (!ALIGNED && (tok < in.s.first || tok >= in.s.len))
                 return;
             row_seen = true;
@@ -446,7 +474,7 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
         };
         // Copies the tile that `in` stands at, looked up before.
         auto fetch = [&](uint32_t base) {
-            const bool fresh = new_run || in.k == 0;
+            const bool fresh = new_run || in.k == 1;
             if (fresh) {       // the query rows of a new state: into L1 by the time its first tile is there
                 const int rows = min(p.group - in.blk * 16, p.rows);
                 const char *src = reinterpret_cast<const char *>(a.q + ((int64_t)in.b * a.Hq + in.h * p.group + in.blk * 16) * D);
@@ -459,7 +487,7 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
             const int row_bytes = D * ES;
             uint32_t mask;
             if (ALIGNED) {
-                const int tok = (in.s.first / kTile + in.k) * kTile;
+                const int tok = (in.s.first / kTile + in.k - 1) * kTile;
                 mask = 0xFFFFu;
                 if (!ok || tok < in.s.first || tok + kTile > in.s.len) {
                     const int lo = max(in.s.first - tok, 0), hi = min(in.s.len - tok, kTile);
@@ -518,15 +546,15 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
             if (lane == 0) {
                 const uint32_t info = base + 2 * Sh::kKv + Sh::kScales;
                 const int u = in.h * p.blocks + in.blk;
-                const uint32_t what = (mask & 0xFFFFu) | (fresh ? kNew : 0u) | (in.k == 0 ? kFirst : 0u) |
-                                      (in.k == in.s.tiles - 1 ? kLast : 0u) | (left == 1 ? kStop : 0u);
+                const uint32_t what = (mask & 0xFFFFu) | (fresh ? kNew : 0u) | (in.k == 1 ? kFirst : 0u) |
+                                      (in.k == in.s.tiles ? kLast : 0u) | (left == 1 ? kStop : 0u);
                 asm volatile("st.shared.u32 [%0], %1;" ::"r"(info), "r"(what) : "memory");
                 if (fresh) {
                     asm volatile("st.shared.u32 [%0], %1;" ::"r"(info + 4), "r"(in.b) : "memory");
                     asm volatile("st.shared.u32 [%0], %1;" ::"r"(info + 8), "r"(u) : "memory");
                     asm volatile("st.shared.u32 [%0], %1;" ::"r"(info + 12), "r"(run) : "memory");
                 }
-                if (in.k == 0) {
+                if (in.k == 1) {
                     int2 join = make_int2(-1, -1);
                     if (in.s.tiles > left)    // goes on behind this run
                         join = make_int2(run, runs.of(runs.begin(run) + runs.length(run) - left + in.s.tiles - 1));
@@ -535,7 +563,7 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
             }
         };
 
-        look_up(true);
+        look_up(!done);
         int fetched = 0;
 #pragma unroll
         for (int s = 0; s < STAGES - 1; ++s) {
