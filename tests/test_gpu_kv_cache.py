@@ -403,6 +403,64 @@ def test_append(heads, group, dim, rotary, page, order, int8, interleaved):
         assert torch.equal(store.cpu()[~touched], before[i].cpu()[~touched])
 
 
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("T,heads,group,dim,rotary,interleaved,apart", [
+    (305, 8, 4, 128, 128, False, False), (1500, 2, 4, 128, 64, False, True), (5003, 1, 1, 16, 16, True, False),
+    (777, 2, 3, 48, 32, True, True), (640, 1, 8, 256, 0, False, False), (401, 3, 2, 80, 48, False, False),
+    (350, 2, 2, 64, 22, False, False), (613, 16, 8, 256, 256, True, True),
+])
+def test_append_many_tokens(T, heads, group, dim, rotary, interleaved, apart, int8):
+    """Many tokens at once: against the formula in 64 bits, with padding, positions past the
+    table of angles, rows past the table of pages and pages that are not there among them;
+    `apart`: heads of q that do not follow one another."""
+    g = torch.Generator().manual_seed(T)
+    page, n_rows, Hq = 16, 4, heads * group
+    width = T // n_rows // page + 2
+    max_pos = width * page - 5
+    cache = _cache(n_rows * width, page, heads, dim, int8, "head", fill=-1.0)
+    before = [t.clone() for t in (cache.k, cache.v)]
+    table = torch.randperm(n_rows * width, generator=g).to(I32).view(n_rows, width)
+    table[2, 1], table[3, 0] = n_rows * width, -1
+    place = torch.randperm(n_rows * (T // n_rows + 1), generator=g)[:T]
+    rows, pos = (place % n_rows).to(I32), (place // n_rows).to(I32)
+    pos[7], pos[T - 1], pos[T // 2] = -1, -9, max_pos if rotary else width * page
+    rows[11], rows[12] = n_rows, -1
+    fused = _rand(g, T, Hq + 2 * heads, dim)
+    q, k, v = fused[:, :Hq], fused[:, Hq:-heads], fused[:, -heads:]
+    if apart:
+        q = _rand(g, T, 2 * Hq, dim)[:, ::2]
+    angle = torch.rand((max_pos, rotary // 2), generator=g) * 6
+    cos, sin = angle.cos().to(dev()), angle.sin().to(dev())
+    assert s3d8.device_status() == 0
+    out = s3d8.rope_append(q, k, v, cos, sin, pos.to(dev()), cache, table.to(dev()), rows=rows.to(dev()),
+                           interleaved=interleaved)
+    assert s3d8.device_status() == -7
+    real = (pos >= 0) & ((pos < max_pos) | (rotary == 0))
+    col = pos.clamp(min=0).long() // page
+    stored = real & (rows >= 0) & (rows < n_rows) & (col < width)
+    pages = table[rows.clamp(0, n_rows - 1).long(), col.clamp(max=width - 1)].long()
+    stored &= (pages >= 0) & (pages < n_rows * width)
+    c, s = (t.double().cpu().numpy()[pos.clamp(0, max_pos - 1).long()] for t in (cos, sin))
+    ref = _turn(bf16_to_f64(q), c, s, rotary, interleaved) * real.numpy()[:, None, None]
+    assert (np.abs(bf16_to_f64(out) - ref) <= 2.0 ** -8 * np.abs(ref) + 1e-6).all()
+    where = (pages[stored], pos[stored].long() % page)
+    touched = torch.zeros(cache.k.shape[:2], dtype=torch.bool)
+    touched[where] = True
+    at = tuple(i.to(dev()) for i in where)
+    for i, (store, sc, new) in enumerate(((cache.k, cache.k_scale, _turn(bf16_to_f64(k), c, s, rotary, interleaved)),
+                                          (cache.v, cache.v_scale, bf16_to_f64(v)))):
+        new = new[stored.numpy()]
+        have = store[at].double().cpu().numpy()
+        tol = 2.0 ** -8 * np.abs(new) + 1e-6
+        if int8:
+            step = sc[at].double().cpu().numpy()[..., None]
+            top = np.abs(new).max(-1, keepdims=True)
+            assert (np.abs(step * 127 - top) <= 1e-6 * top + 1e-30).all()
+            have, tol = have * step, 0.5 * step + 2.0 ** -8 * np.abs(new) + 1e-6
+        assert (np.abs(have - new) <= tol).all(), np.abs(have - new).max()
+        assert torch.equal(store.cpu()[~touched], before[i].cpu()[~touched])
+
+
 def test_append_then_attend_and_rows_default():
     """A decode step: token t of row t, then attention over it and what was there."""
     g = torch.Generator().manual_seed(21)
