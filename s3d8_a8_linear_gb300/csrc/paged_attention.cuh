@@ -6,9 +6,9 @@
 // Bound by HBM: every visible key and value is read once, for up to 16 query rows
 // at a time.  The unit of work is a tile of 16 tokens of one (sequence, key/value
 // head); the list of all tiles (a sequence's beginning counting as one more) is cut
-// into contiguous runs, whatever the lengths are.  A warp streams its runs through a ring of its own in shared memory
-// (cp.async, no barrier with other warps) and carries the softmax's running maximum
-// m, sum l and the output sums O in fp32:
+// into contiguous runs, whatever the lengths are.  A warp streams its runs through
+// a ring of its own in shared memory (cp.async, no barrier with other warps) and
+// carries the softmax's running maximum m, sum l and the output sums O in fp32:
 //   S = K Q^T (tensor cores, rows = tokens, columns = 8 or 16 query rows),
 //   m' = max(m, S), O = 2^(m - m') O + V^T 2^(S - m'), l likewise.
 // The matrix products are mma.sync (tcgen05's smallest tile is 64 rows, and the
@@ -24,9 +24,9 @@
 // the parts of each such sequence, in order of position.
 //
 // Measured with 32 / 8 heads of 128, join included: 8 sequences of up to 131072 tokens
-// 531 us (6.8 TB/s), 64 of up to 8191 177 us (6.1 TB/s; 5 us until the first tiles
+// 533 us (6.8 TB/s), 64 of up to 8191 181 us (5.9 TB/s; 5 us until the first tiles
 // arrive, 5 to 10 from the last ones through the join), 48 int8 sequences with a window
-// 214 us (5.6 TB/s; 65% of the issue slots, a third of them turning codes into fp16).
+// 212 us (5.7 TB/s; 65% of the issue slots, a third of them turning codes into fp16).
 #pragma once
 
 #include "common.cuh"
