@@ -225,28 +225,6 @@ uint2 quant_chunk8(uint4 v, float s, float r)
     return make_uint2(lo, hi);
 }
 
-// Eight bf16 values (one 16-byte chunk) as fp32, and back (rounded to nearest).
-__device__ __forceinline__ void unpack8(uint4 v, float (&f)[8])
-{
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        f[2 * j] = __uint_as_float(w[j] << 16);
-        f[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-    }
-}
-
-__device__ __forceinline__ uint4 pack8(const float (&f)[8])
-{
-    uint32_t w[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const __nv_bfloat162 p = __floats2bfloat162_rn(f[2 * j], f[2 * j + 1]);
-        w[j] = *reinterpret_cast<const uint32_t *>(&p);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
 __device__ __forceinline__ int warp_sum(int v)
 {
 #pragma unroll

@@ -15,6 +15,7 @@
 //     from global memory.
 // Measured, with a post-norm: forward of 16383 x 4096 88 us (6.1 TB/s of what it has
 // to move), backward of 8192 x 4096 70 us (5.7 TB/s), forward of one token 2.7 us.
+#include "bf16x8.cuh"
 #include "common.cuh"
 #include "launch.h"
 #include "tcgen05.cuh"

@@ -10,6 +10,7 @@
 // token's stores.  Measured: 61 tokens of 32 + 16 heads of 128 in 2.4 us, 16384 in
 // 73 us (5.6 TB/s of what it has to move; 77 us without the ring), 4099 into int8 in
 // 22 us (25 us).
+#include "bf16x8.cuh"
 #include "common.cuh"
 #include "launch.h"
 #include "tcgen05.cuh"
