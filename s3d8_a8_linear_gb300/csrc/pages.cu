@@ -206,6 +206,7 @@ __global__ __launch_bounds__(kMetaThreads) void fork_pages_kernel(PagesArgs a)
                 }
             }
         }
+        __syncwarp();     // every lane has read the entry's lists
         if (lane == 0) {
             src[i] = from;
             dst[i] = fresh;
