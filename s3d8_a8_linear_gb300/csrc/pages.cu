@@ -8,6 +8,7 @@
 // move 40 MB), compaction of 250 pages in 40 layers 206 us (6.4 TB/s).
 #include "common.cuh"
 #include "launch.h"
+#include "page_room.h"
 #include "tcgen05.cuh"
 
 namespace s3d8 {
@@ -17,13 +18,14 @@ namespace {
 constexpr int kMetaThreads = 1024, kMetaWarps = kMetaThreads / 32;
 
 // Exclusive prefix sum of one value per thread; `total` receives the sum.
-__device__ int block_scan(int v, int *warp_sums, int &total)
+template <class T>
+__device__ T block_scan(T v, T *warp_sums, T &total)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int inc = v;
+    T inc = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, inc, o);
+        const T u = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o)
             inc += u;
     }
@@ -31,10 +33,10 @@ __device__ int block_scan(int v, int *warp_sums, int &total)
     if (lane == 31)
         warp_sums[warp] = inc;
     __syncthreads();
-    int w = warp_sums[lane];
+    T w = warp_sums[lane];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(0xffffffffu, w, o);
+        const T u = __shfl_up_sync(0xffffffffu, w, o);
         if (lane >= o)
             w += u;
     }
@@ -85,10 +87,11 @@ __device__ __forceinline__ int32_t *ws_list(const PagesArgs &a, int k)
 __global__ __launch_bounds__(kMetaThreads) void extend_pages_kernel(PagesArgs a)
 {
     __shared__ int sums[32];
+    __shared__ long long wanted[32];
     tc::pdl_launch_dependents();
     tc::pdl_wait();
     int32_t *ids = ws_list(a, 0), *begins = ws_list(a, 3), *needs = ws_list(a, 4);
-    int asked = 0;
+    long long asked = 0;   // a page for every column of every entry may pass 2^31
     for (int i0 = 0; i0 < a.n; i0 += kMetaThreads) {
         const int i = i0 + threadIdx.x;
         int need = -1;   // refused
@@ -104,22 +107,22 @@ __global__ __launch_bounds__(kMetaThreads) void extend_pages_kernel(PagesArgs a)
                     need = (int)(want - have);
             }
         }
-        int total;
-        const int begin = asked + block_scan(max(need, 0), sums, total);
+        long long total;
+        const long long begin = asked + block_scan((long long)max(need, 0), wanted, total);
         asked += total;
         if (i < a.n) {
-            begins[i] = begin;
+            begins[i] = page_rank(begin);
             needs[i] = need;
         }
     }
     __syncthreads();
     const int32_t *refs = a.refs;
-    const int free = enumerate(0, a.pages, min(asked, a.pages), sums, [&](int id) { return refs[id] == 0; },
+    const int free = enumerate(0, a.pages, min(page_rank(asked), a.pages), sums, [&](int id) { return refs[id] == 0; },
                                [&](int id, int at) { ids[at] = id; });
     __syncthreads();
     for (int i = threadIdx.x >> 5; i < a.n; i += kMetaWarps) {
         const int lane = threadIdx.x & 31, need = needs[i], begin = begins[i];
-        const bool ok = need == 0 || (need > 0 && begin + need <= free);
+        const bool ok = page_room(begin, need, free);
         if (ok) {
             const int s = a.who[i];
             const int len = max(a.lens[s], 0);
@@ -160,7 +163,7 @@ __global__ __launch_bounds__(kMetaThreads) void fork_pages_kernel(PagesArgs a)
             }
         }
         int total;
-        const int begin = asked + block_scan(part > 0, sums, total);
+        const int begin = asked + block_scan((int)(part > 0), sums, total);
         asked += total;
         if (i < a.n) {
             src[i] = at;

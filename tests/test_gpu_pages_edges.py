@@ -33,3 +33,18 @@ def test_forks_of_many_entries_and_wide_rows():
                 want[b, :tokens] = old[a, :tokens]
             assert torch.equal(have, want)
             have.copy_(old)
+
+
+def test_growth_that_wants_more_pages_than_an_int_counts():
+    """Two entries that want 2^30 pages each between two that want a few, on a table of 2^32 entries."""
+    width, pages = 1 << 30, 64
+    table = torch.empty((4, width), dtype=torch.int32, device=dev())
+    table[:, :8] = -1
+    table[:, -8:] = -1
+    lens, refs = torch.zeros(4, dtype=torch.int32, device=dev()), torch.zeros(pages, dtype=torch.int32, device=dev())
+    space = torch.full((4 * (3 * pages + 3 * 4 + 4),), 255, dtype=torch.uint8, device=dev())
+    got = s3d8.extend_pages(table, lens, refs, _i32([2, 0, 3, 1]), _i32([3, width, width, 5]), 1, workspace=space)
+    assert got.tolist() == [1, 0, 0, 0]
+    assert lens.tolist() == [0, 0, 3, 0] and refs.tolist() == [1] * 3 + [0] * (pages - 3)
+    assert table[:, :8].tolist() == [[-1] * 8, [-1] * 8, [0, 1, 2] + [-1] * 5, [-1] * 8]
+    assert bool((table[:, -8:] == -1).all())
