@@ -420,7 +420,8 @@ int s3d8_paged_attention(const void *q_bf16, const s3d8_kv_cache *cache, const i
  *                    are shared (refs + 1), the tokens of a last, partial page are
  *                    copied to a new one in every layer.  What a child's row held
  *                    is overwritten, not freed; no child is a parent of the call.
- *                    A refused child gets an empty row (-1, lens 0).  got [n]
+ *                    A refused child (no page was left, or one of the parent's ids
+ *                    is out of range) gets an empty row (-1, lens 0).  got [n]
  * s3d8_free_pages    rows seqs[i]: refs - 1 for each page held, row -1, lens 0
  * s3d8_compact_pages live pages move to the ids 0 .. live-1: those at or above
  *                    live go, in ascending order, to the free ids below it; their

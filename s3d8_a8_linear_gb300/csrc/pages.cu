@@ -147,29 +147,56 @@ __global__ __launch_bounds__(kMetaThreads) void fork_pages_kernel(PagesArgs a)
     tc::pdl_launch_dependents();
     tc::pdl_wait();
     int32_t *ids = ws_list(a, 0), *src = ws_list(a, 3), *dst = ws_list(a, 4), *tokens = ws_list(a, 5);
+    // what can be forked: a warp an entry, since every page of the parent is looked at before any is shared; four entries'
+    // loads leave together (200 forks on one layer: 23 us, against 27 one after another)
+    constexpr int kAhead = 4;
+    for (int i0 = threadIdx.x >> 5; i0 < a.n; i0 += kAhead * kMetaWarps) {
+        const int lane = threadIdx.x & 31;
+        int64_t p[kAhead];
+        int len[kAhead], id[kAhead];
+        bool bad[kAhead];
+#pragma unroll
+        for (int x = 0; x < kAhead; ++x) {
+            const int i = min(i0 + x * kMetaWarps, a.n - 1);
+            const int64_t c = a.other[i];
+            p[x] = a.who[i];
+            bad[x] = p[x] < 0 || p[x] >= a.rows || c < 0 || c >= a.rows;
+        }
+#pragma unroll
+        for (int x = 0; x < kAhead; ++x)
+            len[x] = bad[x] ? 0 : a.lens[p[x]];
+#pragma unroll
+        for (int x = 0; x < kAhead; ++x) {
+            bad[x] |= len[x] < 0 || len[x] > a.width * a.page_size;
+            len[x] = bad[x] ? 0 : len[x];
+            id[x] = (int64_t)lane * a.page_size < len[x] ? a.table[p[x] * a.width + lane] : 0;
+        }
+#pragma unroll
+        for (int x = 0; x < kAhead; ++x) {
+            const int i = i0 + x * kMetaWarps, full = len[x] / a.page_size, part = len[x] - full * a.page_size;
+            bad[x] |= id[x] < 0 || id[x] >= a.pages;
+            for (int k = lane + 32; k < full + (part > 0); k += 32) {
+                const int more = a.table[p[x] * a.width + k];
+                bad[x] |= more < 0 || more >= a.pages;
+            }
+            bad[x] = __any_sync(0xffffffffu, bad[x]);
+            if (lane == 0 && i < a.n) {
+                src[i] = bad[x] ? -2 : part ? full : -1;   // the partial page's column; -2: refused
+                tokens[i] = bad[x] ? 0 : part;
+                if (bad[x])
+                    atomicExch(a.status, kStatusBounds);
+            }
+        }
+    }
+    __syncthreads();
     int asked = 0;
     for (int i0 = 0; i0 < a.n; i0 += kMetaThreads) {
         const int i = i0 + threadIdx.x;
-        int part = 0, at = -1;   // tokens of the last page, its column; at -2: refused
-        if (i < a.n) {
-            const int64_t p = a.who[i], c = a.other[i];
-            if (p < 0 || p >= a.rows || c < 0 || c >= a.rows || a.lens[p] < 0 ||
-                a.lens[p] > a.width * a.page_size) {
-                at = -2;
-                atomicExch(a.status, kStatusBounds);
-            } else {
-                part = a.lens[p] % a.page_size;
-                at = part ? a.lens[p] / a.page_size : -1;
-            }
-        }
         int total;
-        const int begin = asked + block_scan((int)(part > 0), sums, total);
+        const int begin = asked + block_scan((int)(i < a.n && tokens[i] > 0), sums, total);
         asked += total;
-        if (i < a.n) {
-            src[i] = at;
+        if (i < a.n)
             dst[i] = begin;
-            tokens[i] = part;
-        }
     }
     __syncthreads();
     const int32_t *refs = a.refs;
@@ -188,7 +215,7 @@ __global__ __launch_bounds__(kMetaThreads) void fork_pages_kernel(PagesArgs a)
                 int id = -1;
                 if (k < full) {
                     id = a.table[p * a.width + k];
-                    if (id >= 0 && id < a.pages)
+                    if (id >= 0 && id < a.pages)   // else the row is a child of this call as well
                         atomicAdd(a.refs + id, 1);
                     else
                         id = -1;
@@ -202,10 +229,8 @@ __global__ __launch_bounds__(kMetaThreads) void fork_pages_kernel(PagesArgs a)
                 if (fresh >= 0) {
                     a.refs[fresh] = 1;
                     from = a.table[p * a.width + full];
-                    if (from < 0 || from >= a.pages) {
+                    if (from >= a.pages)
                         from = -1;
-                        atomicExch(a.status, kStatusBounds);
-                    }
                 }
             }
         }
