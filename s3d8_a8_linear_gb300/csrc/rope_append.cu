@@ -13,6 +13,7 @@
 #include "bf16x8.cuh"
 #include "common.cuh"
 #include "launch.h"
+#include "rope_plan.h"
 #include "tcgen05.cuh"
 
 namespace s3d8 {
@@ -50,8 +51,6 @@ enum RopeMode {
     kNeighbours,    // pairs (2i, 2i + 1): two neighbouring chunks
     kHalvesOdd      // any other rotary: neighbouring chunks, partners read one by one
 };
-
-constexpr int kRopeThreads = 256;   // at most
 
 // A lane's part of every row: two chunks, and whether its pairs 8 lane .. 8 lane + 7 turn.
 struct RopeLane {
@@ -249,10 +248,6 @@ __global__ __launch_bounds__(kRopeThreads, 3) void rope_append_kernel(const __gr
 // turn and store.  Many small CTAs, as the turning and the stores want warps:
 // 16384 tokens of 48 heads of 128 take 78 us with two CTAs an SM of eight stages,
 // 77 with three of five, 73 with five of three (int8: 102, 92, 70).
-constexpr int kRingStages = 8;           // at most
-constexpr int kRingBytes = 110 * 1024;   // of a CTA, at most
-constexpr int kRingThreads = 800;        // of an SM
-
 template <int MODE, bool INT8>
 __global__ __launch_bounds__(kRopeThreads + 32, 3) void rope_append_ring_kernel(const __grid_constant__ RopeArgs a, int log_lanes,
                                                                               int stages, int stage_bytes)
@@ -377,29 +372,19 @@ cudaError_t launch_mode(const RopeArgs &a, cudaStream_t stream)
     const int heads = a.Hq + 2 * a.kv.heads, rows = a.T <= 2 * device_sm_count() ? 2 : 4;
     const int vec = a.rotary % 16 == 0 && ((uintptr_t)a.cos & 15) == 0 && ((uintptr_t)a.sin & 15) == 0;
     if constexpr (MODE != kHalvesOdd) {
-        const int64_t sms = device_sm_count();
-        const int stage = heads * a.kv.dim * 2 + a.rotary * 4;
+        const RopeRing ring = rope_ring(heads, a.kv.dim, a.rotary, log_lanes);
         const bool whole = a.qs[1] == a.kv.dim && a.ks[1] == a.kv.dim && a.vs[1] == a.kv.dim;   // a token's heads in one piece
         // The ring from about as many tokens as there is room for at once (500 tokens of 48 heads of 128: 4.6 us against
         // 5.2).  Not for small rows in int8, which want more warps than it has (16384 tokens of 16 heads of 64: 31 us
         // against 27; of 12 heads of 256: 48 against 58).
-        if (rows == 4 && vec && whole && 3 * stage <= kRingBytes && (!INT8 || stage >= 4096)) {
-            int threads = (((heads + 2) / 3 << log_lanes) + 31) / 32 * 32;
-            threads = threads < kRopeThreads ? threads : kRopeThreads;
-            // five CTAs of three stages at 48 heads of 128; more of them where a token has fewer rows
-            int ctas = kRingThreads / (threads + 32), stages = (227 * 1024 / ctas - 1536) / stage;
-            if (stages < 3) {
-                stages = 3;
-                ctas = 227 * 1024 / (3 * stage + 1536);
-            }
-            stages = stages < kRingStages ? stages : kRingStages;
-            const int64_t grid = sms * ctas;
+        if (rows == 4 && vec && whole && ring.stages && (!INT8 || ring.stage >= 4096)) {
+            const int64_t grid = (int64_t)device_sm_count() * ring.ctas;
             auto kernel = rope_append_ring_kernel<MODE, INT8>;
             static std::atomic<unsigned long long> allowed;
             const cudaError_t e = tc::allow_smem(kernel, kRingBytes, allowed);
             return e != cudaSuccess ? e
-                                    : tc::launch_pdl(kernel, dim3((unsigned)(a.T < grid ? a.T : grid)), dim3(threads + 32),
-                                                     (size_t)stages * stage, stream, a, log_lanes, stages, stage);
+                                    : tc::launch_pdl(kernel, dim3((unsigned)(a.T < grid ? a.T : grid)), dim3(ring.threads + 32),
+                                                     (size_t)ring.stages * ring.stage, stream, a, log_lanes, ring.stages, ring.stage);
         }
     }
     int threads = (((heads + rows - 1) / rows << log_lanes) + 31) / 32 * 32;

@@ -1,0 +1,17 @@
+"""The append's ring of bulk copies at layouts where its shared memory is nearly all that a
+CTA may have, against the formula in 64 bits."""
+import pytest
+
+import test_gpu_kv_cache as kv
+from test_gpu_kv_cache import _lib  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("T,heads,group,dim,rotary,interleaved", [
+    (400, 32, 1, 96, 96, False), (305, 8, 10, 96, 96, True), (700, 8, 12, 128, 0, False), (400, 29, 1, 80, 80, False),
+    (400, 4, 16, 192, 192, False), (333, 8, 9, 128, 64, True), (400, 31, 2, 112, 112, False),
+])
+def test_append_of_many_heads(T, heads, group, dim, rotary, interleaved, int8):
+    kv.test_append_many_tokens(T, heads, group, dim, rotary, interleaved, False, int8)
