@@ -373,7 +373,8 @@ cudaError_t launch_mode(const RopeArgs &a, cudaStream_t stream)
     const int vec = a.rotary % 16 == 0 && ((uintptr_t)a.cos & 15) == 0 && ((uintptr_t)a.sin & 15) == 0;
     if constexpr (MODE != kHalvesOdd) {
         const RopeRing ring = rope_ring(heads, a.kv.dim, a.rotary, log_lanes);
-        const bool whole = a.qs[1] == a.kv.dim && a.ks[1] == a.kv.dim && a.vs[1] == a.kv.dim;   // a token's heads in one piece
+        const bool whole = rope_whole(a.Hq, a.qs[1], a.kv.dim) && rope_whole(a.kv.heads, a.ks[1], a.kv.dim) &&
+                           rope_whole(a.kv.heads, a.vs[1], a.kv.dim);
         // The ring from about as many tokens as there is room for at once (500 tokens of 48 heads of 128: 4.6 us against
         // 5.2).  Not for small rows in int8, which want more warps than it has (16384 tokens of 16 heads of 64: 31 us
         // against 27; of 12 heads of 256: 48 against 58).

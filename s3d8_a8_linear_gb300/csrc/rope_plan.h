@@ -35,4 +35,8 @@ inline RopeRing rope_ring(int heads, int dim, int rotary, int log_lanes)
     return r;
 }
 
+// Whether the rows of one token's `heads` heads, `stride` elements apart, lie in one
+// piece.  The stride of a single head means nothing (the binding passes 0).
+inline bool rope_whole(int heads, long long stride, int dim) { return heads == 1 || stride == dim; }
+
 }  // namespace s3d8

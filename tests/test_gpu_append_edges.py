@@ -15,3 +15,13 @@ pytestmark = pytest.mark.gpu
 ])
 def test_append_of_many_heads(T, heads, group, dim, rotary, interleaved, int8):
     kv.test_append_many_tokens(T, heads, group, dim, rotary, interleaved, False, int8)
+
+
+@pytest.mark.parametrize("int8", [False, True])
+@pytest.mark.parametrize("T,group,dim,rotary,interleaved", [
+    (305, 32, 128, 128, False), (1100, 8, 256, 64, True), (5003, 1, 16, 16, False), (640, 71, 64, 64, False),
+    (400, 4, 80, 0, False), (3001, 1, 128, 128, True),
+])
+def test_append_many_tokens_of_one_key_value_head(T, group, dim, rotary, interleaved, int8):
+    """One key/value head (and one query head): the stride of an axis of one element is whatever it is."""
+    kv.test_append_many_tokens(T, 1, group, dim, rotary, interleaved, False, int8)

@@ -19,12 +19,14 @@ def lib(tmp_path_factory):
     src, lib = out / "plan.cpp", out / "plan.so"
     names = ("kRopeThreads", "kRingStages", "kRingBytes", "kRingSm", "kRingFixed")
     src.write_text('#include "rope_plan.h"\n'
-                   'extern "C" s3d8::RopeRing ring(int h, int d, int r, int l) { return s3d8::rope_ring(h, d, r, l); }\n' +
+                   'extern "C" s3d8::RopeRing ring(int h, int d, int r, int l) { return s3d8::rope_ring(h, d, r, l); }\n'
+                   'extern "C" int whole(int h, long long s, int d) { return s3d8::rope_whole(h, s, d); }\n' +
                    "".join(f'extern "C" int {n}() {{ return s3d8::{n}; }}\n' for n in names))
     subprocess.run(["g++", "-std=c++17", "-O2", "-Wall", "-Werror", "-shared", "-fPIC", "-I", _build.CSRC, str(src), "-o", str(lib)],
                    check=True)
     L = ctypes.CDLL(os.fspath(lib))
     L.ring.restype = Ring
+    L.whole.argtypes = [ctypes.c_int, ctypes.c_longlong, ctypes.c_int]
     return L, {n: getattr(L, n)() for n in names}
 
 
@@ -58,3 +60,10 @@ def test_the_ring_stays_within_what_a_launch_is_allowed(lib, dim):
 def test_the_ring_of_some_models(lib, heads, dim, rotary, want):
     r = lib[0].ring(heads, dim, rotary, (dim // 16 - 1).bit_length())
     assert (r.threads, r.ctas, r.stages) == want
+
+
+def test_heads_lie_in_one_piece(lib):
+    whole = lib[0].whole
+    assert whole(8, 128, 128) and not whole(8, 256, 128) and not whole(2, 0, 64) and not whole(2, 1 << 40, 64)
+    for stride in (0, 64, 128, 1 << 40):      # one head is one piece, whatever its stride says
+        assert whole(1, stride, 64)
