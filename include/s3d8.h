@@ -392,7 +392,9 @@ int s3d8_rope_append(const void *q_bf16, const int64_t q_stride[2], const void *
  * a sequence's last token, or in front of its window, is never used, whatever it
  * is.  A page id out of range counts as masked tokens and records
  * S3D8_ERR_BOUNDS; so does a length beyond the table (cut to it).  Scores, the softmax's maximum and sum
- * and the output sums are fp32.
+ * and the output sums are fp32.  The factor of a value is rounded on its way into the
+ * product with it: a bf16 cache's weights to 16 bits; with an int8 cache, weight times
+ * scale to 22 bits, or to 2^-30 of the largest one of its query row, whichever is coarser.
  */
 size_t s3d8_paged_attention_workspace_size(const s3d8_kv_cache *cache, int64_t B, int64_t Hq);
 int s3d8_paged_attention(const void *q_bf16, const s3d8_kv_cache *cache, const int32_t *table,

@@ -13,8 +13,10 @@
 //   m' = max(m, S), O = 2^(m - m') O + V^T 2^(S - m'), l likewise.
 // The matrix products are mma.sync (tcgen05's smallest tile is 64 rows, and the
 // rate needed here is far below the tensor cores' limit).  The weights 2^(S - m')
-// enter the second product as a 16-bit value and its 16-bit remainder, so that
-// they keep 16 bits or more.
+// enter the second product as a 16-bit value and its 16-bit remainder: 16 bits of
+// them in bf16.  With an int8 cache it is the weight times the value's scale, in fp16:
+// 22 bits, or 2^-30 of the largest such product that its query row has met, whichever
+// is coarser.
 //
 // Every warp begins with a run of three quarters of its even share; the last quarter
 // of each share is in short runs that go to whichever warp is free (SMs differ by a
@@ -26,8 +28,10 @@
 // Measured with 32 / 8 heads of 128, join included: 8 sequences of up to 131072 tokens
 // 533 us (6.8 TB/s), 64 of up to 8191 181 us (5.9 TB/s; 5 us until the first tiles
 // arrive, 5 to 10 from the last ones through the join), 48 int8 sequences with a window
-// 212 us (5.7 TB/s; 65% of the issue slots, a third of them turning codes into fp16).
+// 213 us (5.6 TB/s; 65% of the issue slots, a third of them turning codes into fp16).
 #pragma once
+
+#include <cfloat>
 
 #include "common.cuh"
 #include "launch.h"
@@ -40,8 +44,11 @@ namespace attn {
 constexpr int kTile = 16;          // tokens
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kSlack = 8.0f;     // weights reach 2^8,
-constexpr int kUp = 6;             // and with their value scales, below 2^6, stay inside fp16 (int8 caches)
+constexpr float kSlack = 8.0f;     // weights reach 2^8
+// int8 caches: what a value's code is multiplied with, its weight times its scale, is carried times a power of two of its
+// query row (2^kFar at most), which makes the row's largest product about 2^kUp when it is met and lets none pass 2^kFull:
+// inside fp16.  By the products, not by the scales: a large scale on a token of no weight must not push the others down.
+constexpr float kUp = 6.0f, kFull = 15.0f, kFar = 116.0f;
 
 template <int DP, bool INT8>
 struct Shape {
@@ -160,6 +167,12 @@ __device__ __forceinline__ float ex2(float x)
 {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float lg2(float x)
+{
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 
@@ -310,6 +323,11 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
     __shared__ long long warp_tiles[WARPS];
     __shared__ int warp_some[WARPS];
     __shared__ uint4 state[WARPS];                // what each warp's running state is of (as its first tile says)
+    // int8: the powers of two that a lane's query rows carry (x = 0, 1 by y = 0, 1), and the value scale up to which no
+    // product passes 2^kFull, whatever the weight.  In registers for 8 query rows (48 sequences with a window: 212 us, 219
+    // from here); 16 leave none (64 sequences, 12 heads a key/value head of 128: 172 us from here, 183 in registers).
+    constexpr bool kShared = INT8 && NB == 2;
+    __shared__ __align__(16) float carried[kShared ? WARPS : 1][4][8];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int D = a.kv.dim, S = a.kv.page_size;
     tc::pdl_launch_dependents();
@@ -581,7 +599,21 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
         float o[MT][NB][4], m[NB][2], l[NB][2];
         uint32_t q[DP / 16][NB][2];
         float qs[NB][2];                      // factor of a query row's scores, log2(e) in it
-        float vf = 0.0f, vinv = 0.0f;         // int8: the power of two that carries the value scales
+        float up[2][2], limit = 0.0f;
+        float *const mine = carried[kShared ? warp : 0][t];
+        auto read_powers = [&]() {
+            if (!kShared)
+                return;
+            const uint4 v = lds_v4(smem_addr(mine));
+            up[0][0] = __uint_as_float(v.x), up[0][1] = __uint_as_float(v.y);
+            up[1][0] = __uint_as_float(v.z), up[1][1] = __uint_as_float(v.w);
+        };
+        auto write_powers = [&]() {
+            if (kShared && g == 0) {
+                *reinterpret_cast<float4 *>(mine) = make_float4(up[0][0], up[0][1], up[1][0], up[1][1]);
+                mine[4] = limit;
+            }
+        };
         bool whole = false;                   // this run has the sequence from its first tile on
 
         uint32_t base = ring, filled = ring + (STAGES - 1) * Sh::kStage;   // stages of the tile, and of the next one to fetch
@@ -606,17 +638,19 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
                 const uint4 info = lds_v4(base + 2 * Sh::kKv + Sh::kScales);
                 if (lane == 0)
                     state[warp] = info;           // for the state's end
-                const int u = (int)info.z, h = p.blocks == 1 ? u : u / p.blocks, blk = u - h * p.blocks;
+                const int unit = (int)info.z, h = p.blocks == 1 ? unit : unit / p.blocks, blk = unit - h * p.blocks;
                 const int rows = min(p.group - blk * 16, p.rows);
                 const int64_t head0 = (int64_t)info.y * a.Hq + h * p.group + blk * 16;   // query row of the state's row 0
                 whole = mask & kFirst;
-                vf = vinv = 0.0f;
+                up[0][0] = up[0][1] = up[1][0] = up[1][1] = 1.0f;
+                limit = 0.0f;
+                write_powers();
 #pragma unroll
                 for (int x = 0; x < NB; ++x) {
 #pragma unroll
                     for (int j = 0; j < MT; ++j)
                         o[j][x][0] = o[j][x][1] = o[j][x][2] = o[j][x][3] = 0.0f;
-                    m[x][0] = m[x][1] = -INFINITY;
+                    m[x][0] = m[x][1] = INT8 ? -FLT_MAX : -INFINITY;
                     l[x][0] = l[x][1] = 0.0f;
                     qs[x][0] = qs[x][1] = a.scale * kLog2e;
                     const __nv_bfloat16 *src = a.q + (head0 + g + 8 * x) * D;
@@ -709,9 +743,12 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
             }
             const bool see0 = (mask >> g) & 1, see1 = (mask >> (g + 8)) & 1;
             // ---- running maximum, weights ---------------------------------------------------------------
-            // The maximum (and, in int8, the power of two over the value scales) moves only when a tile exceeds it by more
-            // than 2^kSlack: until then no lane has to hear of the others' scores, and the weights stay below 2^kSlack.
-            bool above = INT8 && fmaxf(fabsf(vs0), fabsf(vs1)) > vf;
+            // The maximum moves only when a tile exceeds it by more than 2^kSlack: until then no lane has to hear of the others'
+            // scores, and the weights stay below 2^kSlack.  int8 keeps the next whole number, and moves a row's power of two
+            // only when a product passes 2^kFull, which takes a value scale above a limit: steps are by powers of two.
+            if (kShared)
+                limit = __uint_as_float(lds_u32(smem_addr(mine) + 16));
+            bool above = false, heavy = INT8 && fmaxf(fabsf(vs0), fabsf(vs1)) > limit;
 #pragma unroll
             for (int x = 0; x < NB; ++x)
 #pragma unroll
@@ -720,35 +757,48 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
                     sc[x][2 + y] = see1 ? sc[x][2 + y] * (INT8 ? qs[x][y] * ks1 : qs[x][y]) : -INFINITY;
                     above |= fmaxf(sc[x][y], sc[x][2 + y]) > m[x][y] + kSlack;
                 }
-            if (__any_sync(0xffffffffu, above)) {
-                float vkeep = 1.0f;
-                if (INT8) {
-                    float vtop = fmaxf(fabsf(vs0), fabsf(vs1));
+            bool move = __any_sync(0xffffffffu, above || heavy);
+            if (INT8 && move) {
+                read_powers();
 #pragma unroll
-                    for (int off = 4; off <= 16; off <<= 1)
-                        vtop = fmaxf(vtop, __shfl_xor_sync(0xffffffffu, vtop, off));
-                    if (vtop > vf) {
-                        const uint32_t e = min(max((__float_as_uint(vtop) >> 23) + 1u, 16u), 253u);   // 2^(e - 127) > vtop
-                        const float old = vf;
-                        vf = __uint_as_float(e << 23);
-                        vinv = __uint_as_float((254u + (uint32_t)kUp - e) << 23);   // 2^kUp / vf
-                        vkeep = old / vf;
+                for (int x = 0; x < NB; ++x)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        const float top = fmaxf(fabsf(ex2(sc[x][y] - m[x][y]) * vs0), fabsf(ex2(sc[x][2 + y] - m[x][y]) * vs1));
+                        above |= top * up[x][y] > (float)(1 << (int)kFull);
                     }
-                }
+                move = __any_sync(0xffffffffu, above);
+            }
+            if (move) {
+                const float lv0 = INT8 ? lg2(fabsf(vs0)) : 0.0f, lv1 = INT8 ? lg2(fabsf(vs1)) : 0.0f;
+                limit = FLT_MAX;
                 float keep[NB][2];
 #pragma unroll
                 for (int x = 0; x < NB; ++x)
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
                         float top = fmaxf(sc[x][y], sc[x][2 + y]);
+                        float product = INT8 ? fmaxf(sc[x][y] + lv0, sc[x][2 + y] + lv1) : 0.0f;
 #pragma unroll
-                        for (int off = 4; off <= 16; off <<= 1)
+                        for (int off = 4; off <= 16; off <<= 1) {
                             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-                        top = fmaxf(m[x][y], top);
-                        keep[x][y] = top == m[x][y] ? 1.0f : ex2(m[x][y] - top);
+                            if (INT8)
+                                product = fmaxf(product, __shfl_xor_sync(0xffffffffu, product, off));
+                        }
+                        const float was = m[x][y];
+                        top = fmaxf(was, INT8 ? ceilf(top) : top);
+                        keep[x][y] = top == was ? 1.0f : ex2(was - top);
                         m[x][y] = top;
                         l[x][y] *= keep[x][y];
-                        keep[x][y] *= vkeep;
+                        if (INT8) {
+                            // `same`: the exponent that leaves the output sums as they are
+                            float &power = up[x][y];
+                            const float same = (float)((int)(__float_as_uint(power) >> 23) - 127) + (top - was);
+                            const float now = fmaxf(fminf(same, fminf(kUp - ceilf(product - top), kFar)), -100.0f);
+                            keep[x][y] = now == same ? 1.0f : ex2(now - same);
+                            power = __uint_as_float((uint32_t)((int)now + 127) << 23);
+                            limit = fminf(limit, __uint_as_float((uint32_t)(127 + (int)(kFull - kSlack) - (int)now) << 23));
+                        }
                     }
 #pragma unroll
                 for (int j = 0; j < MT; ++j)
@@ -759,19 +809,21 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
                         o[j][x][2] *= keep[x][0];
                         o[j][x][3] *= keep[x][1];
                     }
+                write_powers();
+                __syncwarp();
             }
-            vs0 *= vinv;
-            vs1 *= vinv;
+            read_powers();
             uint32_t hi[NB][2], lo[NB][2];     // P^T as the second operand: tokens 2t, 2t + 1 (+ 8) of query row g
 #pragma unroll
             for (int x = 0; x < NB; ++x) {
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
-                    const float zero = m[x][y] == -INFINITY ? 0.0f : m[x][y];   // nothing seen so far: every weight is 0
+                    // nothing seen so far: every weight is 0
+                    const float zero = !INT8 && m[x][y] == -INFINITY ? 0.0f : m[x][y];
                     const float w0 = ex2(sc[x][y] - zero), w1 = ex2(sc[x][2 + y] - zero);
                     l[x][y] += w0 + w1;
-                    sc[x][y] = INT8 ? w0 * vs0 : w0;
-                    sc[x][2 + y] = INT8 ? w1 * vs1 : w1;
+                    sc[x][y] = INT8 ? w0 * vs0 * up[x][y] : w0;
+                    sc[x][2 + y] = INT8 ? w1 * vs1 * up[x][y] : w1;
                 }
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
@@ -840,8 +892,9 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
             // ---- the end of the sequence, or of the run ----------------------------------------------------
             if (mask & (kLast | kStop)) {
                 __syncwarp();
+                read_powers();
                 const uint4 info = state[warp];
-                const int u = (int)info.z, h = p.blocks == 1 ? u : u / p.blocks, blk = u - h * p.blocks;
+                const int unit = (int)info.z, h = p.blocks == 1 ? unit : unit / p.blocks, blk = unit - h * p.blocks;
                 const int rows = min(p.group - blk * 16, p.rows);
                 const int64_t head0 = (int64_t)info.y * a.Hq + h * p.group + blk * 16;
 #pragma unroll
@@ -853,13 +906,14 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
                             l[x][y] += __shfl_xor_sync(0xffffffffu, l[x][y], off);
                 const bool final = (mask & kLast) && whole;
                 float *part = p.parts + ((size_t)info.w * 2 + (whole ? 1 : 0)) * part_size;
-                const float f = INT8 ? vf * (1.0f / (1 << kUp)) : 1.0f;
 #pragma unroll
                 for (int x = 0; x < NB; ++x) {
                     float inv[2];
 #pragma unroll
-                    for (int y = 0; y < 2; ++y)
+                    for (int y = 0; y < 2; ++y) {
+                        const float f = INT8 ? __uint_as_float(0x7F000000u - __float_as_uint(up[x][y])) : 1.0f;   // 1 / up
                         inv[y] = final ? (l[x][y] == 0.0f ? 0.0f : f / l[x][y]) : f;
+                    }
 #pragma unroll
                     for (int j = 0; j < MT; ++j) {
                         // columns of the tile's rows g and g + 8
