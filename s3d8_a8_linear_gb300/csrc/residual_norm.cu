@@ -734,12 +734,14 @@ __global__ __launch_bounds__(kRowsThreads) void residual_norm_backward_rows_kern
 #pragma unroll
         for (int i = 0; i < 6; ++i)
             s[i] = group_sum<GS>(s[i]);
-        const RowGrad q = grad_factors(a, inv_d, s[0], s[1], s[2], s[3], s[4], s[5]);
+        RowGrad q = grad_factors(a, inv_d, s[0], s[1], s[2], s[3], s[4], s[5]);
+        if (m >= a.M)     // no row: nothing for the columns' sums, not even 0 times an infinite root (eps = 0)
+            q.r = q.ch = q.rp = q.cy = 0.0f;
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
             const int c = lane + i * GS;
             uint4 dh, dy;
-            grad_chunk(hv[i], yv[i], xv[i], gv[i], w[i], f[i], q, P[i], S[i], dh, dy);   // zeros where there is no row
+            grad_chunk(hv[i], yv[i], xv[i], gv[i], w[i], f[i], q, P[i], S[i], dh, dy);
             if (m < a.M && c < chunks) {
                 reinterpret_cast<uint4 *>(g.dh_in)[base + c] = dh;
                 if (a.y)

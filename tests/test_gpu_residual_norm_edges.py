@@ -1,0 +1,41 @@
+"""Residual norms at the ends of their range, against the formulas in 64 bits (those of
+test_gpu_residual_norm, with its tolerances: 2^-8 of a bf16 output and 2^-18 of its
+summands' size; (summands + 40) 2^-24 of a column sum's)."""
+import numpy as np
+import pytest
+import torch
+
+import s3d8_a8_linear_gb300 as s3d8
+import test_gpu_residual_norm as norm
+from gpu_util import dev
+from test_gpu_residual_norm import BF, _f, _inputs, _lib, _rand  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def _check_backward(i, dh, dx, eps, monkeypatch):
+    monkeypatch.setattr(norm, "EPS", eps)
+    got = s3d8.residual_norm_backward(dh, dx, **i, eps=eps)
+    ref = norm._gradients(i, _f(dh), _f(dx), 1.0, False)
+    h, y, wo, wp = (_f(i[k]) for k in ("h", "y", "w_post", "w_pre"))
+    inv = 1 / np.sqrt((h * h).mean(-1, keepdims=True) + eps)
+    a = np.abs(_f(dx) * wp)
+    size = np.abs(_f(dh)) + inv * (a + np.abs(h) * inv * (a * np.abs(h) * inv).mean(-1, keepdims=True))
+    rp = 1 / np.sqrt((y * y).mean(-1, keepdims=True) + eps)
+    b = size * np.abs(wo)
+    sizes = {"dh": size, "dy": rp * (b + np.abs(y) * rp * (b * np.abs(y) * rp).mean(-1, keepdims=True))}
+    for k, t in got.items():
+        if k in sizes:
+            norm._close(_f(t), ref[k], tol=2.0 ** -18 * sizes[k])
+        else:
+            tol = (min(h.shape[0], 4096) + 40) * 2.0 ** -24 * ref["abs_" + k]
+            assert (np.abs(t.double().cpu().numpy() - ref[k]) <= tol).all(), k
+
+
+@pytest.mark.parametrize("M", [1, 5, 33, 700])
+@pytest.mark.parametrize("D", [16, 64, 128, 256, 512, 1024, 4096, 8200])
+def test_backward_without_epsilon(M, D, monkeypatch):
+    """eps = 0: a group of lanes that has no row must add nothing to the columns' sums."""
+    i = _inputs(M, D, True, "none", M + D)
+    rng = np.random.default_rng(D)
+    _check_backward(i, _rand(rng, M, D), _rand(rng, M, D), 0.0, monkeypatch)
