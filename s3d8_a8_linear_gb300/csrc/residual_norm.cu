@@ -633,11 +633,12 @@ __device__ __forceinline__ void fold_sums(const f2 (&s)[6], float (&v)[8])
 __device__ __forceinline__ RowGrad grad_factors(const NormArgs &a, float inv_d, float hh, float ah, float yy, float yg, float ya,
                                                 float yh)
 {
+    // the cubes of the roots from the mean outwards: alone they would pass fp32's range for rows below 1e-13
     RowGrad q;
     q.r = rsqrtf(hh * inv_d + a.eps);
-    q.ch = q.r * q.r * q.r * (ah * inv_d);
+    q.ch = q.r * (q.r * (q.r * (ah * inv_d)));
     q.rp = a.w_post ? rsqrtf(yy * inv_d + a.eps) : 1.0f;
-    q.cy = a.w_post ? q.rp * q.rp * q.rp * ((yg + q.r * ya - q.ch * yh) * inv_d) : 0.0f;
+    q.cy = a.w_post ? q.rp * (q.rp * (q.rp * ((yg + q.r * ya - q.ch * yh) * inv_d))) : 0.0f;
     return q;
 }
 

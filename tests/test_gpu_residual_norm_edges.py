@@ -39,3 +39,14 @@ def test_backward_without_epsilon(M, D, monkeypatch):
     i = _inputs(M, D, True, "none", M + D)
     rng = np.random.default_rng(D)
     _check_backward(i, _rand(rng, M, D), _rand(rng, M, D), 0.0, monkeypatch)
+
+
+@pytest.mark.parametrize("size", [1e-14, 1e-17])
+@pytest.mark.parametrize("which", ["h", "y"])
+@pytest.mark.parametrize("M,D", [(40, 64), (7, 512), (9, 1024), (5, 4096), (3, 8200)])
+def test_backward_of_tiny_rows(M, D, which, size, monkeypatch):
+    """Roots whose cube passes fp32's range, though no gradient does."""
+    i = _inputs(M, D, True, "none", M + D)
+    i[which] = (i[which].float() * size).to(BF)
+    rng = np.random.default_rng(D)
+    _check_backward(i, _rand(rng, M, D), _rand(rng, M, D), 0.0, monkeypatch)
