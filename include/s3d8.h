@@ -280,6 +280,8 @@ int s3d8_linear_batch(const s3d8_linear_job *jobs, int count, int64_t M, void *s
  *   x  = h' * rsqrt(mean(h'^2) + eps) * w_pre
  * per row of D columns, in fp32 from bf16 inputs; x is normalised from h' as it
  * is stored, so that it equals the norm of the stream that later layers read.
+ * Sums of squares are fp32: a row whose sum passes 3.4e38 has a root of 0, so that
+ * its normalised values are zeros (the update u, or x and its codes).
  *   h       : [M, D] bfloat16, the residual stream
  *   y       : [M, D] bfloat16, the block's output, or NULL (then h' = h, and
  *             h_out must be NULL: a norm alone)

@@ -50,3 +50,22 @@ def test_backward_of_tiny_rows(M, D, which, size, monkeypatch):
     i[which] = (i[which].float() * size).to(BF)
     rng = np.random.default_rng(D)
     _check_backward(i, _rand(rng, M, D), _rand(rng, M, D), 0.0, monkeypatch)
+
+
+@pytest.mark.parametrize("M,D", [(2, 64), (5, 512), (3, 1024), (3, 4096), (400, 2048), (310, 8192), (3, 16384)])
+def test_rows_whose_squares_pass_the_range_become_zeros(M, D):
+    """Sums of squares are fp32: past 3.4e38 the root is 0, as the header says, and no other row is touched."""
+    i = _inputs(M, D, True, "none", D)
+    plain = [t.clone() for t in s3d8.residual_norm(**i)] + [t.clone() for t in s3d8.residual_norm_quant(**i)[1:]]
+    i["y"][1] = 1e19
+    h, x = s3d8.residual_norm(**i)
+    _, q, s = s3d8.residual_norm_quant(**i)
+    assert torch.equal(h[1], i["h"][1])                     # the update is 0, the stream stays
+    norm._close(_f(x[1:2]), norm._norm(_f(i["h"][1:2]), _f(i["w_pre"])))
+    i["h"][1] = -3e19
+    h, x = s3d8.residual_norm(**i)
+    _, q, s = s3d8.residual_norm_quant(**i)
+    assert torch.equal(h[1], i["h"][1]) and bool((x[1] == 0).all()) and bool((q[1] == 0).all()) and float(s[1]) == 0.0
+    keep = [m for m in range(M) if m != 1]
+    for got, want in zip((h, x, q, s), plain):
+        assert torch.equal(got[keep], want[keep])
