@@ -196,7 +196,8 @@ def residual_norm_backward(dh: torch.Tensor | None, dx: torch.Tensor | None, h: 
 
 class ResidualNorm(torch.autograd.Function):
     """residual_norm with its gradients: apply(h, y, w_post, gate, w_pre, alpha,
-    eps, tanh_gate) -> (h', x).  Weight gradients come in the weights' bf16."""
+    eps, tanh_gate) -> (h', x).  Weight gradients come in the weights' bf16; a
+    second derivative through it raises."""
 
     @staticmethod
     def forward(ctx, h, y, w_post, gate, w_pre, alpha=1.0, eps=1e-5, tanh_gate=False):
@@ -207,6 +208,7 @@ class ResidualNorm(torch.autograd.Function):
         return (h_out.view_as(h_out) if y is None else h_out), x
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, dh, dx):
         h, y, w_post, gate, w_pre = ctx.saved_tensors
         if dh is None and dx is None:

@@ -69,3 +69,13 @@ def test_rows_whose_squares_pass_the_range_become_zeros(M, D):
     keep = [m for m in range(M) if m != 1]
     for got, want in zip((h, x, q, s), plain):
         assert torch.equal(got[keep], want[keep])
+
+
+def test_a_second_derivative_is_refused():
+    """The gradients are kernels without a graph: a loss that differentiates through them raises instead of losing terms."""
+    i = _inputs(3, 64, True, "scalar", 1)
+    leaf = {k: t.clone().requires_grad_() for k, t in i.items()}
+    _, x = s3d8.ResidualNorm.apply(leaf["h"], leaf["y"], leaf["w_post"], leaf["gate"], leaf["w_pre"], 1.0, 1e-5, True)
+    (first,) = torch.autograd.grad(x.float().square().sum(), leaf["h"], create_graph=True)
+    with pytest.raises(RuntimeError, match="twice"):
+        (first.float().square().sum() + leaf["h"].float().square().sum()).backward()
