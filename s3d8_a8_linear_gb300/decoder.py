@@ -69,9 +69,12 @@ def _rows(t, name, dtype):
     *lead, last = t.stride()
     if last != 1 and t.shape[-1] != 1:
         raise ValueError(f"{name} must have contiguous columns")
-    if 1 in t.shape:        # an axis of one element may have any stride
-        lead = [st if n > 1 else 0 for n, st in zip(t.shape, lead)]
-    return t.data_ptr(), lead
+    return t.data_ptr(), _strides(t.shape, lead)
+
+
+def _strides(shape, strides):
+    """The strides that matter: an axis of one element may have any (here 0)."""
+    return [st if n > 1 else 0 for n, st in zip(shape, strides)] if 1 in shape else list(strides)
 
 
 def _space(workspace, need, device):
@@ -244,13 +247,14 @@ class KVCache:
         s.v, vs = _rows(v, "v", k.dtype)
         s.k_stride[:], s.v_stride[:] = ks, vs
         if int8:
+            scales = _strides(k_scale.shape, k_scale.stride())
             for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-                if t.shape != k.shape[:3] or t.stride() != k_scale.stride():
+                if t.shape != k.shape[:3] or _strides(t.shape, t.stride()) != scales:
                     raise ValueError(f"{name} must be [pages, page_size, heads], and both laid out alike")
                 if not t.is_cuda or t.dtype != torch.float32:
                     raise TypeError(f"{name} must be a CUDA tensor of torch.float32")
             s.k_scale, s.v_scale = k_scale.data_ptr(), v_scale.data_ptr()
-            s.scale_stride[:] = [st if n > 1 else 0 for n, st in zip(k_scale.shape, k_scale.stride())]
+            s.scale_stride[:] = scales
         s.pages, s.page_size, s.heads, s.dim = k.shape
         s.dtype = KV_INT8 if int8 else KV_BF16
         if s.dim % 16 or not 16 <= s.dim <= 256:
