@@ -26,9 +26,9 @@
 // the parts of each such sequence, in order of position.
 //
 // Measured with 32 / 8 heads of 128, join included: 8 sequences of up to 131072 tokens
-// 533 us (6.8 TB/s), 64 of up to 8191 181 us (5.9 TB/s; 5 us until the first tiles
+// 531 to 547 us (6.6 to 6.8 TB/s), 64 of up to 8191 181 us (5.9 TB/s; 5 us until the first tiles
 // arrive, 5 to 10 from the last ones through the join), 48 int8 sequences with a window
-// 213 us (5.6 TB/s; 65% of the issue slots, a third of them turning codes into fp16).
+// 213 us (5.6 TB/s; 64% of the issue slots, a third of them turning codes into fp16).
 #pragma once
 
 #include <cfloat>

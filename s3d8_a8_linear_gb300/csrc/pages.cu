@@ -4,7 +4,7 @@
 // The bookkeeping (block table, lengths, reference counts) is a few hundred KB
 // at most and runs in one CTA, which needs no ordering between CTAs; the page
 // copies that follow read their list from the workspace and use the whole GPU.
-// Measured: growth of 16 sequences 4 us, a fork of 16 in 40 layers 13 us (its copies
+// Measured: growth of 16 sequences 4 us, a fork of 16 in 40 layers 14 us (its copies
 // move 40 MB), compaction of 250 pages in 40 layers 206 us (6.4 TB/s).
 #include "common.cuh"
 #include "launch.h"
@@ -411,8 +411,8 @@ cudaError_t launch_copy_pages(const PoolArgs &p, const int32_t *src, const int32
 {
     if (n == 0)
         return cudaSuccess;
-    // Few pages: four loads a thread, so that more CTAs fit (16 pages of 40 layers: 13 us against 16; a fork of 16 sequences
-    // 15 against 17); many: eight.
+    // Few pages: four loads a thread, so that more CTAs fit (16 pages of 40 layers: 13 us against 16); many:
+    // eight.
     const int64_t jobs = (int64_t)n * p.layers * 2, sms = device_sm_count();
     const bool many = jobs > 32 * sms;
     return tc::launch_pdl(many ? copy_pages_kernel<8> : copy_pages_kernel<4>, dim3((unsigned)(jobs < 16 * sms ? jobs : 16 * sms)),
