@@ -69,12 +69,12 @@ def _rows(t, name, dtype):
     *lead, last = t.stride()
     if last != 1 and t.shape[-1] != 1:
         raise ValueError(f"{name} must have contiguous columns")
-    return t.data_ptr(), _strides(t.shape, lead)
+    return t.data_ptr(), _strides(t.shape, lead) if 1 in t.shape else lead
 
 
 def _strides(shape, strides):
     """The strides that matter: an axis of one element may have any (here 0)."""
-    return [st if n > 1 else 0 for n, st in zip(shape, strides)] if 1 in shape else list(strides)
+    return [st if n > 1 else 0 for n, st in zip(shape, strides)]
 
 
 def _space(workspace, need, device):
