@@ -46,9 +46,9 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.0f;     // weights reach 2^8
 // int8 caches: what a value's code is multiplied with, its weight times its scale, is carried times a power of two of its
-// query row (2^kFar at most), which makes the row's largest product about 2^kUp when it is met and lets none pass 2^kFull:
-// inside fp16.  By the products, not by the scales: a large scale on a token of no weight must not push the others down.
-constexpr float kUp = 6.0f, kFull = 15.0f, kFar = 116.0f;
+// query row (2^-kLeast to 2^kFar), which makes the row's largest product about 2^kUp when it is met and lets none pass
+// 2^kFull: inside fp16.  By the products, not by the scales: a large scale on a token of no weight must not push the others down.
+constexpr float kUp = 6.0f, kFull = 15.0f, kFar = 116.0f, kLeast = 120.0f;
 
 template <int DP, bool INT8>
 struct Shape {
@@ -794,7 +794,7 @@ __global__ __launch_bounds__(WARPS * 32, 1) void paged_attention_kernel(const __
                             // `same`: the exponent that leaves the output sums as they are
                             float &power = up[x][y];
                             const float same = (float)((int)(__float_as_uint(power) >> 23) - 127) + (top - was);
-                            const float now = fmaxf(fminf(same, fminf(kUp - ceilf(product - top), kFar)), -100.0f);
+                            const float now = fmaxf(fminf(same, fminf(kUp - ceilf(product - top), kFar)), -kLeast);
                             keep[x][y] = now == same ? 1.0f : ex2(now - same);
                             power = __uint_as_float((uint32_t)((int)now + 127) << 23);
                             limit = fminf(limit, __uint_as_float((uint32_t)(127 + (int)(kFull - kSlack) - (int)now) << 23));

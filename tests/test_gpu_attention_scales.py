@@ -106,6 +106,13 @@ def test_scales_at_both_ends_of_their_range():
     _check([5000] * 40, 2, 4, 64, 16, 0.05, late)
 
 
+def test_scales_next_to_the_largest_and_the_smallest():
+    """Value scales up to 2^117 and down to 2^-120: outputs that bf16 still holds."""
+    for factor in (4e36, 1e-34):
+        _check([40, 17], 2, 4, 128, 16, 0.05, lambda s, sc: sc * factor)
+        _check([40, 17], 2, 12, 64, 16, 0.05, lambda s, sc: sc * factor)
+
+
 def test_scales_that_grow_along_the_sequence():
     def grow(s, sc):
         return sc * 2.0 ** (np.arange(len(sc)) * (60.0 / len(sc)) - 30)[:, None]
