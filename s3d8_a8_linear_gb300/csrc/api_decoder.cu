@@ -242,11 +242,11 @@ int s3d8_residual_norm_backward(const void *dh_bf16, const void *dx_bf16, const 
     return cuda_status(launch_residual_norm_backward(g, s));
 }
 
-int s3d8_rope_append(const void *q_bf16, const int64_t q_stride[2], const void *k_bf16, const int64_t k_stride[2],
+int s3d8_norm_rope_append(const void *q_bf16, const int64_t q_stride[2], const void *k_bf16, const int64_t k_stride[2],
                      const void *v_bf16, const int64_t v_stride[2], const float *cos, const float *sin, int64_t max_pos,
                      int64_t rotary, int interleaved, const int32_t *positions, const int32_t *rows, int64_t T, int64_t Hq,
-                     const int32_t *table, int64_t table_rows, int64_t width, const s3d8_kv_cache *cache, void *q_out_bf16,
-                     void *stream)
+                     const int32_t *table, int64_t table_rows, int64_t width, const void *q_norm_bf16, const void *k_norm_bf16, float eps,
+                          const s3d8_kv_cache *cache, void *q_out_bf16, void *stream)
 {
     RopeArgs a;
     int st = check_cache(cache, &a.kv);
@@ -270,7 +270,8 @@ int s3d8_rope_append(const void *q_bf16, const int64_t q_stride[2], const void *
                 return S3D8_ERR_ALIGNMENT;
         }
     if (!aligned(q_bf16, 16) || !aligned(k_bf16, 16) || !aligned(v_bf16, 16) || !aligned(q_out_bf16, 16) ||
-        !aligned(cos, 4) || !aligned(sin, 4) || !aligned(positions, 4) || !aligned(rows, 4) || !aligned(table, 4))
+        !aligned(cos, 4) || !aligned(sin, 4) || !aligned(positions, 4) || !aligned(rows, 4) || !aligned(table, 4) ||
+        !aligned(q_norm_bf16, 16) || !aligned(k_norm_bf16, 16))
         return S3D8_ERR_ALIGNMENT;
     a.q = bf(q_bf16);
     a.k = bf(k_bf16);
@@ -293,10 +294,24 @@ int s3d8_rope_append(const void *q_bf16, const int64_t q_stride[2], const void *
     a.table_rows = table_rows;
     a.width = width;
     a.q_out = static_cast<__nv_bfloat16 *>(q_out_bf16);
+    a.q_norm = bf(q_norm_bf16);
+    a.k_norm = bf(k_norm_bf16);
+    a.eps = eps;
     a.status = device_status_ptr();
     if (!a.status)
         return S3D8_ERR_CUDA;
     return cuda_status(launch_rope_append(a, static_cast<cudaStream_t>(stream)));
+}
+
+int s3d8_rope_append(const void *q_bf16, const int64_t q_stride[2], const void *k_bf16, const int64_t k_stride[2],
+                     const void *v_bf16, const int64_t v_stride[2], const float *cos, const float *sin, int64_t max_pos,
+                     int64_t rotary, int interleaved, const int32_t *positions, const int32_t *rows, int64_t T, int64_t Hq,
+                     const int32_t *table, int64_t table_rows, int64_t width, const s3d8_kv_cache *cache, void *q_out_bf16,
+                     void *stream)
+{
+    return s3d8_norm_rope_append(q_bf16, q_stride, k_bf16, k_stride, v_bf16, v_stride, cos, sin, max_pos, rotary, interleaved,
+                                 positions, rows, T, Hq, table, table_rows, width, nullptr, nullptr, 0.0f, cache, q_out_bf16,
+                                 stream);
 }
 
 size_t s3d8_paged_attention_workspace_size(const s3d8_kv_cache *cache, int64_t B, int64_t Hq)

@@ -139,6 +139,8 @@ struct RopeArgs {
     KvCache kv;
     __nv_bfloat16 *q_out;
     int *status;
+    const __nv_bfloat16 *q_norm, *k_norm;   // [dim], or null: as they are
+    float eps;
 };
 cudaError_t launch_rope_append(const RopeArgs &a, cudaStream_t stream);
 
@@ -188,5 +190,60 @@ struct PagePairs {
 cudaError_t launch_fork_pages(const PagesArgs &a, PagePairs *pairs, cudaStream_t stream);
 cudaError_t launch_free_pages(const PagesArgs &a, cudaStream_t stream);
 cudaError_t launch_compact_pages(const PagesArgs &a, PagePairs *pairs, cudaStream_t stream);
+
+// ---- a vision decoder's calls (norm_rope.cu, cross_attention.cu, sample.cu)
+struct NormRopeArgs {
+    const __nv_bfloat16 *x[2];          // queries and keys; the keys may have no heads
+    int64_t xs[2][2];                   // token, head
+    const __nv_bfloat16 *w[2];          // [dim], or null: not normed
+    int heads[2];
+    const float *cos, *sin;
+    int64_t max_pos;
+    int rotary, interleaved;
+    const int32_t *positions;           // or null: token t at t
+    int64_t T;
+    int dim;
+    float eps;
+    __nv_bfloat16 *out[2];              // z, or dx
+    const __nv_bfloat16 *dz[2];         // backward only
+    int64_t dzs[2][2];
+    float *dw[2], *part;                // part: [CTAs][2 dim]
+    int *status;
+};
+cudaError_t launch_norm_rope(const NormRopeArgs &a, cudaStream_t stream);
+size_t norm_rope_backward_workspace(int64_t T, int heads, int dim);
+cudaError_t launch_norm_rope_backward(const NormRopeArgs &a, cudaStream_t stream);
+
+struct CrossArgs {
+    const __nv_bfloat16 *q, *k, *v;
+    int64_t qs[2], ks[2], vs[2];        // token, head
+    const int32_t *spans;               // [T, 2], or null: every state
+    int T, S, Hq, heads, dim;
+    float scale;
+    __nv_bfloat16 *out;
+    float *lse;
+    void *ws;
+    int *status;
+    // backward: out and lse are inputs
+    const __nv_bfloat16 *dout;
+    int64_t ds[2];
+    __nv_bfloat16 *dq, *dk, *dv;
+};
+size_t cross_attention_workspace(int64_t T, int64_t S, int64_t Hq, int64_t heads, int64_t dim);
+cudaError_t launch_cross_attention(const CrossArgs &a, cudaStream_t stream);
+size_t cross_attention_backward_workspace(int64_t T, int64_t S, int64_t Hq, int64_t heads, int64_t dim);
+cudaError_t launch_cross_attention_backward(const CrossArgs &a, cudaStream_t stream);
+
+struct SampleArgs {
+    const __nv_bfloat16 *logits;        // [B, V], rows `stride` elements apart
+    int64_t stride;
+    int B, V;
+    const float *u, *temperature, *top_p, *min_p;   // [B]; all but u may be null
+    const int32_t *top_k;
+    int32_t *tokens;
+    float *logprob;                     // or null
+    int *status;
+};
+cudaError_t launch_sample(const SampleArgs &a, cudaStream_t stream);
 
 }  // namespace s3d8

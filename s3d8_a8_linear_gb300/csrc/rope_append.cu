@@ -13,6 +13,7 @@
 #include "bf16x8.cuh"
 #include "common.cuh"
 #include "launch.h"
+#include "rope_lane.cuh"
 #include "rope_plan.h"
 #include "tcgen05.cuh"
 
@@ -43,54 +44,6 @@ __device__ __forceinline__ uint2 codes8(const float (&x)[8], float s, float r)
     }
     return make_uint2(prmt(prmt(b[0], b[1], 0x0040), prmt(b[2], b[3], 0x0040), 0x5410),
                       prmt(prmt(b[4], b[5], 0x0040), prmt(b[6], b[7], 0x0040), 0x5410));
-}
-
-// Which two chunks a lane holds, and where the partners of its columns are.
-enum RopeMode {
-    kHalves,        // pairs (i, i + rotary/2), rotary a multiple of 16: both in one lane
-    kNeighbours,    // pairs (2i, 2i + 1): two neighbouring chunks
-    kHalvesOdd      // any other rotary: neighbouring chunks, partners read one by one
-};
-
-// A lane's part of every row: two chunks, and whether its pairs 8 lane .. 8 lane + 7 turn.
-struct RopeLane {
-    int lane, lanes, half, chunk[2];
-    bool in_row, turns;
-
-    __device__ __forceinline__ RopeLane(const RopeArgs &a, int mode, int log_lanes)
-        : lane((int)threadIdx.x & ((1 << log_lanes) - 1)), lanes(1 << log_lanes), half(a.rotary / 2)
-    {
-        chunk[0] = 2 * lane;
-        chunk[1] = 2 * lane + 1;
-        if (mode == kHalves && lane < a.rotary / 16) {
-            chunk[0] = lane;
-            chunk[1] = lane + a.rotary / 16;
-        }
-        in_row = 16 * lane < a.kv.dim;
-        turns = in_row && 8 * lane < half;
-    }
-};
-
-template <int MODE>
-__device__ __forceinline__ void turn(const RopeLane &l, float (&f)[2][8], const float (&cs)[8], const float (&sn)[8])
-{
-    if (MODE == kHalves) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float u = f[0][e], w = f[1][e];
-            f[0][e] = u * cs[e] - w * sn[e];
-            f[1][e] = w * cs[e] + u * sn[e];
-        }
-    } else if (MODE == kNeighbours) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {     // pair 8 lane + e: chunk e / 4, columns 2 (e % 4), + 1
-            if (8 * l.lane + e >= l.half)
-                continue;
-            const float u = f[e / 4][2 * (e % 4)], w = f[e / 4][2 * (e % 4) + 1];
-            f[e / 4][2 * (e % 4)] = u * cs[e] - w * sn[e];
-            f[e / 4][2 * (e % 4) + 1] = w * cs[e] + u * sn[e];
-        }
-    }
 }
 
 // Writes a row: q as it is, keys and values into their page (page < 0: nowhere).
@@ -136,6 +89,48 @@ __device__ __forceinline__ void put_row(const RopeArgs &a, const RopeLane &l, in
         (kind == 1 ? a.kv.k_scale : a.kv.v_scale)[page * a.kv.ss[0] + slot * a.kv.ss[1] + h * a.kv.ss[2]] = s;
 }
 
+// A lane's columns of the two norms' weights, in bf16 (absent: not normed).
+struct RowNorm {
+    uint4 w[2][2];
+};
+
+__device__ __forceinline__ RowNorm row_norm(const RopeArgs &a, const RopeLane &l)
+{
+    RowNorm n;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+            const __nv_bfloat16 *w = i ? a.k_norm : a.q_norm;
+            n.w[i][y] = w && l.in_row ? __ldg(reinterpret_cast<const uint4 *>(w) + l.chunk[y]) : make_uint4(0u, 0u, 0u, 0u);
+        }
+    return n;
+}
+
+// x -> x rsqrt(mean x^2 + eps) w on a query or key row of a token (`ok`; a padding token's
+// zeros stay); returns the root.  Whole warps together (shuffles); the sum of squares is
+// fp32, as the rest.
+__device__ __forceinline__ float norm_row(const RopeArgs &a, const RopeLane &l, int head, bool ok, const RowNorm &n, float (&f)[2][8])
+{
+    float sum = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        sum = fmaf(f[0][e], f[0][e], fmaf(f[1][e], f[1][e], sum));
+    sum = l.in_row ? sum : 0.0f;
+    const float r = rsqrtf(row_sum(sum, l.lanes) / (float)a.kv.dim + a.eps);
+    if (!ok || head >= a.Hq + a.kv.heads || !(head < a.Hq ? a.q_norm : a.k_norm))
+        return 1.0f;
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+        float w[8];
+        unpack8(head < a.Hq ? n.w[0][y] : n.w[1][y], w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            f[y][e] = f[y][e] * r * w[e];
+    }
+    return r;
+}
+
 // Where token t goes: whether it is a token with an angle, and its page (-1: nowhere)
 // and slot.  What is out of range is recorded once, by `one` thread.
 __device__ __forceinline__ bool place(const RopeArgs &a, int pos, int64_t row, bool one, int &page, int &slot)
@@ -161,14 +156,14 @@ __device__ __forceinline__ bool place(const RopeArgs &a, int pos, int64_t row, b
 }
 
 // ROWS: rows of a lane whose loads leave together.
-template <int MODE, bool INT8, int ROWS>
+template <int MODE, bool INT8, bool NORM, int ROWS>
 __global__ __launch_bounds__(kRopeThreads, 3) void rope_append_kernel(const __grid_constant__ RopeArgs a, int log_lanes, int vec)
 {
     tc::pdl_launch_dependents();
     tc::pdl_wait();
     const int heads = a.Hq + 2 * a.kv.heads, slots = blockDim.x >> log_lanes;
     const int64_t t = blockIdx.x;
-    const RopeLane l(a, MODE, log_lanes);
+    const RopeLane l(a.rotary, a.kv.dim, MODE, log_lanes);
 
     // the rows do not depend on where the token stands: their loads leave first
     uint4 raw[ROWS][2];
@@ -187,27 +182,16 @@ __global__ __launch_bounds__(kRopeThreads, 3) void rope_append_kernel(const __gr
         }
     };
     load_rows(0);
+    RowNorm norm;
+    if (NORM)
+        norm = row_norm(a, l);
     const int pos = a.positions[t];
     int page, slot;
     const bool ok = place(a, pos, a.rows ? a.rows[t] : t, threadIdx.x == 0, page, slot);
     float cs[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f}, sn[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
     if (ok && l.turns && MODE != kHalvesOdd) {
         const float *c = a.cos + (int64_t)pos * l.half + 8 * l.lane, *s = a.sin + (int64_t)pos * l.half + 8 * l.lane;
-        if (vec) {
-#pragma unroll
-            for (int e = 0; e < 8; e += 4) {
-                const float4 u = __ldg(reinterpret_cast<const float4 *>(c + e)), w = __ldg(reinterpret_cast<const float4 *>(s + e));
-                cs[e] = u.x, cs[e + 1] = u.y, cs[e + 2] = u.z, cs[e + 3] = u.w;
-                sn[e] = w.x, sn[e + 1] = w.y, sn[e + 2] = w.z, sn[e + 3] = w.w;
-            }
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (8 * l.lane + e < l.half) {
-                    cs[e] = __ldg(c + e);
-                    sn[e] = __ldg(s + e);
-                }
-        }
+        load_angles(l, c, s, vec, cs, sn);
     }
 
     for (int base = 0; base < heads; base += slots * ROWS) {   // whole warps together: there are shuffles below
@@ -222,19 +206,24 @@ __global__ __launch_bounds__(kRopeThreads, 3) void rope_append_kernel(const __gr
             const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
             unpack8(ok ? raw[i][0] : zero, f[0]);
             unpack8(ok ? raw[i][1] : zero, f[1]);
+            float root = 1.0f;
+            if (NORM)
+                root = norm_row(a, l, head, ok, norm, f);
             if (keyed && l.turns)
                 turn<MODE>(l, f, cs, sn);
             if (MODE == kHalvesOdd && keyed && live && ok) {
                 const __nv_bfloat16 *x = head < a.Hq ? a.q + t * a.qs[0] + head * a.qs[1]
                                                      : a.k + t * a.ks[0] + (head - a.Hq) * a.ks[1];
                 const float *c = a.cos + (int64_t)pos * l.half, *s = a.sin + (int64_t)pos * l.half;
+                const __nv_bfloat16 *w = NORM ? head < a.Hq ? a.q_norm : a.k_norm : nullptr;
+                auto partner = [&](int d) {
+                    const float v = __bfloat162float(x[d]);
+                    return w ? v * root * __bfloat162float(w[d]) : v;
+                };
                 for (int e = 0; e < 16; ++e) {
                     const int d = 16 * l.lane + e;
-                    float &v = f[e / 8][e % 8];
-                    if (d < l.half)
-                        v = v * c[d] - __bfloat162float(x[d + l.half]) * s[d];
-                    else if (d < a.rotary)
-                        v = v * c[d - l.half] + __bfloat162float(x[d - l.half]) * s[d - l.half];
+                    if (d < a.rotary)
+                        f[e / 8][e % 8] = turn_odd(d, l.half, f[e / 8][e % 8], c, s, partner);
                 }
             }
             put_row<INT8>(a, l, t, head, live, page, slot, f);
@@ -248,7 +237,7 @@ __global__ __launch_bounds__(kRopeThreads, 3) void rope_append_kernel(const __gr
 // turn and store.  Many small CTAs, as the turning and the stores want warps:
 // 16384 tokens of 48 heads of 128 take 78 us with two CTAs an SM of eight stages,
 // 77 with three of five, 73 with five of three (int8: 102, 92, 70).
-template <int MODE, bool INT8>
+template <int MODE, bool INT8, bool NORM>
 __global__ __launch_bounds__(kRopeThreads + 32, 3) void rope_append_ring_kernel(const __grid_constant__ RopeArgs a, int log_lanes,
                                                                               int stages, int stage_bytes)
 {
@@ -321,8 +310,11 @@ __global__ __launch_bounds__(kRopeThreads + 32, 3) void rope_append_ring_kernel(
             if (!mbar_wait_bounded(full + 8 * (k % stages), (k / stages) & 1))
                 timed_out = true;
     } else {
-        const RopeLane l(a, MODE, log_lanes);
+        const RopeLane l(a.rotary, a.kv.dim, MODE, log_lanes);
         const int slots = (consumers * 32) >> log_lanes;
+        RowNorm norm;
+        if (NORM)
+            norm = row_norm(a, l);
         for (int i = 0; i < n; ++i) {
             const int s = i % stages;
             if (!tc::warp_wait(full + 8 * s, (i / stages) & 1)) {
@@ -348,6 +340,8 @@ __global__ __launch_bounds__(kRopeThreads + 32, 3) void rope_append_ring_kernel(
                 float f[2][8];
                 unpack8(live && m.x ? lds_v4(from + head * row_bytes + 16 * l.chunk[0]) : zero, f[0]);
                 unpack8(live && m.x ? lds_v4(from + head * row_bytes + 16 * l.chunk[1]) : zero, f[1]);
+                if (NORM)
+                    norm_row(a, l, head, m.x, norm, f);
                 if (head < a.Hq + a.kv.heads && l.turns)
                     turn<MODE>(l, f, cs, sn);
                 put_row<INT8>(a, l, t, head, live, m.y, m.z, f);
@@ -361,7 +355,7 @@ __global__ __launch_bounds__(kRopeThreads + 32, 3) void rope_append_ring_kernel(
         record_timeout(a.status);
 }
 
-template <int MODE, bool INT8>
+template <int MODE, bool INT8, bool NORM>
 cudaError_t launch_mode(const RopeArgs &a, cudaStream_t stream)
 {
     int log_lanes = 0;
@@ -380,7 +374,7 @@ cudaError_t launch_mode(const RopeArgs &a, cudaStream_t stream)
         // against 27; of 12 heads of 256: 48 against 58).
         if (rows == 4 && vec && whole && ring.stages && (!INT8 || ring.stage >= 4096)) {
             const int64_t grid = (int64_t)device_sm_count() * ring.ctas;
-            auto kernel = rope_append_ring_kernel<MODE, INT8>;
+            auto kernel = rope_append_ring_kernel<MODE, INT8, NORM>;
             static std::atomic<unsigned long long> allowed;
             const cudaError_t e = tc::allow_smem(kernel, kRingBytes, allowed);
             return e != cudaSuccess ? e
@@ -390,14 +384,16 @@ cudaError_t launch_mode(const RopeArgs &a, cudaStream_t stream)
     }
     int threads = (((heads + rows - 1) / rows << log_lanes) + 31) / 32 * 32;
     threads = threads < kRopeThreads ? threads : kRopeThreads;
-    return tc::launch_pdl(rows == 2 ? rope_append_kernel<MODE, INT8, 2> : rope_append_kernel<MODE, INT8, 4>,
+    return tc::launch_pdl(rows == 2 ? rope_append_kernel<MODE, INT8, NORM, 2> : rope_append_kernel<MODE, INT8, NORM, 4>,
                           dim3((unsigned)a.T), dim3(threads), 0, stream, a, log_lanes, vec);
 }
 
 template <int MODE>
 cudaError_t launch_type(const RopeArgs &a, cudaStream_t stream)
 {
-    return a.kv.int8 ? launch_mode<MODE, true>(a, stream) : launch_mode<MODE, false>(a, stream);
+    if (a.q_norm || a.k_norm)
+        return a.kv.int8 ? launch_mode<MODE, true, true>(a, stream) : launch_mode<MODE, false, true>(a, stream);
+    return a.kv.int8 ? launch_mode<MODE, true, false>(a, stream) : launch_mode<MODE, false, false>(a, stream);
 }
 
 }  // namespace
