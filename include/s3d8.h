@@ -380,6 +380,21 @@ int s3d8_rope_append(const void *q_bf16, const int64_t q_stride[2], const void *
                      const s3d8_kv_cache *cache, void *q_out_bf16, void *stream);
 
 /*
+ * The same with norms of the query and key heads in the same pass: in front of the
+ * rotation, x -> x * rsqrt(mean(x^2) + eps) * w over the dim columns of each head of q
+ * (w = q_norm) and k (w = k_norm), in fp32.
+ *   q_norm, k_norm : [dim] bfloat16, 16-byte aligned, or NULL (not normed)
+ * Values and everything else as in s3d8_rope_append, which this is without norms.
+ */
+int s3d8_norm_rope_append(const void *q_bf16, const int64_t q_stride[2], const void *k_bf16,
+                          const int64_t k_stride[2], const void *v_bf16, const int64_t v_stride[2],
+                          const float *cos, const float *sin, int64_t max_pos, int64_t rotary,
+                          int interleaved, const int32_t *positions, const int32_t *rows, int64_t T,
+                          int64_t Hq, const int32_t *table, int64_t table_rows, int64_t width,
+                          const void *q_norm_bf16, const void *k_norm_bf16, float eps,
+                          const s3d8_kv_cache *cache, void *q_out_bf16, void *stream);
+
+/*
  * Attention of one new token per sequence over the paged cache:
  *   out[b, h] = sum_j softmax_j(scale * q[b, h] . k[j]) v[j]
  * over the last `window` (0: all) of the first lens[b] tokens of row b, query
@@ -447,6 +462,131 @@ int s3d8_free_pages(int32_t *table, int64_t rows, int64_t width, int32_t *lens, 
 int s3d8_compact_pages(const s3d8_kv_cache *layers, int64_t count, int32_t *table, int64_t rows,
                        int64_t width, int32_t *refs, int32_t *live, void *workspace,
                        size_t workspace_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * A vision decoder's calls: normed rotary heads as tensors, attention of text
+ * tokens to the encoder's states of their images, and the next token.
+ * ------------------------------------------------------------------------- */
+
+/*
+ * The norm of each query and key head with the rotation in the same pass, in fp32 from
+ * bf16 inputs, rounded once:
+ *   y = x * rsqrt(mean(x^2) + eps) * w over the dim columns of a head, z = R(position) y
+ * with R as in s3d8_rope_append: columns 0..rotary-1 turn in pairs (i, i + rotary/2), or
+ * (2i, 2i + 1) when `interleaved`.
+ *   q, k    : [T, Hq, dim] and [T, Hk, dim] bfloat16, strides (token, head) in elements;
+ *             Hk = 0: no keys (k NULL)
+ *   q_norm, k_norm : [dim] bfloat16, 16-byte aligned, or NULL (not normed)
+ *   cos, sin: [max_pos, rotary / 2] fp32 contiguous; rotary even, 0 (none) .. dim
+ *   positions : [T] int32, or NULL (token t at position t); a negative one marks a padding
+ *             token: its output rows (and gradients) are zero; so are those of a position
+ *             >= max_pos, which records S3D8_ERR_BOUNDS (with rotary > 0)
+ *   q_out, k_out : [T, Hq, dim], [T, Hk, dim] bfloat16 contiguous outputs, not overlapping
+ *             the inputs
+ * dim: a multiple of 16, 16..256.  Rows start on 16 bytes.
+ */
+int s3d8_norm_rope(const void *q_bf16, const int64_t q_stride[2], int64_t Hq, const void *k_bf16,
+                   const int64_t k_stride[2], int64_t Hk, const void *q_norm_bf16,
+                   const void *k_norm_bf16, const float *cos, const float *sin, int64_t max_pos,
+                   int64_t rotary, int interleaved, const int32_t *positions, int64_t T, int64_t dim,
+                   float eps, void *q_out_bf16, void *k_out_bf16, void *stream);
+
+/*
+ * Its gradients, from those of q_out and k_out and the forward call's inputs.  With
+ * dy = R^T dz, a = dy * w and r the reciprocal root:
+ *   dx = r a - x r^3 mean(a x)     (dy without a norm),     dw = sum over rows of dy x r
+ *   dq, dk  : [T, Hq, dim], [T, Hk, dim] bfloat16, strides (token, head)
+ *   dq_in, dk_in : contiguous bfloat16 outputs, not overlapping the inputs
+ *   dq_norm, dk_norm : [dim] fp32 outputs, required with their weight
+ *   workspace : s3d8_norm_rope_backward_workspace_size(T, Hq, Hk, dim) bytes, 16-byte
+ *             aligned, not shared by calls that overlap on the GPU
+ * The sums over rows run in a fixed order: equal inputs give equal bits.
+ */
+size_t s3d8_norm_rope_backward_workspace_size(int64_t T, int64_t Hq, int64_t Hk, int64_t dim);
+int s3d8_norm_rope_backward(const void *dq_bf16, const int64_t dq_stride[2], const void *dk_bf16,
+                            const int64_t dk_stride[2], const void *q_bf16, const int64_t q_stride[2],
+                            int64_t Hq, const void *k_bf16, const int64_t k_stride[2], int64_t Hk,
+                            const void *q_norm_bf16, const void *k_norm_bf16, const float *cos,
+                            const float *sin, int64_t max_pos, int64_t rotary, int interleaved,
+                            const int32_t *positions, int64_t T, int64_t dim, float eps,
+                            void *dq_in_bf16, void *dk_in_bf16, float *dq_norm, float *dk_norm,
+                            void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Attention of T text tokens to S states of an encoder, each token over a span of them:
+ *   out[t, h] = sum_j softmax_j(scale * q[t, h] . k[j, g]) v[j, g],
+ *   spans[t][0] <= j < spans[t][1], g = h / (Hq / heads)
+ * The tokens and states of a whole batch stand one behind the other: a token's span names
+ * the states of its own image.
+ *   q       : [T, Hq, dim] bfloat16, strides (token, head) in elements
+ *   k, v    : [S, heads, dim] bfloat16, strides likewise
+ *   spans   : [T, 2] int32, 8-byte aligned, or NULL (every token sees every state).  An
+ *             empty span (end <= begin) gives zeros and lse = -inf; one that leaves the
+ *             states is cut to them and records S3D8_ERR_BOUNDS
+ *   out     : [T, Hq, dim] bfloat16 contiguous output, 16-byte aligned
+ *   lse     : [T, Hq] fp32 output log(sum_j exp(scale * q . k[j])), or NULL
+ *   workspace : s3d8_cross_attention_workspace_size(T, S, Hq, heads, dim) bytes, 16-byte
+ *             aligned, not shared by calls that overlap on the GPU
+ * dim: a multiple of 8, 8..S3D8_MAX_CROSS_DIM; Hq a multiple of heads, at most
+ * S3D8_MAX_CROSS_GROUP times as many.  Rows start on 16 bytes.  A state that a token does
+ * not see has no part in the token's output, whatever it holds.
+ */
+#define S3D8_MAX_CROSS_DIM 128
+#define S3D8_MAX_CROSS_GROUP 128
+size_t s3d8_cross_attention_workspace_size(int64_t T, int64_t S, int64_t Hq, int64_t heads, int64_t dim);
+int s3d8_cross_attention(const void *q_bf16, const int64_t q_stride[2], const void *k_bf16,
+                         const int64_t k_stride[2], const void *v_bf16, const int64_t v_stride[2],
+                         const int32_t *spans, int64_t T, int64_t S, int64_t Hq, int64_t heads,
+                         int64_t dim, float scale, void *out_bf16, float *lse, void *workspace,
+                         size_t workspace_bytes, void *stream);
+
+/*
+ * Its gradients.  With p_j = exp(scale * q . k[j] - lse), delta = dout . out and
+ * ds_j = p_j (dout . v[j] - delta):
+ *   dq = scale * sum_j ds_j k[j],  dk[j] = scale * sum ds_j q,  dv[j] = sum p_j dout,
+ * the last two over the tokens that see state j and the query heads of its head.
+ *   dout    : [T, Hq, dim] bfloat16, strides (token, head)
+ *   q, k, v, spans, scale : as in the forward call; out, lse : as it wrote them
+ *   dq      : [T, Hq, dim]; dk, dv : [S, heads, dim] bfloat16 contiguous outputs, 16-byte
+ *             aligned
+ *   workspace : s3d8_cross_attention_backward_workspace_size(...) bytes, as above
+ * No atomics: equal inputs give equal bits.  A state that no token sees has zero gradients.
+ */
+size_t s3d8_cross_attention_backward_workspace_size(int64_t T, int64_t S, int64_t Hq, int64_t heads,
+                                                    int64_t dim);
+int s3d8_cross_attention_backward(const void *dout_bf16, const int64_t dout_stride[2],
+                                  const void *q_bf16, const int64_t q_stride[2], const void *k_bf16,
+                                  const int64_t k_stride[2], const void *v_bf16,
+                                  const int64_t v_stride[2], const void *out_bf16, const float *lse,
+                                  const int32_t *spans, int64_t T, int64_t S, int64_t Hq, int64_t heads,
+                                  int64_t dim, float scale, void *dq_bf16, void *dk_bf16, void *dv_bf16,
+                                  void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * The next token of each row from its logits and one uniform number.  A row's tokens stand
+ * in the order of their logits (equal ones by index), with weights exp((l - max) / T).
+ * Each limit keeps a beginning of that order, and the shortest holds:
+ *   top_k : the first k tokens (k <= 0: all)
+ *   top_p : the fewest first tokens that have a share >= p of the weight of the top_k
+ *           (p >= 1: all; p <= 0: one)
+ *   min_p : the tokens whose weight is >= min_p (of the largest, which is 1); at least one
+ * The token is the first whose weight, with that of all before it, exceeds u times the kept
+ * weight (the last kept one for u >= 1).  T <= 0: the largest logit, lowest index.
+ *   logits  : [B, V] bfloat16, rows logits_stride elements apart.  A logit of -inf or NaN is
+ *             never drawn
+ *   u       : [B] fp32, in [0, 1)
+ *   temperature, top_p, min_p : [B] fp32, or NULL (1, no limit, no limit); top_k : [B] int32
+ *             or NULL (no limit)
+ *   tokens  : [B] int32 output; -1 for a row that has no token to draw
+ *   logprob : [B] fp32 output, the log of the token's share of the kept weight (0 for
+ *             T <= 0, -inf for -1), or NULL
+ * Weights are whole numbers of 2^-45 of the largest one, so a token's share is right to 2^-45.
+ * V: 1..S3D8_MAX_SAMPLE_V.  Rows that start on 16 bytes are read faster.
+ */
+#define S3D8_MAX_SAMPLE_V 524224
+int s3d8_sample(const void *logits_bf16, int64_t logits_stride, int64_t B, int64_t V, const float *u,
+                const float *temperature, const int32_t *top_k, const float *top_p, const float *min_p,
+                int32_t *tokens, float *logprob, void *stream);
 
 /* Synchronises `stream`, then returns and clears the sticky device status word
  * (S3D8_OK, S3D8_ERR_TIMEOUT or S3D8_ERR_BOUNDS), or S3D8_ERR_CUDA if the synchronisation fails. */

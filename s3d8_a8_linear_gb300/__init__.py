@@ -102,6 +102,7 @@ def load(build_if_missing: bool = False):
                "s3d8_device_status", "s3d8_version"):
         getattr(L, fn).restype = I
     decoder.declare(L)
+    vision.declare(L)
     _lib = L
     return L
 
@@ -409,6 +410,10 @@ from .decoder import (KVCache, KVPool, ResidualNorm, compact_pages, copy_pages, 
                       paged_attention_workspace, pages_workspace, residual_norm,
                       residual_norm_backward, residual_norm_backward_workspace,
                       residual_norm_quant, rope_append)
+from . import vision  # noqa: E402
+from .vision import (CrossAttention, NormRope, cross_attention, cross_attention_backward,  # noqa: E402,F401
+                     cross_attention_backward_workspace, cross_attention_workspace, norm_rope,
+                     norm_rope_backward, norm_rope_backward_workspace, sample)
 
 
 def selftest_wait_timeout(polls: int = 1000) -> None:

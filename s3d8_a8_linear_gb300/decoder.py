@@ -38,6 +38,8 @@ def declare(L):
     L.s3d8_residual_norm_backward_workspace_size.argtypes = [_I64, _I64]
     L.s3d8_rope_append.argtypes = [_P, two, _P, two, _P, two, _P, _P, _I64, _I64, ctypes.c_int, _P,
                                    _P, _I64, _I64, _P, _I64, _I64, cache, _P, _P]
+    L.s3d8_norm_rope_append.argtypes = [_P, two, _P, two, _P, two, _P, _P, _I64, _I64, ctypes.c_int, _P,
+                                        _P, _I64, _I64, _P, _I64, _I64, _P, _P, _F, cache, _P, _P]
     L.s3d8_paged_attention_workspace_size.argtypes = [cache, _I64, _I64]
     L.s3d8_paged_attention.argtypes = [_P, cache, _P, _I64, _P, _I64, _I64, _F, _I64, _P, _P, _P, _SZ, _P]
     L.s3d8_pages_workspace_size.argtypes = [_I64, _I64]
@@ -49,8 +51,8 @@ def declare(L):
     for fn in ("residual_norm_backward_workspace_size", "paged_attention_workspace_size",
                "pages_workspace_size"):
         getattr(L, "s3d8_" + fn).restype = _SZ
-    for fn in ("residual_norm", "residual_norm_backward", "rope_append", "paged_attention",
-               "copy_pages", "extend_pages", "fork_pages", "free_pages", "compact_pages"):
+    for fn in ("residual_norm", "residual_norm_backward", "rope_append", "norm_rope_append",
+               "paged_attention", "copy_pages", "extend_pages", "fork_pages", "free_pages", "compact_pages"):
         getattr(L, "s3d8_" + fn).restype = ctypes.c_int
 
 
@@ -293,11 +295,13 @@ _Two = _I64 * 2
 def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cos: torch.Tensor, sin: torch.Tensor,
                 positions: torch.Tensor, cache: KVCache, table: torch.Tensor,
                 rows: torch.Tensor | None = None, q_out: torch.Tensor | None = None,
-                interleaved: bool = False) -> torch.Tensor:
+                interleaved: bool = False, q_norm: torch.Tensor | None = None,
+                k_norm: torch.Tensor | None = None, eps: float = 1e-5) -> torch.Tensor:
     """Rotate q [T, Hq, dim] and k [T, heads, dim] by cos/sin [max_pos, rotary/2]
     (fp32) at positions [T], and store k, v as tokens `positions` of the block
     table's rows (rows None: token t of row t).  Returns the rotated q; a negative
-    position marks a padding token."""
+    position marks a padding token.  q_norm, k_norm (bf16 [dim]): each head is
+    normed in front of its rotation, in the same pass."""
     (qp, qs), (kp, ks), (vp, vs) = _rows(q, "q", _BF), _rows(k, "k", _BF), _rows(v, "v", _BF)
     shape = q.shape
     T, Hq, D = shape
@@ -310,11 +314,16 @@ def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cos: torch.Te
     turns = cos.shape
     max_pos, half = turns
     n, width = table.shape
-    st = _load().s3d8_rope_append(
-        qp, _Two(*qs), kp, _Two(*ks), vp, _Two(*vs), _dev(cos, "cos", _F32), _dev(sin, "sin", _F32, turns),
-        max_pos, 2 * half, interleaved, _dev(positions, "positions", _I32T, shape[:1]),
-        None if rows is None else _dev(rows, "rows", _I32T, shape[:1]), T, Hq, _dev(table, "table", _I32T),
-        n, width, cache.ref, _dev(q_out, "q_out", _BF, shape), _stream(q.device))
+    args = (qp, _Two(*qs), kp, _Two(*ks), vp, _Two(*vs), _dev(cos, "cos", _F32), _dev(sin, "sin", _F32, turns),
+            max_pos, 2 * half, interleaved, _dev(positions, "positions", _I32T, shape[:1]),
+            None if rows is None else _dev(rows, "rows", _I32T, shape[:1]), T, Hq, _dev(table, "table", _I32T),
+            n, width)
+    end = (cache.ref, _dev(q_out, "q_out", _BF, shape), _stream(q.device))
+    if q_norm is None and k_norm is None:
+        st = _load().s3d8_rope_append(*args, *end)
+    else:
+        st = _load().s3d8_norm_rope_append(*args, _opt(q_norm, "q_norm", _BF, (D,)), _opt(k_norm, "k_norm", _BF, (D,)),
+                                           eps, *end)
     if st:
         _check("s3d8_rope_append", st)
     return q_out
