@@ -1,168 +1,735 @@
-// Attention of text tokens to an encoder's states, each token over a span of them, and its
-// gradients (s3d8_cross_attention, s3d8_cross_attention_backward):
+// Attention of text tokens to an encoder's states, each token over a span of them
+// (s3d8_cross_attention):
 //
 //   s_j = scale q . k_j (a <= j < b), out = sum softmax(s)_j v_j, lse = log sum exp s_j
-//   delta = dout . out, p_j = exp(s_j - lse), ds_j = p_j (dout . v_j - delta)
-//   dq = scale sum_j ds_j k_j, dk_j = scale sum ds_j q, dv_j = sum p_j dout
-#include "common.cuh"
-#include "launch.h"
-#include "tcgen05.cuh"
+//
+// Tiles of 128 query rows: the query heads of a key/value head stand behind one another,
+// token by token, so that they share its keys and values, and one token of 4 heads is four
+// rows.  The states pass in tiles of 128.  S = Q K^T and O += P V run on the tensor cores
+// (tcgen05, sums in tensor memory); the softmax's weights P go from registers into tensor
+// memory as the second product's A operand, over the scores they come from.  A CTA an SM:
+// one warp copies (bulk tensor copies into a ring), one issues the products, two groups of
+// four warps have a row a thread each, and two warps look the values over (below).
+//
+// Two chains of score, softmax and product run in turn, so that the tensor cores work on
+// one while the other is in its softmax: two query tiles over the same states where their
+// spans are nearly the same (a prompt), or else one query tile whose states alternate (a
+// decode step: every token its own image).  Every CTA looks over all spans, makes the same
+// list of work from them, and takes an equal share of its state tiles, wherever that begins
+// or ends; what a share cuts leaves fp32 sums, which a second kernel joins in order.
+//
+// The running maximum moves only where a tile exceeds it by 2^8 (rescaling O costs a round
+// through tensor memory); sums are fp32 throughout.  The weights are rounded to bf16, the
+// values' type, on their way into the product: 2^-8 of each, which averages to about the
+// rounding of the output; 16 more bits would double the product.
+//
+// A weight of zero does not silence an infinity or NaN among the values: 0 * inf is NaN.
+// Where some row of the query tiles does not see all of a state tile, the two other warps
+// look at its values, replace what is not finite by zeros, and note which rows do see it;
+// those rows get the infinity or NaN in that column at the end.
+#include "cross_tiles.cuh"
 
 namespace s3d8 {
 
 namespace {
 
-constexpr int kWarps = 4;
+using namespace cross;
 
-__device__ __forceinline__ float warp_sum_f(float v)
-{
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-}
+constexpr int kThreads = 384;
+constexpr int kMostTiles = 1024;        // query tiles of a launch
+constexpr int kJoinWarps = 8, kJoinRows = 32;
 
-// Token t's span, within the states; one that is not is cut to them and recorded.
-__device__ __forceinline__ int2 span_of(const CrossArgs &a, int t)
-{
-    if (!a.spans)
-        return make_int2(0, a.S);
-    const int2 s = make_int2(a.spans[2 * (int64_t)t], a.spans[2 * (int64_t)t + 1]);
-    if (s.x >= s.y)
-        return make_int2(0, 0);
-    if (s.x < 0 || s.y > a.S)
-        atomicExch(a.status, kStatusBounds);
-    return make_int2(max(s.x, 0), min(s.y, a.S));
-}
+// A piece of the work: query tile a (and b, with the same states), state tiles j0 and on;
+// `begin`: state tiles of one key/value head in front of it.
+struct Item {
+    int tiles, j0, begin, end_;
+};
+constexpr int kNoTile = 0xFFFF;
 
-struct Cols {
-    float v[4];
+struct Plan {
+    int tokens_a_tile, tiles, rows;     // rows: of a slot of partial sums
+    int chunk_rows;                     // query rows that a copy fills
+    int ctas;
+    float *parts, *tops;                // [ctas][2][rows][DP], [ctas][2][rows][2]
+    Item *items;                        // the list, for the join (its first entry: how many)
+    int negative;                       // scale < 0: the scores are those of -Q
 };
 
-__device__ __forceinline__ Cols columns(const __nv_bfloat16 *x, int dim)
-{
-    Cols c;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int d = (threadIdx.x & 31) + 32 * i;
-        c.v[i] = d < dim ? __bfloat162float(x[d]) : 0.0f;
+template <int DP>
+struct Layout {
+    static constexpr int CHUNKS = DP / 64;
+    static constexpr int TILE = kTile * DP * 2;             // bytes of a tile of Q, K or V
+    static constexpr int STAGES = DP == 128 ? 4 : 8;
+    static constexpr int Q = 0, KV = 2 * TILE, ITEMS = KV + STAGES * TILE;
+    static constexpr int RANGES = ITEMS + (kMostTiles + 1) * (int)sizeof(Item);     // of the query tiles, while the list is made
+    static constexpr int BAD = RANGES + kMostTiles * 8;     // [2][128][8]: columns of +inf, of -inf
+    static constexpr int TOPS = BAD + 2 * 128 * 32;         // [128] maximum and sum of the second chain
+    static constexpr int BARS = TOPS + 128 * 8;
+    static constexpr int BYTES = 1024 + BARS + 512;
+};
+
+struct Unit {
+    int ta, tb, head, j0, n, slot;      // slot: -1 for a whole piece, else where its sums go
+    bool pair;
+};
+
+// How many CTAs have a share: none of them an empty one.
+__device__ __forceinline__ int64_t busy(int ctas, int64_t all) { return all < ctas ? all : ctas; }
+
+// The CTA's share of the work, piece by piece.
+struct Share {
+    const Item *items;
+    int n_items, per_head;
+    int64_t at, first, end;
+
+    __device__ __forceinline__ Share(const Item *list, int n, int heads, int ctas)
+        : items(list), n_items(n), per_head(list[n].begin)
+    {
+        const int64_t all = (int64_t)heads * per_head, some = busy(ctas, all);
+        first = at = blockIdx.x < some ? all * blockIdx.x / some : 0;
+        end = blockIdx.x < some ? all * (blockIdx.x + 1) / some : 0;
     }
-    return c;
-}
 
-__device__ __forceinline__ float dot(const Cols &a, const Cols &b)
-{
-    return warp_sum_f(a.v[0] * b.v[0] + a.v[1] * b.v[1] + a.v[2] * b.v[2] + a.v[3] * b.v[3]);
-}
-
-__device__ __forceinline__ void store(__nv_bfloat16 *x, const Cols &c, float f, int dim)
-{
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int d = (threadIdx.x & 31) + 32 * i;
-        if (d < dim)
-            x[d] = __float2bfloat16_rn(c.v[i] * f);
+    __device__ __forceinline__ bool next(Unit &u)
+    {
+        if (at >= end)
+            return false;
+        u.head = (int)(at / per_head);
+        const int r = (int)(at - (int64_t)u.head * per_head);
+        int lo = 0, hi = n_items;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (items[mid].begin <= r)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        const Item it = items[lo];
+        const int off = r - it.begin, left = items[lo + 1].begin - r;
+        u.ta = it.tiles & 0xFFFF;
+        u.tb = it.tiles >> 16 & 0xFFFF;
+        u.pair = u.tb != kNoTile;
+        u.j0 = it.j0 + off;
+        u.n = (int)(end - at < left ? end - at : left);
+        u.slot = off == 0 && u.n == left ? -1 : at != first;
+        at += u.n;
+        return true;
     }
-}
+};
 
-// A warp a (token, query head).
-__global__ __launch_bounds__(kWarps * 32) void cross_forward_kernel(const __grid_constant__ CrossArgs a)
+// The list of work: for each pair of query tiles whether they go together.  One warp.
+__device__ __forceinline__ int make_items(const int2 *ranges, int tiles, Item *items)
 {
-    const int64_t row = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    if (row >= (int64_t)a.T * a.Hq)
-        return;
-    const int t = (int)(row / a.Hq), h = (int)(row % a.Hq), g = h / (a.Hq / a.heads);
-    const int2 s = span_of(a, t);
-    const Cols q = columns(a.q + t * a.qs[0] + h * a.qs[1], a.dim);
-    float top = -INFINITY, sum = 0.0f;
-    Cols acc = {};
-    for (int j = s.x; j < s.y; ++j) {
-        const float x = a.scale * dot(q, columns(a.k + j * a.ks[0] + g * a.ks[1], a.dim));
-        const Cols v = columns(a.v + j * a.vs[0] + g * a.vs[1], a.dim);
-        const float next = fmaxf(top, x), turn = expf(top - next), p = expf(x - next);
-        sum = sum * turn + p;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            acc.v[i] = acc.v[i] * turn + p * v.v[i];
-        top = next;
-    }
-    store(a.out + row * a.dim, acc, s.x < s.y ? 1.0f / sum : 0.0f, a.dim);
-    if (a.lse && (threadIdx.x & 31) == 0)
-        a.lse[row] = s.x < s.y ? top + logf(sum) : -INFINITY;
-}
-
-// A warp a (token, query head): dq, and delta for the other kernel.
-__global__ __launch_bounds__(kWarps * 32) void cross_dq_kernel(const __grid_constant__ CrossArgs a)
-{
-    const int64_t row = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    if (row >= (int64_t)a.T * a.Hq)
-        return;
-    const int t = (int)(row / a.Hq), h = (int)(row % a.Hq), g = h / (a.Hq / a.heads);
-    const int2 s = span_of(a, t);
-    const Cols q = columns(a.q + t * a.qs[0] + h * a.qs[1], a.dim), d = columns(a.dout + t * a.ds[0] + h * a.ds[1], a.dim);
-    const float delta = dot(d, columns(a.out + row * a.dim, a.dim)), lse = a.lse[row];
-    Cols acc = {};
-    for (int j = s.x; j < s.y; ++j) {
-        const Cols k = columns(a.k + j * a.ks[0] + g * a.ks[1], a.dim);
-        const float p = expf(a.scale * dot(q, k) - lse), ds = p * (dot(d, columns(a.v + j * a.vs[0] + g * a.vs[1], a.dim)) - delta);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            acc.v[i] += ds * k.v[i];
-    }
-    store(a.dq + row * a.dim, acc, a.scale, a.dim);
-    if ((threadIdx.x & 31) == 0)
-        static_cast<float *>(a.ws)[row] = delta;
-}
-
-// A warp a (state, key/value head).
-__global__ __launch_bounds__(kWarps * 32) void cross_dkv_kernel(const __grid_constant__ CrossArgs a)
-{
-    const int64_t row = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    if (row >= (int64_t)a.S * a.heads)
-        return;
-    const int j = (int)(row / a.heads), g = (int)(row % a.heads), group = a.Hq / a.heads;
-    const Cols k = columns(a.k + j * a.ks[0] + g * a.ks[1], a.dim), v = columns(a.v + j * a.vs[0] + g * a.vs[1], a.dim);
-    Cols dk = {}, dv = {};
-    for (int t = 0; t < a.T; ++t) {
-        const int2 s = span_of(a, t);
-        if (j < s.x || j >= s.y)
-            continue;
-        for (int h = g * group; h < (g + 1) * group; ++h) {
-            const Cols q = columns(a.q + t * a.qs[0] + h * a.qs[1], a.dim), d = columns(a.dout + t * a.ds[0] + h * a.ds[1], a.dim);
-            const int64_t at = (int64_t)t * a.Hq + h;
-            const float p = expf(a.scale * dot(q, k) - a.lse[at]), ds = p * (dot(d, v) - static_cast<const float *>(a.ws)[at]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                dk.v[i] += ds * q.v[i];
-                dv.v[i] += p * d.v[i];
+    const int lane = threadIdx.x & 31;
+    int count = 0, begin = 0;
+    auto span = [&](int t, int &j0, int &j1) {      // state tiles; one (of which nothing is seen) for an empty span
+        const int2 r = ranges[t];
+        j0 = r.x < r.y ? r.x / kTile : 0;
+        j1 = r.x < r.y ? (r.y + kTile - 1) / kTile : 1;
+    };
+    for (int base = 0; base < (tiles + 1) / 2; base += 32) {
+        const int a = 2 * (base + lane), b = a + 1;
+        int n = 0, a0 = 0, a1 = 0, b0 = 0, b1 = 0;
+        bool pair = false;
+        if (a < tiles) {
+            n = 1;
+            span(a, a0, a1);
+            if (b < tiles) {
+                span(b, b0, b1);
+                // together, both chains pass the states of either
+                const int u0 = min(a0, b0), u1 = max(a1, b1);
+                pair = 8 * (u1 - u0) <= 5 * (a1 - a0 + b1 - b0) + 8;
+                if (pair)
+                    a0 = u0, a1 = u1;
+                else
+                    n = 2;
             }
         }
+        const int size = n ? a1 - a0 + (n == 2 ? b1 - b0 : 0) : 0;
+        int c = n, s = size;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int pc = __shfl_up_sync(0xffffffffu, c, o), ps = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o)
+                c += pc, s += ps;
+        }
+        if (n)
+            items[count + c - n] = {a | (pair ? b : kNoTile) << 16, a0, begin + s - size, 0};
+        if (n == 2)
+            items[count + c - 1] = {b | kNoTile << 16, b0, begin + s - (b1 - b0), 0};
+        count += __shfl_sync(0xffffffffu, c, 31);
+        begin += __shfl_sync(0xffffffffu, s, 31);
     }
-    store(a.dk + row * a.dim, dk, a.scale, a.dim);
-    store(a.dv + row * a.dim, dv, 1.0f, a.dim);
+    if (lane == 0)
+        items[count] = {0, 0, begin, 0};
+    return count;
 }
 
-unsigned blocks(int64_t rows) { return (unsigned)((rows + kWarps - 1) / kWarps); }
+__device__ __forceinline__ bool finite2(uint32_t top) { return (top & 0xFFFFu) < 0x7F80u && (top >> 16) < 0x7F80u; }
+
+// Looks over a state tile's values (in shared memory at v): a row a thread at a time.
+// What is not finite becomes zero, and is noted for the rows that see its state.
+template <int DP>
+__device__ __forceinline__ void look_over(uint32_t v, int c0, const CrossArgs &a, const Plan &p, const Unit &u, uint32_t *bad, int *any, int thread)
+{
+    for (int r = thread; r < kTile; r += 64) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int c = 0; c < DP / 8; ++c) {
+            const uint4 x = lds_v4(v + (c >> 3) * (kTile * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+            top = absmax_bf16x8(x, top);
+        }
+        if (finite2(top))
+            continue;
+        uint32_t plus[4] = {0, 0, 0, 0}, minus[4] = {0, 0, 0, 0};       // NaN: both
+        for (int c = 0; c < DP / 8; ++c) {
+            const uint32_t at = v + (c >> 3) * (kTile * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+            for (int e = 0; e < 8; ++e) {
+                uint16_t x;
+                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(at + 2 * e));
+                if ((x & 0x7FFF) < 0x7F80)
+                    continue;
+                asm volatile("st.shared.u16 [%0], %1;" ::"r"(at + 2 * e), "h"((uint16_t)0) : "memory");
+                const int d = 8 * c + e;
+                const uint32_t bit = 1u << (d & 31);
+                if (x != 0xFF80)
+                    plus[d >> 5] |= bit;
+                if (x != 0x7F80)
+                    minus[d >> 5] |= bit;
+            }
+        }
+        const int j = c0 + r;
+        if (j >= a.S)
+            continue;
+        for (int s = 0; s < (u.pair ? 2 : 1); ++s)
+            for (int i = 0; i < p.tokens_a_tile; ++i) {
+                const int t = (s ? u.tb : u.ta) * p.tokens_a_tile + i;
+                if (t >= a.T)
+                    break;
+                const int2 see = span_of(a.spans, a.S, t, nullptr);
+                if (j < see.x || j >= see.y)
+                    continue;
+                const int group = a.Hq / a.heads;
+                for (int g = 0; g < group; ++g)
+                    for (int w = 0; w < 4; ++w) {
+                        atomicOr(bad + (s * 128 + i * group + g) * 8 + w, plus[w]);
+                        atomicOr(bad + (s * 128 + i * group + g) * 8 + 4 + w, minus[w]);
+                    }
+                atomicExch(any + s, 1);
+            }
+    }
+}
+
+template <int DP>
+__global__ __launch_bounds__(kThreads, 1) void cross_forward_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                                                                    const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CrossArgs a,
+                                                                    const __grid_constant__ Plan p)
+{
+    using L = Layout<DP>;
+    extern __shared__ unsigned char cross_mem[];
+    __shared__ uint32_t tmem_slot;
+    __shared__ int item_count, bad_any[2];
+    const uint32_t base = (smem_addr(cross_mem) + 1023u) & ~1023u;
+    unsigned char *mem = cross_mem + (base - smem_addr(cross_mem));
+    Item *items = reinterpret_cast<Item *>(mem + L::ITEMS);
+    int2 *ranges = reinterpret_cast<int2 *>(mem + L::RANGES);
+    uint32_t *bad = reinterpret_cast<uint32_t *>(mem + L::BAD);
+    float2 *tops = reinterpret_cast<float2 *>(mem + L::TOPS);
+    const uint32_t bars = base + L::BARS;
+    const uint32_t q_full = bars, q_empty = bars + 8, o_free = bars + 16, s_full = bars + 24, p_ready = bars + 40, pv_done = bars + 56;
+    const uint32_t kv_full = bars + 72, kv_empty = kv_full + 8 * L::STAGES, v_ok = kv_empty + 8 * L::STAGES;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = a.Hq / a.heads;
+
+    if (warp == 0 && lane == 0) {
+        mbar_init(q_full, 1);
+        mbar_init(q_empty, 1);
+        mbar_init(o_free, 8);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(s_full + 8 * s, 1);
+            mbar_init(p_ready + 8 * s, 4);
+            mbar_init(pv_done + 8 * s, 1);
+        }
+        for (int s = 0; s < L::STAGES; ++s) {
+            mbar_init(kv_full + 8 * s, 1);
+            mbar_init(kv_empty + 8 * s, 1);
+            mbar_init(v_ok + 8 * s, 2);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&tmem_slot)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    if (threadIdx.x < 2)
+        bad_any[threadIdx.x] = 0;
+    for (int i = threadIdx.x; i < 2 * 128 * 8; i += kThreads)
+        bad[i] = 0;
+    if (p.chunk_rows < kTile)       // rows that no copy fills are zeros
+        for (int i = threadIdx.x; i < 2 * L::TILE / 16; i += kThreads)
+            reinterpret_cast<uint4 *>(mem + L::Q)[i] = make_uint4(0u, 0u, 0u, 0u);
+    for (int i = threadIdx.x; i < p.tiles; i += kThreads)
+        ranges[i] = make_int2(0x7FFFFFFF, 0);
+    fence_proxy_async_smem();
+    __syncthreads();
+    tc::pdl_launch_dependents();
+    tc::pdl_wait();
+    for (int t = threadIdx.x; t < a.T; t += kThreads) {
+        const int2 s = span_of(a.spans, a.S, t, blockIdx.x == 0 ? a.status : nullptr);
+        if (s.x < s.y) {
+            atomicMin(&ranges[t / p.tokens_a_tile].x, s.x);
+            atomicMax(&ranges[t / p.tokens_a_tile].y, s.y);
+        }
+    }
+    __syncthreads();
+    if (warp == 0) {
+        const int n = make_items(ranges, p.tiles, items);
+        if (lane == 0)
+            item_count = n;
+        __syncwarp();
+        if (blockIdx.x == 0) {      // for the join
+            for (int i = lane; i <= n; i += 32)
+                p.items[1 + i] = items[i];
+            if (lane == 0)
+                p.items[0].begin = n;
+        }
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    Share share(items, item_count, a.heads, p.ctas);
+    Unit u;
+    bool ok = true;
+
+    // registers: 128 x 88 + 256 x 208 = 384 x 168
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        if (warp == 0) {                // copies
+            int at = 0;                 // tiles of K and V so far
+            for (int units = 0; ok && share.next(u); ++units) {
+                if (units > 0 && !(ok = tc::warp_wait(q_empty, (units - 1) & 1)))
+                    break;
+                tc::mbar_arrive_expect_tx_elect(q_full, (u.pair ? 2 : 1) * L::CHUNKS * 128 * p.chunk_rows);
+                for (int s = 0; s < (u.pair ? 2 : 1); ++s)
+                    for (int c = 0; c < L::CHUNKS; ++c)
+                        tma_3d_elect(base + L::Q + s * L::TILE + c * (kTile * 128), &map_q, 64 * c, u.head * group, (s ? u.tb : u.ta) * p.tokens_a_tile, q_full);
+                for (int i = 0; ok && i < 2 * u.n; ++i, ++at) {
+                    const int st = at % L::STAGES;
+                    if (at >= L::STAGES && !(ok = tc::warp_wait(kv_empty + 8 * st, (at / L::STAGES - 1) & 1)))
+                        break;
+                    tc::mbar_arrive_expect_tx_elect(kv_full + 8 * st, L::TILE);
+                    for (int c = 0; c < L::CHUNKS; ++c)
+                        tma_3d_elect(base + L::KV + st * L::TILE + c * (kTile * 128), i & 1 ? &map_v : &map_k, 64 * c, u.head, (u.j0 + (i >> 1)) * kTile,
+                                     kv_full + 8 * st);
+                }
+            }
+            // not before the last copies have landed
+            for (int i = at - L::STAGES < 0 ? 0 : at - L::STAGES; i < at; ++i)
+                ok &= tc::warp_wait(kv_full + 8 * (i % L::STAGES), (i / L::STAGES) & 1);
+        } else if (warp == 1) {         // products
+            const int ksteps = (a.dim + 15) / 16, n_out = ksteps * 16;
+            const uint32_t id_s = idesc_cols(kTile) | (p.negative ? kNegateA : 0u), id_o = idesc_rows(n_out);
+            int at = 0, jobs[2] = {0, 0};       // K/V tiles, and products with V of each chain, so far
+            for (int units = 0; ok && share.next(u); ++units) {
+                const int n = u.pair ? 2 * u.n : u.n;
+                if (!(ok = tc::warp_wait(q_full, units & 1)))
+                    break;
+                for (int job = 0; ok && job <= n; ++job) {
+                    if (job < n) {
+                        const int s = job & 1, k = at + 2 * (u.pair ? job >> 1 : job), st = k % L::STAGES;
+                        const bool last = !u.pair || s;
+                        if (!u.pair || !s)
+                            if (!(ok = tc::warp_wait(kv_full + 8 * st, (k / L::STAGES) & 1)))
+                                break;
+                        tc::tc_fence_after();
+                        const uint32_t q = base + L::Q + (u.pair ? s * L::TILE : 0), kt = base + L::KV + st * L::TILE;
+                        for (int kk = 0; kk < ksteps; ++kk) {
+                            const uint32_t off = (kk >> 2) * (kTile * 128) + (kk & 3) * 32;
+                            tc::mma_bf16_elect(tmem + s * 128, tc::sw128_desc(q + off), tc::sw128_desc(kt + off), id_s, kk > 0);
+                        }
+                        tc::mma_commit_elect(s_full + 8 * s);
+                        if (last)
+                            tc::mma_commit_elect(kv_empty + 8 * st);
+                        if (job == n - 1)
+                            tc::mma_commit_elect(q_empty);
+                    }
+                    if (job > 0) {
+                        const int prev = job - 1, s = prev & 1, v = at + 2 * (u.pair ? prev >> 1 : prev) + 1, st = v % L::STAGES;
+                        if (!u.pair || !s)
+                            if (!(ok = tc::warp_wait(v_ok + 8 * st, (v / L::STAGES) & 1)))
+                                break;
+                        if (!(ok = tc::warp_wait(p_ready + 8 * s, jobs[s] & 1)))
+                            break;
+                        tc::tc_fence_after();
+                        ++jobs[s];
+                        const uint32_t vt = base + L::KV + st * L::TILE;
+                        for (int kk = 0; kk < kTile / 16; ++kk)
+                            mma_tmem_a_elect(tmem + 256 + s * 128, tmem + s * 128 + kk * 8, rows_desc(vt + kk * 2048, kTile * 128), id_o, prev >= 2 || kk > 0);
+                        tc::mma_commit_elect(pv_done + 8 * s);
+                        if (!u.pair || s)
+                            tc::mma_commit_elect(kv_empty + 8 * st);
+                    }
+                }
+                at += 2 * u.n;
+            }
+        } else if (warp < 4) {          // looks the values over
+            int at = 0;
+            for (int units = 0; ok && share.next(u); ++units) {
+                // the states that every row with any sees
+                int lo = 0, hi = 0x7FFFFFFF;
+                for (int s = 0; s < (u.pair ? 2 : 1); ++s)
+                    for (int i = lane; i < p.tokens_a_tile; i += 32) {
+                        const int t = (s ? u.tb : u.ta) * p.tokens_a_tile + i;
+                        const int2 see = t < a.T ? span_of(a.spans, a.S, t, nullptr) : make_int2(0, 0);
+                        if (see.x < see.y) {
+                            lo = max(lo, see.x);
+                            hi = min(hi, see.y);
+                        }
+                    }
+                lo = __reduce_max_sync(0xffffffffu, lo);
+                hi = __reduce_min_sync(0xffffffffu, hi);
+                if (units > 0 && !(ok = tc::warp_wait(o_free, (units - 1) & 1)))   // the notes of the piece before are read
+                    break;
+                for (int i = 0; i < u.n; ++i) {
+                    const int v = at + 2 * i + 1, st = v % L::STAGES, c0 = (u.j0 + i) * kTile;
+                    if (!(ok = tc::warp_wait(kv_full + 8 * st, (v / L::STAGES) & 1)))
+                        break;
+                    if (c0 < lo || c0 + kTile > hi) {
+                        look_over<DP>(base + L::KV + st * L::TILE, c0, a, p, u, bad, bad_any, (warp - 2) * 32 + lane);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                    if (lane == 0)
+                        tc::mbar_arrive(v_ok + 8 * st);
+                }
+                at += 2 * u.n;
+            }
+        }
+    } else {                        // softmax, a row a thread
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        const int s = (warp - 4) >> 2, row = threadIdx.x & 127;
+        const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21), sc = lanes + s * 128, oc = lanes + 256 + s * 128;
+        const float scale = fmaxf(fabsf(a.scale) * kLog2e, 1e-30f);      // not 0: a hidden score is -inf
+        int jobs = 0;
+        for (int units = 0; ok && share.next(u); ++units) {
+            const int tile = u.pair && s ? u.tb : u.ta, t = tile * p.tokens_a_tile + row / group;
+            const bool live = row < p.chunk_rows && t < a.T;
+            const int2 see = live ? span_of(a.spans, a.S, t, nullptr) : make_int2(0, 0);
+            const int mine = u.pair ? u.n : (u.n + 1 - s) / 2;
+            float top = -INFINITY, sum = 0.0f;      // in units of base-2 exponents
+            for (int i = 0; i < mine; ++i, ++jobs) {
+                const int c0 = (u.j0 + (u.pair ? i : 2 * i + s)) * kTile;
+                if (!(ok = tc::warp_wait(s_full + 8 * s, jobs & 1)))
+                    break;
+                tc::tc_fence_after();
+                float x[kTile];
+#pragma unroll
+                for (int c = 0; c < kTile; c += 32)
+                    tmem_ld32(sc + c, x + c);
+                tmem_wait_ld();
+                if (!__all_sync(0xffffffffu, see.x <= c0 && see.y >= c0 + kTile)) {
+                    const unsigned from = see.x - c0, n = see.y - see.x;
+#pragma unroll
+                    for (int c = 0; c < kTile; ++c)
+                        x[c] = c - from < n ? x[c] : -INFINITY;
+                }
+                float m[4] = {x[0], x[1], x[2], x[3]};
+#pragma unroll
+                for (int c = 4; c < kTile; c += 4)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        m[e] = fmaxf(m[e], x[c + e]);
+                const float peak = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * scale;
+                const bool rise = peak > top + 8.0f || top == -INFINITY;
+                if (__any_sync(0xffffffffu, rise && peak > -INFINITY)) {
+                    const float next = rise ? peak : top, turn = rise ? ex2(top - (next == -INFINITY ? 0.0f : next)) : 1.0f;
+                    top = next;
+                    sum *= turn;
+                    if (i > 0) {
+                        if (!(ok = tc::warp_wait(pv_done + 8 * s, (jobs - 1) & 1)))
+                            break;
+                        tc::tc_fence_after();
+#pragma unroll
+                        for (int c = 0; c < DP; c += 32) {
+                            float o[32];
+                            uint32_t b[32];
+                            tmem_ld32(oc + c, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                b[e] = __float_as_uint(o[e] * turn);
+                            tmem_st32(oc + c, b);
+                        }
+                    }
+                }
+                const float shift = top == -INFINITY ? 0.0f : -top;
+                const float2 scale2 = make_float2(scale, scale), shift2 = make_float2(shift, shift);
+                float2 part[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+                uint32_t w[kTile / 2];
+#pragma unroll
+                for (int c = 0; c < kTile / 2; ++c) {
+                    const float2 e = fma2(make_float2(x[2 * c], x[2 * c + 1]), scale2, shift2), y = make_float2(ex2(e.x), ex2(e.y));
+                    part[c & 1] = add2(part[c & 1], y);
+                    w[c] = pack2(y.x, y.y);
+                }
+                tmem_st32(sc, w);
+                tmem_st32(sc + 32, w + 32);
+                tmem_wait_st();
+                tc::tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    tc::mbar_arrive(p_ready + 8 * s);
+                part[0] = add2(part[0], part[1]);
+                sum += part[0].x + part[0].y;
+            }
+            if (!ok)
+                break;
+            if (mine > 0) {
+                if (!(ok = tc::warp_wait(pv_done + 8 * s, (jobs - 1) & 1)))
+                    break;
+                tc::tc_fence_after();
+            }
+            // one query tile: the first group joins the two chains
+            float turn[2] = {1.0f, 0.0f};
+            if (!u.pair) {
+                if (s == 1)
+                    tops[row] = make_float2(top, sum);
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+                if (s == 0) {
+                    const float2 other = tops[row];
+                    const float next = fmaxf(top, other.x), from = next == -INFINITY ? 0.0f : next;
+                    turn[0] = ex2(top - from);
+                    turn[1] = ex2(other.x - from);
+                    sum = sum * turn[0] + other.y * turn[1];
+                    top = next;
+                }
+            }
+            if (u.pair || s == 0) {
+                const bool whole = u.slot < 0;
+                const float by = whole ? (sum != 0.0f ? 1.0f / sum : 0.0f) : 1.0f;
+                const bool both = !u.pair && u.n > 1, noted = bad_any[u.pair ? s : 0];
+                const uint32_t *note = bad + ((u.pair ? s : 0) * 128 + row) * 8;
+                __nv_bfloat16 *out = a.out + ((int64_t)t * a.Hq + u.head * group + row % group) * a.dim;
+                const int64_t slot = ((int64_t)blockIdx.x * 2 + u.slot) * p.rows + (u.pair ? s * 128 : 0) + row;
+                const bool some = see.x < see.y;
+#pragma unroll
+                for (int c = 0; c < DP; c += 32) {
+                    float o[32];
+                    tmem_ld32(oc + c, o);
+                    tmem_wait_ld();
+                    if (!u.pair) {
+                        float o2[32];
+                        if (both) {
+                            tmem_ld32(oc + 128 + c, o2);
+                            tmem_wait_ld();
+                        }
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            o[e] = o[e] * turn[0] + (both ? o2[e] * turn[1] : 0.0f);
+                    }
+                    if (noted) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            if (note[c / 32] >> e & 1)
+                                o[e] += INFINITY;
+                            if (note[4 + c / 32] >> e & 1)
+                                o[e] -= INFINITY;
+                        }
+                    }
+                    if (!live)
+                        continue;
+                    if (whole) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8)
+                            if (c + e < a.dim) {
+                                uint32_t r[4];
+#pragma unroll
+                                for (int y = 0; y < 4; ++y)
+                                    r[y] = some ? pack2(o[e + 2 * y] * by, o[e + 2 * y + 1] * by) : 0u;
+                                *reinterpret_cast<uint4 *>(out + c + e) = make_uint4(r[0], r[1], r[2], r[3]);
+                            }
+                    } else if (some) {
+                        float4 *part = reinterpret_cast<float4 *>(p.parts + slot * DP + c);
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            part[e / 4] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                    }
+                }
+                if (live) {
+                    if (!whole)
+                        reinterpret_cast<float2 *>(p.tops)[slot] = make_float2(some ? top : -INFINITY, some ? sum : 0.0f);
+                    else if (a.lse)
+                        a.lse[(int64_t)t * a.Hq + u.head * group + row % group] = some ? (top + __log2f(sum)) * kLn2 : -INFINITY;
+                }
+                if (noted) {        // used: gone, before the next piece
+                    for (int w = 0; w < 8; ++w)
+                        bad[((u.pair ? s : 0) * 128 + row) * 8 + w] = 0;
+                    if (s == 0)
+                        asm volatile("bar.sync 2, 128;" ::: "memory");
+                    else
+                        asm volatile("bar.sync 3, 128;" ::: "memory");
+                    if (row == 0)
+                        bad_any[u.pair ? s : 0] = 0;
+                }
+            }
+            tc::tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                tc::mbar_arrive(o_free);
+        }
+    }
+    if (!ok)
+        record_timeout(a.status);
+    tc::tc_fence_before();
+    __syncthreads();
+    if (warp == 1)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+// Joins the parts of the pieces that shares cut: a warp a row, parts in order.
+template <int DP>
+__global__ __launch_bounds__(kJoinWarps * 32) void cross_join_kernel(const __grid_constant__ CrossArgs a, const __grid_constant__ Plan p)
+{
+    constexpr int V = DP / 32;
+    tc::pdl_launch_dependents();
+    tc::pdl_wait();
+    const int n = p.items[0].begin, i = blockIdx.x / a.heads, head = blockIdx.x % a.heads;
+    if (i >= n)
+        return;
+    const Item *items = p.items + 1, it = items[i];
+    const int64_t per_head = items[n].begin, all = per_head * a.heads;
+    const int64_t from = head * per_head + it.begin, to = head * per_head + items[i + 1].begin - 1;
+    const int64_t ctas = busy(p.ctas, all);
+    auto owner = [&](int64_t w) { return (int)(((w + 1) * ctas - 1) / all); };
+    const int c0 = owner(from), c1 = owner(to);
+    if (c0 == c1)
+        return;
+    const int first_slot = from != all * c0 / ctas, group = a.Hq / a.heads, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int r = blockIdx.y * kJoinRows + warp; r < blockIdx.y * kJoinRows + kJoinRows && r < p.rows; r += kJoinWarps) {
+        const int tile = r < kTile ? it.tiles & 0xFFFF : it.tiles >> 16 & 0xFFFF, row = r % kTile;
+        const int t = tile * p.tokens_a_tile + row / group;
+        if (tile == kNoTile || row >= p.chunk_rows || t >= a.T)
+            continue;
+        auto slot = [&](int c) { return ((int64_t)c * 2 + (c == c0 ? first_slot : 0)) * p.rows + r; };
+        float top = -INFINITY;
+        for (int c = c0 + lane; c <= c1; c += 32)
+            top = fmaxf(top, p.tops[2 * slot(c)]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const float zero = top == -INFINITY ? 0.0f : top;
+        float sum = 0.0f, acc[V] = {};
+        for (int c = c0; c <= c1; ++c) {
+            const int64_t at = slot(c);
+            const float2 part = reinterpret_cast<const float2 *>(p.tops)[at];
+            if (part.y == 0.0f)         // saw nothing: its sums were not written
+                continue;
+            const float turn = ex2(part.x - zero);
+            sum += part.y * turn;
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                acc[v] = fmaf(p.parts[at * DP + lane + 32 * v], turn, acc[v]);
+        }
+        const int64_t at = (int64_t)t * a.Hq + head * group + row % group;
+        const int2 see = span_of(a.spans, a.S, t, nullptr);
+        const bool some = see.x < see.y;
+        const float by = some ? 1.0f / sum : 0.0f;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (lane + 32 * v < a.dim)
+                a.out[at * a.dim + lane + 32 * v] = __float2bfloat16_rn(some ? acc[v] * by : 0.0f);
+        if (a.lse && lane == 0)
+            a.lse[at] = some ? (top + __log2f(sum)) * kLn2 : -INFINITY;
+    }
+}
+
+// No states at all.
+__global__ void cross_nothing_kernel(const __grid_constant__ CrossArgs a)
+{
+    const int64_t rows = (int64_t)a.T * a.Hq;
+    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < rows * a.dim / 8; i += (int64_t)gridDim.x * blockDim.x) {
+        reinterpret_cast<uint4 *>(a.out)[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (a.lse && i < rows)
+            a.lse[i] = -INFINITY;
+    }
+}
+
+// Of at most kMostTiles query tiles.
+Plan plan_of(int64_t T, int64_t Hq, int64_t heads, int DP, size_t *bytes)
+{
+    Plan p;
+    const int group = (int)(Hq / heads);
+    p.tokens_a_tile = kTile / group;
+    p.chunk_rows = p.tokens_a_tile * group;
+    const int64_t tiles = (T + p.tokens_a_tile - 1) / p.tokens_a_tile;
+    p.tiles = (int)(tiles < kMostTiles ? tiles : kMostTiles);
+    p.rows = tiles > 1 ? 2 * kTile : (int)(T * group);
+    p.ctas = device_sm_count();
+    size_t at = (size_t)p.ctas * 2 * p.rows * DP * sizeof(float);
+    p.parts = nullptr;
+    p.tops = reinterpret_cast<float *>(at);
+    at += ((size_t)p.ctas * 2 * p.rows * 2 * sizeof(float) + 15) / 16 * 16;
+    p.items = reinterpret_cast<Item *>(at);
+    *bytes = at + (kMostTiles + 2) * sizeof(Item);
+    return p;
+}
+
+template <int DP>
+cudaError_t launch(const CrossArgs &a, cudaStream_t stream)
+{
+    using L = Layout<DP>;
+    static_assert(L::BYTES <= 232448 && L::BARS % 8 == 0 && L::ITEMS % 16 == 0, "shared memory");
+    size_t bytes;
+    Plan p = plan_of(a.T, a.Hq, a.heads, DP, &bytes);
+    char *ws = static_cast<char *>(a.ws);
+    p.parts = reinterpret_cast<float *>(ws);
+    p.tops = reinterpret_cast<float *>(ws + reinterpret_cast<size_t>(p.tops));
+    p.items = reinterpret_cast<Item *>(ws + reinterpret_cast<size_t>(p.items));
+    p.negative = a.scale < 0.0f;
+    CUtensorMap mq, mk, mv;
+    cudaError_t e = row_map(&mq, a.q, a.T, a.Hq, a.dim, a.qs, a.Hq / a.heads, p.tokens_a_tile);
+    if (e == cudaSuccess)
+        e = row_map(&mk, a.k, a.S, a.heads, a.dim, a.ks, 1, kTile);
+    if (e == cudaSuccess)
+        e = row_map(&mv, a.v, a.S, a.heads, a.dim, a.vs, 1, kTile);
+    static std::atomic<unsigned long long> allowed;
+    if (e == cudaSuccess)
+        e = tc::allow_smem(cross_forward_kernel<DP>, L::BYTES, allowed);
+    if (e == cudaSuccess)
+        e = tc::launch_pdl(cross_forward_kernel<DP>, dim3(p.ctas), dim3(kThreads), L::BYTES, stream, mq, mk, mv, a, p);
+    if (e == cudaSuccess)
+        e = tc::launch_pdl(cross_join_kernel<DP>, dim3(p.tiles * a.heads, (p.rows + kJoinRows - 1) / kJoinRows), dim3(kJoinWarps * 32), 0, stream, a, p);
+    return e;
+}
 
 }  // namespace
 
-size_t cross_attention_workspace(int64_t, int64_t, int64_t, int64_t, int64_t) { return 16; }
-
-cudaError_t launch_cross_attention(const CrossArgs &a, cudaStream_t stream)
+size_t cross_attention_workspace(int64_t T, int64_t, int64_t Hq, int64_t heads, int64_t dim)
 {
-    cross_forward_kernel<<<blocks((int64_t)a.T * a.Hq), kWarps * 32, 0, stream>>>(a);
-    return cudaGetLastError();
+    size_t bytes;
+    plan_of(T, Hq, heads, dim > 64 ? 128 : 64, &bytes);
+    return bytes;
 }
 
-size_t cross_attention_backward_workspace(int64_t T, int64_t, int64_t Hq, int64_t, int64_t) { return (size_t)(T * Hq) * sizeof(float) + 16; }
-
-cudaError_t launch_cross_attention_backward(const CrossArgs &a, cudaStream_t stream)
+cudaError_t launch_cross_attention(const CrossArgs &all, cudaStream_t stream)
 {
-    if (a.T > 0)
-        cross_dq_kernel<<<blocks((int64_t)a.T * a.Hq), kWarps * 32, 0, stream>>>(a);
-    if (a.S > 0)
-        cross_dkv_kernel<<<blocks((int64_t)a.S * a.heads), kWarps * 32, 0, stream>>>(a);
-    return cudaGetLastError();
+    if (all.S == 0) {
+        cross_nothing_kernel<<<device_sm_count(), 256, 0, stream>>>(all);
+        return cudaGetLastError();
+    }
+    const int64_t step = (int64_t)kMostTiles * (kTile / (all.Hq / all.heads));
+    for (int64_t t = 0; t < all.T; t += step) {
+        CrossArgs a = all;
+        a.T = (int)(all.T - t < step ? all.T - t : step);
+        a.q += t * a.qs[0];
+        a.out += t * a.Hq * a.dim;
+        a.lse = a.lse ? a.lse + t * a.Hq : nullptr;
+        a.spans = a.spans ? a.spans + 2 * t : nullptr;
+        const cudaError_t e = a.dim > 64 ? launch<128>(a, stream) : launch<64>(a, stream);
+        if (e != cudaSuccess)
+            return e;
+    }
+    return cudaSuccess;
 }
 
 }  // namespace s3d8
