@@ -39,12 +39,7 @@ constexpr int kThreads = 384;
 constexpr int kMostTiles = 1024;        // query tiles of a launch
 constexpr int kJoinWarps = 8, kJoinRows = 32;
 
-// A piece of the work: query tile a (and b, with the same states), state tiles j0 and on;
-// `begin`: state tiles of one key/value head in front of it.
-struct Item {
-    int tiles, j0, begin, end_;
-};
-constexpr int kNoTile = 0xFFFF;
+constexpr int kNoTile = 0xFFFF;         // of the two query tiles of a piece, low and high half of its `tile`
 
 struct Plan {
     int tokens_a_tile, tiles, rows;     // rows: of a slot of partial sums
@@ -61,61 +56,28 @@ struct Layout {
     static constexpr int TILE = kTile * DP * 2;             // bytes of a tile of Q, K or V
     static constexpr int STAGES = DP == 128 ? 4 : 8;
     static constexpr int Q = 0, KV = 2 * TILE, ITEMS = KV + STAGES * TILE;
-    static constexpr int RANGES = ITEMS + (kMostTiles + 1) * (int)sizeof(Item);     // of the query tiles, while the list is made
+    static constexpr int RANGES = ITEMS + ((kMostTiles + 1) * (int)sizeof(Item) + 15) / 16 * 16;     // of the query tiles, while the list is made
     static constexpr int BAD = RANGES + kMostTiles * 8;     // [2][128][8]: columns of +inf, of -inf
     static constexpr int TOPS = BAD + 2 * 128 * 32;         // [128] maximum and sum of the second chain
     static constexpr int BARS = TOPS + 128 * 8;
     static constexpr int BYTES = 1024 + BARS + 512;
 };
 
-struct Unit {
-    int ta, tb, head, j0, n, slot;      // slot: -1 for a whole piece, else where its sums go
+// A piece of a CTA's share: query tile a (and b, with the same states).
+struct Unit : Piece {
+    int ta, tb;
     bool pair;
 };
 
-// How many CTAs have a share: none of them an empty one.
-__device__ __forceinline__ int64_t busy(int ctas, int64_t all) { return all < ctas ? all : ctas; }
-
-// The CTA's share of the work, piece by piece.
-struct Share {
-    const Item *items;
-    int n_items, per_head;
-    int64_t at, first, end;
-
-    __device__ __forceinline__ Share(const Item *list, int n, int heads, int ctas)
-        : items(list), n_items(n), per_head(list[n].begin)
-    {
-        const int64_t all = (int64_t)heads * per_head, some = busy(ctas, all);
-        first = at = blockIdx.x < some ? all * blockIdx.x / some : 0;
-        end = blockIdx.x < some ? all * (blockIdx.x + 1) / some : 0;
-    }
-
-    __device__ __forceinline__ bool next(Unit &u)
-    {
-        if (at >= end)
-            return false;
-        u.head = (int)(at / per_head);
-        const int r = (int)(at - (int64_t)u.head * per_head);
-        int lo = 0, hi = n_items;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (items[mid].begin <= r)
-                lo = mid;
-            else
-                hi = mid;
-        }
-        const Item it = items[lo];
-        const int off = r - it.begin, left = items[lo + 1].begin - r;
-        u.ta = it.tiles & 0xFFFF;
-        u.tb = it.tiles >> 16 & 0xFFFF;
-        u.pair = u.tb != kNoTile;
-        u.j0 = it.j0 + off;
-        u.n = (int)(end - at < left ? end - at : left);
-        u.slot = off == 0 && u.n == left ? -1 : at != first;
-        at += u.n;
-        return true;
-    }
-};
+__device__ __forceinline__ bool next_unit(Share &share, Unit &u)
+{
+    if (!share.next(u))
+        return false;
+    u.ta = u.tile & 0xFFFF;
+    u.tb = u.tile >> 16 & 0xFFFF;
+    u.pair = u.tb != kNoTile;
+    return true;
+}
 
 // The list of work: for each pair of query tiles whether they go together.  One warp.
 __device__ __forceinline__ int make_items(const int2 *ranges, int tiles, Item *items)
@@ -154,18 +116,16 @@ __device__ __forceinline__ int make_items(const int2 *ranges, int tiles, Item *i
                 c += pc, s += ps;
         }
         if (n)
-            items[count + c - n] = {a | (pair ? b : kNoTile) << 16, a0, begin + s - size, 0};
+            items[count + c - n] = {a | (pair ? b : kNoTile) << 16, a0, begin + s - size};
         if (n == 2)
-            items[count + c - 1] = {b | kNoTile << 16, b0, begin + s - (b1 - b0), 0};
+            items[count + c - 1] = {b | kNoTile << 16, b0, begin + s - (b1 - b0)};
         count += __shfl_sync(0xffffffffu, c, 31);
         begin += __shfl_sync(0xffffffffu, s, 31);
     }
     if (lane == 0)
-        items[count] = {0, 0, begin, 0};
+        items[count] = {0, 0, begin};
     return count;
 }
-
-__device__ __forceinline__ bool finite2(uint32_t top) { return (top & 0xFFFFu) < 0x7F80u && (top >> 16) < 0x7F80u; }
 
 // Looks over a state tile's values (in shared memory at v): a row a thread at a time.
 // What is not finite becomes zero, and is noted for the rows that see its state.
@@ -176,14 +136,14 @@ __device__ __forceinline__ void look_over(uint32_t v, int c0, const CrossArgs &a
         uint32_t top = 0;
 #pragma unroll
         for (int c = 0; c < DP / 8; ++c) {
-            const uint4 x = lds_v4(v + (c >> 3) * (kTile * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
+            const uint4 x = lds_v4(chunk_at(v, r, c));
             top = absmax_bf16x8(x, top);
         }
         if (finite2(top))
             continue;
         uint32_t plus[4] = {0, 0, 0, 0}, minus[4] = {0, 0, 0, 0};       // NaN: both
         for (int c = 0; c < DP / 8; ++c) {
-            const uint32_t at = v + (c >> 3) * (kTile * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+            const uint32_t at = chunk_at(v, r, c);
             for (int e = 0; e < 8; ++e) {
                 uint16_t x;
                 asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(at + 2 * e));
@@ -306,7 +266,7 @@ __global__ __launch_bounds__(kThreads, 1) void cross_forward_kernel(const __grid
         asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         if (warp == 0) {                // copies
             int at = 0;                 // tiles of K and V so far
-            for (int units = 0; ok && share.next(u); ++units) {
+            for (int units = 0; ok && next_unit(share, u); ++units) {
                 if (units > 0 && !(ok = tc::warp_wait(q_empty, (units - 1) & 1)))
                     break;
                 tc::mbar_arrive_expect_tx_elect(q_full, (u.pair ? 2 : 1) * L::CHUNKS * 128 * p.chunk_rows);
@@ -330,7 +290,7 @@ __global__ __launch_bounds__(kThreads, 1) void cross_forward_kernel(const __grid
             const int ksteps = (a.dim + 15) / 16, n_out = ksteps * 16;
             const uint32_t id_s = idesc_cols(kTile) | (p.negative ? kNegateA : 0u), id_o = idesc_rows(n_out);
             int at = 0, jobs[2] = {0, 0};       // K/V tiles, and products with V of each chain, so far
-            for (int units = 0; ok && share.next(u); ++units) {
+            for (int units = 0; ok && next_unit(share, u); ++units) {
                 const int n = u.pair ? 2 * u.n : u.n;
                 if (!(ok = tc::warp_wait(q_full, units & 1)))
                     break;
@@ -374,7 +334,7 @@ __global__ __launch_bounds__(kThreads, 1) void cross_forward_kernel(const __grid
             }
         } else if (warp < 4) {          // looks the values over
             int at = 0;
-            for (int units = 0; ok && share.next(u); ++units) {
+            for (int units = 0; ok && next_unit(share, u); ++units) {
                 // the states that every row with any sees
                 int lo = 0, hi = 0x7FFFFFFF;
                 for (int s = 0; s < (u.pair ? 2 : 1); ++s)
@@ -411,7 +371,7 @@ __global__ __launch_bounds__(kThreads, 1) void cross_forward_kernel(const __grid
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21), sc = lanes + s * 128, oc = lanes + 256 + s * 128;
         const float scale = fmaxf(fabsf(a.scale) * kLog2e, 1e-30f);      // not 0: a hidden score is -inf
         int jobs = 0;
-        for (int units = 0; ok && share.next(u); ++units) {
+        for (int units = 0; ok && next_unit(share, u); ++units) {
             const int tile = u.pair && s ? u.tb : u.ta, t = tile * p.tokens_a_tile + row / group;
             const bool live = row < p.chunk_rows && t < a.T;
             const int2 see = live ? span_of(a.spans, a.S, t, nullptr) : make_int2(0, 0);
@@ -596,21 +556,17 @@ __global__ __launch_bounds__(kJoinWarps * 32) void cross_join_kernel(const __gri
     const int n = p.items[0].begin, i = blockIdx.x / a.heads, head = blockIdx.x % a.heads;
     if (i >= n)
         return;
-    const Item *items = p.items + 1, it = items[i];
-    const int64_t per_head = items[n].begin, all = per_head * a.heads;
-    const int64_t from = head * per_head + it.begin, to = head * per_head + items[i + 1].begin - 1;
-    const int64_t ctas = busy(p.ctas, all);
-    auto owner = [&](int64_t w) { return (int)(((w + 1) * ctas - 1) / all); };
-    const int c0 = owner(from), c1 = owner(to);
-    if (c0 == c1)
+    const Cut cut(p.items + 1, n, i, head, a.heads, p.ctas);
+    if (cut.c0 == cut.c1)
         return;
-    const int first_slot = from != all * c0 / ctas, group = a.Hq / a.heads, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const Item it = p.items[1 + i];
+    const int c0 = cut.c0, c1 = cut.c1, group = a.Hq / a.heads, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int r = blockIdx.y * kJoinRows + warp; r < blockIdx.y * kJoinRows + kJoinRows && r < p.rows; r += kJoinWarps) {
-        const int tile = r < kTile ? it.tiles & 0xFFFF : it.tiles >> 16 & 0xFFFF, row = r % kTile;
+        const int tile = r < kTile ? it.tile & 0xFFFF : it.tile >> 16 & 0xFFFF, row = r % kTile;
         const int t = tile * p.tokens_a_tile + row / group;
         if (tile == kNoTile || row >= p.chunk_rows || t >= a.T)
             continue;
-        auto slot = [&](int c) { return ((int64_t)c * 2 + (c == c0 ? first_slot : 0)) * p.rows + r; };
+        auto slot = [&](int c) { return cut.slot(c) * p.rows + r; };
         float top = -INFINITY;
         for (int c = c0 + lane; c <= c1; c += 32)
             top = fmaxf(top, p.tops[2 * slot(c)]);

@@ -2,131 +2,874 @@
 //
 //   delta = dout . out, p_j = exp(s_j - lse), ds_j = p_j (dout . v_j - delta)
 //   dq = scale sum_j ds_j k_j, dk_j = scale sum ds_j q, dv_j = sum p_j dout
-#include "common.cuh"
-#include "launch.h"
-#include "tcgen05.cuh"
+//
+// Without atomics, so that equal inputs give equal bits: one kernel passes the states for
+// each tile of 128 query rows (S = Q K^T, dP = dO V^T, dQ += dS K), one the query rows for
+// each tile of 128 states (S^T = K Q^T, dP^T = V dO^T, dV += P^T dO, dK += dS^T Q): seven
+// products where one pass with atomic sums would have five.  Tiles, sums in tensor memory,
+// and shares of the work are as in the forward pass (cross_attention.cu); the two groups of
+// four softmax warps take 64 columns each of every tile, and P and dS go back into tensor
+// memory as bf16 A operands (2^-8 of each, which averages to about the rounding of the
+// gradients).  Products are issued so that the tensor cores have two of them to do while a
+// softmax step runs.
+//
+// A first kernel makes delta and lse ready, a row a half warp, and the range of states that
+// each query tile sees.  Rows of the query tiles or the states that have no part in a tile
+// are taken out of it where they hold infinities or NaN, which a weight of zero would not
+// silence.
+#include "cross_tiles.cuh"
 
 namespace s3d8 {
 
 namespace {
 
-constexpr int kWarps = 4;
+using namespace cross;
 
-__device__ __forceinline__ float warp_sum_f(float v)
-{
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-}
+constexpr int kThreads = 384;
+constexpr int kMostTiles = 1024;        // tiles of a launch that have sums of their own
+constexpr int kJoinWarps = 8;
 
-// Token t's span, within the states; one that is not is cut to them and recorded.
-__device__ __forceinline__ int2 span_of(const CrossArgs &a, int t)
-{
-    if (!a.spans)
-        return make_int2(0, a.S);
-    const int2 s = make_int2(a.spans[2 * (int64_t)t], a.spans[2 * (int64_t)t + 1]);
-    if (s.x >= s.y)
-        return make_int2(0, 0);
-    if (s.x < 0 || s.y > a.S)
-        atomicExch(a.status, kStatusBounds);
-    return make_int2(max(s.x, 0), min(s.y, a.S));
-}
-
-struct Cols {
-    float v[4];
+struct Plan {
+    int tokens_a_tile, chunk_rows;      // query rows that a copy fills
+    int q_tiles;                        // in all
+    int first, tiles;                   // of this launch: query tiles or tiles of states
+    int rows, ctas;                     // rows of a slot of partial sums
+    float2 *info;                       // [T * Hq]: -lse in base-2 exponents, -delta
+    int2 *ranges;                       // [q_tiles]: states that some row sees
+    float *parts;                       // [ctas][2][1 or 2][rows][DP]
+    Item *items;                        // the list, for the join (its first entry: how many)
+    int negative;
 };
 
-__device__ __forceinline__ Cols columns(const __nv_bfloat16 *x, int dim)
+// delta and lse of a tile's rows of one key/value head, and the tile's range.
+__global__ __launch_bounds__(256) void cross_ready_kernel(const __grid_constant__ CrossArgs a, const __grid_constant__ Plan p)
 {
-    Cols c;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int d = (threadIdx.x & 31) + 32 * i;
-        c.v[i] = d < dim ? __bfloat162float(x[d]) : 0.0f;
+    tc::pdl_launch_dependents();
+    tc::pdl_wait();
+    const int tile = blockIdx.x, head = blockIdx.y, group = a.Hq / a.heads, half = threadIdx.x >> 4, lane = threadIdx.x & 15;
+    const int t0 = tile * p.tokens_a_tile;
+    if (head == 0 && threadIdx.x < 32) {
+        int lo = 0x7FFFFFFF, hi = 0;
+        for (int i = threadIdx.x; i < p.tokens_a_tile && t0 + i < a.T; i += 32) {
+            const int2 s = span_of(a.spans, a.S, t0 + i, a.status);
+            if (s.x < s.y)
+                lo = min(lo, s.x), hi = max(hi, s.y);
+        }
+        lo = __reduce_min_sync(0xffffffffu, lo);
+        hi = __reduce_max_sync(0xffffffffu, hi);
+        if (threadIdx.x == 0)
+            p.ranges[tile] = make_int2(lo, hi);
     }
-    return c;
-}
-
-__device__ __forceinline__ float dot(const Cols &a, const Cols &b)
-{
-    return warp_sum_f(a.v[0] * b.v[0] + a.v[1] * b.v[1] + a.v[2] * b.v[2] + a.v[3] * b.v[3]);
-}
-
-__device__ __forceinline__ void store(__nv_bfloat16 *x, const Cols &c, float f, int dim)
-{
+#pragma unroll 4
+    for (int r = half; r < kTile; r += 16) {        // whole warps together
+        const int t = t0 + r / group, h = head * group + r % group;
+        const bool live = r < p.chunk_rows && t < a.T;
+        float sum = 0.0f;
+        if (live && 8 * lane < a.dim) {
+            const uint4 x = ldg_stream_v4(a.dout + t * a.ds[0] + h * a.ds[1] + 8 * lane);
+            const uint4 y = ldg_stream_v4(a.out + ((int64_t)t * a.Hq + h) * a.dim + 8 * lane);
+            const uint32_t u[4] = {x.x, x.y, x.z, x.w}, w[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int d = (threadIdx.x & 31) + 32 * i;
-        if (d < dim)
-            x[d] = __float2bfloat16_rn(c.v[i] * f);
-    }
-}
-
-// A warp a (token, query head): dq, and delta for the other kernel.
-__global__ __launch_bounds__(kWarps * 32) void cross_dq_kernel(const __grid_constant__ CrossArgs a)
-{
-    const int64_t row = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    if (row >= (int64_t)a.T * a.Hq)
-        return;
-    const int t = (int)(row / a.Hq), h = (int)(row % a.Hq), g = h / (a.Hq / a.heads);
-    const int2 s = span_of(a, t);
-    const Cols q = columns(a.q + t * a.qs[0] + h * a.qs[1], a.dim), d = columns(a.dout + t * a.ds[0] + h * a.ds[1], a.dim);
-    const float delta = dot(d, columns(a.out + row * a.dim, a.dim)), lse = a.lse[row];
-    Cols acc = {};
-    for (int j = s.x; j < s.y; ++j) {
-        const Cols k = columns(a.k + j * a.ks[0] + g * a.ks[1], a.dim);
-        const float p = expf(a.scale * dot(q, k) - lse), ds = p * (dot(d, columns(a.v + j * a.vs[0] + g * a.vs[1], a.dim)) - delta);
+            for (int e = 0; e < 4; ++e)
+                sum = fmaf(__uint_as_float(u[e] & 0xFFFF0000u), __uint_as_float(w[e] & 0xFFFF0000u),
+                           fmaf(__uint_as_float(u[e] << 16), __uint_as_float(w[e] << 16), sum));
+        }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            acc.v[i] += ds * k.v[i];
-    }
-    store(a.dq + row * a.dim, acc, a.scale, a.dim);
-    if ((threadIdx.x & 31) == 0)
-        static_cast<float *>(a.ws)[row] = delta;
-}
-
-// A warp a (state, key/value head).
-__global__ __launch_bounds__(kWarps * 32) void cross_dkv_kernel(const __grid_constant__ CrossArgs a)
-{
-    const int64_t row = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-    if (row >= (int64_t)a.S * a.heads)
-        return;
-    const int j = (int)(row / a.heads), g = (int)(row % a.heads), group = a.Hq / a.heads;
-    const Cols k = columns(a.k + j * a.ks[0] + g * a.ks[1], a.dim), v = columns(a.v + j * a.vs[0] + g * a.vs[1], a.dim);
-    Cols dk = {}, dv = {};
-    for (int t = 0; t < a.T; ++t) {
-        const int2 s = span_of(a, t);
-        if (j < s.x || j >= s.y)
-            continue;
-        for (int h = g * group; h < (g + 1) * group; ++h) {
-            const Cols q = columns(a.q + t * a.qs[0] + h * a.qs[1], a.dim), d = columns(a.dout + t * a.ds[0] + h * a.ds[1], a.dim);
+        for (int o = 8; o > 0; o >>= 1)
+            sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (live && lane == 0) {
             const int64_t at = (int64_t)t * a.Hq + h;
-            const float p = expf(a.scale * dot(q, k) - a.lse[at]), ds = p * (dot(d, v) - static_cast<const float *>(a.ws)[at]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                dk.v[i] += ds * q.v[i];
-                dv.v[i] += p * d.v[i];
-            }
+            const int2 s = span_of(a.spans, a.S, t, nullptr);
+            p.info[at] = s.x < s.y ? make_float2(-a.lse[at] * kLog2e, -sum) : make_float2(-INFINITY, 0.0f);
         }
     }
-    store(a.dk + row * a.dim, dk, a.scale, a.dim);
-    store(a.dv + row * a.dim, dv, 1.0f, a.dim);
 }
 
-unsigned blocks(int64_t rows) { return (unsigned)((rows + kWarps - 1) / kWarps); }
+// The list of work of a launch: for each of its tiles, the tiles of the other kind that have
+// a part in it, or one (of which nothing is seen).  One warp, from each tile's first and end.
+template <typename Range>
+__device__ __forceinline__ int make_list(int tiles, Item *items, Range range)
+{
+    const int lane = threadIdx.x & 31;
+    int begin = 0;
+    for (int base = 0; base < tiles; base += 32) {
+        const int i = base + lane;
+        int2 r = make_int2(0, 0);
+        if (i < tiles) {
+            r = range(i);
+            if (r.x >= r.y)
+                r = make_int2(0, 1);
+        }
+        const int size = r.y - r.x;
+        int s = size;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int ps = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o)
+                s += ps;
+        }
+        if (i < tiles)
+            items[i] = {i, r.x, begin + s - size};
+        begin += __shfl_sync(0xffffffffu, s, 31);
+    }
+    if (lane == 0)
+        items[tiles] = {0, 0, begin};
+    return tiles;
+}
+
+template <int DP>
+struct Layout {
+    static constexpr int CHUNKS = DP / 64;
+    static constexpr int TILE = kTile * DP * 2;
+    static constexpr int STAGES = DP == 128 ? 4 : 8;
+    static constexpr int FIX = 0, RING = 2 * TILE, ITEMS = RING + STAGES * TILE;
+    static constexpr int RANGES = ITEMS + ((kMostTiles + 1) * (int)sizeof(Item) + 15) / 16 * 16;   // [tiles] while the list is made
+    static constexpr int INFO = RANGES + kMostTiles * 8;        // [STAGES / 2][4][128]: -lse, -delta, span
+    static constexpr int FULL = INFO + STAGES / 2 * 4 * kTile * 4;      // [STAGES / 2][2]
+    static constexpr int BARS = FULL + STAGES / 2 * 8;
+    static constexpr int BYTES = 1024 + BARS + 512;
+};
+
+__device__ __forceinline__ void setup_common(uint32_t *tmem_slot, int warp)
+{
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(tmem_slot)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+}
+
+// A row of 128-byte swizzled chunks that holds an infinity or NaN.
+template <int DP>
+__device__ __forceinline__ bool bad_row(uint32_t tile, int r)
+{
+    uint32_t top = 0;
+#pragma unroll
+    for (int c = 0; c < DP / 8; ++c)
+        top = absmax_bf16x8(lds_v4(chunk_at(tile, r, c)), top);
+    return !finite2(top);
+}
+
+template <int DP>
+__device__ __forceinline__ void clear_row(uint32_t tile, int r)
+{
+    for (int c = 0; c < DP / 8; ++c)
+        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(chunk_at(tile, r, c)), "r"(0u) : "memory");
+}
+
+// 32 columns of sums: times `by`, as bf16 to `out` (those below dim), or as they are to `part`.
+__device__ __forceinline__ void put32(const float *o, int c, int dim, float by, __nv_bfloat16 *out, float *part)
+{
+    if (part) {
+#pragma unroll
+        for (int e = 0; e < 32; e += 4)
+            *reinterpret_cast<float4 *>(part + c + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 32; e += 8)
+        if (c + e < dim)
+            *reinterpret_cast<uint4 *>(out + c + e) = make_uint4(pack2(o[e] * by, o[e + 1] * by), pack2(o[e + 2] * by, o[e + 3] * by),
+                                                                 pack2(o[e + 4] * by, o[e + 5] * by), pack2(o[e + 6] * by, o[e + 7] * by));
+}
+
+// ---- dq ---------------------------------------------------------------------
+
+// Tensor memory: S 128 columns, dP twice 128 (dS over each), dQ.
+template <int DP>
+__global__ __launch_bounds__(kThreads, 1) void cross_dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_d,
+                                                               const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                                                               const __grid_constant__ CrossArgs a, const __grid_constant__ Plan p)
+{
+    using L = Layout<DP>;
+    extern __shared__ unsigned char cross_mem[];
+    __shared__ uint32_t tmem_slot;
+    const uint32_t base = (smem_addr(cross_mem) + 1023u) & ~1023u;
+    unsigned char *mem = cross_mem + (base - smem_addr(cross_mem));
+    Item *items = reinterpret_cast<Item *>(mem + L::ITEMS);
+    const uint32_t bars = base + L::BARS;
+    const uint32_t q_full = bars, q_empty = bars + 8, o_free = bars + 16, s_full = bars + 24, s_read = bars + 32, done = bars + 40;
+    const uint32_t dp_full = bars + 48, ds_ready = bars + 64;       // two each: of either buffer
+    const uint32_t kv_full = bars + 80, kv_empty = kv_full + 8 * L::STAGES, k_ok = kv_empty + 8 * L::STAGES;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = a.Hq / a.heads;
+    if (threadIdx.x == 0) {
+        mbar_init(q_full, 1);
+        mbar_init(q_empty, 1);
+        mbar_init(o_free, 8);
+        mbar_init(s_full, 1);
+        mbar_init(s_read, 8);
+        mbar_init(done, 1);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(dp_full + 8 * s, 1);
+            mbar_init(ds_ready + 8 * s, 8);
+        }
+        for (int s = 0; s < L::STAGES; ++s) {
+            mbar_init(kv_full + 8 * s, 1);
+            mbar_init(kv_empty + 8 * s, 1);
+            mbar_init(k_ok + 8 * s, 2);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    setup_common(&tmem_slot, warp);
+    if (p.chunk_rows < kTile)       // rows that no copy fills are zeros
+        for (int i = threadIdx.x; i < 2 * L::TILE / 16; i += kThreads)
+            reinterpret_cast<uint4 *>(mem + L::FIX)[i] = make_uint4(0u, 0u, 0u, 0u);
+    fence_proxy_async_smem();
+    __syncthreads();
+    tc::pdl_launch_dependents();
+    tc::pdl_wait();
+    if (warp == 0) {
+        make_list(p.tiles, items, [&](int i) {
+            const int2 r = p.ranges[p.first + i];
+            return make_int2(r.x / kTile, (r.y + kTile - 1) / kTile);
+        });
+        __syncwarp();
+        if (blockIdx.x == 0) {
+            for (int i = lane; i <= p.tiles; i += 32)
+                p.items[1 + i] = items[i];
+            if (lane == 0)
+                p.items[0].begin = p.tiles;
+        }
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    Share share(items, p.tiles, a.heads, p.ctas);
+    Piece u;
+    bool ok = true;
+
+    if (warp == 0) {                // copies
+        int at = 0;
+        for (int units = 0; ok && share.next(u); ++units) {
+            if (units > 0 && !(ok = tc::warp_wait(q_empty, (units - 1) & 1)))
+                break;
+            tc::mbar_arrive_expect_tx_elect(q_full, 2 * L::CHUNKS * 128 * p.chunk_rows);
+            for (int s = 0; s < 2; ++s)
+                for (int c = 0; c < L::CHUNKS; ++c)
+                    tma_3d_elect(base + L::FIX + s * L::TILE + c * (kTile * 128), s ? &map_d : &map_q, 64 * c, u.head * group,
+                                 (p.first + u.tile) * p.tokens_a_tile, q_full);
+            for (int i = 0; ok && i < 2 * u.n; ++i, ++at) {
+                const int st = at % L::STAGES;
+                if (at >= L::STAGES && !(ok = tc::warp_wait(kv_empty + 8 * st, (at / L::STAGES - 1) & 1)))
+                    break;
+                tc::mbar_arrive_expect_tx_elect(kv_full + 8 * st, L::TILE);
+                for (int c = 0; c < L::CHUNKS; ++c)
+                    tma_3d_elect(base + L::RING + st * L::TILE + c * (kTile * 128), i & 1 ? &map_v : &map_k, 64 * c, u.head, (u.j0 + (i >> 1)) * kTile,
+                                 kv_full + 8 * st);
+            }
+        }
+        for (int i = at - L::STAGES < 0 ? 0 : at - L::STAGES; i < at; ++i)      // not before the last copies have landed
+            ok &= tc::warp_wait(kv_full + 8 * (i % L::STAGES), (i / L::STAGES) & 1);
+    } else if (warp == 1) {         // products
+        const int ksteps = (a.dim + 15) / 16;
+        const uint32_t id_s = idesc_cols(kTile) | (p.negative ? kNegateA : 0u), id_p = idesc_cols(kTile), id_o = idesc_rows(ksteps * 16);
+        int at = 0, jobs = 0;
+        for (int units = 0; ok && share.next(u); ++units) {
+            if (!(ok = tc::warp_wait(q_full, units & 1)))
+                break;
+            for (int j = 0; ok && j <= u.n; ++j) {
+                if (j < u.n) {
+                    const int k = at + 2 * j, ks = k % L::STAGES, v = k + 1, vs = v % L::STAGES, job = jobs + j;
+                    if (!(ok = tc::warp_wait(k_ok + 8 * ks, (k / L::STAGES) & 1)))
+                        break;
+                    if (job > 0 && !(ok = tc::warp_wait(s_read, (job - 1) & 1)))
+                        break;
+                    tc::tc_fence_after();
+                    for (int kk = 0; kk < ksteps; ++kk) {
+                        const uint32_t off = (kk >> 2) * (kTile * 128) + (kk & 3) * 32;
+                        tc::mma_bf16_elect(tmem, tc::sw128_desc(base + L::FIX + off), tc::sw128_desc(base + L::RING + ks * L::TILE + off), id_s, kk > 0);
+                    }
+                    tc::mma_commit_elect(s_full);
+                    if (!(ok = tc::warp_wait(k_ok + 8 * vs, (v / L::STAGES) & 1)))
+                        break;
+                    tc::tc_fence_after();
+                    for (int kk = 0; kk < ksteps; ++kk) {
+                        const uint32_t off = (kk >> 2) * (kTile * 128) + (kk & 3) * 32;
+                        tc::mma_bf16_elect(tmem + 128 + (job & 1) * 128, tc::sw128_desc(base + L::FIX + L::TILE + off),
+                                           tc::sw128_desc(base + L::RING + vs * L::TILE + off), id_p, kk > 0);
+                    }
+                    tc::mma_commit_elect(dp_full + 8 * (job & 1));
+                    tc::mma_commit_elect(kv_empty + 8 * vs);
+                    if (j == u.n - 1)
+                        tc::mma_commit_elect(q_empty);
+                }
+                if (j > 0) {
+                    const int k = at + 2 * (j - 1), ks = k % L::STAGES, job = jobs + j - 1;
+                    if (j == 1 && units > 0 && !(ok = tc::warp_wait(o_free, (units - 1) & 1)))
+                        break;
+                    if (!(ok = tc::warp_wait(ds_ready + 8 * (job & 1), (job >> 1) & 1)))
+                        break;
+                    tc::tc_fence_after();
+                    for (int kk = 0; kk < kTile / 16; ++kk)
+                        mma_tmem_a_elect(tmem + 384, tmem + 128 + (job & 1) * 128 + (kk >> 2) * 64 + (kk & 3) * 8,
+                                         rows_desc(base + L::RING + ks * L::TILE + kk * 2048, kTile * 128), id_o, j > 1 || kk > 0);
+                    tc::mma_commit_elect(kv_empty + 8 * ks);
+                    if (j == u.n)
+                        tc::mma_commit_elect(done);
+                }
+            }
+            at += 2 * u.n;
+            jobs += u.n;
+        }
+    } else if (warp < 4) {          // looks the keys over
+        int at = 0;
+        while (ok && share.next(u)) {
+            const int t0 = (p.first + u.tile) * p.tokens_a_tile;
+            int lo = 0, hi = 0x7FFFFFFF;        // the states that every row with any sees
+            for (int i = lane; i < p.tokens_a_tile && t0 + i < a.T; i += 32) {
+                const int2 see = span_of(a.spans, a.S, t0 + i, nullptr);
+                if (see.x < see.y)
+                    lo = max(lo, see.x), hi = min(hi, see.y);
+            }
+            lo = __reduce_max_sync(0xffffffffu, lo);
+            hi = __reduce_min_sync(0xffffffffu, hi);
+            for (int i = 0; i < 2 * u.n; ++i) {
+                const int st = (at + i) % L::STAGES, c0 = (u.j0 + (i >> 1)) * kTile;
+                if (!(ok = tc::warp_wait(kv_full + 8 * st, ((at + i) / L::STAGES) & 1)))
+                    break;
+                if (!(i & 1) && (c0 < lo || c0 + kTile > hi)) {
+                    const uint32_t tile = base + L::RING + st * L::TILE;
+                    for (int r = (warp - 2) * 32 + lane; r < kTile; r += 64) {
+                        if (!bad_row<DP>(tile, r))
+                            continue;
+                        bool seen = false;
+                        for (int y = 0; y < p.tokens_a_tile && t0 + y < a.T; ++y) {
+                            const int2 see = span_of(a.spans, a.S, t0 + y, nullptr);
+                            seen |= see.x <= c0 + r && c0 + r < see.y;
+                        }
+                        if (!seen)
+                            clear_row<DP>(tile, r);
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+                if (lane == 0)
+                    tc::mbar_arrive(k_ok + 8 * st);
+            }
+            at += 2 * u.n;
+        }
+    } else {                        // softmax: a row a thread, 64 columns a group of warps
+        const int half = (warp - 4) >> 2, row = threadIdx.x & 127;
+        const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
+        const float scale = fmaxf(fabsf(a.scale) * kLog2e, 1e-30f);
+        int jobs = 0;
+        for (int units = 0; ok && share.next(u); ++units) {
+            const int t = (p.first + u.tile) * p.tokens_a_tile + row / group;
+            const bool live = row < p.chunk_rows && t < a.T;
+            const int64_t at = (int64_t)t * a.Hq + u.head * group + row % group;
+            const int2 see = live ? span_of(a.spans, a.S, t, nullptr) : make_int2(0, 0);
+            const float2 info = see.x < see.y ? p.info[at] : make_float2(-INFINITY, 0.0f);
+            const float2 scale2 = make_float2(scale, scale), lse2 = make_float2(info.x, info.x), delta2 = make_float2(info.y, info.y);
+            for (int i = 0; i < u.n; ++i, ++jobs) {
+                const int c0 = (u.j0 + i) * kTile + 64 * half;
+                if (!(ok = tc::warp_wait(s_full, jobs & 1)))
+                    break;
+                tc::tc_fence_after();
+                float x[64], y[64];
+                tmem_ld32(lanes + 64 * half, x);
+                tmem_ld32(lanes + 64 * half + 32, x + 32);
+                tmem_wait_ld();
+                tc::tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    tc::mbar_arrive(s_read);
+#pragma unroll
+                for (int c = 0; c < 32; ++c) {
+                    const float2 e = fma2(make_float2(x[2 * c], x[2 * c + 1]), scale2, lse2);
+                    x[2 * c] = ex2(e.x);
+                    x[2 * c + 1] = ex2(e.y);
+                }
+                if (!(ok = tc::warp_wait(dp_full + 8 * (jobs & 1), (jobs >> 1) & 1)))
+                    break;
+                tc::tc_fence_after();
+                const uint32_t dp = lanes + 128 + (jobs & 1) * 128 + 64 * half;
+                tmem_ld32(dp, y);
+                tmem_ld32(dp + 32, y + 32);
+                tmem_wait_ld();
+                uint32_t w[32];
+#pragma unroll
+                for (int c = 0; c < 32; ++c) {
+                    const float2 g = mul2(make_float2(x[2 * c], x[2 * c + 1]), add2(make_float2(y[2 * c], y[2 * c + 1]), delta2));
+                    x[2 * c] = g.x;
+                    x[2 * c + 1] = g.y;
+                }
+                if (!__all_sync(0xffffffffu, see.x <= c0 && see.y >= c0 + 64)) {
+                    const unsigned from = see.x - c0, n = see.y - see.x;
+#pragma unroll
+                    for (int c = 0; c < 64; ++c)
+                        x[c] = c - from < n ? x[c] : 0.0f;
+                }
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                    w[c] = pack2(x[2 * c], x[2 * c + 1]);
+                tmem_st32(dp, w);
+                tmem_wait_st();
+                tc::tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    tc::mbar_arrive(ds_ready + 8 * (jobs & 1));
+            }
+            if (!ok || !(ok = tc::warp_wait(done, units & 1)))
+                break;
+            tc::tc_fence_after();
+            const int64_t slot = ((int64_t)blockIdx.x * 2 + u.slot) * p.rows + row;
+#pragma unroll
+            for (int c = 0; c < DP / 2; c += 32) {
+                float o[32];
+                tmem_ld32(lanes + 384 + half * (DP / 2) + c, o);
+                tmem_wait_ld();
+                if (live)
+                    put32(o, half * (DP / 2) + c, a.dim, a.scale, a.dq + at * a.dim, u.slot < 0 ? nullptr : p.parts + slot * DP);
+            }
+            tc::tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                tc::mbar_arrive(o_free);
+        }
+    }
+    if (!ok)
+        record_timeout(a.status);
+    tc::tc_fence_before();
+    __syncthreads();
+    if (warp == 1)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+// ---- dk, dv -----------------------------------------------------------------
+
+// Tensor memory: S^T (P^T over it), dP^T (dS^T over it), dV, dK, 128 columns each.
+template <int DP>
+__global__ __launch_bounds__(kThreads, 1) void cross_dkv_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_d,
+                                                                const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                                                                const __grid_constant__ CrossArgs a, const __grid_constant__ Plan p)
+{
+    using L = Layout<DP>;
+    constexpr int PAIRS = L::STAGES / 2;        // query tiles that the ring holds
+    extern __shared__ unsigned char cross_mem[];
+    __shared__ uint32_t tmem_slot;
+    const uint32_t base = (smem_addr(cross_mem) + 1023u) & ~1023u;
+    unsigned char *mem = cross_mem + (base - smem_addr(cross_mem));
+    Item *items = reinterpret_cast<Item *>(mem + L::ITEMS);
+    int2 *ranges = reinterpret_cast<int2 *>(mem + L::RANGES);
+    const uint32_t bars = base + L::BARS;
+    const uint32_t kv_full = bars, kv_empty = bars + 8, o_free = bars + 16, s_full = bars + 24, p_ready = bars + 32, dp_full = bars + 40, ds_ready = bars + 48,
+                   done = bars + 56;
+    const uint32_t q_full = bars + 64, q_empty = q_full + 8 * L::STAGES, q_ok = q_empty + 8 * L::STAGES;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = a.Hq / a.heads;
+    if (threadIdx.x == 0) {
+        mbar_init(kv_full, 1);
+        mbar_init(kv_empty, 1);
+        mbar_init(o_free, 8);
+        mbar_init(s_full, 1);
+        mbar_init(p_ready, 8);
+        mbar_init(dp_full, 1);
+        mbar_init(ds_ready, 8);
+        mbar_init(done, 1);
+        for (int s = 0; s < L::STAGES; ++s) {
+            mbar_init(q_full + 8 * s, 1);
+            mbar_init(q_empty + 8 * s, 1);
+            mbar_init(q_ok + 8 * s, 2);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    setup_common(&tmem_slot, warp);
+    if (p.chunk_rows < kTile)
+        for (int i = threadIdx.x; i < L::STAGES * L::TILE / 16; i += kThreads)
+            reinterpret_cast<uint4 *>(mem + L::RING)[i] = make_uint4(0u, 0u, 0u, 0u);
+    fence_proxy_async_smem();
+    __syncthreads();
+    tc::pdl_launch_dependents();
+    tc::pdl_wait();
+    for (int i = threadIdx.x; i < p.tiles; i += kThreads) {       // the query tiles that see something of a tile of states
+        const int c0 = (p.first + i) * kTile;
+        int lo = 0x7FFFFFFF, hi = 0;
+        for (int t = 0; t < p.q_tiles; ++t) {
+            const int2 r = __ldg(p.ranges + t);
+            if (r.x < c0 + kTile && r.y > c0)
+                lo = min(lo, t), hi = t + 1;
+        }
+        ranges[i] = make_int2(lo, hi);
+    }
+    __syncthreads();
+    if (warp == 0) {
+        make_list(p.tiles, items, [&](int i) { return ranges[i]; });
+        __syncwarp();
+        if (blockIdx.x == 0) {
+            for (int i = lane; i <= p.tiles; i += 32)
+                p.items[1 + i] = items[i];
+            if (lane == 0)
+                p.items[0].begin = p.tiles;
+        }
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    Share share(items, p.tiles, a.heads, p.ctas);
+    Piece u;
+    bool ok = true;
+
+    if (warp == 0) {                // copies
+        int at = 0;
+        for (int units = 0; ok && share.next(u); ++units) {
+            if (units > 0 && !(ok = tc::warp_wait(kv_empty, (units - 1) & 1)))
+                break;
+            tc::mbar_arrive_expect_tx_elect(kv_full, 2 * L::TILE);
+            for (int s = 0; s < 2; ++s)
+                for (int c = 0; c < L::CHUNKS; ++c)
+                    tma_3d_elect(base + L::FIX + s * L::TILE + c * (kTile * 128), s ? &map_v : &map_k, 64 * c, u.head, (p.first + u.tile) * kTile, kv_full);
+            for (int i = 0; ok && i < 2 * u.n; ++i, ++at) {
+                const int st = at % L::STAGES;
+                if (at >= L::STAGES && !(ok = tc::warp_wait(q_empty + 8 * st, (at / L::STAGES - 1) & 1)))
+                    break;
+                tc::mbar_arrive_expect_tx_elect(q_full + 8 * st, L::CHUNKS * 128 * p.chunk_rows);
+                for (int c = 0; c < L::CHUNKS; ++c)
+                    tma_3d_elect(base + L::RING + st * L::TILE + c * (kTile * 128), i & 1 ? &map_d : &map_q, 64 * c, u.head * group,
+                                 (u.j0 + (i >> 1)) * p.tokens_a_tile, q_full + 8 * st);
+            }
+        }
+        for (int i = at - L::STAGES < 0 ? 0 : at - L::STAGES; i < at; ++i)
+            ok &= tc::warp_wait(q_full + 8 * (i % L::STAGES), (i / L::STAGES) & 1);
+    } else if (warp == 1) {         // products
+        const int ksteps = (a.dim + 15) / 16;
+        const uint32_t id_s = idesc_cols(kTile) | (p.negative ? kNegateA : 0u), id_p = idesc_cols(kTile), id_o = idesc_rows(ksteps * 16);
+        int at = 0, jobs = 0;
+        for (int units = 0; ok && share.next(u); ++units) {
+            if (!(ok = tc::warp_wait(kv_full, units & 1)))
+                break;
+            auto scores = [&](int j) {
+                const int q = at + 2 * j, qs = q % L::STAGES;
+                if (!(ok = tc::warp_wait(q_ok + 8 * qs, (q / L::STAGES) & 1)))
+                    return;
+                tc::tc_fence_after();
+                for (int kk = 0; kk < ksteps; ++kk) {
+                    const uint32_t off = (kk >> 2) * (kTile * 128) + (kk & 3) * 32;
+                    tc::mma_bf16_elect(tmem, tc::sw128_desc(base + L::FIX + off), tc::sw128_desc(base + L::RING + qs * L::TILE + off), id_s, kk > 0);
+                }
+                tc::mma_commit_elect(s_full);
+            };
+            scores(0);
+            for (int j = 0; ok && j < u.n; ++j, ++jobs) {
+                const int q = at + 2 * j, qs = q % L::STAGES, d = q + 1, ds = d % L::STAGES;
+                if (!(ok = tc::warp_wait(q_ok + 8 * ds, (d / L::STAGES) & 1)))
+                    break;
+                tc::tc_fence_after();
+                for (int kk = 0; kk < ksteps; ++kk) {
+                    const uint32_t off = (kk >> 2) * (kTile * 128) + (kk & 3) * 32;
+                    tc::mma_bf16_elect(tmem + 128, tc::sw128_desc(base + L::FIX + L::TILE + off), tc::sw128_desc(base + L::RING + ds * L::TILE + off), id_p,
+                                       kk > 0);
+                }
+                tc::mma_commit_elect(dp_full);
+                if (j == u.n - 1)
+                    tc::mma_commit_elect(kv_empty);
+                if (j == 0 && units > 0 && !(ok = tc::warp_wait(o_free, (units - 1) & 1)))
+                    break;
+                if (!(ok = tc::warp_wait(p_ready, jobs & 1)))
+                    break;
+                tc::tc_fence_after();
+                for (int kk = 0; kk < kTile / 16; ++kk)
+                    mma_tmem_a_elect(tmem + 256, tmem + (kk >> 2) * 64 + (kk & 3) * 8, rows_desc(base + L::RING + ds * L::TILE + kk * 2048, kTile * 128), id_o,
+                                     j > 0 || kk > 0);
+                tc::mma_commit_elect(q_empty + 8 * ds);
+                if (j + 1 < u.n)
+                    scores(j + 1);
+                if (!ok || !(ok = tc::warp_wait(ds_ready, jobs & 1)))
+                    break;
+                tc::tc_fence_after();
+                for (int kk = 0; kk < kTile / 16; ++kk)
+                    mma_tmem_a_elect(tmem + 384, tmem + 128 + (kk >> 2) * 64 + (kk & 3) * 8, rows_desc(base + L::RING + qs * L::TILE + kk * 2048, kTile * 128),
+                                     id_o, j > 0 || kk > 0);
+                tc::mma_commit_elect(q_empty + 8 * qs);
+                if (j == u.n - 1)
+                    tc::mma_commit_elect(done);
+            }
+            at += 2 * u.n;
+        }
+    } else if (warp < 4) {          // the rows' lse, delta and spans; looks the query rows over
+        int at = 0;
+        while (ok && share.next(u)) {
+            const int c0 = (p.first + u.tile) * kTile;
+            for (int i = 0; ok && i < u.n; ++i) {
+                const int q = at + 2 * i, pair = q / 2 % PAIRS;
+                float2 info[2];
+                int2 see[2];
+                bool all = true;
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const int r = (warp - 2) * 64 + y * 32 + lane, t = (u.j0 + i) * p.tokens_a_tile + r / group;
+                    const bool live = r < p.chunk_rows && t < a.T;
+                    see[y] = live ? span_of(a.spans, a.S, t, nullptr) : make_int2(0, 0);
+                    info[y] = see[y].x < see[y].y ? p.info[(int64_t)t * a.Hq + u.head * group + r % group] : make_float2(-INFINITY, 0.0f);
+                    all &= see[y].x <= c0 && see[y].y >= c0 + kTile;
+                }
+                all = __all_sync(0xffffffffu, all);
+                for (int s = 0; s < 2; ++s) {
+                    const int st = (q + s) % L::STAGES;
+                    if (!(ok = tc::warp_wait(q_full + 8 * st, ((q + s) / L::STAGES) & 1)))
+                        break;
+                    if (s == 0) {       // the tile before in this place is done with: its copy has begun anew
+                        float *to = reinterpret_cast<float *>(mem + L::INFO) + pair * 4 * kTile;
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const int r = (warp - 2) * 64 + y * 32 + lane;
+                            to[r] = info[y].x;
+                            to[kTile + r] = info[y].y;
+                            to[2 * kTile + r] = __int_as_float(see[y].x);
+                            to[3 * kTile + r] = __int_as_float(see[y].y);
+                        }
+                        if (lane == 0)
+                            reinterpret_cast<int *>(mem + L::FULL)[pair * 2 + warp - 2] = all;
+                    }
+                    if (!all) {
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const int r = (warp - 2) * 64 + y * 32 + lane;
+                            const bool part = max(see[y].x, c0) < min(see[y].y, c0 + kTile);
+                            if (!part && bad_row<DP>(base + L::RING + st * L::TILE, r))
+                                clear_row<DP>(base + L::RING + st * L::TILE, r);
+                        }
+                        fence_proxy_async_smem();
+                    }
+                    __syncwarp();
+                    if (lane == 0)
+                        tc::mbar_arrive(q_ok + 8 * st);
+                }
+            }
+            at += 2 * u.n;
+        }
+    } else {                        // softmax: a state a thread, 64 query rows a group of warps
+        const int half = (warp - 4) >> 2, row = threadIdx.x & 127;
+        const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21), sc = lanes + 64 * half, dp = lanes + 128 + 64 * half;
+        const float scale = fmaxf(fabsf(a.scale) * kLog2e, 1e-30f);
+        const float2 scale2 = make_float2(scale, scale);
+        int jobs = 0;
+        for (int units = 0; ok && share.next(u); ++units) {
+            const int j = (p.first + u.tile) * kTile + row;
+            for (int i = 0; i < u.n; ++i, ++jobs) {
+                if (!(ok = tc::warp_wait(s_full, jobs & 1)))
+                    break;
+                tc::tc_fence_after();
+                const int pair = jobs % PAIRS;
+                const uint32_t info = base + L::INFO + (pair * 4 * kTile + 64 * half) * 4;
+                const int *full = reinterpret_cast<const int *>(mem + L::FULL) + pair * 2;
+                const bool whole = full[half] != 0;
+                float x[64], y[64];
+                uint32_t w[32];
+                tmem_ld32(sc, x);
+                tmem_ld32(sc + 32, x + 32);
+                tmem_wait_ld();
+#pragma unroll
+                for (int c = 0; c < 64; c += 4) {
+                    const uint4 l = lds_v4(info + 4 * c);
+                    const float2 e = fma2(make_float2(x[c], x[c + 1]), scale2, make_float2(__uint_as_float(l.x), __uint_as_float(l.y)));
+                    const float2 f = fma2(make_float2(x[c + 2], x[c + 3]), scale2, make_float2(__uint_as_float(l.z), __uint_as_float(l.w)));
+                    x[c] = ex2(e.x), x[c + 1] = ex2(e.y), x[c + 2] = ex2(f.x), x[c + 3] = ex2(f.y);
+                }
+                if (!whole) {
+#pragma unroll
+                    for (int c = 0; c < 64; c += 4) {
+                        const uint4 lo = lds_v4(info + (2 * kTile + c) * 4), hi = lds_v4(info + (3 * kTile + c) * 4);
+                        x[c] = j >= (int)lo.x && j < (int)hi.x ? x[c] : 0.0f;
+                        x[c + 1] = j >= (int)lo.y && j < (int)hi.y ? x[c + 1] : 0.0f;
+                        x[c + 2] = j >= (int)lo.z && j < (int)hi.z ? x[c + 2] : 0.0f;
+                        x[c + 3] = j >= (int)lo.w && j < (int)hi.w ? x[c + 3] : 0.0f;
+                    }
+                }
+#pragma unroll
+                for (int c = 0; c < 32; ++c)
+                    w[c] = pack2(x[2 * c], x[2 * c + 1]);
+                tmem_st32(sc, w);
+                tmem_wait_st();
+                tc::tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    tc::mbar_arrive(p_ready);
+                if (!(ok = tc::warp_wait(dp_full, jobs & 1)))
+                    break;
+                tc::tc_fence_after();
+                tmem_ld32(dp, y);
+                tmem_ld32(dp + 32, y + 32);
+                tmem_wait_ld();
+#pragma unroll
+                for (int c = 0; c < 64; c += 4) {
+                    const uint4 l = lds_v4(info + (kTile + c) * 4);
+                    const float2 e = add2(make_float2(y[c], y[c + 1]), make_float2(__uint_as_float(l.x), __uint_as_float(l.y)));
+                    const float2 f = add2(make_float2(y[c + 2], y[c + 3]), make_float2(__uint_as_float(l.z), __uint_as_float(l.w)));
+                    y[c] = e.x, y[c + 1] = e.y, y[c + 2] = f.x, y[c + 3] = f.y;
+                }
+                if (!whole) {       // not 0 times what an unseen value gives
+#pragma unroll
+                    for (int c = 0; c < 64; ++c)
+                        y[c] = x[c] == 0.0f ? 0.0f : y[c];
+                }
+#pragma unroll
+                for (int c = 0; c < 32; ++c) {
+                    const float2 g = mul2(make_float2(x[2 * c], x[2 * c + 1]), make_float2(y[2 * c], y[2 * c + 1]));
+                    w[c] = pack2(g.x, g.y);
+                }
+                tmem_st32(dp, w);
+                tmem_wait_st();
+                tc::tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    tc::mbar_arrive(ds_ready);
+            }
+            if (!ok || !(ok = tc::warp_wait(done, units & 1)))
+                break;
+            tc::tc_fence_after();
+            const int64_t slot = ((int64_t)blockIdx.x * 2 + u.slot) * 2 * kTile + row, at = ((int64_t)j * a.heads + u.head) * a.dim;
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int c = 0; c < DP / 2; c += 32) {
+                    float o[32];
+                    tmem_ld32(lanes + 256 + s * 128 + half * (DP / 2) + c, o);
+                    tmem_wait_ld();
+                    if (j < a.S)
+                        put32(o, half * (DP / 2) + c, a.dim, s ? a.scale : 1.0f, (s ? a.dk : a.dv) + at,
+                              u.slot < 0 ? nullptr : p.parts + (slot + s * kTile) * DP);
+                }
+            tc::tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                tc::mbar_arrive(o_free);
+        }
+    }
+    if (!ok)
+        record_timeout(a.status);
+    tc::tc_fence_before();
+    __syncthreads();
+    if (warp == 1)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+// Adds the parts of the items that shares cut: a warp a row, in order.  STATES: rows are
+// states (dv and dk, one behind the other in a slot), else query rows.
+template <int DP, bool STATES>
+__global__ __launch_bounds__(kJoinWarps * 32) void cross_add_kernel(const __grid_constant__ CrossArgs a, const __grid_constant__ Plan p)
+{
+    constexpr int V = DP / 32;
+    tc::pdl_launch_dependents();
+    tc::pdl_wait();
+    const int n = p.items[0].begin, i = blockIdx.x / a.heads, head = blockIdx.x % a.heads;
+    const Cut cut(p.items + 1, n, i, head, a.heads, p.ctas);
+    if (cut.c0 == cut.c1)
+        return;
+    const int tile = p.first + p.items[1 + i].tile, group = a.Hq / a.heads, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int slot_rows = STATES ? 2 * kTile : p.rows;
+    for (int r = blockIdx.y * 32 + warp; r < blockIdx.y * 32 + 32 && r < slot_rows; r += kJoinWarps) {
+        const int row = STATES ? r % kTile : r;
+        __nv_bfloat16 *out;
+        float by = a.scale;
+        if (STATES) {
+            const int64_t j = (int64_t)tile * kTile + row;
+            if (j >= a.S)
+                continue;
+            out = (r < kTile ? a.dv : a.dk) + (j * a.heads + head) * a.dim;
+            by = r < kTile ? 1.0f : a.scale;
+        } else {
+            const int64_t t = (int64_t)tile * p.tokens_a_tile + row / group;
+            if (row >= p.chunk_rows || t >= a.T)
+                continue;
+            out = a.dq + (t * a.Hq + head * group + row % group) * a.dim;
+        }
+        float acc[V] = {};
+        for (int c = cut.c0; c <= cut.c1; ++c) {
+            const float *part = p.parts + (cut.slot(c) * slot_rows + r) * DP + lane;
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                acc[v] += part[32 * v];
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (lane + 32 * v < a.dim)
+                out[lane + 32 * v] = __float2bfloat16_rn(acc[v] * by);
+    }
+}
+
+// Where the workspace's parts are (the pointers as offsets), and how long it is.
+Plan plan_of(int64_t T, int64_t Hq, int64_t heads, int DP, size_t *bytes)
+{
+    Plan p;
+    const int group = (int)(Hq / heads);
+    p.tokens_a_tile = kTile / group;
+    p.chunk_rows = p.tokens_a_tile * group;
+    p.q_tiles = (int)((T + p.tokens_a_tile - 1) / p.tokens_a_tile);
+    p.rows = T * group < kTile ? (int)(T * group) : kTile;
+    p.ctas = device_sm_count();
+    p.first = p.tiles = p.negative = 0;
+    size_t at = 0;
+    auto take = [&](size_t n) {
+        const size_t from = at;
+        at += (n + 15) / 16 * 16;
+        return from;
+    };
+    p.info = reinterpret_cast<float2 *>(take((size_t)T * Hq * sizeof(float2)));
+    p.ranges = reinterpret_cast<int2 *>(take((size_t)p.q_tiles * sizeof(int2)));
+    p.parts = reinterpret_cast<float *>(take((size_t)p.ctas * 2 * 2 * kTile * DP * sizeof(float)));
+    p.items = reinterpret_cast<Item *>(take((kMostTiles + 2) * sizeof(Item)));
+    *bytes = at;
+    return p;
+}
+
+template <int DP>
+cudaError_t launch(const CrossArgs &a, cudaStream_t stream)
+{
+    using L = Layout<DP>;
+    static_assert(L::BYTES <= 232448 && L::BARS % 8 == 0 && L::INFO % 16 == 0, "shared memory");
+    size_t bytes;
+    Plan p = plan_of(a.T, a.Hq, a.heads, DP, &bytes);
+    char *ws = static_cast<char *>(a.ws);
+    p.info = reinterpret_cast<float2 *>(ws + reinterpret_cast<size_t>(p.info));
+    p.ranges = reinterpret_cast<int2 *>(ws + reinterpret_cast<size_t>(p.ranges));
+    p.parts = reinterpret_cast<float *>(ws + reinterpret_cast<size_t>(p.parts));
+    p.items = reinterpret_cast<Item *>(ws + reinterpret_cast<size_t>(p.items));
+    p.negative = a.scale < 0.0f;
+    CUtensorMap mq, md, mk, mv;
+    cudaError_t e = row_map(&mq, a.q, a.T, a.Hq, a.dim, a.qs, a.Hq / a.heads, p.tokens_a_tile);
+    if (e == cudaSuccess)
+        e = row_map(&md, a.dout, a.T, a.Hq, a.dim, a.ds, a.Hq / a.heads, p.tokens_a_tile);
+    if (e == cudaSuccess)
+        e = row_map(&mk, a.k, a.S, a.heads, a.dim, a.ks, 1, kTile);
+    if (e == cudaSuccess)
+        e = row_map(&mv, a.v, a.S, a.heads, a.dim, a.vs, 1, kTile);
+    static std::atomic<unsigned long long> allowed_q, allowed_kv;
+    if (e == cudaSuccess)
+        e = tc::allow_smem(cross_dq_kernel<DP>, L::BYTES, allowed_q);
+    if (e == cudaSuccess)
+        e = tc::allow_smem(cross_dkv_kernel<DP>, L::BYTES, allowed_kv);
+    if (e == cudaSuccess)
+        e = tc::launch_pdl(cross_ready_kernel, dim3(p.q_tiles, a.heads), dim3(256), 0, stream, a, p);
+    for (p.first = 0; e == cudaSuccess && p.first < p.q_tiles; p.first += kMostTiles) {
+        p.tiles = p.q_tiles - p.first < kMostTiles ? p.q_tiles - p.first : kMostTiles;
+        e = tc::launch_pdl(cross_dq_kernel<DP>, dim3(p.ctas), dim3(kThreads), L::BYTES, stream, mq, md, mk, mv, a, p);
+        if (e == cudaSuccess)
+            e = tc::launch_pdl(cross_add_kernel<DP, false>, dim3(p.tiles * a.heads, (p.rows + 31) / 32), dim3(kJoinWarps * 32), 0, stream, a, p);
+    }
+    const int tiles = (a.S + kTile - 1) / kTile;
+    for (p.first = 0; e == cudaSuccess && p.first < tiles; p.first += kMostTiles) {
+        p.tiles = tiles - p.first < kMostTiles ? tiles - p.first : kMostTiles;
+        e = tc::launch_pdl(cross_dkv_kernel<DP>, dim3(p.ctas), dim3(kThreads), L::BYTES, stream, mq, md, mk, mv, a, p);
+        if (e == cudaSuccess)
+            e = tc::launch_pdl(cross_add_kernel<DP, true>, dim3(p.tiles * a.heads, 2 * kTile / 32), dim3(kJoinWarps * 32), 0, stream, a, p);
+    }
+    return e;
+}
 
 }  // namespace
 
-size_t cross_attention_backward_workspace(int64_t T, int64_t, int64_t Hq, int64_t, int64_t) { return (size_t)(T * Hq) * sizeof(float) + 16; }
+size_t cross_attention_backward_workspace(int64_t T, int64_t, int64_t Hq, int64_t heads, int64_t dim)
+{
+    size_t bytes;
+    plan_of(T, Hq, heads, dim > 64 ? 128 : 64, &bytes);
+    return bytes;
+}
 
 cudaError_t launch_cross_attention_backward(const CrossArgs &a, cudaStream_t stream)
 {
-    if (a.T > 0)
-        cross_dq_kernel<<<blocks((int64_t)a.T * a.Hq), kWarps * 32, 0, stream>>>(a);
-    if (a.S > 0)
-        cross_dkv_kernel<<<blocks((int64_t)a.S * a.heads), kWarps * 32, 0, stream>>>(a);
-    return cudaGetLastError();
+    if (a.S == 0)       // (and tokens: their gradients are zero)
+        return cudaMemsetAsync(a.dq, 0, (size_t)a.T * a.Hq * a.dim * sizeof(__nv_bfloat16), stream);
+    return a.dim > 64 ? launch<128>(a, stream) : launch<64>(a, stream);
 }
 
 }  // namespace s3d8

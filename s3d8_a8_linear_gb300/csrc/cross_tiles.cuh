@@ -135,6 +135,88 @@ __device__ __forceinline__ int2 span_of(const int32_t *spans, int S, int t, int 
     return c.x < c.y ? c : make_int2(0, 0);
 }
 
+// ---- work -------------------------------------------------------------------
+
+// A piece of the work of every key/value head: a tile (of query rows, or of states) and the
+// tiles j0 and on of the other kind; `begin`: such tiles of the pieces in front of it.  Lists
+// end with an entry that has only that.
+struct Item {
+    int tile, j0, begin;
+};
+
+struct Piece {
+    int tile, head, j0, n, slot;        // slot: -1 for a whole item, else where its sums go: 0 or 1
+};
+
+// How many CTAs have a share: none of them an empty one.
+__device__ __forceinline__ int64_t busy(int ctas, int64_t all) { return all < ctas ? all : ctas; }
+
+// A CTA's share of the work of all heads: as many tiles as any other's, one behind the
+// other, piece by piece.
+struct Share {
+    const Item *items;
+    int n_items, per_head;
+    int64_t at, first, end;
+
+    __device__ __forceinline__ Share(const Item *list, int n, int heads, int ctas)
+        : items(list), n_items(n), per_head(list[n].begin)
+    {
+        const int64_t all = (int64_t)heads * per_head, some = busy(ctas, all);
+        first = at = blockIdx.x < some ? all * blockIdx.x / some : 0;
+        end = blockIdx.x < some ? all * (blockIdx.x + 1) / some : 0;
+    }
+
+    __device__ __forceinline__ bool next(Piece &u)
+    {
+        if (at >= end)
+            return false;
+        u.head = (int)(at / per_head);
+        const int r = (int)(at - (int64_t)u.head * per_head);
+        int lo = 0, hi = n_items;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (items[mid].begin <= r)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        const Item it = items[lo];
+        const int off = r - it.begin, left = items[lo + 1].begin - r;
+        u.tile = it.tile;
+        u.j0 = it.j0 + off;
+        u.n = (int)(end - at < left ? end - at : left);
+        u.slot = off == 0 && u.n == left ? -1 : at != first;
+        at += u.n;
+        return true;
+    }
+};
+
+// The CTAs whose shares hold parts of item i of a head (c0 == c1: it is whole), and where
+// each has put its part.
+struct Cut {
+    int c0, c1, first_slot;
+
+    __device__ __forceinline__ Cut(const Item *items, int n, int i, int head, int heads, int ctas)
+    {
+        const int64_t per_head = items[n].begin, all = per_head * heads, some = busy(ctas, all);
+        const int64_t from = head * per_head + items[i].begin, to = head * per_head + items[i + 1].begin - 1;
+        c0 = (int)(((from + 1) * some - 1) / all);
+        c1 = (int)(((to + 1) * some - 1) / all);
+        first_slot = from != all * c0 / some;
+    }
+
+    __device__ __forceinline__ int64_t slot(int c) const { return (int64_t)c * 2 + (c == c0 ? first_slot : 0); }
+};
+
+// Whether two packed maxima of |bf16| bits are of finite values.
+__device__ __forceinline__ bool finite2(uint32_t top) { return (top & 0xFFFFu) < 0x7F80u && (top >> 16) < 0x7F80u; }
+
+// Where 16-byte chunk c of row r lies in a tile of 128-byte swizzled rows, 64 columns a block.
+__device__ __forceinline__ uint32_t chunk_at(uint32_t tile, int r, int c)
+{
+    return tile + (c >> 3) * (kTile * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+}
+
 // ---- host -------------------------------------------------------------------
 
 // Rows [n, heads, dim] with strides (row, head) in elements, copied in pieces of `box_rows`
