@@ -127,6 +127,14 @@ __device__ __forceinline__ int make_items(const int2 *ranges, int tiles, Item *i
     return count;
 }
 
+// Scores of columns outside from .. from + n - 1: -inf.
+__device__ __forceinline__ void hide(float (&x)[64], unsigned from, unsigned n)
+{
+#pragma unroll
+    for (int c = 0; c < 64; ++c)
+        x[c] = c - from < n ? x[c] : -INFINITY;
+}
+
 // Looks over a state tile's values (in shared memory at v): a row a thread at a time.
 // What is not finite becomes zero, and is noted for the rows that see its state.
 template <int DP>
@@ -196,8 +204,8 @@ __global__ __launch_bounds__(kThreads, 1) void cross_forward_kernel(const __grid
     uint32_t *bad = reinterpret_cast<uint32_t *>(mem + L::BAD);
     float2 *tops = reinterpret_cast<float2 *>(mem + L::TOPS);
     const uint32_t bars = base + L::BARS;
-    const uint32_t q_full = bars, q_empty = bars + 8, o_free = bars + 16, s_full = bars + 24, p_ready = bars + 40, pv_done = bars + 56;
-    const uint32_t kv_full = bars + 72, kv_empty = kv_full + 8 * L::STAGES, v_ok = kv_empty + 8 * L::STAGES;
+    const uint32_t q_full = bars, q_empty = bars + 8, o_free = bars + 16, s_full = bars + 24, p_ready = bars + 40, pv_done = bars + 56, p_half = bars + 72;
+    const uint32_t kv_full = bars + 88, kv_empty = kv_full + 8 * L::STAGES, v_ok = kv_empty + 8 * L::STAGES;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = a.Hq / a.heads;
 
     if (warp == 0 && lane == 0) {
@@ -206,6 +214,7 @@ __global__ __launch_bounds__(kThreads, 1) void cross_forward_kernel(const __grid
         mbar_init(o_free, 8);
         for (int s = 0; s < 2; ++s) {
             mbar_init(s_full + 8 * s, 1);
+            mbar_init(p_half + 8 * s, 4);
             mbar_init(p_ready + 8 * s, 4);
             mbar_init(pv_done + 8 * s, 1);
         }
@@ -318,13 +327,18 @@ __global__ __launch_bounds__(kThreads, 1) void cross_forward_kernel(const __grid
                         if (!u.pair || !s)
                             if (!(ok = tc::warp_wait(v_ok + 8 * st, (v / L::STAGES) & 1)))
                                 break;
-                        if (!(ok = tc::warp_wait(p_ready + 8 * s, jobs[s] & 1)))
-                            break;
-                        tc::tc_fence_after();
-                        ++jobs[s];
                         const uint32_t vt = base + L::KV + st * L::TILE;
-                        for (int kk = 0; kk < kTile / 16; ++kk)
-                            mma_tmem_a_elect(tmem + 256 + s * 128, tmem + s * 128 + kk * 8, rows_desc(vt + kk * 2048, kTile * 128), id_o, prev >= 2 || kk > 0);
+                        for (int half = 1; ok && half >= 0; --half) {     // the second half of the states is ready first
+                            if (!(ok = tc::warp_wait((half ? p_half : p_ready) + 8 * s, jobs[s] & 1)))
+                                break;
+                            tc::tc_fence_after();
+                            for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
+                                mma_tmem_a_elect(tmem + 256 + s * 128, tmem + s * 128 + half * 64 + (kk & 3) * 8, rows_desc(vt + kk * 2048, kTile * 128), id_o,
+                                                 prev >= 2 || kk != 4);
+                        }
+                        if (!ok)
+                            break;
+                        ++jobs[s];
                         tc::mma_commit_elect(pv_done + 8 * s);
                         if (!u.pair || s)
                             tc::mma_commit_elect(kv_empty + 8 * st);
@@ -382,23 +396,23 @@ __global__ __launch_bounds__(kThreads, 1) void cross_forward_kernel(const __grid
                 if (!(ok = tc::warp_wait(s_full + 8 * s, jobs & 1)))
                     break;
                 tc::tc_fence_after();
-                float x[kTile];
+                float x[64], m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                const bool all = __all_sync(0xffffffffu, see.x <= c0 && see.y >= c0 + kTile);
+                const unsigned from = see.x - c0, n = see.y - see.x;
+                // the second half stays in registers; the first one is read twice
 #pragma unroll
-                for (int c = 0; c < kTile; c += 32)
-                    tmem_ld32(sc + c, x + c);
-                tmem_wait_ld();
-                if (!__all_sync(0xffffffffu, see.x <= c0 && see.y >= c0 + kTile)) {
-                    const unsigned from = see.x - c0, n = see.y - see.x;
+                for (int b = 0; b < kTile; b += 64) {
+                    tmem_ld32(sc + b, x);
+                    tmem_ld32(sc + b + 32, x + 32);
+                    tmem_wait_ld();
+                    if (!all)
+                        hide(x, from - b, n);
 #pragma unroll
-                    for (int c = 0; c < kTile; ++c)
-                        x[c] = c - from < n ? x[c] : -INFINITY;
+                    for (int c = 0; c < 64; c += 4)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            m[e] = fmaxf(m[e], x[c + e]);
                 }
-                float m[4] = {x[0], x[1], x[2], x[3]};
-#pragma unroll
-                for (int c = 4; c < kTile; c += 4)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        m[e] = fmaxf(m[e], x[c + e]);
                 const float peak = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * scale;
                 const bool rise = peak > top + 8.0f || top == -INFINITY;
                 if (__any_sync(0xffffffffu, rise && peak > -INFINITY)) {
@@ -425,20 +439,29 @@ __global__ __launch_bounds__(kThreads, 1) void cross_forward_kernel(const __grid
                 const float shift = top == -INFINITY ? 0.0f : -top;
                 const float2 scale2 = make_float2(scale, scale), shift2 = make_float2(shift, shift);
                 float2 part[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-                uint32_t w[kTile / 2];
 #pragma unroll
-                for (int c = 0; c < kTile / 2; ++c) {
-                    const float2 e = fma2(make_float2(x[2 * c], x[2 * c + 1]), scale2, shift2), y = make_float2(ex2(e.x), ex2(e.y));
-                    part[c & 1] = add2(part[c & 1], y);
-                    w[c] = pack2(y.x, y.y);
+                for (int b = 64; b >= 0; b -= 64) {     // each half of P over its half of the scores
+                    if (b == 0) {
+                        tmem_ld32(sc, x);
+                        tmem_ld32(sc + 32, x + 32);
+                        tmem_wait_ld();
+                        if (!all)
+                            hide(x, from, n);
+                    }
+                    uint32_t w[32];
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) {
+                        const float2 e = fma2(make_float2(x[2 * c], x[2 * c + 1]), scale2, shift2), y = make_float2(ex2(e.x), ex2(e.y));
+                        part[c & 1] = add2(part[c & 1], y);
+                        w[c] = pack2(y.x, y.y);
+                    }
+                    tmem_st32(sc + b, w);
+                    tmem_wait_st();
+                    tc::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        tc::mbar_arrive((b ? p_half : p_ready) + 8 * s);
                 }
-                tmem_st32(sc, w);
-                tmem_st32(sc + 32, w + 32);
-                tmem_wait_st();
-                tc::tc_fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    tc::mbar_arrive(p_ready + 8 * s);
                 part[0] = add2(part[0], part[1]);
                 sum += part[0].x + part[0].y;
             }
