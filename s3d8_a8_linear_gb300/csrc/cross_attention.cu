@@ -35,7 +35,7 @@ namespace {
 
 using namespace cross;
 
-constexpr int kThreads = 384;
+constexpr int kThreads = 512;
 constexpr int kMostTiles = 1024;        // query tiles of a launch
 constexpr int kJoinWarps = 8, kJoinRows = 32;
 
@@ -138,17 +138,18 @@ __device__ __forceinline__ void hide(float (&x)[64], unsigned from, unsigned n)
 // Looks over a state tile's values (in shared memory at v): a row a thread at a time.
 // What is not finite becomes zero, and is noted for the rows that see its state.
 template <int DP>
-__device__ __forceinline__ void look_over(uint32_t v, int c0, const CrossArgs &a, const Plan &p, const Unit &u, uint32_t *bad, int *any, int thread)
+__device__ __forceinline__ void look_over(uint32_t v, int c0, const CrossArgs &a, const Plan &p, const Unit &u, uint32_t *bad, int *any)
 {
-    for (int r = thread; r < kTile; r += 64) {
+    {
+        const int r = threadIdx.x & 127;
         uint32_t top = 0;
-#pragma unroll
+#pragma unroll 8
         for (int c = 0; c < DP / 8; ++c) {
             const uint4 x = lds_v4(chunk_at(v, r, c));
             top = absmax_bf16x8(x, top);
         }
         if (finite2(top))
-            continue;
+            return;
         uint32_t plus[4] = {0, 0, 0, 0}, minus[4] = {0, 0, 0, 0};       // NaN: both
         for (int c = 0; c < DP / 8; ++c) {
             const uint32_t at = chunk_at(v, r, c);
@@ -168,7 +169,7 @@ __device__ __forceinline__ void look_over(uint32_t v, int c0, const CrossArgs &a
         }
         const int j = c0 + r;
         if (j >= a.S)
-            continue;
+            return;
         for (int s = 0; s < (u.pair ? 2 : 1); ++s)
             for (int i = 0; i < p.tokens_a_tile; ++i) {
                 const int t = (s ? u.tb : u.ta) * p.tokens_a_tile + i;
@@ -221,7 +222,7 @@ __global__ __launch_bounds__(kThreads, 1) void cross_forward_kernel(const __grid
         for (int s = 0; s < L::STAGES; ++s) {
             mbar_init(kv_full + 8 * s, 1);
             mbar_init(kv_empty + 8 * s, 1);
-            mbar_init(v_ok + 8 * s, 2);
+            mbar_init(v_ok + 8 * s, 4);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -270,9 +271,9 @@ __global__ __launch_bounds__(kThreads, 1) void cross_forward_kernel(const __grid
     Unit u;
     bool ok = true;
 
-    // registers: 128 x 88 + 256 x 208 = 384 x 168
+    // registers: 128 x (56 + 48) + 256 x 200 = 512 x 126
     if (warp < 4) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (warp == 0) {                // copies
             int at = 0;                 // tiles of K and V so far
             for (int units = 0; ok && next_unit(share, u); ++units) {
@@ -295,58 +296,66 @@ __global__ __launch_bounds__(kThreads, 1) void cross_forward_kernel(const __grid
             // not before the last copies have landed
             for (int i = at - L::STAGES < 0 ? 0 : at - L::STAGES; i < at; ++i)
                 ok &= tc::warp_wait(kv_full + 8 * (i % L::STAGES), (i / L::STAGES) & 1);
-        } else if (warp == 1) {         // products
-            const int ksteps = (a.dim + 15) / 16, n_out = ksteps * 16;
-            const uint32_t id_s = idesc_cols(kTile) | (p.negative ? kNegateA : 0u), id_o = idesc_rows(n_out);
-            int at = 0, jobs[2] = {0, 0};       // K/V tiles, and products with V of each chain, so far
+        } else if (warp == 1) {         // scores, a chain after the other
+            const int ksteps = (a.dim + 15) / 16;
+            const uint32_t id_s = idesc_cols(kTile) | (p.negative ? kNegateA : 0u);
+            int at = 0, jobs[2] = {0, 0};       // tiles of K and V, and products with V of each chain, so far
             for (int units = 0; ok && next_unit(share, u); ++units) {
                 const int n = u.pair ? 2 * u.n : u.n;
                 if (!(ok = tc::warp_wait(q_full, units & 1)))
                     break;
-                for (int job = 0; ok && job <= n; ++job) {
-                    if (job < n) {
-                        const int s = job & 1, k = at + 2 * (u.pair ? job >> 1 : job), st = k % L::STAGES;
-                        const bool last = !u.pair || s;
-                        if (!u.pair || !s)
-                            if (!(ok = tc::warp_wait(kv_full + 8 * st, (k / L::STAGES) & 1)))
-                                break;
-                        tc::tc_fence_after();
-                        const uint32_t q = base + L::Q + (u.pair ? s * L::TILE : 0), kt = base + L::KV + st * L::TILE;
-                        for (int kk = 0; kk < ksteps; ++kk) {
-                            const uint32_t off = (kk >> 2) * (kTile * 128) + (kk & 3) * 32;
-                            tc::mma_bf16_elect(tmem + s * 128, tc::sw128_desc(q + off), tc::sw128_desc(kt + off), id_s, kk > 0);
-                        }
-                        tc::mma_commit_elect(s_full + 8 * s);
-                        if (last)
-                            tc::mma_commit_elect(kv_empty + 8 * st);
-                        if (job == n - 1)
-                            tc::mma_commit_elect(q_empty);
-                    }
-                    if (job > 0) {
-                        const int prev = job - 1, s = prev & 1, v = at + 2 * (u.pair ? prev >> 1 : prev) + 1, st = v % L::STAGES;
-                        if (!u.pair || !s)
-                            if (!(ok = tc::warp_wait(v_ok + 8 * st, (v / L::STAGES) & 1)))
-                                break;
-                        const uint32_t vt = base + L::KV + st * L::TILE;
-                        for (int half = 1; ok && half >= 0; --half) {     // the second half of the states is ready first
-                            if (!(ok = tc::warp_wait((half ? p_half : p_ready) + 8 * s, jobs[s] & 1)))
-                                break;
-                            tc::tc_fence_after();
-                            for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
-                                mma_tmem_a_elect(tmem + 256 + s * 128, tmem + s * 128 + half * 64 + (kk & 3) * 8, rows_desc(vt + kk * 2048, kTile * 128), id_o,
-                                                 prev >= 2 || kk != 4);
-                        }
-                        if (!ok)
+                for (int job = 0; job < n; ++job) {
+                    const int s = job & 1, k = at + 2 * (u.pair ? job >> 1 : job), st = k % L::STAGES;
+                    if (!u.pair || !s)
+                        if (!(ok = tc::warp_wait(kv_full + 8 * st, (k / L::STAGES) & 1)))
                             break;
-                        ++jobs[s];
-                        tc::mma_commit_elect(pv_done + 8 * s);
-                        if (!u.pair || s)
-                            tc::mma_commit_elect(kv_empty + 8 * st);
+                    // over the weights of this chain's product before
+                    if (jobs[s] > 0 && !(ok = tc::warp_wait(pv_done + 8 * s, (jobs[s] - 1) & 1)))
+                        break;
+                    ++jobs[s];
+                    tc::tc_fence_after();
+                    const uint32_t q = base + L::Q + (u.pair ? s * L::TILE : 0), kt = base + L::KV + st * L::TILE;
+                    for (int kk = 0; kk < ksteps; ++kk) {
+                        const uint32_t off = (kk >> 2) * (kTile * 128) + (kk & 3) * 32;
+                        tc::mma_bf16_elect(tmem + s * 128, tc::sw128_desc(q + off), tc::sw128_desc(kt + off), id_s, kk > 0);
                     }
+                    tc::mma_commit_elect(s_full + 8 * s);
+                    if (!u.pair || s)
+                        tc::mma_commit_elect(kv_empty + 8 * st);
+                }
+                tc::mma_commit_elect(q_empty);
+                at += 2 * u.n;
+            }
+        } else if (warp == 2) {         // products with the values, likewise
+            const uint32_t id_o = idesc_rows((a.dim + 15) / 16 * 16);
+            int at = 0, jobs[2] = {0, 0};
+            while (ok && next_unit(share, u)) {
+                const int n = u.pair ? 2 * u.n : u.n;
+                for (int job = 0; ok && job < n; ++job) {
+                    const int s = job & 1, v = at + 2 * (u.pair ? job >> 1 : job) + 1, st = v % L::STAGES;
+                    if (!u.pair || !s)
+                        if (!(ok = tc::warp_wait(v_ok + 8 * st, (v / L::STAGES) & 1)))
+                            break;
+                    const uint32_t vt = base + L::KV + st * L::TILE;
+                    for (int half = 1; ok && half >= 0; --half) {     // the second half of the states is ready first
+                        if (!(ok = tc::warp_wait((half ? p_half : p_ready) + 8 * s, jobs[s] & 1)))
+                            break;
+                        tc::tc_fence_after();
+                        for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
+                            mma_tmem_a_elect(tmem + 256 + s * 128, tmem + s * 128 + half * 64 + (kk & 3) * 8, rows_desc(vt + kk * 2048, kTile * 128), id_o,
+                                             job >= 2 || kk != 4);
+                    }
+                    ++jobs[s];
+                    tc::mma_commit_elect(pv_done + 8 * s);
+                    if (!u.pair || s)
+                        tc::mma_commit_elect(kv_empty + 8 * st);
                 }
                 at += 2 * u.n;
             }
-        } else if (warp < 4) {          // looks the values over
+        }
+    } else if (warp >= 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
+        {                               // looks the values over
             int at = 0;
             for (int units = 0; ok && next_unit(share, u); ++units) {
                 // the states that every row with any sees
@@ -369,7 +378,7 @@ __global__ __launch_bounds__(kThreads, 1) void cross_forward_kernel(const __grid
                     if (!(ok = tc::warp_wait(kv_full + 8 * st, (v / L::STAGES) & 1)))
                         break;
                     if (c0 < lo || c0 + kTile > hi) {
-                        look_over<DP>(base + L::KV + st * L::TILE, c0, a, p, u, bad, bad_any, (warp - 2) * 32 + lane);
+                        look_over<DP>(base + L::KV + st * L::TILE, c0, a, p, u, bad, bad_any);
                         fence_proxy_async_smem();
                         __syncwarp();
                     }
@@ -380,12 +389,12 @@ __global__ __launch_bounds__(kThreads, 1) void cross_forward_kernel(const __grid
             }
         }
     } else {                        // softmax, a row a thread
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         const int s = (warp - 4) >> 2, row = threadIdx.x & 127;
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21), sc = lanes + s * 128, oc = lanes + 256 + s * 128;
         const float scale = fmaxf(fabsf(a.scale) * kLog2e, 1e-30f);      // not 0: a hidden score is -inf
         int jobs = 0;
-        for (int units = 0; ok && next_unit(share, u); ++units) {
+        while (next_unit(share, u)) {
             const int tile = u.pair && s ? u.tb : u.ta, t = tile * p.tokens_a_tile + row / group;
             const bool live = row < p.chunk_rows && t < a.T;
             const int2 see = live ? span_of(a.spans, a.S, t, nullptr) : make_int2(0, 0);
@@ -393,9 +402,7 @@ __global__ __launch_bounds__(kThreads, 1) void cross_forward_kernel(const __grid
             float top = -INFINITY, sum = 0.0f;      // in units of base-2 exponents
             for (int i = 0; i < mine; ++i, ++jobs) {
                 const int c0 = (u.j0 + (u.pair ? i : 2 * i + s)) * kTile;
-                if (!(ok = tc::warp_wait(s_full + 8 * s, jobs & 1)))
-                    break;
-                tc::tc_fence_after();
+                wait_on(ok, s_full + 8 * s, jobs & 1);
                 float x[64], m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
                 const bool all = __all_sync(0xffffffffu, see.x <= c0 && see.y >= c0 + kTile);
                 const unsigned from = see.x - c0, n = see.y - see.x;
@@ -420,9 +427,7 @@ __global__ __launch_bounds__(kThreads, 1) void cross_forward_kernel(const __grid
                     top = next;
                     sum *= turn;
                     if (i > 0) {
-                        if (!(ok = tc::warp_wait(pv_done + 8 * s, (jobs - 1) & 1)))
-                            break;
-                        tc::tc_fence_after();
+                        wait_on(ok, pv_done + 8 * s, (jobs - 1) & 1);
 #pragma unroll
                         for (int c = 0; c < DP; c += 32) {
                             float o[32];
@@ -465,19 +470,16 @@ __global__ __launch_bounds__(kThreads, 1) void cross_forward_kernel(const __grid
                 part[0] = add2(part[0], part[1]);
                 sum += part[0].x + part[0].y;
             }
-            if (!ok)
-                break;
-            if (mine > 0) {
-                if (!(ok = tc::warp_wait(pv_done + 8 * s, (jobs - 1) & 1)))
-                    break;
-                tc::tc_fence_after();
-            }
+            if (mine > 0)
+                wait_on(ok, pv_done + 8 * s, (jobs - 1) & 1);
             // one query tile: the first group joins the two chains
             float turn[2] = {1.0f, 0.0f};
             if (!u.pair) {
                 if (s == 1)
                     tops[row] = make_float2(top, sum);
+                tc::tc_fence_before();
                 asm volatile("bar.sync 1, 256;" ::: "memory");
+                tc::tc_fence_after();
                 if (s == 0) {
                     const float2 other = tops[row];
                     const float next = fmaxf(top, other.x), from = next == -INFINITY ? 0.0f : next;
@@ -696,7 +698,7 @@ cudaError_t launch_cross_attention(const CrossArgs &all, cudaStream_t stream)
         cross_nothing_kernel<<<device_sm_count(), 256, 0, stream>>>(all);
         return cudaGetLastError();
     }
-    const int64_t step = (int64_t)kMostTiles * (kTile / (all.Hq / all.heads));
+    const int64_t step = (int64_t)most_tiles(all.heads, (all.S + kTile - 1) / kTile, kMostTiles) * (kTile / (all.Hq / all.heads));
     for (int64_t t = 0; t < all.T; t += step) {
         CrossArgs a = all;
         a.T = (int)(all.T - t < step ? all.T - t : step);

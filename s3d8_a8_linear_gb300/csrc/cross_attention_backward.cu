@@ -840,15 +840,15 @@ cudaError_t launch(const CrossArgs &a, cudaStream_t stream)
         e = tc::allow_smem(cross_dkv_kernel<DP>, L::BYTES, allowed_kv);
     if (e == cudaSuccess)
         e = tc::launch_pdl(cross_ready_kernel, dim3(p.q_tiles, a.heads), dim3(256), 0, stream, a, p);
-    for (p.first = 0; e == cudaSuccess && p.first < p.q_tiles; p.first += kMostTiles) {
-        p.tiles = p.q_tiles - p.first < kMostTiles ? p.q_tiles - p.first : kMostTiles;
+    const int tiles = (a.S + kTile - 1) / kTile, most_q = most_tiles(a.heads, tiles, kMostTiles), most_kv = most_tiles(a.heads, p.q_tiles, kMostTiles);
+    for (p.first = 0; e == cudaSuccess && p.first < p.q_tiles; p.first += most_q) {
+        p.tiles = p.q_tiles - p.first < most_q ? p.q_tiles - p.first : most_q;
         e = tc::launch_pdl(cross_dq_kernel<DP>, dim3(p.ctas), dim3(kThreads), L::BYTES, stream, mq, md, mk, mv, a, p);
         if (e == cudaSuccess)
             e = tc::launch_pdl(cross_add_kernel<DP, false>, dim3(p.tiles * a.heads, (p.rows + 31) / 32), dim3(kJoinWarps * 32), 0, stream, a, p);
     }
-    const int tiles = (a.S + kTile - 1) / kTile;
-    for (p.first = 0; e == cudaSuccess && p.first < tiles; p.first += kMostTiles) {
-        p.tiles = tiles - p.first < kMostTiles ? tiles - p.first : kMostTiles;
+    for (p.first = 0; e == cudaSuccess && p.first < tiles; p.first += most_kv) {
+        p.tiles = tiles - p.first < most_kv ? tiles - p.first : most_kv;
         e = tc::launch_pdl(cross_dkv_kernel<DP>, dim3(p.ctas), dim3(kThreads), L::BYTES, stream, mq, md, mk, mv, a, p);
         if (e == cudaSuccess)
             e = tc::launch_pdl(cross_add_kernel<DP, true>, dim3(p.tiles * a.heads, 2 * kTile / 32), dim3(kJoinWarps * 32), 0, stream, a, p);

@@ -42,6 +42,14 @@ __device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t *r)
                  : "memory");
 }
 
+__device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t *r)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+                 "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+                 : "memory");
+}
+
 __device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
@@ -77,6 +85,15 @@ __device__ __forceinline__ void tma_3d_elect(uint32_t dst, const CUtensorMap *ma
         "[%5];\n}\n" ::"r"(dst),
         "l"((uint64_t)map), "r"(x), "r"(y), "r"(z), "r"(bar)
         : "memory");
+}
+
+// A wait of a warp that meets others at barriers: once one ran out it waits no more, and runs
+// on to the end with what it finds, so that the others are not left waiting.
+__device__ __forceinline__ void wait_on(bool &ok, uint32_t bar, uint32_t parity)
+{
+    if (ok)
+        ok = tc::warp_wait(bar, parity);
+    tc::tc_fence_after();
 }
 
 // ---- arithmetic -------------------------------------------------------------
@@ -152,26 +169,26 @@ struct Piece {
 __device__ __forceinline__ int64_t busy(int ctas, int64_t all) { return all < ctas ? all : ctas; }
 
 // A CTA's share of the work of all heads: as many tiles as any other's, one behind the
-// other, piece by piece.
+// other, piece by piece.  (Launches keep the number of all tiles below 2^31.)
 struct Share {
     const Item *items;
-    int n_items, per_head;
-    int64_t at, first, end;
+    int n_items, per_head, at, end;
+    bool begun;
 
     __device__ __forceinline__ Share(const Item *list, int n, int heads, int ctas)
-        : items(list), n_items(n), per_head(list[n].begin)
+        : items(list), n_items(n), per_head(list[n].begin), begun(false)
     {
         const int64_t all = (int64_t)heads * per_head, some = busy(ctas, all);
-        first = at = blockIdx.x < some ? all * blockIdx.x / some : 0;
-        end = blockIdx.x < some ? all * (blockIdx.x + 1) / some : 0;
+        at = blockIdx.x < some ? (int)(all * blockIdx.x / some) : 0;
+        end = blockIdx.x < some ? (int)(all * (blockIdx.x + 1) / some) : 0;
     }
 
     __device__ __forceinline__ bool next(Piece &u)
     {
         if (at >= end)
             return false;
-        u.head = (int)(at / per_head);
-        const int r = (int)(at - (int64_t)u.head * per_head);
+        u.head = at / per_head;
+        const int r = at - u.head * per_head;
         int lo = 0, hi = n_items;
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
@@ -180,16 +197,23 @@ struct Share {
             else
                 hi = mid;
         }
-        const Item it = items[lo];
-        const int off = r - it.begin, left = items[lo + 1].begin - r;
-        u.tile = it.tile;
-        u.j0 = it.j0 + off;
-        u.n = (int)(end - at < left ? end - at : left);
-        u.slot = off == 0 && u.n == left ? -1 : at != first;
+        const int off = r - items[lo].begin, left = items[lo + 1].begin - r;
+        u.tile = items[lo].tile;
+        u.j0 = items[lo].j0 + off;
+        u.n = min(end - at, left);
+        u.slot = off == 0 && u.n == left ? -1 : begun;
         at += u.n;
+        begun = true;
         return true;
     }
 };
+
+// Most tiles of a launch that have sums of their own, where each may pass `others`.
+inline int most_tiles(int64_t heads, int64_t others, int most)
+{
+    const int64_t fit = 0x7FFFFFFF / (heads * (others > 0 ? others : 1));
+    return (int)(fit < most ? fit : most);
+}
 
 // The CTAs whose shares hold parts of item i of a head (c0 == c1: it is whole), and where
 // each has put its part.
