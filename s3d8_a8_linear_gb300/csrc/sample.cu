@@ -4,18 +4,22 @@
 // Tokens stand in the order of their logits, equal ones by index, with weights
 // w = exp((l - max) / T); every limit keeps a beginning of that order, and u times the kept
 // weight falls on one token of it.  A bf16 logit is one of 65536 values, so nothing is
-// sorted: a row is counted into a histogram of its values, and weights are computed once
+// sorted: tokens are counted into a histogram of their values, and weights are computed once
 // per value instead of once per token.  That leaves time for exact ones: exp in pairs of
-// fp32 (about 2^-43), summed as whole numbers of 2^-45 of the largest weight.  Such sums do
+// fp32 (about 2^-44), summed as whole numbers of 2^-45 of the largest weight.  Such sums do
 // not depend on their order, so equal inputs give equal bits, and a token next to a border
 // is decided as in 64 bits.
 //
-// A cluster of CTAs takes a row, a part of the vocabulary each (16-bit counts in shared
-// memory, so at most 65535 tokens a CTA).  The values are dealt in groups of 128, one power
-// of two each; a CTA adds up the counts of its share of the groups from all CTAs of the
-// cluster, skipping groups that none has.  The first CTA then finds the limits and the
-// value by searching the groups' sums, and the CTA whose part holds the token reads its
-// part again for it.
+// Counting costs an atomic addition in shared memory a token, so only the head of the order
+// is counted, the values within 16 T of the largest logit; of the others only the sum of the
+// weights is taken, in fp32 (each is below 2^-23 of the largest, so that its error of 2^-21
+// or so is nothing).  Where a limit or the drawn token turns out to lie behind the head,
+// the row is counted again as a whole.
+//
+// A cluster of CTAs takes a row, a part of the vocabulary each (16-bit counts, so at most
+// 65535 tokens a CTA), and reads it three times, from L2 but for the first.  Values form groups of 128, one power of
+// two each.  The first CTA adds up the groups' counts from all CTAs, finds the limits and
+// the value by searching the groups' sums, and tells the CTA whose part has the token.
 #include "launch.h"
 #include "tcgen05.cuh"
 
@@ -29,28 +33,35 @@ constexpr int kHistWords = kGroups * kKeys / 2; // two 16-bit counts a word
 constexpr int kMostTokens = 65528;              // of a CTA: counts stay below 2^16, parts begin on 8
 constexpr int kScale = 45;                      // weights are whole numbers of 2^-45
 
+constexpr int kUnits = 512;                      // runs of values that the first CTA adds up, at most
+constexpr int kCached = 64;                     // runs of 32 whose values' counts and weights it keeps
+constexpr float kHead = 16.0f;                  // counted: values within kHead T of the largest
+constexpr float kHeadWeight = 1.2e-7f;          // exp(-kHead), and a little
+
+// A value's tokens and weight, and what stands in front of it in its run.
+struct Value {
+    uint32_t count, count_before;
+    unsigned long long weight, mass_before;
+};
+
 struct Shared {
     uint32_t hist[kHistWords];
     uint32_t flags[kGroups / 32];               // groups that this CTA's part has
-    uint32_t top;                               // its largest key
-    // in the first CTA
-    uint32_t count[kGroups], above[kGroups];    // of a group, all CTAs': tokens, those that min-p keeps
-    unsigned long long mass[kGroups];
-    // first: group sums, from the largest group downwards, in front of each
-    uint32_t count_before[kGroups];
-    unsigned long long mass_before[kGroups];
-    uint32_t warp_count[kWarps], warp_above[kWarps];
-    unsigned long long warp_mass[kWarps];
-    uint32_t found_key, found_rank;             // the token: its value, and its rank among equals
-    int found;
-    uint32_t match[kWarps];
-    unsigned long long best[kWarps];
-    // what a search found
-    uint32_t hit_count;
-    unsigned long long hit_mass, hit_weight;
-    uint32_t hit_key;
-    int hit_group;
+    uint32_t top;                               // its largest key, times 2^16; the least of its lanes' largest (below)
+    unsigned long long tail;                    // the weights that it has not counted
+    uint32_t wave[kWarps];
+    unsigned long long wide[kWarps];
+    // told by the first CTA
+    int verdict;                                // what a row comes to: below
+    uint32_t key, rank;                         // the token: its value, and its rank among this CTA's
+    // of the first CTA.  Of run i, from the largest values downwards, all CTAs': tokens, those
+    // that min-p keeps, weight; and what stands in front of it
+    uint32_t count[kUnits], above[kUnits], count_before[kUnits];
+    unsigned long long mass[kUnits], mass_before[kUnits];
+    Value values[kCached][32];
 };
+
+enum Verdict { kNothing, kMine, kOther, kAgain };
 
 // Keys rise with the value; both zeros are one.  0: a token that is never drawn (-inf, NaN).
 __device__ __forceinline__ uint32_t key_of(uint32_t bits)
@@ -95,11 +106,11 @@ __device__ __forceinline__ Pair add(Pair a, Pair b)
     return quick_sum(s.hi, __fadd_rn(s.lo, __fadd_rn(a.lo, b.lo)));
 }
 
-// The two parts of a double (to 2^-48 of it).
-__device__ __forceinline__ Pair pair_of(double x)
+// 1 / x (to 2^-46 of it; just rounded where that is 0 or infinite).
+__device__ __forceinline__ Pair reciprocal(float x)
 {
-    const float hi = (float)x;
-    return {hi, isfinite(hi) ? (float)(x - (double)hi) : 0.0f};
+    const float r = __frcp_rn(x);
+    return {r, isfinite(r) && r > 0.0f ? __fmul_rn(r, __fmaf_rn(-r, x, 1.0f)) : 0.0f};
 }
 
 // 2^45 exp(x) to the nearest whole number, x <= 0: exp(x) = 2^n exp(r), r = x - n ln 2,
@@ -134,6 +145,28 @@ __device__ __forceinline__ unsigned long long weight(Pair x)
     return (unsigned long long)(__float2ll_rn(__fmul_rn(y.hi, scale)) + __float2ll_rn(__fmul_rn(y.lo, scale)));
 }
 
+// Two fp32 at once.
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    uint64_t d, x = *reinterpret_cast<uint64_t *>(&a), y = *reinterpret_cast<uint64_t *>(&b);
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
+    return *reinterpret_cast<float2 *>(&d);
+}
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    uint64_t d, x = *reinterpret_cast<uint64_t *>(&a), y = *reinterpret_cast<uint64_t *>(&b);
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
+    return *reinterpret_cast<float2 *>(&d);
+}
+
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    uint64_t d, x = *reinterpret_cast<uint64_t *>(&a), y = *reinterpret_cast<uint64_t *>(&b), z = *reinterpret_cast<uint64_t *>(&c);
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(x), "l"(y), "l"(z));
+    return *reinterpret_cast<float2 *>(&d);
+}
+
 struct Row {
     uint32_t top;       // the largest key
     float top_value;
@@ -165,92 +198,196 @@ __device__ __forceinline__ void remote_store_u32(uint32_t addr, uint32_t v)
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
-__device__ __forceinline__ void remote_store_u64(uint32_t addr, unsigned long long v)
-{
-    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
-}
+// How the counted values are cut into runs: of 32, a value a lane, or of 128 where those
+// were too many.  Run i ends in front of key `end` - i * size.
+struct Runs {
+    int end, count;
+    bool fine;
+    __device__ __forceinline__ Runs(int first_group, int last_group)
+        : end((last_group + 1) * kKeys), fine((last_group - first_group + 1) * 4 <= kUnits)
+    {
+        count = (last_group - first_group + 1) * (fine ? 4 : 1);
+    }
+    __device__ __forceinline__ int size() const { return fine ? 32 : 128; }
+};
 
-// The counts of a lane's four neighbouring values of a group (values 4 lane .. 4 lane + 3), all CTAs'.
+// All CTAs' tokens of a lane's values of a run, the largest value first: value `first` - e, e
+// < 4 (fine: e = 0 alone).
 template <int C>
-__device__ __forceinline__ void group_counts(Shared &s, int group, int lane, uint32_t (&n)[4])
+__device__ __forceinline__ void run_counts(Shared &s, const Runs &r, int first, uint32_t (&n)[4])
 {
     n[0] = n[1] = n[2] = n[3] = 0;
-    const uint32_t at = smem_addr(s.hist) + (group * (kKeys / 2) + 2 * lane) * 4;
+    if (r.fine) {
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-        uint32_t a, b;
-        asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(a), "=r"(b) : "r"(tc::map_to_rank(at, c)));
-        n[0] += a & 0xFFFFu, n[1] += a >> 16, n[2] += b & 0xFFFFu, n[3] += b >> 16;
-    }
-}
-
-// The eight tokens from i on (i a multiple of 8; those at n and behind are no tokens).
-__device__ __forceinline__ void eight(const uint16_t *x, int i, int n, bool vec, uint32_t (&key)[8])
-{
-    if (vec && i + 8 <= n) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4 *>(x + i));
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            key[e] = key_of(e & 1 ? w[e / 2] >> 16 : w[e / 2] & 0xFFFFu);
+        for (int c = 0; c < C; ++c) {
+            uint16_t v;
+            asm volatile("ld.shared::cluster.u16 %0, [%1];" : "=h"(v) : "r"(tc::map_to_rank(smem_addr(s.hist) + 2 * first, c)));
+            n[0] += v;
+        }
     } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            key[e] = i + e < n ? key_of(__ldg(x + i + e)) : 0u;
+        for (int c = 0; c < C; ++c) {
+            uint32_t a, b;
+            asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];" : "=r"(a), "=r"(b) : "r"(tc::map_to_rank(smem_addr(s.hist) + 2 * (first - 3), c)));
+            n[3] += a & 0xFFFFu, n[2] += a >> 16, n[1] += b & 0xFFFFu, n[0] += b >> 16;
+        }
     }
 }
 
-// Searches the order of all tokens, by count or by mass: the value that holds the
-// `target`-th unit (from 0).  All threads of the first CTA.  Leaves in s.hit_*: the value,
-// its weight, and the tokens and mass in front of it.
-template <int C>
-__device__ __forceinline__ void search(Shared &s, const Row &row, bool by_mass, unsigned long long target)
+// A run's tokens and weight in front of a lane's first value, and (at the last lane) with its
+// values: inclusive sums over the lanes.
+__device__ __forceinline__ void scan_run(const uint32_t (&n)[4], const unsigned long long (&w)[4], uint32_t &count, unsigned long long &mass)
 {
-    if (threadIdx.x < kGroups) {
-        const int g = threadIdx.x;
-        const unsigned long long before = by_mass ? s.mass_before[g] : s.count_before[g], n = by_mass ? s.mass[g] : s.count[g];
-        if (target >= before && target < before + n)
-            s.hit_group = g;
+    count = n[0] + n[1] + n[2] + n[3];
+    mass = n[0] * w[0] + n[1] * w[1] + n[2] * w[2] + n[3] * w[3];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t pc = __shfl_up_sync(0xffffffffu, count, o);
+        const unsigned long long pm = __shfl_up_sync(0xffffffffu, mass, o);
+        if ((int)(threadIdx.x & 31) >= o)
+            count += pc, mass += pm;
     }
-    __syncthreads();
-    if (threadIdx.x < 32) {
-        const int lane = 31 - threadIdx.x;      // the largest values first
-        const int g = s.hit_group;
-        uint32_t n[4];
-        group_counts<C>(s, g, lane, n);
-        unsigned long long w[4], mass = 0;
-        uint32_t count = 0;
+}
+
+// The eight tokens from i on (i a multiple of 8), two a word; those at n and behind are -inf.
+__device__ __forceinline__ uint4 eight(const uint16_t *x, int i, int n, bool vec)
+{
+    if (vec && i + 8 <= n)
+        return __ldg(reinterpret_cast<const uint4 *>(x + i));
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const uint32_t lo = i + 2 * e < n ? __ldg(x + i + 2 * e) : 0xFF80u, hi = i + 2 * e + 1 < n ? __ldg(x + i + 2 * e + 1) : 0xFF80u;
+        w[e] = lo | hi << 16;
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The larger of each two bf16 (of a NaN and a number, the number).
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+__device__ __forceinline__ uint32_t max_of(const uint4 &v) { return max_bf16x2(max_bf16x2(v.x, v.y), max_bf16x2(v.z, v.w)); }
+
+__device__ __forceinline__ float lo_value(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float hi_value(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// Which of eight tokens have a value.
+__device__ __forceinline__ uint32_t equal_mask(uint4 v, uint32_t key)
+{
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint32_t mask = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+        mask |= (key_of(e & 1 ? w[e / 2] >> 16 : w[e / 2] & 0xFFFFu) == key ? 1u : 0u) << e;
+    return mask;
+}
+
+// Halves of a word that are at least those of another: 0xFFFF, else (and for NaN) 0.
+__device__ __forceinline__ uint32_t at_least(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    asm("set.ge.u32.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+// Counts those of eight tokens whose value is at least `cut` (bf16, twice in a word) and that
+// are tokens.  A lane has few of them, so that a loop over a lane's takes fewer atomic
+// instructions than eight.
+__device__ __forceinline__ void count_eight(Shared &s, uint4 v, uint32_t cut)
+{
+    const unsigned long long lo = v.x | (unsigned long long)v.y << 32, hi = v.z | (unsigned long long)v.w << 32;
+    uint32_t some = (at_least(v.x, cut) & 0x00010002u) | (at_least(v.y, cut) & 0x00040008u) | (at_least(v.z, cut) & 0x00100020u) |
+                    (at_least(v.w, cut) & 0x00400080u);
+    // the bits of odd tokens came from the low halves: token 2 j is bit 2 j + 1, token 2 j + 1 is bit 16 + 2 j
+    while (__any_sync(0xffffffffu, some)) {
+        if (some) {
+            const int bit = __ffs(some) - 1, e = bit < 16 ? bit - 1 : bit - 15;
+            some &= some - 1;
+            const uint32_t key = key_of((uint32_t)((e < 4 ? lo : hi) >> (16 * (e & 3))) & 0xFFFFu);
+            if (key)
+                atomicAdd(&s.hist[key >> 1], key & 1 ? 0x10000u : 1u);
+        }
+        __syncwarp();
+    }
+}
+
+// The weights of two tokens, where they are not counted, from base-2 exponents d * to2 of
+// their distance to the largest; 0 for -inf, NaN and what is below 2^-126.
+__device__ __forceinline__ float behind(uint32_t w, uint32_t cut, float2 minus_top, float2 to2_hi, float2 to2_lo)
+{
+    const float2 d = add2(make_float2(lo_value(w), hi_value(w)), minus_top), x = mul2(d, to2_hi);
+    const float2 rest = mul2(fma2(d, to2_lo, fma2(d, to2_hi, make_float2(-x.x, -x.y))), make_float2(0.693147f, 0.693147f));
+    float2 p;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p.x) : "f"(x.x));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p.y) : "f"(x.y));
+    p = fma2(p, rest, p);
+    const uint32_t counted = at_least(w, cut);
+    return (x.x > -126.0f && !(counted & 1) ? p.x : 0.0f) + (x.y > -126.0f && !(counted >> 31) ? p.y : 0.0f);
+}
+
+// A value of the order of all counted tokens, its weight, and the tokens and weight in front of it.
+struct Hit {
+    uint32_t key, count;
+    unsigned long long mass, weight;
+};
+
+// The value that holds the `target`-th unit (from 0) of the tokens, or of their weight.  One
+// warp of the first CTA.
+template <int C>
+__device__ __forceinline__ Hit search(Shared &s, const Row &row, const Runs &runs, bool by_mass, unsigned long long target)
+{
+    const int lane = threadIdx.x & 31;
+    int i = 0;
+    for (int base = 0; base < runs.count; base += 32) {
+        const int at = base + lane;
+        const unsigned long long before = at >= runs.count ? 0 : by_mass ? s.mass_before[at] : s.count_before[at];
+        const unsigned long long size = at >= runs.count ? 0 : by_mass ? s.mass[at] : s.count[at];
+        const uint32_t in = __ballot_sync(0xffffffffu, target >= before && target < before + size);
+        if (in) {
+            i = base + __ffs(in) - 1;
+            break;
+        }
+    }
+    Hit hit = {0, 0, 0, 0};
+    bool has = false;
+    if (runs.fine && i < kCached) {
+        const Value v = s.values[i][lane];
+        hit = {(uint32_t)(runs.end - i * 32 - 1 - lane), s.count_before[i] + v.count_before, s.mass_before[i] + v.mass_before, v.weight};
+        const unsigned long long before = by_mass ? hit.mass : hit.count, size = by_mass ? v.count * v.weight : v.count;
+        has = target >= before && target < before + size;
+    } else {
+        const int first = runs.end - i * runs.size() - 1 - (runs.fine ? 1 : 4) * lane;
+        uint32_t n[4], c;
+        run_counts<C>(s, runs, first, n);
+        unsigned long long w[4], m;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            w[e] = n[e] ? weight_of(first - e, row) : 0;
+        scan_run(n, w, c, m);
+        c += s.count_before[i] - (n[0] + n[1] + n[2] + n[3]);
+        m += s.mass_before[i] - (n[0] * w[0] + n[1] * w[1] + n[2] * w[2] + n[3] * w[3]);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            w[e] = n[e] ? weight_of(g * kKeys + 4 * lane + e, row) : 0;
-            mass += n[e] * w[e];
-            count += n[e];
-        }
-        uint32_t c = count;
-        unsigned long long m = mass;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const uint32_t pc = __shfl_up_sync(0xffffffffu, c, o);
-            const unsigned long long pm = __shfl_up_sync(0xffffffffu, m, o);
-            if (threadIdx.x >= o)
-                c += pc, m += pm;
-        }
-        c += s.count_before[g] - count;
-        m += s.mass_before[g] - mass;
-#pragma unroll
-        for (int e = 3; e >= 0; --e) {
             const unsigned long long before = by_mass ? m : c, size = by_mass ? n[e] * w[e] : n[e];
             if (target >= before && target < before + size) {
-                s.hit_key = g * kKeys + 4 * lane + e;
-                s.hit_weight = w[e];
-                s.hit_count = c;
-                s.hit_mass = m;
+                hit = {(uint32_t)(first - e), c, m, w[e]};
+                has = true;
             }
             c += n[e];
             m += n[e] * w[e];
         }
     }
-    __syncthreads();
+    const int from = __ffs(__ballot_sync(0xffffffffu, has)) - 1;
+    hit.key = __shfl_sync(0xffffffffu, hit.key, from);
+    hit.count = __shfl_sync(0xffffffffu, hit.count, from);
+    hit.mass = __shfl_sync(0xffffffffu, hit.mass, from);
+    hit.weight = __shfl_sync(0xffffffffu, hit.weight, from);
+    return hit;
 }
 
 template <int C>
@@ -262,136 +399,52 @@ __device__ __forceinline__ void row_sync()
         __syncthreads();
 }
 
+// Adds up the runs' counts of all CTAs and their weights, a warp a run.  All warps of the first CTA.
 template <int C>
-__global__ __launch_bounds__(kThreads) void sample_kernel(const __grid_constant__ SampleArgs a, int part, int vec)
+__device__ __forceinline__ void add_runs(Shared &s, const Row &row, unsigned long long least, const Runs &runs)
 {
-    extern __shared__ __align__(16) unsigned char sample_mem[];
-    Shared &s = *reinterpret_cast<Shared *>(sample_mem);
-    const int rank = C > 1 ? (int)tc::cluster_rank() : 0, b = blockIdx.x / C;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int first = rank * part, n = max(0, min(part, a.V - first));
-    for (int i = threadIdx.x; i < kHistWords / 4; i += kThreads)
-        reinterpret_cast<uint4 *>(s.hist)[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (threadIdx.x < kGroups / 32)
-        s.flags[threadIdx.x] = 0;
-    if (threadIdx.x == 0) {
-        s.top = 0;
-        s.found = 0;
-    }
-    tc::pdl_launch_dependents();
-    tc::pdl_wait();
-    const uint16_t *x = reinterpret_cast<const uint16_t *>(a.logits) + (int64_t)b * a.stride + first;
-    const float temp = a.temperature ? a.temperature[b] : 1.0f;
-    __syncthreads();
-
-    uint32_t top = 0;
-    if (!(temp > 0.0f)) {       // the largest logit, the lowest index among equals
-        unsigned long long best = 0;
-        for (int i = threadIdx.x * 8; i < n; i += kThreads * 8) {
-            uint32_t key[8];
-            eight(x, i, n, vec, key);
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                best = max(best, (unsigned long long)key[e] << 32 | (0xFFFFFFFFu - (uint32_t)(first + i + e)));
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
-        if (lane == 0)
-            s.best[warp] = best;
-        row_sync<C>();          // and the first CTA has begun
-        if (warp == 0) {
-            best = s.best[lane];
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1)
-                best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
-            if (lane == 0)
-                remote_store_u64(tc::map_to_rank(smem_addr(s.mass) + 8 * rank, 0), best);
-        }
-        row_sync<C>();
-        if (rank == 0 && threadIdx.x == 0) {
-            best = s.mass[0];
-            for (int c = 1; c < C; ++c)
-                best = max(best, s.mass[c]);
-            const bool some = best >> 32;
-            a.tokens[b] = some ? (int32_t)(0xFFFFFFFFu - (uint32_t)best) : -1;
-            if (a.logprob)
-                a.logprob[b] = some ? 0.0f : -INFINITY;
-        }
-        return;
-    }
-
-    for (int i = threadIdx.x * 8; i < n; i += kThreads * 8) {
-        uint32_t key[8];
-        eight(x, i, n, vec, key);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            if (key[e])
-                atomicAdd(&s.hist[key[e] >> 1], key[e] & 1 ? 0x10000u : 1u);
-            top = max(top, key[e]);
-        }
-    }
-    top = __reduce_max_sync(0xffffffffu, top);
-    if (lane == 0)
-        atomicMax(&s.top, top);
-    __syncthreads();
-    for (int g = warp; g < kGroups; g += kWarps) {
-        const uint2 v = reinterpret_cast<const uint2 *>(s.hist)[g * (kKeys / 4) + lane];
-        if (__any_sync(0xffffffffu, v.x | v.y) && lane == 0)
-            atomicOr(&s.flags[g / 32], 1u << (g & 31));
-    }
-    row_sync<C>();
-
-    Row row;
-    row.top = 0;
-#pragma unroll
-    for (int c = 0; c < C; ++c)
-        row.top = max(row.top, remote_u32(tc::map_to_rank(smem_addr(&s.top), c)));
-    row.top_value = value_of(row.top);
-    row.inverse = pair_of(1.0 / (double)temp);
-    const double min_p = a.min_p ? (double)a.min_p[b] : 0.0;
-    // the groups g, g + C, ... of this CTA, a warp each
-    for (int g = rank + C * warp; g < kGroups; g += C * kWarps) {
+    for (int i = warp; i < runs.count; i += kWarps) {
+        const int first = runs.end - i * runs.size() - 1 - (runs.fine ? 1 : 4) * lane, g = (runs.end - i * runs.size() - 1) / kKeys;
         uint32_t some = 0;
-#pragma unroll
-        for (int c = 0; c < C; ++c)
-            some |= remote_u32(tc::map_to_rank(smem_addr(s.flags) + 4 * (g / 32), c));
-        uint32_t count = 0, above = 0;
-        unsigned long long mass = 0;
-        if (some >> (g & 31) & 1) {
-            uint32_t cnt[4];
-            group_counts<C>(s, g, lane, cnt);
+        if (lane < C)
+            some = remote_u32(tc::map_to_rank(smem_addr(s.flags) + 4 * (g / 32), lane));
+        uint32_t n[4] = {0, 0, 0, 0}, count = 0, above = 0;
+        unsigned long long w[4] = {0, 0, 0, 0}, mass = 0;
+        if (__any_sync(0xffffffffu, some >> (g & 31) & 1)) {
+            run_counts<C>(s, runs, first, n);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                if (!cnt[e])
-                    continue;
-                const unsigned long long w = weight_of(g * kKeys + 4 * lane + e, row);
-                count += cnt[e];
-                mass += cnt[e] * w;
-                above += (double)w >= min_p * (double)(1ull << kScale) ? cnt[e] : 0u;
+                w[e] = n[e] ? weight_of(first - e, row) : 0;
+                above += w[e] >= least ? n[e] : 0u;
             }
-            count = __reduce_add_sync(0xffffffffu, count);
             above = __reduce_add_sync(0xffffffffu, above);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1)
-                mass += __shfl_xor_sync(0xffffffffu, mass, o);
+            scan_run(n, w, count, mass);
         }
-        if (lane == 0) {
-            remote_store_u32(tc::map_to_rank(smem_addr(&s.count[g]), 0), count);
-            remote_store_u32(tc::map_to_rank(smem_addr(&s.above[g]), 0), above);
-            remote_store_u64(tc::map_to_rank(smem_addr(&s.mass[g]), 0), mass);
+        if (runs.fine && i < kCached)
+            s.values[i][lane] = {n[0], count - n[0], w[0], mass - n[0] * w[0]};
+        if (lane == 31) {
+            s.count[i] = count;
+            s.above[i] = above;
+            s.mass[i] = mass;
         }
     }
-    row_sync<C>();
+}
 
-    if (rank == 0) {
-        // sums in front of each group, from the largest values downwards
-        uint32_t count = 0, above = 0;
-        unsigned long long mass = 0;
-        const int g = kGroups - 1 - (int)threadIdx.x;
-        if (threadIdx.x < kGroups)
-            count = s.count[g], above = s.above[g], mass = s.mass[g];
-        uint32_t c = count, k = above;
+// The token's value, its rank among its equals and its share, from the groups' sums; or that
+// all tokens have to be counted.  One warp of the first CTA (the 64-bit arithmetic is slow).
+template <int C>
+__device__ __forceinline__ Verdict choose(Shared &s, const SampleArgs &a, int b, const Row &row, bool cold, bool whole, const Runs &runs, uint32_t &key,
+                                          uint32_t &rank)
+{
+    const int lane = threadIdx.x & 31;
+    uint32_t stay = 0, kept = 0;        // a beginning of the order: its tokens and its mass
+    unsigned long long head = 0, held = 0;
+    for (int base = 0; base < runs.count; base += 32) {     // sums in front of each run
+        const int i = base + lane;
+        const uint32_t count = i < runs.count ? s.count[i] : 0;
+        const unsigned long long mass = i < runs.count ? s.mass[i] : 0;
+        uint32_t c = count, k = i < runs.count ? s.above[i] : 0;
         unsigned long long m = mass;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -400,136 +453,249 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(const __grid_constant_
             if (lane >= o)
                 c += pc, k += pk, m += pm;
         }
-        if (lane == 31)
-            s.warp_count[warp] = c, s.warp_above[warp] = k, s.warp_mass[warp] = m;
-        __syncthreads();
-        uint32_t all = 0, kept = 0;
-        unsigned long long whole = 0;
-        for (int w = 0; w < kGroups / 32; ++w) {
-            if (w < warp)
-                c += s.warp_count[w], m += s.warp_mass[w];
-            all += s.warp_count[w], kept += s.warp_above[w], whole += s.warp_mass[w];
-        }
-        if (threadIdx.x < kGroups)
-            s.count_before[g] = c - count, s.mass_before[g] = m - mass;
-        __syncthreads();
+        if (i < runs.count)
+            s.count_before[i] = stay + c - count, s.mass_before[i] = head + m - mass;
+        stay += __shfl_sync(0xffffffffu, c, 31);
+        kept += __shfl_sync(0xffffffffu, k, 31);
+        head += __shfl_sync(0xffffffffu, m, 31);
+    }
+    if (lane < C)
+        asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(held) : "r"(tc::map_to_rank(smem_addr(&s.tail), lane)));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        held += __shfl_xor_sync(0xffffffffu, held, o);
+    held += head;
+    __syncwarp();
 
-        if (all == 0) {         // nothing to draw
-            if (threadIdx.x == 0) {
-                a.tokens[b] = -1;
-                if (a.logprob)
-                    a.logprob[b] = -INFINITY;
-            }
-        } else {
-            uint32_t stay = all;        // a beginning of the order: its tokens and its mass
-            unsigned long long held = whole;
-            const int32_t top_k = a.top_k ? a.top_k[b] : 0;
-            if (top_k > 0 && (uint32_t)top_k < stay) {
-                search<C>(s, row, false, (unsigned long long)top_k - 1);
-                stay = (uint32_t)top_k;
-                held = s.hit_mass + (stay - s.hit_count) * s.hit_weight;
-                __syncthreads();
-            }
-            const double top_p = a.top_p ? (double)a.top_p[b] : 1.0;
-            if (top_p < 1.0) {          // the first tokens whose mass reaches top_p of what is held
-                const double want = ceil(top_p * (double)held);
-                const unsigned long long need = want > 1.0 ? min((unsigned long long)want, held) : 1ull;
-                search<C>(s, row, true, need - 1);
-                const uint32_t more = (uint32_t)((need - s.hit_mass + s.hit_weight - 1) / s.hit_weight);
-                if (s.hit_count + more <= stay) {
-                    stay = s.hit_count + more;
-                    held = s.hit_mass + more * s.hit_weight;
-                }
-                __syncthreads();
-            }
-            if (kept < stay && a.min_p) {
-                stay = max(kept, 1u);
-                search<C>(s, row, false, (unsigned long long)stay - 1);
-                held = s.hit_mass + (stay - s.hit_count) * s.hit_weight;
-                __syncthreads();
-            }
-            const double want = (double)a.u[b] * (double)held;
-            const unsigned long long t = want > 0.0 ? min((unsigned long long)want, held - 1) : 0ull;
-            search<C>(s, row, true, t);
-            if (threadIdx.x == 0) {
-                const uint32_t key = s.hit_key, r = (uint32_t)((t - s.hit_mass) / s.hit_weight);
-                for (int to = 0; to < C; ++to) {
-                    remote_store_u32(tc::map_to_rank(smem_addr(&s.found_key), to), key);
-                    remote_store_u32(tc::map_to_rank(smem_addr(&s.found_rank), to), r);
-                    remote_store_u32(tc::map_to_rank(smem_addr(&s.found), to), 1u);
-                }
-                if (a.logprob) {
-                    const double gap = key == row.top ? 0.0 : ((double)value_of(key) - (double)row.top_value) / (double)temp;
-                    a.logprob[b] = (float)(gap - log((double)held / (double)(1ull << kScale)));
-                }
-            }
+    const int32_t top_k = cold ? 1 : a.top_k ? a.top_k[b] : 0;
+    if (top_k > 0 && (uint32_t)top_k > stay && !whole)
+        return kAgain;
+    if (top_k > 0 && (uint32_t)top_k <= stay) {
+        const Hit hit = search<C>(s, row, runs, false, (unsigned long long)top_k - 1);
+        stay = (uint32_t)top_k;
+        held = hit.mass + (stay - hit.count) * hit.weight;
+    } else if (!whole)
+        stay = 0xFFFFFFFFu;             // with those that were not counted
+    const float top_p = !cold && a.top_p ? a.top_p[b] : 1.0f;
+    if (top_p < 1.0f) {                 // the first tokens whose mass reaches top_p of what is held
+        const double want = ceil((double)top_p * (double)held);
+        const unsigned long long need = want > 1.0 ? min((unsigned long long)want, held) : 1ull;
+        if (need > head)
+            return kAgain;
+        const Hit hit = search<C>(s, row, runs, true, need - 1);
+        const uint32_t more = (uint32_t)((need - hit.mass + hit.weight - 1) / hit.weight);
+        if (hit.count + more <= stay) {
+            stay = hit.count + more;
+            held = hit.mass + more * hit.weight;
         }
+    }
+    const float min_p = !cold && a.min_p ? a.min_p[b] : 0.0f;
+    if (!(min_p <= 0.0f) && kept < stay) {
+        if (!whole && min_p <= kHeadWeight)
+            return kAgain;
+        stay = max(kept, 1u);
+        const Hit hit = search<C>(s, row, runs, false, (unsigned long long)stay - 1);
+        held = hit.mass + (stay - hit.count) * hit.weight;
+    }
+    const double want = (double)a.u[b] * (double)held;
+    const unsigned long long t = want > 0.0 ? min((unsigned long long)want, held - 1) : 0ull;
+    if (t >= head)
+        return kAgain;
+    const Hit hit = search<C>(s, row, runs, true, t);
+    key = hit.key;
+    rank = (uint32_t)((t - hit.mass) / hit.weight);
+    if (a.logprob && lane == 0) {
+        const float d = value_of(key) - row.top_value, gap = key == row.top ? 0.0f : __fmaf_rn(d, row.inverse.hi, d * row.inverse.lo);
+        a.logprob[b] = gap - log1pf((float)(held - (1ull << kScale)) * (1.0f / (float)(1ull << kScale)));
+    }
+    return kMine;
+}
+
+template <int C>
+__global__ __launch_bounds__(kThreads) void sample_kernel(const __grid_constant__ SampleArgs a, int part, int vec, int ahead)
+{
+    extern __shared__ __align__(16) unsigned char sample_mem[];
+    Shared &s = *reinterpret_cast<Shared *>(sample_mem);
+    const int cta = C > 1 ? (int)tc::cluster_rank() : 0, b = blockIdx.x / C;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int first = cta * part, n = max(0, min(part, a.V - first));
+    tc::pdl_launch_dependents();
+    tc::pdl_wait();
+    const uint16_t *x = reinterpret_cast<const uint16_t *>(a.logits) + (int64_t)b * a.stride + first;
+    // what a CTA of the next wave reads, into L2 meanwhile
+    const int next = b + ahead;
+    if (vec && threadIdx.x == 0 && ahead && next < a.B && n >= 8)
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(x + (int64_t)ahead * a.stride), "r"((uint32_t)(n / 8 * 16)) : "memory");
+    uint32_t most = 0xFF80FF80u;        // of this thread's tokens; -inf
+#pragma unroll 4
+    for (int i = threadIdx.x * 8; i < n; i += kThreads * 8)
+        most = max_bf16x2(most, max_of(eight(x, i, n, vec)));
+    float temp = a.temperature ? a.temperature[b] : 1.0f;
+    const bool cold = !(temp > 0.0f);   // the first token of the order alone
+    temp = cold ? 1.0f : temp;
+    if (threadIdx.x < kGroups / 32)
+        s.flags[threadIdx.x] = 0;
+    // The largest value, and one that 256 tokens reach, or as many as there are groups of 4 C
+    // lanes with any: the least of the groups' largest.
+    uint32_t top = max(key_of(most & 0xFFFFu), key_of(most >> 16));
+#pragma unroll
+    for (int o = 1; o < 4 * C; o <<= 1)
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const uint32_t low = __reduce_min_sync(0xffffffffu, top ? top : 0xFFFFu);
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (lane == 0)
+        s.wave[warp] = top << 16 | low;
+    __syncthreads();
+    if (warp == 0) {
+        const uint32_t w = s.wave[lane];
+        top = __reduce_max_sync(0xffffffffu, w >> 16);
+        const uint32_t least = __reduce_min_sync(0xffffffffu, w & 0xFFFFu);
+        if (lane == 0)
+            s.top = top << 16 | least;
     }
     row_sync<C>();
-
-    // the found_rank-th token of the value found_key, over the CTAs' parts in order
-    bool mine = s.found;
-    if (mine) {
-        const uint32_t key = s.found_key;
-        uint32_t want = s.found_rank;
-        for (int c = 0; c <= rank && mine; ++c) {
-            const uint32_t w = remote_u32(tc::map_to_rank(smem_addr(&s.hist[key >> 1]), c)), has = key & 1 ? w >> 16 : w & 0xFFFFu;
-            if (c == rank)
-                mine = want < has;
-            else if (want < has)
-                mine = false;
-            else
-                want -= has;
+    Row row;
+    uint32_t reached;
+    {
+        const uint32_t t = lane < C ? remote_u32(tc::map_to_rank(smem_addr(&s.top), lane)) : 0xFFFFu;
+        row.top = __reduce_max_sync(0xffffffffu, t >> 16);
+        reached = __reduce_min_sync(0xffffffffu, t & 0xFFFFu);
+    }
+    if (row.top == 0) {                 // nothing to draw (all CTAs of the row alike)
+        if (cta == 0 && threadIdx.x == 0) {
+            a.tokens[b] = -1;
+            if (a.logprob)
+                a.logprob[b] = -INFINITY;
         }
-        if (mine) {     // each warp a run of the part
-            const int run = ((n + kWarps - 1) / kWarps + 255) / 256 * 256, from = warp * run, to = min(n, from + run);
-            uint32_t hits = 0;
-            for (int i = from + lane * 8; i < to; i += 256) {
-                uint32_t k[8];
-                eight(x, i, n, vec, k);
+        row_sync<C>();
+        return;
+    }
+    row.top_value = value_of(row.top);
+    row.inverse = reciprocal(temp);
+    const int last_group = row.top / kKeys;
+    for (bool whole = false;; whole = true) {
+        // counted: values from `cut` on; the second time all that have a weight (2^-46 is none)
+        float cut = cold ? row.top_value : fminf(row.top_value - (whole ? 33.0f : kHead) * temp, whole ? INFINITY : value_of(reached));
+        if (!(cut <= row.top_value))    // (infinite ones of both)
+            cut = row.top_value;
+        const uint32_t bits = __float_as_uint(cut) >> 16, cut2 = bits | bits << 16;     // bf16: towards zero
+        const int first_group = bits == 0xFF80u ? 0 : key_of(bits) / kKeys;
+        for (int i = first_group * (kKeys / 8) + threadIdx.x; i < (last_group + 1) * (kKeys / 8); i += kThreads)
+            reinterpret_cast<uint4 *>(s.hist)[i] = make_uint4(0u, 0u, 0u, 0u);
+        __syncthreads();
+        // base-2 exponents of the weights behind it
+        const Pair to2 = mul(row.inverse, {1.44269502f, 1.92596303e-08f});
+        const float2 to2_hi = make_float2(to2.hi, to2.hi), to2_lo = make_float2(to2.lo, to2.lo), minus_top = make_float2(-row.top_value, -row.top_value);
+        float tail = 0.0f;
+        const uint4 none = make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);      // -inf
+        auto load = [&](int base) {
+            const int i = base + (int)threadIdx.x * 8;
+            return i < n ? eight(x, i, n, vec) : none;
+        };
+        uint4 ahead1 = load(0), ahead2 = load(kThreads * 8);    // loads do not pass the atomics
+        for (int base = 0; base < n; base += kThreads * 8) {    // whole warps together
+            const uint4 v = ahead1;
+            ahead1 = ahead2;
+            ahead2 = load(base + 2 * kThreads * 8);
+            count_eight(s, v, cut2);
+            if (!whole)
+                tail += (behind(v.x, cut2, minus_top, to2_hi, to2_lo) + behind(v.y, cut2, minus_top, to2_hi, to2_lo)) +
+                        (behind(v.z, cut2, minus_top, to2_hi, to2_lo) + behind(v.w, cut2, minus_top, to2_hi, to2_lo));
+        }
+        unsigned long long sum = (unsigned long long)__float2ll_rn(tail * (float)(1ull << kScale));
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    hits += k[e] == key;
-            }
-            hits = __reduce_add_sync(0xffffffffu, hits);
+        for (int o = 16; o > 0; o >>= 1)
+            sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (lane == 0)
+            s.wide[warp] = sum;
+        __syncthreads();
+        for (int g = first_group + warp; g <= last_group; g += kWarps) {
+            const uint2 h = reinterpret_cast<const uint2 *>(s.hist)[g * (kKeys / 4) + lane];
+            if (__any_sync(0xffffffffu, h.x | h.y) && lane == 0)
+                atomicOr(&s.flags[g / 32], 1u << (g & 31));
+        }
+        if (warp == 0) {
+            sum = lane < kWarps ? s.wide[lane] : 0ull;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+                sum += __shfl_xor_sync(0xffffffffu, sum, o);
             if (lane == 0)
-                s.match[warp] = hits;
+                s.tail = sum;
+        }
+        row_sync<C>();
+
+        if (cta == 0) {
+            const float min_p = !cold && a.min_p ? a.min_p[b] : 0.0f;
+            // the least weight that min-p keeps: min_p 2^45, and 0 (min_p NaN, or past 1: none)
+            const unsigned long long least = min_p <= 0.0f ? 0ull : min_p <= 1.0f ? (unsigned long long)__float2ll_ru(min_p * (float)(1ull << kScale)) : ~0ull;
+            const Runs runs(first_group, last_group);
+            add_runs<C>(s, row, least, runs);
             __syncthreads();
-            uint32_t before_run = 0;
-            for (int w = 0; w < warp; ++w)
-                before_run += s.match[w];
-            if (want >= before_run && want < before_run + hits) {
-                want -= before_run;
-                for (int i0 = from; i0 < to; i0 += 256) {
-                    const int i = i0 + lane * 8;
-                    uint32_t k[8], mask = 0;
-                    if (i < to)
-                        eight(x, i, n, vec, k);
+            if (warp == 0) {            // whose part has the token, and its rank there
+                uint32_t key = 0, rank = 0;
+                const Verdict verdict = choose<C>(s, a, b, row, cold, whole, runs, key, rank);
+                uint32_t has = 0;
+                if (verdict == kMine && lane < C) {
+                    const uint32_t w = remote_u32(tc::map_to_rank(smem_addr(&s.hist[key >> 1]), lane));
+                    has = key & 1 ? w >> 16 : w & 0xFFFFu;
+                }
+                uint32_t before = has;
 #pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        mask |= (i < to && k[e] == key ? 1u : 0u) << e;
-                    uint32_t before = __popc(mask);
-#pragma unroll
-                    for (int o = 1; o < 32; o <<= 1) {
-                        const uint32_t p = __shfl_up_sync(0xffffffffu, before, o);
-                        before += lane >= o ? p : 0;
-                    }
-                    const uint32_t sum = __shfl_sync(0xffffffffu, before, 31);
-                    before -= __popc(mask);
-                    if (want >= before && want < before + __popc(mask)) {
-                        for (uint32_t skip = want - before; skip > 0; --skip)
-                            mask &= mask - 1;
-                        a.tokens[b] = first + i + __ffs(mask) - 1;
-                    }
-                    if (want < sum)
-                        break;
-                    want -= sum;
+                for (int o = 1; o < C; o <<= 1) {
+                    const uint32_t p = __shfl_up_sync(0xffffffffu, before, o);
+                    before += lane >= o ? p : 0;
+                }
+                before -= has;
+                if (lane < C) {
+                    const bool mine = rank >= before && rank < before + has;
+                    remote_store_u32(tc::map_to_rank(smem_addr(&s.key), lane), key);
+                    remote_store_u32(tc::map_to_rank(smem_addr(&s.rank), lane), rank - before);
+                    remote_store_u32(tc::map_to_rank(smem_addr(&s.verdict), lane), verdict == kMine && !mine ? kOther : verdict);
                 }
             }
         }
+        row_sync<C>();
+        if (s.verdict != kAgain)
+            break;
     }
-    if (C > 1)
-        tc::cluster_sync();     // no CTA leaves while another may read its counts
+    if (s.verdict != kMine)
+        return;
+
+    // the token: a warp looks at a run of the part
+    const uint32_t key = s.key, rank = s.rank;
+    const int run = ((n + kWarps - 1) / kWarps + 255) / 256 * 256, from = warp * run, to = min(n, from + run);
+    uint32_t hits = 0;
+#pragma unroll 4
+    for (int i = from + lane * 8; i < to; i += 256)
+        hits += __popc(equal_mask(eight(x, i, to, vec), key));
+    hits = __reduce_add_sync(0xffffffffu, hits);
+    if (lane == 0)
+        s.wave[warp] = hits;
+    __syncthreads();
+    const uint32_t in_front = __reduce_add_sync(0xffffffffu, lane < warp ? s.wave[lane] : 0u);
+    if (rank < in_front || rank >= in_front + hits)
+        return;
+    uint32_t want = rank - in_front;
+    for (int base = from; base < to; base += 256) {
+        const int i = base + lane * 8;
+        const uint32_t mask = i < to ? equal_mask(eight(x, i, to, vec), key) : 0u, mine = __popc(mask);
+        uint32_t upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t p = __shfl_up_sync(0xffffffffu, upto, o);
+            upto += lane >= o ? p : 0;
+        }
+        if (want >= upto - mine && want < upto) {
+            uint32_t left = mask;
+            for (uint32_t skip = want - (upto - mine); skip > 0; --skip)
+                left &= left - 1;
+            a.tokens[b] = first + i + __ffs(left) - 1;
+        }
+        const uint32_t all = __shfl_sync(0xffffffffu, upto, 31);
+        if (want < all)
+            return;
+        want -= all;
+    }
 }
 
 template <int C>
@@ -555,7 +721,7 @@ cudaError_t launch(const SampleArgs &a, cudaStream_t stream)
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = C > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kernel, a, part, vec);
+    return cudaLaunchKernelEx(&cfg, kernel, a, part, vec, device_sm_count() / C);
 }
 
 }  // namespace
