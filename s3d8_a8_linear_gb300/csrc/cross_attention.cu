@@ -207,7 +207,7 @@ __global__ __launch_bounds__(kThreads, 1) void cross_forward_kernel(const __grid
     const uint32_t bars = base + L::BARS;
     const uint32_t q_full = bars, q_empty = bars + 8, o_free = bars + 16, s_full = bars + 24, p_ready = bars + 40, pv_done = bars + 56, p_half = bars + 72;
     const uint32_t kv_full = bars + 88, kv_empty = kv_full + 8 * L::STAGES, v_ok = kv_empty + 8 * L::STAGES;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = a.Hq / a.heads;
+    const int warp = warp_index(), lane = threadIdx.x & 31, group = a.Hq / a.heads;
 
     if (warp == 0 && lane == 0) {
         mbar_init(q_full, 1);
@@ -267,7 +267,7 @@ __global__ __launch_bounds__(kThreads, 1) void cross_forward_kernel(const __grid
     __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = tmem_slot;
-    Share share(items, item_count, a.heads, p.ctas);
+    Share share(items, uniform(item_count), a.heads, p.ctas);
     Unit u;
     bool ok = true;
 
@@ -492,7 +492,7 @@ __global__ __launch_bounds__(kThreads, 1) void cross_forward_kernel(const __grid
             if (u.pair || s == 0) {
                 const bool whole = u.slot < 0;
                 const float by = whole ? (sum != 0.0f ? 1.0f / sum : 0.0f) : 1.0f;
-                const bool both = !u.pair && u.n > 1, noted = bad_any[u.pair ? s : 0];
+                const bool both = !u.pair && u.n > 1, noted = uniform(bad_any[u.pair ? s : 0]);
                 const uint32_t *note = bad + ((u.pair ? s : 0) * 128 + row) * 8;
                 __nv_bfloat16 *out = a.out + ((int64_t)t * a.Hq + u.head * group + row % group) * a.dim;
                 const int64_t slot = ((int64_t)blockIdx.x * 2 + u.slot) * p.rows + (u.pair ? s * 128 : 0) + row;
@@ -585,7 +585,7 @@ __global__ __launch_bounds__(kJoinWarps * 32) void cross_join_kernel(const __gri
     if (cut.c0 == cut.c1)
         return;
     const Item it = p.items[1 + i];
-    const int c0 = cut.c0, c1 = cut.c1, group = a.Hq / a.heads, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int c0 = cut.c0, c1 = cut.c1, group = a.Hq / a.heads, warp = warp_index(), lane = threadIdx.x & 31;
     for (int r = blockIdx.y * kJoinRows + warp; r < blockIdx.y * kJoinRows + kJoinRows && r < p.rows; r += kJoinWarps) {
         const int tile = r < kTile ? it.tile & 0xFFFF : it.tile >> 16 & 0xFFFF, row = r % kTile;
         const int t = tile * p.tokens_a_tile + row / group;

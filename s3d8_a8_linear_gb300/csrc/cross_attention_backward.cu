@@ -190,7 +190,7 @@ __global__ __launch_bounds__(kThreads, 1) void cross_dq_kernel(const __grid_cons
     const uint32_t q_full = bars, q_empty = bars + 8, o_free = bars + 16, s_full = bars + 24, s_read = bars + 32, done = bars + 40;
     const uint32_t dp_full = bars + 48, ds_ready = bars + 64;       // two each: of either buffer
     const uint32_t kv_full = bars + 80, kv_empty = kv_full + 8 * L::STAGES, k_ok = kv_empty + 8 * L::STAGES;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = a.Hq / a.heads;
+    const int warp = warp_index(), lane = threadIdx.x & 31, group = a.Hq / a.heads;
     if (threadIdx.x == 0) {
         mbar_init(q_full, 1);
         mbar_init(q_empty, 1);
@@ -455,7 +455,7 @@ __global__ __launch_bounds__(kThreads, 1) void cross_dkv_kernel(const __grid_con
     const uint32_t kv_full = bars, kv_empty = bars + 8, o_free = bars + 16, s_full = bars + 24, p_ready = bars + 32, dp_full = bars + 40, ds_ready = bars + 48,
                    done = bars + 56;
     const uint32_t q_full = bars + 64, q_empty = q_full + 8 * L::STAGES, q_ok = q_empty + 8 * L::STAGES;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, group = a.Hq / a.heads;
+    const int warp = warp_index(), lane = threadIdx.x & 31, group = a.Hq / a.heads;
     if (threadIdx.x == 0) {
         mbar_init(kv_full, 1);
         mbar_init(kv_empty, 1);
@@ -652,7 +652,7 @@ __global__ __launch_bounds__(kThreads, 1) void cross_dkv_kernel(const __grid_con
                 const int pair = jobs % PAIRS;
                 const uint32_t info = base + L::INFO + (pair * 4 * kTile + 64 * half) * 4;
                 const int *full = reinterpret_cast<const int *>(mem + L::FULL) + pair * 2;
-                const bool whole = full[half] != 0;
+                const bool whole = uniform(full[half]) != 0;
                 float x[64], y[64];
                 uint32_t w[32];
                 tmem_ld32(sc, x);
@@ -755,7 +755,7 @@ __global__ __launch_bounds__(kJoinWarps * 32) void cross_add_kernel(const __grid
     const Cut cut(p.items + 1, n, i, head, a.heads, p.ctas);
     if (cut.c0 == cut.c1)
         return;
-    const int tile = p.first + p.items[1 + i].tile, group = a.Hq / a.heads, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int tile = p.first + p.items[1 + i].tile, group = a.Hq / a.heads, warp = warp_index(), lane = threadIdx.x & 31;
     const int slot_rows = STATES ? 2 * kTile : p.rows;
     for (int r = blockIdx.y * 32 + warp; r < blockIdx.y * 32 + 32 && r < slot_rows; r += kJoinWarps) {
         const int row = STATES ? r % kTile : r;

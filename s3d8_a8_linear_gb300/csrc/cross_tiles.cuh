@@ -176,7 +176,7 @@ struct Share {
     bool begun;
 
     __device__ __forceinline__ Share(const Item *list, int n, int heads, int ctas)
-        : items(list), n_items(n), per_head(list[n].begin), begun(false)
+        : items(list), n_items(n), per_head(uniform(list[n].begin)), begun(false)
     {
         const int64_t all = (int64_t)heads * per_head, some = busy(ctas, all);
         at = blockIdx.x < some ? (int)(all * blockIdx.x / some) : 0;
@@ -192,14 +192,14 @@ struct Share {
         int lo = 0, hi = n_items;
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
-            if (items[mid].begin <= r)
+            if (uniform(items[mid].begin) <= r)
                 lo = mid;
             else
                 hi = mid;
         }
-        const int off = r - items[lo].begin, left = items[lo + 1].begin - r;
-        u.tile = items[lo].tile;
-        u.j0 = items[lo].j0 + off;
+        const int off = r - uniform(items[lo].begin), left = uniform(items[lo + 1].begin) - r;
+        u.tile = uniform(items[lo].tile);
+        u.j0 = uniform(items[lo].j0) + off;
         u.n = min(end - at, left);
         u.slot = off == 0 && u.n == left ? -1 : begun;
         at += u.n;

@@ -153,13 +153,6 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b)
     return *reinterpret_cast<float2 *>(&d);
 }
 
-__device__ __forceinline__ float2 mul2(float2 a, float2 b)
-{
-    uint64_t d, x = *reinterpret_cast<uint64_t *>(&a), y = *reinterpret_cast<uint64_t *>(&b);
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(x), "l"(y));
-    return *reinterpret_cast<float2 *>(&d);
-}
-
 __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
 {
     uint64_t d, x = *reinterpret_cast<uint64_t *>(&a), y = *reinterpret_cast<uint64_t *>(&b), z = *reinterpret_cast<uint64_t *>(&c);
@@ -173,7 +166,8 @@ struct Row {
     Pair inverse;       // 1 / T
 };
 
-__device__ __forceinline__ unsigned long long weight_of(uint32_t key, const Row &r)
+// (Out of line, as search() is: a CTA passes its code once, and what is short is there sooner.)
+__device__ __noinline__ unsigned long long weight_of(uint32_t key, Row r)
 {
     if (key == r.top)
         return 1ull << kScale;
@@ -244,23 +238,27 @@ __device__ __forceinline__ void scan_run(const uint32_t (&n)[4], const unsigned 
     for (int o = 1; o < 32; o <<= 1) {
         const uint32_t pc = __shfl_up_sync(0xffffffffu, count, o);
         const unsigned long long pm = __shfl_up_sync(0xffffffffu, mass, o);
-        if ((int)(threadIdx.x & 31) >= o)
-            count += pc, mass += pm;
+        const bool in = (int)(threadIdx.x & 31) >= o;
+        count += in ? pc : 0u;
+        mass += in ? pm : 0ull;
     }
 }
 
 // The eight tokens from i on (i a multiple of 8), two a word; those at n and behind are -inf.
-__device__ __forceinline__ uint4 eight(const uint16_t *x, int i, int n, bool vec)
+__device__ __noinline__ uint4 eight_slowly(const uint16_t *x, int left)
 {
-    if (vec && i + 8 <= n)
-        return __ldg(reinterpret_cast<const uint4 *>(x + i));
     uint32_t w[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        const uint32_t lo = i + 2 * e < n ? __ldg(x + i + 2 * e) : 0xFF80u, hi = i + 2 * e + 1 < n ? __ldg(x + i + 2 * e + 1) : 0xFF80u;
+        const uint32_t lo = 2 * e < left ? __ldg(x + 2 * e) : 0xFF80u, hi = 2 * e + 1 < left ? __ldg(x + 2 * e + 1) : 0xFF80u;
         w[e] = lo | hi << 16;
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ uint4 eight(const uint16_t *x, int i, int n, bool vec)
+{
+    return vec && i + 8 <= n ? __ldg(reinterpret_cast<const uint4 *>(x + i)) : eight_slowly(x + i, n - i);
 }
 
 // The larger of each two bf16 (of a NaN and a number, the number).
@@ -276,15 +274,20 @@ __device__ __forceinline__ uint32_t max_of(const uint4 &v) { return max_bf16x2(m
 __device__ __forceinline__ float lo_value(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_value(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-// Which of eight tokens have a value.
-__device__ __forceinline__ uint32_t equal_mask(uint4 v, uint32_t key)
+// Which of eight tokens have a value (bf16, twice in a word; both zeros are one).
+__device__ __forceinline__ uint32_t equal(uint32_t a, uint32_t b)
 {
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-    uint32_t mask = 0;
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-        mask |= (key_of(e & 1 ? w[e / 2] >> 16 : w[e / 2] & 0xFFFFu) == key ? 1u : 0u) << e;
-    return mask;
+    uint32_t d;
+    asm("set.eq.u32.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+__device__ __forceinline__ uint32_t equal_mask(uint4 v, uint32_t value)
+{
+    // token 2 j is bit 2 j, token 2 j + 1 is bit 16 + 2 j + 1; then side by side
+    const uint32_t m = (equal(v.x, value) & 0x00020001u) | (equal(v.y, value) & 0x00080004u) | (equal(v.z, value) & 0x00200010u) |
+                       (equal(v.w, value) & 0x00800040u);
+    return (m | m >> 16) & 0xFFu;
 }
 
 // Halves of a word that are at least those of another: 0xFFFF, else (and for NaN) 0.
@@ -316,19 +319,34 @@ __device__ __forceinline__ void count_eight(Shared &s, uint4 v, uint32_t cut)
     }
 }
 
-// The weights of two tokens, where they are not counted, from base-2 exponents d * to2 of
-// their distance to the largest; 0 for -inf, NaN and what is below 2^-126.
-__device__ __forceinline__ float behind(uint32_t w, uint32_t cut, float2 minus_top, float2 to2_hi, float2 to2_lo)
-{
-    const float2 d = add2(make_float2(lo_value(w), hi_value(w)), minus_top), x = mul2(d, to2_hi);
-    const float2 rest = mul2(fma2(d, to2_lo, fma2(d, to2_hi, make_float2(-x.x, -x.y))), make_float2(0.693147f, 0.693147f));
-    float2 p;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p.x) : "f"(x.x));
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p.y) : "f"(x.y));
-    p = fma2(p, rest, p);
-    const uint32_t counted = at_least(w, cut);
-    return (x.x > -126.0f && !(counted & 1) ? p.x : 0.0f) + (x.y > -126.0f && !(counted >> 31) ? p.y : 0.0f);
-}
+// How the weights behind the head are taken: base-2 exponents y c + b, and the parts of c and
+// b that fp32 does not hold, times ln 2.
+struct Behind {
+    float cut;
+    float2 c, b, c_rest, b_rest;
+
+    __device__ __forceinline__ Behind(float cut, const Row &row)
+        : cut(cut)
+    {
+        const Pair to2 = mul(row.inverse, {1.44269502f, 1.92596303e-08f}), top = mul(to2, {-row.top_value, 0.0f});
+        c = make_float2(to2.hi, to2.hi);
+        b = make_float2(top.hi, top.hi);
+        c_rest = make_float2(to2.lo * 0.693147f, to2.lo * 0.693147f);
+        b_rest = make_float2(top.lo * 0.693147f, top.lo * 0.693147f);
+    }
+
+    // Of two tokens, where they are not counted.
+    __device__ __forceinline__ float2 operator()(uint32_t w) const
+    {
+        w = max_bf16x2(w, 0xF149F149u);         // -inf and NaN: -1e30, which has no weight
+        const float2 y = make_float2(lo_value(w), hi_value(w)), x = fma2(y, c, b), rest = fma2(y, c_rest, b_rest);
+        float2 p;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p.x) : "f"(x.x));
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p.y) : "f"(x.y));
+        p = fma2(p, rest, p);
+        return make_float2(y.x < cut ? p.x : 0.0f, y.y < cut ? p.y : 0.0f);
+    }
+};
 
 // A value of the order of all counted tokens, its weight, and the tokens and weight in front of it.
 struct Hit {
@@ -339,7 +357,7 @@ struct Hit {
 // The value that holds the `target`-th unit (from 0) of the tokens, or of their weight.  One
 // warp of the first CTA.
 template <int C>
-__device__ __forceinline__ Hit search(Shared &s, const Row &row, const Runs &runs, bool by_mass, unsigned long long target)
+__device__ __noinline__ Hit search(Shared &s, Row row, Runs runs, bool by_mass, unsigned long long target)
 {
     const int lane = threadIdx.x & 31;
     int i = 0;
@@ -403,7 +421,7 @@ __device__ __forceinline__ void row_sync()
 template <int C>
 __device__ __forceinline__ void add_runs(Shared &s, const Row &row, unsigned long long least, const Runs &runs)
 {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = warp_index(), lane = threadIdx.x & 31;
     for (int i = warp; i < runs.count; i += kWarps) {
         const int first = runs.end - i * runs.size() - 1 - (runs.fine ? 1 : 4) * lane, g = (runs.end - i * runs.size() - 1) / kKeys;
         uint32_t some = 0;
@@ -450,8 +468,9 @@ __device__ __forceinline__ Verdict choose(Shared &s, const SampleArgs &a, int b,
         for (int o = 1; o < 32; o <<= 1) {
             const uint32_t pc = __shfl_up_sync(0xffffffffu, c, o), pk = __shfl_up_sync(0xffffffffu, k, o);
             const unsigned long long pm = __shfl_up_sync(0xffffffffu, m, o);
-            if (lane >= o)
-                c += pc, k += pk, m += pm;
+            c += lane >= o ? pc : 0u;
+            k += lane >= o ? pk : 0u;
+            m += lane >= o ? pm : 0ull;
         }
         if (i < runs.count)
             s.count_before[i] = stay + c - count, s.mass_before[i] = head + m - mass;
@@ -467,7 +486,7 @@ __device__ __forceinline__ Verdict choose(Shared &s, const SampleArgs &a, int b,
     held += head;
     __syncwarp();
 
-    const int32_t top_k = cold ? 1 : a.top_k ? a.top_k[b] : 0;
+    const int32_t top_k = uniform(cold ? 1 : a.top_k ? a.top_k[b] : 0);
     if (top_k > 0 && (uint32_t)top_k > stay && !whole)
         return kAgain;
     if (top_k > 0 && (uint32_t)top_k <= stay) {
@@ -476,7 +495,7 @@ __device__ __forceinline__ Verdict choose(Shared &s, const SampleArgs &a, int b,
         held = hit.mass + (stay - hit.count) * hit.weight;
     } else if (!whole)
         stay = 0xFFFFFFFFu;             // with those that were not counted
-    const float top_p = !cold && a.top_p ? a.top_p[b] : 1.0f;
+    const float top_p = uniform(!cold && a.top_p ? a.top_p[b] : 1.0f);
     if (top_p < 1.0f) {                 // the first tokens whose mass reaches top_p of what is held
         const double want = ceil((double)top_p * (double)held);
         const unsigned long long need = want > 1.0 ? min((unsigned long long)want, held) : 1ull;
@@ -489,7 +508,7 @@ __device__ __forceinline__ Verdict choose(Shared &s, const SampleArgs &a, int b,
             held = hit.mass + more * hit.weight;
         }
     }
-    const float min_p = !cold && a.min_p ? a.min_p[b] : 0.0f;
+    const float min_p = uniform(!cold && a.min_p ? a.min_p[b] : 0.0f);
     if (!(min_p <= 0.0f) && kept < stay) {
         if (!whole && min_p <= kHeadWeight)
             return kAgain;
@@ -497,7 +516,7 @@ __device__ __forceinline__ Verdict choose(Shared &s, const SampleArgs &a, int b,
         const Hit hit = search<C>(s, row, runs, false, (unsigned long long)stay - 1);
         held = hit.mass + (stay - hit.count) * hit.weight;
     }
-    const double want = (double)a.u[b] * (double)held;
+    const double want = (double)uniform(a.u[b]) * (double)held;
     const unsigned long long t = want > 0.0 ? min((unsigned long long)want, held - 1) : 0ull;
     if (t >= head)
         return kAgain;
@@ -516,8 +535,8 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(const __grid_constant_
 {
     extern __shared__ __align__(16) unsigned char sample_mem[];
     Shared &s = *reinterpret_cast<Shared *>(sample_mem);
-    const int cta = C > 1 ? (int)tc::cluster_rank() : 0, b = blockIdx.x / C;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int cta = C > 1 ? uniform((int)tc::cluster_rank()) : 0, b = blockIdx.x / C;
+    const int warp = warp_index(), lane = threadIdx.x & 31;
     const int first = cta * part, n = max(0, min(part, a.V - first));
     tc::pdl_launch_dependents();
     tc::pdl_wait();
@@ -530,7 +549,7 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(const __grid_constant_
 #pragma unroll 4
     for (int i = threadIdx.x * 8; i < n; i += kThreads * 8)
         most = max_bf16x2(most, max_of(eight(x, i, n, vec)));
-    float temp = a.temperature ? a.temperature[b] : 1.0f;
+    float temp = uniform(a.temperature ? a.temperature[b] : 1.0f);
     const bool cold = !(temp > 0.0f);   // the first token of the order alone
     temp = cold ? 1.0f : temp;
     if (threadIdx.x < kGroups / 32)
@@ -573,6 +592,7 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(const __grid_constant_
     row.top_value = value_of(row.top);
     row.inverse = reciprocal(temp);
     const int last_group = row.top / kKeys;
+    Verdict verdict;
     for (bool whole = false;; whole = true) {
         // counted: values from `cut` on; the second time all that have a weight (2^-46 is none)
         float cut = cold ? row.top_value : fminf(row.top_value - (whole ? 33.0f : kHead) * temp, whole ? INFINITY : value_of(reached));
@@ -583,10 +603,8 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(const __grid_constant_
         for (int i = first_group * (kKeys / 8) + threadIdx.x; i < (last_group + 1) * (kKeys / 8); i += kThreads)
             reinterpret_cast<uint4 *>(s.hist)[i] = make_uint4(0u, 0u, 0u, 0u);
         __syncthreads();
-        // base-2 exponents of the weights behind it
-        const Pair to2 = mul(row.inverse, {1.44269502f, 1.92596303e-08f});
-        const float2 to2_hi = make_float2(to2.hi, to2.hi), to2_lo = make_float2(to2.lo, to2.lo), minus_top = make_float2(-row.top_value, -row.top_value);
-        float tail = 0.0f;
+        const Behind behind(__uint_as_float(bits << 16), row);
+        float2 tails = make_float2(0.0f, 0.0f);
         const uint4 none = make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u);      // -inf
         auto load = [&](int base) {
             const int i = base + (int)threadIdx.x * 8;
@@ -599,9 +617,9 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(const __grid_constant_
             ahead2 = load(base + 2 * kThreads * 8);
             count_eight(s, v, cut2);
             if (!whole)
-                tail += (behind(v.x, cut2, minus_top, to2_hi, to2_lo) + behind(v.y, cut2, minus_top, to2_hi, to2_lo)) +
-                        (behind(v.z, cut2, minus_top, to2_hi, to2_lo) + behind(v.w, cut2, minus_top, to2_hi, to2_lo));
+                tails = add2(tails, add2(add2(behind(v.x), behind(v.y)), add2(behind(v.z), behind(v.w))));
         }
+        const float tail = tails.x + tails.y;
         unsigned long long sum = (unsigned long long)__float2ll_rn(tail * (float)(1ull << kScale));
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
@@ -625,7 +643,7 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(const __grid_constant_
         row_sync<C>();
 
         if (cta == 0) {
-            const float min_p = !cold && a.min_p ? a.min_p[b] : 0.0f;
+            const float min_p = uniform(!cold && a.min_p ? a.min_p[b] : 0.0f);
             // the least weight that min-p keeps: min_p 2^45, and 0 (min_p NaN, or past 1: none)
             const unsigned long long least = min_p <= 0.0f ? 0ull : min_p <= 1.0f ? (unsigned long long)__float2ll_ru(min_p * (float)(1ull << kScale)) : ~0ull;
             const Runs runs(first_group, last_group);
@@ -633,9 +651,9 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(const __grid_constant_
             __syncthreads();
             if (warp == 0) {            // whose part has the token, and its rank there
                 uint32_t key = 0, rank = 0;
-                const Verdict verdict = choose<C>(s, a, b, row, cold, whole, runs, key, rank);
+                const Verdict found = choose<C>(s, a, b, row, cold, whole, runs, key, rank);
                 uint32_t has = 0;
-                if (verdict == kMine && lane < C) {
+                if (found == kMine && lane < C) {
                     const uint32_t w = remote_u32(tc::map_to_rank(smem_addr(&s.hist[key >> 1]), lane));
                     has = key & 1 ? w >> 16 : w & 0xFFFFu;
                 }
@@ -650,24 +668,26 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(const __grid_constant_
                     const bool mine = rank >= before && rank < before + has;
                     remote_store_u32(tc::map_to_rank(smem_addr(&s.key), lane), key);
                     remote_store_u32(tc::map_to_rank(smem_addr(&s.rank), lane), rank - before);
-                    remote_store_u32(tc::map_to_rank(smem_addr(&s.verdict), lane), verdict == kMine && !mine ? kOther : verdict);
+                    remote_store_u32(tc::map_to_rank(smem_addr(&s.verdict), lane), found == kMine && !mine ? kOther : found);
                 }
             }
+            __syncthreads();
         }
         row_sync<C>();
-        if (s.verdict != kAgain)
+        verdict = (Verdict)uniform(s.verdict);
+        if (verdict != kAgain)
             break;
     }
-    if (s.verdict != kMine)
+    if (verdict != kMine)
         return;
 
     // the token: a warp looks at a run of the part
-    const uint32_t key = s.key, rank = s.rank;
+    const uint32_t rank = s.rank, bits = __float_as_uint(value_of(s.key)) >> 16, value = bits | bits << 16;
     const int run = ((n + kWarps - 1) / kWarps + 255) / 256 * 256, from = warp * run, to = min(n, from + run);
     uint32_t hits = 0;
 #pragma unroll 4
     for (int i = from + lane * 8; i < to; i += 256)
-        hits += __popc(equal_mask(eight(x, i, to, vec), key));
+        hits += __popc(equal_mask(eight(x, i, to, vec), value));
     hits = __reduce_add_sync(0xffffffffu, hits);
     if (lane == 0)
         s.wave[warp] = hits;
@@ -678,7 +698,7 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(const __grid_constant_
     uint32_t want = rank - in_front;
     for (int base = from; base < to; base += 256) {
         const int i = base + lane * 8;
-        const uint32_t mask = i < to ? equal_mask(eight(x, i, to, vec), key) : 0u, mine = __popc(mask);
+        const uint32_t mask = i < to ? equal_mask(eight(x, i, to, vec), value) : 0u, mine = __popc(mask);
         uint32_t upto = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
