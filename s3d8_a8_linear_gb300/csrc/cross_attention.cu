@@ -46,7 +46,7 @@ struct Plan {
     int chunk_rows;                     // query rows that a copy fills
     int ctas;
     float *parts, *tops;                // [ctas][2][rows][DP], [ctas][2][rows][2]
-    Item *items;                        // the list, for the join (its first entry: how many)
+    Cut *cuts;                          // [ctas]: what there is to join
     int negative;                       // scale < 0: the scores are those of -Q
 };
 
@@ -256,12 +256,6 @@ __global__ __launch_bounds__(kThreads, 1) void cross_forward_kernel(const __grid
         if (lane == 0)
             item_count = n;
         __syncwarp();
-        if (blockIdx.x == 0) {      // for the join
-            for (int i = lane; i <= n; i += 32)
-                p.items[1 + i] = items[i];
-            if (lane == 0)
-                p.items[0].begin = n;
-        }
     }
     tc::tc_fence_before();
     __syncthreads();
@@ -296,6 +290,8 @@ __global__ __launch_bounds__(kThreads, 1) void cross_forward_kernel(const __grid
             // not before the last copies have landed
             for (int i = at - L::STAGES < 0 ? 0 : at - L::STAGES; i < at; ++i)
                 ok &= tc::warp_wait(kv_full + 8 * (i % L::STAGES), (i / L::STAGES) & 1);
+            if (lane == 0)
+                p.cuts[blockIdx.x] = cut_of(share, u, at > 0, a.heads, p.ctas);
         } else if (warp == 1) {         // scores, a chain after the other
             const int ksteps = (a.dim + 15) / 16;
             const uint32_t id_s = idesc_cols(kTile) | (p.negative ? kNegateA : 0u);
@@ -571,47 +567,52 @@ __global__ __launch_bounds__(kThreads, 1) void cross_forward_kernel(const __grid
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
-// Joins the parts of the pieces that shares cut: a warp a row, parts in order.
+// Joins the parts of what shares cut: a warp a row, parts in order.  Block (CTA, rows).
 template <int DP>
 __global__ __launch_bounds__(kJoinWarps * 32) void cross_join_kernel(const __grid_constant__ CrossArgs a, const __grid_constant__ Plan p)
 {
     constexpr int V = DP / 32;
     tc::pdl_launch_dependents();
     tc::pdl_wait();
-    const int n = p.items[0].begin, i = blockIdx.x / a.heads, head = blockIdx.x % a.heads;
-    if (i >= n)
+    const Cut cut = p.cuts[blockIdx.x];
+    if (cut.c1 < 0)
         return;
-    const Cut cut(p.items + 1, n, i, head, a.heads, p.ctas);
-    if (cut.c0 == cut.c1)
-        return;
-    const Item it = p.items[1 + i];
-    const int c0 = cut.c0, c1 = cut.c1, group = a.Hq / a.heads, warp = warp_index(), lane = threadIdx.x & 31;
+    const int warp = warp_index(), lane = threadIdx.x & 31, group = a.Hq / a.heads, n = cut.c1 - (int)blockIdx.x + 1;
     for (int r = blockIdx.y * kJoinRows + warp; r < blockIdx.y * kJoinRows + kJoinRows && r < p.rows; r += kJoinWarps) {
-        const int tile = r < kTile ? it.tile & 0xFFFF : it.tile >> 16 & 0xFFFF, row = r % kTile;
+        const int tile = r < kTile ? cut.tile & 0xFFFF : cut.tile >> 16 & 0xFFFF, row = r % kTile;
         const int t = tile * p.tokens_a_tile + row / group;
         if (tile == kNoTile || row >= p.chunk_rows || t >= a.T)
             continue;
-        auto slot = [&](int c) { return cut.slot(c) * p.rows + r; };
+        auto slot = [&](int i) { return ((int64_t)(blockIdx.x + i) * 2 + (i == 0 ? cut.slot : 0)) * p.rows + r; };
         float top = -INFINITY;
-        for (int c = c0 + lane; c <= c1; c += 32)
-            top = fmaxf(top, p.tops[2 * slot(c)]);
+        for (int i = lane; i < n; i += 32)
+            top = fmaxf(top, p.tops[2 * slot(i)]);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         const float zero = top == -INFINITY ? 0.0f : top;
         float sum = 0.0f, acc[V] = {};
-        for (int c = c0; c <= c1; ++c) {
-            const int64_t at = slot(c);
-            const float2 part = reinterpret_cast<const float2 *>(p.tops)[at];
-            if (part.y == 0.0f)         // saw nothing: its sums were not written
-                continue;
-            const float turn = ex2(part.x - zero);
-            sum += part.y * turn;
+        for (int base = 0; base < n; base += 32) {
+            float2 mine = make_float2(-INFINITY, 0.0f);
+            if (base + lane < n)
+                mine = reinterpret_cast<const float2 *>(p.tops)[slot(base + lane)];
+            const float turn = mine.y == 0.0f ? 0.0f : ex2(mine.x - zero);      // saw nothing: its sums were not written
+            float s = mine.y * turn;
 #pragma unroll
-            for (int v = 0; v < V; ++v)
-                acc[v] = fmaf(p.parts[at * DP + lane + 32 * v], turn, acc[v]);
+            for (int o = 16; o > 0; o >>= 1)
+                s += __shfl_xor_sync(0xffffffffu, s, o);
+            sum += s;
+            const int count = min(32, n - base);
+#pragma unroll 4
+            for (int i = 0; i < count; ++i) {
+                const float by = __shfl_sync(0xffffffffu, turn, i), some = __shfl_sync(0xffffffffu, mine.y, i);
+                const float *part = p.parts + slot(base + i) * DP + lane;
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+                    acc[v] = fmaf(some == 0.0f ? 0.0f : part[32 * v], by, acc[v]);
+            }
         }
-        const int64_t at = (int64_t)t * a.Hq + head * group + row % group;
+        const int64_t at = (int64_t)t * a.Hq + cut.head * group + row % group;
         const int2 see = span_of(a.spans, a.S, t, nullptr);
         const bool some = see.x < see.y;
         const float by = some ? 1.0f / sum : 0.0f;
@@ -650,8 +651,8 @@ Plan plan_of(int64_t T, int64_t Hq, int64_t heads, int DP, size_t *bytes)
     p.parts = nullptr;
     p.tops = reinterpret_cast<float *>(at);
     at += ((size_t)p.ctas * 2 * p.rows * 2 * sizeof(float) + 15) / 16 * 16;
-    p.items = reinterpret_cast<Item *>(at);
-    *bytes = at + (kMostTiles + 2) * sizeof(Item);
+    p.cuts = reinterpret_cast<Cut *>(at);
+    *bytes = at + p.ctas * sizeof(Cut);
     return p;
 }
 
@@ -665,7 +666,7 @@ cudaError_t launch(const CrossArgs &a, cudaStream_t stream)
     char *ws = static_cast<char *>(a.ws);
     p.parts = reinterpret_cast<float *>(ws);
     p.tops = reinterpret_cast<float *>(ws + reinterpret_cast<size_t>(p.tops));
-    p.items = reinterpret_cast<Item *>(ws + reinterpret_cast<size_t>(p.items));
+    p.cuts = reinterpret_cast<Cut *>(ws + reinterpret_cast<size_t>(p.cuts));
     p.negative = a.scale < 0.0f;
     CUtensorMap mq, mk, mv;
     cudaError_t e = row_map(&mq, a.q, a.T, a.Hq, a.dim, a.qs, a.Hq / a.heads, p.tokens_a_tile);
@@ -679,7 +680,7 @@ cudaError_t launch(const CrossArgs &a, cudaStream_t stream)
     if (e == cudaSuccess)
         e = tc::launch_pdl(cross_forward_kernel<DP>, dim3(p.ctas), dim3(kThreads), L::BYTES, stream, mq, mk, mv, a, p);
     if (e == cudaSuccess)
-        e = tc::launch_pdl(cross_join_kernel<DP>, dim3(p.tiles * a.heads, (p.rows + kJoinRows - 1) / kJoinRows), dim3(kJoinWarps * 32), 0, stream, a, p);
+        e = tc::launch_pdl(cross_join_kernel<DP>, dim3(p.ctas, (p.rows + kJoinRows - 1) / kJoinRows), dim3(kJoinWarps * 32), 0, stream, a, p);
     return e;
 }
 

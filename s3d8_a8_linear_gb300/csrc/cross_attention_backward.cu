@@ -27,7 +27,7 @@ using namespace cross;
 
 constexpr int kThreads = 384;
 constexpr int kMostTiles = 1024;        // tiles of a launch that have sums of their own
-constexpr int kJoinWarps = 8;
+constexpr int kJoinWarps = 8, kJoinRows = 32;
 
 struct Plan {
     int tokens_a_tile, chunk_rows;      // query rows that a copy fills
@@ -37,18 +37,20 @@ struct Plan {
     float2 *info;                       // [T * Hq]: -lse in base-2 exponents, -delta
     int2 *ranges;                       // [q_tiles]: states that some row sees
     float *parts;                       // [ctas][2][1 or 2][rows][DP]
-    Item *items;                        // the list, for the join (its first entry: how many)
+    Cut *cuts;                          // [ctas]: what there is to add
     int negative;
 };
 
-// delta and lse of a tile's rows of one key/value head, and the tile's range.
+constexpr int kReadyRows = 32;          // of a block
+
+// delta and lse of some of a tile's rows of one key/value head, and the tile's range.
 __global__ __launch_bounds__(256) void cross_ready_kernel(const __grid_constant__ CrossArgs a, const __grid_constant__ Plan p)
 {
     tc::pdl_launch_dependents();
     tc::pdl_wait();
     const int tile = blockIdx.x, head = blockIdx.y, group = a.Hq / a.heads, half = threadIdx.x >> 4, lane = threadIdx.x & 15;
     const int t0 = tile * p.tokens_a_tile;
-    if (head == 0 && threadIdx.x < 32) {
+    if (head == 0 && blockIdx.z == 0 && threadIdx.x < 32) {
         int lo = 0x7FFFFFFF, hi = 0;
         for (int i = threadIdx.x; i < p.tokens_a_tile && t0 + i < a.T; i += 32) {
             const int2 s = span_of(a.spans, a.S, t0 + i, a.status);
@@ -60,8 +62,8 @@ __global__ __launch_bounds__(256) void cross_ready_kernel(const __grid_constant_
         if (threadIdx.x == 0)
             p.ranges[tile] = make_int2(lo, hi);
     }
-#pragma unroll 4
-    for (int r = half; r < kTile; r += 16) {        // whole warps together
+#pragma unroll
+    for (int r = blockIdx.z * kReadyRows + half; r < (int)(blockIdx.z + 1) * kReadyRows; r += 16) {    // whole warps together
         const int t = t0 + r / group, h = head * group + r % group;
         const bool live = r < p.chunk_rows && t < a.T;
         float sum = 0.0f;
@@ -222,13 +224,6 @@ __global__ __launch_bounds__(kThreads, 1) void cross_dq_kernel(const __grid_cons
             const int2 r = p.ranges[p.first + i];
             return make_int2(r.x / kTile, (r.y + kTile - 1) / kTile);
         });
-        __syncwarp();
-        if (blockIdx.x == 0) {
-            for (int i = lane; i <= p.tiles; i += 32)
-                p.items[1 + i] = items[i];
-            if (lane == 0)
-                p.items[0].begin = p.tiles;
-        }
     }
     tc::tc_fence_before();
     __syncthreads();
@@ -260,6 +255,8 @@ __global__ __launch_bounds__(kThreads, 1) void cross_dq_kernel(const __grid_cons
         }
         for (int i = at - L::STAGES < 0 ? 0 : at - L::STAGES; i < at; ++i)      // not before the last copies have landed
             ok &= tc::warp_wait(kv_full + 8 * (i % L::STAGES), (i / L::STAGES) & 1);
+        if (lane == 0)
+            p.cuts[blockIdx.x] = cut_of(share, u, at > 0, a.heads, p.ctas);
     } else if (warp == 1) {         // products
         const int ksteps = (a.dim + 15) / 16;
         const uint32_t id_s = idesc_cols(kTile) | (p.negative ? kNegateA : 0u), id_p = idesc_cols(kTile), id_o = idesc_rows(ksteps * 16);
@@ -493,13 +490,6 @@ __global__ __launch_bounds__(kThreads, 1) void cross_dkv_kernel(const __grid_con
     __syncthreads();
     if (warp == 0) {
         make_list(p.tiles, items, [&](int i) { return ranges[i]; });
-        __syncwarp();
-        if (blockIdx.x == 0) {
-            for (int i = lane; i <= p.tiles; i += 32)
-                p.items[1 + i] = items[i];
-            if (lane == 0)
-                p.items[0].begin = p.tiles;
-        }
     }
     tc::tc_fence_before();
     __syncthreads();
@@ -530,6 +520,8 @@ __global__ __launch_bounds__(kThreads, 1) void cross_dkv_kernel(const __grid_con
         }
         for (int i = at - L::STAGES < 0 ? 0 : at - L::STAGES; i < at; ++i)
             ok &= tc::warp_wait(q_full + 8 * (i % L::STAGES), (i / L::STAGES) & 1);
+        if (lane == 0)
+            p.cuts[blockIdx.x] = cut_of(share, u, at > 0, a.heads, p.ctas);
     } else if (warp == 1) {         // products
         const int ksteps = (a.dim + 15) / 16;
         const uint32_t id_s = idesc_cols(kTile) | (p.negative ? kNegateA : 0u), id_p = idesc_cols(kTile), id_o = idesc_rows(ksteps * 16);
@@ -743,21 +735,20 @@ __global__ __launch_bounds__(kThreads, 1) void cross_dkv_kernel(const __grid_con
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
 }
 
-// Adds the parts of the items that shares cut: a warp a row, in order.  STATES: rows are
-// states (dv and dk, one behind the other in a slot), else query rows.
+// Adds the parts of what shares cut: a warp a row, in order.  Block (CTA, rows).  STATES: rows
+// are states (dv and dk, one behind the other in a slot), else query rows.
 template <int DP, bool STATES>
 __global__ __launch_bounds__(kJoinWarps * 32) void cross_add_kernel(const __grid_constant__ CrossArgs a, const __grid_constant__ Plan p)
 {
     constexpr int V = DP / 32;
     tc::pdl_launch_dependents();
     tc::pdl_wait();
-    const int n = p.items[0].begin, i = blockIdx.x / a.heads, head = blockIdx.x % a.heads;
-    const Cut cut(p.items + 1, n, i, head, a.heads, p.ctas);
-    if (cut.c0 == cut.c1)
+    const Cut cut = p.cuts[blockIdx.x];
+    if (cut.c1 < 0)
         return;
-    const int tile = p.first + p.items[1 + i].tile, group = a.Hq / a.heads, warp = warp_index(), lane = threadIdx.x & 31;
+    const int tile = p.first + cut.tile, group = a.Hq / a.heads, warp = warp_index(), lane = threadIdx.x & 31, n = cut.c1 - (int)blockIdx.x + 1;
     const int slot_rows = STATES ? 2 * kTile : p.rows;
-    for (int r = blockIdx.y * 32 + warp; r < blockIdx.y * 32 + 32 && r < slot_rows; r += kJoinWarps) {
+    for (int r = blockIdx.y * kJoinRows + warp; r < blockIdx.y * kJoinRows + kJoinRows && r < slot_rows; r += kJoinWarps) {
         const int row = STATES ? r % kTile : r;
         __nv_bfloat16 *out;
         float by = a.scale;
@@ -765,17 +756,18 @@ __global__ __launch_bounds__(kJoinWarps * 32) void cross_add_kernel(const __grid
             const int64_t j = (int64_t)tile * kTile + row;
             if (j >= a.S)
                 continue;
-            out = (r < kTile ? a.dv : a.dk) + (j * a.heads + head) * a.dim;
+            out = (r < kTile ? a.dv : a.dk) + (j * a.heads + cut.head) * a.dim;
             by = r < kTile ? 1.0f : a.scale;
         } else {
             const int64_t t = (int64_t)tile * p.tokens_a_tile + row / group;
             if (row >= p.chunk_rows || t >= a.T)
                 continue;
-            out = a.dq + (t * a.Hq + head * group + row % group) * a.dim;
+            out = a.dq + (t * a.Hq + cut.head * group + row % group) * a.dim;
         }
         float acc[V] = {};
-        for (int c = cut.c0; c <= cut.c1; ++c) {
-            const float *part = p.parts + (cut.slot(c) * slot_rows + r) * DP + lane;
+#pragma unroll 4
+        for (int i = 0; i < n; ++i) {
+            const float *part = p.parts + (((int64_t)(blockIdx.x + i) * 2 + (i == 0 ? cut.slot : 0)) * slot_rows + r) * DP + lane;
 #pragma unroll
             for (int v = 0; v < V; ++v)
                 acc[v] += part[32 * v];
@@ -807,7 +799,7 @@ Plan plan_of(int64_t T, int64_t Hq, int64_t heads, int DP, size_t *bytes)
     p.info = reinterpret_cast<float2 *>(take((size_t)T * Hq * sizeof(float2)));
     p.ranges = reinterpret_cast<int2 *>(take((size_t)p.q_tiles * sizeof(int2)));
     p.parts = reinterpret_cast<float *>(take((size_t)p.ctas * 2 * 2 * kTile * DP * sizeof(float)));
-    p.items = reinterpret_cast<Item *>(take((kMostTiles + 2) * sizeof(Item)));
+    p.cuts = reinterpret_cast<Cut *>(take(p.ctas * sizeof(Cut)));
     *bytes = at;
     return p;
 }
@@ -823,7 +815,7 @@ cudaError_t launch(const CrossArgs &a, cudaStream_t stream)
     p.info = reinterpret_cast<float2 *>(ws + reinterpret_cast<size_t>(p.info));
     p.ranges = reinterpret_cast<int2 *>(ws + reinterpret_cast<size_t>(p.ranges));
     p.parts = reinterpret_cast<float *>(ws + reinterpret_cast<size_t>(p.parts));
-    p.items = reinterpret_cast<Item *>(ws + reinterpret_cast<size_t>(p.items));
+    p.cuts = reinterpret_cast<Cut *>(ws + reinterpret_cast<size_t>(p.cuts));
     p.negative = a.scale < 0.0f;
     CUtensorMap mq, md, mk, mv;
     cudaError_t e = row_map(&mq, a.q, a.T, a.Hq, a.dim, a.qs, a.Hq / a.heads, p.tokens_a_tile);
@@ -839,19 +831,19 @@ cudaError_t launch(const CrossArgs &a, cudaStream_t stream)
     if (e == cudaSuccess)
         e = tc::allow_smem(cross_dkv_kernel<DP>, L::BYTES, allowed_kv);
     if (e == cudaSuccess)
-        e = tc::launch_pdl(cross_ready_kernel, dim3(p.q_tiles, a.heads), dim3(256), 0, stream, a, p);
+        e = tc::launch_pdl(cross_ready_kernel, dim3(p.q_tiles, a.heads, kTile / kReadyRows), dim3(256), 0, stream, a, p);
     const int tiles = (a.S + kTile - 1) / kTile, most_q = most_tiles(a.heads, tiles, kMostTiles), most_kv = most_tiles(a.heads, p.q_tiles, kMostTiles);
     for (p.first = 0; e == cudaSuccess && p.first < p.q_tiles; p.first += most_q) {
         p.tiles = p.q_tiles - p.first < most_q ? p.q_tiles - p.first : most_q;
         e = tc::launch_pdl(cross_dq_kernel<DP>, dim3(p.ctas), dim3(kThreads), L::BYTES, stream, mq, md, mk, mv, a, p);
         if (e == cudaSuccess)
-            e = tc::launch_pdl(cross_add_kernel<DP, false>, dim3(p.tiles * a.heads, (p.rows + 31) / 32), dim3(kJoinWarps * 32), 0, stream, a, p);
+            e = tc::launch_pdl(cross_add_kernel<DP, false>, dim3(p.ctas, (p.rows + kJoinRows - 1) / kJoinRows), dim3(kJoinWarps * 32), 0, stream, a, p);
     }
     for (p.first = 0; e == cudaSuccess && p.first < tiles; p.first += most_kv) {
         p.tiles = tiles - p.first < most_kv ? tiles - p.first : most_kv;
         e = tc::launch_pdl(cross_dkv_kernel<DP>, dim3(p.ctas), dim3(kThreads), L::BYTES, stream, mq, md, mk, mv, a, p);
         if (e == cudaSuccess)
-            e = tc::launch_pdl(cross_add_kernel<DP, true>, dim3(p.tiles * a.heads, 2 * kTile / 32), dim3(kJoinWarps * 32), 0, stream, a, p);
+            e = tc::launch_pdl(cross_add_kernel<DP, true>, dim3(p.ctas, 2 * kTile / kJoinRows), dim3(kJoinWarps * 32), 0, stream, a, p);
     }
     return e;
 }

@@ -163,6 +163,8 @@ struct Item {
 
 struct Piece {
     int tile, head, j0, n, slot;        // slot: -1 for a whole item, else where its sums go: 0 or 1
+    int item_end;                       // tiles of all heads in front of the item's end
+    bool begins;                        // the item, and not only a piece of it
 };
 
 // How many CTAs have a share: none of them an empty one.
@@ -202,6 +204,8 @@ struct Share {
         u.j0 = uniform(items[lo].j0) + off;
         u.n = min(end - at, left);
         u.slot = off == 0 && u.n == left ? -1 : begun;
+        u.begins = off == 0;
+        u.item_end = at + left;
         at += u.n;
         begun = true;
         return true;
@@ -215,22 +219,22 @@ inline int most_tiles(int64_t heads, int64_t others, int most)
     return (int)(fit < most ? fit : most);
 }
 
-// The CTAs whose shares hold parts of item i of a head (c0 == c1: it is whole), and where
-// each has put its part.
+// What a CTA's share leaves to be joined: the item that begins in it and ends in a later one's.
+// Its parts are in slot `slot` of this CTA and the first slots of those behind it, up to c1.
 struct Cut {
-    int c0, c1, first_slot;
-
-    __device__ __forceinline__ Cut(const Item *items, int n, int i, int head, int heads, int ctas)
-    {
-        const int64_t per_head = items[n].begin, all = per_head * heads, some = busy(ctas, all);
-        const int64_t from = head * per_head + items[i].begin, to = head * per_head + items[i + 1].begin - 1;
-        c0 = (int)(((from + 1) * some - 1) / all);
-        c1 = (int)(((to + 1) * some - 1) / all);
-        first_slot = from != all * c0 / some;
-    }
-
-    __device__ __forceinline__ int64_t slot(int c) const { return (int64_t)c * 2 + (c == c0 ? first_slot : 0); }
+    int tile, head, slot, c1;           // c1 < 0: nothing
 };
+
+// From the last piece of a share (`some`: there was one).
+__device__ __forceinline__ Cut cut_of(const Share &share, const Piece &u, bool some, int heads, int ctas)
+{
+    Cut c = {0, 0, 0, -1};
+    if (some && u.slot >= 0 && u.begins) {
+        const int64_t all = (int64_t)heads * share.per_head;
+        c = {u.tile, u.head, u.slot, (int)((u.item_end * busy(ctas, all) - 1) / all)};
+    }
+    return c;
+}
 
 // Whether two packed maxima of |bf16| bits are of finite values.
 __device__ __forceinline__ bool finite2(uint32_t top) { return (top & 0xFFFFu) < 0x7F80u && (top >> 16) < 0x7F80u; }
