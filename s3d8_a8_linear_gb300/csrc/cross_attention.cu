@@ -8,8 +8,8 @@
 // rows.  The states pass in tiles of 128.  S = Q K^T and O += P V run on the tensor cores
 // (tcgen05, sums in tensor memory); the softmax's weights P go from registers into tensor
 // memory as the second product's A operand, over the scores they come from.  A CTA an SM:
-// one warp copies (bulk tensor copies into a ring), one issues the products, two groups of
-// four warps have a row a thread each, and two warps look the values over (below).
+// one warp copies (bulk tensor copies into a ring), two issue the products, two groups of
+// four warps have a row a thread each, and four warps look the values over (below).
 //
 // Two chains of score, softmax and product run in turn, so that the tensor cores work on
 // one while the other is in its softmax: two query tiles over the same states where their
@@ -24,7 +24,7 @@
 // rounding of the output; 16 more bits would double the product.
 //
 // A weight of zero does not silence an infinity or NaN among the values: 0 * inf is NaN.
-// Where some row of the query tiles does not see all of a state tile, the two other warps
+// Where some row of the query tiles does not see all of a state tile, the four other warps
 // look at its values, replace what is not finite by zeros, and note which rows do see it;
 // those rows get the infinity or NaN in that column at the end.
 #include "cross_tiles.cuh"
@@ -135,6 +135,14 @@ __device__ __forceinline__ void hide(float (&x)[64], unsigned from, unsigned n)
         x[c] = c - from < n ? x[c] : -INFINITY;
 }
 
+// A stage of the ring is free when both chains have used it, or the only one that does.
+__device__ __forceinline__ void release(uint32_t empty, bool pair)
+{
+    tc::mma_commit_elect(empty);
+    if (!pair)
+        tc::mma_commit_elect(empty);
+}
+
 // Looks over a state tile's values (in shared memory at v): a row a thread at a time.
 // What is not finite becomes zero, and is noted for the rows that see its state.
 template <int DP>
@@ -211,7 +219,7 @@ __global__ __launch_bounds__(kThreads, 1) void cross_forward_kernel(const __grid
 
     if (warp == 0 && lane == 0) {
         mbar_init(q_full, 1);
-        mbar_init(q_empty, 1);
+        mbar_init(q_empty, 2);
         mbar_init(o_free, 8);
         for (int s = 0; s < 2; ++s) {
             mbar_init(s_full + 8 * s, 1);
@@ -221,7 +229,7 @@ __global__ __launch_bounds__(kThreads, 1) void cross_forward_kernel(const __grid
         }
         for (int s = 0; s < L::STAGES; ++s) {
             mbar_init(kv_full + 8 * s, 1);
-            mbar_init(kv_empty + 8 * s, 1);
+            mbar_init(kv_empty + 8 * s, 2);
             mbar_init(v_ok + 8 * s, 4);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -292,61 +300,49 @@ __global__ __launch_bounds__(kThreads, 1) void cross_forward_kernel(const __grid
                 ok &= tc::warp_wait(kv_full + 8 * (i % L::STAGES), (i / L::STAGES) & 1);
             if (lane == 0)
                 p.cuts[blockIdx.x] = cut_of(share, u, at > 0, a.heads, p.ctas);
-        } else if (warp == 1) {         // scores, a chain after the other
-            const int ksteps = (a.dim + 15) / 16;
-            const uint32_t id_s = idesc_cols(kTile) | (p.negative ? kNegateA : 0u);
-            int at = 0, jobs[2] = {0, 0};       // tiles of K and V, and products with V of each chain, so far
+        } else if (warp < 3) {          // products of a chain
+            const int s = warp - 1, ksteps = (a.dim + 15) / 16;
+            const uint32_t id_s = idesc_cols(kTile) | (p.negative ? kNegateA : 0u), id_o = idesc_rows(ksteps * 16);
+            int at = 0, jobs = 0;       // tiles of K and V, and this chain's products, so far
             for (int units = 0; ok && next_unit(share, u); ++units) {
-                const int n = u.pair ? 2 * u.n : u.n;
+                const int mine = u.pair ? u.n : (u.n + 1 - s) / 2;
+                const uint32_t q = base + L::Q + (u.pair ? s * L::TILE : 0);
                 if (!(ok = tc::warp_wait(q_full, units & 1)))
                     break;
-                for (int job = 0; job < n; ++job) {
-                    const int s = job & 1, k = at + 2 * (u.pair ? job >> 1 : job), st = k % L::STAGES;
-                    if (!u.pair || !s)
-                        if (!(ok = tc::warp_wait(kv_full + 8 * st, (k / L::STAGES) & 1)))
-                            break;
-                    // over the weights of this chain's product before
-                    if (jobs[s] > 0 && !(ok = tc::warp_wait(pv_done + 8 * s, (jobs[s] - 1) & 1)))
+                for (int i = 0; ok && i < mine; ++i, ++jobs) {
+                    const int k = at + 2 * (u.pair ? i : 2 * i + s), ks = k % L::STAGES, v = k + 1, vs = v % L::STAGES;
+                    if (!(ok = tc::warp_wait(kv_full + 8 * ks, (k / L::STAGES) & 1)))
                         break;
-                    ++jobs[s];
                     tc::tc_fence_after();
-                    const uint32_t q = base + L::Q + (u.pair ? s * L::TILE : 0), kt = base + L::KV + st * L::TILE;
+                    const uint32_t kt = base + L::KV + ks * L::TILE, vt = base + L::KV + vs * L::TILE;
                     for (int kk = 0; kk < ksteps; ++kk) {
                         const uint32_t off = (kk >> 2) * (kTile * 128) + (kk & 3) * 32;
                         tc::mma_bf16_elect(tmem + s * 128, tc::sw128_desc(q + off), tc::sw128_desc(kt + off), id_s, kk > 0);
                     }
                     tc::mma_commit_elect(s_full + 8 * s);
-                    if (!u.pair || s)
-                        tc::mma_commit_elect(kv_empty + 8 * st);
-                }
-                tc::mma_commit_elect(q_empty);
-                at += 2 * u.n;
-            }
-        } else if (warp == 2) {         // products with the values, likewise
-            const uint32_t id_o = idesc_rows((a.dim + 15) / 16 * 16);
-            int at = 0, jobs[2] = {0, 0};
-            while (ok && next_unit(share, u)) {
-                const int n = u.pair ? 2 * u.n : u.n;
-                for (int job = 0; ok && job < n; ++job) {
-                    const int s = job & 1, v = at + 2 * (u.pair ? job >> 1 : job) + 1, st = v % L::STAGES;
-                    if (!u.pair || !s)
-                        if (!(ok = tc::warp_wait(v_ok + 8 * st, (v / L::STAGES) & 1)))
-                            break;
-                    const uint32_t vt = base + L::KV + st * L::TILE;
+                    release(kv_empty + 8 * ks, u.pair);
+                    if (i == mine - 1)
+                        tc::mma_commit_elect(q_empty);
+                    if (!(ok = tc::warp_wait(v_ok + 8 * vs, (v / L::STAGES) & 1)))
+                        break;
                     for (int half = 1; ok && half >= 0; --half) {     // the second half of the states is ready first
-                        if (!(ok = tc::warp_wait((half ? p_half : p_ready) + 8 * s, jobs[s] & 1)))
+                        if (!(ok = tc::warp_wait((half ? p_half : p_ready) + 8 * s, jobs & 1)))
                             break;
                         tc::tc_fence_after();
                         for (int kk = 4 * half; kk < 4 * half + 4; ++kk)
                             mma_tmem_a_elect(tmem + 256 + s * 128, tmem + s * 128 + half * 64 + (kk & 3) * 8, rows_desc(vt + kk * 2048, kTile * 128), id_o,
-                                             job >= 2 || kk != 4);
+                                             i > 0 || kk != 4);
                     }
-                    ++jobs[s];
                     tc::mma_commit_elect(pv_done + 8 * s);
-                    if (!u.pair || s)
-                        tc::mma_commit_elect(kv_empty + 8 * st);
+                    release(kv_empty + 8 * vs, u.pair);
                 }
+                if (mine == 0 && lane == 0)     // (one state tile: the second chain has none)
+                    tc::mbar_arrive(q_empty);
                 at += 2 * u.n;
+                // The last values, where they were the first chain's: a wait for a stage's next
+                // phase means that one only once the phase before is known to be over.
+                if (ok && s == 1 && !u.pair && u.n % 2 == 1)
+                    ok = tc::warp_wait(v_ok + 8 * ((at - 1) % L::STAGES), ((at - 1) / L::STAGES) & 1);
             }
         }
     } else if (warp >= 12) {
