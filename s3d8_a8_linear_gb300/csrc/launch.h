@@ -207,7 +207,7 @@ struct NormRopeArgs {
     __nv_bfloat16 *out[2];              // z, or dx
     const __nv_bfloat16 *dz[2];         // backward only
     int64_t dzs[2][2];
-    float *dw[2], *part;                // part: [CTAs][2 dim]
+    float *dw[2], *part;                // part: [CTAs][dim]
     int *status;
 };
 cudaError_t launch_norm_rope(const NormRopeArgs &a, cudaStream_t stream);

@@ -6,11 +6,17 @@
 //
 // HBM-bound: 4 bytes an element forward, 6 backward.  A row of D columns belongs to
 // D/16 neighbouring lanes, as in the append (rope_lane.cuh), so that the two sums of a
-// row are a few shuffles and nothing else waits.  A warp takes a part of a token's rows
-// and reads the token's cosines once; few tokens are cut into more parts.  The weights'
-// gradients: a lane keeps its columns' sums in registers over all its rows, a CTA adds
-// its lanes' in shared memory, a second kernel adds the CTAs' rows; every order is fixed,
-// so equal inputs give equal bits.
+// row are a few shuffles and nothing else waits; a warp has 32 lanes' worth of one token's
+// rows at a time, a group.  Queries and keys are CTAs of their own, by their share of the
+// rows (a warp keeps one weight's columns in registers, and one weight's sums), and each
+// warp an equal run of its kind's groups.  It copies them through a ring of its own in
+// shared memory, the token's angles with the first group of a token: MEASURED
+//
+// The weights' gradients: a lane keeps its columns' sums in registers over all its rows,
+// a CTA adds its lanes' in shared memory, a second kernel adds the CTAs' rows; every order
+// is fixed, so equal inputs give equal bits.  All arithmetic is fp32, rounded once.
+#include "async_copy.cuh"
+#include "cross_tiles.cuh"
 #include "launch.h"
 #include "rope_lane.cuh"
 #include "tcgen05.cuh"
@@ -19,315 +25,385 @@ namespace s3d8 {
 
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+using cross::add2;
+using cross::fma2;
+using cross::mul2;
+using cross::pack2;
+
+constexpr int kThreads = 512, kWarps = kThreads / 32;
 
 struct Work {
-    int parts;      // warps that share a token's rows
     int log_lanes, vec;
-    int64_t items;  // tokens times parts
+    int ctas[2];    // of the queries, of the keys
 };
 
-__device__ __forceinline__ const __nv_bfloat16 *row_of(const __nv_bfloat16 *const (&x)[2], const int64_t (&st)[2][2], int64_t t, int kind, int h)
+template <bool BACK>
+struct Ring {
+    static constexpr int STAGES = BACK ? 4 : 6;
+    static constexpr int DZ = 1024, ANGLES = BACK ? 2048 : 1024, STAGE = ANGLES + 1024;     // x first; cosines, sines
+    static constexpr int BYTES = kWarps * STAGES * STAGE;
+};
+
+__device__ __forceinline__ float2 twice(float x) { return make_float2(x, x); }
+
+// Sixteen values: two chunks of four pairs.
+__device__ __forceinline__ void unpack(uint4 v, float2 (&f)[4])
 {
-    return x[kind] + t * st[kind][0] + h * st[kind][1];
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        f[j] = make_float2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xFFFF0000u));
 }
 
-// The position of token t; false for a padding token, or one without angles (recorded once).
-__device__ __forceinline__ bool position(const NormRopeArgs &a, int64_t t, bool one, int64_t &pos)
+__device__ __forceinline__ uint4 pack(const float2 (&f)[4])
 {
-    pos = a.positions ? a.positions[t] : t;
-    if (pos < 0)
-        return false;
-    if (a.rotary && pos >= a.max_pos) {
-        if (one)
-            atomicExch(a.status, kStatusBounds);
-        return false;
+    return make_uint4(pack2(f[0].x, f[0].y), pack2(f[1].x, f[1].y), pack2(f[2].x, f[2].y), pack2(f[3].x, f[3].y));
+}
+
+__device__ __forceinline__ float lds_f32(uint32_t at)
+{
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at));
+    return v;
+}
+
+// What a warp has to copy: a run of its kind's groups, in order of token and head.
+template <int MODE, bool BACK>
+struct Feed {
+    using R = Ring<BACK>;
+    const NormRopeArgs &a;
+    const RopeLane &l;
+    const int kind, slots, groups, vec;
+    const uint32_t ring, angles;    // this lane's place in it, and the angles'
+    int64_t left, t;
+    int group, stage, next;
+    bool fresh, ok;
+
+    __device__ __forceinline__ Feed(const NormRopeArgs &a, const RopeLane &l, int kind, int slots, int slot, int vec, uint32_t ring, uint32_t angles, int64_t begin, int64_t n)
+        : a(a), l(l), kind(kind), slots(slots), groups((a.heads[kind] + slots - 1) / slots), vec(vec), ring(ring), angles(angles), left(n), t(begin / groups),
+          group((int)(begin - t * groups)), stage(0), next(0), fresh(true), ok(false)
+    {
+        if (a.positions && n > 0)
+            next = __ldg(a.positions + t);
+        head = group * slots + slot;
     }
-    return true;
-}
 
-// ROWS: rows of a lane whose loads leave together.
-template <int MODE, int ROWS>
-__global__ __launch_bounds__(kThreads) void norm_rope_kernel(const __grid_constant__ NormRopeArgs a, const __grid_constant__ Work p)
-{
-    tc::pdl_launch_dependents();
-    tc::pdl_wait();
-    const RopeLane l(a.rotary, a.dim, MODE, p.log_lanes);
-    const int slots = 32 >> p.log_lanes, slot = (threadIdx.x & 31) >> p.log_lanes, heads = a.heads[0] + a.heads[1];
-    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-    for (int64_t item = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); item < p.items; item += (int64_t)gridDim.x * kWarps) {
-        const int64_t t = item / p.parts;
-        const int part = (int)(item - t * p.parts);
-        float cs[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f}, sn[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-        int64_t pos = 0;
-        bool ok = false;
-        for (int base = part * slots * ROWS; base < heads; base += p.parts * slots * ROWS) {
-            uint4 raw[ROWS][2];
-#pragma unroll
-            for (int i = 0; i < ROWS; ++i) {
-                const int head = base + slot + i * slots, kind = head >= a.heads[0];
-                raw[i][0] = raw[i][1] = zero;
-                if (head < heads && l.in_row) {
-                    const __nv_bfloat16 *x = row_of(a.x, a.xs, t, kind, kind ? head - a.heads[0] : head);
-                    raw[i][0] = ldg_stream_v4(x + 8 * l.chunk[0]);
-                    raw[i][1] = ldg_stream_v4(x + 8 * l.chunk[1]);
-                }
+    // Copies a group, if one is left; whether its token has a place.
+    __device__ __forceinline__ bool operator()()
+    {
+        if (left > 0) {
+            const uint32_t to = ring + stage * R::STAGE;
+            const bool live = head < a.heads[kind] && l.in_row;
+            const __nv_bfloat16 *x = a.x[kind] + t * a.xs[kind][0] + (live ? head * a.xs[kind][1] : 0);
+            if (!BACK || a.w[kind]) {
+                cp_async16(to, x + (live ? 8 * l.chunk[0] : 0), live ? 16 : 0);
+                cp_async16(to + 512, x + (live ? 8 * l.chunk[1] : 0), live ? 16 : 0);
             }
-            if (base == part * slots * ROWS) {
-                ok = position(a, t, part == 0 && (threadIdx.x & 31) == 0, pos);
-                if (ok && l.turns && MODE != kHalvesOdd)
-                    load_angles(l, a.cos + pos * l.half + 8 * l.lane, a.sin + pos * l.half + 8 * l.lane, p.vec, cs, sn);
+            if (BACK) {
+                const __nv_bfloat16 *z = a.dz[kind] + t * a.dzs[kind][0] + (live ? head * a.dzs[kind][1] : 0);
+                cp_async16(to + R::DZ, z + (live ? 8 * l.chunk[0] : 0), live ? 16 : 0);
+                cp_async16(to + R::DZ + 512, z + (live ? 8 * l.chunk[1] : 0), live ? 16 : 0);
             }
-#pragma unroll
-            for (int i = 0; i < ROWS; ++i) {
-                const int head = base + slot + i * slots, kind = head >= a.heads[0], h = kind ? head - a.heads[0] : head;
-                const bool live = head < heads && l.in_row;
-                float f[2][8];
-                unpack8(ok ? raw[i][0] : zero, f[0]);
-                unpack8(ok ? raw[i][1] : zero, f[1]);
-                float sum = 0.0f;
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    sum = fmaf(f[0][e], f[0][e], fmaf(f[1][e], f[1][e], sum));
-                const float r = rsqrtf(row_sum(sum, l.lanes) / (float)a.dim + a.eps);
-                const __nv_bfloat16 *w = live && ok ? a.w[kind] : nullptr;
-                if (w) {
-#pragma unroll
-                    for (int y = 0; y < 2; ++y) {
-                        float g[8];
-                        unpack8(__ldg(reinterpret_cast<const uint4 *>(w) + l.chunk[y]), g);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            f[y][e] = f[y][e] * r * g[e];
-                    }
+            if (fresh) {
+                const int64_t pos = a.positions ? uniform(next) : t;
+                if (a.positions && t + 1 < a.T)
+                    next = __ldg(a.positions + t + 1);
+                ok = pos >= 0;
+                if (ok && a.rotary && pos >= a.max_pos) {
+                    ok = false;
+                    atomicExch(a.status, kStatusBounds);
                 }
-                if (l.turns)
-                    turn<MODE>(l, f, cs, sn);
-                if (MODE == kHalvesOdd && live && ok) {
-                    const __nv_bfloat16 *x = row_of(a.x, a.xs, t, kind, h);
-                    for (int e = 0; e < 16; ++e)
-                        f[e / 8][e % 8] = turn_odd(16 * l.lane + e, l.half, f[e / 8][e % 8], a.cos + pos * l.half, a.sin + pos * l.half,
-                                                   [&](int d) { return __bfloat162float(x[d]) * (w ? r * __bfloat162float(w[d]) : 1.0f); });
-                }
-                if (live) {
-                    __nv_bfloat16 *o = a.out[kind] + (t * a.heads[kind] + h) * a.dim;
-                    *reinterpret_cast<uint4 *>(o + 8 * l.chunk[0]) = pack8(f[0]);
-                    *reinterpret_cast<uint4 *>(o + 8 * l.chunk[1]) = pack8(f[1]);
-                }
-            }
-        }
-    }
-}
-
-// A lane's share of one kind's rows (queries or keys) of a token.
-template <int MODE, int ROWS>
-__device__ __forceinline__ void back_rows(const NormRopeArgs &a, const Work &p, const RopeLane &l, int kind, int64_t t, int first, int step, bool ok,
-                                          int64_t pos, const float (&cs)[8], const float (&sn)[8], const float (&w)[2][8], float (&dw)[2][8])
-{
-    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-    const int slots = 32 >> p.log_lanes, slot = (threadIdx.x & 31) >> p.log_lanes;
-    for (int base = first; base < a.heads[kind]; base += step) {
-        uint4 rx[ROWS][2], rz[ROWS][2];
-#pragma unroll
-        for (int i = 0; i < ROWS; ++i) {
-            const int h = base + slot + i * slots;
-            rx[i][0] = rx[i][1] = rz[i][0] = rz[i][1] = zero;
-            if (ok && h < a.heads[kind] && l.in_row) {
-                const __nv_bfloat16 *z = row_of(a.dz, a.dzs, t, kind, h), *x = row_of(a.x, a.xs, t, kind, h);
-                rz[i][0] = ldg_stream_v4(z + 8 * l.chunk[0]);
-                rz[i][1] = ldg_stream_v4(z + 8 * l.chunk[1]);
-                if (a.w[kind]) {
-                    rx[i][0] = ldg_stream_v4(x + 8 * l.chunk[0]);
-                    rx[i][1] = ldg_stream_v4(x + 8 * l.chunk[1]);
-                }
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < ROWS; ++i) {
-            const int h = base + slot + i * slots;
-            const bool live = h < a.heads[kind] && l.in_row;
-            float f[2][8], x[2][8];
-            unpack8(rz[i][0], f[0]);
-            unpack8(rz[i][1], f[1]);
-            unpack8(rx[i][0], x[0]);
-            unpack8(rx[i][1], x[1]);
-            if (l.turns)
-                turn<MODE>(l, f, cs, sn);       // sn holds the sines with their signs turned
-            if (MODE == kHalvesOdd && live && ok) {
-                const __nv_bfloat16 *z = row_of(a.dz, a.dzs, t, kind, h);
-                for (int e = 0; e < 16; ++e) {
-                    const int d = 16 * l.lane + e;
+                if (ok && MODE != kHalvesOdd) {
                     const float *c = a.cos + pos * l.half, *s = a.sin + pos * l.half;
-                    float &v = f[e / 8][e % 8];
-                    if (d < l.half)
-                        v = v * c[d] + __bfloat162float(z[d + l.half]) * s[d];
-                    else if (d < a.rotary)
-                        v = v * c[d - l.half] - __bfloat162float(z[d - l.half]) * s[d - l.half];
+                    const int lane = threadIdx.x & 31, n = l.half;
+                    if (vec) {
+                        for (int i = lane; i < n / 2; i += 32)
+                            cp_async16(angles + stage * R::STAGE + 16 * i, 4 * i < n ? c + 4 * i : s + 4 * i - n);
+                    } else {
+                        for (int i = lane; i < 2 * n; i += 32)
+                            cp_async4(angles + stage * R::STAGE + 4 * i, i < n ? c + i : s + i - n, 4);
+                    }
                 }
+                fresh = false;
             }
-            if (a.w[kind]) {
-                float sum = 0.0f, dot = 0.0f;
-#pragma unroll
-                for (int y = 0; y < 2; ++y)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        sum = fmaf(x[y][e], x[y][e], sum);
-                        dot = fmaf(f[y][e] * w[y][e], x[y][e], dot);
-                    }
-                sum = row_sum(sum, l.lanes);
-                dot = row_sum(dot, l.lanes);
-                const float r = ok && h < a.heads[kind] ? rsqrtf(sum / (float)a.dim + a.eps) : 0.0f;   // no row: not 0 times infinity
-                const float back = r * r * (dot / (float)a.dim);      // times r x: r^3 mean(a x) x
-#pragma unroll
-                for (int y = 0; y < 2; ++y)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        dw[y][e] = fmaf(f[y][e], x[y][e] * r, dw[y][e]);
-                        f[y][e] = r * fmaf(-x[y][e], back, f[y][e] * w[y][e]);
-                    }
+            head += slots;
+            if (++group == groups) {
+                head -= groups * slots;
+                group = 0;
+                ++t;
+                fresh = true;
             }
-            if (live) {
-                __nv_bfloat16 *o = a.out[kind] + (t * a.heads[kind] + h) * a.dim;
-                *reinterpret_cast<uint4 *>(o + 8 * l.chunk[0]) = pack8(f[0]);
-                *reinterpret_cast<uint4 *>(o + 8 * l.chunk[1]) = pack8(f[1]);
-            }
+            --left;
+            stage = stage + 1 == R::STAGES ? 0 : stage + 1;
         }
+        cp_commit();
+        return ok;
     }
-}
 
-// gridDim.x partial rows [2][dim] of the weights' gradients into a.part.
-template <int MODE, int ROWS>
-__global__ __launch_bounds__(kThreads) void norm_rope_backward_kernel(const __grid_constant__ NormRopeArgs a, const __grid_constant__ Work p)
+private:
+    int head;
+};
+
+// BACK: gridDim.x partial rows [dim] of the weights' gradients into a.part, those of the queries' CTAs first.
+template <int MODE, bool BACK>
+__global__ __launch_bounds__(kThreads, 1) void norm_rope_kernel(const __grid_constant__ NormRopeArgs a, const __grid_constant__ Work p)
 {
-    __shared__ float sums[2][kWarps][512];      // of a warp: its slots' columns side by side
+    using R = Ring<BACK>;
+    extern __shared__ __align__(16) unsigned char norm_rope_mem[];
+    const int warp = warp_index(), kind = (int)blockIdx.x >= p.ctas[0];
+    const RopeLane l(a.rotary, a.dim, MODE, p.log_lanes);
+    const int slots = 32 >> p.log_lanes, slot = (threadIdx.x & 31) >> p.log_lanes, heads = a.heads[kind], groups = (heads + slots - 1) / slots;
+    const int64_t total = a.T * groups, part = (int64_t)(blockIdx.x - (kind ? p.ctas[0] : 0)) * kWarps + warp, parts = (int64_t)p.ctas[kind] * kWarps;
+    const int64_t begin = total * part / parts, end = total * (part + 1) / parts;
+    const uint32_t warps = smem_addr(norm_rope_mem) + warp * (R::STAGES * R::STAGE), ring = warps + (threadIdx.x & 31) * 16, angles = warps + R::ANGLES;
+    const float inv = 1.0f / (float)a.dim;
+    const bool normed = a.w[kind] != nullptr;
     tc::pdl_launch_dependents();
     tc::pdl_wait();
-    const RopeLane l(a.rotary, a.dim, MODE, p.log_lanes);
-    const int slots = 32 >> p.log_lanes, slot = (threadIdx.x & 31) >> p.log_lanes, warp = threadIdx.x >> 5;
-    float w[2][2][8], dw[2][2][8];
+    float2 w[2][4], dw[2][4], cs[4], sn[4];
 #pragma unroll
-    for (int kind = 0; kind < 2; ++kind)
+    for (int y = 0; y < 2; ++y) {
+        unpack(normed && l.in_row ? __ldg(reinterpret_cast<const uint4 *>(a.w[kind]) + l.chunk[y]) : make_uint4(0u, 0u, 0u, 0u), w[y]);
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-            unpack8(a.w[kind] && l.in_row ? __ldg(reinterpret_cast<const uint4 *>(a.w[kind]) + l.chunk[y]) : make_uint4(0u, 0u, 0u, 0u), w[kind][y]);
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                dw[kind][y][e] = 0.0f;
-        }
-    for (int64_t item = (int64_t)blockIdx.x * kWarps + warp; item < p.items; item += (int64_t)gridDim.x * kWarps) {
-        const int64_t t = item / p.parts;
-        const int part = (int)(item - t * p.parts);
-        float cs[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f}, sn[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-        int64_t pos;
-        const bool ok = position(a, t, part == 0 && (threadIdx.x & 31) == 0, pos);
-        if (ok && l.turns && MODE != kHalvesOdd) {
-            load_angles(l, a.cos + pos * l.half + 8 * l.lane, a.sin + pos * l.half + 8 * l.lane, p.vec, cs, sn);
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                sn[e] = -sn[e];
-        }
-        back_rows<MODE, ROWS>(a, p, l, 0, t, part * slots * ROWS, p.parts * slots * ROWS, ok, pos, cs, sn, w[0], dw[0]);
-        back_rows<MODE, ROWS>(a, p, l, 1, t, part * slots * ROWS, p.parts * slots * ROWS, ok, pos, cs, sn, w[1], dw[1]);
+        for (int e = 0; e < 4; ++e)
+            dw[y][e] = make_float2(0.0f, 0.0f);
     }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        cs[e] = sn[e] = make_float2(0.0f, 0.0f);
+
+    Feed<MODE, BACK> feed(a, l, kind, slots, slot, p.vec, ring, angles, begin, end - begin);
+    int64_t t = begin / groups;
+    int group = (int)(begin - t * groups), stage = 0;
+    unsigned places = 0;        // of the groups in the ring: whether their token has one, the newest lowest
+#pragma unroll
+    for (int i = 0; i < R::STAGES - 1; ++i)
+        places = places << 1 | feed();
+    bool fresh = true;
+    for (int64_t i = begin; i < end; ++i) {
+        cp_wait<R::STAGES - 2>();
+        __syncwarp();               // the angles are other lanes' copies, and the stage filled next is read
+        places = places << 1 | feed();
+        const bool ok = places >> (R::STAGES - 1) & 1;
+        const int h = group * slots + slot;
+        const bool live = h < heads && l.in_row;
+        const uint32_t from = ring + stage * R::STAGE;
+        float2 f[2][4], x[2][4];
+        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+        if (!BACK || normed) {
+            unpack(ok ? lds_v4(from) : zero, x[0]);
+            unpack(ok ? lds_v4(from + 512) : zero, x[1]);
+        }
+        if (BACK) {
+            unpack(ok ? lds_v4(from + R::DZ) : zero, f[0]);
+            unpack(ok ? lds_v4(from + R::DZ + 512) : zero, f[1]);
+        }
+        if (fresh && ok && l.turns && MODE != kHalvesOdd) {
+            // (beyond half, where it is no multiple of 8: not used)
+            const uint32_t at = angles + stage * R::STAGE + 32 * l.lane;
+            float c[8], sine[8];
+            if (p.vec) {
+#pragma unroll
+                for (int e = 0; e < 8; e += 4) {
+                    const uint4 u = lds_v4(at + 4 * e), v = lds_v4(at + 4 * (l.half + e));
+                    c[e] = __uint_as_float(u.x), c[e + 1] = __uint_as_float(u.y), c[e + 2] = __uint_as_float(u.z), c[e + 3] = __uint_as_float(u.w);
+                    sine[e] = __uint_as_float(v.x), sine[e + 1] = __uint_as_float(v.y), sine[e + 2] = __uint_as_float(v.z), sine[e + 3] = __uint_as_float(v.w);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    c[e] = lds_f32(at + 4 * e);
+                    sine[e] = lds_f32(at + 4 * (l.half + e));
+                }
+            }
+            const float by = BACK ? -1.0f : 1.0f;       // the gradient turns back
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                cs[e] = make_float2(c[2 * e], c[2 * e + 1]);
+                sn[e] = make_float2(sine[2 * e] * by, sine[2 * e + 1] * by);
+            }
+        }
+        float r = 0.0f;
+        if (!BACK) {
+            float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    sum = fma2(x[y][e], x[y][e], sum);
+                    f[y][e] = x[y][e];
+                }
+            r = rsqrtf(fmaf(row_sum(sum.x + sum.y, l.lanes), inv, a.eps));
+            if (normed && ok && live) {
+#pragma unroll
+                for (int y = 0; y < 2; ++y)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        f[y][e] = mul2(mul2(f[y][e], twice(r)), w[y][e]);
+            }
+        }
+        if (l.turns && MODE == kHalves) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 u = f[0][e], v = f[1][e];
+                f[0][e] = fma2(u, cs[e], mul2(v, make_float2(-sn[e].x, -sn[e].y)));
+                f[1][e] = fma2(v, cs[e], mul2(u, sn[e]));
+            }
+        }
+        if (l.turns && MODE == kNeighbours) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {     // pair 8 lane + e
+                if (8 * l.lane + e >= l.half)
+                    continue;
+                const float2 u = f[e / 4][e % 4];
+                const float c = e & 1 ? cs[e / 2].y : cs[e / 2].x, s = e & 1 ? sn[e / 2].y : sn[e / 2].x;
+                f[e / 4][e % 4] = make_float2(fmaf(u.x, c, -(u.y * s)), fmaf(u.y, c, u.x * s));
+            }
+        }
+        if (MODE == kHalvesOdd && live && ok && a.rotary) {
+            const int64_t pos = a.positions ? __ldg(a.positions + t) : t;
+            const float *c = a.cos + pos * l.half, *s = a.sin + pos * l.half;
+            const __nv_bfloat16 *row = BACK ? a.dz[kind] + t * a.dzs[kind][0] + h * a.dzs[kind][1] : a.x[kind] + t * a.xs[kind][0] + h * a.xs[kind][1];
+            auto partner = [&](int d) { return __bfloat162float(row[d]) * (BACK || !normed ? 1.0f : r * __bfloat162float(a.w[kind][d])); };
+            auto turned = [&](int d, float v) {
+                if (d < l.half)
+                    return v * c[d] + partner(d + l.half) * (BACK ? s[d] : -s[d]);
+                return d < a.rotary ? v * c[d - l.half] + partner(d - l.half) * (BACK ? -s[d - l.half] : s[d - l.half]) : v;
+            };
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int d = 16 * l.lane + 2 * e;
+                f[e / 4][e % 4] = make_float2(turned(d, f[e / 4][e % 4].x), turned(d + 1, f[e / 4][e % 4].y));
+            }
+        }
+        if (BACK && normed) {
+            float2 sum = make_float2(0.0f, 0.0f), dot = make_float2(0.0f, 0.0f), g[2][4];
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    g[y][e] = mul2(f[y][e], w[y][e]);
+                    sum = fma2(x[y][e], x[y][e], sum);
+                    dot = fma2(g[y][e], x[y][e], dot);
+                }
+            const float squares = row_sum(sum.x + sum.y, l.lanes), back = row_sum(dot.x + dot.y, l.lanes);
+            r = ok && h < heads ? rsqrtf(fmaf(squares, inv, a.eps)) : 0.0f;   // no row: not 0 times infinity
+            const float2 r2 = twice(r), by = twice(-(r * r * (back * inv)));
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    dw[y][e] = fma2(f[y][e], mul2(x[y][e], r2), dw[y][e]);
+                    f[y][e] = mul2(r2, fma2(x[y][e], by, g[y][e]));
+                }
+        }
+        if (live) {
+            uint4 *o = reinterpret_cast<uint4 *>(a.out[kind] + (t * heads + h) * a.dim);
+            o[l.chunk[0]] = pack(f[0]);
+            o[l.chunk[1]] = pack(f[1]);
+        }
+        fresh = false;
+        if (++group == groups) {
+            group = 0;
+            ++t;
+            fresh = true;
+        }
+        stage = stage + 1 == R::STAGES ? 0 : stage + 1;
+    }
+    cp_wait<0>();
+    if (!BACK)
+        return;
     // columns of a warp's slots, then of the warps, each in order
-#pragma unroll
-    for (int kind = 0; kind < 2; ++kind)
-#pragma unroll
-        for (int y = 0; y < 2; ++y)
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (l.in_row)
-                    sums[kind][warp][slot * (16 << p.log_lanes) + 8 * l.chunk[y] + e] = dw[kind][y][e];
+    float *sums = reinterpret_cast<float *>(norm_rope_mem);     // [kWarps][512]: a warp's slots side by side
     __syncthreads();
-    for (int i = threadIdx.x; i < 2 * a.dim; i += kThreads) {
-        const int kind = i >= a.dim, d = kind ? i - a.dim : i;
+#pragma unroll
+    for (int y = 0; y < 2; ++y)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (l.in_row)
+                *reinterpret_cast<float2 *>(sums + warp * 512 + slot * (16 << p.log_lanes) + 8 * l.chunk[y] + 2 * e) = dw[y][e];
+    __syncthreads();
+    for (int d = threadIdx.x; d < a.dim; d += kThreads) {
         float s = 0.0f;
         for (int x = 0; x < kWarps; ++x)
             for (int y = 0; y < slots; ++y)
-                s += sums[kind][x][y * (16 << p.log_lanes) + d];
-        a.part[(int64_t)blockIdx.x * 2 * a.dim + i] = s;
+                s += sums[x * 512 + y * (16 << p.log_lanes) + d];
+        a.part[(int64_t)blockIdx.x * a.dim + d] = s;
     }
 }
 
-// Adds the CTAs' partial rows: a block 32 columns, its eight warps a share of the rows each.
-__global__ __launch_bounds__(kThreads) void norm_rope_weights_kernel(const __grid_constant__ NormRopeArgs a, int rows)
+constexpr int kSumWarps = 8;
+
+// Adds the CTAs' partial rows: a block 32 columns of a kind, its eight warps a share of the rows each.
+__global__ __launch_bounds__(kSumWarps * 32) void norm_rope_weights_kernel(const __grid_constant__ NormRopeArgs a, const __grid_constant__ Work p)
 {
-    __shared__ float sums[kWarps][32];
+    __shared__ float sums[kSumWarps][32];
     tc::pdl_launch_dependents();
     tc::pdl_wait();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, i = blockIdx.x * 32 + lane;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, i = blockIdx.x * 32 + lane, kind = blockIdx.y;
+    const int first = kind ? p.ctas[0] : 0;
     float s = 0.0f;
-    if (i < 2 * a.dim)
-        for (int r = warp; r < rows; r += kWarps)
-            s += a.part[(int64_t)r * 2 * a.dim + i];
+    if (i < a.dim)
+        for (int r = warp; r < p.ctas[kind]; r += kSumWarps)
+            s += a.part[(int64_t)(first + r) * a.dim + i];
     sums[warp][lane] = s;
     __syncthreads();
-    if (warp == 0 && i < 2 * a.dim) {
-        for (int x = 1; x < kWarps; ++x)
+    if (warp == 0 && i < a.dim) {
+        for (int x = 1; x < kSumWarps; ++x)
             s += sums[x][lane];
-        const int kind = i >= a.dim;
         if (a.dw[kind])
-            a.dw[kind][kind ? i - a.dim : i] = s;
+            a.dw[kind][i] = s;
     }
 }
 
-Work plan(const NormRopeArgs &a, int rows)
+Work plan(const NormRopeArgs &a)
 {
     Work p;
     p.log_lanes = 0;
     while (16 << p.log_lanes < a.dim)
         ++p.log_lanes;
     p.vec = a.rotary % 16 == 0 && ((uintptr_t)a.cos & 15) == 0 && ((uintptr_t)a.sin & 15) == 0;
-    // as many warps a token as its rows have loads for, as long as the GPU has room for them
-    const int heads = a.heads[0] > a.heads[1] ? a.heads[0] : a.heads[1], each = (32 >> p.log_lanes) * rows;
-    const int64_t most = (heads + each - 1) / each, room = (int64_t)device_sm_count() * 32 / (a.T > 0 ? a.T : 1);
-    p.parts = (int)(room < 1 ? 1 : room < most ? room : most);
-    p.items = a.T * p.parts;
+    const int slots = 32 >> p.log_lanes;
+    int64_t groups[2];
+    for (int kind = 0; kind < 2; ++kind)
+        groups[kind] = a.T * ((a.heads[kind] + slots - 1) / slots);
+    const int64_t all = groups[0] + groups[1], need = (all + kWarps - 1) / kWarps, most = device_sm_count();
+    const int ctas = (int)(need < most ? need : most);
+    p.ctas[1] = groups[1] == 0 ? 0 : (int)((groups[1] * ctas + all / 2) / all);
+    if (groups[1] > 0 && p.ctas[1] == 0)
+        p.ctas[1] = 1;
+    p.ctas[0] = ctas > p.ctas[1] ? ctas - p.ctas[1] : 1;        // (together at most one more than the SMs)
     return p;
 }
 
-int grid_of(const Work &p, int ctas)
+template <int MODE, bool BACK>
+cudaError_t run(const NormRopeArgs &a, cudaStream_t stream)
 {
-    const int64_t need = (p.items + kWarps - 1) / kWarps, most = (int64_t)device_sm_count() * ctas;
-    return (int)(need < most ? need : most);
-}
-
-constexpr int kBackCtas = 2;     // an SM
-
-template <int MODE>
-cudaError_t forward(const NormRopeArgs &a, cudaStream_t stream)
-{
-    const Work p = plan(a, 4);
-    return tc::launch_pdl(norm_rope_kernel<MODE, 4>, dim3(grid_of(p, 8)), dim3(kThreads), 0, stream, a, p);
-}
-
-template <int MODE>
-cudaError_t backward(const NormRopeArgs &a, cudaStream_t stream)
-{
-    const Work p = plan(a, 2);
-    const int grid = grid_of(p, kBackCtas);
-    cudaError_t e = tc::launch_pdl(norm_rope_backward_kernel<MODE, 2>, dim3(grid), dim3(kThreads), 0, stream, a, p);
-    if (e == cudaSuccess && (a.dw[0] || a.dw[1]))
-        e = tc::launch_pdl(norm_rope_weights_kernel, dim3((2 * a.dim + 31) / 32), dim3(kThreads), 0, stream, a, grid);
+    using R = Ring<BACK>;
+    const Work p = plan(a);
+    static std::atomic<unsigned long long> allowed;
+    cudaError_t e = tc::allow_smem(norm_rope_kernel<MODE, BACK>, R::BYTES, allowed);
+    if (e == cudaSuccess)
+        e = tc::launch_pdl(norm_rope_kernel<MODE, BACK>, dim3(p.ctas[0] + p.ctas[1]), dim3(kThreads), R::BYTES, stream, a, p);
+    if (BACK && e == cudaSuccess && (a.dw[0] || a.dw[1]))
+        e = tc::launch_pdl(norm_rope_weights_kernel, dim3((a.dim + 31) / 32, 2), dim3(kSumWarps * 32), 0, stream, a, p);
     return e;
+}
+
+template <bool BACK>
+cudaError_t run_mode(const NormRopeArgs &a, cudaStream_t stream)
+{
+    if (a.interleaved)
+        return run<kNeighbours, BACK>(a, stream);
+    return a.rotary % 16 == 0 ? run<kHalves, BACK>(a, stream) : run<kHalvesOdd, BACK>(a, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_norm_rope(const NormRopeArgs &a, cudaStream_t stream)
-{
-    if (a.interleaved)
-        return forward<kNeighbours>(a, stream);
-    return a.rotary % 16 == 0 ? forward<kHalves>(a, stream) : forward<kHalvesOdd>(a, stream);
-}
+cudaError_t launch_norm_rope(const NormRopeArgs &a, cudaStream_t stream) { return run_mode<false>(a, stream); }
 
-size_t norm_rope_backward_workspace(int64_t, int, int dim) { return (size_t)device_sm_count() * kBackCtas * 2 * dim * sizeof(float); }
+size_t norm_rope_backward_workspace(int64_t, int, int dim) { return (size_t)(device_sm_count() + 1) * dim * sizeof(float); }
 
-cudaError_t launch_norm_rope_backward(const NormRopeArgs &a, cudaStream_t stream)
-{
-    if (a.interleaved)
-        return backward<kNeighbours>(a, stream);
-    return a.rotary % 16 == 0 ? backward<kHalves>(a, stream) : backward<kHalvesOdd>(a, stream);
-}
+cudaError_t launch_norm_rope_backward(const NormRopeArgs &a, cudaStream_t stream) { return run_mode<true>(a, stream); }
 
 }  // namespace s3d8
