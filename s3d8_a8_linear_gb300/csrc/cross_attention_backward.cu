@@ -26,7 +26,7 @@ namespace {
 using namespace cross;
 
 constexpr int kThreads = 384;
-constexpr int kMostTiles = 1024;        // tiles of a launch that have sums of their own
+constexpr int kMostTiles = 128;         // tiles of a launch that have sums of their own (their list fits beside five tiles of 32 KB)
 constexpr int kJoinWarps = 8, kJoinRows = 32;
 
 struct Plan {
@@ -34,12 +34,15 @@ struct Plan {
     int q_tiles;                        // in all
     int first, tiles;                   // of this launch: query tiles or tiles of states
     int rows, ctas;                     // rows of a slot of partial sums
-    float2 *info;                       // [T * Hq]: -lse in base-2 exponents, -delta
+    float *info;                        // [q_tiles][heads][4][128]: -lse in base-2 exponents, -delta, the span's ends
     int2 *ranges;                       // [q_tiles]: states that some row sees
     float *parts;                       // [ctas][2][1 or 2][rows][DP]
     Cut *cuts;                          // [ctas]: what there is to add
     int negative;
 };
+
+// What there is to know about the rows of a tile of one key/value head.
+__device__ __forceinline__ float *info_of(const Plan &p, int heads, int tile, int head) { return p.info + ((int64_t)tile * heads + head) * 4 * kTile; }
 
 constexpr int kReadyRows = 32;          // of a block
 
@@ -79,10 +82,14 @@ __global__ __launch_bounds__(256) void cross_ready_kernel(const __grid_constant_
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1)
             sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (live && lane == 0) {
-            const int64_t at = (int64_t)t * a.Hq + h;
-            const int2 s = span_of(a.spans, a.S, t, nullptr);
-            p.info[at] = s.x < s.y ? make_float2(-a.lse[at] * kLog2e, -sum) : make_float2(-INFINITY, 0.0f);
+        if (lane == 0) {
+            const int2 see = live ? span_of(a.spans, a.S, t, nullptr) : make_int2(0, 0);
+            const bool some = see.x < see.y;
+            float *to = info_of(p, a.heads, tile, head) + r;
+            to[0] = some ? -a.lse[(int64_t)t * a.Hq + h] * kLog2e : -INFINITY;
+            to[kTile] = some ? -sum : 0.0f;
+            to[2 * kTile] = __int_as_float(see.x);
+            to[3 * kTile] = __int_as_float(see.y);
         }
     }
 }
@@ -123,13 +130,19 @@ template <int DP>
 struct Layout {
     static constexpr int CHUNKS = DP / 64;
     static constexpr int TILE = kTile * DP * 2;
-    static constexpr int STAGES = DP == 128 ? 4 : 8;
+    // of the ring: keys or queries, which are in use from the first product to the last, and values or dout
+    static constexpr int LONG = DP == 128 ? 3 : 6, SHORT = DP == 128 ? 2 : 4, STAGES = LONG + SHORT;
     static constexpr int FIX = 0, RING = 2 * TILE, ITEMS = RING + STAGES * TILE;
-    static constexpr int RANGES = ITEMS + ((kMostTiles + 1) * (int)sizeof(Item) + 15) / 16 * 16;   // [tiles] while the list is made
-    static constexpr int INFO = RANGES + kMostTiles * 8;        // [STAGES / 2][4][128]: -lse, -delta, span
-    static constexpr int FULL = INFO + STAGES / 2 * 4 * kTile * 4;      // [STAGES / 2][2]
-    static constexpr int BARS = FULL + STAGES / 2 * 8;
-    static constexpr int BYTES = 1024 + BARS + 512;
+    static constexpr int BARS = ITEMS + ((kMostTiles + 1) * (int)sizeof(Item) + 7) / 8 * 8, SLOT = BARS + 80 + 24 * STAGES;
+    static constexpr int DQ_BYTES = SLOT + 8;
+    // of a visit's query rows: [LONG][2] whether 64 of them see the whole tile, [128] the part of
+    // it that each sees, [2][128] -lse and -delta
+    static constexpr int FULL = SLOT + 8, SEEN = (FULL + LONG * 8 + 15) / 16 * 16, INFO = SEEN + kTile * 2;
+    static constexpr int DKV_BYTES = INFO + 2 * kTile * 4;      // with the tiles, all that a CTA can have
+
+    // where visit v's tile is, and how often its place was filled before
+    static __device__ __forceinline__ int place(int v, int s) { return s ? LONG + v % SHORT : v % LONG; }
+    static __device__ __forceinline__ int lap(int v, int s) { return s ? v / SHORT : v / LONG; }
 };
 
 __device__ __forceinline__ void setup_common(uint32_t *tmem_slot, int warp)
@@ -140,12 +153,25 @@ __device__ __forceinline__ void setup_common(uint32_t *tmem_slot, int warp)
     }
 }
 
+// Not before the last copies of `visits` visits have landed.
+template <typename L>
+__device__ __forceinline__ bool landed(uint32_t full, int visits)
+{
+    bool ok = true;
+    for (int st = 0; st < L::STAGES; ++st) {
+        const int s = st >= L::LONG, i = st - s * L::LONG, n = s ? L::SHORT : L::LONG, uses = (visits - i + n - 1) / n;
+        if (visits > i)
+            ok &= tc::warp_wait(full + 8 * st, (uses - 1) & 1);
+    }
+    return ok;
+}
+
 // A row of 128-byte swizzled chunks that holds an infinity or NaN.
 template <int DP>
 __device__ __forceinline__ bool bad_row(uint32_t tile, int r)
 {
     uint32_t top = 0;
-#pragma unroll
+#pragma unroll 4
     for (int c = 0; c < DP / 8; ++c)
         top = absmax_bf16x8(lds_v4(chunk_at(tile, r, c)), top);
     return !finite2(top);
@@ -183,10 +209,14 @@ __global__ __launch_bounds__(kThreads, 1) void cross_dq_kernel(const __grid_cons
                                                                const __grid_constant__ CrossArgs a, const __grid_constant__ Plan p)
 {
     using L = Layout<DP>;
-    extern __shared__ unsigned char cross_mem[];
-    __shared__ uint32_t tmem_slot;
-    const uint32_t base = (smem_addr(cross_mem) + 1023u) & ~1023u;
-    unsigned char *mem = cross_mem + (base - smem_addr(cross_mem));
+    extern __shared__ __align__(1024) unsigned char cross_mem_aligned[];
+    unsigned char *mem = cross_mem_aligned;
+    const uint32_t base = smem_addr(mem);
+    if (base & 1023u) {         // (the first of the CTA's shared memory)
+        record_timeout(a.status);
+        return;
+    }
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(mem + L::SLOT);
     Item *items = reinterpret_cast<Item *>(mem + L::ITEMS);
     const uint32_t bars = base + L::BARS;
     const uint32_t q_full = bars, q_empty = bars + 8, o_free = bars + 16, s_full = bars + 24, s_read = bars + 32, done = bars + 40;
@@ -211,7 +241,7 @@ __global__ __launch_bounds__(kThreads, 1) void cross_dq_kernel(const __grid_cons
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    setup_common(&tmem_slot, warp);
+    setup_common(tmem_slot, warp);
     if (p.chunk_rows < kTile)       // rows that no copy fills are zeros
         for (int i = threadIdx.x; i < 2 * L::TILE / 16; i += kThreads)
             reinterpret_cast<uint4 *>(mem + L::FIX)[i] = make_uint4(0u, 0u, 0u, 0u);
@@ -228,122 +258,124 @@ __global__ __launch_bounds__(kThreads, 1) void cross_dq_kernel(const __grid_cons
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
-    const uint32_t tmem = tmem_slot;
+    const uint32_t tmem = *tmem_slot;
     Share share(items, p.tiles, a.heads, p.ctas);
     Piece u;
     bool ok = true;
 
-    if (warp == 0) {                // copies
-        int at = 0;
-        for (int units = 0; ok && share.next(u); ++units) {
-            if (units > 0 && !(ok = tc::warp_wait(q_empty, (units - 1) & 1)))
-                break;
-            tc::mbar_arrive_expect_tx_elect(q_full, 2 * L::CHUNKS * 128 * p.chunk_rows);
-            for (int s = 0; s < 2; ++s)
-                for (int c = 0; c < L::CHUNKS; ++c)
-                    tma_3d_elect(base + L::FIX + s * L::TILE + c * (kTile * 128), s ? &map_d : &map_q, 64 * c, u.head * group,
-                                 (p.first + u.tile) * p.tokens_a_tile, q_full);
-            for (int i = 0; ok && i < 2 * u.n; ++i, ++at) {
-                const int st = at % L::STAGES;
-                if (at >= L::STAGES && !(ok = tc::warp_wait(kv_empty + 8 * st, (at / L::STAGES - 1) & 1)))
+    if (warp < 4) {
+        if (warp == 0) {                // copies
+            int at = 0, last = 0;
+            for (int units = 0; ok && share.next(u); ++units) {
+                if (units > 0 && !(ok = tc::warp_wait(q_empty, (units - 1) & 1)))
                     break;
-                tc::mbar_arrive_expect_tx_elect(kv_full + 8 * st, L::TILE);
-                for (int c = 0; c < L::CHUNKS; ++c)
-                    tma_3d_elect(base + L::RING + st * L::TILE + c * (kTile * 128), i & 1 ? &map_v : &map_k, 64 * c, u.head, (u.j0 + (i >> 1)) * kTile,
-                                 kv_full + 8 * st);
-            }
-        }
-        for (int i = at - L::STAGES < 0 ? 0 : at - L::STAGES; i < at; ++i)      // not before the last copies have landed
-            ok &= tc::warp_wait(kv_full + 8 * (i % L::STAGES), (i / L::STAGES) & 1);
-        if (lane == 0)
-            p.cuts[blockIdx.x] = cut_of(share, u, at > 0, a.heads, p.ctas);
-    } else if (warp == 1) {         // products
-        const int ksteps = (a.dim + 15) / 16;
-        const uint32_t id_s = idesc_cols(kTile) | (p.negative ? kNegateA : 0u), id_p = idesc_cols(kTile), id_o = idesc_rows(ksteps * 16);
-        int at = 0, jobs = 0;
-        for (int units = 0; ok && share.next(u); ++units) {
-            if (!(ok = tc::warp_wait(q_full, units & 1)))
-                break;
-            for (int j = 0; ok && j <= u.n; ++j) {
-                if (j < u.n) {
-                    const int k = at + 2 * j, ks = k % L::STAGES, v = k + 1, vs = v % L::STAGES, job = jobs + j;
-                    if (!(ok = tc::warp_wait(k_ok + 8 * ks, (k / L::STAGES) & 1)))
+                tc::mbar_arrive_expect_tx_elect(q_full, 2 * L::CHUNKS * 128 * p.chunk_rows);
+                for (int s = 0; s < 2; ++s)
+                    for (int c = 0; c < L::CHUNKS; ++c)
+                        tma_3d_elect(base + L::FIX + s * L::TILE + c * (kTile * 128), s ? &map_d : &map_q, 64 * c, u.head * group,
+                                     (p.first + u.tile) * p.tokens_a_tile, q_full);
+                for (int i = 0; ok && i < 2 * u.n; ++i) {
+                    const int v = at + (i >> 1), s = i & 1, st = L::place(v, s), lap = L::lap(v, s);
+                    if (lap > 0 && !(ok = tc::warp_wait(kv_empty + 8 * st, (lap - 1) & 1)))
                         break;
-                    if (job > 0 && !(ok = tc::warp_wait(s_read, (job - 1) & 1)))
-                        break;
-                    tc::tc_fence_after();
-                    for (int kk = 0; kk < ksteps; ++kk) {
-                        const uint32_t off = (kk >> 2) * (kTile * 128) + (kk & 3) * 32;
-                        tc::mma_bf16_elect(tmem, tc::sw128_desc(base + L::FIX + off), tc::sw128_desc(base + L::RING + ks * L::TILE + off), id_s, kk > 0);
-                    }
-                    tc::mma_commit_elect(s_full);
-                    if (!(ok = tc::warp_wait(k_ok + 8 * vs, (v / L::STAGES) & 1)))
-                        break;
-                    tc::tc_fence_after();
-                    for (int kk = 0; kk < ksteps; ++kk) {
-                        const uint32_t off = (kk >> 2) * (kTile * 128) + (kk & 3) * 32;
-                        tc::mma_bf16_elect(tmem + 128 + (job & 1) * 128, tc::sw128_desc(base + L::FIX + L::TILE + off),
-                                           tc::sw128_desc(base + L::RING + vs * L::TILE + off), id_p, kk > 0);
-                    }
-                    tc::mma_commit_elect(dp_full + 8 * (job & 1));
-                    tc::mma_commit_elect(kv_empty + 8 * vs);
-                    if (j == u.n - 1)
-                        tc::mma_commit_elect(q_empty);
+                    tc::mbar_arrive_expect_tx_elect(kv_full + 8 * st, L::TILE);
+                    last = v + 1;
+                    for (int c = 0; c < L::CHUNKS; ++c)
+                        tma_3d_elect(base + L::RING + st * L::TILE + c * (kTile * 128), s ? &map_v : &map_k, 64 * c, u.head, (u.j0 + (i >> 1)) * kTile,
+                                     kv_full + 8 * st);
                 }
-                if (j > 0) {
-                    const int k = at + 2 * (j - 1), ks = k % L::STAGES, job = jobs + j - 1;
-                    if (j == 1 && units > 0 && !(ok = tc::warp_wait(o_free, (units - 1) & 1)))
-                        break;
-                    if (!(ok = tc::warp_wait(ds_ready + 8 * (job & 1), (job >> 1) & 1)))
-                        break;
-                    tc::tc_fence_after();
-                    for (int kk = 0; kk < kTile / 16; ++kk)
-                        mma_tmem_a_elect(tmem + 384, tmem + 128 + (job & 1) * 128 + (kk >> 2) * 64 + (kk & 3) * 8,
-                                         rows_desc(base + L::RING + ks * L::TILE + kk * 2048, kTile * 128), id_o, j > 1 || kk > 0);
-                    tc::mma_commit_elect(kv_empty + 8 * ks);
-                    if (j == u.n)
-                        tc::mma_commit_elect(done);
-                }
+                at += u.n;
             }
-            at += 2 * u.n;
-            jobs += u.n;
-        }
-    } else if (warp < 4) {          // looks the keys over
-        int at = 0;
-        while (ok && share.next(u)) {
-            const int t0 = (p.first + u.tile) * p.tokens_a_tile;
-            int lo = 0, hi = 0x7FFFFFFF;        // the states that every row with any sees
-            for (int i = lane; i < p.tokens_a_tile && t0 + i < a.T; i += 32) {
-                const int2 see = span_of(a.spans, a.S, t0 + i, nullptr);
-                if (see.x < see.y)
-                    lo = max(lo, see.x), hi = min(hi, see.y);
-            }
-            lo = __reduce_max_sync(0xffffffffu, lo);
-            hi = __reduce_min_sync(0xffffffffu, hi);
-            for (int i = 0; i < 2 * u.n; ++i) {
-                const int st = (at + i) % L::STAGES, c0 = (u.j0 + (i >> 1)) * kTile;
-                if (!(ok = tc::warp_wait(kv_full + 8 * st, ((at + i) / L::STAGES) & 1)))
+            ok &= landed<L>(kv_full, last);
+            if (lane == 0)
+                p.cuts[blockIdx.x] = cut_of(share, u, at > 0, a.heads, p.ctas);
+        } else if (warp == 1) {         // products
+            const int ksteps = (a.dim + 15) / 16;
+            const uint32_t id_s = idesc_cols(kTile) | (p.negative ? kNegateA : 0u), id_p = idesc_cols(kTile), id_o = idesc_rows(ksteps * 16);
+            int jobs = 0;
+            for (int units = 0; ok && share.next(u); ++units) {
+                if (!(ok = tc::warp_wait(q_full, units & 1)))
                     break;
-                if (!(i & 1) && (c0 < lo || c0 + kTile > hi)) {
-                    const uint32_t tile = base + L::RING + st * L::TILE;
-                    for (int r = (warp - 2) * 32 + lane; r < kTile; r += 64) {
-                        if (!bad_row<DP>(tile, r))
-                            continue;
-                        bool seen = false;
-                        for (int y = 0; y < p.tokens_a_tile && t0 + y < a.T; ++y) {
-                            const int2 see = span_of(a.spans, a.S, t0 + y, nullptr);
-                            seen |= see.x <= c0 + r && c0 + r < see.y;
+                for (int j = 0; ok && j <= u.n; ++j) {
+                    if (j < u.n) {
+                        const int job = jobs + j, ks = L::place(job, 0), vs = L::place(job, 1);
+                        if (!(ok = tc::warp_wait(k_ok + 8 * ks, L::lap(job, 0) & 1)))
+                            break;
+                        if (job > 0 && !(ok = tc::warp_wait(s_read, (job - 1) & 1)))
+                            break;
+                        tc::tc_fence_after();
+                        for (int kk = 0; kk < ksteps; ++kk) {
+                            const uint32_t off = (kk >> 2) * (kTile * 128) + (kk & 3) * 32;
+                            tc::mma_bf16_elect(tmem, tc::sw128_desc(base + L::FIX + off), tc::sw128_desc(base + L::RING + ks * L::TILE + off), id_s, kk > 0);
                         }
-                        if (!seen)
-                            clear_row<DP>(tile, r);
+                        tc::mma_commit_elect(s_full);
+                        if (!(ok = tc::warp_wait(k_ok + 8 * vs, L::lap(job, 1) & 1)))
+                            break;
+                        tc::tc_fence_after();
+                        for (int kk = 0; kk < ksteps; ++kk) {
+                            const uint32_t off = (kk >> 2) * (kTile * 128) + (kk & 3) * 32;
+                            tc::mma_bf16_elect(tmem + 128 + (job & 1) * 128, tc::sw128_desc(base + L::FIX + L::TILE + off),
+                                               tc::sw128_desc(base + L::RING + vs * L::TILE + off), id_p, kk > 0);
+                        }
+                        tc::mma_commit_elect(dp_full + 8 * (job & 1));
+                        tc::mma_commit_elect(kv_empty + 8 * vs);
+                        if (j == u.n - 1)
+                            tc::mma_commit_elect(q_empty);
                     }
-                    fence_proxy_async_smem();
-                    __syncwarp();
+                    if (j > 0) {
+                        const int job = jobs + j - 1, ks = L::place(job, 0);
+                        if (j == 1 && units > 0 && !(ok = tc::warp_wait(o_free, (units - 1) & 1)))
+                            break;
+                        if (!(ok = tc::warp_wait(ds_ready + 8 * (job & 1), (job >> 1) & 1)))
+                            break;
+                        tc::tc_fence_after();
+                        for (int kk = 0; kk < kTile / 16; ++kk)
+                            mma_tmem_a_elect(tmem + 384, tmem + 128 + (job & 1) * 128 + (kk >> 2) * 64 + (kk & 3) * 8,
+                                             rows_desc(base + L::RING + ks * L::TILE + kk * 2048, kTile * 128), id_o, j > 1 || kk > 0);
+                        tc::mma_commit_elect(kv_empty + 8 * ks);
+                        if (j == u.n)
+                            tc::mma_commit_elect(done);
+                    }
                 }
-                if (lane == 0)
-                    tc::mbar_arrive(k_ok + 8 * st);
+                jobs += u.n;
             }
-            at += 2 * u.n;
+        } else if (warp < 4) {          // looks the keys over
+            int at = 0;
+            while (ok && share.next(u)) {
+                const int t0 = (p.first + u.tile) * p.tokens_a_tile;
+                int lo = 0, hi = 0x7FFFFFFF;        // the states that every row with any sees
+                for (int i = lane; i < p.tokens_a_tile && t0 + i < a.T; i += 32) {
+                    const int2 see = span_of(a.spans, a.S, t0 + i, nullptr);
+                    if (see.x < see.y)
+                        lo = max(lo, see.x), hi = min(hi, see.y);
+                }
+                lo = __reduce_max_sync(0xffffffffu, lo);
+                hi = __reduce_min_sync(0xffffffffu, hi);
+                for (int i = 0; i < 2 * u.n; ++i) {
+                    const int v = at + (i >> 1), st = L::place(v, i & 1), c0 = (u.j0 + (i >> 1)) * kTile;
+                    if (!(ok = tc::warp_wait(kv_full + 8 * st, L::lap(v, i & 1) & 1)))
+                        break;
+                    if (!(i & 1) && (c0 < lo || c0 + kTile > hi)) {
+                        const uint32_t tile = base + L::RING + st * L::TILE;
+                        for (int r = (warp - 2) * 32 + lane; r < kTile; r += 64) {
+                            if (!bad_row<DP>(tile, r))
+                                continue;
+                            bool seen = false;
+                            for (int y = 0; y < p.tokens_a_tile && t0 + y < a.T; ++y) {
+                                const int2 see = span_of(a.spans, a.S, t0 + y, nullptr);
+                                seen |= see.x <= c0 + r && c0 + r < see.y;
+                            }
+                            if (!seen)
+                                clear_row<DP>(tile, r);
+                        }
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                    if (lane == 0)
+                        tc::mbar_arrive(k_ok + 8 * st);
+                }
+                at += u.n;
+            }
         }
     } else {                        // softmax: a row a thread, 64 columns a group of warps
         const int half = (warp - 4) >> 2, row = threadIdx.x & 127;
@@ -355,7 +387,8 @@ __global__ __launch_bounds__(kThreads, 1) void cross_dq_kernel(const __grid_cons
             const bool live = row < p.chunk_rows && t < a.T;
             const int64_t at = (int64_t)t * a.Hq + u.head * group + row % group;
             const int2 see = live ? span_of(a.spans, a.S, t, nullptr) : make_int2(0, 0);
-            const float2 info = see.x < see.y ? p.info[at] : make_float2(-INFINITY, 0.0f);
+            const float *known = info_of(p, a.heads, p.first + u.tile, u.head) + row;
+            const float2 info = make_float2(known[0], known[kTile]);
             const float2 scale2 = make_float2(scale, scale), lse2 = make_float2(info.x, info.x), delta2 = make_float2(info.y, info.y);
             for (int i = 0; i < u.n; ++i, ++jobs) {
                 const int c0 = (u.j0 + i) * kTile + 64 * half;
@@ -441,13 +474,16 @@ __global__ __launch_bounds__(kThreads, 1) void cross_dkv_kernel(const __grid_con
                                                                 const __grid_constant__ CrossArgs a, const __grid_constant__ Plan p)
 {
     using L = Layout<DP>;
-    constexpr int PAIRS = L::STAGES / 2;        // query tiles that the ring holds
-    extern __shared__ unsigned char cross_mem[];
-    __shared__ uint32_t tmem_slot;
-    const uint32_t base = (smem_addr(cross_mem) + 1023u) & ~1023u;
-    unsigned char *mem = cross_mem + (base - smem_addr(cross_mem));
+    extern __shared__ __align__(1024) unsigned char cross_mem_aligned[];
+    unsigned char *mem = cross_mem_aligned;
+    const uint32_t base = smem_addr(mem);
+    if (base & 1023u) {         // (the first of the CTA's shared memory)
+        record_timeout(a.status);
+        return;
+    }
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(mem + L::SLOT);
     Item *items = reinterpret_cast<Item *>(mem + L::ITEMS);
-    int2 *ranges = reinterpret_cast<int2 *>(mem + L::RANGES);
+    int2 *ranges = reinterpret_cast<int2 *>(mem + L::RING);     // (while the list is made)
     const uint32_t bars = base + L::BARS;
     const uint32_t kv_full = bars, kv_empty = bars + 8, o_free = bars + 16, s_full = bars + 24, p_ready = bars + 32, dp_full = bars + 40, ds_ready = bars + 48,
                    done = bars + 56;
@@ -469,11 +505,7 @@ __global__ __launch_bounds__(kThreads, 1) void cross_dkv_kernel(const __grid_con
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    setup_common(&tmem_slot, warp);
-    if (p.chunk_rows < kTile)
-        for (int i = threadIdx.x; i < L::STAGES * L::TILE / 16; i += kThreads)
-            reinterpret_cast<uint4 *>(mem + L::RING)[i] = make_uint4(0u, 0u, 0u, 0u);
-    fence_proxy_async_smem();
+    setup_common(tmem_slot, warp);
     __syncthreads();
     tc::pdl_launch_dependents();
     tc::pdl_wait();
@@ -491,143 +523,156 @@ __global__ __launch_bounds__(kThreads, 1) void cross_dkv_kernel(const __grid_con
     if (warp == 0) {
         make_list(p.tiles, items, [&](int i) { return ranges[i]; });
     }
+    __syncthreads();
+    if (p.chunk_rows < kTile)       // rows that no copy fills are zeros
+        for (int i = threadIdx.x; i < L::STAGES * L::TILE / 16; i += kThreads)
+            reinterpret_cast<uint4 *>(mem + L::RING)[i] = make_uint4(0u, 0u, 0u, 0u);
+    fence_proxy_async_smem();
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
-    const uint32_t tmem = tmem_slot;
+    const uint32_t tmem = *tmem_slot;
     Share share(items, p.tiles, a.heads, p.ctas);
     Piece u;
     bool ok = true;
 
-    if (warp == 0) {                // copies
-        int at = 0;
-        for (int units = 0; ok && share.next(u); ++units) {
-            if (units > 0 && !(ok = tc::warp_wait(kv_empty, (units - 1) & 1)))
-                break;
-            tc::mbar_arrive_expect_tx_elect(kv_full, 2 * L::TILE);
-            for (int s = 0; s < 2; ++s)
-                for (int c = 0; c < L::CHUNKS; ++c)
-                    tma_3d_elect(base + L::FIX + s * L::TILE + c * (kTile * 128), s ? &map_v : &map_k, 64 * c, u.head, (p.first + u.tile) * kTile, kv_full);
-            for (int i = 0; ok && i < 2 * u.n; ++i, ++at) {
-                const int st = at % L::STAGES;
-                if (at >= L::STAGES && !(ok = tc::warp_wait(q_empty + 8 * st, (at / L::STAGES - 1) & 1)))
+    if (warp < 4) {
+        if (warp == 0) {                // copies
+            int at = 0, last = 0;
+            for (int units = 0; ok && share.next(u); ++units) {
+                if (units > 0 && !(ok = tc::warp_wait(kv_empty, (units - 1) & 1)))
                     break;
-                tc::mbar_arrive_expect_tx_elect(q_full + 8 * st, L::CHUNKS * 128 * p.chunk_rows);
-                for (int c = 0; c < L::CHUNKS; ++c)
-                    tma_3d_elect(base + L::RING + st * L::TILE + c * (kTile * 128), i & 1 ? &map_d : &map_q, 64 * c, u.head * group,
-                                 (u.j0 + (i >> 1)) * p.tokens_a_tile, q_full + 8 * st);
-            }
-        }
-        for (int i = at - L::STAGES < 0 ? 0 : at - L::STAGES; i < at; ++i)
-            ok &= tc::warp_wait(q_full + 8 * (i % L::STAGES), (i / L::STAGES) & 1);
-        if (lane == 0)
-            p.cuts[blockIdx.x] = cut_of(share, u, at > 0, a.heads, p.ctas);
-    } else if (warp == 1) {         // products
-        const int ksteps = (a.dim + 15) / 16;
-        const uint32_t id_s = idesc_cols(kTile) | (p.negative ? kNegateA : 0u), id_p = idesc_cols(kTile), id_o = idesc_rows(ksteps * 16);
-        int at = 0, jobs = 0;
-        for (int units = 0; ok && share.next(u); ++units) {
-            if (!(ok = tc::warp_wait(kv_full, units & 1)))
-                break;
-            auto scores = [&](int j) {
-                const int q = at + 2 * j, qs = q % L::STAGES;
-                if (!(ok = tc::warp_wait(q_ok + 8 * qs, (q / L::STAGES) & 1)))
-                    return;
-                tc::tc_fence_after();
-                for (int kk = 0; kk < ksteps; ++kk) {
-                    const uint32_t off = (kk >> 2) * (kTile * 128) + (kk & 3) * 32;
-                    tc::mma_bf16_elect(tmem, tc::sw128_desc(base + L::FIX + off), tc::sw128_desc(base + L::RING + qs * L::TILE + off), id_s, kk > 0);
-                }
-                tc::mma_commit_elect(s_full);
-            };
-            scores(0);
-            for (int j = 0; ok && j < u.n; ++j, ++jobs) {
-                const int q = at + 2 * j, qs = q % L::STAGES, d = q + 1, ds = d % L::STAGES;
-                if (!(ok = tc::warp_wait(q_ok + 8 * ds, (d / L::STAGES) & 1)))
-                    break;
-                tc::tc_fence_after();
-                for (int kk = 0; kk < ksteps; ++kk) {
-                    const uint32_t off = (kk >> 2) * (kTile * 128) + (kk & 3) * 32;
-                    tc::mma_bf16_elect(tmem + 128, tc::sw128_desc(base + L::FIX + L::TILE + off), tc::sw128_desc(base + L::RING + ds * L::TILE + off), id_p,
-                                       kk > 0);
-                }
-                tc::mma_commit_elect(dp_full);
-                if (j == u.n - 1)
-                    tc::mma_commit_elect(kv_empty);
-                if (j == 0 && units > 0 && !(ok = tc::warp_wait(o_free, (units - 1) & 1)))
-                    break;
-                if (!(ok = tc::warp_wait(p_ready, jobs & 1)))
-                    break;
-                tc::tc_fence_after();
-                for (int kk = 0; kk < kTile / 16; ++kk)
-                    mma_tmem_a_elect(tmem + 256, tmem + (kk >> 2) * 64 + (kk & 3) * 8, rows_desc(base + L::RING + ds * L::TILE + kk * 2048, kTile * 128), id_o,
-                                     j > 0 || kk > 0);
-                tc::mma_commit_elect(q_empty + 8 * ds);
-                if (j + 1 < u.n)
-                    scores(j + 1);
-                if (!ok || !(ok = tc::warp_wait(ds_ready, jobs & 1)))
-                    break;
-                tc::tc_fence_after();
-                for (int kk = 0; kk < kTile / 16; ++kk)
-                    mma_tmem_a_elect(tmem + 384, tmem + 128 + (kk >> 2) * 64 + (kk & 3) * 8, rows_desc(base + L::RING + qs * L::TILE + kk * 2048, kTile * 128),
-                                     id_o, j > 0 || kk > 0);
-                tc::mma_commit_elect(q_empty + 8 * qs);
-                if (j == u.n - 1)
-                    tc::mma_commit_elect(done);
-            }
-            at += 2 * u.n;
-        }
-    } else if (warp < 4) {          // the rows' lse, delta and spans; looks the query rows over
-        int at = 0;
-        while (ok && share.next(u)) {
-            const int c0 = (p.first + u.tile) * kTile;
-            for (int i = 0; ok && i < u.n; ++i) {
-                const int q = at + 2 * i, pair = q / 2 % PAIRS;
-                float2 info[2];
-                int2 see[2];
-                bool all = true;
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    const int r = (warp - 2) * 64 + y * 32 + lane, t = (u.j0 + i) * p.tokens_a_tile + r / group;
-                    const bool live = r < p.chunk_rows && t < a.T;
-                    see[y] = live ? span_of(a.spans, a.S, t, nullptr) : make_int2(0, 0);
-                    info[y] = see[y].x < see[y].y ? p.info[(int64_t)t * a.Hq + u.head * group + r % group] : make_float2(-INFINITY, 0.0f);
-                    all &= see[y].x <= c0 && see[y].y >= c0 + kTile;
-                }
-                all = __all_sync(0xffffffffu, all);
-                for (int s = 0; s < 2; ++s) {
-                    const int st = (q + s) % L::STAGES;
-                    if (!(ok = tc::warp_wait(q_full + 8 * st, ((q + s) / L::STAGES) & 1)))
+                tc::mbar_arrive_expect_tx_elect(kv_full, 2 * L::TILE);
+                for (int s = 0; s < 2; ++s)
+                    for (int c = 0; c < L::CHUNKS; ++c)
+                        tma_3d_elect(base + L::FIX + s * L::TILE + c * (kTile * 128), s ? &map_v : &map_k, 64 * c, u.head, (p.first + u.tile) * kTile, kv_full);
+                for (int i = 0; ok && i < 2 * u.n; ++i) {
+                    const int v = at + (i >> 1), s = i & 1, st = L::place(v, s), lap = L::lap(v, s);
+                    if (lap > 0 && !(ok = tc::warp_wait(q_empty + 8 * st, (lap - 1) & 1)))
                         break;
-                    if (s == 0) {       // the tile before in this place is done with: its copy has begun anew
-                        float *to = reinterpret_cast<float *>(mem + L::INFO) + pair * 4 * kTile;
-#pragma unroll
-                        for (int y = 0; y < 2; ++y) {
-                            const int r = (warp - 2) * 64 + y * 32 + lane;
-                            to[r] = info[y].x;
-                            to[kTile + r] = info[y].y;
-                            to[2 * kTile + r] = __int_as_float(see[y].x);
-                            to[3 * kTile + r] = __int_as_float(see[y].y);
-                        }
-                        if (lane == 0)
-                            reinterpret_cast<int *>(mem + L::FULL)[pair * 2 + warp - 2] = all;
+                    tc::mbar_arrive_expect_tx_elect(q_full + 8 * st, L::CHUNKS * 128 * p.chunk_rows);
+                    last = v + 1;
+                    for (int c = 0; c < L::CHUNKS; ++c)
+                        tma_3d_elect(base + L::RING + st * L::TILE + c * (kTile * 128), s ? &map_d : &map_q, 64 * c, u.head * group,
+                                     (u.j0 + (i >> 1)) * p.tokens_a_tile, q_full + 8 * st);
+                }
+                at += u.n;
+            }
+            ok &= landed<L>(q_full, last);
+            if (lane == 0)
+                p.cuts[blockIdx.x] = cut_of(share, u, at > 0, a.heads, p.ctas);
+        } else if (warp == 1) {         // products
+            const int ksteps = (a.dim + 15) / 16;
+            const uint32_t id_s = idesc_cols(kTile) | (p.negative ? kNegateA : 0u), id_p = idesc_cols(kTile), id_o = idesc_rows(ksteps * 16);
+            int jobs = 0;
+            for (int units = 0; ok && share.next(u); ++units) {
+                if (!(ok = tc::warp_wait(kv_full, units & 1)))
+                    break;
+                auto scores = [&](int v) {
+                    const int qs = L::place(v, 0);
+                    if (!(ok = tc::warp_wait(q_ok + 8 * qs, L::lap(v, 0) & 1)))
+                        return;
+                    tc::tc_fence_after();
+                    for (int kk = 0; kk < ksteps; ++kk) {
+                        const uint32_t off = (kk >> 2) * (kTile * 128) + (kk & 3) * 32;
+                        tc::mma_bf16_elect(tmem, tc::sw128_desc(base + L::FIX + off), tc::sw128_desc(base + L::RING + qs * L::TILE + off), id_s, kk > 0);
                     }
-                    if (!all) {
-#pragma unroll
-                        for (int y = 0; y < 2; ++y) {
-                            const int r = (warp - 2) * 64 + y * 32 + lane;
-                            const bool part = max(see[y].x, c0) < min(see[y].y, c0 + kTile);
-                            if (!part && bad_row<DP>(base + L::RING + st * L::TILE, r))
-                                clear_row<DP>(base + L::RING + st * L::TILE, r);
-                        }
-                        fence_proxy_async_smem();
+                    tc::mma_commit_elect(s_full);
+                };
+                scores(jobs);
+                for (int j = 0; ok && j < u.n; ++j, ++jobs) {
+                    const int qs = L::place(jobs, 0), ds = L::place(jobs, 1);
+                    if (!(ok = tc::warp_wait(q_ok + 8 * ds, L::lap(jobs, 1) & 1)))
+                        break;
+                    tc::tc_fence_after();
+                    for (int kk = 0; kk < ksteps; ++kk) {
+                        const uint32_t off = (kk >> 2) * (kTile * 128) + (kk & 3) * 32;
+                        tc::mma_bf16_elect(tmem + 128, tc::sw128_desc(base + L::FIX + L::TILE + off), tc::sw128_desc(base + L::RING + ds * L::TILE + off), id_p,
+                                           kk > 0);
                     }
-                    __syncwarp();
-                    if (lane == 0)
-                        tc::mbar_arrive(q_ok + 8 * st);
+                    tc::mma_commit_elect(dp_full);
+                    if (j == u.n - 1)
+                        tc::mma_commit_elect(kv_empty);
+                    if (j == 0 && units > 0 && !(ok = tc::warp_wait(o_free, (units - 1) & 1)))
+                        break;
+                    if (!(ok = tc::warp_wait(p_ready, jobs & 1)))
+                        break;
+                    tc::tc_fence_after();
+                    for (int kk = 0; kk < kTile / 16; ++kk)
+                        mma_tmem_a_elect(tmem + 256, tmem + (kk >> 2) * 64 + (kk & 3) * 8, rows_desc(base + L::RING + ds * L::TILE + kk * 2048, kTile * 128), id_o,
+                                         j > 0 || kk > 0);
+                    tc::mma_commit_elect(q_empty + 8 * ds);
+                    if (j + 1 < u.n)
+                        scores(jobs + 1);
+                    if (!ok || !(ok = tc::warp_wait(ds_ready, jobs & 1)))
+                        break;
+                    tc::tc_fence_after();
+                    for (int kk = 0; kk < kTile / 16; ++kk)
+                        mma_tmem_a_elect(tmem + 384, tmem + 128 + (kk >> 2) * 64 + (kk & 3) * 8, rows_desc(base + L::RING + qs * L::TILE + kk * 2048, kTile * 128),
+                                         id_o, j > 0 || kk > 0);
+                    tc::mma_commit_elect(q_empty + 8 * qs);
+                    if (j == u.n - 1)
+                        tc::mma_commit_elect(done);
                 }
             }
-            at += 2 * u.n;
+        } else if (warp < 4) {          // looks the query rows over, and lays out what there is to know about them
+            int at = 0;
+            uint16_t *seen = reinterpret_cast<uint16_t *>(mem + L::SEEN);
+            float *known = reinterpret_cast<float *>(mem + L::INFO);
+            while (ok && share.next(u)) {
+                const int c0 = (p.first + u.tile) * kTile, row = (warp - 2) * 64 + lane;
+                float next[2][4];
+                auto fetch = [&](int i) {
+                    const float *info = info_of(p, a.heads, u.j0 + i, u.head) + row;
+#pragma unroll
+                    for (int y = 0; y < 2; ++y)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            next[y][e] = info[32 * y + e * kTile];
+                };
+                fetch(0);
+                for (int i = 0; ok && i < u.n; ++i) {
+                    const int v = at + i;
+                    float info[2][2];
+                    int lo[2], n[2];
+#pragma unroll
+                    for (int y = 0; y < 2; ++y) {
+                        info[y][0] = next[y][0], info[y][1] = next[y][1];
+                        lo[y] = min(max(__float_as_int(next[y][2]) - c0, 0), kTile);
+                        n[y] = max(min(__float_as_int(next[y][3]) - c0, kTile) - lo[y], 0);
+                    }
+                    if (i + 1 < u.n)
+                        fetch(i + 1);
+                    const bool all = __all_sync(0xffffffffu, n[0] == kTile && n[1] == kTile);
+                    for (int s = 0; s < 2; ++s) {
+                        const int st = L::place(v, s);
+                        if (!(ok = tc::warp_wait(q_full + 8 * st, L::lap(v, s) & 1)))
+                            break;
+                        if (!all) {
+#pragma unroll
+                            for (int y = 0; y < 2; ++y)
+                                if (n[y] == 0 && bad_row<DP>(base + L::RING + st * L::TILE, row + 32 * y))
+                                    clear_row<DP>(base + L::RING + st * L::TILE, row + 32 * y);
+                            fence_proxy_async_smem();
+                        }
+                        // the softmax step before has read its own
+                        if (v > 0 && !(ok = tc::warp_wait(s ? ds_ready : p_ready, (v - 1) & 1)))
+                            break;
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            known[s * kTile + row + 32 * y] = info[y][s];
+                            if (s == 0)
+                                seen[row + 32 * y] = (uint16_t)(lo[y] | n[y] << 8);
+                        }
+                        if (s == 0 && lane == 0)
+                            reinterpret_cast<int *>(mem + L::FULL)[st * 2 + warp - 2] = all;
+                        __syncwarp();
+                        if (lane == 0)
+                            tc::mbar_arrive(q_ok + 8 * st);
+                    }
+                }
+                at += u.n;
+            }
         }
     } else {                        // softmax: a state a thread, 64 query rows a group of warps
         const int half = (warp - 4) >> 2, row = threadIdx.x & 127;
@@ -641,11 +686,10 @@ __global__ __launch_bounds__(kThreads, 1) void cross_dkv_kernel(const __grid_con
                 if (!(ok = tc::warp_wait(s_full, jobs & 1)))
                     break;
                 tc::tc_fence_after();
-                const int pair = jobs % PAIRS;
-                const uint32_t info = base + L::INFO + (pair * 4 * kTile + 64 * half) * 4;
-                const int *full = reinterpret_cast<const int *>(mem + L::FULL) + pair * 2;
+                const uint32_t info = base + L::INFO + 64 * half * 4, seen = base + L::SEEN + 64 * half * 2;
+                const int *full = reinterpret_cast<const int *>(mem + L::FULL) + L::place(jobs, 0) * 2;
                 const bool whole = uniform(full[half]) != 0;
-                float x[64], y[64];
+                float x[64], y[32];
                 uint32_t w[32];
                 tmem_ld32(sc, x);
                 tmem_ld32(sc + 32, x + 32);
@@ -659,12 +703,14 @@ __global__ __launch_bounds__(kThreads, 1) void cross_dkv_kernel(const __grid_con
                 }
                 if (!whole) {
 #pragma unroll
-                    for (int c = 0; c < 64; c += 4) {
-                        const uint4 lo = lds_v4(info + (2 * kTile + c) * 4), hi = lds_v4(info + (3 * kTile + c) * 4);
-                        x[c] = j >= (int)lo.x && j < (int)hi.x ? x[c] : 0.0f;
-                        x[c + 1] = j >= (int)lo.y && j < (int)hi.y ? x[c + 1] : 0.0f;
-                        x[c + 2] = j >= (int)lo.z && j < (int)hi.z ? x[c + 2] : 0.0f;
-                        x[c + 3] = j >= (int)lo.w && j < (int)hi.w ? x[c + 3] : 0.0f;
+                    for (int c = 0; c < 64; c += 8) {
+                        const uint4 l = lds_v4(seen + 2 * c);
+                        const uint32_t y[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const uint32_t part = y[e / 2] >> (16 * (e & 1));       // first, count
+                            x[c + e] = row - (part & 0xFFu) < (part >> 8 & 0xFFu) ? x[c + e] : 0.0f;
+                        }
                     }
                 }
 #pragma unroll
@@ -679,25 +725,24 @@ __global__ __launch_bounds__(kThreads, 1) void cross_dkv_kernel(const __grid_con
                 if (!(ok = tc::warp_wait(dp_full, jobs & 1)))
                     break;
                 tc::tc_fence_after();
-                tmem_ld32(dp, y);
-                tmem_ld32(dp + 32, y + 32);
-                tmem_wait_ld();
 #pragma unroll
-                for (int c = 0; c < 64; c += 4) {
-                    const uint4 l = lds_v4(info + (kTile + c) * 4);
-                    const float2 e = add2(make_float2(y[c], y[c + 1]), make_float2(__uint_as_float(l.x), __uint_as_float(l.y)));
-                    const float2 f = add2(make_float2(y[c + 2], y[c + 3]), make_float2(__uint_as_float(l.z), __uint_as_float(l.w)));
-                    y[c] = e.x, y[c + 1] = e.y, y[c + 2] = f.x, y[c + 3] = f.y;
-                }
-                if (!whole) {       // not 0 times what an unseen value gives
+                for (int b = 0; b < 64; b += 32) {
+                    tmem_ld32(dp + b, y);
+                    tmem_wait_ld();
 #pragma unroll
-                    for (int c = 0; c < 64; ++c)
-                        y[c] = x[c] == 0.0f ? 0.0f : y[c];
-                }
-#pragma unroll
-                for (int c = 0; c < 32; ++c) {
-                    const float2 g = mul2(make_float2(x[2 * c], x[2 * c + 1]), make_float2(y[2 * c], y[2 * c + 1]));
-                    w[c] = pack2(g.x, g.y);
+                    for (int c = 0; c < 32; c += 4) {
+                        const uint4 l = lds_v4(info + (kTile + b + c) * 4);
+                        float2 e = add2(make_float2(y[c], y[c + 1]), make_float2(__uint_as_float(l.x), __uint_as_float(l.y)));
+                        float2 f = add2(make_float2(y[c + 2], y[c + 3]), make_float2(__uint_as_float(l.z), __uint_as_float(l.w)));
+                        if (!whole) {       // not 0 times what an unseen value gives
+                            e = make_float2(x[b + c] == 0.0f ? 0.0f : e.x, x[b + c + 1] == 0.0f ? 0.0f : e.y);
+                            f = make_float2(x[b + c + 2] == 0.0f ? 0.0f : f.x, x[b + c + 3] == 0.0f ? 0.0f : f.y);
+                        }
+                        e = mul2(make_float2(x[b + c], x[b + c + 1]), e);
+                        f = mul2(make_float2(x[b + c + 2], x[b + c + 3]), f);
+                        w[(b + c) / 2] = pack2(e.x, e.y);
+                        w[(b + c) / 2 + 1] = pack2(f.x, f.y);
+                    }
                 }
                 tmem_st32(dp, w);
                 tmem_wait_st();
@@ -796,7 +841,7 @@ Plan plan_of(int64_t T, int64_t Hq, int64_t heads, int DP, size_t *bytes)
         at += (n + 15) / 16 * 16;
         return from;
     };
-    p.info = reinterpret_cast<float2 *>(take((size_t)T * Hq * sizeof(float2)));
+    p.info = reinterpret_cast<float *>(take((size_t)p.q_tiles * heads * 4 * kTile * sizeof(float)));
     p.ranges = reinterpret_cast<int2 *>(take((size_t)p.q_tiles * sizeof(int2)));
     p.parts = reinterpret_cast<float *>(take((size_t)p.ctas * 2 * 2 * kTile * DP * sizeof(float)));
     p.cuts = reinterpret_cast<Cut *>(take(p.ctas * sizeof(Cut)));
@@ -808,11 +853,11 @@ template <int DP>
 cudaError_t launch(const CrossArgs &a, cudaStream_t stream)
 {
     using L = Layout<DP>;
-    static_assert(L::BYTES <= 232448 && L::BARS % 8 == 0 && L::INFO % 16 == 0, "shared memory");
+    static_assert(L::DKV_BYTES <= 232448 && L::BARS % 8 == 0 && L::INFO % 16 == 0, "shared memory");
     size_t bytes;
     Plan p = plan_of(a.T, a.Hq, a.heads, DP, &bytes);
     char *ws = static_cast<char *>(a.ws);
-    p.info = reinterpret_cast<float2 *>(ws + reinterpret_cast<size_t>(p.info));
+    p.info = reinterpret_cast<float *>(ws + reinterpret_cast<size_t>(p.info));
     p.ranges = reinterpret_cast<int2 *>(ws + reinterpret_cast<size_t>(p.ranges));
     p.parts = reinterpret_cast<float *>(ws + reinterpret_cast<size_t>(p.parts));
     p.cuts = reinterpret_cast<Cut *>(ws + reinterpret_cast<size_t>(p.cuts));
@@ -827,21 +872,21 @@ cudaError_t launch(const CrossArgs &a, cudaStream_t stream)
         e = row_map(&mv, a.v, a.S, a.heads, a.dim, a.vs, 1, kTile);
     static std::atomic<unsigned long long> allowed_q, allowed_kv;
     if (e == cudaSuccess)
-        e = tc::allow_smem(cross_dq_kernel<DP>, L::BYTES, allowed_q);
+        e = tc::allow_smem(cross_dq_kernel<DP>, L::DQ_BYTES, allowed_q);
     if (e == cudaSuccess)
-        e = tc::allow_smem(cross_dkv_kernel<DP>, L::BYTES, allowed_kv);
+        e = tc::allow_smem(cross_dkv_kernel<DP>, L::DKV_BYTES, allowed_kv);
     if (e == cudaSuccess)
         e = tc::launch_pdl(cross_ready_kernel, dim3(p.q_tiles, a.heads, kTile / kReadyRows), dim3(256), 0, stream, a, p);
     const int tiles = (a.S + kTile - 1) / kTile, most_q = most_tiles(a.heads, tiles, kMostTiles), most_kv = most_tiles(a.heads, p.q_tiles, kMostTiles);
     for (p.first = 0; e == cudaSuccess && p.first < p.q_tiles; p.first += most_q) {
         p.tiles = p.q_tiles - p.first < most_q ? p.q_tiles - p.first : most_q;
-        e = tc::launch_pdl(cross_dq_kernel<DP>, dim3(p.ctas), dim3(kThreads), L::BYTES, stream, mq, md, mk, mv, a, p);
+        e = tc::launch_pdl(cross_dq_kernel<DP>, dim3(p.ctas), dim3(kThreads), L::DQ_BYTES, stream, mq, md, mk, mv, a, p);
         if (e == cudaSuccess)
             e = tc::launch_pdl(cross_add_kernel<DP, false>, dim3(p.ctas, (p.rows + kJoinRows - 1) / kJoinRows), dim3(kJoinWarps * 32), 0, stream, a, p);
     }
     for (p.first = 0; e == cudaSuccess && p.first < tiles; p.first += most_kv) {
         p.tiles = tiles - p.first < most_kv ? tiles - p.first : most_kv;
-        e = tc::launch_pdl(cross_dkv_kernel<DP>, dim3(p.ctas), dim3(kThreads), L::BYTES, stream, mq, md, mk, mv, a, p);
+        e = tc::launch_pdl(cross_dkv_kernel<DP>, dim3(p.ctas), dim3(kThreads), L::DKV_BYTES, stream, mq, md, mk, mv, a, p);
         if (e == cudaSuccess)
             e = tc::launch_pdl(cross_add_kernel<DP, true>, dim3(p.ctas, 2 * kTile / kJoinRows), dim3(kJoinWarps * 32), 0, stream, a, p);
     }
