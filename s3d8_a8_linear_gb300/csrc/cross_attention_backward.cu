@@ -25,7 +25,8 @@ namespace {
 
 using namespace cross;
 
-constexpr int kThreads = 384;
+constexpr int kDqThreads = 512;         // warps: 0 copies, 1 and 2 products, 4 to 11 softmax, 12 to 15 look tiles over
+constexpr int kThreads = 384;           // 0 copies, 1 products, 2 and 3 look tiles over, 4 to 11 softmax
 constexpr int kMostTiles = 128;         // tiles of a launch that have sums of their own (their list fits beside five tiles of 32 KB)
 constexpr int kJoinWarps = 8, kJoinRows = 32;
 
@@ -126,23 +127,35 @@ __device__ __forceinline__ int make_list(int tiles, Item *items, Range range)
     return tiles;
 }
 
-template <int DP>
+// LONG places of the ring are for tiles in use from a visit's first product to its last (keys,
+// or query rows), SHORT ones for the others (values, or dout).
+template <int DP, int LONG_, int SHORT_>
 struct Layout {
     static constexpr int CHUNKS = DP / 64;
     static constexpr int TILE = kTile * DP * 2;
-    // of the ring: keys or queries, which are in use from the first product to the last, and values or dout
-    static constexpr int LONG = DP == 128 ? 3 : 6, SHORT = DP == 128 ? 2 : 4, STAGES = LONG + SHORT;
+    static constexpr int LONG = LONG_, SHORT = SHORT_, STAGES = LONG + SHORT;
     static constexpr int FIX = 0, RING = 2 * TILE, ITEMS = RING + STAGES * TILE;
     static constexpr int BARS = ITEMS + ((kMostTiles + 1) * (int)sizeof(Item) + 7) / 8 * 8, SLOT = BARS + 80 + 24 * STAGES;
-    static constexpr int DQ_BYTES = SLOT + 8;
-    // of a visit's query rows: [LONG][2] whether 64 of them see the whole tile, [128] the part of
-    // it that each sees, [2][128] -lse and -delta
-    static constexpr int FULL = SLOT + 8, SEEN = (FULL + LONG * 8 + 15) / 16 * 16, INFO = SEEN + kTile * 2;
-    static constexpr int DKV_BYTES = INFO + 2 * kTile * 4;      // with the tiles, all that a CTA can have
 
     // where visit v's tile is, and how often its place was filled before
     static __device__ __forceinline__ int place(int v, int s) { return s ? LONG + v % SHORT : v % LONG; }
     static __device__ __forceinline__ int lap(int v, int s) { return s ? v / SHORT : v / LONG; }
+};
+
+// Five tiles of 32 KB are all that fits beside the two fixed ones: with four, dq waited for its
+// keys (338 us of 2 x 2048 tokens' gradients, 216 with five and a product warp more).  dkv has
+// four and its rows' statistics: a fifth with those in single places took 399 us for 351.
+template <int DP>
+struct DqLayout : Layout<DP, DP == 128 ? 3 : 6, DP == 128 ? 2 : 4> {
+    static constexpr int DS_FREE = DqLayout::SLOT + 8, BYTES = DS_FREE + 16;
+};
+
+// Of a visit's query rows: [LONG][2] whether 64 of them see the whole tile, [LONG][128] the part of
+// it that each sees, [LONG][2][128] -lse and -delta.
+template <int DP>
+struct DkvLayout : Layout<DP, DP == 128 ? 2 : 4, DP == 128 ? 2 : 4> {
+    static constexpr int FULL = DkvLayout::SLOT + 8, SEEN = (FULL + DkvLayout::LONG * 8 + 15) / 16 * 16, INFO = SEEN + DkvLayout::LONG * kTile * 2;
+    static constexpr int BYTES = INFO + DkvLayout::LONG * 2 * kTile * 4;
 };
 
 __device__ __forceinline__ void setup_common(uint32_t *tmem_slot, int warp)
@@ -204,11 +217,11 @@ __device__ __forceinline__ void put32(const float *o, int c, int dim, float by, 
 
 // Tensor memory: S 128 columns, dP twice 128 (dS over each), dQ.
 template <int DP>
-__global__ __launch_bounds__(kThreads, 1) void cross_dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_d,
+__global__ __launch_bounds__(kDqThreads, 1) void cross_dq_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_d,
                                                                const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                                                                const __grid_constant__ CrossArgs a, const __grid_constant__ Plan p)
 {
-    using L = Layout<DP>;
+    using L = DqLayout<DP>;
     extern __shared__ __align__(1024) unsigned char cross_mem_aligned[];
     unsigned char *mem = cross_mem_aligned;
     const uint32_t base = smem_addr(mem);
@@ -220,7 +233,7 @@ __global__ __launch_bounds__(kThreads, 1) void cross_dq_kernel(const __grid_cons
     Item *items = reinterpret_cast<Item *>(mem + L::ITEMS);
     const uint32_t bars = base + L::BARS;
     const uint32_t q_full = bars, q_empty = bars + 8, o_free = bars + 16, s_full = bars + 24, s_read = bars + 32, done = bars + 40;
-    const uint32_t dp_full = bars + 48, ds_ready = bars + 64;       // two each: of either buffer
+    const uint32_t dp_full = bars + 48, ds_ready = bars + 64, ds_free = base + L::DS_FREE;     // two each: of either buffer
     const uint32_t kv_full = bars + 80, kv_empty = kv_full + 8 * L::STAGES, k_ok = kv_empty + 8 * L::STAGES;
     const int warp = warp_index(), lane = threadIdx.x & 31, group = a.Hq / a.heads;
     if (threadIdx.x == 0) {
@@ -233,17 +246,18 @@ __global__ __launch_bounds__(kThreads, 1) void cross_dq_kernel(const __grid_cons
         for (int s = 0; s < 2; ++s) {
             mbar_init(dp_full + 8 * s, 1);
             mbar_init(ds_ready + 8 * s, 8);
+            mbar_init(ds_free + 8 * s, 1);
         }
         for (int s = 0; s < L::STAGES; ++s) {
             mbar_init(kv_full + 8 * s, 1);
             mbar_init(kv_empty + 8 * s, 1);
-            mbar_init(k_ok + 8 * s, 2);
+            mbar_init(k_ok + 8 * s, 4);
         }
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     setup_common(tmem_slot, warp);
     if (p.chunk_rows < kTile)       // rows that no copy fills are zeros
-        for (int i = threadIdx.x; i < 2 * L::TILE / 16; i += kThreads)
+        for (int i = threadIdx.x; i < 2 * L::TILE / 16; i += kDqThreads)
             reinterpret_cast<uint4 *>(mem + L::FIX)[i] = make_uint4(0u, 0u, 0u, 0u);
     fence_proxy_async_smem();
     __syncthreads();
@@ -263,7 +277,9 @@ __global__ __launch_bounds__(kThreads, 1) void cross_dq_kernel(const __grid_cons
     Piece u;
     bool ok = true;
 
-    if (warp < 4) {
+    // registers: 256 x 56 + 256 x 200 = 512 x 128
+    if (warp < 4 || warp >= 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         if (warp == 0) {                // copies
             int at = 0, last = 0;
             for (int units = 0; ok && share.next(u); ++units) {
@@ -289,57 +305,62 @@ __global__ __launch_bounds__(kThreads, 1) void cross_dq_kernel(const __grid_cons
             ok &= landed<L>(kv_full, last);
             if (lane == 0)
                 p.cuts[blockIdx.x] = cut_of(share, u, at > 0, a.heads, p.ctas);
-        } else if (warp == 1) {         // products
+        } else if (warp == 1) {         // S and dP
             const int ksteps = (a.dim + 15) / 16;
-            const uint32_t id_s = idesc_cols(kTile) | (p.negative ? kNegateA : 0u), id_p = idesc_cols(kTile), id_o = idesc_rows(ksteps * 16);
-            int jobs = 0;
+            const uint32_t id_s = idesc_cols(kTile) | (p.negative ? kNegateA : 0u), id_p = idesc_cols(kTile);
+            int job = 0;
             for (int units = 0; ok && share.next(u); ++units) {
                 if (!(ok = tc::warp_wait(q_full, units & 1)))
                     break;
-                for (int j = 0; ok && j <= u.n; ++j) {
-                    if (j < u.n) {
-                        const int job = jobs + j, ks = L::place(job, 0), vs = L::place(job, 1);
-                        if (!(ok = tc::warp_wait(k_ok + 8 * ks, L::lap(job, 0) & 1)))
-                            break;
-                        if (job > 0 && !(ok = tc::warp_wait(s_read, (job - 1) & 1)))
-                            break;
-                        tc::tc_fence_after();
-                        for (int kk = 0; kk < ksteps; ++kk) {
-                            const uint32_t off = (kk >> 2) * (kTile * 128) + (kk & 3) * 32;
-                            tc::mma_bf16_elect(tmem, tc::sw128_desc(base + L::FIX + off), tc::sw128_desc(base + L::RING + ks * L::TILE + off), id_s, kk > 0);
-                        }
-                        tc::mma_commit_elect(s_full);
-                        if (!(ok = tc::warp_wait(k_ok + 8 * vs, L::lap(job, 1) & 1)))
-                            break;
-                        tc::tc_fence_after();
-                        for (int kk = 0; kk < ksteps; ++kk) {
-                            const uint32_t off = (kk >> 2) * (kTile * 128) + (kk & 3) * 32;
-                            tc::mma_bf16_elect(tmem + 128 + (job & 1) * 128, tc::sw128_desc(base + L::FIX + L::TILE + off),
-                                               tc::sw128_desc(base + L::RING + vs * L::TILE + off), id_p, kk > 0);
-                        }
-                        tc::mma_commit_elect(dp_full + 8 * (job & 1));
-                        tc::mma_commit_elect(kv_empty + 8 * vs);
-                        if (j == u.n - 1)
-                            tc::mma_commit_elect(q_empty);
+                for (int j = 0; ok && j < u.n; ++j, ++job) {
+                    const int ks = L::place(job, 0), vs = L::place(job, 1);
+                    if (!(ok = tc::warp_wait(k_ok + 8 * ks, L::lap(job, 0) & 1)))
+                        break;
+                    if (job > 0 && !(ok = tc::warp_wait(s_read, (job - 1) & 1)))
+                        break;
+                    tc::tc_fence_after();
+                    for (int kk = 0; kk < ksteps; ++kk) {
+                        const uint32_t off = (kk >> 2) * (kTile * 128) + (kk & 3) * 32;
+                        tc::mma_bf16_elect(tmem, tc::sw128_desc(base + L::FIX + off), tc::sw128_desc(base + L::RING + ks * L::TILE + off), id_s, kk > 0);
                     }
-                    if (j > 0) {
-                        const int job = jobs + j - 1, ks = L::place(job, 0);
-                        if (j == 1 && units > 0 && !(ok = tc::warp_wait(o_free, (units - 1) & 1)))
-                            break;
-                        if (!(ok = tc::warp_wait(ds_ready + 8 * (job & 1), (job >> 1) & 1)))
-                            break;
-                        tc::tc_fence_after();
-                        for (int kk = 0; kk < kTile / 16; ++kk)
-                            mma_tmem_a_elect(tmem + 384, tmem + 128 + (job & 1) * 128 + (kk >> 2) * 64 + (kk & 3) * 8,
-                                             rows_desc(base + L::RING + ks * L::TILE + kk * 2048, kTile * 128), id_o, j > 1 || kk > 0);
-                        tc::mma_commit_elect(kv_empty + 8 * ks);
-                        if (j == u.n)
-                            tc::mma_commit_elect(done);
+                    tc::mma_commit_elect(s_full);
+                    if (!(ok = tc::warp_wait(k_ok + 8 * vs, L::lap(job, 1) & 1)))
+                        break;
+                    if (job > 1 && !(ok = tc::warp_wait(ds_free + 8 * (job & 1), ((job >> 1) - 1) & 1)))
+                        break;
+                    tc::tc_fence_after();
+                    for (int kk = 0; kk < ksteps; ++kk) {
+                        const uint32_t off = (kk >> 2) * (kTile * 128) + (kk & 3) * 32;
+                        tc::mma_bf16_elect(tmem + 128 + (job & 1) * 128, tc::sw128_desc(base + L::FIX + L::TILE + off),
+                                           tc::sw128_desc(base + L::RING + vs * L::TILE + off), id_p, kk > 0);
                     }
+                    tc::mma_commit_elect(dp_full + 8 * (job & 1));
+                    tc::mma_commit_elect(kv_empty + 8 * vs);
+                    if (j == u.n - 1)
+                        tc::mma_commit_elect(q_empty);
                 }
-                jobs += u.n;
             }
-        } else if (warp < 4) {          // looks the keys over
+        } else if (warp == 2) {         // dQ
+            const uint32_t id_o = idesc_rows((a.dim + 15) / 16 * 16);
+            int job = 0;
+            for (int units = 0; ok && share.next(u); ++units) {
+                if (units > 0 && !(ok = tc::warp_wait(o_free, (units - 1) & 1)))
+                    break;
+                for (int j = 0; ok && j < u.n; ++j, ++job) {
+                    const int ks = L::place(job, 0);
+                    if (!(ok = tc::warp_wait(ds_ready + 8 * (job & 1), (job >> 1) & 1)))
+                        break;
+                    tc::tc_fence_after();
+                    for (int kk = 0; kk < kTile / 16; ++kk)
+                        mma_tmem_a_elect(tmem + 384, tmem + 128 + (job & 1) * 128 + (kk >> 2) * 64 + (kk & 3) * 8,
+                                         rows_desc(base + L::RING + ks * L::TILE + kk * 2048, kTile * 128), id_o, j > 0 || kk > 0);
+                    tc::mma_commit_elect(kv_empty + 8 * ks);
+                    tc::mma_commit_elect(ds_free + 8 * (job & 1));
+                    if (j == u.n - 1)
+                        tc::mma_commit_elect(done);
+                }
+            }
+        } else if (warp >= 12) {        // looks the keys over
             int at = 0;
             while (ok && share.next(u)) {
                 const int t0 = (p.first + u.tile) * p.tokens_a_tile;
@@ -357,9 +378,8 @@ __global__ __launch_bounds__(kThreads, 1) void cross_dq_kernel(const __grid_cons
                         break;
                     if (!(i & 1) && (c0 < lo || c0 + kTile > hi)) {
                         const uint32_t tile = base + L::RING + st * L::TILE;
-                        for (int r = (warp - 2) * 32 + lane; r < kTile; r += 64) {
-                            if (!bad_row<DP>(tile, r))
-                                continue;
+                        const int r = (warp - 12) * 32 + lane;
+                        if (bad_row<DP>(tile, r)) {
                             bool seen = false;
                             for (int y = 0; y < p.tokens_a_tile && t0 + y < a.T; ++y) {
                                 const int2 see = span_of(a.spans, a.S, t0 + y, nullptr);
@@ -378,6 +398,7 @@ __global__ __launch_bounds__(kThreads, 1) void cross_dq_kernel(const __grid_cons
             }
         }
     } else {                        // softmax: a row a thread, 64 columns a group of warps
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         const int half = (warp - 4) >> 2, row = threadIdx.x & 127;
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
         const float scale = fmaxf(fabsf(a.scale) * kLog2e, 1e-30f);
@@ -473,7 +494,7 @@ __global__ __launch_bounds__(kThreads, 1) void cross_dkv_kernel(const __grid_con
                                                                 const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                                                                 const __grid_constant__ CrossArgs a, const __grid_constant__ Plan p)
 {
-    using L = Layout<DP>;
+    using L = DkvLayout<DP>;
     extern __shared__ __align__(1024) unsigned char cross_mem_aligned[];
     unsigned char *mem = cross_mem_aligned;
     const uint32_t base = smem_addr(mem);
@@ -655,17 +676,16 @@ __global__ __launch_bounds__(kThreads, 1) void cross_dkv_kernel(const __grid_con
                                     clear_row<DP>(base + L::RING + st * L::TILE, row + 32 * y);
                             fence_proxy_async_smem();
                         }
-                        // the softmax step before has read its own
-                        if (v > 0 && !(ok = tc::warp_wait(s ? ds_ready : p_ready, (v - 1) & 1)))
-                            break;
+                        if (s == 0) {       // the tile before in this place is done with: its copy has begun anew
 #pragma unroll
-                        for (int y = 0; y < 2; ++y) {
-                            known[s * kTile + row + 32 * y] = info[y][s];
-                            if (s == 0)
-                                seen[row + 32 * y] = (uint16_t)(lo[y] | n[y] << 8);
+                            for (int y = 0; y < 2; ++y) {
+                                known[st * 2 * kTile + row + 32 * y] = info[y][0];
+                                known[(st * 2 + 1) * kTile + row + 32 * y] = info[y][1];
+                                seen[st * kTile + row + 32 * y] = (uint16_t)(lo[y] | n[y] << 8);
+                            }
+                            if (lane == 0)
+                                reinterpret_cast<int *>(mem + L::FULL)[st * 2 + warp - 2] = all;
                         }
-                        if (s == 0 && lane == 0)
-                            reinterpret_cast<int *>(mem + L::FULL)[st * 2 + warp - 2] = all;
                         __syncwarp();
                         if (lane == 0)
                             tc::mbar_arrive(q_ok + 8 * st);
@@ -686,10 +706,11 @@ __global__ __launch_bounds__(kThreads, 1) void cross_dkv_kernel(const __grid_con
                 if (!(ok = tc::warp_wait(s_full, jobs & 1)))
                     break;
                 tc::tc_fence_after();
-                const uint32_t info = base + L::INFO + 64 * half * 4, seen = base + L::SEEN + 64 * half * 2;
-                const int *full = reinterpret_cast<const int *>(mem + L::FULL) + L::place(jobs, 0) * 2;
+                const int place = L::place(jobs, 0);
+                const uint32_t info = base + L::INFO + (place * 2 * kTile + 64 * half) * 4, seen = base + L::SEEN + (place * kTile + 64 * half) * 2;
+                const int *full = reinterpret_cast<const int *>(mem + L::FULL) + place * 2;
                 const bool whole = uniform(full[half]) != 0;
-                float x[64], y[32];
+                float x[64], y[64];
                 uint32_t w[32];
                 tmem_ld32(sc, x);
                 tmem_ld32(sc + 32, x + 32);
@@ -725,24 +746,25 @@ __global__ __launch_bounds__(kThreads, 1) void cross_dkv_kernel(const __grid_con
                 if (!(ok = tc::warp_wait(dp_full, jobs & 1)))
                     break;
                 tc::tc_fence_after();
+                tmem_ld32(dp, y);
+                tmem_ld32(dp + 32, y + 32);
+                tmem_wait_ld();
 #pragma unroll
-                for (int b = 0; b < 64; b += 32) {
-                    tmem_ld32(dp + b, y);
-                    tmem_wait_ld();
+                for (int c = 0; c < 64; c += 4) {
+                    const uint4 l = lds_v4(info + (kTile + c) * 4);
+                    const float2 e = add2(make_float2(y[c], y[c + 1]), make_float2(__uint_as_float(l.x), __uint_as_float(l.y)));
+                    const float2 f = add2(make_float2(y[c + 2], y[c + 3]), make_float2(__uint_as_float(l.z), __uint_as_float(l.w)));
+                    y[c] = e.x, y[c + 1] = e.y, y[c + 2] = f.x, y[c + 3] = f.y;
+                }
+                if (!whole) {       // not 0 times what an unseen value gives
 #pragma unroll
-                    for (int c = 0; c < 32; c += 4) {
-                        const uint4 l = lds_v4(info + (kTile + b + c) * 4);
-                        float2 e = add2(make_float2(y[c], y[c + 1]), make_float2(__uint_as_float(l.x), __uint_as_float(l.y)));
-                        float2 f = add2(make_float2(y[c + 2], y[c + 3]), make_float2(__uint_as_float(l.z), __uint_as_float(l.w)));
-                        if (!whole) {       // not 0 times what an unseen value gives
-                            e = make_float2(x[b + c] == 0.0f ? 0.0f : e.x, x[b + c + 1] == 0.0f ? 0.0f : e.y);
-                            f = make_float2(x[b + c + 2] == 0.0f ? 0.0f : f.x, x[b + c + 3] == 0.0f ? 0.0f : f.y);
-                        }
-                        e = mul2(make_float2(x[b + c], x[b + c + 1]), e);
-                        f = mul2(make_float2(x[b + c + 2], x[b + c + 3]), f);
-                        w[(b + c) / 2] = pack2(e.x, e.y);
-                        w[(b + c) / 2 + 1] = pack2(f.x, f.y);
-                    }
+                    for (int c = 0; c < 64; ++c)
+                        y[c] = x[c] == 0.0f ? 0.0f : y[c];
+                }
+#pragma unroll
+                for (int c = 0; c < 32; ++c) {
+                    const float2 g = mul2(make_float2(x[2 * c], x[2 * c + 1]), make_float2(y[2 * c], y[2 * c + 1]));
+                    w[c] = pack2(g.x, g.y);
                 }
                 tmem_st32(dp, w);
                 tmem_wait_st();
@@ -852,8 +874,9 @@ Plan plan_of(int64_t T, int64_t Hq, int64_t heads, int DP, size_t *bytes)
 template <int DP>
 cudaError_t launch(const CrossArgs &a, cudaStream_t stream)
 {
-    using L = Layout<DP>;
-    static_assert(L::DKV_BYTES <= 232448 && L::BARS % 8 == 0 && L::INFO % 16 == 0, "shared memory");
+    using Lq = DqLayout<DP>;
+    using L = DkvLayout<DP>;
+    static_assert(Lq::BYTES <= 232448 && L::BYTES <= 232448 && L::BARS % 8 == 0 && L::INFO % 16 == 0, "shared memory");
     size_t bytes;
     Plan p = plan_of(a.T, a.Hq, a.heads, DP, &bytes);
     char *ws = static_cast<char *>(a.ws);
@@ -872,21 +895,21 @@ cudaError_t launch(const CrossArgs &a, cudaStream_t stream)
         e = row_map(&mv, a.v, a.S, a.heads, a.dim, a.vs, 1, kTile);
     static std::atomic<unsigned long long> allowed_q, allowed_kv;
     if (e == cudaSuccess)
-        e = tc::allow_smem(cross_dq_kernel<DP>, L::DQ_BYTES, allowed_q);
+        e = tc::allow_smem(cross_dq_kernel<DP>, Lq::BYTES, allowed_q);
     if (e == cudaSuccess)
-        e = tc::allow_smem(cross_dkv_kernel<DP>, L::DKV_BYTES, allowed_kv);
+        e = tc::allow_smem(cross_dkv_kernel<DP>, L::BYTES, allowed_kv);
     if (e == cudaSuccess)
         e = tc::launch_pdl(cross_ready_kernel, dim3(p.q_tiles, a.heads, kTile / kReadyRows), dim3(256), 0, stream, a, p);
     const int tiles = (a.S + kTile - 1) / kTile, most_q = most_tiles(a.heads, tiles, kMostTiles), most_kv = most_tiles(a.heads, p.q_tiles, kMostTiles);
     for (p.first = 0; e == cudaSuccess && p.first < p.q_tiles; p.first += most_q) {
         p.tiles = p.q_tiles - p.first < most_q ? p.q_tiles - p.first : most_q;
-        e = tc::launch_pdl(cross_dq_kernel<DP>, dim3(p.ctas), dim3(kThreads), L::DQ_BYTES, stream, mq, md, mk, mv, a, p);
+        e = tc::launch_pdl(cross_dq_kernel<DP>, dim3(p.ctas), dim3(kDqThreads), Lq::BYTES, stream, mq, md, mk, mv, a, p);
         if (e == cudaSuccess)
             e = tc::launch_pdl(cross_add_kernel<DP, false>, dim3(p.ctas, (p.rows + kJoinRows - 1) / kJoinRows), dim3(kJoinWarps * 32), 0, stream, a, p);
     }
     for (p.first = 0; e == cudaSuccess && p.first < tiles; p.first += most_kv) {
         p.tiles = tiles - p.first < most_kv ? tiles - p.first : most_kv;
-        e = tc::launch_pdl(cross_dkv_kernel<DP>, dim3(p.ctas), dim3(kThreads), L::DKV_BYTES, stream, mq, md, mk, mv, a, p);
+        e = tc::launch_pdl(cross_dkv_kernel<DP>, dim3(p.ctas), dim3(kThreads), L::BYTES, stream, mq, md, mk, mv, a, p);
         if (e == cudaSuccess)
             e = tc::launch_pdl(cross_add_kernel<DP, true>, dim3(p.ctas, 2 * kTile / kJoinRows), dim3(kJoinWarps * 32), 0, stream, a, p);
     }
