@@ -9,7 +9,12 @@ attention blocks are gated (through tanh), as cross-attention blocks of vision
 decoders are.  Half way, every sequence is forked into two continuations, the first
 ones are released, and the cache is compacted.
 
-    python examples/decode.py [--layers 4] [--steps 32] [--int8-cache] ...
+With --images, every second layer attends to the states of its sequence's image instead of
+the text: their keys (each head normed) and values are made once, and forked sequences share
+them.  --head-norms norms the heads of the other layers in front of their rotation.  With
+--temperature the next tokens are drawn, from the --top-k first ones and the share --top-p.
+
+    python examples/decode.py [--layers 4] [--steps 32] [--int8-cache] [--images 1601] ...
 """
 import argparse
 import os
@@ -35,7 +40,8 @@ def _linear(gen, n, k):
 
 
 class Decoder:
-    def __init__(self, layers=2, hidden=512, heads=8, kv_heads=2, dim=64, mlp=1024, vocab=1000, seed=0):
+    def __init__(self, layers=2, hidden=512, heads=8, kv_heads=2, dim=64, mlp=1024, vocab=1000, seed=0,
+                 images=False, head_norms=False):
         gen = torch.Generator(device="cuda").manual_seed(seed)
         self.heads, self.kv_heads, self.dim = heads, kv_heads, dim
         norm = lambda: (1 + 0.1 * torch.randn(hidden, generator=gen, device="cuda")).to(BF)  # noqa: E731
@@ -47,6 +53,20 @@ class Decoder:
                             attn_gate=torch.randn(1, generator=gen, device="cuda").add_(1).to(BF))
                        for _ in range(layers)]
         self.final_norm, self.head = norm(), _linear(gen, vocab, hidden)
+        self.crossing = [bool(images) and i % 2 == 1 for i in range(layers)]     # layers that attend to an image
+        for w, crosses in zip(self.layers, self.crossing):
+            for name in ("q_norm", "k_norm"):
+                w[name] = (1 + 0.1 * torch.randn(dim, generator=gen, device="cuda")).to(BF) \
+                    if crosses or head_norms else None
+
+    def look(self, states, ops=s3d8):
+        """Keys and values of image states [S, hidden] for each layer that attends to them."""
+        x = s3d8.quantize_act(states)
+        made = []
+        for w in (w for w, crosses in zip(self.layers, self.crossing) if crosses):
+            k, v = (t.view(states.shape[0], -1, self.dim) for t in _project(x, w["k"], w["v"]))
+            made.append((ops.norm_rope(k, q_norm=w["k_norm"])[0], v))
+        return made
 
     def angles(self, length):
         freq = 10000.0 ** (-torch.arange(0, self.dim, 2, device="cuda") / self.dim)
@@ -62,17 +82,25 @@ def _project(x, *weights):
     return [s3d8.linear(w["packed"], w["centroids"], w["chan_scale"], xq, xs, w["N"]) for w in weights]
 
 
-def step(model, tokens, positions, rows, pool, table, lens, cos, sin, ops=s3d8, workspace=None):
+def step(model, tokens, positions, rows, pool, table, lens, cos, sin, ops=s3d8, workspace=None, images=(), spans=None):
     """Logits of one new token per sequence, whose keys and values go to `positions`
-    of the block table's `rows`; `lens` counts the tokens with the new one."""
+    of the block table's `rows`; `lens` counts the tokens with the new one.  `images`:
+    what look() made; `spans`: each token's states of them."""
     h = model.embed[tokens]
     n, norms = h.shape[0], [w["attn_norm"] for w in model.layers[1:]] + [model.final_norm]
     _, *x = ops.residual_norm_quant(h, w_pre=model.layers[0]["attn_norm"])
-    for w, cache, next_norm in zip(model.layers, pool.caches, norms):
-        q, k, v = _project(x, w["q"], w["k"], w["v"])
-        q, k, v = (t.view(n, -1, model.dim) for t in (q, k, v))
-        q = ops.rope_append(q, k, v, cos, sin, positions, cache, table, rows=rows)
-        a = ops.paged_attention(q, cache, table[rows.long()], lens, workspace=workspace)
+    caches, images = iter(pool.caches), iter(images)
+    for w, crosses, next_norm in zip(model.layers, model.crossing, norms):
+        if crosses:
+            (q,) = _project(x, w["q"])
+            q, _ = ops.norm_rope(q.view(n, -1, model.dim), q_norm=w["q_norm"])
+            a = ops.cross_attention(q, *next(images), spans)
+        else:
+            q, k, v = _project(x, w["q"], w["k"], w["v"])
+            q, k, v = (t.view(n, -1, model.dim) for t in (q, k, v))
+            cache, normed = next(caches), {} if w["q_norm"] is None else dict(q_norm=w["q_norm"], k_norm=w["k_norm"])
+            q = ops.rope_append(q, k, v, cos, sin, positions, cache, table, rows=rows, **normed)
+            a = ops.paged_attention(q, cache, table[rows.long()], lens, workspace=workspace)
         (o,) = _project(s3d8.quantize_act(a.view(n, -1)), w["o"])
         h, *x = ops.residual_norm_quant(h, o, gate=w["attn_gate"], tanh_gate=True, w_pre=w["mlp_norm"])
         gate, up = _project(x, w["gate"], w["up"])
@@ -84,18 +112,24 @@ def step(model, tokens, positions, rows, pool, table, lens, cos, sin, ops=s3d8, 
 
 
 class Server:
-    """Sequences in rows of one block table over the caches of all layers."""
+    """Sequences in rows of one block table over the caches of all layers that have one."""
 
     def __init__(self, model, pages=256, page=16, rows=16, width=16, dtype=BF):
         self.model, self.page = model, page
         self.pool = s3d8.KVPool([s3d8.KVCache.empty(pages, page, model.kv_heads, model.dim, dtype)
-                                 for _ in model.layers])
+                                 for crosses in model.crossing if not crosses])
+        self.images, self.spans = (), torch.zeros((rows, 2), dtype=torch.int32, device="cuda")
         self.table = torch.full((rows, width), -1, dtype=torch.int32, device="cuda")
         self.lens = torch.zeros(rows, dtype=torch.int32, device="cuda")
         self.refs = torch.zeros(pages, dtype=torch.int32, device="cuda")
         self.space = s3d8.pages_workspace(self.pool, rows)
         self.attention = s3d8.paged_attention_workspace(self.pool.caches[0], rows, model.heads)
         self.cos, self.sin = model.angles(width * page)
+
+    def show(self, states, rows, spans, ops=s3d8):
+        """The states [S, hidden] of all images, and the ones that each row's sequence sees."""
+        self.images = self.model.look(states, ops)
+        self.spans[rows.long()] = spans
 
     def feed(self, rows, tokens, ops=s3d8):
         """One more token in each row (int32); the logits behind them."""
@@ -105,9 +139,10 @@ class Server:
         # a sequence that found no page waits: a padding token, of an empty sequence
         positions = torch.where(got > 0, lens - 1, -1)
         return step(self.model, tokens, positions, rows, self.pool, self.table, torch.where(got > 0, lens, 0),
-                    self.cos, self.sin, ops, self.attention)
+                    self.cos, self.sin, ops, self.attention, self.images, self.spans[rows.long()])
 
     def fork(self, parents, children):
+        self.spans[children.long()] = self.spans[parents.long()]
         return s3d8.fork_pages(self.pool, self.table, self.lens, self.refs, parents, children, workspace=self.space)
 
     def free(self, rows):
@@ -117,12 +152,17 @@ class Server:
         return s3d8.compact_pages(self.pool, self.table, self.refs, workspace=self.space)
 
 
-def serve(model, prompts, steps, dtype=BF, compact=True, ops=s3d8, **sizes):
+def serve(model, prompts, steps, dtype=BF, compact=True, ops=s3d8, states=None, spans=None, limits=None, seed=0, **sizes):
     """Read prompts [n, length], continue each for `steps` tokens; half way the
-    sequences move to forked rows.  Returns the tokens and the last logits."""
+    sequences move to forked rows.  `states` [S, hidden] and `spans` [n, 2]: the images.
+    `limits`: temperature, top_k, ... of sample(), [n] each; None takes the likeliest token.
+    Returns the tokens and the last logits."""
     n = prompts.shape[0]
     server = Server(model, rows=2 * n, dtype=dtype, **sizes)
     rows = torch.arange(n, dtype=torch.int32, device="cuda")
+    if states is not None:
+        server.show(states, rows, spans, ops)
+    gen = torch.Generator(device="cuda").manual_seed(seed)
     for t in range(prompts.shape[1]):
         logits = server.feed(rows, prompts[:, t], ops)
     out = []
@@ -134,7 +174,10 @@ def serve(model, prompts, steps, dtype=BF, compact=True, ops=s3d8, **sizes):
             if compact:
                 server.compact()
             rows = children
-        out.append(logits.float().argmax(-1))
+        if limits is None:
+            out.append(logits.float().argmax(-1))
+        else:
+            out.append(ops.sample(logits, torch.rand(n, generator=gen, device="cuda"), **limits).long())
         logits = server.feed(rows, out[-1], ops)
     return torch.stack(out, 1), logits
 
@@ -145,17 +188,32 @@ def main():
                         ("mlp", 14336), ("vocab", 32000), ("sequences", 4), ("prompt", 32), ("steps", 32)):
         p.add_argument("--" + name, type=int, default=value)
     p.add_argument("--int8-cache", action="store_true")
+    p.add_argument("--images", type=int, default=0, metavar="STATES", help="one image of so many states a sequence")
+    p.add_argument("--head-norms", action="store_true")
+    p.add_argument("--temperature", type=float)
+    p.add_argument("--top-k", type=int, default=0)
+    p.add_argument("--top-p", type=float, default=1.0)
     a = p.parse_args()
     s3d8.load(build_if_missing=True)
-    model = Decoder(a.layers, a.hidden, a.heads, a.kv_heads, a.dim, a.mlp, a.vocab)
+    model = Decoder(a.layers, a.hidden, a.heads, a.kv_heads, a.dim, a.mlp, a.vocab,
+                    images=a.images > 0, head_norms=a.head_norms)
     gen = torch.Generator(device="cuda").manual_seed(1)
     prompts = torch.randint(0, a.vocab, (a.sequences, a.prompt), device="cuda", generator=gen)
     dtype = torch.int8 if a.int8_cache else BF
     width = -(-(a.prompt + a.steps) // 16)
-    serve(model, prompts, a.steps, dtype, width=width)
+    more = dict(width=width)
+    if a.images:
+        first = torch.arange(a.sequences, dtype=torch.int32, device="cuda") * a.images
+        more.update(states=torch.randn((a.sequences * a.images, a.hidden), generator=gen, device="cuda").to(BF),
+                    spans=torch.stack((first, first + a.images), -1))
+    if a.temperature is not None:
+        each = lambda x, t: torch.full((a.sequences,), x, dtype=t, device="cuda")  # noqa: E731
+        more["limits"] = dict(temperature=each(a.temperature, torch.float32), top_k=each(a.top_k, torch.int32),
+                              top_p=each(a.top_p, torch.float32))
+    serve(model, prompts, a.steps, dtype, **more)
     torch.cuda.synchronize()
     begin = time.perf_counter()
-    tokens, _ = serve(model, prompts, a.steps, dtype, width=width)
+    tokens, _ = serve(model, prompts, a.steps, dtype, **more)
     torch.cuda.synchronize()
     took = time.perf_counter() - begin
     if s3d8.device_status() != 0:

@@ -4,6 +4,10 @@ the encoder's states of their images, and the next token of each sequence.
 As the rest of the binding, this module checks tensors and passes pointers and the
 current stream; the work is in the CUDA library (``include/s3d8.h`` holds the formulas,
 layouts and errors).
+
+NormRope and CrossAttention may be captured into a CUDA graph with their backward pass, while
+no eager autograd graph of the same leaves is alive: autograd joins that graph's stream to the
+captured one, which CUDA refuses.
 """
 from __future__ import annotations
 
