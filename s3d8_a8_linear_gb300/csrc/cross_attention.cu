@@ -36,7 +36,8 @@ namespace {
 using namespace cross;
 
 constexpr int kThreads = 512;
-constexpr int kMostTiles = 1024;        // query tiles of a launch
+constexpr int kMostTiles = 512;         // query tiles of a launch
+constexpr int kRuns = 1536;             // runs of states of all items, and their ends
 constexpr int kJoinWarps = 8, kJoinRows = 32;
 
 constexpr int kNoTile = 0xFFFF;         // of the two query tiles of a piece, low and high half of its `tile`
@@ -56,10 +57,11 @@ struct Layout {
     static constexpr int TILE = kTile * DP * 2;             // bytes of a tile of Q, K or V
     static constexpr int STAGES = DP == 128 ? 4 : 8;
     static constexpr int Q = 0, KV = 2 * TILE, ITEMS = KV + STAGES * TILE;
-    static constexpr int RANGES = ITEMS + ((kMostTiles + 1) * (int)sizeof(Item) + 15) / 16 * 16;     // of the query tiles, while the list is made
-    static constexpr int BAD = RANGES + kMostTiles * 8;     // [2][128][8]: columns of +inf, of -inf
+    static constexpr int RUNS = ITEMS + ((kMostTiles + 1) * (int)sizeof(Item) + 15) / 16 * 16;   // at first the query tiles' ranges
+    static constexpr int BAD = RUNS + kRuns * (int)sizeof(Run);     // [2][128][8]: columns of +inf, of -inf
     static constexpr int TOPS = BAD + 2 * 128 * 32;         // [128] maximum and sum of the second chain
     static constexpr int BARS = TOPS + 128 * 8;
+    static constexpr int PLACES = BARS + 384;               // [STAGES]: the first state of the visits whose copies were issued last
     static constexpr int BYTES = 1024 + BARS + 512;
 };
 
@@ -79,11 +81,11 @@ __device__ __forceinline__ bool next_unit(Share &share, Unit &u)
     return true;
 }
 
-// The list of work: for each pair of query tiles whether they go together.  One warp.
+// The list of items: for each pair of query tiles whether they go together.  One warp.
 __device__ __forceinline__ int make_items(const int2 *ranges, int tiles, Item *items)
 {
     const int lane = threadIdx.x & 31;
-    int count = 0, begin = 0;
+    int count = 0;
     auto span = [&](int t, int &j0, int &j1) {      // state tiles; one (of which nothing is seen) for an empty span
         const int2 r = ranges[t];
         j0 = r.x < r.y ? r.x / kTile : 0;
@@ -91,7 +93,7 @@ __device__ __forceinline__ int make_items(const int2 *ranges, int tiles, Item *i
     };
     for (int base = 0; base < (tiles + 1) / 2; base += 32) {
         const int a = 2 * (base + lane), b = a + 1;
-        int n = 0, a0 = 0, a1 = 0, b0 = 0, b1 = 0;
+        int n = 0, a0 = 0, a1 = 0, b0 = 0, b1 = 0;      // (the gaps of their spans counted in)
         bool pair = false;
         if (a < tiles) {
             n = 1;
@@ -101,30 +103,45 @@ __device__ __forceinline__ int make_items(const int2 *ranges, int tiles, Item *i
                 // together, both chains pass the states of either
                 const int u0 = min(a0, b0), u1 = max(a1, b1);
                 pair = 8 * (u1 - u0) <= 5 * (a1 - a0 + b1 - b0) + 8;
-                if (pair)
-                    a0 = u0, a1 = u1;
-                else
-                    n = 2;
+                n = pair ? 1 : 2;
             }
         }
-        const int size = n ? a1 - a0 + (n == 2 ? b1 - b0 : 0) : 0;
-        int c = n, s = size;
+        int c = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const int pc = __shfl_up_sync(0xffffffffu, c, o), ps = __shfl_up_sync(0xffffffffu, s, o);
+            const int pc = __shfl_up_sync(0xffffffffu, c, o);
             if (lane >= o)
-                c += pc, s += ps;
+                c += pc;
         }
         if (n)
-            items[count + c - n] = {a | (pair ? b : kNoTile) << 16, a0, begin + s - size};
+            items[count + c - n] = {a | (pair ? b : kNoTile) << 16, 0, 0};
         if (n == 2)
-            items[count + c - 1] = {b | kNoTile << 16, b0, begin + s - (b1 - b0)};
+            items[count + c - 1] = {b | kNoTile << 16, 0, 0};
         count += __shfl_sync(0xffffffffu, c, 31);
-        begin += __shfl_sync(0xffffffffu, s, 31);
+    }
+    return count;
+}
+
+// From the items' sizes (in `begin`) what lies in front of each.  One warp.
+__device__ __forceinline__ void add_up(Item *items, int n)
+{
+    const int lane = threadIdx.x & 31;
+    int sum = 0;
+    for (int base = 0; base < n; base += 32) {
+        const int size = base + lane < n ? items[base + lane].begin : 0;
+        int s = size;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int ps = __shfl_up_sync(0xffffffffu, s, o);
+            if (lane >= o)
+                s += ps;
+        }
+        if (base + lane < n)
+            items[base + lane].begin = sum + s - size;
+        sum += __shfl_sync(0xffffffffu, s, 31);
     }
     if (lane == 0)
-        items[count] = {0, 0, begin};
-    return count;
+        items[n] = {0, 0, sum};
 }
 
 // Scores of columns outside from .. from + n - 1: -inf.
@@ -209,9 +226,11 @@ __global__ __launch_bounds__(kThreads, 1) void cross_forward_kernel(const __grid
     const uint32_t base = (smem_addr(cross_mem) + 1023u) & ~1023u;
     unsigned char *mem = cross_mem + (base - smem_addr(cross_mem));
     Item *items = reinterpret_cast<Item *>(mem + L::ITEMS);
-    int2 *ranges = reinterpret_cast<int2 *>(mem + L::RANGES);
+    int2 *ranges = reinterpret_cast<int2 *>(mem + L::RUNS);
+    Run *runs = reinterpret_cast<Run *>(mem + L::RUNS);
     uint32_t *bad = reinterpret_cast<uint32_t *>(mem + L::BAD);
     float2 *tops = reinterpret_cast<float2 *>(mem + L::TOPS);
+    volatile int *places = reinterpret_cast<int *>(mem + L::PLACES);
     const uint32_t bars = base + L::BARS;
     const uint32_t q_full = bars, q_empty = bars + 8, o_free = bars + 16, s_full = bars + 24, p_ready = bars + 40, pv_done = bars + 56, p_half = bars + 72;
     const uint32_t kv_full = bars + 88, kv_empty = kv_full + 8 * L::STAGES, v_ok = kv_empty + 8 * L::STAGES;
@@ -251,25 +270,49 @@ __global__ __launch_bounds__(kThreads, 1) void cross_forward_kernel(const __grid
     __syncthreads();
     tc::pdl_launch_dependents();
     tc::pdl_wait();
-    for (int t = threadIdx.x; t < a.T; t += kThreads) {
-        const int2 s = span_of(a.spans, a.S, t, blockIdx.x == 0 ? a.status : nullptr);
-        if (s.x < s.y) {
-            atomicMin(&ranges[t / p.tokens_a_tile].x, s.x);
-            atomicMax(&ranges[t / p.tokens_a_tile].y, s.y);
+    int *record = blockIdx.x == 0 ? a.status : nullptr;
+    int n_items = 1;
+    if (p.tiles > 1) {
+        for (int t = threadIdx.x; t < a.T; t += kThreads) {
+            const int2 s = span_of(a.spans, a.S, t, record);
+            if (s.x < s.y) {
+                atomicMin(&ranges[t / p.tokens_a_tile].x, s.x);
+                atomicMax(&ranges[t / p.tokens_a_tile].y, s.y);
+            }
         }
+        record = nullptr;
+        __syncthreads();
+        if (warp == 0) {
+            const int n = make_items(ranges, p.tiles, items);
+            if (lane == 0)
+                item_count = n;
+        }
+        __syncthreads();
+        n_items = uniform(item_count);
+    } else if (threadIdx.x == 0) {
+        items[0] = {kNoTile << 16, 0, 0};
     }
-    __syncthreads();
-    if (warp == 0) {
-        const int n = make_items(ranges, p.tiles, items);
+    __syncwarp();
+    const int run_step = kRuns / n_items;
+    for (int i = warp; i < n_items; i += kThreads / 32) {
+        const int t0 = (items[i].tile & 0xFFFF) * p.tokens_a_tile;
+        const int n = min(a.T - t0, (items[i].tile >> 16 & 0xFFFF) != kNoTile ? 2 * p.tokens_a_tile : p.tokens_a_tile);
+        Run *to = runs + i * run_step;
+        const int size = n <= 32 ? make_runs<1>(a.spans, a.S, t0, n, run_step - 1, to, record)
+                                 : make_runs<8>(a.spans, a.S, t0, n, run_step - 1, to, record);
         if (lane == 0)
-            item_count = n;
-        __syncwarp();
+            items[i].begin = size;
     }
+    if (p.tiles > 1)
+        __syncthreads();
+    __syncwarp();
+    if (warp == 0)
+        add_up(items, n_items);
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
     const uint32_t tmem = tmem_slot;
-    Share share(items, uniform(item_count), a.heads, p.ctas);
+    Share share(items, n_items, a.heads, p.ctas);
     Unit u;
     bool ok = true;
 
@@ -285,13 +328,21 @@ __global__ __launch_bounds__(kThreads, 1) void cross_forward_kernel(const __grid
                 for (int s = 0; s < (u.pair ? 2 : 1); ++s)
                     for (int c = 0; c < L::CHUNKS; ++c)
                         tma_3d_elect(base + L::Q + s * L::TILE + c * (kTile * 128), &map_q, 64 * c, u.head * group, (s ? u.tb : u.ta) * p.tokens_a_tile, q_full);
+                Walk walk(runs + u.item * run_step, u.j0);
+                int j = 0;
                 for (int i = 0; ok && i < 2 * u.n; ++i, ++at) {
                     const int st = at % L::STAGES;
                     if (at >= L::STAGES && !(ok = tc::warp_wait(kv_empty + 8 * st, (at / L::STAGES - 1) & 1)))
                         break;
+                    if (!(i & 1)) {     // (the values before these took the place of those half a ring back, which were used)
+                        j = walk(i >> 1);
+                        if (lane == 0)
+                            places[(at >> 1) % L::STAGES] = j * kTile;
+                        __syncwarp();
+                    }
                     tc::mbar_arrive_expect_tx_elect(kv_full + 8 * st, L::TILE);
                     for (int c = 0; c < L::CHUNKS; ++c)
-                        tma_3d_elect(base + L::KV + st * L::TILE + c * (kTile * 128), i & 1 ? &map_v : &map_k, 64 * c, u.head, (u.j0 + (i >> 1)) * kTile,
+                        tma_3d_elect(base + L::KV + st * L::TILE + c * (kTile * 128), i & 1 ? &map_v : &map_k, 64 * c, u.head, j * kTile,
                                      kv_full + 8 * st);
                 }
             }
@@ -366,9 +417,10 @@ __global__ __launch_bounds__(kThreads, 1) void cross_forward_kernel(const __grid
                 if (units > 0 && !(ok = tc::warp_wait(o_free, (units - 1) & 1)))   // the notes of the piece before are read
                     break;
                 for (int i = 0; i < u.n; ++i) {
-                    const int v = at + 2 * i + 1, st = v % L::STAGES, c0 = (u.j0 + i) * kTile;
+                    const int v = at + 2 * i + 1, st = v % L::STAGES;
                     if (!(ok = tc::warp_wait(kv_full + 8 * st, (v / L::STAGES) & 1)))
                         break;
+                    const int c0 = uniform((int)places[(v >> 1) % L::STAGES]);
                     if (c0 < lo || c0 + kTile > hi) {
                         look_over<DP>(base + L::KV + st * L::TILE, c0, a, p, u, bad, bad_any);
                         fence_proxy_async_smem();
@@ -385,7 +437,7 @@ __global__ __launch_bounds__(kThreads, 1) void cross_forward_kernel(const __grid
         const int s = (warp - 4) >> 2, row = threadIdx.x & 127;
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21), sc = lanes + s * 128, oc = lanes + 256 + s * 128;
         const float scale = fmaxf(fabsf(a.scale) * kLog2e, 1e-30f);      // not 0: a hidden score is -inf
-        int jobs = 0;
+        int jobs = 0, visits = 0;       // of this chain, and of both before this piece
         while (next_unit(share, u)) {
             const int tile = u.pair && s ? u.tb : u.ta, t = tile * p.tokens_a_tile + row / group;
             const bool live = row < p.chunk_rows && t < a.T;
@@ -393,8 +445,8 @@ __global__ __launch_bounds__(kThreads, 1) void cross_forward_kernel(const __grid
             const int mine = u.pair ? u.n : (u.n + 1 - s) / 2;
             float top = -INFINITY, sum = 0.0f;      // in units of base-2 exponents
             for (int i = 0; i < mine; ++i, ++jobs) {
-                const int c0 = (u.j0 + (u.pair ? i : 2 * i + s)) * kTile;
                 wait_on(ok, s_full + 8 * s, jobs & 1);
+                const int c0 = places[(visits + (u.pair ? i : 2 * i + s)) % L::STAGES];
                 float x[64], m[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
                 const bool all = __all_sync(0xffffffffu, see.x <= c0 && see.y >= c0 + kTile);
                 const unsigned from = see.x - c0, n = see.y - see.x;
@@ -549,6 +601,7 @@ __global__ __launch_bounds__(kThreads, 1) void cross_forward_kernel(const __grid
                         bad_any[u.pair ? s : 0] = 0;
                 }
             }
+            visits += u.n;
             tc::tc_fence_before();
             __syncwarp();
             if (lane == 0)
@@ -656,7 +709,7 @@ template <int DP>
 cudaError_t launch(const CrossArgs &a, cudaStream_t stream)
 {
     using L = Layout<DP>;
-    static_assert(L::BYTES <= 232448 && L::BARS % 8 == 0 && L::ITEMS % 16 == 0, "shared memory");
+    static_assert(L::BYTES <= 232448 && L::BARS % 8 == 0 && L::ITEMS % 16 == 0 && 88 + 24 * L::STAGES <= 384, "shared memory");
     size_t bytes;
     Plan p = plan_of(a.T, a.Hq, a.heads, DP, &bytes);
     char *ws = static_cast<char *>(a.ws);

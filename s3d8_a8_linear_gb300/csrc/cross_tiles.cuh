@@ -162,7 +162,7 @@ struct Item {
 };
 
 struct Piece {
-    int tile, head, j0, n, slot;        // slot: -1 for a whole item, else where its sums go: 0 or 1
+    int item, tile, head, j0, n, slot;  // slot: -1 for a whole item, else where its sums go: 0 or 1
     int item_end;                       // tiles of all heads in front of the item's end
     bool begins;                        // the item, and not only a piece of it
 };
@@ -200,6 +200,7 @@ struct Share {
                 hi = mid;
         }
         const int off = r - uniform(items[lo].begin), left = uniform(items[lo + 1].begin) - r;
+        u.item = lo;
         u.tile = uniform(items[lo].tile);
         u.j0 = uniform(items[lo].j0) + off;
         u.n = min(end - at, left);
@@ -211,6 +212,86 @@ struct Share {
         return true;
     }
 };
+
+// A run of tiles of states that some row of an item sees: its first, and how many come in
+// front of it in the item's runs, which end with an entry that has only that.
+struct Run {
+    int first, begin;
+};
+
+// Which tile of states a piece's i-th one is, for growing i.
+struct Walk {
+    const Run *run;
+    int off, end, shift;
+
+    // `off`: tiles of the item's runs in front of the piece
+    __device__ __forceinline__ Walk(const Run *runs, int off) : run(runs), off(off), end(0), shift(0) { load(); }
+    __device__ __forceinline__ void load()
+    {
+        const int begin = uniform(run->begin);
+        shift = uniform(run->first) - begin + off;
+        end = uniform(run[1].begin) - off;
+    }
+    __device__ __forceinline__ int operator()(int i)
+    {
+        while (i >= end) {
+            ++run;
+            load();
+        }
+        return i + shift;
+    }
+};
+
+// The runs of tokens t0 .. t0 + n - 1 (at most 32 E), at most `most` of them: the last one
+// goes on over tiles that nobody sees.  One warp; how many tiles.
+template <int E>
+__device__ __forceinline__ int make_runs(const int32_t *spans, int S, int t0, int n, int most, Run *runs, int *record)
+{
+    const int lane = threadIdx.x & 31;
+    int lo[E], hi[E], last = 0;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        const int2 s = e * 32 + lane < n ? span_of(spans, S, t0 + e * 32 + lane, record) : make_int2(0, 0);
+        lo[e] = s.x < s.y ? s.x / kTile : 0x7FFFFFFF;
+        hi[e] = s.x < s.y ? (s.y + kTile - 1) / kTile : 0;
+        last = max(last, hi[e]);
+    }
+    last = __reduce_max_sync(0xffffffffu, last);
+    int end = 0, count = 0, made = 0;
+    while (end < last) {
+        int first = 0x7FFFFFFF;
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            if (hi[e] > end)
+                first = min(first, max(lo[e], end));
+        first = __reduce_min_sync(0xffffffffu, first);
+        if (lane == 0)
+            runs[made] = {first, count};
+        ++made;
+        end = first;
+        if (made == most)
+            end = last;
+        for (bool more = end < last; more;) {
+            int to = end;
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                if (lo[e] <= end)
+                    to = max(to, hi[e]);
+            to = __reduce_max_sync(0xffffffffu, to);
+            more = to > end;
+            end = to;
+        }
+        count += end - first;
+    }
+    if (count == 0) {           // one, of which nothing is seen
+        if (lane == 0)
+            runs[0] = {0, 0};
+        made = count = 1;
+    }
+    if (lane == 0)
+        runs[made] = {0, count};
+    return count;
+}
 
 // Most tiles of a launch that have sums of their own, where each may pass `others`.
 inline int most_tiles(int64_t heads, int64_t others, int most)

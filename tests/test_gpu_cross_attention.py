@@ -414,3 +414,39 @@ def test_far_states():
     out = s3d8.cross_attention(q, both[:, :1], both[:, 1:], spans)
     r = _reference(q, near[:, :1], near[:, 1:], moved, dim ** -0.5)
     _within(out, r["out"], r["out_tol"], "out")
+
+
+@pytest.mark.parametrize("T,group,kind", [(1, 4, "gaps"), (48, 4, "gaps"), (200, 1, "gaps"), (97, 8, "gaps"), (1000, 4, "gaps"), (700, 128, "gaps"),
+                                          (64, 4, "behind"), (513, 2, "behind")])
+def test_states_that_nobody_sees(T, group, kind):
+    """Sequences of their own states, most of which are padding: whole tiles between the ones
+    that are seen hold NaN, and the visits of a query tile jump over them."""
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    heads, dim, S = 2, 64, 60000
+    t = torch.arange(T, device="cuda")
+    if kind == "gaps":          # token t's states begin anywhere in its share of them, and are few
+        share = S // T
+        lo = t * share + torch.randint(0, max(share // 2, 1), (T,), generator=gen, device="cuda")
+        hi = torch.minimum(lo + torch.randint(0, 300, (T,), generator=gen, device="cuda"), (t + 1) * share)
+    else:                       # far first, near last
+        lo = (T - 1 - t) * (S // T)
+        hi = lo + 37
+    spans = torch.stack((lo, hi), -1).int()
+    q, k, v = _rand(gen, T, heads * group, dim), _rand(gen, S, heads, dim), _rand(gen, S, heads, dim)
+    seen = torch.zeros(S + 1, dtype=torch.int32, device="cuda")
+    seen.index_add_(0, spans[:, 0].long(), torch.ones(T, dtype=torch.int32, device="cuda"))
+    seen.index_add_(0, spans[:, 1].long(), -torch.ones(T, dtype=torch.int32, device="cuda"))
+    unseen = seen.cumsum(0)[:S] == 0
+    k[unseen] = float("nan")
+    v[unseen] = float("nan")
+    out = torch.full_like(q, 3.0)
+    lse = torch.full((T, heads * group), 3.0, device="cuda")
+    s3d8.cross_attention(q, k, v, spans, out=out, lse=lse)
+    for i in range(0, T, max(1, T // 40)):
+        a, b = spans[i].tolist()
+        r = _reference(q[i:i + 1], k[a:b], v[a:b], None, dim ** -0.5) if b > a else None
+        if r is None:
+            assert not out[i].any() and bool((lse[i] == -float("inf")).all())
+        else:
+            _within(out[i:i + 1], r["out"], r["out_tol"], f"token {i}")
+            _within_lse(lse[i:i + 1], r["lse"])
