@@ -38,7 +38,7 @@ using namespace cross;
 constexpr int kThreads = 512;
 constexpr int kMostTiles = 512;         // query tiles of a launch
 constexpr int kRuns = 1536;             // runs of states of all items, and their ends
-constexpr int kJoinWarps = 8, kJoinRows = 32;
+constexpr int kJoinWarps = 8;
 
 constexpr int kNoTile = 0xFFFF;         // of the two query tiles of a piece, low and high half of its `tile`
 
@@ -627,51 +627,57 @@ __global__ __launch_bounds__(kJoinWarps * 32) void cross_join_kernel(const __gri
     if (cut.c1 < 0)
         return;
     const int warp = warp_index(), lane = threadIdx.x & 31, group = a.Hq / a.heads, n = cut.c1 - (int)blockIdx.x + 1;
-    for (int r = blockIdx.y * kJoinRows + warp; r < blockIdx.y * kJoinRows + kJoinRows && r < p.rows; r += kJoinWarps) {
-        const int tile = r < kTile ? cut.tile & 0xFFFF : cut.tile >> 16 & 0xFFFF, row = r % kTile;
-        const int t = tile * p.tokens_a_tile + row / group;
-        if (tile == kNoTile || row >= p.chunk_rows || t >= a.T)
-            continue;
-        auto slot = [&](int i) { return ((int64_t)(blockIdx.x + i) * 2 + (i == 0 ? cut.slot : 0)) * p.rows + r; };
-        float top = -INFINITY;
-        for (int i = lane; i < n; i += 32)
-            top = fmaxf(top, p.tops[2 * slot(i)]);
+    const int r = blockIdx.y * kJoinWarps + warp;
+    if (r >= p.rows)
+        return;
+    const int tile = r < kTile ? cut.tile & 0xFFFF : cut.tile >> 16 & 0xFFFF, row = r % kTile;
+    const int t = tile * p.tokens_a_tile + row / group;
+    if (tile == kNoTile || row >= p.chunk_rows || t >= a.T)
+        return;
+    auto slot = [&](int i) { return ((int64_t)(blockIdx.x + i) * 2 + (i == 0 ? cut.slot : 0)) * p.rows + r; };
+    float top = -INFINITY;
+    float2 mine = make_float2(-INFINITY, 0.0f);     // maximum and sum of a lane's part
+    if (lane < n)
+        mine = reinterpret_cast<const float2 *>(p.tops)[slot(lane)];
+    top = mine.x;
+    for (int i = lane + 32; i < n; i += 32)
+        top = fmaxf(top, p.tops[2 * slot(i)]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    const float zero = top == -INFINITY ? 0.0f : top;
+    float sum = 0.0f, acc[V] = {};
+    for (int base = 0; base < n; base += 32) {
+        if (base > 0)
+            mine = base + lane < n ? reinterpret_cast<const float2 *>(p.tops)[slot(base + lane)] : make_float2(-INFINITY, 0.0f);
+        const float turn = mine.y == 0.0f ? 0.0f : ex2(mine.x - zero);      // saw nothing: its sums were not written
+        float s = mine.y * turn;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        const float zero = top == -INFINITY ? 0.0f : top;
-        float sum = 0.0f, acc[V] = {};
-        for (int base = 0; base < n; base += 32) {
-            float2 mine = make_float2(-INFINITY, 0.0f);
-            if (base + lane < n)
-                mine = reinterpret_cast<const float2 *>(p.tops)[slot(base + lane)];
-            const float turn = mine.y == 0.0f ? 0.0f : ex2(mine.x - zero);      // saw nothing: its sums were not written
-            float s = mine.y * turn;
+            s += __shfl_xor_sync(0xffffffffu, s, o);
+        sum += s;
+        const int count = min(32, n - base);
+#pragma unroll 8
+        for (int i = 0; i < count; ++i) {
+            const float by = __shfl_sync(0xffffffffu, turn, i), some = __shfl_sync(0xffffffffu, mine.y, i);
+            float part[V];
+            Columns<DP>::get(p.parts + slot(base + i) * DP, part);
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1)
-                s += __shfl_xor_sync(0xffffffffu, s, o);
-            sum += s;
-            const int count = min(32, n - base);
-#pragma unroll 4
-            for (int i = 0; i < count; ++i) {
-                const float by = __shfl_sync(0xffffffffu, turn, i), some = __shfl_sync(0xffffffffu, mine.y, i);
-                const float *part = p.parts + slot(base + i) * DP + lane;
-#pragma unroll
-                for (int v = 0; v < V; ++v)
-                    acc[v] = fmaf(some == 0.0f ? 0.0f : part[32 * v], by, acc[v]);
-            }
+            for (int v = 0; v < V; ++v)
+                acc[v] = fmaf(some == 0.0f ? 0.0f : part[v], by, acc[v]);
         }
-        const int64_t at = (int64_t)t * a.Hq + cut.head * group + row % group;
-        const int2 see = span_of(a.spans, a.S, t, nullptr);
-        const bool some = see.x < see.y;
-        const float by = some ? 1.0f / sum : 0.0f;
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-            if (lane + 32 * v < a.dim)
-                a.out[at * a.dim + lane + 32 * v] = __float2bfloat16_rn(some ? acc[v] * by : 0.0f);
-        if (a.lse && lane == 0)
-            a.lse[at] = some ? (top + __log2f(sum)) * kLn2 : -INFINITY;
     }
+    const int64_t at = (int64_t)t * a.Hq + cut.head * group + row % group;
+    const int2 see = span_of(a.spans, a.S, t, nullptr);
+    const bool some = see.x < see.y;
+    const float by = some ? 1.0f / sum : 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+        acc[v] = some ? acc[v] * by : 0.0f;
+    if (lane * V < a.dim)
+        Columns<DP>::put(a.out + at * a.dim, acc);
+    if (a.lse && lane == 0)
+        a.lse[at] = some ? (top + __log2f(sum)) * kLn2 : -INFINITY;
 }
 
 // No states at all.
@@ -729,7 +735,7 @@ cudaError_t launch(const CrossArgs &a, cudaStream_t stream)
     if (e == cudaSuccess)
         e = tc::launch_pdl(cross_forward_kernel<DP>, dim3(p.ctas), dim3(kThreads), L::BYTES, stream, mq, mk, mv, a, p);
     if (e == cudaSuccess)
-        e = tc::launch_pdl(cross_join_kernel<DP>, dim3(p.ctas, (p.rows + kJoinRows - 1) / kJoinRows), dim3(kJoinWarps * 32), 0, stream, a, p);
+        e = tc::launch_pdl(cross_join_kernel<DP>, dim3(p.ctas, (p.rows + kJoinWarps - 1) / kJoinWarps), dim3(kJoinWarps * 32), 0, stream, a, p);
     return e;
 }
 

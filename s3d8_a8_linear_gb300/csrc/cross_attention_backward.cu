@@ -28,7 +28,7 @@ using namespace cross;
 constexpr int kDqThreads = 512;         // warps: 0 copies, 1 and 2 products, 4 to 11 softmax, 12 to 15 look tiles over
 constexpr int kThreads = 384;           // 0 copies, 1 products, 2 and 3 look tiles over, 4 to 11 softmax
 constexpr int kMostTiles = 128;         // tiles of a launch that have sums of their own (their list fits beside five tiles of 32 KB)
-constexpr int kJoinWarps = 8, kJoinRows = 32;
+constexpr int kJoinWarps = 8;
 
 struct Plan {
     int tokens_a_tile, chunk_rows;      // query rows that a copy fills
@@ -815,35 +815,38 @@ __global__ __launch_bounds__(kJoinWarps * 32) void cross_add_kernel(const __grid
         return;
     const int tile = p.first + cut.tile, group = a.Hq / a.heads, warp = warp_index(), lane = threadIdx.x & 31, n = cut.c1 - (int)blockIdx.x + 1;
     const int slot_rows = STATES ? 2 * kTile : p.rows;
-    for (int r = blockIdx.y * kJoinRows + warp; r < blockIdx.y * kJoinRows + kJoinRows && r < slot_rows; r += kJoinWarps) {
-        const int row = STATES ? r % kTile : r;
-        __nv_bfloat16 *out;
-        float by = a.scale;
-        if (STATES) {
-            const int64_t j = (int64_t)tile * kTile + row;
-            if (j >= a.S)
-                continue;
-            out = (r < kTile ? a.dv : a.dk) + (j * a.heads + cut.head) * a.dim;
-            by = r < kTile ? 1.0f : a.scale;
-        } else {
-            const int64_t t = (int64_t)tile * p.tokens_a_tile + row / group;
-            if (row >= p.chunk_rows || t >= a.T)
-                continue;
-            out = a.dq + (t * a.Hq + cut.head * group + row % group) * a.dim;
-        }
-        float acc[V] = {};
-#pragma unroll 4
-        for (int i = 0; i < n; ++i) {
-            const float *part = p.parts + (((int64_t)(blockIdx.x + i) * 2 + (i == 0 ? cut.slot : 0)) * slot_rows + r) * DP + lane;
-#pragma unroll
-            for (int v = 0; v < V; ++v)
-                acc[v] += part[32 * v];
-        }
+    const int r = blockIdx.y * kJoinWarps + warp;
+    if (r >= slot_rows)
+        return;
+    const int row = STATES ? r % kTile : r;
+    __nv_bfloat16 *out;
+    float by = a.scale;
+    if (STATES) {
+        const int64_t j = (int64_t)tile * kTile + row;
+        if (j >= a.S)
+            return;
+        out = (r < kTile ? a.dv : a.dk) + (j * a.heads + cut.head) * a.dim;
+        by = r < kTile ? 1.0f : a.scale;
+    } else {
+        const int64_t t = (int64_t)tile * p.tokens_a_tile + row / group;
+        if (row >= p.chunk_rows || t >= a.T)
+            return;
+        out = a.dq + (t * a.Hq + cut.head * group + row % group) * a.dim;
+    }
+    float acc[V] = {};
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) {
+        float part[V];
+        Columns<DP>::get(p.parts + (((int64_t)(blockIdx.x + i) * 2 + (i == 0 ? cut.slot : 0)) * slot_rows + r) * DP, part);
 #pragma unroll
         for (int v = 0; v < V; ++v)
-            if (lane + 32 * v < a.dim)
-                out[lane + 32 * v] = __float2bfloat16_rn(acc[v] * by);
+            acc[v] += part[v];
     }
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+        acc[v] *= by;
+    if (lane * V < a.dim)
+        Columns<DP>::put(out, acc);
 }
 
 // Where the workspace's parts are (the pointers as offsets), and how long it is.
@@ -905,13 +908,13 @@ cudaError_t launch(const CrossArgs &a, cudaStream_t stream)
         p.tiles = p.q_tiles - p.first < most_q ? p.q_tiles - p.first : most_q;
         e = tc::launch_pdl(cross_dq_kernel<DP>, dim3(p.ctas), dim3(kDqThreads), Lq::BYTES, stream, mq, md, mk, mv, a, p);
         if (e == cudaSuccess)
-            e = tc::launch_pdl(cross_add_kernel<DP, false>, dim3(p.ctas, (p.rows + kJoinRows - 1) / kJoinRows), dim3(kJoinWarps * 32), 0, stream, a, p);
+            e = tc::launch_pdl(cross_add_kernel<DP, false>, dim3(p.ctas, (p.rows + kJoinWarps - 1) / kJoinWarps), dim3(kJoinWarps * 32), 0, stream, a, p);
     }
     for (p.first = 0; e == cudaSuccess && p.first < tiles; p.first += most_kv) {
         p.tiles = tiles - p.first < most_kv ? tiles - p.first : most_kv;
         e = tc::launch_pdl(cross_dkv_kernel<DP>, dim3(p.ctas), dim3(kThreads), L::BYTES, stream, mq, md, mk, mv, a, p);
         if (e == cudaSuccess)
-            e = tc::launch_pdl(cross_add_kernel<DP, true>, dim3(p.ctas, 2 * kTile / kJoinRows), dim3(kJoinWarps * 32), 0, stream, a, p);
+            e = tc::launch_pdl(cross_add_kernel<DP, true>, dim3(p.ctas, 2 * kTile / kJoinWarps), dim3(kJoinWarps * 32), 0, stream, a, p);
     }
     return e;
 }

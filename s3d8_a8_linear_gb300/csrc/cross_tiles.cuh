@@ -293,6 +293,31 @@ __device__ __forceinline__ int make_runs(const int32_t *spans, int S, int t0, in
     return count;
 }
 
+// A lane's columns of a row of DP fp32 sums: DP / 32 neighbouring ones.
+template <int DP>
+struct Columns;
+template <>
+struct Columns<64> {
+    static __device__ __forceinline__ void get(const float *row, float (&x)[2])
+    {
+        const float2 v = reinterpret_cast<const float2 *>(row)[threadIdx.x & 31];
+        x[0] = v.x, x[1] = v.y;
+    }
+    static __device__ __forceinline__ void put(__nv_bfloat16 *row, const float (&x)[2]) { reinterpret_cast<uint32_t *>(row)[threadIdx.x & 31] = pack2(x[0], x[1]); }
+};
+template <>
+struct Columns<128> {
+    static __device__ __forceinline__ void get(const float *row, float (&x)[4])
+    {
+        const float4 v = reinterpret_cast<const float4 *>(row)[threadIdx.x & 31];
+        x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+    }
+    static __device__ __forceinline__ void put(__nv_bfloat16 *row, const float (&x)[4])
+    {
+        reinterpret_cast<uint2 *>(row)[threadIdx.x & 31] = make_uint2(pack2(x[0], x[1]), pack2(x[2], x[3]));
+    }
+};
+
 // Most tiles of a launch that have sums of their own, where each may pass `others`.
 inline int most_tiles(int64_t heads, int64_t others, int most)
 {
