@@ -29,17 +29,6 @@ __device__ __forceinline__ uint32_t smem_addr(const void *p)
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
-// A value that all lanes of the warp have, as one that the compiler knows to be the same in
-// them: behind a branch on it, shuffles and votes need no check for lanes that are elsewhere
-// (about 240 clocks each).  Whole warps together.
-template <typename T>
-__device__ __forceinline__ T uniform(T x)
-{
-    return __shfl_sync(0xffffffffu, x, 0);
-}
-
-__device__ __forceinline__ int warp_index() { return uniform((int)threadIdx.x >> 5); }
-
 __device__ __forceinline__ uint32_t lds_u32(uint32_t addr)
 {
     uint32_t v;

@@ -5,6 +5,7 @@
 
 #include "launch.h"
 #include "tcgen05.cuh"
+#include "uniform.cuh"
 
 namespace s3d8 {
 

@@ -20,6 +20,7 @@
 #include "launch.h"
 #include "rope_lane.cuh"
 #include "tcgen05.cuh"
+#include "uniform.cuh"
 
 namespace s3d8 {
 

@@ -22,6 +22,7 @@
 // the value by searching the groups' sums, and tells the CTA whose part has the token.
 #include "launch.h"
 #include "tcgen05.cuh"
+#include "uniform.cuh"
 
 namespace s3d8 {
 
