@@ -550,7 +550,10 @@ int s3d8_cross_attention(const void *q_bf16, const int64_t q_stride[2], const vo
  *   dq      : [T, Hq, dim]; dk, dv : [S, heads, dim] bfloat16 contiguous outputs, 16-byte
  *             aligned
  *   workspace : s3d8_cross_attention_backward_workspace_size(...) bytes, as above
- * No atomics: equal inputs give equal bits.  A state that no token sees has zero gradients.
+ * No atomics: equal inputs give equal bits.  A state that no token sees has zero gradients,
+ * and neither it nor a token that sees nothing has a part in any other gradient, whatever
+ * they hold.  An infinity or NaN that some token does see may reach the gradients of other
+ * tokens and states in the same 128 of them.
  */
 size_t s3d8_cross_attention_backward_workspace_size(int64_t T, int64_t S, int64_t Hq, int64_t heads,
                                                     int64_t dim);
