@@ -17,9 +17,14 @@
 // the row is counted again as a whole.
 //
 // A cluster of CTAs takes a row, a part of the vocabulary each (16-bit counts, so at most
-// 65535 tokens a CTA), and reads it three times, from L2 but for the first.  Values form groups of 128, one power of
-// two each.  The first CTA adds up the groups' counts from all CTAs, finds the limits and
-// the value by searching the groups' sums, and tells the CTA whose part has the token.
+// 65535 tokens a CTA), and reads it three times, from L2 but for the first.  Values form
+// groups of 128, one power of two each.  The first CTA adds up the counts of the groups that have any from all CTAs,
+// finds the limits and the value by searching the groups' sums, and tells the CTA whose part
+// has the token.
+//
+// Bound by instructions and by the barriers between those steps (42% of the issue slots with
+// 509 rows), not by HBM.  Measured with 128256 logits: one row 13 us, 64 rows with limits of
+// their own 28 us, 509 rows 160 us (302 when every token was counted).
 #include "launch.h"
 #include "tcgen05.cuh"
 #include "uniform.cuh"
@@ -55,7 +60,10 @@ struct Shared {
     // told by the first CTA
     int verdict;                                // what a row comes to: below
     uint32_t key, rank;                         // the token: its value, and its rank among this CTA's
-    // of the first CTA.  Of run i, from the largest values downwards, all CTAs': tokens, those
+    // of the first CTA.  The groups that some CTA's part has, from the largest values downwards
+    int groups;
+    uint16_t order[kGroups];
+    // Of run i, from the largest values downwards, all CTAs': tokens, those
     // that min-p keeps, weight; and what stands in front of it
     uint32_t count[kUnits], above[kUnits], count_before[kUnits];
     unsigned long long mass[kUnits], mass_before[kUnits];
@@ -193,18 +201,41 @@ __device__ __forceinline__ void remote_store_u32(uint32_t addr, uint32_t v)
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
-// How the counted values are cut into runs: of 32, a value a lane, or of 128 where those
-// were too many.  Run i ends in front of key `end` - i * size.
+// How the counted values are cut into runs, groups without any left out: runs of 32, a value a
+// lane, or of 128 where those were too many.
 struct Runs {
-    int end, count;
+    int count;
     bool fine;
-    __device__ __forceinline__ Runs(int first_group, int last_group)
-        : end((last_group + 1) * kKeys), fine((last_group - first_group + 1) * 4 <= kUnits)
+    __device__ __forceinline__ explicit Runs(int groups) : count(groups), fine(groups * 4 <= kUnits) { count *= fine ? 4 : 1; }
+    // the largest of a lane's values of run i
+    __device__ __forceinline__ int first(const Shared &s, int i) const
     {
-        count = (last_group - first_group + 1) * (fine ? 4 : 1);
+        const int lane = threadIdx.x & 31;
+        return fine ? s.order[i >> 2] * kKeys + (kKeys - 1) - 32 * (i & 3) - lane : s.order[i] * kKeys + (kKeys - 1) - 4 * lane;
     }
-    __device__ __forceinline__ int size() const { return fine ? 32 : 128; }
 };
+
+// Which groups some CTA's part has (most rows have few, but those around zero span many
+// powers of two that they do not have).  One warp of the first CTA.
+template <int C>
+__device__ __forceinline__ void list_groups(Shared &s)
+{
+    const int lane = threadIdx.x & 31;
+    uint32_t mine = 0;
+    if (lane < kGroups / 32)
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+            mine |= remote_u32(tc::map_to_rank(smem_addr(s.flags) + 4 * lane, c));
+    int count = 0;
+    for (int w = kGroups / 32 - 1; w >= 0; --w) {
+        const uint32_t some = __shfl_sync(0xffffffffu, mine, w);
+        if (some >> lane & 1)
+            s.order[count + __popc(some >> lane) - 1] = (uint16_t)(32 * w + lane);
+        count += __popc(some);
+    }
+    if (lane == 0)
+        s.groups = count;
+}
 
 // All CTAs' tokens of a lane's values of a run, the largest value first: value `first` - e, e
 // < 4 (fine: e = 0 alone).
@@ -376,11 +407,11 @@ __device__ __noinline__ Hit search(Shared &s, Row row, Runs runs, bool by_mass, 
     bool has = false;
     if (runs.fine && i < kCached) {
         const Value v = s.values[i][lane];
-        hit = {(uint32_t)(runs.end - i * 32 - 1 - lane), s.count_before[i] + v.count_before, s.mass_before[i] + v.mass_before, v.weight};
+        hit = {(uint32_t)runs.first(s, i), s.count_before[i] + v.count_before, s.mass_before[i] + v.mass_before, v.weight};
         const unsigned long long before = by_mass ? hit.mass : hit.count, size = by_mass ? v.count * v.weight : v.count;
         has = target >= before && target < before + size;
     } else {
-        const int first = runs.end - i * runs.size() - 1 - (runs.fine ? 1 : 4) * lane;
+        const int first = runs.first(s, i);
         uint32_t n[4], c;
         run_counts<C>(s, runs, first, n);
         unsigned long long w[4], m;
@@ -424,14 +455,11 @@ __device__ __forceinline__ void add_runs(Shared &s, const Row &row, unsigned lon
 {
     const int warp = warp_index(), lane = threadIdx.x & 31;
     for (int i = warp; i < runs.count; i += kWarps) {
-        const int first = runs.end - i * runs.size() - 1 - (runs.fine ? 1 : 4) * lane, g = (runs.end - i * runs.size() - 1) / kKeys;
-        uint32_t some = 0;
-        if (lane < C)
-            some = remote_u32(tc::map_to_rank(smem_addr(s.flags) + 4 * (g / 32), lane));
-        uint32_t n[4] = {0, 0, 0, 0}, count = 0, above = 0;
+        const int first = runs.first(s, i);
+        uint32_t n[4], count = 0, above = 0;
         unsigned long long w[4] = {0, 0, 0, 0}, mass = 0;
-        if (__any_sync(0xffffffffu, some >> (g & 31) & 1)) {
-            run_counts<C>(s, runs, first, n);
+        run_counts<C>(s, runs, first, n);
+        if (__any_sync(0xffffffffu, n[0] | n[1] | n[2] | n[3])) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 w[e] = n[e] ? weight_of(first - e, row) : 0;
@@ -647,7 +675,10 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(const __grid_constant_
             const float min_p = uniform(!cold && a.min_p ? a.min_p[b] : 0.0f);
             // the least weight that min-p keeps: min_p 2^45, and 0 (min_p NaN, or past 1: none)
             const unsigned long long least = min_p <= 0.0f ? 0ull : min_p <= 1.0f ? (unsigned long long)__float2ll_ru(min_p * (float)(1ull << kScale)) : ~0ull;
-            const Runs runs(first_group, last_group);
+            if (warp == 0)
+                list_groups<C>(s);
+            __syncthreads();
+            const Runs runs(uniform(s.groups));
             add_runs<C>(s, row, least, runs);
             __syncthreads();
             if (warp == 0) {            // whose part has the token, and its rank there
@@ -749,13 +780,18 @@ cudaError_t launch(const SampleArgs &a, cudaStream_t stream)
 
 cudaError_t launch_sample(const SampleArgs &a, cudaStream_t stream)
 {
-    // as few CTAs a row as fill the GPU (one fits an SM), and as many as 16-bit counts ask for
+    // One CTA fits an SM, and 16-bit counts ask for a CTA for every 65528 tokens.  More CTAs a
+    // row shorten its counting while all rows still run at once (clusters of 8 and 4 do not fill
+    // the last SMs of a group of them).  Measured with 1, 2, 4 and 8 CTAs (us): up to 8192 logits
+    // 17, 18, 18, 18 with 8 rows; 32768 logits: 8 rows 26, 22, 20, 19, 16 rows 25, 22, 20, 24, 38
+    // rows 26, 22, 31, 52, 152 rows 26, 44, 80, 171; 128256 logits: one row -, 31, 28, 15, 16 rows
+    // -, 39, 28, 31, 38 rows -, 40, 38, 52, 64 rows -, 41, 53, 86.
     const int64_t sms = device_sm_count(), most = kMostTokens;
     if (a.V <= 8192 || ((int64_t)a.B > sms / 2 && a.V <= most))
         return launch<1>(a, stream);
-    if (a.B > sms / 4 && a.V <= 2 * most)
+    if (a.B > sms / 8 && a.V <= 2 * most)
         return launch<2>(a, stream);
-    if (a.B > sms / 8 && a.V <= 4 * most)
+    if (a.B > sms / 16 && a.V <= 4 * most)
         return launch<4>(a, stream);
     return launch<8>(a, stream);
 }
