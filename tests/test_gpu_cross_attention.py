@@ -450,3 +450,28 @@ def test_states_that_nobody_sees(T, group, kind):
         else:
             _within(out[i:i + 1], r["out"], r["out_tol"], f"token {i}")
             _within_lse(lse[i:i + 1], r["lse"])
+
+
+def test_more_tiles_than_a_launch():
+    """Gradients with more query tiles and more tiles of states than one launch sums up (128
+    of either), ragged at both ends."""
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    T, S, heads, group, dim = 4237, 16999, 1, 4, 64
+    q, k, v = _rand(gen, T, heads * group, dim), _rand(gen, S, heads, dim), _rand(gen, S, heads, dim)
+    at = torch.arange(T, device="cuda") * 5 // T
+    spans = torch.stack((at * (S // 5), at * (S // 5) + S // 5 - 7 * at), -1).int()
+    _check(q, k, v, spans)
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_pieces_of_every_size(dim):
+    """Sequences of one to many tiles of states in one call, so that pieces of one visit follow
+    ones of many, in pairs and alone."""
+    gen = torch.Generator(device="cuda").manual_seed(dim)
+    sizes = [1, 130, 1, 1, 700, 127, 128, 129, 0, 3000, 2, 255, 257, 40, 511] * 4
+    tokens = [33, 1, 2, 64, 31, 32, 5, 97, 3, 40, 1, 1, 130, 20, 7] * 4
+    begin = torch.tensor([0] + sizes).cumsum(0)
+    spans = torch.cat([torch.tensor([[int(b), int(b) + n]]).expand(t, 2) for b, n, t in zip(begin, sizes, tokens)]).int().cuda()
+    T, S = spans.shape[0], int(begin[-1])
+    q, k, v = _rand(gen, T, 8, dim), _rand(gen, S, 2, dim), _rand(gen, S, 2, dim)
+    _check(q, k, v, spans)
