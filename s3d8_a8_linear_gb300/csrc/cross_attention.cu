@@ -558,6 +558,8 @@ __global__ __launch_bounds__(kThreads, 1) void cross_forward_kernel(const __grid
                 const bool some = see.x < see.y;
 #pragma unroll
                 for (int c = 0; c < DP; c += 32) {
+                    if (c >= a.dim)
+                        break;
                     float o[32];
                     tmem_ld32(oc + c, o);
                     tmem_wait_ld();

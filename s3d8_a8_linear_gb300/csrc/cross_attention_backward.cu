@@ -203,22 +203,6 @@ __device__ __forceinline__ void clear_row(uint32_t tile, int r)
         asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(chunk_at(tile, r, c)), "r"(0u) : "memory");
 }
 
-// 32 columns of sums: times `by`, as bf16 to `out` (those below dim), or as they are to `part`.
-__device__ __forceinline__ void put32(const float *o, int c, int dim, float by, __nv_bfloat16 *out, float *part)
-{
-    if (part) {
-#pragma unroll
-        for (int e = 0; e < 32; e += 4)
-            *reinterpret_cast<float4 *>(part + c + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-        return;
-    }
-#pragma unroll
-    for (int e = 0; e < 32; e += 8)
-        if (c + e < dim)
-            *reinterpret_cast<uint4 *>(out + c + e) = make_uint4(pack2(o[e] * by, o[e + 1] * by), pack2(o[e + 2] * by, o[e + 3] * by),
-                                                                 pack2(o[e + 4] * by, o[e + 5] * by), pack2(o[e + 6] * by, o[e + 7] * by));
-}
-
 // ---- dq ---------------------------------------------------------------------
 
 // Tensor memory: S 128 columns, dP twice 128 (dS over each), dQ.
@@ -469,14 +453,19 @@ __global__ __launch_bounds__(kDqThreads, 1) void cross_dq_kernel(const __grid_co
             if (!ok || !(ok = tc::warp_wait(done, units & 1)))
                 break;
             tc::tc_fence_after();
-            const int64_t slot = ((int64_t)blockIdx.x * 2 + u.slot) * p.rows + row;
+            const bool whole = u.slot < 0;
+            const RowStores rows(!live ? -1 : whole ? at * a.dim : (((int64_t)blockIdx.x * 2 + u.slot) * p.rows + row) * DP);
 #pragma unroll
-            for (int c = 0; c < DP / 2; c += 32) {
+            for (int c = half * (DP / 2); c < (half + 1) * (DP / 2); c += 32) {
+                if (c >= a.dim)
+                    break;
                 float o[32];
-                tmem_ld32(lanes + 384 + half * (DP / 2) + c, o);
+                tmem_ld32(lanes + 384 + c, o);
                 tmem_wait_ld();
-                if (live)
-                    put32(o, half * (DP / 2) + c, a.dim, a.scale, a.dq + at * a.dim, u.slot < 0 ? nullptr : p.parts + slot * DP);
+                if (whole)
+                    rows.bf16(a.dq, o, c, a.dim, a.scale);
+                else
+                    rows.fp32(p.parts, o, c);
             }
             tc::tc_fence_before();
             __syncwarp();
@@ -782,17 +771,21 @@ __global__ __launch_bounds__(kThreads, 1) void cross_dkv_kernel(const __grid_con
             if (!ok || !(ok = tc::warp_wait(done, units & 1)))
                 break;
             tc::tc_fence_after();
-            const int64_t slot = ((int64_t)blockIdx.x * 2 + u.slot) * 2 * kTile + row, at = ((int64_t)j * a.heads + u.head) * a.dim;
+            const bool whole = u.slot < 0;
+            const RowStores rows(j >= a.S ? -1 : whole ? ((int64_t)j * a.heads + u.head) * a.dim : (((int64_t)blockIdx.x * 2 + u.slot) * 2 * kTile + row) * DP);
 #pragma unroll
             for (int s = 0; s < 2; ++s)
 #pragma unroll
-                for (int c = 0; c < DP / 2; c += 32) {
+                for (int c = half * (DP / 2); c < (half + 1) * (DP / 2); c += 32) {
+                    if (c >= a.dim)
+                        break;
                     float o[32];
-                    tmem_ld32(lanes + 256 + s * 128 + half * (DP / 2) + c, o);
+                    tmem_ld32(lanes + 256 + s * 128 + c, o);
                     tmem_wait_ld();
-                    if (j < a.S)
-                        put32(o, half * (DP / 2) + c, a.dim, s ? a.scale : 1.0f, (s ? a.dk : a.dv) + at,
-                              u.slot < 0 ? nullptr : p.parts + (slot + s * kTile) * DP);
+                    if (whole)
+                        rows.bf16(s ? a.dk : a.dv, o, c, a.dim, s ? a.scale : 1.0f);
+                    else
+                        rows.fp32(p.parts + s * kTile * DP, o, c);
                 }
             tc::tc_fence_before();
             __syncwarp();

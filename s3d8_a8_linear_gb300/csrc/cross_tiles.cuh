@@ -294,6 +294,71 @@ __device__ __forceinline__ int make_runs(const int32_t *spans, int S, int t0, in
     return count;
 }
 
+// How a warp stores 32 columns of the rows that its lanes have: four lanes exchange 16-byte
+// pieces, so that each store writes 64 bytes of eight rows and not 16 of 32 (which takes the
+// load/store unit a step a row: a tile's 128 KB of results 4000 clocks).
+struct RowStores {
+    int64_t at[4];              // of the rows of this lane's four: where they begin, or -1
+
+    __device__ __forceinline__ explicit RowStores(int64_t mine)
+    {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            at[i] = __shfl_sync(0xffffffffu, mine, (threadIdx.x & 28) + i);
+    }
+    // piece i of row j to row i of piece j, of four lanes
+    static __device__ __forceinline__ void turn(uint4 (&x)[4])
+    {
+        const int lane = threadIdx.x & 31;
+#pragma unroll
+        for (int b = 1; b < 4; b <<= 1)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (i & b)
+                    continue;
+                const uint4 to = lane & b ? x[i] : x[i | b];
+                const uint4 from = make_uint4(__shfl_xor_sync(0xffffffffu, to.x, b), __shfl_xor_sync(0xffffffffu, to.y, b),
+                                              __shfl_xor_sync(0xffffffffu, to.z, b), __shfl_xor_sync(0xffffffffu, to.w, b));
+                if (lane & b)
+                    x[i] = from;
+                else
+                    x[i | b] = from;
+            }
+    }
+    // columns c .. c + 31 as bf16, those below dim
+    __device__ __forceinline__ void bf16(__nv_bfloat16 *out, const float *o, int c, int dim, float by) const
+    {
+        uint4 x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            x[i] = make_uint4(pack2(o[8 * i] * by, o[8 * i + 1] * by), pack2(o[8 * i + 2] * by, o[8 * i + 3] * by),
+                              pack2(o[8 * i + 4] * by, o[8 * i + 5] * by), pack2(o[8 * i + 6] * by, o[8 * i + 7] * by));
+        turn(x);
+        c += 8 * (threadIdx.x & 3);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (at[i] >= 0 && c < dim)
+                *reinterpret_cast<uint4 *>(out + at[i] + c) = x[i];
+    }
+    // as they are
+    __device__ __forceinline__ void fp32(float *out, const float *o, int c) const
+    {
+#pragma unroll
+        for (int h = 0; h < 32; h += 16) {
+            uint4 x[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                x[i] = make_uint4(__float_as_uint(o[h + 4 * i]), __float_as_uint(o[h + 4 * i + 1]), __float_as_uint(o[h + 4 * i + 2]),
+                                  __float_as_uint(o[h + 4 * i + 3]));
+            turn(x);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (at[i] >= 0)
+                    *reinterpret_cast<uint4 *>(out + at[i] + c + h + 4 * (threadIdx.x & 3)) = x[i];
+        }
+    }
+};
+
 // A lane's columns of a row of DP fp32 sums: DP / 32 neighbouring ones.
 template <int DP>
 struct Columns;
