@@ -13,9 +13,9 @@
 // gradients).  Products are issued so that the tensor cores have two of them to do while a
 // softmax step runs.
 //
-// Measured (2 x 2048 tokens of 32 / 8 heads of 128, 4 images of 3202 states): dq 215 us, its
-// tensor pipe busy 65% of the time; dkv 351 us, 52%; with the first kernel and the sums of what
-// shares cut 595 us.  dkv's four products of a visit take 3200 clocks where 2060 would be the
+// Measured (2 x 2048 tokens of 32 / 8 heads of 128, 4 images of 3202 states): dq 210 us, its
+// tensor pipe busy 65% of the time; dkv 340 us, 52%; with the first kernel and the sums of what
+// shares cut 580 us.  dkv's four products of a visit take 3200 clocks where 2060 would be the
 // least: their operands and the copies use shared memory's bandwidth nearly whole (a product of
 // two operands there takes 128 bytes a clock), and P and dS wait for one another.
 //
