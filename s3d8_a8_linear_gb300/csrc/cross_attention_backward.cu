@@ -23,6 +23,7 @@
 // each query tile sees.  Rows of the query tiles or the states that have no part in a tile
 // are taken out of it where they hold infinities or NaN, which a weight of zero would not
 // silence.
+#include "bf16x8.cuh"
 #include "cross_tiles.cuh"
 
 namespace s3d8 {
@@ -52,6 +53,48 @@ struct Plan {
 __device__ __forceinline__ float *info_of(const Plan &p, int heads, int tile, int head) { return p.info + ((int64_t)tile * heads + head) * 4 * kTile; }
 
 constexpr int kReadyRows = 32;          // of a block
+
+// delta is dout . out, but out is rounded to bf16: that is off by 2^-9 of a product whose size
+// falls with the square root of the number n of states, as against the dout . v_j that it is
+// taken from.  With few states it would be most of the error of dq and dk (n = 2: 2.4 times
+// that of their own rounding, 19: 1.6 times, from 64 on 1.45 times, which is that of ds), so
+// there it is summed from its parts, p_j (dout . v_j), at 60 instructions a state and row.
+constexpr int kFew = 64;
+
+__device__ __forceinline__ void row_chunk(const __nv_bfloat16 *row, bool some, float (&f)[8])
+{
+    const uint4 x = some ? __ldg(reinterpret_cast<const uint4 *>(row)) : make_uint4(0u, 0u, 0u, 0u);
+    unpack8(x, f);
+}
+
+// That sum, of half a warp's row, eight columns a lane.
+__device__ __noinline__ float delta_of_few(const CrossArgs &a, int t, int h, int head, int2 see, int lane)
+{
+    const unsigned mask = 0xFFFFu << (threadIdx.x & 16);
+    const bool some = 8 * lane < a.dim;
+    float q[8], d[8], sum = 0.0f;
+    row_chunk(a.q + t * a.qs[0] + h * a.qs[1] + 8 * lane, some, q);
+    row_chunk(a.dout + t * a.ds[0] + h * a.ds[1] + 8 * lane, some, d);
+    const float lse = -a.lse[(int64_t)t * a.Hq + h] * kLog2e, scale = a.scale * kLog2e;
+#pragma unroll 4
+    for (int j = see.x; j < see.y; ++j) {
+        float k[8], v[8], x = 0.0f, y = 0.0f;
+        row_chunk(a.k + j * a.ks[0] + head * a.ks[1] + 8 * lane, some, k);
+        row_chunk(a.v + j * a.vs[0] + head * a.vs[1] + 8 * lane, some, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            x = fmaf(q[e], k[e], x);
+            y = fmaf(d[e], v[e], y);
+        }
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) {
+            x += __shfl_xor_sync(mask, x, o);
+            y += __shfl_xor_sync(mask, y, o);
+        }
+        sum = fmaf(ex2(fmaf(x, scale, lse)), y, sum);
+    }
+    return sum;
+}
 
 // delta and lse of some of a tile's rows of one key/value head, and the tile's range.
 __global__ __launch_bounds__(256) void cross_ready_kernel(const __grid_constant__ CrossArgs a, const __grid_constant__ Plan p)
@@ -89,9 +132,12 @@ __global__ __launch_bounds__(256) void cross_ready_kernel(const __grid_constant_
 #pragma unroll
         for (int o = 8; o > 0; o >>= 1)
             sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        const int2 see = live ? span_of(a.spans, a.S, t, nullptr) : make_int2(0, 0);
+        const bool some = see.x < see.y;
+        if (some && see.y - see.x <= kFew)
+            sum = delta_of_few(a, t, h, head, see, lane);
+        __syncwarp();
         if (lane == 0) {
-            const int2 see = live ? span_of(a.spans, a.S, t, nullptr) : make_int2(0, 0);
-            const bool some = see.x < see.y;
             float *to = info_of(p, a.heads, tile, head) + r;
             to[0] = some ? -a.lse[(int64_t)t * a.Hq + h] * kLog2e : -INFINITY;
             to[kTile] = some ? -sum : 0.0f;

@@ -9,7 +9,8 @@ the values it is rounded to bf16, 2^-8 of it.  So
   |out - ref| <= (2^-8 + 2^-12) sum_j p_j |v_j| + 2^-8 |ref|   (the last for its own rounding).
 
 dv likewise with |dout| for |v|.  ds_j = p_j (dout . v_j - delta) is right to 2^-12 of
-A_j = p_j (sum |dout| |v_j| + sum |dout| |out|) and is rounded to bf16 for the products with k
+A_j = p_j (sum |dout| |v_j| + sum |dout| |out|), or of p_j (sum |dout| |v_j| + sum_i p_i sum
+|dout| |v_i|) where delta is summed from its parts, and is rounded to bf16 for the products with k
 and q:  |dq - ref| <= scale sum_j (2^-8 |ds_j| + 2^-11 A_j) |k_j| + 2^-8 |ref|, dk likewise.
 The fp32 sums over up to n tokens or states add n 2^-24 of the summands' sizes, below 2^-11
 of them here.  lse: 2^-13 (its scores' error) and 2^-22 of its size.
@@ -68,9 +69,13 @@ def _reference(q, k, v, spans, scale, dout=None, out=None):
             continue
         dO, O = dout[:, h].double(), out[:, h].double()
         dO = torch.where(seen.any(1)[:, None], dO, 0.0)
-        delta = (dO * O).sum(-1, keepdim=True)
+        # a token of at most 64 states: delta is summed from p_j (dout . v_j), each right to 2^-12
+        # of p_j sum |dout| |v_j|; else it is that of the given output
+        few = (seen.sum(1) <= 64)[:, None]
+        size = dO.abs() @ V.abs().T
+        delta = torch.where(few, (p * (dO @ V.T)).sum(-1, keepdim=True), (dO * O).sum(-1, keepdim=True))
         ds = p * (dO @ V.T - delta)
-        A = p * (dO.abs() @ V.abs().T + (dO * O).abs().sum(-1, keepdim=True))
+        A = p * (size + torch.where(few, (p * size).sum(-1, keepdim=True), (dO * O).abs().sum(-1, keepdim=True)))
         e = abs(scale) * (2.0 ** -8 * ds.abs() + 2.0 ** -11 * A)
         r["dq"][:, h] = scale * ds @ K
         r["dq_tol"][:, h] = e @ K.abs()
