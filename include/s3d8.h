@@ -542,7 +542,7 @@ int s3d8_cross_attention(const void *q_bf16, const int64_t q_stride[2], const vo
 
 /*
  * Its gradients.  With p_j = exp(scale * q . k[j] - lse), delta = dout . out (for a token of at
- * most 64 states: sum_j p_j (dout . v[j]), which out's rounding has no part in) and
+ * most 128 states: sum_j p_j (dout . v[j]), which out's rounding has no part in) and
  * ds_j = p_j (dout . v[j] - delta):
  *   dq = scale * sum_j ds_j k[j],  dk[j] = scale * sum ds_j q,  dv[j] = sum p_j dout,
  * the last two over the tokens that see state j and the query heads of its head.

@@ -15,7 +15,7 @@
 //
 // Measured (2 x 2048 tokens of 32 / 8 heads of 128, 4 images of 3202 states): dq 210 us, its
 // tensor pipe busy 65% of the time; dkv 340 us, 52%; with the first kernel and the sums of what
-// shares cut 580 us.  dkv's four products of a visit take 3200 clocks where 2060 would be the
+// shares cut 590 us.  dkv's four products of a visit take 3200 clocks where 2060 would be the
 // least: their operands and the copies use shared memory's bandwidth nearly whole (a product of
 // two operands there takes 128 bytes a clock), and P and dS wait for one another.
 //
@@ -57,9 +57,9 @@ constexpr int kReadyRows = 32;          // of a block
 // delta is dout . out, but out is rounded to bf16: that is off by 2^-9 of a product whose size
 // falls with the square root of the number n of states, as against the dout . v_j that it is
 // taken from.  With few states it would be most of the error of dq and dk (n = 2: 2.4 times
-// that of their own rounding, 19: 1.6 times, from 64 on 1.45 times, which is that of ds), so
+// that of their own rounding, 19: 1.6 times, from 128 on 1.45 times, which is that of ds), so
 // there it is summed from its parts, p_j (dout . v_j), at 60 instructions a state and row.
-constexpr int kFew = 64;
+constexpr int kFew = 128;
 
 __device__ __forceinline__ void row_chunk(const __nv_bfloat16 *row, bool some, float (&f)[8])
 {
@@ -76,7 +76,7 @@ __device__ __noinline__ float delta_of_few(const CrossArgs &a, int t, int h, int
     row_chunk(a.q + t * a.qs[0] + h * a.qs[1] + 8 * lane, some, q);
     row_chunk(a.dout + t * a.ds[0] + h * a.ds[1] + 8 * lane, some, d);
     const float lse = -a.lse[(int64_t)t * a.Hq + h] * kLog2e, scale = a.scale * kLog2e;
-#pragma unroll 4
+#pragma unroll 2
     for (int j = see.x; j < see.y; ++j) {
         float k[8], v[8], x = 0.0f, y = 0.0f;
         row_chunk(a.k + j * a.ks[0] + head * a.ks[1] + 8 * lane, some, k);

@@ -69,9 +69,9 @@ def _reference(q, k, v, spans, scale, dout=None, out=None):
             continue
         dO, O = dout[:, h].double(), out[:, h].double()
         dO = torch.where(seen.any(1)[:, None], dO, 0.0)
-        # a token of at most 64 states: delta is summed from p_j (dout . v_j), each right to 2^-12
+        # a token of at most 128 states: delta is summed from p_j (dout . v_j), each right to 2^-12
         # of p_j sum |dout| |v_j|; else it is that of the given output
-        few = (seen.sum(1) <= 64)[:, None]
+        few = (seen.sum(1) <= 128)[:, None]
         size = dO.abs() @ V.abs().T
         delta = torch.where(few, (p * (dO @ V.T)).sum(-1, keepdim=True), (dO * O).sum(-1, keepdim=True))
         ds = p * (dO @ V.T - delta)
