@@ -71,8 +71,8 @@ struct Layout {
     static constexpr int Q = 0, KV = 2 * TILE, ITEMS = KV + STAGES * TILE;
     static constexpr int RUNS = ITEMS + ((kMostTiles + 1) * (int)sizeof(Item) + 15) / 16 * 16;   // at first the query tiles' ranges
     static constexpr int BAD = RUNS + kRuns * (int)sizeof(Run);     // [2][128][8]: columns of +inf, of -inf
-    static constexpr int TOPS = BAD + 2 * 128 * 32;         // [128] maximum and sum of the second chain
-    static constexpr int BARS = TOPS + 128 * 8;
+    static constexpr int TOPS = BAD + 2 * 128 * 32;         // [2][128] maximum and sum of the second chain
+    static constexpr int BARS = TOPS + 2 * 128 * 8;
     static constexpr int PLACES = BARS + 384;               // [STAGES]: the first state of the visits whose copies were issued last
     static constexpr int BYTES = 1024 + BARS + 512;
 };
@@ -453,6 +453,7 @@ __global__ __launch_bounds__(kThreads, 1) void cross_forward_kernel(const __grid
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21), sc = lanes + s * 128, oc = lanes + 256 + s * 128;
         const float scale = fmaxf(fabsf(a.scale) * kLog2e, 1e-30f);      // not 0: a hidden score is -inf
         int jobs = 0, visits = 0;       // of this chain, and of both before this piece
+        int joins = 0;                  // of the two chains, so far
         while (next_unit(share, u)) {
             const int tile = u.pair && s ? u.tb : u.ta, t = tile * p.tokens_a_tile + row / group;
             const bool live = row < p.chunk_rows && t < a.T;
@@ -531,16 +532,20 @@ __global__ __launch_bounds__(kThreads, 1) void cross_forward_kernel(const __grid
             }
             if (mine > 0)
                 wait_on(ok, pv_done + 8 * s, (jobs - 1) & 1);
-            // one query tile: the first group joins the two chains
+            // One query tile: the first group joins the two chains.  The second one may be through
+            // with the next piece before that has read: in a piece of one visit it has nothing to
+            // do, and so nothing to wait for.  It writes to the other half then, and to this one
+            // again behind the next join's barrier, where the first group arrives after it has read.
             float turn[2] = {1.0f, 0.0f};
             if (!u.pair) {
+                float2 *const at = tops + (joins++ & 1) * 128 + row;
                 if (s == 1)
-                    tops[row] = make_float2(top, sum);
+                    *at = make_float2(top, sum);
                 tc::tc_fence_before();
                 asm volatile("bar.sync 1, 256;" ::: "memory");
                 tc::tc_fence_after();
                 if (s == 0) {
-                    const float2 other = tops[row];
+                    const float2 other = *at;
                     const float next = fmaxf(top, other.x), from = next == -INFINITY ? 0.0f : next;
                     turn[0] = ex2(top - from);
                     turn[1] = ex2(other.x - from);

@@ -1,0 +1,66 @@
+"""Cross attention where its schedule and its numbers end, against the formulas in 64 bits
+(those of test_gpu_cross_attention, with its tolerances)."""
+import numpy as np
+import pytest
+import torch
+
+import s3d8_a8_linear_gb300 as s3d8
+from test_gpu_cross_attention import BF, _check, _lib, _rand, _reference, _within, _within_lse  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+TILE = 128
+
+
+# ---- pieces of one visit behind longer ones ---------------------------------
+
+
+def _pieces(spans, S, heads, group, ctas):
+    """How the forward pass divides its work, replayed: for each CTA its pieces, as (whether two
+    query tiles go together, visits)."""
+    each = TILE // group
+    spans = [(max(a, 0), min(b, S)) if a < b else (0, 0) for a, b in spans.tolist()]
+    tiles = -(-len(spans) // each)
+    seen = [[(a // TILE, -(-b // TILE)) for a, b in spans[i * each:(i + 1) * each] if a < b] for i in range(tiles)]
+    ends = [(min(a for a, _ in s), max(b for _, b in s)) if s else (0, 1) for s in seen]
+    items = []
+    for i in range(0, tiles, 2):
+        both = ends[i:i + 2]
+        if len(both) == 2 and 8 * (max(b for _, b in both) - min(a for a, _ in both)) <= 5 * sum(b - a for a, b in both) + 8:
+            items.append((True, seen[i] + seen[i + 1]))
+        else:
+            items += [(False, s) for s in seen[i:i + 2]]
+    sizes = [max(len({j for a, b in s for j in range(a, b)}), 1) for _, s in items]
+    begin, total = np.cumsum([0] + sizes * heads), heads * sum(sizes)
+    used, shares = min(total, ctas), []
+    for c in range(used):
+        at, end, share = total * c // used, total * (c + 1) // used, []
+        while at < end:
+            k = int(np.searchsorted(begin, at, "right")) - 1
+            n = min(end, int(begin[k + 1])) - at
+            share.append((items[k % len(items)][0], n))
+            at += n
+        shares.append(share)
+    return shares
+
+
+@pytest.mark.parametrize("T,most,dim,seeds", [(65, 1601, 128, (4, 5)), (97, 700, 128, (0, 1)), (33, 1601, 64, (1, 20))])
+def test_pieces_of_one_visit(T, most, dim, seeds):
+    """Batches of single tokens whose shares have a piece of one visit, in which the second of a
+    CTA's two chains has nothing to do, right behind a longer one, whose two chains are joined."""
+    ctas = torch.cuda.get_device_properties(0).multi_processor_count
+    for seed in seeds:
+        sizes = np.random.default_rng(seed).integers(0, most + 1, T)
+        ends = np.cumsum(sizes)
+        spans = torch.from_numpy(np.stack((ends - sizes, ends), -1).astype(np.int32)).cuda()
+        S = int(ends[-1])
+        shares = _pieces(spans, S, 8, 4, ctas)
+        if ctas == 152:
+            assert any(not a[0] and a[1] > 1 and b == (False, 1) for s in shares for a, b in zip(s, s[1:]))
+        gen = torch.Generator(device="cuda").manual_seed(seed)
+        q, k, v = _rand(gen, T, 32, dim), _rand(gen, S, 8, dim), _rand(gen, S, 8, dim)
+        got = _check(q, k, v, spans, back=False)
+        out, lse = torch.empty_like(got["out"]), torch.empty_like(got["lse"])
+        for _ in range(200):
+            s3d8.cross_attention(q, k, v, spans, out=out, lse=lse)
+            assert torch.equal(out, got["out"]) and torch.equal(lse, got["lse"])
