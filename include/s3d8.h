@@ -521,8 +521,9 @@ int s3d8_norm_rope_backward(const void *dq_bf16, const int64_t dq_stride[2], con
  *   q       : [T, Hq, dim] bfloat16, strides (token, head) in elements
  *   k, v    : [S, heads, dim] bfloat16, strides likewise
  *   spans   : [T, 2] int32, 8-byte aligned, or NULL (every token sees every state).  An
- *             empty span (end <= begin) gives zeros and lse = -inf; one that leaves the
- *             states is cut to them and records S3D8_ERR_BOUNDS
+ *             empty span (end <= begin) gives zeros and lse = -inf, as one does whose scores
+ *             are all -inf; one that leaves the states is cut to them and records
+ *             S3D8_ERR_BOUNDS
  *   out     : [T, Hq, dim] bfloat16 contiguous output, 16-byte aligned
  *   lse     : [T, Hq] fp32 output log(sum_j exp(scale * q . k[j])), or NULL
  *   workspace : s3d8_cross_attention_workspace_size(T, S, Hq, heads, dim) bytes, 16-byte

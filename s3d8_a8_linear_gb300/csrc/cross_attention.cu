@@ -692,7 +692,7 @@ __global__ __launch_bounds__(kJoinWarps * 32) void cross_join_kernel(const __gri
     const int64_t at = (int64_t)t * a.Hq + cut.head * group + row % group;
     const int2 see = span_of(a.spans, a.S, t, nullptr);
     const bool some = see.x < see.y;
-    const float by = some ? 1.0f / sum : 0.0f;
+    const float by = some && sum != 0.0f ? 1.0f / sum : 0.0f;       // (no weight at all where every score is -inf)
 #pragma unroll
     for (int v = 0; v < V; ++v)
         acc[v] = some ? acc[v] * by : 0.0f;

@@ -64,3 +64,24 @@ def test_pieces_of_one_visit(T, most, dim, seeds):
         for _ in range(200):
             s3d8.cross_attention(q, k, v, spans, out=out, lse=lse)
             assert torch.equal(out, got["out"]) and torch.equal(lse, got["lse"])
+
+
+# ---- numbers at the ends of their range -------------------------------------
+
+
+@pytest.mark.parametrize("T,S", [(1, 100), (1, 300), (1, 20000), (3, 130), (40, 9000), (70, 500)])
+def test_scores_of_minus_infinity(T, S):
+    """A token whose scores are all -infinity gets zeros and lse = -infinity, whether one piece of
+    the work or several make its output; one that has others gets what those give."""
+    gen = torch.Generator(device="cuda").manual_seed(S)
+    q, k, v = _rand(gen, T, 4, 64), _rand(gen, S, 1, 64), _rand(gen, S, 1, 64)
+    q[..., 0] = 1.0
+    k[..., 0] = -float("inf")
+    lse = torch.empty((T, 4), device="cuda")
+    out = s3d8.cross_attention(q, k, v, lse=lse)
+    assert not out.any() and (lse == -float("inf")).all()
+    k[S // 2:, :, 0] = 0.5
+    out = s3d8.cross_attention(q, k, v, lse=lse)
+    r = _reference(q, k[S // 2:], v[S // 2:], None, 64 ** -0.5)
+    _within(out, r["out"], r["out_tol"], "out")
+    _within_lse(lse, r["lse"])
