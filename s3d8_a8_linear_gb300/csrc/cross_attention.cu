@@ -451,7 +451,7 @@ __global__ __launch_bounds__(kThreads, 1) void cross_forward_kernel(const __grid
         asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         const int s = (warp - 4) >> 2, row = threadIdx.x & 127;
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21), sc = lanes + s * 128, oc = lanes + 256 + s * 128;
-        const float scale = fmaxf(fabsf(a.scale) * kLog2e, 1e-30f);      // not 0: a hidden score is -inf
+        const float scale = exponents(a.scale);
         int jobs = 0, visits = 0;       // of this chain, and of both before this piece
         int joins = 0;                  // of the two chains, so far
         while (next_unit(share, u)) {

@@ -437,7 +437,7 @@ __global__ __launch_bounds__(kDqThreads, 1) void cross_dq_kernel(const __grid_co
         asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
         const int half = (warp - 4) >> 2, row = threadIdx.x & 127;
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21);
-        const float scale = fmaxf(fabsf(a.scale) * kLog2e, 1e-30f);
+        const float scale = exponents(a.scale);
         int jobs = 0;
         for (int units = 0; ok && share.next(u); ++units) {
             const int t = (p.first + u.tile) * p.tokens_a_tile + row / group;
@@ -738,7 +738,7 @@ __global__ __launch_bounds__(kThreads, 1) void cross_dkv_kernel(const __grid_con
     } else {                        // softmax: a state a thread, 64 query rows a group of warps
         const int half = (warp - 4) >> 2, row = threadIdx.x & 127;
         const uint32_t lanes = tmem + ((uint32_t)(warp & 3) << 21), sc = lanes + 64 * half, dp = lanes + 128 + 64 * half;
-        const float scale = fmaxf(fabsf(a.scale) * kLog2e, 1e-30f);
+        const float scale = exponents(a.scale);
         const float2 scale2 = make_float2(scale, scale);
         int jobs = 0;
         for (int units = 0; ok && share.next(u); ++units) {

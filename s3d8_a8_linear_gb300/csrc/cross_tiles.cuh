@@ -106,6 +106,10 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
+// What turns a product q . k into a base-2 exponent, but for its sign.  Not 0, so that a hidden
+// score stays -inf: the least number that there is, which makes nothing of any other score.
+__device__ __forceinline__ float exponents(float scale) { return fmaxf(fabsf(scale) * kLog2e, __uint_as_float(1u)); }
+
 // Two bf16 in a word, lo first.
 __device__ __forceinline__ uint32_t pack2(float lo, float hi)
 {

@@ -85,3 +85,10 @@ def test_scores_of_minus_infinity(T, S):
     r = _reference(q, k[S // 2:], v[S // 2:], None, 64 ** -0.5)
     _within(out, r["out"], r["out_tol"], "out")
     _within_lse(lse, r["lse"])
+
+
+@pytest.mark.parametrize("scale,size", [(0.0, 2.0 ** 60), (2.0 ** -110, 2.0 ** 52), (-2.0 ** -110, 2.0 ** 52), (2.0 ** -60, 2.0 ** 30)])
+def test_small_scales_of_large_products(scale, size):
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    q, k, v = _rand(gen, 40, 4, 64) * size, _rand(gen, 300, 2, 64) * size, _rand(gen, 300, 2, 64)
+    _check(q, k, v, None, scale)
