@@ -525,6 +525,7 @@ int s3d8_norm_rope_backward(const void *dq_bf16, const int64_t dq_stride[2], con
  *             are all -inf; one that leaves the states is cut to them and records
  *             S3D8_ERR_BOUNDS
  *   out     : [T, Hq, dim] bfloat16 contiguous output, 16-byte aligned
+ *   scale   : any finite number
  *   lse     : [T, Hq] fp32 output log(sum_j exp(scale * q . k[j])), or NULL
  *   workspace : s3d8_cross_attention_workspace_size(T, S, Hq, heads, dim) bytes, 16-byte
  *             aligned, not shared by calls that overlap on the GPU

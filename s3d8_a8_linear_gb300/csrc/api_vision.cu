@@ -4,6 +4,7 @@
 #include "launch.h"
 
 #include <cuda_runtime.h>
+#include <math.h>
 
 using namespace s3d8;
 
@@ -84,7 +85,7 @@ int cross_args(CrossArgs *a, const void *q, const int64_t q_stride[2], const voi
                float scale)
 {
     if (T < 0 || S < 0 || T > S3D8_MAX_M || S > S3D8_MAX_M || heads < 1 || Hq < 1 || Hq > 65535 || Hq % heads != 0 || dim < 8 ||
-        dim % 8 != 0)
+        dim % 8 != 0 || !isfinite(scale))
         return S3D8_ERR_INVALID_ARG;
     if (dim > S3D8_MAX_CROSS_DIM || Hq / heads > S3D8_MAX_CROSS_GROUP || T * Hq > kMaxInt || S * heads > kMaxInt)
         return S3D8_ERR_UNSUPPORTED;

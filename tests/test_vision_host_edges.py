@@ -1,0 +1,12 @@
+"""More host-side checks of the vision decoder's calls (no GPU), as test_vision_host has them."""
+import pytest
+
+from test_vision_host import A, B, BIG, D, lib, no_device_only, two  # noqa: F401
+
+
+@no_device_only
+@pytest.mark.parametrize("scale", [float("nan"), float("inf"), -float("inf")])
+def test_cross_attention_rejects_scales_that_are_not_finite(lib, scale):  # noqa: F811
+    q, kv = two(256, 64), two(128, 64)
+    assert lib.s3d8_cross_attention(A, q, B, kv, B, kv, A, 3, 5, 4, 2, 64, scale, D, None, A, BIG, None) == -1
+    assert lib.s3d8_cross_attention_backward(A, q, A, q, B, kv, B, kv, A, A, A, 3, 5, 4, 2, 64, scale, D, D, D, A, BIG, None) == -1
