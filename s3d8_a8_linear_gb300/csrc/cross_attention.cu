@@ -702,15 +702,17 @@ __global__ __launch_bounds__(kJoinWarps * 32) void cross_join_kernel(const __gri
         a.lse[at] = some ? (top + __log2f(sum)) * kLn2 : -INFINITY;
 }
 
-// No states at all.
+// No states at all: rows of zeros; a span that is not empty leaves the states.
 __global__ void cross_nothing_kernel(const __grid_constant__ CrossArgs a)
 {
-    const int64_t rows = (int64_t)a.T * a.Hq;
-    for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < rows * a.dim / 8; i += (int64_t)gridDim.x * blockDim.x) {
+    const int64_t rows = (int64_t)a.T * a.Hq, first = (int64_t)blockIdx.x * blockDim.x + threadIdx.x, step = (int64_t)gridDim.x * blockDim.x;
+    for (int64_t i = first; i < rows * a.dim / 8; i += step) {
         reinterpret_cast<uint4 *>(a.out)[i] = make_uint4(0u, 0u, 0u, 0u);
         if (a.lse && i < rows)
             a.lse[i] = -INFINITY;
     }
+    for (int64_t t = first; t < a.T; t += step)
+        span_of(a.spans, 0, (int)t, a.status);
 }
 
 // Of at most kMostTiles query tiles.
@@ -770,12 +772,16 @@ size_t cross_attention_workspace(int64_t T, int64_t, int64_t Hq, int64_t heads, 
     return bytes;
 }
 
+cudaError_t launch_cross_nothing(const CrossArgs &a, cudaStream_t stream)
+{
+    cross_nothing_kernel<<<device_sm_count(), 256, 0, stream>>>(a);
+    return cudaGetLastError();
+}
+
 cudaError_t launch_cross_attention(const CrossArgs &all, cudaStream_t stream)
 {
-    if (all.S == 0) {
-        cross_nothing_kernel<<<device_sm_count(), 256, 0, stream>>>(all);
-        return cudaGetLastError();
-    }
+    if (all.S == 0)
+        return launch_cross_nothing(all, stream);
     const int64_t step = (int64_t)most_tiles(all.heads, (all.S + kTile - 1) / kTile, kMostTiles) * (kTile / (all.Hq / all.heads));
     for (int64_t t = 0; t < all.T; t += step) {
         CrossArgs a = all;

@@ -975,8 +975,12 @@ size_t cross_attention_backward_workspace(int64_t T, int64_t, int64_t Hq, int64_
 
 cudaError_t launch_cross_attention_backward(const CrossArgs &a, cudaStream_t stream)
 {
-    if (a.S == 0)       // (and tokens: their gradients are zero)
-        return cudaMemsetAsync(a.dq, 0, (size_t)a.T * a.Hq * a.dim * sizeof(__nv_bfloat16), stream);
+    if (a.S == 0) {     // (and tokens: their gradients are zero)
+        CrossArgs zeros = a;
+        zeros.out = a.dq;
+        zeros.lse = nullptr;
+        return launch_cross_nothing(zeros, stream);
+    }
     return a.dim > 64 ? launch<128>(a, stream) : launch<64>(a, stream);
 }
 

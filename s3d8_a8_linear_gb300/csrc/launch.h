@@ -231,6 +231,8 @@ struct CrossArgs {
 };
 size_t cross_attention_workspace(int64_t T, int64_t S, int64_t Hq, int64_t heads, int64_t dim);
 cudaError_t launch_cross_attention(const CrossArgs &a, cudaStream_t stream);
+// Without states: zeros into out, -inf into lse (if any), and the spans looked at.
+cudaError_t launch_cross_nothing(const CrossArgs &a, cudaStream_t stream);
 size_t cross_attention_backward_workspace(int64_t T, int64_t S, int64_t Hq, int64_t heads, int64_t dim);
 cudaError_t launch_cross_attention_backward(const CrossArgs &a, cudaStream_t stream);
 

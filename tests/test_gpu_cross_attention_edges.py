@@ -92,3 +92,21 @@ def test_small_scales_of_large_products(scale, size):
     gen = torch.Generator(device="cuda").manual_seed(3)
     q, k, v = _rand(gen, 40, 4, 64) * size, _rand(gen, 300, 2, 64) * size, _rand(gen, 300, 2, 64)
     _check(q, k, v, None, scale)
+
+
+def test_spans_of_no_states_are_recorded():
+    """Without states every span that is not empty leaves them."""
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    q, none = _rand(gen, 5, 4, 64), torch.empty((0, 2, 64), dtype=BF, device="cuda")
+    lse = torch.empty((5, 4), device="cuda")
+    spans = torch.tensor([[0, 0], [3, 3], [9, 2], [0, 0], [-4, -4]], device="cuda").int()
+    out = s3d8.cross_attention(q, none, none, spans, lse=lse)
+    g = s3d8.cross_attention_backward(q, q, none, none, out, lse, spans)
+    assert s3d8.device_status() == 0
+    assert not out.any() and not g["dq"].any() and (lse == -float("inf")).all()
+    for bad in ([0, 1], [-3, 0], [5, 9]):
+        spans[3] = torch.tensor(bad, device="cuda")
+        out = s3d8.cross_attention(q, none, none, spans, lse=lse)
+        assert s3d8.device_status() == -7 and not out.any() and (lse == -float("inf")).all()
+        g = s3d8.cross_attention_backward(q, q, none, none, out, lse, spans)
+        assert s3d8.device_status() == -7 and not g["dq"].any()
