@@ -294,7 +294,8 @@ __global__ __launch_bounds__(kThreads, 1) void norm_rope_kernel(const __grid_con
                 }
             const float squares = row_sum(sum.x + sum.y, l.lanes), back = row_sum(dot.x + dot.y, l.lanes);
             r = ok && h < heads ? rsqrtf(fmaf(squares, inv, a.eps)) : 0.0f;   // no row: not 0 times infinity
-            const float2 r2 = twice(r), by = twice(-(r * r * (back * inv)));
+            // from the mean outwards: r^2 alone passes fp32's range for rows below 5e-20
+            const float2 r2 = twice(r), by = twice(-(r * (r * (back * inv))));
 #pragma unroll
             for (int y = 0; y < 2; ++y)
 #pragma unroll
