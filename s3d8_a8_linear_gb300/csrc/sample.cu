@@ -352,7 +352,8 @@ __device__ __forceinline__ void count_eight(Shared &s, uint4 v, uint32_t cut)
 }
 
 // How the weights behind the head are taken: base-2 exponents y c + b, and the parts of c and
-// b that fp32 does not hold, times ln 2.
+// b that fp32 does not hold, times ln 2.  Of rows that are not far: T between 2^-80 and 2^60 and
+// the largest logit within 2^31, so that c, b and the rests of a logit of -2^68 are finite.
 struct Behind {
     float cut;
     float2 c, b, c_rest, b_rest;
@@ -370,7 +371,7 @@ struct Behind {
     // Of two tokens, where they are not counted.
     __device__ __forceinline__ float2 operator()(uint32_t w) const
     {
-        w = max_bf16x2(w, 0xF149F149u);         // -inf and NaN: -1e30, which has no weight
+        w = max_bf16x2(w, 0xE180E180u);         // -inf and NaN: -2^68, which is more than 100 T down and has no weight
         const float2 y = make_float2(lo_value(w), hi_value(w)), x = fma2(y, c, b), rest = fma2(y, c_rest, b_rest);
         float2 p;
         asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(p.x) : "f"(x.x));
@@ -620,6 +621,7 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(const __grid_constant_
     }
     row.top_value = value_of(row.top);
     row.inverse = reciprocal(temp);
+    const bool far = temp >= 0x1p60f || temp <= 0x1p-80f || !(fabsf(row.top_value) < 0x1p31f);
     const int last_group = row.top / kKeys;
     Verdict verdict;
     for (bool whole = false;; whole = true) {
@@ -627,6 +629,8 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(const __grid_constant_
         float cut = cold ? row.top_value : fminf(row.top_value - (whole ? 33.0f : kHead) * temp, whole ? INFINITY : value_of(reached));
         if (!(cut <= row.top_value))    // (infinite ones of both)
             cut = row.top_value;
+        if (far)                        // all tokens, as Behind's terms may be infinite
+            cut = -INFINITY;
         const uint32_t bits = __float_as_uint(cut) >> 16, cut2 = bits | bits << 16;     // bf16: towards zero
         const int first_group = bits == 0xFF80u ? 0 : key_of(bits) / kKeys;
         for (int i = first_group * (kKeys / 8) + threadIdx.x; i < (last_group + 1) * (kKeys / 8); i += kThreads)
