@@ -172,7 +172,8 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
 struct Row {
     uint32_t top;       // the largest key
     float top_value;
-    Pair inverse;       // 1 / T
+    float unit;         // a power of two that brings T near enough to 1 for
+    Pair inverse;       // 1 / (unit T)
 };
 
 // (Out of line, as search() is: a CTA passes its code once, and what is short is there sooner.)
@@ -180,11 +181,11 @@ __device__ __noinline__ unsigned long long weight_of(uint32_t key, Row r)
 {
     if (key == r.top)
         return 1ull << kScale;
-    const Pair d = two_sum(value_of(key), -r.top_value);
-    if (!isfinite(d.hi))        // an infinite largest logit takes all; -3.4e38 below 3.4e38 is nothing
+    const Pair d = two_sum(value_of(key) * r.unit, -r.top_value * r.unit);
+    if (!isfinite(d.hi))        // an infinite largest logit takes all, and so does one far past a small unit
         return 0ull;
     const float p = __fmul_rn(d.hi, r.inverse.hi);
-    if (!(p > -40.0f))          // past what a weight can show (and NaN where 1 / T is infinite)
+    if (!(p > -40.0f))          // past what a weight can show
         return 0ull;
     return weight(mul(d, r.inverse));
 }
@@ -554,7 +555,7 @@ __device__ __forceinline__ Verdict choose(Shared &s, const SampleArgs &a, int b,
     key = hit.key;
     rank = (uint32_t)((t - hit.mass) / hit.weight);
     if (a.logprob && lane == 0) {
-        const float d = value_of(key) - row.top_value, gap = key == row.top ? 0.0f : __fmaf_rn(d, row.inverse.hi, d * row.inverse.lo);
+        const float d = value_of(key) * row.unit - row.top_value * row.unit, gap = key == row.top ? 0.0f : __fmaf_rn(d, row.inverse.hi, d * row.inverse.lo);
         a.logprob[b] = gap - log1pf((float)(held - (1ull << kScale)) * (1.0f / (float)(1ull << kScale)));
     }
     return kMine;
@@ -620,8 +621,10 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(const __grid_constant_
         return;
     }
     row.top_value = value_of(row.top);
-    row.inverse = reciprocal(temp);
-    const bool far = temp >= 0x1p60f || temp <= 0x1p-80f || !(fabsf(row.top_value) < 0x1p31f);
+    // else 1 / T, or the part of it that fp32 does not hold, may pass fp32's range
+    row.unit = temp >= 0x1p60f ? 0x1p-64f : temp <= 0x1p-80f ? 0x1p64f : 1.0f;
+    row.inverse = reciprocal(temp * row.unit);
+    const bool far = row.unit != 1.0f || !(fabsf(row.top_value) < 0x1p31f);
     const int last_group = row.top / kKeys;
     Verdict verdict;
     for (bool whole = false;; whole = true) {

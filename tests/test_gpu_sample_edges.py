@@ -22,3 +22,22 @@ def test_rows_that_are_all_counted(V, value, temp):
     for u in (0.0, 2.0 ** -17, 0.3, 1.0 - 2.0 ** -24):
         _check(x, u, temp)
         _check(x, u, temp, p=0.5)
+
+
+@pytest.mark.parametrize("temp", [1e36, 3e37, 2e38])
+def test_temperatures_near_the_largest_number(temp):
+    """Logits a few temperatures apart, which fill the range, and ones that are never drawn."""
+    low = torch.finfo(BF).min
+    x = torch.tensor([3e38, low, 0.0, 1e38, -1e38, -float("inf"), float("nan"), 1.0, low, -2e38, 2.5e38], dtype=BF, device=dev())
+    x = torch.cat((x, torch.full((3000,), -float("inf"), dtype=BF, device=dev()))).expand(6, -1)
+    _check(x, np.array([0.0, 0.2, 0.4, 0.6, 0.8, 0.999]), temp)
+
+
+@pytest.mark.parametrize("temp", [2.0 ** -79, 2.0 ** -81, 2.0 ** -110, 2.0 ** -126])
+def test_temperatures_near_the_smallest_number(temp):
+    """Logits a few temperatures apart: neither 1 / T nor a logit over T is infinite."""
+    rng = np.random.default_rng(3)
+    x = torch.from_numpy(rng.standard_normal((6, 3000)) * 8.0 * temp).to(BF).to(dev())
+    _check(x, np.array([0.0, 0.2, 0.4, 0.6, 0.8, 0.999]), temp)
+    x[:, 7] = 1.0
+    assert int(_check(x, 0.5, temp)[0]) == 7
