@@ -21,6 +21,7 @@
  *   - Calls are asynchronous on `stream` (a cudaStream_t passed as void*; NULL
  *     is the legacy default stream).  They neither synchronise nor read device
  *     memory from the host.
+ *   - The memory and the stream are those of the current device.
  *   - Arguments are checked before anything is launched; a failed check returns
  *     a negative s3d8_status and touches no memory.  A launch failure returns
  *     S3D8_ERR_CUDA.

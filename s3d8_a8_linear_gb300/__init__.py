@@ -114,10 +114,16 @@ def _check(fn: str, status: int):
 
 # The stream's handle without a Stream object around it (0.1 us against 2).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(device) -> int:
+    """The current stream of the tensors' GPU, which has to be the current one: a kernel is
+    launched there, and an address of another GPU would be a fault."""
     if _raw_stream is not None and device is not None and device.index is not None:
+        if _current_device() != device.index:
+            raise ValueError(f"the tensors are on {device}, the current device is cuda:{_current_device()}: "
+                             "call under torch.cuda.device(...)")
         return _raw_stream(device.index)
     return torch.cuda.current_stream(device).cuda_stream
 
