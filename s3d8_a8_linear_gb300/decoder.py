@@ -322,6 +322,9 @@ def rope_append(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cos: torch.Te
     if q_norm is None and k_norm is None:
         st = _load().s3d8_rope_append(*args, *end)
     else:
+        for name, w in (("q_norm", q_norm), ("k_norm", k_norm)):
+            if w is not None and w.device != q.device:
+                raise ValueError(f"{name} must be on {q.device}, got {w.device}")
         st = _load().s3d8_norm_rope_append(*args, _opt(q_norm, "q_norm", _BF, (D,)), _opt(k_norm, "k_norm", _BF, (D,)),
                                            eps, *end)
     if st:
