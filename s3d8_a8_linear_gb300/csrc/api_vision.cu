@@ -314,8 +314,6 @@ int s3d8_sample(const void *logits_bf16, int64_t logits_stride, int64_t B, int64
     a.min_p = min_p;
     a.tokens = tokens;
     a.logprob = logprob;
-    if (!(a.status = device_status_ptr()))
-        return S3D8_ERR_CUDA;
     return cuda_status(launch_sample(a, static_cast<cudaStream_t>(stream)));
 }
 

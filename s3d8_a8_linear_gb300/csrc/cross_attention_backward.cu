@@ -150,7 +150,7 @@ __global__ __launch_bounds__(256) void cross_ready_kernel(const __grid_constant_
 // The list of work of a launch: for each of its tiles, the tiles of the other kind that have
 // a part in it, or one (of which nothing is seen).  One warp, from each tile's first and end.
 template <typename Range>
-__device__ __forceinline__ int make_list(int tiles, Item *items, Range range)
+__device__ __forceinline__ void make_list(int tiles, Item *items, Range range)
 {
     const int lane = threadIdx.x & 31;
     int begin = 0;
@@ -176,7 +176,6 @@ __device__ __forceinline__ int make_list(int tiles, Item *items, Range range)
     }
     if (lane == 0)
         items[tiles] = {0, 0, begin};
-    return tiles;
 }
 
 // LONG places of the ring are for tiles in use from a visit's first product to its last (keys,

@@ -244,7 +244,6 @@ struct SampleArgs {
     const int32_t *top_k;
     int32_t *tokens;
     float *logprob;                     // or null
-    int *status;
 };
 cudaError_t launch_sample(const SampleArgs &a, cudaStream_t stream);
 
