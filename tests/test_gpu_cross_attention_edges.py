@@ -110,3 +110,56 @@ def test_spans_of_no_states_are_recorded():
         assert s3d8.device_status() == -7 and not out.any() and (lse == -float("inf")).all()
         g = s3d8.cross_attention_backward(q, q, none, none, out, lse, spans)
         assert s3d8.device_status() == -7 and not g["dq"].any()
+
+
+# ---- gradients ----------------------------------------------------------------
+
+
+def test_what_an_infinity_reaches():
+    """Infinities and NaN that tokens do see reach no gradient past the 128 query rows (here 64
+    tokens) and the 128 states of the tiles that those tokens and states are in."""
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    T, S = 400, 1000
+    q, k, v, dout = _rand(gen, T, 4, 64), _rand(gen, S, 2, 64), _rand(gen, S, 2, 64), _rand(gen, T, 4, 64)
+    image = torch.arange(T, device="cuda") // 100
+    spans = torch.stack((image * 250, image * 250 + 250), -1).int()
+    lse = torch.empty((T, 4), device="cuda")
+
+    def gradients():
+        out = s3d8.cross_attention(q, k, v, spans, lse=lse)
+        return s3d8.cross_attention_backward(dout, q, k, v, out, lse, spans)
+
+    clean = gradients()
+    tokens, states = torch.ones(T, dtype=torch.bool, device="cuda"), torch.ones(S, dtype=torch.bool, device="cuda")
+    tokens[64:256], states[128:512] = False, False      # tiles with tokens 100 .. 199, with states 250 .. 499
+    for t, j, bad in ((q, 150, float("nan")), (dout, 101, float("inf")), (k, 300, -float("inf")), (v, 499, float("nan")), (k, 250, float("inf"))):
+        kept = t[j].clone()
+        t[j] = bad
+        got = gradients()
+        t[j] = kept
+        assert torch.equal(got["dq"][tokens], clean["dq"][tokens])
+        assert all(torch.equal(got[n][states], clean[n][states]) for n in ("dk", "dv"))
+
+
+def test_gradients_of_far_states():
+    """Offsets past 2^31 elements, in keys and values and in their gradients."""
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("needs 60 GB")
+    S, dim = (1 << 24) - 5, 128
+    both = torch.empty((S, 4, dim), dtype=BF, device="cuda")        # 8.6 billion elements
+    gen = torch.Generator(device="cuda").manual_seed(15)
+    both[-700:] = _rand(gen, 700, 4, dim)
+    both[:300] = _rand(gen, 300, 4, dim)
+    q, dout = _rand(gen, 6, 4, dim), _rand(gen, 6, 4, dim)
+    spans = torch.tensor([[S - 700, S], [S - 300, S - 1], [0, 300], [S - 30, S], [0, 100], [S - 40, S - 39]], device="cuda").int()
+    near = torch.cat((both[:300], both[-700:]))
+    moved = torch.where(spans >= 1000, spans - (S - 1000), spans)
+    lse = torch.empty((6, 4), device="cuda")
+    out = s3d8.cross_attention(q, both[:, :2], both[:, 2:], spans, lse=lse)
+    g = s3d8.cross_attention_backward(dout, q, both[:, :2], both[:, 2:], out, lse, spans)
+    r = _reference(q, near[:, :2], near[:, 2:], moved, dim ** -0.5, dout, out)
+    _within(g["dq"], r["dq"], r["dq_tol"], "dq")
+    for n in ("dk", "dv"):
+        got = torch.cat((g[n][:300], g[n][-700:]))
+        _within(got, r[n], r[n + "_tol"], n)
+        assert not any(bool(part.any()) for part in g[n][300:-700].split(1 << 20)), n

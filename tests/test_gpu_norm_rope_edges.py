@@ -31,3 +31,46 @@ def test_tiny_rows_without_epsilon(T, Hq, Hk, D, rotary, inter, size, monkeypatc
         ref, scale, dw_ref, dw_size = _backward(dz_, x, w, cos, sin, pos, inter)
         _close(g[dx], ref, scale)
         _close_sum(g[dw], dw_ref, 1.25 * dw_size, T * x.shape[1])
+
+
+@pytest.mark.parametrize("T,Hq,Hk,D,rotary,inter", [(5, 7, 2, 80, 40, False), (61, 32, 8, 128, 128, False), (9, 4, 4, 256, 64, True), (40, 3, 1, 48, 6, False)])
+def test_rows_whose_squares_pass_the_range_become_zeros(T, Hq, Hk, D, rotary, inter):
+    """Sums of squares are fp32: past 3.4e38 the root is 0, as the header says, and with it the row,
+    its gradient and its part of the weight's; no other row is touched."""
+    rng, q, k, wq, wk, cos, sin, pos = _case(T, Hq, Hk, D, rotary, seed=8, fused=False)
+    dz = _rand(rng, T, Hq + Hk, D)
+
+    def run(q, k, dq, dk):
+        return *s3d8.norm_rope(q, k, wq, wk, cos, sin, pos, norm.EPS, inter), s3d8.norm_rope_backward(dq, dk, q, k, wq, wk, cos, sin, pos, norm.EPS, inter)
+
+    dq, dk = dz[:, :Hq].contiguous(), dz[:, Hq:].contiguous()
+    none_q, none_k = dq.clone(), dk.clone()
+    none_q[1, Hq - 1], none_k[2, 0] = 0, 0
+    zq, zk, g = run(q, k, none_q, none_k)           # (no part in the weights' gradients, whatever the rows hold)
+    large_q, large_k = q.clone(), k.clone()
+    large_q[1, Hq - 1], large_k[2, 0] = 1e19, -3e19
+    yq, yk, h = run(large_q, large_k, dq, dk)
+    for got, want, at in ((yq, zq, (1, Hq - 1)), (yk, zk, (2, 0)), (h["dq"], g["dq"], (1, Hq - 1)), (h["dk"], g["dk"], (2, 0))):
+        assert not got[at].any()
+        want[at] = 0
+        assert torch.equal(got, want)
+    assert torch.equal(h["dq_norm"], g["dq_norm"]) and torch.equal(h["dk_norm"], g["dk_norm"])
+
+
+@pytest.mark.parametrize("T", [5, 1700])
+def test_the_append_s_rows_whose_squares_pass_the_range(T):
+    rng, q, k, wq, wk, cos, sin, _ = _case(T, 8, 2, 128, 128, seed=9, fused=False)
+    v = _rand(rng, T, 2, 128)
+    pos, table = torch.arange(T, device=dev()).int(), torch.arange(T, device=dev()).int().view(T, 1)
+    pos = pos % 16
+    caches = [s3d8.KVCache.empty(T, 16, 2, 128) for _ in range(2)]
+    want = s3d8.rope_append(q, k, v, cos, sin, pos, caches[0], table, q_norm=wq, k_norm=wk)
+    q, k = q.clone(), k.clone()
+    q[3, 1], k[2, 1] = 1e19, -3e19
+    got = s3d8.rope_append(q, k, v, cos, sin, pos, caches[1], table, q_norm=wq, k_norm=wk)
+    want[3, 1] = 0
+    assert torch.equal(got, want)
+    at = torch.arange(T, device=dev()), pos.long()
+    stored, plain = caches[1].k[at], caches[0].k[at]
+    plain[2, 1] = 0
+    assert torch.equal(stored, plain) and torch.equal(caches[1].v[at], v)
