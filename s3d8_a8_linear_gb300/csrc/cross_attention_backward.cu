@@ -20,7 +20,7 @@
 // two operands there takes 128 bytes a clock), and P and dS wait for one another.
 //
 // A first kernel makes delta and lse ready, a row a half warp, and the range of states that
-// each query tile sees.  Rows of the query tiles or the states that have no part in a tile
+// each query tile sees; one behind it delta of the rows that see few states.  Rows of the query tiles or the states that have no part in a tile
 // are taken out of it where they hold infinities or NaN, which a weight of zero would not
 // silence.
 #include "bf16x8.cuh"
@@ -53,48 +53,6 @@ struct Plan {
 __device__ __forceinline__ float *info_of(const Plan &p, int heads, int tile, int head) { return p.info + ((int64_t)tile * heads + head) * 4 * kTile; }
 
 constexpr int kReadyRows = 32;          // of a block
-
-// delta is dout . out, but out is rounded to bf16: that is off by 2^-9 of a product whose size
-// falls with the square root of the number n of states, as against the dout . v_j that it is
-// taken from.  With few states it would be most of the error of dq and dk (n = 2: 2.4 times
-// that of their own rounding, 19: 1.6 times, from 128 on 1.45 times, which is that of ds), so
-// there it is summed from its parts, p_j (dout . v_j), at 60 instructions a state and row.
-constexpr int kFew = 128;
-
-__device__ __forceinline__ void row_chunk(const __nv_bfloat16 *row, bool some, float (&f)[8])
-{
-    const uint4 x = some ? __ldg(reinterpret_cast<const uint4 *>(row)) : make_uint4(0u, 0u, 0u, 0u);
-    unpack8(x, f);
-}
-
-// That sum, of half a warp's row, eight columns a lane.
-__device__ __noinline__ float delta_of_few(const CrossArgs &a, int t, int h, int head, int2 see, int lane)
-{
-    const unsigned mask = 0xFFFFu << (threadIdx.x & 16);
-    const bool some = 8 * lane < a.dim;
-    float q[8], d[8], sum = 0.0f;
-    row_chunk(a.q + t * a.qs[0] + h * a.qs[1] + 8 * lane, some, q);
-    row_chunk(a.dout + t * a.ds[0] + h * a.ds[1] + 8 * lane, some, d);
-    const float lse = -a.lse[(int64_t)t * a.Hq + h] * kLog2e, scale = a.scale * kLog2e;
-#pragma unroll 2
-    for (int j = see.x; j < see.y; ++j) {
-        float k[8], v[8], x = 0.0f, y = 0.0f;
-        row_chunk(a.k + j * a.ks[0] + head * a.ks[1] + 8 * lane, some, k);
-        row_chunk(a.v + j * a.vs[0] + head * a.vs[1] + 8 * lane, some, v);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            x = fmaf(q[e], k[e], x);
-            y = fmaf(d[e], v[e], y);
-        }
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) {
-            x += __shfl_xor_sync(mask, x, o);
-            y += __shfl_xor_sync(mask, y, o);
-        }
-        sum = fmaf(ex2(fmaf(x, scale, lse)), y, sum);
-    }
-    return sum;
-}
 
 // delta and lse of some of a tile's rows of one key/value head, and the tile's range.
 __global__ __launch_bounds__(256) void cross_ready_kernel(const __grid_constant__ CrossArgs a, const __grid_constant__ Plan p)
@@ -134,9 +92,6 @@ __global__ __launch_bounds__(256) void cross_ready_kernel(const __grid_constant_
             sum += __shfl_xor_sync(0xffffffffu, sum, o);
         const int2 see = live ? span_of(a.spans, a.S, t, nullptr) : make_int2(0, 0);
         const bool some = see.x < see.y;
-        if (some && see.y - see.x <= kFew)
-            sum = delta_of_few(a, t, h, head, see, lane);
-        __syncwarp();
         if (lane == 0) {
             float *to = info_of(p, a.heads, tile, head) + r;
             to[0] = some ? -a.lse[(int64_t)t * a.Hq + h] * kLog2e : -INFINITY;
@@ -144,6 +99,114 @@ __global__ __launch_bounds__(256) void cross_ready_kernel(const __grid_constant_
             to[2 * kTile] = __int_as_float(see.x);
             to[3 * kTile] = __int_as_float(see.y);
         }
+    }
+}
+
+// delta is dout . out, but out is rounded to bf16: that is off by 2^-9 of a product whose size
+// falls with the square root of the number n of states, as against the dout . v_j that it is
+// taken from.  With few states it would be most of the error of dq and dk (n = 2: 2.4 times
+// that of their own rounding, 19: 1.6 times, from 128 on 1.45 times, which is that of ds), so
+// there it is summed from its parts, p_j (dout . v_j).
+constexpr int kFew = 128;
+constexpr int kFewWarps = 4;            // of a block
+constexpr int kNever = 0x7FFFFFFF;
+
+__device__ __forceinline__ void mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// A lane's part of a row: columns 8 (c + 4 i) .. + 7.
+template <int N>
+__device__ __forceinline__ void row_chunks(const __nv_bfloat16 *row, int c, int dim, bool some, uint4 (&x)[N])
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        x[i] = some && 8 * (c + 4 * i) < dim ? __ldg(reinterpret_cast<const uint4 *>(row) + c + 4 * i) : make_uint4(0u, 0u, 0u, 0u);
+}
+
+// delta of a tile's rows that see few states.  A warp has 16 rows and passes the states that some
+// of them see, 16 at a time.  Its products are mma.sync: they are a hundredth of the call's, and
+// operands go from global memory straight into registers, whatever the spans are (a lane's chunks
+// of 16 bytes are the columns of two products, in the same order for both operands).
+// Measured (step of 8 x 1024 tokens of 32 / 8 heads of 128, 128 states each): 99 us of 320, 10 where
+// no token sees few; half a warp a row with scalar sums took 2.06 ms of 2.24.
+template <int DP>
+__global__ __launch_bounds__(kFewWarps * 32, 3) void cross_few_kernel(const __grid_constant__ CrossArgs a, const __grid_constant__ Plan p)
+{
+    constexpr int N = DP / 32;
+    tc::pdl_launch_dependents();
+    tc::pdl_wait();
+    const int tile = blockIdx.x, head = blockIdx.y, group = a.Hq / a.heads, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    const int r0 = (blockIdx.z * kFewWarps + warp_index()) * 16;
+    int2 see[2];
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+        const int r = r0 + 8 * y + g, t = tile * p.tokens_a_tile + r / group;
+        see[y] = r < p.chunk_rows && t < a.T ? span_of(a.spans, a.S, t, nullptr) : make_int2(0, 0);
+        if (see[y].y - see[y].x > kFew)
+            see[y] = make_int2(0, 0);
+    }
+    // the first state from `from` on that some row sees
+    auto next = [&](int from) {
+        int n = kNever;
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+            if (see[y].y > from && see[y].x < see[y].y)
+                n = min(n, max(see[y].x, from));
+        return __reduce_min_sync(0xffffffffu, n);
+    };
+    int at = next(0);
+    if (at == kNever)
+        return;
+    uint4 q[2][N], d[2][N];
+    float lse[2], sum[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+        const int r = r0 + 8 * y + g, h = head * group + r % group;
+        const int64_t t = tile * p.tokens_a_tile + r / group;
+        const bool some = see[y].x < see[y].y;
+        row_chunks(a.q + t * a.qs[0] + h * a.qs[1], c, a.dim, some, q[y]);
+        row_chunks(a.dout + t * a.ds[0] + h * a.ds[1], c, a.dim, some, d[y]);
+        lse[y] = some ? -a.lse[t * a.Hq + h] * kLog2e : 0.0f;
+    }
+    const float scale = a.scale * kLog2e;
+    for (; at != kNever; at = next(at + 16)) {
+        uint4 k[2][N], v[2][N];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            const int j = at + 8 * n + g;
+            row_chunks(a.k + j * a.ks[0] + head * a.ks[1], c, a.dim, j < a.S, k[n]);
+            row_chunks(a.v + j * a.vs[0] + head * a.vs[1], c, a.dim, j < a.S, v[n]);
+        }
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            float s[4] = {0.0f, 0.0f, 0.0f, 0.0f}, dp[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const uint32_t q0[4] = {q[0][i].x, q[1][i].x, q[0][i].y, q[1][i].y}, q1[4] = {q[0][i].z, q[1][i].z, q[0][i].w, q[1][i].w};
+                const uint32_t d0[4] = {d[0][i].x, d[1][i].x, d[0][i].y, d[1][i].y}, d1[4] = {d[0][i].z, d[1][i].z, d[0][i].w, d[1][i].w};
+                mma_bf16(s, q0, k[n][i].x, k[n][i].y);
+                mma_bf16(dp, d0, v[n][i].x, v[n][i].y);
+                mma_bf16(s, q1, k[n][i].z, k[n][i].w);
+                mma_bf16(dp, d1, v[n][i].z, v[n][i].w);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int y = e >> 1, j = at + 8 * n + 2 * c + (e & 1);
+                const float part = ex2(fmaf(s[e], scale, lse[y])) * dp[e];
+                sum[y] += j >= see[y].x && j < see[y].y ? part : 0.0f;
+            }
+        }
+    }
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+        sum[y] += __shfl_xor_sync(0xffffffffu, sum[y], 1);
+        sum[y] += __shfl_xor_sync(0xffffffffu, sum[y], 2);
+        if (c == 0 && see[y].x < see[y].y)
+            info_of(p, a.heads, tile, head)[kTile + r0 + 8 * y + g] = -sum[y];
     }
 }
 
@@ -947,6 +1010,8 @@ cudaError_t launch(const CrossArgs &a, cudaStream_t stream)
         e = tc::allow_smem(cross_dkv_kernel<DP>, L::BYTES, allowed_kv);
     if (e == cudaSuccess)
         e = tc::launch_pdl(cross_ready_kernel, dim3(p.q_tiles, a.heads, kTile / kReadyRows), dim3(256), 0, stream, a, p);
+    if (e == cudaSuccess && (a.spans || a.S <= kFew))
+        e = tc::launch_pdl(cross_few_kernel<DP>, dim3(p.q_tiles, a.heads, kTile / (16 * kFewWarps)), dim3(kFewWarps * 32), 0, stream, a, p);
     const int tiles = (a.S + kTile - 1) / kTile, most_q = most_tiles(a.heads, tiles, kMostTiles), most_kv = most_tiles(a.heads, p.q_tiles, kMostTiles);
     for (p.first = 0; e == cudaSuccess && p.first < p.q_tiles; p.first += most_q) {
         p.tiles = p.q_tiles - p.first < most_q ? p.q_tiles - p.first : most_q;

@@ -163,3 +163,14 @@ def test_gradients_of_far_states():
         got = torch.cat((g[n][:300], g[n][-700:]))
         _within(got, r[n], r[n + "_tol"], n)
         assert not any(bool(part.any()) for part in g[n][300:-700].split(1 << 20)), n
+
+
+@pytest.mark.parametrize("T,S,Hq,heads,dim", [(150, 5000, 2, 2, 128), (150, 5000, 4, 1, 40), (60, 2000, 128, 1, 8), (33, 700, 10, 2, 96), (90, 20, 3, 1, 64)])
+def test_few_states_and_many_side_by_side(T, S, Hq, heads, dim):
+    """Tokens of no, one, few and more than 128 states in one tile, in any order and far apart: the
+    ones of at most 128 have delta from its parts."""
+    gen = torch.Generator(device="cuda").manual_seed(dim)
+    n = torch.tensor([0, 1, 2, 15, 16, 17, 100, 127, 128, 129, 130, 300], device="cuda")[torch.randint(0, 12, (T,), generator=gen, device="cuda")]
+    lo = (torch.rand(T, generator=gen, device="cuda") * S).long()
+    spans = torch.stack((lo, (lo + n).clamp(max=S)), -1).int()
+    _check(_rand(gen, T, Hq, dim), _rand(gen, S, heads, dim), _rand(gen, S, heads, dim), spans)
