@@ -484,7 +484,9 @@ int s3d8_compact_pages(const s3d8_kv_cache *layers, int64_t count, int32_t *tabl
  *             >= max_pos, which records S3D8_ERR_BOUNDS (with rotary > 0)
  *   q_out, k_out : [T, Hq, dim], [T, Hk, dim] bfloat16 contiguous outputs, not overlapping
  *             the inputs
- * dim: a multiple of 16, 16..256.  Rows start on 16 bytes.
+ * dim: a multiple of 16, 16..256.  Rows start on 16 bytes.  Sums of squares are fp32: a row past
+ * their range (values of 1e18 and more) has a root of 0, so that it becomes zeros, as do its
+ * gradients (without a norm rows are not summed).
  */
 int s3d8_norm_rope(const void *q_bf16, const int64_t q_stride[2], int64_t Hq, const void *k_bf16,
                    const int64_t k_stride[2], int64_t Hk, const void *q_norm_bf16,
@@ -531,8 +533,12 @@ int s3d8_norm_rope_backward(const void *dq_bf16, const int64_t dq_stride[2], con
  *   workspace : s3d8_cross_attention_workspace_size(T, S, Hq, heads, dim) bytes, 16-byte
  *             aligned, not shared by calls that overlap on the GPU
  * dim: a multiple of 8, 8..S3D8_MAX_CROSS_DIM; Hq a multiple of heads, at most
- * S3D8_MAX_CROSS_GROUP times as many.  Rows start on 16 bytes.  A state that a token does
- * not see has no part in the token's output, whatever it holds.
+ * S3D8_MAX_CROSS_GROUP times as many.  Rows start on 16 bytes.  out and lse do not overlap the
+ * inputs.  A state that a token does not see has no part in the token's output, whatever it holds.
+ * Scores, the softmax's maximum and sum and the output sums are fp32; a weight is rounded to
+ * bf16 on its way into the product with the values.  So out is off by at most 2^-8 of
+ * sum_j p_j |v_j| beside its own rounding (2^-8 of itself) and what the scores' fp32 sums add to
+ * the weights: with random values about 1.4 times as far as by its own rounding alone.
  */
 #define S3D8_MAX_CROSS_DIM 128
 #define S3D8_MAX_CROSS_GROUP 128
@@ -552,12 +558,14 @@ int s3d8_cross_attention(const void *q_bf16, const int64_t q_stride[2], const vo
  *   dout    : [T, Hq, dim] bfloat16, strides (token, head)
  *   q, k, v, spans, scale : as in the forward call; out, lse : as it wrote them
  *   dq      : [T, Hq, dim]; dk, dv : [S, heads, dim] bfloat16 contiguous outputs, 16-byte
- *             aligned
+ *             aligned, not overlapping the inputs
  *   workspace : s3d8_cross_attention_backward_workspace_size(...) bytes, as above
  * No atomics: equal inputs give equal bits.  A state that no token sees has zero gradients,
  * and neither it nor a token that sees nothing has a part in any other gradient, whatever
- * they hold.  An infinity or NaN that some token does see may reach the gradients of other
- * tokens and states in the same 128 of them.
+ * they hold.  An infinity or NaN that some token does see may reach the gradients of the other
+ * tokens and states in its tiles: 128 query rows of a key/value head (128 / (Hq / heads) tokens),
+ * 128 states.  p_j and ds_j are rounded to bf16 on their way into the products with dout, k and q
+ * (2^-8 of each summand), as the weights are in the forward pass; sums are fp32.
  */
 size_t s3d8_cross_attention_backward_workspace_size(int64_t T, int64_t S, int64_t Hq, int64_t heads,
                                                     int64_t dim);
@@ -587,7 +595,10 @@ int s3d8_cross_attention_backward(const void *dout_bf16, const int64_t dout_stri
  *   tokens  : [B] int32 output; -1 for a row that has no token to draw
  *   logprob : [B] fp32 output, the log of the token's share of the kept weight (0 for
  *             T <= 0, -inf for -1), or NULL
- * Weights are whole numbers of 2^-45 of the largest one, so a token's share is right to 2^-45.
+ * A weight is right to 2^-45 of the largest one.  A sum of weights (what is kept, what stands in
+ * front of a token) is right to that for each of its tokens, and to 2^-18 of the weight of the
+ * tokens that are less than exp(-16) times as likely as the first; a border between two tokens
+ * lies that close to its place.  logprob is fp32.
  * V: 1..S3D8_MAX_SAMPLE_V.  Rows that start on 16 bytes are read faster.
  */
 #define S3D8_MAX_SAMPLE_V 524224

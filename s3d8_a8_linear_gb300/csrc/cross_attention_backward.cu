@@ -14,15 +14,15 @@
 // softmax step runs.
 //
 // Measured (2 x 2048 tokens of 32 / 8 heads of 128, 4 images of 3202 states): dq 210 us, its
-// tensor pipe busy 65% of the time; dkv 340 us, 52%; with the first kernel and the sums of what
-// shares cut 590 us.  dkv's four products of a visit take 3200 clocks where 2060 would be the
+// tensor pipe busy 65% of the time; dkv 340 us, 52%; with the first two kernels and the sums of
+// what shares cut 580 us.  dkv's four products of a visit take 3200 clocks where 2060 would be the
 // least: their operands and the copies use shared memory's bandwidth nearly whole (a product of
 // two operands there takes 128 bytes a clock), and P and dS wait for one another.
 //
 // A first kernel makes delta and lse ready, a row a half warp, and the range of states that
-// each query tile sees; one behind it delta of the rows that see few states.  Rows of the query tiles or the states that have no part in a tile
-// are taken out of it where they hold infinities or NaN, which a weight of zero would not
-// silence.
+// each query tile sees; one behind it delta of the rows that see few states.  Rows of the query
+// tiles or the states that have no part in a tile are taken out of it where they hold infinities
+// or NaN, which a weight of zero would not silence.
 #include "bf16x8.cuh"
 #include "cross_tiles.cuh"
 

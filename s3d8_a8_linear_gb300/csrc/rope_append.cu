@@ -10,7 +10,8 @@
 // token's stores.  Measured: 61 tokens of 32 + 16 heads of 128 in 2.4 us, 16384 in
 // 73 us (5.6 TB/s of what it has to move; 77 us without the ring), 4099 into int8 in
 // 22 us (25 us).  With norms of the heads in front of the rotation (s3d8_norm_rope_append,
-// instances of their own) two sums of a row's lanes come first: 61 tokens 2.9 us, 16384 78 us.
+// instances of their own) two sums of a row's lanes come first: 61 tokens 2.9 us, 16384 78 us;
+// into int8, where the ring's instances spill a few registers, 4.8 and 108 us.
 #include "bf16x8.cuh"
 #include "common.cuh"
 #include "launch.h"

@@ -6,25 +6,26 @@
 // weight falls on one token of it.  A bf16 logit is one of 65536 values, so nothing is
 // sorted: tokens are counted into a histogram of their values, and weights are computed once
 // per value instead of once per token.  That leaves time for exact ones: exp in pairs of
-// fp32 (about 2^-44), summed as whole numbers of 2^-45 of the largest weight.  Such sums do
-// not depend on their order, so equal inputs give equal bits, and a token next to a border
-// is decided as in 64 bits.
+// fp32 (to 2^-43 of itself and 2^-46 of the largest weight), summed as whole numbers of 2^-45
+// of the largest weight.  Such sums do not depend on their order, so equal inputs give equal
+// bits, and are right to 2^-45 for each of their tokens.
 //
 // Counting costs an atomic addition in shared memory a token, so only the head of the order
 // is counted, the values within 16 T of the largest logit; of the others only the sum of the
-// weights is taken, in fp32 (each is below 2^-23 of the largest, so that its error of 2^-21
-// or so is nothing).  Where a limit or the drawn token turns out to lie behind the head,
-// the row is counted again as a whole.
+// weights is taken, in fp32: base-2 exponents of 23 to 64, which are rounded by up to 2^-19,
+// ex2.approx (2^-22), and a dozen additions, together at most 2^-18 of that sum (which is at most
+// 2^-6 of the largest weight with 128256 logits).  Where a limit or the drawn token turns out to
+// lie behind the head, the row is counted again as a whole.
 //
 // A cluster of CTAs takes a row, a part of the vocabulary each (16-bit counts, so at most
 // 65535 tokens a CTA), and reads it three times, from L2 but for the first.  Values form
-// groups of 128, one power of two each.  The first CTA adds up the counts of the groups that have any from all CTAs,
-// finds the limits and the value by searching the groups' sums, and tells the CTA whose part
-// has the token.
+// groups of 128, one power of two each.  The first CTA adds up the counts of the groups that
+// have any from all CTAs, finds the limits and the value by searching the groups' sums, and
+// tells the CTA whose part has the token.
 //
 // Bound by instructions and by the barriers between those steps (42% of the issue slots with
 // 509 rows), not by HBM.  Measured with 128256 logits: one row 13 us, 64 rows with limits of
-// their own 28 us, 509 rows 160 us (302 when every token was counted).
+// their own 28 us, 509 rows 164 us (302 when every token was counted).
 #include "launch.h"
 #include "tcgen05.cuh"
 #include "uniform.cuh"
