@@ -128,9 +128,10 @@ __device__ __forceinline__ void row_chunks(const __nv_bfloat16 *row, int c, int 
 }
 
 // delta of a tile's rows that see few states.  A warp has 16 rows and passes the states that some
-// of them see, 16 at a time.  Its products are mma.sync: they are a hundredth of the call's, and
-// operands go from global memory straight into registers, whatever the spans are (a lane's chunks
-// of 16 bytes are the columns of two products, in the same order for both operands).
+// of them see, 16 at a time.  Its products are mma.sync: a tcgen05 tile of 128 rows would pass the
+// states of all their tokens, and here operands go from global memory straight into registers,
+// whatever the spans are (a lane's chunks of 16 bytes are the columns of two products, in the same
+// order for both operands).
 // Measured (step of 8 x 1024 tokens of 32 / 8 heads of 128, 128 states each): 99 us of 320, 10 where
 // no token sees few; half a warp a row with scalar sums took 2.06 ms of 2.24.
 template <int DP>

@@ -11,11 +11,12 @@
 // rows (a warp keeps one weight's columns in registers, and one weight's sums), and each
 // warp an equal run of its kind's groups.  It copies them through a ring of its own in
 // shared memory, the token's angles with the first group of a token, five groups (backward
-// three) in flight beside the one in use: what bounds it is HBM and, backward, the issue slots (70% busy).
-// Measured: 25616 tokens of 8 heads of 128 in 22.5 to 23 us (4.6 TB/s of what it has to move;
-// 33.5 with each warp waiting for the rows that it had asked for), 8191 tokens of 32 + 8 heads
-// with rotation in 32 us (5.4 TB/s) and their gradients in 54 us (4.7 TB/s; 82.6).  Shorter runs in two rounds of CTAs measured 25.6
-// and 56.6 us, four CTAs of 128 threads an SM 22.9 and 55.4.
+// three) in flight beside the one in use: what bounds it is HBM and, backward, the issue slots
+// (70% busy). Measured: 25616 tokens of 8 heads of 128 in 22.5 to 23 us (4.6 TB/s of what it
+// has to move; 33.5 with each warp waiting for the rows that it had asked for), 8191 tokens of
+// 32 + 8 heads with rotation in 32 us (5.4 TB/s) and their gradients in 54 us (4.7 TB/s; 82.6).
+// Shorter runs in two rounds of CTAs measured 25.6 and 56.6 us, four CTAs of 128 threads an SM
+// 22.9 and 55.4.
 //
 // The weights' gradients: a lane keeps its columns' sums in registers over all its rows,
 // a CTA adds its lanes' in shared memory, a second kernel adds the CTAs' rows; every order
